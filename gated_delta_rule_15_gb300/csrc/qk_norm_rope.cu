@@ -1,0 +1,499 @@
+// qk_norm_rope.cu -- norm of every query and key head and the rotation by its position, in
+// one pass over q and k, and the gradients (declared in include/dr.h).
+//
+// Per row x of d values, with weights w (1 without), n = d (RMS) or 1 (L2):
+//     r = 1 / sqrt(sum x^2 / n + eps)   (1 without a norm),   y = w x r,
+//     the pairs (y_a, y_b) of the first rot values are rotated by pos * f_i and scaled by c.
+// Gradient, with u the output gradient rotated back (and scaled by c) and g = w u:
+//     dx = r g - x r^3 (g . x) / n,    dw = sum over rows of u x r.
+//
+// Angles: f_i enters as turns per position in units of 2^-64 turns (dr_rope_table), so the
+// 64-bit product with the position wraps to the exact fraction of a turn, however far the
+// position; its upper 32 bits go to sincospi in fp32.
+//
+// Both directions stream q and k once and are bound by HBM bandwidth.  A row is held by
+// d / 8 lanes with 8 values each, so a warp's accesses are whole rows; a group of lanes takes
+// one token and runs over its heads, so that sines and cosines are computed once for all of
+// them.  A pair's other half sits in the same lane (interleaved) or rot / 16 lanes away
+// (half): its raw values come by shuffle.
+#include <math.h>
+
+#include "../../include/dr.h"
+#include "common.cuh"
+
+namespace dr {
+namespace {
+
+struct RopeArgs {
+    const void *x[2];        // q, k: rows of `stride` elements per token, heads d apart
+    const void *dy[2];       // (gradient) of the outputs, contiguous
+    void *y[2];              // outputs, or gradients of x
+    int64_t stride[2], out_stride[2];
+    const float *w[2];
+    const uint64_t *table;
+    const int64_t *pos;
+    int64_t n_tok, seq_len, pos0;
+    int heads[2], rot, groups;   // groups: runs of heads a token's rows are split into
+    float eps, scale;
+    float *partial;          // (gradient) [blocks][2][d] partial weight gradients, or NULL
+};
+
+template <typename T> struct Vec8;   // 8 storage elements
+template <> struct Vec8<float> { float4 a, b; };
+template <> struct Vec8<__nv_bfloat16> { uint4 a; };
+
+__device__ __forceinline__ Vec8<float> ld8(const float *p) {
+    return {*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + 4)};
+}
+__device__ __forceinline__ Vec8<__nv_bfloat16> ld8(const __nv_bfloat16 *p) { return {*reinterpret_cast<const uint4 *>(p)}; }
+__device__ __forceinline__ void unpack(const Vec8<float> &v, float (&f)[8]) {
+    f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
+    f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
+}
+__device__ __forceinline__ void unpack(const Vec8<__nv_bfloat16> &v, float (&f)[8]) {
+    const uint32_t u[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // bf16 is the upper half of fp32
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ Vec8<float> shfl8(const Vec8<float> &v, int src) {
+    Vec8<float> o;
+    o.a.x = __shfl_sync(0xffffffffu, v.a.x, src); o.a.y = __shfl_sync(0xffffffffu, v.a.y, src);
+    o.a.z = __shfl_sync(0xffffffffu, v.a.z, src); o.a.w = __shfl_sync(0xffffffffu, v.a.w, src);
+    o.b.x = __shfl_sync(0xffffffffu, v.b.x, src); o.b.y = __shfl_sync(0xffffffffu, v.b.y, src);
+    o.b.z = __shfl_sync(0xffffffffu, v.b.z, src); o.b.w = __shfl_sync(0xffffffffu, v.b.w, src);
+    return o;
+}
+__device__ __forceinline__ Vec8<__nv_bfloat16> shfl8(const Vec8<__nv_bfloat16> &v, int src) {
+    Vec8<__nv_bfloat16> o;
+    o.a.x = __shfl_sync(0xffffffffu, v.a.x, src); o.a.y = __shfl_sync(0xffffffffu, v.a.y, src);
+    o.a.z = __shfl_sync(0xffffffffu, v.a.z, src); o.a.w = __shfl_sync(0xffffffffu, v.a.w, src);
+    return o;
+}
+__device__ __forceinline__ void st8(float *p, const float (&f)[8]) {
+    store4(p, make_float4(f[0], f[1], f[2], f[3]));
+    store4(p + 4, make_float4(f[4], f[5], f[6], f[7]));
+}
+__device__ __forceinline__ void st8(__nv_bfloat16 *p, const float (&f)[8]) {
+    uint4 u;
+    uint32_t *w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = u;
+}
+
+// Cosine and sine (times c) of this lane's pairs: 8 (half layout, one per value) or 4.
+template <bool HALF>
+__device__ __forceinline__ void angles(const RopeArgs &a, int64_t pos, int l, float (&co)[HALF ? 8 : 4],
+                                       float (&si)[HALF ? 8 : 4]) {
+    constexpr int NP = HALF ? 8 : 4;
+    const int hr = a.rot / 2, i0 = HALF ? (8 * l < hr ? 8 * l : 8 * l - hr) : 4 * l;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+        co[e] = 1.f;
+        si[e] = 0.f;
+    }
+    if (8 * l < a.rot) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const uint64_t turn = (uint64_t)pos * __ldg(a.table + i0 + e);
+            // signed upper half: [-1/2, 1/2) turns, i.e. that many times 2 pi
+            const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;   // 2^-31
+            float s, c;
+            sincospif(half_turns, &s, &c);
+            co[e] = c * a.scale;
+            si[e] = s * a.scale;
+        }
+    }
+}
+
+// (x_a cos - x_b sin, x_b cos + x_a sin) of this lane's 8 values; `other` holds the pairs'
+// other halves in the half layout.  The angle's sign is in si.
+template <bool HALF>
+__device__ __forceinline__ void rotate(float (&x)[8], const float (&other)[8], bool first, const float (&co)[HALF ? 8 : 4],
+                                       const float (&si)[HALF ? 8 : 4]) {
+    if (HALF) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(first ? -other[e] : other[e], si[e], x[e] * co[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float p = x[2 * e], q = x[2 * e + 1];
+            x[2 * e] = fmaf(-q, si[e], p * co[e]);
+            x[2 * e + 1] = fmaf(p, si[e], q * co[e]);
+        }
+    }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// `it`-th unit of work: a token and a run of its q and k heads (numbered behind one another).
+template <int D, bool HALF, typename T>
+__global__ void __launch_bounds__(256)
+qk_rope_kernel(const RopeArgs a, int norm) {
+    constexpr int LPR = D / 8, U = 2;
+    const int lane = threadIdx.x & 31, l = lane % LPR;
+    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+    const int64_t tok = unit / a.groups;
+    const int g = (int)(unit % a.groups), all = a.heads[0] + a.heads[1];
+    const int h0 = (int)((int64_t)all * g / a.groups), h1 = (int)((int64_t)all * (g + 1) / a.groups);
+    const bool live = tok < a.n_tok;   // shuffles are by whole warps: idle groups stay, on no heads
+    const int64_t pos = !live ? 0 : a.pos ? a.pos[tok] : a.pos0 + tok % a.seq_len;
+    float co[HALF ? 8 : 4], si[HALF ? 8 : 4];
+    angles<HALF>(a, pos, l, co, si);
+    const bool rotated = 8 * l < a.rot, first = 16 * l < a.rot;
+    const int src = HALF && rotated ? (lane + (first ? a.rot / 16 : -(a.rot / 16))) : lane;
+    // every group of a warp runs as often as the longest one
+    const int most = (all + a.groups - 1) / a.groups;
+    for (int i = 0; i < most; i += U) {
+        Vec8<T> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + i + u, s = h >= a.heads[0];
+            if (live && h < h1)
+                raw[u] = ld8((const T *)a.x[s] + tok * a.stride[s] + (int64_t)(h - s * a.heads[0]) * D + 8 * l);
+            else raw[u] = Vec8<T>{};
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + i + u, s = h >= a.heads[0];
+            float x[8], o[8];
+            unpack(raw[u], x);
+            if (HALF) {
+                const Vec8<T> other = shfl8(raw[u], src);
+                unpack(other, o);
+            }
+            float r = 1.f;
+            if (norm != DR_NORM_NONE) {
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                ss = row_sum<LPR>(ss);
+                r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
+            }
+            const float *w = a.w[s];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] *= w ? r * __ldg(w + 8 * l + e) : r;
+                if (HALF) o[e] *= w ? r * __ldg(w + 8 * (l + src - lane) + e) : r;
+            }
+            if (rotated) rotate<HALF>(x, o, first, co, si);
+            if (live && h < h1)
+                st8((T *)a.y[s] + tok * a.out_stride[s] + (int64_t)(h - s * a.heads[0]) * D + 8 * l, x);
+        }
+    }
+}
+
+// Gradient: persistent groups of lanes over the tokens, the weight gradients of a lane's 8
+// values in registers, summed over the block at the end (a fixed order: no atomics).
+template <int D, bool HALF, typename T>
+__global__ void __launch_bounds__(256)
+qk_rope_bwd_kernel(const RopeArgs a, int norm) {
+    constexpr int LPR = D / 8, RPB = 256 / LPR;
+    const int lane = threadIdx.x & 31, l = lane % LPR, all = a.heads[0] + a.heads[1];
+    const bool rotated = 8 * l < a.rot, first = 16 * l < a.rot;
+    const int src = HALF && rotated ? (lane + (first ? a.rot / 16 : -(a.rot / 16))) : lane;
+    const int64_t units = a.n_tok * a.groups;
+    const int most = (all + a.groups - 1) / a.groups;
+    float dw[2][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+    for (int64_t u0 = (int64_t)blockIdx.x * RPB; u0 < units; u0 += (int64_t)gridDim.x * RPB) {
+        const int64_t unit = u0 + threadIdx.x / LPR, tok = unit / a.groups;
+        const bool live = unit < units;
+        const int g = (int)(unit % a.groups);
+        const int h0 = (int)((int64_t)all * g / a.groups), h1 = (int)((int64_t)all * (g + 1) / a.groups);
+        const int64_t pos = !live ? 0 : a.pos ? a.pos[tok] : a.pos0 + tok % a.seq_len;
+        float co[HALF ? 8 : 4], si[HALF ? 8 : 4];
+        angles<HALF>(a, pos, l, co, si);
+#pragma unroll
+        for (int e = 0; e < (HALF ? 8 : 4); ++e) si[e] = -si[e];   // back
+        for (int i = 0; i < most; ++i) {
+            const int h = h0 + i, s = h >= a.heads[0];
+            const bool on = live && h < h1;
+            const int64_t row = (int64_t)(h - s * a.heads[0]) * D + 8 * l;
+            Vec8<T> vx{}, vd{};
+            if (on) {
+                vx = ld8((const T *)a.x[s] + tok * a.stride[s] + row);
+                vd = ld8((const T *)a.dy[s] + tok * (int64_t)a.heads[s] * D + row);
+            }
+            float x[8], u[8], o[8];
+            unpack(vx, x);
+            unpack(vd, u);
+            if (HALF) {
+                const Vec8<T> other = shfl8(vd, src);
+                unpack(other, o);
+            }
+            if (rotated) rotate<HALF>(u, o, first, co, si);
+            const float *w = a.w[s];
+            float r = 1.f, gx = 0.f, ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            if (norm != DR_NORM_NONE) {
+                ss = row_sum<LPR>(ss);
+                r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
+            }
+            if (a.partial) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float t = u[e] * x[e] * r;
+                    if (s) dw[1][e] += t; else dw[0][e] += t;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (w) u[e] *= __ldg(w + 8 * l + e);
+                gx = fmaf(u[e], x[e], gx);
+            }
+            if (norm != DR_NORM_NONE) {
+                gx = row_sum<LPR>(gx);
+                const float f = -r * r * r * gx * (norm == DR_NORM_RMS ? 1.f / D : 1.f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = fmaf(x[e], f, u[e] * r);
+            }
+            if (on) st8((T *)a.y[s] + tok * a.out_stride[s] + row, u);
+        }
+    }
+    if (!a.partial) return;
+    __shared__ float sum[RPB][D];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[threadIdx.x / LPR][8 * l + e] = dw[s][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < D; c += 256) {
+            float t = 0.f;
+            for (int r = 0; r < RPB; ++r) t += sum[r][c];
+            a.partial[((size_t)blockIdx.x * 2 + s) * D + c] = t;
+        }
+    }
+}
+
+// dw[s][c] = sum of the blocks' partial sums, in a fixed order: one warp per value.
+__global__ void __launch_bounds__(256)
+rope_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, float *__restrict__ dwq, float *__restrict__ dwk) {
+    const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // of 2 d
+    if (c >= 2 * d) return;
+    float t = 0.f;
+    for (int b = lane; b < blocks; b += 32) t += partial[(size_t)b * 2 * d + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    float *dst = c < d ? dwq : dwk;
+    if (lane == 0 && dst) dst[c < d ? c : c - d] = t;
+}
+
+constexpr int kGradBlocks = 608;   // four per SM
+
+template <int D, typename T>
+int launch_fwd(const RopeArgs &a, int norm, bool half, cudaStream_t s) {
+    const int64_t threads = a.n_tok * a.groups * (D / 8);
+    const unsigned blocks = (unsigned)((threads + 255) / 256);
+    if (half) qk_rope_kernel<D, true, T><<<blocks, 256, 0, s>>>(a, norm);
+    else qk_rope_kernel<D, false, T><<<blocks, 256, 0, s>>>(a, norm);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+template <int D, typename T>
+int launch_bwd(const RopeArgs &a, int norm, bool half, int blocks, float *dwq, float *dwk, cudaStream_t s) {
+    if (half) qk_rope_bwd_kernel<D, true, T><<<blocks, 256, 0, s>>>(a, norm);
+    else qk_rope_bwd_kernel<D, false, T><<<blocks, 256, 0, s>>>(a, norm);
+    if (cudaGetLastError() != cudaSuccess) return kErrCuda;
+    if (!a.partial) return kOk;
+    rope_weight_sum_kernel<<<(2 * D + 7) / 8, 256, 0, s>>>(a.partial, blocks, D, dwq, dwk);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+int check_desc(const dr_qk_norm_rope_desc *d) {
+    if (!d) return kErrInvalid;
+    if (d->n_tok < 0 || d->Hq < 1 || d->Hk < 0 || d->d < 1 || d->rot < 0 || d->rot > d->d || d->seq_len < 0)
+        return kErrInvalid;
+    if (d->dtype != DR_F32 && d->dtype != DR_BF16) return kErrInvalid;
+    if (d->norm < DR_NORM_NONE || d->norm > DR_NORM_RMS || d->layout < DR_ROPE_HALF || d->layout > DR_ROPE_INTERLEAVED)
+        return kErrInvalid;
+    if (!(d->eps >= 0.f) || !(d->rot_scale == d->rot_scale) || d->reserved != 0) return kErrInvalid;
+    if (d->d != 64 && d->d != 128 && d->d != 256) return kErrUnsupported;
+    if (d->rot % 16 != 0) return kErrUnsupported;
+    if (d->Hq > (1 << 16) || d->Hk > (1 << 16) || d->n_tok > ((int64_t)1 << 31)) return kErrUnsupported;
+    const int64_t unit = d->dtype == DR_BF16 ? 8 : 4;   // rows start on 16-byte boundaries
+    const int64_t strides[4] = {d->q_stride, d->q_out_stride, d->k_stride, d->k_out_stride};
+    for (int i = 0; i < 4; ++i) {
+        if (strides[i] == 0) continue;
+        if (strides[i] < (i < 2 ? d->Hq : d->Hk) * d->d || strides[i] % unit != 0) return kErrInvalid;
+        if (strides[i] > ((int64_t)1 << 31)) return kErrUnsupported;
+    }
+    return kOk;
+}
+
+// Runs of heads a token's rows are split into: one while the tokens alone give every SM its
+// 2048 threads (the sines are then computed once a token), more for few tokens.
+int head_groups(const dr_qk_norm_rope_desc &d) {
+    const int64_t threads = d.n_tok * (d.d / 8), all = d.Hq + d.Hk, want = (int64_t)152 * 2048;
+    int64_t g = threads >= want ? 1 : (want + threads - 1) / (threads > 0 ? threads : 1);
+    return (int)(g < all ? g : all);
+}
+
+RopeArgs common_args(const dr_qk_norm_rope_desc &d, const void *q, const void *k, const float *wq, const float *wk,
+                     const uint64_t *table, const int64_t *positions) {
+    RopeArgs a{};
+    a.x[0] = q; a.x[1] = k;
+    a.stride[0] = d.q_stride ? d.q_stride : d.Hq * d.d;
+    a.stride[1] = d.k_stride ? d.k_stride : d.Hk * d.d;
+    a.out_stride[0] = d.q_out_stride ? d.q_out_stride : d.Hq * d.d;
+    a.out_stride[1] = d.k_out_stride ? d.k_out_stride : d.Hk * d.d;
+    a.w[0] = wq; a.w[1] = wk;
+    a.table = table; a.pos = positions;
+    a.n_tok = d.n_tok; a.seq_len = d.seq_len > 0 ? d.seq_len : (d.n_tok > 0 ? d.n_tok : 1); a.pos0 = d.pos0;
+    a.heads[0] = (int)d.Hq; a.heads[1] = (int)d.Hk; a.rot = (int)d.rot;
+    a.eps = d.eps; a.scale = d.rot_scale;
+    a.groups = head_groups(d);
+    return a;
+}
+
+int grad_blocks(const dr_qk_norm_rope_desc &d) {
+    const int64_t rpb = 256 / (d.d / 8), need = (d.n_tok * head_groups(d) + rpb - 1) / rpb;
+    return (int)(need < kGradBlocks ? (need < 1 ? 1 : need) : kGradBlocks);
+}
+
+bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// n_tok rows of `width` elements, `stride` apart
+struct Rows {
+    const void *p;
+    int64_t width, stride;
+};
+// Whether rows of a and b share a byte.  Rows of one stride may lie between one another (the
+// parts of a fused projection's row); of different strides their whole spans count.
+bool meet(const Rows &a, const Rows &b, int64_t n_tok, int64_t e) {
+    if (!a.p || !b.p || n_tok < 1 || a.width < 1 || b.width < 1) return false;
+    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
+    if (a0 + ((n_tok - 1) * a.stride + a.width) * e <= b0 || b0 + ((n_tok - 1) * b.stride + b.width) * e <= a0) return false;
+    if (a.stride != b.stride) return true;
+    const int64_t row = a.stride * e, off = ((b0 - a0) % row + row) % row;
+    return off < a.width * e || off + b.width * e > row;
+}
+bool same(const Rows &a, const Rows &b) { return a.p == b.p && a.width == b.width && a.stride == b.stride; }
+
+}  // namespace
+}  // namespace dr
+
+using namespace dr;
+
+extern "C" int dr_rope_table(int64_t rot, double base, int32_t scaling, double factor, double original, double low,
+                             double high, uint64_t *table) {
+    if (!table || rot < 0 || rot > 256 || !(base > 1.0) || !isfinite(base)) return kErrInvalid;
+    if (scaling < DR_ROPE_PLAIN || scaling > DR_ROPE_BY_PARTS) return kErrInvalid;
+    if (scaling != DR_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return kErrInvalid;
+    if (scaling == DR_ROPE_BY_PARTS && (!(original > 0.0) || !(high > low) || !isfinite(original) || !isfinite(low) || !isfinite(high)))
+        return kErrInvalid;
+    if (rot % 16 != 0) return kErrUnsupported;
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * (double)i / (double)rot);   // radians a position
+        if (scaling == DR_ROPE_LINEAR) f /= factor;
+        if (scaling == DR_ROPE_BY_PARTS) {
+            double w = (original * f / two_pi - low) / (high - low);
+            w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+            f *= w + (1.0 - w) / factor;
+        }
+        table[i] = (uint64_t)(f / two_pi * 18446744073709551616.0 + 0.5);   // 2^64; f <= 1, so below 2^62
+    }
+    return kOk;
+}
+
+extern "C" int dr_qk_norm_rope(const dr_qk_norm_rope_desc *desc, const void *q, const void *k, const float *wq,
+                               const float *wk, const uint64_t *table, const int64_t *positions, void *q_out, void *k_out,
+                               dr_stream_t stream) {
+    const int rc = check_desc(desc);
+    if (rc != kOk) return rc;
+    const dr_qk_norm_rope_desc &d = *desc;
+    if (d.n_tok == 0) return kOk;
+    if (!q || !q_out || (d.Hk > 0 && (!k || !k_out)) || (d.rot > 0 && !table)) return kErrInvalid;
+    if (d.norm == DR_NORM_NONE && (wq || wk)) return kErrInvalid;
+    const void *ptrs[] = {q, k, q_out, k_out};
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return kErrInvalid;
+    if (!aligned(wq, 4) || !aligned(wk, 4) || !aligned(table, 8) || !aligned(positions, 8)) return kErrInvalid;
+    RopeArgs a = common_args(d, q, k, wq, wk, table, positions);
+    a.y[0] = q_out; a.y[1] = k_out;
+    // an output is its own input (every row is read before it is written) or meets neither
+    // input nor the other output
+    const int64_t e = d.dtype == DR_BF16 ? 2 : 4, wide[2] = {d.Hq * d.d, d.Hk * d.d};
+    if (meet({q_out, wide[0], a.out_stride[0]}, {k_out, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
+    for (int o = 0; o < 2; ++o)
+        for (int i = 0; i < 2; ++i) {
+            const Rows y{a.y[o], wide[o], a.out_stride[o]}, x{a.x[i], wide[i], a.stride[i]};
+            if (meet(y, x, d.n_tok, e) && !(o == i && same(y, x))) return kErrInvalid;
+        }
+    const bool half = d.layout == DR_ROPE_HALF;
+    cudaStream_t s = (cudaStream_t)stream;
+    using bf = __nv_bfloat16;
+    if (d.n_tok * a.groups * (d.d / 8) > (int64_t)256 * 0x7fffffff) return kErrUnsupported;
+    if (d.dtype == DR_BF16)
+        return d.d == 64 ? launch_fwd<64, bf>(a, d.norm, half, s) : d.d == 128 ? launch_fwd<128, bf>(a, d.norm, half, s)
+                                                                               : launch_fwd<256, bf>(a, d.norm, half, s);
+    return d.d == 64 ? launch_fwd<64, float>(a, d.norm, half, s) : d.d == 128 ? launch_fwd<128, float>(a, d.norm, half, s)
+                                                                              : launch_fwd<256, float>(a, d.norm, half, s);
+}
+
+extern "C" int dr_qk_norm_rope_bwd_workspace_bytes(const dr_qk_norm_rope_desc *desc, size_t *bytes) {
+    if (!bytes) return kErrInvalid;
+    const int rc = check_desc(desc);
+    if (rc != kOk) return rc;
+    *bytes = desc->norm == DR_NORM_NONE ? 0 : sizeof(float) * 2 * (size_t)desc->d * grad_blocks(*desc);
+    return kOk;
+}
+
+extern "C" int dr_qk_norm_rope_bwd(const dr_qk_norm_rope_desc *desc, const void *q, const void *k, const float *wq,
+                                   const float *wk, const uint64_t *table, const int64_t *positions, const void *dq_out,
+                                   const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                                   size_t workspace_bytes, dr_stream_t stream) {
+    const int rc = check_desc(desc);
+    if (rc != kOk) return rc;
+    const dr_qk_norm_rope_desc &d = *desc;
+    if (d.n_tok > 0 && (!q || !dq_out || !dq || (d.Hk > 0 && (!k || !dk_out || !dk)) || (d.rot > 0 && !table))) return kErrInvalid;
+    if (d.norm == DR_NORM_NONE && (wq || wk)) return kErrInvalid;
+    if ((dwq && !wq) || (dwk && !wk)) return kErrInvalid;   // no weights, no gradient of them
+    const void *ptrs[] = {q, k, dq_out, dk_out, dq, dk, workspace};
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return kErrInvalid;
+    const void *words[] = {wq, wk, dwq, dwk};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return kErrInvalid;
+    if (!aligned(table, 8) || !aligned(positions, 8)) return kErrInvalid;
+    RopeArgs a = common_args(d, q, k, wq, wk, table, positions);
+    a.dy[0] = dq_out; a.dy[1] = dk_out;
+    a.y[0] = dq; a.y[1] = dk;
+    // dq may be q and dk may be k; otherwise no written row meets another or an input's
+    const int64_t e = d.dtype == DR_BF16 ? 2 : 4, wide[2] = {d.Hq * d.d, d.Hk * d.d};
+    if (meet({dq, wide[0], a.out_stride[0]}, {dk, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
+    for (int o = 0; o < 2; ++o)
+        for (int i = 0; i < 2; ++i) {
+            const Rows y{a.y[o], wide[o], a.out_stride[o]}, x{a.x[i], wide[i], a.stride[i]};
+            if (meet(y, x, d.n_tok, e) && !(o == i && same(y, x))) return kErrInvalid;
+            if (meet(y, {a.dy[i], wide[i], wide[i]}, d.n_tok, e)) return kErrInvalid;
+        }
+    const bool weights = dwq || dwk;
+    const int blocks = grad_blocks(d);
+    if (weights && (!workspace || workspace_bytes < sizeof(float) * 2 * (size_t)d.d * blocks)) return kErrWorkspace;
+    if (d.n_tok == 0 && !weights) return kOk;
+    a.partial = weights ? (float *)workspace : nullptr;
+    const bool half = d.layout == DR_ROPE_HALF;
+    cudaStream_t s = (cudaStream_t)stream;
+    using bf = __nv_bfloat16;
+    if (d.dtype == DR_BF16)
+        return d.d == 64    ? launch_bwd<64, bf>(a, d.norm, half, blocks, dwq, dwk, s)
+               : d.d == 128 ? launch_bwd<128, bf>(a, d.norm, half, blocks, dwq, dwk, s)
+                            : launch_bwd<256, bf>(a, d.norm, half, blocks, dwq, dwk, s);
+    return d.d == 64    ? launch_bwd<64, float>(a, d.norm, half, blocks, dwq, dwk, s)
+           : d.d == 128 ? launch_bwd<128, float>(a, d.norm, half, blocks, dwq, dwk, s)
+                        : launch_bwd<256, float>(a, d.norm, half, blocks, dwq, dwk, s);
+}

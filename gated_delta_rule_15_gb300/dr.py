@@ -11,6 +11,7 @@ is the end-to-end path a caller with host buffers takes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,13 +34,21 @@ DR_FUSE_QK_L2NORM, DR_FUSE_BETA_SIGMOID, DR_FUSE_OUT_SILU_GATE = 1, 2, 4
 DR_FUSE_ALL = 7
 L2NORM_EPS = 1e-6   # DR_L2NORM_EPS
 
+# queries and keys (dr_qk_norm_rope): norms, rotation layouts, frequency scalings
+DR_NORM_NONE, DR_NORM_L2, DR_NORM_RMS = 0, 1, 2
+DR_ROPE_HALF, DR_ROPE_INTERLEAVED = 0, 1
+DR_ROPE_PLAIN, DR_ROPE_LINEAR, DR_ROPE_BY_PARTS = 0, 1, 2
+
 # Symbols of include/dr.h (checked by tests/test_abi.py against the header).
 EXPORTED = ("dr_version", "dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd_min_workspace_bytes",
             "dr_chunk_fwd_ex_workspace_bytes", "dr_chunk_fwd",
             "dr_recurrent_step", "dr_get_device_status", "dr_strerror",
             "dr_chunk_fwd_noalloc", "dr_chunk_fwd_ex", "dr_recurrent_step_ex",
             "dr_chunk_bwd_workspace_bytes", "dr_chunk_bwd", "dr_selftest_bounded_wait",
-            "dr_chunk_fwd_host_dev_bytes", "dr_chunk_fwd_host")
+            "dr_chunk_fwd_host_dev_bytes", "dr_chunk_fwd_host",
+            "dr_linrec_fwd_workspace_bytes", "dr_linrec_fwd", "dr_linrec_bwd_workspace_bytes",
+            "dr_linrec_bwd", "dr_linrec_step", "dr_rope_table", "dr_qk_norm_rope",
+            "dr_qk_norm_rope_bwd_workspace_bytes", "dr_qk_norm_rope_bwd")
 
 
 class ChunkDesc(ctypes.Structure):
@@ -54,6 +63,24 @@ class StepDesc(ctypes.Structure):
                 ("dv", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class LinrecDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QkNormRopeDesc(ctypes.Structure):
+    _fields_ = [("n_tok", ctypes.c_int64), ("seq_len", ctypes.c_int64), ("pos0", ctypes.c_int64),
+                ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("rot", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rot_scale", ctypes.c_float)]
 
 
 _vp = ctypes.c_void_p
@@ -100,6 +127,21 @@ _lib.dr_strerror.restype = ctypes.c_char_p
 _lib.dr_chunk_fwd_noalloc.argtypes = [ctypes.POINTER(ChunkDesc), _vp, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _vp]
 _lib.dr_chunk_fwd_noalloc.restype = ctypes.c_int
+for _name in ("dr_linrec_fwd_workspace_bytes", "dr_linrec_bwd_workspace_bytes"):
+    getattr(_lib, _name).argtypes = [ctypes.POINTER(LinrecDesc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.dr_linrec_fwd.argtypes = [ctypes.POINTER(LinrecDesc)] + [_vp] * 9 + [ctypes.c_size_t, _vp]
+_lib.dr_linrec_bwd.argtypes = [ctypes.POINTER(LinrecDesc)] + [_vp] * 14 + [ctypes.c_size_t, _vp]
+_lib.dr_linrec_step.argtypes = [ctypes.POINTER(StepDesc)] + [_vp] * 7
+_lib.dr_rope_table.argtypes = [ctypes.c_int64, ctypes.c_double, ctypes.c_int32] + \
+    [ctypes.c_double] * 4 + [_vp]
+_lib.dr_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeDesc)] + [_vp] * 9
+_lib.dr_qk_norm_rope_bwd_workspace_bytes.argtypes = [ctypes.POINTER(QkNormRopeDesc),
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+_lib.dr_qk_norm_rope_bwd.argtypes = [ctypes.POINTER(QkNormRopeDesc)] + [_vp] * 13 + \
+    [ctypes.c_size_t, _vp]
+for _name in EXPORTED:
+    if "linrec" in _name or "rope" in _name:
+        getattr(_lib, _name).restype = ctypes.c_int
 NOALLOC_SCRATCH_BYTES = 64 << 20   # DR_NOALLOC_SCRATCH_BYTES of include/dr.h
 
 _DT = {torch.float32: DR_F32, torch.bfloat16: DR_BF16}
@@ -413,3 +455,290 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, init_state=None, *, chunk: int = 64
     like = {"q": q, "k": k, "v": v, "log_alpha": log_alpha, "beta": beta,
             "init_state": init_state}
     return HostChunkRunner(like, chunk=chunk, out_dtype=out_dtype, pieces=pieces)(like)
+
+
+# ------------------------------------------------------------ additive gated recurrence
+def _on_one_device(*ts):
+    """Contiguous tensors of the current device, or ValueError."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on the current CUDA device")
+
+
+def _stream_scope(stream):
+    """Buffers allocated for a call belong to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _like(t, shape, dtype, what):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+
+
+def _linrec_desc(q, k, v, log_alpha, cu_seqlens, out_dtype):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B,T,H,d]")
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
+    if k.shape != q.shape or v.shape[:3] != q.shape[:3]:
+        raise ValueError("inconsistent shapes")
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    _like(log_alpha, (B, T, H), torch.float32, "log_alpha")
+    N = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be int64 [N + 1], N >= 1")
+        if B != 1:
+            raise ValueError("packed sequences come as one batch row (B = 1)")
+        N = cu_seqlens.numel() - 1
+    return LinrecDesc(B, T, H, dk, dv, N, _DT[q.dtype], _DT[out_dtype],
+                      DR_GATE_NONE if log_alpha is None else DR_GATE_SCALAR, 0)
+
+
+def _workspace(query, desc, workspace, device, what):
+    n = ctypes.c_size_t(0)
+    rc = query(ctypes.byref(desc), ctypes.byref(n))
+    if rc != DR_OK:
+        raise DrError(rc, what)
+    if workspace is None and n.value > 0:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def linrec_fwd(q, k, v, log_alpha=None, init_state=None, *, cu_seqlens=None, out_dtype=None,
+               return_final_state: bool = True, out=None, final_state=None, workspace=None,
+               stream=None):
+    """The additive gated linear recurrence S_t = exp(log_alpha_t) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t (dr_linrec_fwd).
+
+    q, k [B,T,H,dk]; v [B,T,H,dv]; log_alpha None or fp32 [B,T,H]; init_state None or fp32
+    [N,H,dk,dv].  With ``cu_seqlens`` (int64 [N + 1] on the device) the T rows of the one
+    batch row hold N sequences behind one another; without, N = B.  Returns (out
+    [B,T,H,dv], final_state fp32 [N,H,dk,dv] or None); ``final_state`` may be the
+    ``init_state`` tensor.  Rows of ``out`` that belong to no sequence are left as they
+    are."""
+    _on_one_device(q, k, v, log_alpha, cu_seqlens, init_state, out, final_state, workspace)
+    desc = _linrec_desc(q, k, v, log_alpha, cu_seqlens, out_dtype or (q.dtype if out is None else out.dtype))
+    states = (desc.N or desc.B, desc.H, desc.dk, desc.dv)
+    _like(init_state, states, torch.float32, "init_state")
+    _like(final_state, states, torch.float32, "final_state")
+    _like(out, v.shape, _TORCH_DT[desc.out_dtype], "out")
+    with _stream_scope(stream):
+        if out is None:
+            out = torch.empty(v.shape, dtype=_TORCH_DT[desc.out_dtype], device=q.device)
+        if final_state is None and return_final_state:
+            final_state = torch.empty(states, dtype=torch.float32, device=q.device)
+        workspace = _workspace(_lib.dr_linrec_fwd_workspace_bytes, desc, workspace, q.device,
+                               "dr_linrec_fwd_workspace_bytes")
+        rc = _lib.dr_linrec_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                                _ptr(cu_seqlens), _ptr(init_state), _ptr(out), _ptr(final_state),
+                                _ptr(workspace), _bytes(workspace), _stream_handle(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_linrec_fwd")
+    return out, final_state
+
+
+def linrec_bwd(q, k, v, log_alpha, init_state, d_out, d_final_state=None, *, cu_seqlens=None,
+               return_d_init: bool = True, grads=None, workspace=None, stream=None):
+    """Gradients of <d_out, out> + <d_final_state, final_state> of linrec_fwd
+    (dr_linrec_bwd).  Returns (dq, dk, dv, d_log_alpha, d_init_state): the first three in
+    q's dtype, d_log_alpha fp32 (None without a gate), d_init_state fp32 (None unless
+    return_d_init).  ``grads``: buffers (dq, dk, dv, d_log_alpha) to write into; their rows
+    of no sequence are left as they are."""
+    _on_one_device(q, k, v, log_alpha, cu_seqlens, init_state, d_out, d_final_state, workspace)
+    desc = _linrec_desc(q, k, v, log_alpha, cu_seqlens, d_out.dtype)
+    states = (desc.N or desc.B, desc.H, desc.dk, desc.dv)
+    _like(init_state, states, torch.float32, "init_state")
+    _like(d_final_state, states, torch.float32, "d_final_state")
+    _like(d_out, v.shape, d_out.dtype, "d_out")
+    with _stream_scope(stream):
+        if grads is None:
+            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+                     None if log_alpha is None else torch.empty_like(log_alpha))
+        else:
+            if len(grads) != 4 or (grads[3] is None) != (log_alpha is None):
+                raise ValueError("grads must be (dq, dk, dv, d_log_alpha or None)")
+            _on_one_device(*grads)
+            for g, x, n in zip(grads, (q, k, v, log_alpha), ("dq", "dk", "dv", "d_log_alpha")):
+                if x is not None and (g is None or g.dtype != x.dtype or g.shape != x.shape):
+                    raise ValueError(f"{n} must be {x.dtype} {list(x.shape)}")
+        dq, dk, dv, dla = grads
+        dinit = torch.empty(states, dtype=torch.float32, device=q.device) if return_d_init else None
+        workspace = _workspace(_lib.dr_linrec_bwd_workspace_bytes, desc, workspace, q.device,
+                               "dr_linrec_bwd_workspace_bytes")
+        rc = _lib.dr_linrec_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                                _ptr(cu_seqlens), _ptr(init_state), _ptr(d_out),
+                                _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dla),
+                                _ptr(dinit), _ptr(workspace), _bytes(workspace),
+                                _stream_handle(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_linrec_bwd")
+    return dq, dk, dv, dla, dinit
+
+
+def linrec_step(q, k, v, log_alpha, state, *, out=None, out_dtype=None, stream=None):
+    """One token of linrec_fwd for every chain (dr_linrec_step): ``state`` fp32 [B,H,dk,dv] is
+    updated in place.  q, k [B,H,dk]; v [B,H,dv]; log_alpha None or fp32 [B,H].  Returns out
+    [B,H,dv]."""
+    _on_one_device(q, k, v, log_alpha, state, out)
+    if q.dim() != 3 or v.dim() != 3 or k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+        raise ValueError("inconsistent shapes")
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    odt = out_dtype or (q.dtype if out is None else out.dtype)
+    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype or odt not in _DT:
+        raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
+    if state is None:
+        raise ValueError("state must be given")
+    _like(state, (B, H, dk, dv), torch.float32, "state")
+    _like(log_alpha, (B, H), torch.float32, "log_alpha")
+    _like(out, (B, H, dv), odt, "out")
+    desc = StepDesc(B, H, dk, dv, _DT[q.dtype], _DT[odt],
+                    DR_GATE_NONE if log_alpha is None else DR_GATE_SCALAR, 0)
+    if out is None:
+        with _stream_scope(stream):
+            out = torch.empty((B, H, dv), dtype=odt, device=q.device)
+    rc = _lib.dr_linrec_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                             _ptr(state), _ptr(out), _stream_handle(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_linrec_step")
+    return out
+
+
+# ------------------------------------------------------------ queries and keys
+_NORMS = {None: DR_NORM_NONE, "none": DR_NORM_NONE, "l2": DR_NORM_L2, "rms": DR_NORM_RMS}
+_LAYOUTS = {"half": DR_ROPE_HALF, "interleaved": DR_ROPE_INTERLEAVED}
+
+
+def rope_table(rot: int, *, base: float = 10000.0, scaling=None, device="cuda"):
+    """The rotation's frequencies for qk_norm_rope (dr_rope_table), int64 [rot / 2] on
+    ``device``: base^(-2 i / rot), scaled for long contexts by ``scaling``: None,
+    {"kind": "linear", "factor"} or {"kind": "by_parts", "factor", "original", "low",
+    "high"} (include/dr.h has the formulas)."""
+    sc = dict(scaling or {})
+    kind = sc.pop("kind", None)
+    kinds = {None: (DR_ROPE_PLAIN, ()), "linear": (DR_ROPE_LINEAR, ("factor",)),
+             "by_parts": (DR_ROPE_BY_PARTS, ("factor", "original", "low", "high"))}
+    if kind not in kinds or set(sc) != set(kinds[kind][1]):
+        raise ValueError(f"scaling {scaling!r}: kind linear (factor) or by_parts (factor, original, low, high)")
+    t = torch.empty(max(rot, 0) // 2, dtype=torch.int64)
+    rc = _lib.dr_rope_table(rot, base, kinds[kind][0], *(float(sc.get(n, 0.0)) for n in
+                            ("factor", "original", "low", "high")), _ptr(t) if t.numel() else
+                            ctypes.c_void_p(8))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_rope_table")
+    return t.to(device)
+
+
+def _rows_of(x, what):
+    """(rows, heads, d, elements between rows) of [rows, H, d] or [B, T, H, d]."""
+    if x.dim() not in (3, 4):
+        raise ValueError(f"{what} must be [rows, H, d] or [B, T, H, d]")
+    H, d = x.shape[-2:]
+    if x.numel() and ((d > 1 and x.stride(-1) != 1) or (H > 1 and x.stride(-2) != d)):
+        raise ValueError(f"{what}: a row's heads must lie behind one another")
+    n = x.shape[0] if x.dim() == 3 else x.shape[0] * x.shape[1]
+    step = x.stride(-3) if x.shape[-3] > 1 else (x.stride(0) if x.dim() == 4 and x.shape[0] > 1 else H * d)
+    if x.dim() == 4 and x.shape[0] > 1 and x.shape[1] > 1 and x.stride(0) != x.shape[1] * step:
+        raise ValueError(f"{what}: rows must be equally far apart")
+    return n, H, d, step
+
+
+def _rows_into(given, x, what):
+    """The buffer to write x-shaped rows into and the distance of its rows."""
+    if x is None:
+        if given is not None:
+            raise ValueError(f"{what} without its input")
+        return None, 0
+    if given is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), 0
+    if not given.is_cuda or given.get_device() != x.get_device() or given.dtype != x.dtype \
+            or given.shape != x.shape:
+        raise ValueError(f"{what} must have its input's shape, dtype and device")
+    return given, _rows_of(given, what)[3]
+
+
+def _qk_desc(q, k, table, positions, offset, norm, wq, wk, eps, layout, rot_scale):
+    dev = torch.cuda.current_device()
+    for t in (q, k):
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("q and k must be on the current CUDA device")
+    _on_one_device(table, positions, wq, wk)
+    if q.dtype not in _DT or (k is not None and k.dtype != q.dtype):
+        raise ValueError("q and k must share one dtype (float32 or bfloat16)")
+    if norm not in _NORMS or layout not in _LAYOUTS:
+        raise ValueError("norm must be none, l2 or rms; layout half or interleaved")
+    n, Hq, d, qs = _rows_of(q, "q")
+    Hk, ks = 0, 0
+    if k is not None:
+        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
+            raise ValueError("inconsistent shapes")
+        _, Hk, _, ks = _rows_of(k, "k")
+    if table is not None and (table.dtype != torch.int64 or table.dim() != 1):
+        raise ValueError("table must be rope_table's int64 [rot / 2]")
+    if positions is not None and (positions.dtype != torch.int64 or positions.shape != q.shape[:-2]):
+        raise ValueError("positions must be int64, one per row")
+    _like(wq, (d,), torch.float32, "wq")
+    _like(wk, (d,), torch.float32, "wk")
+    return QkNormRopeDesc(n, q.shape[1] if q.dim() == 4 else 0, int(offset), Hq, Hk, d,
+                          0 if table is None else 2 * table.numel(), qs, ks, 0, 0, _DT[q.dtype],
+                          _NORMS[norm], _LAYOUTS[layout], 0, eps, rot_scale)
+
+
+def qk_norm_rope(q, k, table, *, positions=None, offset: int = 0, norm="rms", wq=None, wk=None,
+                 eps: float = 1e-6, layout="half", rot_scale: float = 1.0, q_out=None, k_out=None,
+                 stream=None):
+    """Every head's row of q [..., Hq, d] and k [..., Hk, d] (or None) normalised (``norm``:
+    "rms" or "l2" with optional fp32 weights wq, wk [d], or "none") and its first
+    2 * len(table) values rotated by the row's position (dr_qk_norm_rope).  Leading shape
+    [rows] or [B, T]; rows may be strided, as parts of a fused projection's output.
+    ``positions`` int64, one per row, or None: offset + t within each of the B sequences.
+    Returns (q_out, k_out): new contiguous tensors, or the given buffers (strided rows, or
+    q, k themselves)."""
+    desc = _qk_desc(q, k, table, positions, offset, norm, wq, wk, eps, layout, rot_scale)
+    with _stream_scope(stream):
+        q_out, desc.q_out_stride = _rows_into(q_out, q, "q_out")
+        k_out, desc.k_out_stride = _rows_into(k_out, k, "k_out")
+    rc = _lib.dr_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(table),
+                              _ptr(positions), _ptr(q_out), _ptr(k_out), _stream_handle(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, table, dq_out, dk_out, *, positions=None, offset: int = 0, norm="rms",
+                     wq=None, wk=None, eps: float = 1e-6, layout="half", rot_scale: float = 1.0,
+                     dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of qk_norm_rope from its inputs and the outputs' gradients (contiguous):
+    (dq, dk, dwq, dwk), the last two fp32 [d] or None without weights.  ``dq``, ``dk``:
+    buffers to write into (strided rows, as parts of a fused gradient, or q, k
+    themselves)."""
+    desc = _qk_desc(q, k, table, positions, offset, norm, wq, wk, eps, layout, rot_scale)
+    _on_one_device(dq_out, dk_out, workspace)
+    if dq_out.dtype != q.dtype or dq_out.shape != q.shape or (dk_out is None) != (k is None):
+        raise ValueError("dq_out, dk_out must have q's, k's dtype and shape")
+    if k is not None and (dk_out.dtype != k.dtype or dk_out.shape != k.shape):
+        raise ValueError("dq_out, dk_out must have q's, k's dtype and shape")
+    with _stream_scope(stream):
+        dq, desc.q_out_stride = _rows_into(dq, q, "dq")
+        dk, desc.k_out_stride = _rows_into(dk, k, "dk")
+        dwq = None if wq is None else torch.empty_like(wq)
+        dwk = None if wk is None else torch.empty_like(wk)
+        if dwq is not None or dwk is not None:
+            workspace = _workspace(_lib.dr_qk_norm_rope_bwd_workspace_bytes, desc, workspace, q.device,
+                                   "dr_qk_norm_rope_bwd_workspace_bytes")
+        rc = _lib.dr_qk_norm_rope_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
+                                      _ptr(table), _ptr(positions), _ptr(dq_out), _ptr(dk_out),
+                                      _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                                      _bytes(workspace), _stream_handle(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk

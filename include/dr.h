@@ -298,6 +298,147 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
                          const float *init_state, void *out, float *final_state,
                          dr_stream_t stream);
 
+/*
+ * The additive gated linear recurrence: the members of the family without the delta rule's
+ * correction ("Linear attention" on the page "NLP: linear attention summary"; the scalar
+ * decay of "Transformer notes (5): linear attention optimisations", summary and Q&A),
+ *
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t,
+ *
+ * alpha_t = exp(log_alpha_t) a scalar per head and token (DR_GATE_SCALAR) or 1
+ * (DR_GATE_NONE).  It is no case of dr_chunk_fwd: there one beta scales both the write and
+ * the correction.  The per-channel gate is not built for it (DR_ERR_UNSUPPORTED).
+ *
+ *   - B sequences of T tokens, laid out as for dr_chunk_fwd; or (N >= 1, B = 1) N sequences
+ *     packed behind one another in the T rows: sequence n has the rows cu_seqlens[n] ..
+ *     cu_seqlens[n + 1] - 1.  cu_seqlens is a device array of N + 1 non-decreasing values in
+ *     0 .. T (values outside are clamped; the sequences must not share rows); a sequence may
+ *     be empty: its state passes through.  Rows of no sequence are neither read for
+ *     another row's sake nor written.  States are [N, H, dk, dv] (N = B if not packed).
+ *   - log_alpha and d_log_alpha need 4-byte, cu_seqlens 8-byte alignment.
+ *   - log_alpha = -inf is a full reset (alpha = 0).  Inputs of the sequences' rows are
+ *     otherwise finite; values in rows of no sequence do not matter.
+ */
+typedef struct {
+    int64_t B, T, H, dk, dv;  /* B, H >= 1; T >= 0; dk, dv in {64, 128}                */
+    int64_t N;                /* 0: B sequences of T tokens; >= 1: packed sequences     */
+    int32_t in_dtype;         /* DR_F32 or DR_BF16: q, k, v and their gradients         */
+    int32_t out_dtype;        /* DR_F32 or DR_BF16: out, d_out                          */
+    int32_t gate;             /* DR_GATE_NONE or DR_GATE_SCALAR                         */
+    int32_t reserved;         /* must be 0                                              */
+} dr_linrec_desc;
+
+/*
+ * Forward.  q, k, v, log_alpha, init_state, out, final_state as for dr_chunk_fwd (final_state
+ * may equal init_state); cu_seqlens NULL unless N >= 1.  out overlaps no input or state.
+ * Sums are fp32.  fp32 inputs: fp32 arithmetic throughout.  bf16 inputs: the state keeps at
+ * least 16 bits of every product's factors and fp32 sums.  Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED,
+ * DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace rules as for dr_chunk_fwd; its size depends
+ * only on the descriptor.
+ */
+int dr_linrec_fwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);
+int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const void *k, const void *v,
+                  const float *log_alpha, const int64_t *cu_seqlens, const float *init_state,
+                  void *out, float *final_state, void *workspace, size_t workspace_bytes,
+                  dr_stream_t stream);
+
+/*
+ * Backward: the gradients of <d_out, out> + <d_final_state, final_state>.
+ *   d_out          [B, T, H, dv]; in_dtype = out_dtype here (DR_ERR_UNSUPPORTED otherwise)
+ *   d_final_state  NULL (zero) or fp32 [N, H, dk, dv]
+ *   dq, dk, dv     in_dtype (written);  d_log_alpha fp32 [B, T, H] (written), NULL exactly
+ *                  when gate is NONE;  d_init_state NULL or fp32 [N, H, dk, dv] (written),
+ *                  may equal d_final_state
+ * Written buffers overlap neither each other nor an input otherwise.  Results do not depend
+ * on the order in which the GPU runs its blocks.  Statuses as for dr_linrec_fwd.
+ */
+int dr_linrec_bwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);
+int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const void *k, const void *v,
+                  const float *log_alpha, const int64_t *cu_seqlens, const float *init_state,
+                  const void *d_out, const float *d_final_state, void *dq, void *dk, void *dv,
+                  float *d_log_alpha, float *d_init_state, void *workspace,
+                  size_t workspace_bytes, dr_stream_t stream);
+
+/*
+ * One token for B x H chains, the state updated in place: layouts and checks of
+ * dr_recurrent_step, without beta (gate NONE or SCALAR).  log_alpha needs 4-byte alignment.
+ */
+int dr_linrec_step(const dr_step_desc *desc, const void *q, const void *k, const void *v,
+                   const float *log_alpha, float *state, void *out, dr_stream_t stream);
+
+/*
+ * Queries and keys as a layer hands them to the recurrences (or to an attention layer
+ * between them): every head's row normalised and rotated by its position, in one pass.
+ *
+ *     y = w x / sqrt(sum(x^2) / n + eps)    n = d (DR_NORM_RMS) or 1 (DR_NORM_L2);
+ *                                           y = x without a norm
+ *     (y_a, y_b) -> s (y_a cos p f_i - y_b sin p f_i,  y_b cos p f_i + y_a sin p f_i)
+ *
+ * for the pairs i < rot / 2 of the first rot values: (a, b) = (i, i + rot / 2) in the half
+ * layout, (2 i, 2 i + 1) in the interleaved one; p is the row's position, s rot_scale.  The
+ * other d - rot values are not rotated.  Statistics are fp32; angles are exact to 2^-31 of a
+ * turn at any position (dr_rope_table).
+ */
+enum { DR_NORM_NONE = 0, DR_NORM_L2 = 1, DR_NORM_RMS = 2 };
+enum { DR_ROPE_HALF = 0, DR_ROPE_INTERLEAVED = 1 };
+/* How the frequencies f_i = base^(-2 i / rot) are scaled for contexts longer than the
+   trained one: not at all; f_i / factor; or by parts, f_i (w + (1 - w) / factor) with
+   w = clamp((r - low) / (high - low), 0, 1) and r = original f_i / (2 pi), the turns within
+   the original context: fast pairs stay, slow ones are interpolated. */
+enum { DR_ROPE_PLAIN = 0, DR_ROPE_LINEAR = 1, DR_ROPE_BY_PARTS = 2 };
+
+typedef struct {
+    int64_t n_tok;            /* rows (tokens) of all sequences, >= 0                    */
+    int64_t seq_len, pos0;    /* without positions: row t is at pos0 + t mod seq_len
+                                 (seq_len 0: n_tok)                                      */
+    int64_t Hq, Hk;           /* query heads >= 1, key heads >= 0 (0: no k)              */
+    int64_t d, rot;           /* head width 64, 128 or 256; rotated part, a multiple of
+                                 16 in 0 .. d                                            */
+    int64_t q_stride, k_stride; /* elements between the rows of q, k: 0 for contiguous,
+                                 else at least Hq d (Hk d), multiples of 16 bytes        */
+    int64_t q_out_stride, k_out_stride; /* the same of what is written: q_out, k_out, or
+                                 dq, dk of the gradient                                  */
+    int32_t dtype;            /* DR_F32 or DR_BF16                                       */
+    int32_t norm, layout;     /* DR_NORM_*, DR_ROPE_HALF or DR_ROPE_INTERLEAVED          */
+    int32_t reserved;         /* must be 0                                               */
+    float eps, rot_scale;     /* eps >= 0                                                */
+} dr_qk_norm_rope_desc;
+
+/* HOST function: the rot / 2 frequencies as turns a position in units of 2^-64 turns, into
+   the host array `table`, which the caller copies to the device and keeps.  base > 1,
+   factor >= 1 (ignored for PLAIN); original, low < high for BY_PARTS only.  Returns DR_OK,
+   DR_ERR_INVALID or DR_ERR_UNSUPPORTED (rot no multiple of 16). */
+int dr_rope_table(int64_t rot, double base, int32_t scaling, double factor, double original,
+                  double low, double high, uint64_t *table);
+
+/*
+ *   q, k           [n_tok, Hq | Hk, d] dtype, rows q_stride, k_stride apart
+ *   wq, wk         NULL (ones) or fp32 [d]; NULL without a norm
+ *   table          device copy of dr_rope_table's array (NULL when rot is 0)
+ *   positions      NULL or int64 [n_tok] (device), any values
+ *   q_out, k_out   [n_tok, Hq | Hk, d], rows q_out_stride, k_out_stride apart (written);
+ *                  may be q, k themselves, with their strides; no written row shares a
+ *                  byte with another or an input's otherwise
+ * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
+ */
+int dr_qk_norm_rope(const dr_qk_norm_rope_desc *desc, const void *q, const void *k,
+                    const float *wq, const float *wk, const uint64_t *table,
+                    const int64_t *positions, void *q_out, void *k_out, dr_stream_t stream);
+
+/*
+ * Its gradients, from the inputs of the forward and the outputs' gradients dq_out, dk_out
+ * (contiguous, dtype).  dq, dk are rows q_out_stride, k_out_stride apart (parts of one fused
+ * gradient's rows, for instance) and may be q, k themselves; dwq, dwk fp32 [d] or NULL
+ * (not returned; only with wq, wk).  Workspace as for dr_chunk_fwd, needed for dwq or dwk only.
+ * The sums' order is fixed: equal inputs give equal results.
+ */
+int dr_qk_norm_rope_bwd_workspace_bytes(const dr_qk_norm_rope_desc *desc, size_t *bytes);
+int dr_qk_norm_rope_bwd(const dr_qk_norm_rope_desc *desc, const void *q, const void *k,
+                        const float *wq, const float *wk, const uint64_t *table,
+                        const int64_t *positions, const void *dq_out, const void *dk_out,
+                        void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                        size_t workspace_bytes, dr_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the library's sticky device status word
    on the current device (DR_OK, or DR_ERR_TIMEOUT if a bounded device wait expired), or
    DR_ERR_CUDA if the synchronisation itself failed. */

@@ -1,0 +1,425 @@
+"""The additive gated linear recurrence: forward, backward and single token against a plain
+token loop in 64 bits.
+
+Tolerances.  u = 2^-24 (fp32), 2^-8 = half a bf16 step.  A state or output is a sum of up to
+n = min(T, memory) + dk products; fp32 sums of random-sign terms are off by about sqrt(n) u of
+their root mean square, at most n u: with n <= 2^12 here the bound 2^12 u = 2.5e-4 of the RMS
+holds for the worst element, taken relative to max(RMS, |value|).  A bf16 output adds its
+rounding, 2^-8 of the value, and the kernels' bf16 operands (each rounded by at most 2^-8 of its
+value, of random sign in sums of many: 3 of them at the worst element's six standard
+deviations of 2^-8 / sqrt(3) each) at most 6 sqrt(3) / sqrt(3) 2^-8 = 2.4e-2 of the RMS.
+fp32 results of bf16 problems (states, the log-decay gradient) carry the fp32 bound.
+"""
+import math
+
+import pytest
+import torch
+
+F32_TOL = 2.5e-4
+BF16_TOL = 2.4e-2
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def dr():
+    import gated_delta_rule_15_gb300.dr as m
+    return m
+
+
+def reference(q, k, v, la, s0, cu=None, do=None, ds=None):
+    """Token loop in 64 bits over each sequence: out, final state and, with d_out, the
+    gradients.  Rows of no sequence are NaN."""
+    q, k, v = (x.double().cpu() for x in (q, k, v))
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    a = torch.ones(B, T, H, dtype=torch.float64) if la is None else la.double().cpu().exp()
+    spans = [(b, 0, T) for b in range(B)] if cu is None else \
+        [(0, int(x), int(y)) for x, y in zip(cu[:-1], cu[1:])]
+    N = len(spans)
+    nan = float("nan")
+    out = torch.full((B, T, H, dv), nan, dtype=torch.float64)
+    fin = torch.zeros(N, H, dk, dv, dtype=torch.float64)
+    g = None
+    if do is not None:
+        do = do.double().cpu()
+        g = dict(dq=torch.full_like(q, nan), dk=torch.full_like(k, nan), dv=torch.full_like(v, nan),
+                 dla=torch.full_like(a, nan), d0=torch.zeros_like(fin))
+    for n, (b, lo, hi) in enumerate(spans):
+        s = torch.zeros(H, dk, dv, dtype=torch.float64) if s0 is None else s0[n].double().cpu().clone()
+        states = [s]
+        for t in range(lo, hi):
+            s = a[b, t, :, None, None] * s + k[b, t, :, :, None] * v[b, t, :, None, :]
+            states.append(s)
+            out[b, t] = torch.einsum("hij,hi->hj", s, q[b, t])
+        fin[n] = s
+        if g is None:
+            continue
+        d = torch.zeros(H, dk, dv, dtype=torch.float64) if ds is None else ds[n].double().cpu().clone()
+        for t in range(hi - 1, lo - 1, -1):
+            g["dq"][b, t] = torch.einsum("hij,hj->hi", states[t - lo + 1], do[b, t])
+            d = d + q[b, t, :, :, None] * do[b, t, :, None, :]
+            g["dk"][b, t] = torch.einsum("hij,hj->hi", d, v[b, t])
+            g["dv"][b, t] = torch.einsum("hij,hi->hj", d, k[b, t])
+            d = a[b, t, :, None, None] * d
+            g["dla"][b, t] = (d * states[t - lo]).sum((-1, -2))
+        g["d0"][n] = d
+    return out, fin, g
+
+
+def inputs(B, T, H, dk, dv, dtype, gate=True, N=0, init=True, strength=0.1, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=gen)
+    q, k, v, do = rn(B, T, H, dk), rn(B, T, H, dk), rn(B, T, H, dv), rn(B, T, H, dv)
+    q, k = q / q.norm(dim=-1, keepdim=True), k / k.norm(dim=-1, keepdim=True)
+    la = -strength * torch.rand((B, T, H), generator=gen) if gate else None
+    M = N or B
+    s0, ds = (0.3 * rn(M, H, dk, dv), rn(M, H, dk, dv)) if init else (None, None)
+    dt = DT[dtype]
+    return dict(q=q.to(dt), k=k.to(dt), v=v.to(dt), la=la, s0=s0, do=do.to(dt), ds=ds)
+
+
+def cuda(d):
+    return {n: None if x is None else x.cuda() for n, x in d.items()}
+
+
+def check(got, ref, dtype, what):
+    """Worst |got - ref| over max(RMS, |ref|) where ref is a number."""
+    got = got.double().cpu()
+    there = ~torch.isnan(ref)
+    assert torch.isfinite(got[there]).all(), what
+    if not there.any():
+        return
+    r = ref[there]
+    rms = r.square().mean().sqrt().item()
+    err = ((got[there] - r).abs() / r.abs().clamp(min=max(rms, 1e-30))).max().item()
+    tol = F32_TOL if dtype == "f32" else BF16_TOL
+    assert err <= tol, f"{what}: {err:.3e} > {tol:.1e}"
+
+
+SHAPES = [  # B, T, H, dk, dv
+    (1, 1, 1, 64, 64), (2, 1, 3, 128, 128), (1, 15, 2, 64, 128), (2, 16, 2, 128, 64), (1, 63, 1, 128, 128),
+    (2, 64, 3, 128, 128), (1, 65, 2, 128, 128), (3, 130, 2, 64, 64), (1, 257, 2, 128, 128), (1, 700, 1, 128, 128),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("B,T,H,dk,dv", SHAPES)
+def test_forward_and_backward(dr, B, T, H, dk, dv, gate, dtype):
+    d = inputs(B, T, H, dk, dv, dtype, gate=gate, seed=T)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
+    check(o, out, dtype, "out")
+    check(f, fin, "f32", "final_state")
+    dq, dk_, dv_, dla, d0 = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
+    for x, n in ((dq, "dq"), (dk_, "dk"), (dv_, "dv")):
+        check(x, g[n], dtype, n)
+    check(d0, g["d0"], "f32", "d_init_state")
+    if gate:
+        check(dla, g["dla"], "f32", "d_log_alpha")
+    else:
+        assert dla is None
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_states(dr, dtype):
+    """Zero initial state, no final state's gradient, neither returned."""
+    d = inputs(2, 150, 2, 128, 128, dtype, init=False, seed=5)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], None, do=d["do"])
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], return_final_state=False)
+    assert f is None
+    check(o, out, dtype, "out")
+    dq, dk_, dv_, dla, d0 = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], None, c["do"], return_d_init=False)
+    assert d0 is None
+    for x, n in ((dq, "dq"), (dk_, "dk"), (dv_, "dv")):
+        check(x, g[n], dtype, n)
+    check(dla, g["dla"], "f32", "d_log_alpha")
+
+
+PACKED = [  # cu_seqlens, rows
+    ([0, 1], 1), ([0, 0, 0], 5), ([0, 64, 64, 65, 200], 200), ([3, 40, 41, 41, 300, 811], 900), ([0, 128, 256], 256),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d_", [64, 128])
+@pytest.mark.parametrize("cu,T", PACKED)
+def test_packed_sequences(dr, cu, T, d_, dtype):
+    """Empty and one-token sequences, ends inside and on tiles; rows of no sequence hold NaN and
+    infinity on the way in and are left alone on the way out."""
+    N, H = len(cu) - 1, 2
+    d = inputs(1, T, H, d_, d_, dtype, N=N, seed=T)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu, d["do"], d["ds"])
+    for n in ("q", "k", "v", "la", "do"):
+        d[n][:, :cu[0]] = float("nan")
+        d[n][:, cu[-1]:] = float("inf")
+    c = cuda(d)
+    cuc = torch.tensor(cu, dtype=torch.int64).cuda()
+    o = torch.full_like(c["v"], 7.0)
+    _, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc, out=o)
+    check(o, out, dtype, "out")
+    check(f, fin, "f32", "final_state")
+    gr = [torch.full_like(c[n], 7.0) for n in ("q", "k", "v", "la")]
+    dq, dk_, dv_, dla, d0 = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc,
+                                          grads=gr)
+    for x, n in ((dq, "dq"), (dk_, "dk"), (dv_, "dv")):
+        check(x, g[n], dtype, n)
+    check(dla, g["dla"], "f32", "d_log_alpha")
+    check(d0, g["d0"], "f32", "d_init_state")
+    for x in (o, dq, dk_, dv_, dla):
+        x = x.float().cpu()
+        assert (x[:, :cu[0]] == 7).all() and (x[:, cu[-1]:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_neighbouring_sequences_do_not_leak(dr, dtype):
+    """A sequence's results do not change with what its neighbours hold, NaN included."""
+    cu = [0, 70, 130, 201]
+    d = cuda(inputs(1, 201, 2, 128, 128, dtype, N=3, seed=9))
+    cuc = torch.tensor(cu, dtype=torch.int64).cuda()
+    run = lambda x: (dr.linrec_fwd(x["q"], x["k"], x["v"], x["la"], x["s0"], cu_seqlens=cuc),
+                     dr.linrec_bwd(x["q"], x["k"], x["v"], x["la"], x["s0"], x["do"], x["ds"], cu_seqlens=cuc))
+    (o1, f1), g1 = run(d)
+    e = {n: x.clone() for n, x in d.items()}
+    for n in ("q", "k", "v", "la", "do"):
+        e[n][:, :70] = float("nan")
+        e[n][:, 130:] = float("inf")
+    (o2, f2), g2 = run(e)
+    assert torch.equal(o1[:, 70:130], o2[:, 70:130]) and torch.equal(f1[1], f2[1])
+    for a, b in zip(g1[:4], g2[:4]):
+        assert torch.equal(a[:, 70:130], b[:, 70:130])
+    assert torch.equal(g1[4][1], g2[4][1])
+
+
+@pytest.mark.gpu
+def test_offsets_outside_the_rows_are_clamped(dr):
+    d = cuda(inputs(1, 100, 1, 128, 128, "bf16", N=3, seed=3))
+    bad = torch.tensor([-50, 40, 30, 1 << 40], dtype=torch.int64).cuda()
+    good = torch.tensor([0, 40, 40, 100], dtype=torch.int64).cuda()     # 40..30 is empty, 30..100 runs
+    o, f = dr.linrec_fwd(d["q"], d["k"], d["v"], d["la"], d["s0"], cu_seqlens=bad)
+    o2, f2 = dr.linrec_fwd(d["q"], d["k"], d["v"], d["la"], d["s0"], cu_seqlens=good)
+    torch.cuda.synchronize()
+    assert torch.equal(f[:2], f2[:2]) and torch.isfinite(f).all()
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("strength", [0.0, 1e-3, 1.0, 5.0, 60.0])
+def test_weak_and_strong_decay(dr, strength, dtype):
+    """Up to exp(-60 * 64) within a chunk.  The log-decay gradient of strong decays is small:
+    its bound is that of its own size."""
+    d = inputs(1, 400, 2, 128, 128, dtype, strength=strength, seed=11)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
+    check(o, out, dtype, "out")
+    check(f, fin, "f32", "final_state")
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
+    for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
+        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_full_resets(dr, dtype):
+    """log_alpha = -inf forgets everything: the tokens behind a reset do not see those before."""
+    d = inputs(1, 300, 2, 128, 128, dtype, seed=13)
+    for t in (0, 5, 63, 64, 65, 66, 200, 299):
+        d["la"][:, t] = -math.inf
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
+    check(o, out, dtype, "out")
+    check(f, fin, "f32", "final_state")
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
+    for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
+        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n)
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences(dr):
+    """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
+    function is quadratic in q, k, v and the state, so the quotient is exact up to its
+    rounding, about 2 sqrt(n) u L / step with n = 10^5 terms of L and step 2^-5: 2e-3."""
+    d = cuda(inputs(1, 90, 2, 64, 64, "f32", seed=21))
+    loss = lambda x: sum((a.double() * b.double()).sum() for a, b in
+                         zip(dr.linrec_fwd(x["q"], x["k"], x["v"], x["la"], x["s0"]), (d["do"], d["ds"])))
+    grads = dr.linrec_bwd(d["q"], d["k"], d["v"], d["la"], d["s0"], d["do"], d["ds"])
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    for n, gr in zip(("q", "k", "v", "la", "s0"), grads):
+        dirn = torch.randn(d[n].shape, generator=gen, device="cuda")
+        step = 2.0 ** -5 if n != "la" else 2.0 ** -9
+        lo, hi = (dict(d, **{n: d[n] + x * dirn}) for x in (-step, step))
+        num = ((loss(hi) - loss(lo)) / (2 * step)).item()
+        ana = (gr.double() * dirn.double()).sum().item()
+        assert abs(num - ana) <= 2e-3 * max(abs(ana), (gr.double().norm() * dirn.double().norm()).item() / math.sqrt(gr.numel())), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("B,H,dk,dv", [(1, 1, 64, 64), (3, 5, 128, 64), (2, 7, 64, 128), (200, 3, 128, 128)])
+def test_step_continues_the_forward(dr, B, H, dk, dv, gate, dtype, out_dtype):
+    d = inputs(B, 4, H, dk, dv, dtype, gate=gate, seed=B)
+    out, fin, _ = reference(d["q"], d["k"], d["v"], d["la"], d["s0"])
+    c = cuda(d)
+    at = lambda x, t: None if x is None else x[:, t].contiguous()
+    s = c["s0"].clone()
+    for t in range(4):
+        o = dr.linrec_step(at(c["q"], t), at(c["k"], t), at(c["v"], t), at(c["la"], t), s, out_dtype=DT[out_dtype])
+        check(o, out[:, t], "f32" if out_dtype == "f32" else "bf16", f"out {t}")
+    check(s, fin, "f32", "state")
+
+
+@pytest.mark.gpu
+def test_state_carried_in_place_and_mixed_output(dr):
+    """Two halves with the state carried in one tensor equal the whole; fp32 outputs of bf16
+    inputs."""
+    d = inputs(2, 192, 2, 128, 128, "bf16", seed=17)
+    out, fin, _ = reference(d["q"], d["k"], d["v"], d["la"], d["s0"])
+    c = cuda(d)
+    s = c["s0"].clone()
+    for a, b in ((0, 100), (100, 192)):
+        x = [c[n][:, a:b].contiguous() for n in ("q", "k", "v", "la")]
+        o, _ = dr.linrec_fwd(*x, s, final_state=s, out_dtype=torch.float32)
+        assert o.dtype == torch.float32
+        check(o, out[:, a:b], "bf16", "out")
+    check(s, fin, "f32", "state")
+
+
+@pytest.mark.gpu
+def test_no_tokens(dr):
+    """T = 0: the state and its gradient pass through."""
+    s = torch.randn(2, 3, 64, 64).cuda()
+    e = torch.empty(2, 0, 3, 64).cuda()
+    la = torch.empty(2, 0, 3).cuda()
+    o, f = dr.linrec_fwd(e, e, e, la, s)
+    assert o.shape == (2, 0, 3, 64) and torch.equal(f, s)
+    g = dr.linrec_bwd(e, e, e, la, s, e, s)
+    assert torch.equal(g[4], s)
+
+
+@pytest.mark.gpu
+def test_equal_calls_give_equal_bits(dr):
+    c = cuda(inputs(2, 500, 3, 128, 128, "bf16", seed=23))
+    runs = [(*dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"]),
+             *dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])) for _ in range(3)]
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], r))
+
+
+@pytest.mark.gpu
+def test_other_stream_and_graph(dr):
+    """On a side stream, two streams at once, and captured and replayed on new inputs."""
+    c = cuda(inputs(2, 200, 2, 128, 128, "bf16", seed=29))
+    args = [c[n] for n in ("q", "k", "v", "la", "s0")]
+    want = (*dr.linrec_fwd(*args), *dr.linrec_bwd(*args, c["do"], c["ds"]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [(*dr.linrec_fwd(*args, stream=s), *dr.linrec_bwd(*args, c["do"], c["ds"], stream=s)) for s in streams]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = (*dr.linrec_fwd(*args), *dr.linrec_bwd(*args, c["do"], c["ds"]))
+    e = cuda(inputs(2, 200, 2, 128, 128, "bf16", seed=31))
+    for n in c:
+        c[n].copy_(e[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    want = (*dr.linrec_fwd(*args), *dr.linrec_bwd(*args, c["do"], c["ds"]))
+    assert all(torch.equal(a, b) for a, b in zip(want, res))
+
+
+# ---------------------------------------------------------------- refusals, without a GPU
+def _desc(dr, **kw):
+    d = dict(B=2, T=100, H=3, dk=128, dv=128, N=0, in_dtype=dr.DR_BF16, out_dtype=dr.DR_BF16,
+             gate=dr.DR_GATE_SCALAR, reserved=0)
+    d.update(kw)
+    return dr.LinrecDesc(**d)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dk=96), -2), (dict(dv=32), -2), (dict(B=0), -1), (dict(H=0), -1), (dict(T=-1), -1), (dict(N=-1), -1),
+    (dict(gate=3), -1), (dict(gate=2), -2), (dict(in_dtype=5), -1), (dict(out_dtype=-1), -1), (dict(reserved=1), -1),
+    (dict(N=4), -1), (dict(B=1, N=1 << 21), -2), (dict(T=1 << 31), -2), (dict(H=1 << 17), -2)])
+def test_bad_descriptors(dr, bad, status):
+    import ctypes
+    n = ctypes.c_size_t(0)
+    for f in (dr.lib().dr_linrec_fwd_workspace_bytes, dr.lib().dr_linrec_bwd_workspace_bytes):
+        assert f(ctypes.byref(_desc(dr, **bad)), ctypes.byref(n)) == status
+
+
+no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake-pointer checks run only without a GPU")
+
+
+@no_gpu_only
+def test_host_side_errors(dr):
+    """Addresses that are never read: every call is refused first."""
+    import ctypes
+    vp = ctypes.c_void_p
+    far = {n: (i + 1) << 36 for i, n in enumerate(
+        ("q", "k", "v", "la", "cu", "s0", "out", "fin", "do", "ds", "dq", "dk", "dv", "dla", "d0", "ws"))}
+
+    def call(f, names, desc, wb=1 << 40, **o):
+        p = [vp(o.get(n, far[n])) if o.get(n, 1) is not None else None for n in names]
+        return f(ctypes.byref(desc), *p, wb, None)
+
+    fwd = lambda desc, **o: call(dr.lib().dr_linrec_fwd, ("q", "k", "v", "la", "cu", "s0", "out", "fin", "ws"), desc, **o)
+    bwd = lambda desc, **o: call(dr.lib().dr_linrec_bwd, ("q", "k", "v", "la", "cu", "s0", "do", "ds", "dq", "dk", "dv",
+                                                        "dla", "d0", "ws"), desc, **o)
+    d = _desc(dr)
+    pk = _desc(dr, B=1, N=3)
+    for n in ("q", "k", "v", "la", "out"):
+        assert fwd(d, **{n: None}) == -1
+        assert fwd(d, **{n: far[n] + (2 if n == "la" else 8)}) == -1
+    assert fwd(pk, cu=None) == -1 and fwd(pk, cu=far["cu"] + 4) == -1
+    assert fwd(d, out=far["q"]) == -1 and fwd(d, out=far["v"] + 16) == -1
+    assert fwd(d, fin=far["s0"] + 1024) == -1
+    for n in ("q", "k", "v", "la", "do", "dq", "dk", "dv", "dla"):
+        assert bwd(d, **{n: None}) == -1
+    assert bwd(_desc(dr, gate=dr.DR_GATE_NONE)) == -1            # a gradient of no gate
+    assert bwd(d, dq=far["q"]) == -1 and bwd(d, dk=far["dv"]) == -1 and bwd(d, d0=far["s0"]) == -1
+    assert bwd(_desc(dr, out_dtype=dr.DR_F32)) == -2
+    assert bwd(d, ws=None) == dr.DR_ERR_WORKSPACE and bwd(d, wb=16) == dr.DR_ERR_WORKSPACE
+    st = dr.StepDesc(4, 2, 128, 128, dr.DR_BF16, dr.DR_BF16, dr.DR_GATE_SCALAR, 0)
+
+    def step(desc, **o):
+        p = [vp(o.get(n, far[n])) if o.get(n, 1) is not None else None for n in ("q", "k", "v", "la", "s0", "out")]
+        return dr.lib().dr_linrec_step(ctypes.byref(desc), *p, None)
+
+    for n in ("q", "k", "v", "la", "s0", "out"):
+        assert step(st, **{n: None}) == -1
+        assert step(st, **{n: far[n] + (2 if n == "la" else 8)}) == -1
+    assert step(st, out=far["s0"]) == -1
+    assert step(dr.StepDesc(4, 2, 128, 128, 1, 1, dr.DR_GATE_CHANNEL, 0)) == -2
+    assert step(dr.StepDesc(4, 2, 128, 96, 1, 1, 1, 0)) == -2
+
+
+def test_host_tensors_are_refused(dr):
+    if not torch.cuda.is_available():
+        pytest.skip("torch.cuda.current_device needs a GPU")
+    x = torch.zeros(1, 4, 1, 64)
+    with pytest.raises(ValueError):
+        dr.linrec_fwd(x, x, x)
+    c = x.cuda()
+    with pytest.raises(ValueError):
+        dr.linrec_fwd(c, c, c, torch.zeros(1, 4, 2).cuda())
+    with pytest.raises(ValueError):
+        dr.linrec_fwd(c.expand(2, 4, 1, 64), c, c)
+    with pytest.raises(ValueError):
+        dr.linrec_fwd(c.half(), c.half(), c.half())
+    with pytest.raises(ValueError):
+        dr.linrec_fwd(c, c, c, cu_seqlens=torch.tensor([0, 4], dtype=torch.int32).cuda())
+    with pytest.raises(dr.DrError):
+        dr.linrec_fwd(torch.zeros(1, 4, 1, 96).cuda(), torch.zeros(1, 4, 1, 96).cuda(), torch.zeros(1, 4, 1, 96).cuda())
