@@ -991,6 +991,8 @@ int launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tc_tensor_map_encoder() { return tensor_map_encoder(); }
+
 bool tc_make_map(CUtensorMap *m, const void *base, int64_t B, int64_t T, int64_t H, bool fp32) {
     return make_map(m, base, B, T, H, fp32);
 }

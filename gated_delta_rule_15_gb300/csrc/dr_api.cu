@@ -11,8 +11,6 @@ namespace dr {
 // Sticky device status word written by kernels whose waits are bounded.
 __device__ int g_device_status = 0;
 
-namespace {
-
 // Device address of g_device_status on the current device (looked up once per device).
 int *device_status_ptr() {
     static int *addr[64] = {nullptr};
@@ -25,6 +23,8 @@ int *device_status_ptr() {
     }
     return addr[dev];
 }
+
+namespace {
 
 // dr_selftest_bounded_wait's kernel: one thread waits, with the chunk kernels' bounded loop
 // (try_wait until a clock64 budget is spent), on an mbarrier that nothing completes; on

@@ -75,6 +75,11 @@ struct LinrecPass {
 constexpr int kSimtCols = 64;    // value columns of one CTA (one "part" of dot and inner)
 int launch_linrec_simt(const LinrecPass &p, cudaStream_t stream);
 
+// Tensor cores: bf16 rows and outputs.  One part.  `status`: the library's device status word.
+bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_bf16);
+size_t linrec_tc_workspace_bytes(const LinrecSeqs &s, int64_t H, int dk, int dv);
+int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStream_t stream);
+
 // dlog a from the two passes' dot products and the inner products; `parts` of each.
 int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int parts, const float *dot_q, const float *dot_k,
                             const float *inner, float *dla, cudaStream_t stream);

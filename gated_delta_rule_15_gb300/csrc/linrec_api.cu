@@ -5,6 +5,9 @@
 #include "linrec.h"
 
 namespace dr {
+
+int *device_status_ptr();   // dr_api.cu
+
 namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -39,21 +42,33 @@ LinrecSeqs seqs_of(const dr_linrec_desc *d, const int64_t *cu) {
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workspace of the backward: the two dot products, the stored states and their inner
-// products (only with a gate).
+bool on_tensor_cores(const dr_linrec_desc *d, const LinrecSeqs &s) {
+    return linrec_tc_supported(s, d->H, d->in_dtype == DR_BF16, d->out_dtype == DR_BF16);
+}
+// What the size of a workspace goes by: packed or not, not where the offsets lie.
+LinrecSeqs shape_of(const dr_linrec_desc *d) {
+    static const int64_t packed = 0;
+    return seqs_of(d, &packed);
+}
+
+// Workspace of the backward: the segments' states; with a gate the two dot products, the
+// stored states and their inner products.
 struct BwdSpace {
     size_t dot_q, dot_k, inner, anchor, bytes;
     int parts;
 };
 BwdSpace bwd_space(const dr_linrec_desc *d) {
     BwdSpace w{};
+    const LinrecSeqs s = shape_of(d);
+    const bool tc = on_tensor_cores(d, s);
+    const size_t segs = tc ? round256(linrec_tc_workspace_bytes(s, d->H, (int)d->dk, (int)d->dv)) : 0;
+    w.bytes = segs;
     if (d->gate == DR_GATE_NONE) return w;
-    const LinrecSeqs s = seqs_of(d, nullptr);
-    w.parts = (int)d->dk / kSimtCols;   // the dq and dk passes' value width is dk
+    w.parts = tc ? 1 : (int)d->dk / kSimtCols;   // the dq and dk passes' value width is dk
     const size_t dot = round256(sizeof(float) * (size_t)w.parts * d->H * s.total);
-    w.dot_q = 0;
-    w.dot_k = dot;
-    w.inner = 2 * dot;
+    w.dot_q = segs;
+    w.dot_k = segs + dot;
+    w.inner = segs + 2 * dot;
     w.anchor = w.inner + round256(sizeof(float) * (size_t)w.parts * linrec_slots(s) * d->H);
     w.bytes = w.anchor + round256(sizeof(float) * (size_t)linrec_slots(s) * d->H * d->dk * d->dv);
     return w;
@@ -68,7 +83,8 @@ extern "C" int dr_linrec_fwd_workspace_bytes(const dr_linrec_desc *desc, size_t 
     if (!bytes) return kErrInvalid;
     const int rc = check_desc(desc);
     if (rc != kOk) return rc;
-    *bytes = 0;
+    const LinrecSeqs s = shape_of(desc);
+    *bytes = on_tensor_cores(desc, s) ? linrec_tc_workspace_bytes(s, desc->H, (int)desc->dk, (int)desc->dv) : 0;
     return kOk;
 }
 
@@ -110,7 +126,10 @@ extern "C" int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const vo
     p.in_bf16 = d.in_dtype == DR_BF16; p.out_bf16 = d.out_dtype == DR_BF16;
     p.q = q; p.k = k; p.v = v; p.la = d.gate == DR_GATE_NONE ? nullptr : log_alpha;
     p.init = init_state; p.fin = final_state; p.out = out;
-    return launch_linrec_simt(p, (cudaStream_t)stream);
+    if (!on_tensor_cores(desc, seqs)) return launch_linrec_simt(p, (cudaStream_t)stream);
+    int *status = device_status_ptr();
+    if (!status) return kErrCuda;
+    return launch_linrec_tc(p, workspace, status, (cudaStream_t)stream);
 }
 
 extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const void *k, const void *v,
@@ -147,6 +166,12 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
     if (w.bytes > 0 && d.T > 0 && (!workspace || workspace_bytes < w.bytes)) return kErrWorkspace;
     if (d.T == 0 && !d_init_state) return kOk;
     char *ws = (char *)workspace;
+    const bool tc = on_tensor_cores(desc, seqs);
+    int *status = tc ? device_status_ptr() : nullptr;
+    if (tc && !status) return kErrCuda;
+    auto pass = [&](const LinrecPass &x) {
+        return tc ? launch_linrec_tc(x, workspace, status, (cudaStream_t)stream) : launch_linrec_simt(x, (cudaStream_t)stream);
+    };
     const bool gate = d.gate != DR_GATE_NONE && d.T > 0;
     LinrecPass p{};
     p.seqs = seqs;
@@ -160,19 +185,19 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
         if (gate) {
             p.y = q; p.dot = (float *)(ws + w.dot_q); p.anchor = (float *)(ws + w.anchor);
         }
-        if ((rc = launch_linrec_simt(p, (cudaStream_t)stream)) != kOk) return rc;
+        if ((rc = pass(p)) != kOk) return rc;
         // dk backwards over dS^T, multiplying it with the stored S
         p.rev = true; p.q = v; p.k = d_out; p.v = q; p.init = d_final_state; p.out = dk;
         if (gate) {
             p.y = k; p.dot = (float *)(ws + w.dot_k); p.inner = (float *)(ws + w.inner);
         }
-        if ((rc = launch_linrec_simt(p, (cudaStream_t)stream)) != kOk) return rc;
+        if ((rc = pass(p)) != kOk) return rc;
     }
     // dv backwards over dS, and the initial state's gradient
     p.dk = (int)d.dk; p.dv = (int)d.dv; p.rev = true; p.state_t = false;
     p.q = k; p.k = q; p.v = d_out; p.init = d_final_state; p.fin = d_init_state; p.out = dv;
     p.y = nullptr; p.dot = p.anchor = p.inner = nullptr;
-    if ((rc = launch_linrec_simt(p, (cudaStream_t)stream)) != kOk) return rc;
+    if ((rc = pass(p)) != kOk) return rc;
     if (!gate) return kOk;
     return launch_linrec_gate_grad(seqs, (int)d.H, w.parts, (const float *)(ws + w.dot_q), (const float *)(ws + w.dot_k),
                                    (const float *)(ws + w.inner), d_log_alpha, (cudaStream_t)stream);

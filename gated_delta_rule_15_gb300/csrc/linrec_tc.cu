@@ -1,0 +1,136 @@
+// linrec_tc.cu -- launches of the additive gated linear recurrence's tensor-core kernel
+// (linrec_tc.cuh): tensor maps, the split of few long chains into segments and the kernel that
+// chains the segments' states.
+#include <cudaTypedefs.h>
+
+#include "linrec_tc.cuh"
+
+namespace dr {
+
+PFN_cuTensorMapEncodeTiled_v12000 tc_tensor_map_encoder();
+
+namespace {
+
+using linrec::TcArgs;
+
+constexpr int kSms = 152;
+
+// [rows, H, d] bf16; boxes of 64 channels x 1 x 64 rows, 128-byte swizzle.  Rows behind the last
+// read as zeros.
+bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t H, int64_t d) {
+    auto enc = tc_tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)(H * d) * 2};
+    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The segments' start states from their sums: per chain, in the order of the pass,
+// start(next) = 2^decay start + sum.  The first segment starts from `init`, which its block
+// reads itself.  One thread per four state entries; in place.
+__global__ void __launch_bounds__(256)
+linrec_chain_kernel(const LinrecSeqs seqs, int H, int quads, bool rev, int64_t seg, const float *__restrict__ init,
+                    float *__restrict__ state, const float *__restrict__ decay) {
+    const int64_t chain = blockIdx.x, n = chain / H;
+    const int h = (int)(chain % H), e = blockIdx.y * 256 + threadIdx.x;
+    int64_t lo, hi;
+    seq_range(seqs, n, lo, hi);
+    const int64_t segs = hi > lo ? (hi - lo + seg - 1) / seg : 1, base = lo / seg + n;
+    if (segs < 2 || e >= quads) return;
+    float4 s = init ? reinterpret_cast<const float4 *>(init)[chain * quads + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    auto at = [&](int64_t i) { return (base + (rev ? segs - 1 - i : i)) * H + h; };
+    float4 *st = reinterpret_cast<float4 *>(state);
+    float4 x = st[at(0) * quads + e];
+    float g = decay[at(0)];
+    for (int64_t i = 1; i < segs; ++i) {
+        const float4 x1 = i + 1 < segs ? st[at(i) * quads + e] : x;   // the next sum, ahead of the store over it
+        const float g1 = i + 1 < segs ? decay[at(i)] : 0.f, f = linrec::ex2(g);
+        s.x = fmaf(f, s.x, x.x); s.y = fmaf(f, s.y, x.y);
+        s.z = fmaf(f, s.z, x.z); s.w = fmaf(f, s.w, x.w);
+        st[at(i) * quads + e] = s;
+        x = x1;
+        g = g1;
+    }
+}
+
+int dispatch(const CUtensorMap *m, const TcArgs &a, bool dot, unsigned grid, cudaStream_t s) {
+    if (a.p.dk == 128)
+        return a.p.dv == 128 ? linrec::launch_128_128(m, a, dot, grid, s) : linrec::launch_128_64(m, a, dot, grid, s);
+    return a.p.dv == 128 ? linrec::launch_64_128(m, a, dot, grid, s) : linrec::launch_64_64(m, a, dot, grid, s);
+}
+
+// Tokens of a segment; at least seqs.total when the chains are not cut.
+//
+// Sequences of one length: the number of segments with the least work on the busiest SM, in
+// chunks of the output launch; the launch that sums the states reads half as much and skips each
+// chain's last segment, and the cut costs about eight chunks' time in launches.
+// Packed sequences: their lengths are on the device.  Segments of half an SM's share of
+// all rows keep one long sequence from holding up the rest; shorter sequences stay whole.
+int64_t segment_tokens(const LinrecSeqs &s, int64_t H) {
+    const int64_t whole = (s.total / kAnchor + 1) * kAnchor, per = kAnchor / linrec::kChunk;
+    if (s.cu) {
+        const int64_t share = (s.total * H / (2 * kSms) + kAnchor - 1) / kAnchor * kAnchor, seg = share < 4 * kAnchor ? 4 * kAnchor : share;
+        return seg < whole ? seg : whole;
+    }
+    const int64_t chains = s.N * H, nc = (s.T + linrec::kChunk - 1) / linrec::kChunk;
+    double best = (double)((chains + kSms - 1) / kSms) * nc;
+    int64_t seg = whole;
+    for (int64_t cut = 2; cut <= kSms && cut * per <= nc; ++cut) {
+        const int64_t len = ((nc + cut - 1) / cut + per - 1) / per * per, segs = (nc + len - 1) / len;
+        const double cost = (double)((chains * segs + kSms - 1) / kSms) * len +
+                            0.5 * (double)((chains * (segs - 1) + kSms - 1) / kSms) * len + 8;
+        if (cost < best) {
+            best = cost;
+            seg = len * linrec::kChunk;
+        }
+    }
+    return seg;
+}
+
+int64_t segment_slots(const LinrecSeqs &s, int64_t seg) { return s.total / seg + s.N; }
+
+}  // namespace
+
+bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_bf16) {
+    return in_bf16 && out_bf16 && s.total > 0 && s.total < ((int64_t)1 << 31) - 64 &&
+           segment_slots(s, segment_tokens(s, H)) * H < ((int64_t)1 << 31);
+}
+
+size_t linrec_tc_workspace_bytes(const LinrecSeqs &s, int64_t H, int dk, int dv) {
+    const int64_t seg = segment_tokens(s, H);
+    if (seg >= s.total) return 0;
+    return sizeof(float) * (size_t)(segment_slots(s, seg) * H) * ((size_t)dk * dv + 4);
+}
+
+int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStream_t stream) {
+    const LinrecSeqs &s = p.seqs;
+    CUtensorMap m[5];
+    if (!make_map(&m[0], p.q, s.total, p.H, p.dk) || !make_map(&m[1], p.k, s.total, p.H, p.dk) ||
+        !make_map(&m[2], p.v, s.total, p.H, p.dv) || !make_map(&m[3], p.dot ? p.y : p.v, s.total, p.H, p.dv) ||
+        !make_map(&m[4], p.out, s.total, p.H, p.dv))
+        return kErrCuda;
+    TcArgs a{};
+    a.p = p;
+    a.status = status;
+    a.seg = segment_tokens(s, p.H);
+    const int64_t slots = segment_slots(s, a.seg);
+    const unsigned grid = (unsigned)(slots * p.H);
+    if (a.seg < s.total) {
+        a.seg_state = (float *)workspace;
+        a.seg_decay = a.seg_state + (size_t)slots * p.H * p.dk * p.dv;
+        a.sums = true;
+        int rc = dispatch(m, a, false, grid, stream);
+        if (rc != kOk) return rc;
+        const int quads = p.dk * p.dv / 4;
+        linrec_chain_kernel<<<dim3((unsigned)(s.N * p.H), (unsigned)(quads / 256)), 256, 0, stream>>>(
+            s, p.H, quads, p.rev, a.seg, p.init, a.seg_state, a.seg_decay);
+        if (cudaGetLastError() != cudaSuccess) return kErrCuda;
+        a.sums = false;
+    }
+    return dispatch(m, a, p.dot != nullptr, grid, stream);
+}
+
+}  // namespace dr

@@ -8,6 +8,10 @@ holds for the worst element, taken relative to max(RMS, |value|).  A bf16 output
 rounding, 2^-8 of the value, and the kernels' bf16 operands (each rounded by at most 2^-8 of its
 value, of random sign in sums of many: 3 of them at the worst element's six standard
 deviations of 2^-8 / sqrt(3) each) at most 6 sqrt(3) / sqrt(3) 2^-8 = 2.4e-2 of the RMS.
+The terms that are rounded are those of the element's own sum, sum_i q_i S_ij over the
+row's token: with random signs the root of their squares' sum is the RMS of that token's
+row, so the RMS of rows [.., d] is the row's own (tokens next to a large state are much
+larger than the others where the decay is strong).
 fp32 results of bf16 problems (states, the log-decay gradient) carry the fp32 bound.
 """
 import math
@@ -83,15 +87,16 @@ def cuda(d):
 
 
 def check(got, ref, dtype, what):
-    """Worst |got - ref| over max(RMS, |ref|) where ref is a number."""
+    """Worst |got - ref| over max(RMS, |ref|) where ref is a number; the RMS of the row for
+    rows of tokens, of all values for states and the log-decay gradient."""
     got = got.double().cpu()
     there = ~torch.isnan(ref)
     assert torch.isfinite(got[there]).all(), what
     if not there.any():
         return
-    r = ref[there]
-    rms = r.square().mean().sqrt().item()
-    err = ((got[there] - r).abs() / r.abs().clamp(min=max(rms, 1e-30))).max().item()
+    rows = what.split()[0] in ("out", "dq", "dk", "dv")
+    rms = (ref.square().mean(-1, keepdim=True) if rows else ref[there].square().mean()).sqrt().expand(ref.shape)
+    err = ((got - ref).abs() / torch.maximum(ref.abs(), rms.clamp(min=1e-30)))[there].max().item()
     tol = F32_TOL if dtype == "f32" else BF16_TOL
     assert err <= tol, f"{what}: {err:.3e} > {tol:.1e}"
 
@@ -242,6 +247,31 @@ def test_full_resets(dr, dtype):
     grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
     for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
         check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("strength", [0.1, 1e-3])
+@pytest.mark.parametrize("T,H,dk,dv,cu", [
+    (4096, 1, 128, 128, None), (3001, 3, 64, 128, None), (5000, 2, 128, 64, None), (6020, 1, 64, 64, [0, 10, 4500, 4500, 6000]),
+    (9000, 2, 128, 128, [5, 2000, 2001, 8999])])
+def test_long_sequences_in_few_chains(dr, T, H, dk, dv, cu, strength):
+    """Long enough for the sequences to be cut into segments that run side by side."""
+    N = len(cu) - 1 if cu else 1
+    d = inputs(1, T, H, dk, dv, "bf16", N=N if cu else 0, strength=strength, seed=T)
+    cuc = None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda()
+    desc = dr.LinrecDesc(1, T, H, dk, dv, N if cu else 0, 1, 1, 1, 0)
+    import ctypes
+    n = ctypes.c_size_t(0)
+    assert dr.lib().dr_linrec_fwd_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)) == 0 and n.value > 0
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu, d["do"], d["ds"])
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc)
+    check(o, out, "bf16", "out")
+    check(f, fin, "f32", "final_state")
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)
+    for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
+        check(x, g[n], "f32" if n in ("dla", "d0") else "bf16", n)
+    assert dr.device_status() == 0
 
 
 @pytest.mark.gpu
