@@ -3,9 +3,13 @@
 // single-token step.  The passes and their use for the gradients: linrec.h.
 #include "common.cuh"
 #include "linrec.h"
+#include "umma.cuh"
 
 namespace dr {
 namespace {
+
+using umma::fma2;
+using umma::mul2;
 
 // ---------------------------------------------------------------- token recurrence
 // One CTA per (sequence, head, 64 value columns): four warps, each with the state's 16
@@ -16,20 +20,6 @@ namespace {
 // element: one multiply (decay), two fused multiply-adds.  Bound by the packed FP32 rate,
 // 3 dk dv / 2 instructions a head-token.
 constexpr int kTile = 16;   // tokens staged in shared memory at a time; divides kAnchor
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
-          "l"(reinterpret_cast<uint64_t &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
 
 template <int DK, int DV, bool REV, bool DOT, typename Tin, typename Tout>
 __global__ void __launch_bounds__(128)

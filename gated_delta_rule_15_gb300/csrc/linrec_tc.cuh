@@ -106,7 +106,20 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, two ulp; 0 below the n
 }
 __device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ float bf16_of(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+// The upper halves of two fp32 values: their leading 8 bits, truncated, as a bf16 pair; and the
+// exact rest.  Three of these hold all 24 bits of a value.
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+    const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    const float2 top = make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u));
+    x = fma2(top, make_float2(-1.f, -1.f), x);
+    return __byte_perm(a, b, 0x7632);
+}
+__device__ __forceinline__ uint32_t last_bf16(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+// Largest log2 decay over a chunk for which P's factor 2^(c_r - c_s) is formed as a product of
+// two powers around the chunk's middle, 2^(c_r - c_31) 2^(c_31 - c_s).
+constexpr float kFactorSpan = 60.f;
 
 // Shared memory.  A stage holds [Y? V | ...panels] and [Q K | ...panels], panels of 64 channels
 // x 64 tokens (8 KB, 128-byte swizzle): every panel used as the first half of a 128-row
@@ -122,8 +135,9 @@ struct Layout {
     static constexpr uint32_t P = KT + 3 * PK * 8192;
     static constexpr uint32_t OUT = P + NP * 8192;           // output staging, PV panels
     static constexpr uint32_t SMALL = OUT + PV * 8192;
-    // per stage: c [66] as (multiple of 2^-10, remainder), 2^.. factors of R [64] and Kt [64]
-    static constexpr uint32_t GATE = 66 * 8 + 64 * 4 * 2;
+    // per stage: c [66] as (multiple of 2^-10, remainder), the last pair's first word for whether
+    // P's factors are products; 2^.. factors of R, Kt, P's rows and P's columns [64] each
+    static constexpr uint32_t GATE = 66 * 8 + 64 * 4 * 4;
     static constexpr uint32_t DOTS = SMALL + STAGES * GATE;  // (kDot) [3][2][64] of X X2, [4][64] of R, [8] of the state
     static constexpr uint32_t DOT_R = 3 * 2 * 64, DOT_S = DOT_R + 4 * 64;
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
@@ -214,7 +228,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     };
     auto stage = [&](int it) { return sm + (it % kStages) * L::STAGE; };
     auto gate_c = [&](int it) { return reinterpret_cast<float2 *>(sm + L::SMALL + (it % kStages) * L::GATE); };
-    auto gate_r = [&](int it) { return reinterpret_cast<float *>(gate_c(it) + 66); };   // factors of R, then of Kt
+    auto gate_f = [&](int it) { return reinterpret_cast<float *>(gate_c(it) + 66); };   // [4][64] factors
     auto chunk_of = [&](int it) { return rev ? chunks - 1 - it : it; };
     auto row_of = [&](int it) { return s_lo + (int64_t)chunk_of(it) * kChunk; };
     auto count_of = [&](int it) { return (int)min((int64_t)kChunk, s_hi - row_of(it)); };
@@ -261,7 +275,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const double ce = __shfl_sync(0xffffffffu, c, 31), c0 = c - y1;   // c0, c: up to its first, its second token
             total += ce;
             float2 *g = gate_c(it);
-            float *gr = gate_r(it);
+            float *gr = gate_f(it);
             auto split = [](double v) {
                 const float big = (float)(rint(v * 1024.0) * (1.0 / 1024.0));
                 return make_float2(big, (float)(v - (double)big));
@@ -275,6 +289,11 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 gr[2 * lane + 1] = ex2((float)(ce - c0));
                 gr[64 + 2 * lane] = ex2((float)cb);
                 gr[64 + 2 * lane + 1] = ex2((float)c0);
+                const double mid = __shfl_sync(0xffffffffu, c0, 15);   // c of token 31
+                gr[128 + 2 * lane] = ex2((float)(mid - cb));
+                gr[128 + 2 * lane + 1] = ex2((float)(mid - c0));
+                gr[192 + 2 * lane] = ex2((float)(cb - mid));
+                gr[192 + 2 * lane + 1] = ex2((float)(c0 - mid));
             } else {
                 g[2 * lane] = split(c0);
                 g[2 * lane + 1] = split(c);
@@ -283,7 +302,13 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 gr[2 * lane + 1] = ex2((float)c);
                 gr[64 + 2 * lane] = ex2((float)(ce - c0));
                 gr[64 + 2 * lane + 1] = ex2((float)(ce - c));
+                const double mid = __shfl_sync(0xffffffffu, c, 15);
+                gr[128 + 2 * lane] = ex2((float)(c0 - mid));
+                gr[128 + 2 * lane + 1] = ex2((float)(c - mid));
+                gr[192 + 2 * lane] = ex2((float)(mid - c0));
+                gr[192 + 2 * lane + 1] = ex2((float)(mid - c));
             }
+            if (lane == 0) g[65].x = -ce < (double)kFactorSpan ? 1.f : 0.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gate + s);
         }
@@ -375,36 +400,31 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const bool mine = 32 * quarter < DV;       // value channel `row` exists
         constexpr int NV = DK / 2;
         auto at = [&](int i) { return p.state_t ? (size_t)row * DK + i0 + i : (size_t)(i0 + i) * DV + row; };
-        float S[NV];
+        float2 S[NV / 2];
         const float *init = a.sums ? nullptr
                             : first_run ? (p.init ? p.init + (size_t)(n * H + h) * (DK * DV) : nullptr)
                                         : a.seg_state + (size_t)(slot * H + h) * (DK * DV);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) S[i] = init && mine ? init[at(i)] : 0.f;
+        for (int i = 0; i < NV / 2; ++i)
+            S[i] = init && mine ? make_float2(init[at(2 * i)], init[at(2 * i + 1)]) : make_float2(0.f, 0.f);
         auto put_operand = [&]() {   // S^T as NS bf16 terms
             if (mine) {
 #pragma unroll
-                for (int b = 0; b < NV / 16; ++b) {
-                    uint32_t w[8];
+                for (int b = 0; b < NV / 8; ++b) {
+                    uint32_t w[NS][4];
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float u = S[16 * b + 2 * i], v = S[16 * b + 2 * i + 1];
-                            if (t > 0) {
-                                const uint32_t w0 = pack_bf16(u, v);
-                                u -= lo_bf16(w0);
-                                v -= hi_bf16(w0);
-                            }
-                            if (t > 1) {
-                                const uint32_t w1 = pack_bf16(u, v);
-                                u -= lo_bf16(w1);
-                                v -= hi_bf16(w1);
-                            }
-                            w[i] = pack_bf16(u, v);
+                    for (int i = 0; i < 4; ++i) {
+                        float2 x = S[4 * b + i];
+                        if (NS == 1) {
+                            w[0][i] = pack_bf16(x.x, x.y);   // to the nearest
+                        } else {
+                            w[0][i] = take_bf16(x);
+                            w[NS > 1 ? 1 : 0][i] = take_bf16(x);
+                            w[NS - 1][i] = last_bf16(x);
                         }
-                        tmem_st8u(tl + L::TM_S + t * (DK / 2) + (i0 + 16 * b) / 2, w);
                     }
+#pragma unroll
+                    for (int t = 0; t < NS; ++t) tmem_st4u(tl + L::TM_S + t * (DK / 2) + (i0 + 8 * b) / 2, w[t]);
                 }
                 tmem_wait_st();
             }
@@ -431,7 +451,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (mine) {
                     const float *d = anchor_ptr(it);
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) x = fmaf(__ldcs(d + (size_t)i * 2 * DV), S[i], x);
+                    for (int i = 0; i < NV; ++i) {
+                        x = fmaf(__ldcs(d + (size_t)i * 2 * DV), i & 1 ? S[i / 2].y : S[i / 2].x, x);
+                        if (i % 8 == 7) asm volatile("" ::: "memory");   // eight loads at a time: registers
+                    }
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -455,7 +478,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     tmem_ld16(tl + L::TM_D + (ND == 2 ? 0 : i0) + 16 * b, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(decay, S[16 * b + i], v[i]);
+                    for (int i = 0; i < 8; ++i)
+                        S[8 * b + i] = fma2(make_float2(decay, decay), S[8 * b + i], make_float2(v[2 * i], v[2 * i + 1]));
                 }
             }
             tc_fence_before();
@@ -467,7 +491,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (!rev && at_anchor(it) && mine) {
                 float *dst = anchor_ptr(it);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) __stcs(dst + (size_t)i * 2 * DV, S[i]);
+                for (int i = 0; i < NV; ++i) __stcs(dst + (size_t)i * 2 * DV, i & 1 ? S[i / 2].y : S[i / 2].x);
             }
             if (outputs && it + 1 < chunks) {
                 wait(b_r, it);
@@ -480,7 +504,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // backwards, the state in front of the sequence is decayed by its first token
             const float f = rev && !a.sums && hi > lo && p.la ? expf(p.la[lo * H + h]) : 1.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) fin[at(i)] = f * S[i];
+            for (int i = 0; i < NV; ++i) fin[at(i)] = f * (i & 1 ? S[i / 2].y : S[i / 2].x);
         }
     } else {
         // ---------------------------------------------------------------- operands and outputs
@@ -490,84 +514,105 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint32_t smb = smem_u32(sm);
         float *dots = reinterpret_cast<float *>(sm + L::DOTS);
 
+        // Kt and P of chunk `it`.  The four warps whose lanes hold X's rows build P and a quarter
+        // of Kt, the other four the rest.
+        const int first_piece = (outputs ? (quarter < 2 ? half * 2 + quarter : 4 + 3 * (half * 2 + quarter - 2)) : 2 * ew) * PK;
+        const int pieces = (outputs ? (quarter < 2 ? 1 : 3) : 2) * PK;
         auto build = [&](int it) {
             const int s = it % kStages, cnt = count_of(it);
             wait(b_gate + s, it / kStages);
             wait(b_load + s, it / kStages);
-            if (quarter < 2) {
-                if (outputs) {
-                    // P: row `row`, columns 32 half ..
-                    const uint32_t dst = smb + L::P + (it % L::NP) * 8192 + row * 128;
-                    wait(b_x, it);
-                    if (L::NP == 1 && it > 0) wait(b_o, it - 1);   // the last chunk's O has read P
-                    float m = 0.f;
-                    if (rev ? quarter <= half : quarter >= half) {
-                        const float2 *c = gate_c(it);
-                        const float2 cr = c[row];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            float x[16], x2[16];
-                            tmem_ld16(tl + L::TM_U + 64 * (it & 1) + 32 * half + 16 * b, x);
-                            if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int col = 32 * half + 16 * b + i;
-                                const float2 cs = c[col];
-                                const float dx = cr.x - cs.x, dy = cr.y - cs.y, e = ex2(rev ? -dx - dy : dx + dy);
-                                const bool in = rev ? col >= row && col < cnt : col <= row;
-                                x[i] = in ? x[i] * e : 0.f;
-                                if (DOT) m = fmaf(x[i], in && col != row ? x2[i] : 0.f, m);
-                            }
-#pragma unroll
-                            for (int g = 0; g < 2; ++g)
-                                sts128(dst + ((((4 * half + 2 * b + g) ^ row) & 7) << 4), pack_bf16(x[8 * g], x[8 * g + 1]),
-                                       pack_bf16(x[8 * g + 2], x[8 * g + 3]), pack_bf16(x[8 * g + 4], x[8 * g + 5]),
-                                       pack_bf16(x[8 * g + 6], x[8 * g + 7]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) sts128(dst + ((((4 * half + g) ^ row) & 7) << 4), 0, 0, 0, 0);
-                    }
-                    if (DOT) dots[((it % 3) * 2 + half) * 64 + row] = m;
-                } else if (it > 0) {
-                    wait(b_d + ND - 1, it - 1);   // no second arrival on b_built within one chunk
-                }
-            } else {
-                // Kt: 16-byte pieces at the places they have in K's panels
-                const int t = (half * 2 + quarter - 2) * 32 + lane;   // 0 .. 127
+            // the last chunk's D has read Kt (and b_built is in this chunk's phase for every warp)
+            if (it > 0) wait(b_d + ND - 1, it - 1);
+            {
                 const unsigned char *k = stage(it) + L::K0;
-                const float *f = gate_r(it) + 64;
-                if (it > 0) wait(b_d + ND - 1, it - 1);   // the last chunk's D has read Kt
-#pragma unroll 2
-                for (int i = 0; i < 4 * PK; ++i) {
-                    const uint32_t o = 16 * (t + 128 * (i & 3)), b = i >> 2;
-                    const int r = o >> 7;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(k + b * L::QK_STEP + o);
+                const float *f = gate_f(it) + 64;
+#pragma unroll
+                for (int i = 0; i < 3 * PK; ++i) {
+                    if (i >= pieces) break;
+                    const uint32_t o = 512 * (first_piece + i) + 16 * lane, b = o >> 13;   // 16 bytes, at the place they have in K's panels
+                    const int r = (o >> 7) & 63;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(k + b * (L::QK_STEP - 8192) + o);
                     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
                     uint32_t w[3][4];
                     const float x = f[r];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float y0 = x * lo_bf16(in[e]), y1 = x * hi_bf16(in[e]);
-                        if (r >= cnt) y0 = y1 = 0.f;
-#pragma unroll
-                        for (int c = 0; c < 3; ++c) {
-                            w[c][e] = pack_bf16(y0, y1);
-                            y0 -= lo_bf16(w[c][e]);
-                            y1 -= hi_bf16(w[c][e]);
-                        }
+                        float2 y = mul2(make_float2(lo_bf16(in[e]), hi_bf16(in[e])), make_float2(x, x));
+                        if (r >= cnt) y = make_float2(0.f, 0.f);
+                        w[0][e] = take_bf16(y);
+                        w[1][e] = take_bf16(y);
+                        w[2][e] = last_bf16(y);
                     }
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)
-                        sts128(smb + L::KT + (c * PK + b) * 8192 + o, w[c][0], w[c][1], w[c][2], w[c][3]);
+                    for (int c = 0; c < 3; ++c) sts128(smb + L::KT + c * PK * 8192 + o, w[c][0], w[c][1], w[c][2], w[c][3]);
                 }
                 if (cnt < kChunk) {   // rows of no token are zero values
-                    for (int i = t; i < PV * 8 * (kChunk - cnt); i += 128) {
-                        const int b = i / (8 * (kChunk - cnt)), o = i % (8 * (kChunk - cnt));
-                        sts128(smem_u32(stage(it)) + L::V0 + b * L::V_STEP + cnt * 128 + o * 16, 0, 0, 0, 0);
-                    }
+                    const int per = 8 * (kChunk - cnt);
+                    for (int i = et; i < PV * per; i += 32 * kEdgeWarps)
+                        sts128(smem_u32(stage(it)) + L::V0 + (i / per) * L::V_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
                 }
+            }
+            if (outputs && quarter < 2) {
+                // P: row `row`, columns 32 half ..
+                const uint32_t dst = smb + L::P + (it % L::NP) * 8192 + row * 128;
+                wait(b_x, it);
+                if (L::NP == 1 && it > 0) wait(b_o, it - 1);   // the last chunk's O has read P
+                float m = 0.f;
+                if (rev ? quarter <= half : quarter >= half) {
+                    const bool diagonal = quarter == half || cnt < kChunk;
+                    const float2 *c = gate_c(it);
+                    const bool product = c[65].x != 0.f;
+                    const float2 cr = c[row];
+                    const float *fs = gate_f(it) + 192 + 32 * half;
+                    const float fr = gate_f(it)[128 + row];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float x[16], x2[16];
+                        tmem_ld16(tl + L::TM_U + 64 * (it & 1) + 32 * half + 16 * b, x);
+                        if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
+                        tmem_wait_ld();
+                        if (product) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 f4 = *reinterpret_cast<const float4 *>(fs + 16 * b + i);
+                                x[i] *= f4.x * fr;
+                                x[i + 1] *= f4.y * fr;
+                                x[i + 2] *= f4.z * fr;
+                                x[i + 3] *= f4.w * fr;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 cs = c[32 * half + 16 * b + i];
+                                const float d = (cr.x - cs.x) + (cr.y - cs.y);
+                                x[i] *= ex2(rev ? -d : d);
+                            }
+                        }
+                        if (diagonal) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int col = 32 * half + 16 * b + i;
+                                const bool in = rev ? col >= row && col < cnt : col <= row;
+                                x[i] = in ? x[i] : 0.f;
+                                if (DOT) x2[i] = in && col != row ? x2[i] : 0.f;
+                            }
+                        }
+                        if (DOT) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) m = fmaf(x[i], x2[i], m);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            sts128(dst + ((((4 * half + 2 * b + g) ^ row) & 7) << 4), pack_bf16(x[8 * g], x[8 * g + 1]),
+                                   pack_bf16(x[8 * g + 2], x[8 * g + 3]), pack_bf16(x[8 * g + 4], x[8 * g + 5]),
+                                   pack_bf16(x[8 * g + 6], x[8 * g + 7]));
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) sts128(dst + ((((4 * half + g) ^ row) & 7) << 4), 0, 0, 0, 0);
+                }
+                if (DOT) dots[((it % 3) * 2 + half) * 64 + row] = m;
             }
             fence_proxy_async();
             tc_fence_before();
@@ -584,42 +629,55 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 continue;
             }
             const int cnt = count_of(it);
-            const float *f = gate_r(it);
             if (et == 0) bulk_wait_read_all();   // the staging has left
             named_sync(1, 32 * kEdgeWarps);
             wait(b_o, it);
             if (32 * quarter < DV) {
-                const uint32_t stg = smb + L::OUT + (row >> 6) * 8192;
-                const uint32_t ysrc = smem_u32(stage(it)) + L::Y0 + (row >> 6) * L::V_STEP;
-                float z[32];
+                // 32 channels x 32 tokens, transposed on the way: accumulator fragments, stored and
+                // (Y) loaded as transposed 8 x 8 matrices
+                float2 f[4], z[4];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < 4; ++b) {
+                    f[b] = *reinterpret_cast<const float2 *>(gate_f(it) + 32 * half + 8 * b + 2 * (lane & 3));
+                    z[b] = make_float2(0.f, 0.f);
+                }
+                // this thread's matrix row: token 8 (matrix / 2) + lane % 8 of 16, channels + 8 (matrix % 2)
+                const int tok = 32 * half + 8 * (lane >> 4) + (lane & 7);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {   // 16 channels
+                    const uint32_t lanes = (uint32_t)(16 * g) << 16;
+                    const int ch = 32 * quarter + 16 * g + 8 * ((lane >> 3) & 1);
+                    const uint32_t mat = (ch >> 6) * 8192 + tok * 128 + ((((ch >> 3) ^ tok) & 7) << 4);
                     float r[16], o[16];
-                    tmem_ld16(tl + (NR == 2 && (it & 1) ? L::TM_X2 : L::TM_R) + 32 * half + 16 * b, r);
-                    tmem_ld16(tl + L::TM_U + 64 * (it & 1) + 32 * half + 16 * b, o);
+                    tmem_ld_frag32(tl + lanes + (NR == 2 && (it & 1) ? L::TM_X2 : L::TM_R) + 32 * half, r);
+                    tmem_ld_frag32(tl + lanes + L::TM_U + 64 * (it & 1) + 32 * half, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = 32 * half + 16 * b + i;
-                        const float x = f[t] * r[i];
-                        if (DOT) z[16 * b + i] = x * bf16_of(lds16(ysrc + sw128_off(t, row & 63)));
-                        const __nv_bfloat16 v = __float2bfloat16_rn(x + o[i]);
-                        sts16(stg + sw128_off(t, row & 63), __bfloat16_as_ushort(v));
+                    for (int e = 0; e < 2; ++e) {   // 16 tokens: matrices (b, channels), b = 2 e, 2 e + 1
+                        uint32_t w[4], y[4];
+                        if (DOT)
+                            ldsm_x4_trans(smem_u32(stage(it)) + L::Y0 + mat + (ch >> 6) * (L::V_STEP - 8192) + e * 2048, y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {   // block b, channels + 8 (i % 2)
+                            const int b = 2 * e + (i >> 1), v = 4 * b + 2 * (i & 1);
+                            const float2 x = mul2(f[b], make_float2(r[v], r[v + 1]));
+                            if (DOT) z[b] = fma2(x, make_float2(lo_bf16(y[i]), hi_bf16(y[i])), z[b]);
+                            w[i] = pack_bf16(x.x + o[v], x.y + o[v + 1]);
+                        }
+                        stsm_x4_trans(smb + L::OUT + mat + e * 2048, w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (DOT) {
-                    // 32 sums over the 32 lanes: each step halves the values a lane holds; lane l
-                    // ends with token l
+                if (DOT) {   // over the 8 lanes of a token pair
 #pragma unroll
-                    for (int w = 16; w > 0; w >>= 1) {
+                    for (int b = 0; b < 4; ++b) {
 #pragma unroll
-                        for (int i = 0; i < w; ++i) {
-                            const bool up = (lane & w) != 0;
-                            const float keep = up ? z[i + w] : z[i], give = up ? z[i] : z[i + w];
-                            z[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+                        for (int w = 4; w < 32; w <<= 1) {
+                            z[b].x += __shfl_xor_sync(0xffffffffu, z[b].x, w);
+                            z[b].y += __shfl_xor_sync(0xffffffffu, z[b].y, w);
                         }
+                        if (lane < 4)
+                            *reinterpret_cast<float2 *>(dots + L::DOT_R + quarter * 64 + 32 * half + 8 * b + 2 * lane) = z[b];
                     }
-                    dots[L::DOT_R + quarter * 64 + 32 * half + lane] = z[0];
                 }
             }
             tc_fence_before();

@@ -13,6 +13,12 @@ row's token: with random signs the root of their squares' sum is the RMS of that
 row, so the RMS of rows [.., d] is the row's own (tokens next to a large state are much
 larger than the others where the decay is strong).
 fp32 results of bf16 problems (states, the log-decay gradient) carry the fp32 bound.
+
+The log-decay gradient is <a_t S_{t-1}, dS_t>, formed as <S, dS> at the end of a run of 256 tokens plus
+the run's q.dq - k.dk behind t.  Each of those numbers is an fp32 sum of 128 products (off by
+about 2 u of its size, random signs) and up to 2 * 256 of them are added: sqrt(512) 2 u < 64 u of
+the largest.  Where the decay is so strong that the gradient is small against q.dq and k.dk, that
+absolute error is the bound.
 """
 import math
 
@@ -86,7 +92,13 @@ def cuda(d):
     return {n: None if x is None else x.cuda() for n, x in d.items()}
 
 
-def check(got, ref, dtype, what):
+def dla_slack(d, g):
+    """64 u of the largest q.dq or k.dk (reference values; rows of no sequence are NaN)."""
+    dots = [(d[x].double() * g["d" + x]).sum(-1).abs() for x in "qk"]
+    return 64 * 2.0 ** -24 * max(x[~torch.isnan(x)].max().item() if (~torch.isnan(x)).any() else 0.0 for x in dots)
+
+
+def check(got, ref, dtype, what, slack=0.0):
     """Worst |got - ref| over max(RMS, |ref|) where ref is a number; the RMS of the row for
     rows of tokens, of all values for states and the log-decay gradient."""
     got = got.double().cpu()
@@ -96,7 +108,7 @@ def check(got, ref, dtype, what):
         return
     rows = what.split()[0] in ("out", "dq", "dk", "dv")
     rms = (ref.square().mean(-1, keepdim=True) if rows else ref[there].square().mean()).sqrt().expand(ref.shape)
-    err = ((got - ref).abs() / torch.maximum(ref.abs(), rms.clamp(min=1e-30)))[there].max().item()
+    err = (((got - ref).abs() - slack).clamp(min=0) / torch.maximum(ref.abs(), rms.clamp(min=1e-30)))[there].max().item()
     tol = F32_TOL if dtype == "f32" else BF16_TOL
     assert err <= tol, f"{what}: {err:.3e} > {tol:.1e}"
 
@@ -114,6 +126,7 @@ SHAPES = [  # B, T, H, dk, dv
 def test_forward_and_backward(dr, B, T, H, dk, dv, gate, dtype):
     d = inputs(B, T, H, dk, dv, dtype, gate=gate, seed=T)
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    slack = dla_slack(d, g)
     c = cuda(d)
     o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
     check(o, out, dtype, "out")
@@ -123,7 +136,7 @@ def test_forward_and_backward(dr, B, T, H, dk, dv, gate, dtype):
         check(x, g[n], dtype, n)
     check(d0, g["d0"], "f32", "d_init_state")
     if gate:
-        check(dla, g["dla"], "f32", "d_log_alpha")
+        check(dla, g["dla"], "f32", "d_log_alpha", slack)
     else:
         assert dla is None
     assert dr.device_status() == 0
@@ -135,6 +148,7 @@ def test_no_states(dr, dtype):
     """Zero initial state, no final state's gradient, neither returned."""
     d = inputs(2, 150, 2, 128, 128, dtype, init=False, seed=5)
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], None, do=d["do"])
+    slack = dla_slack(d, g)
     c = cuda(d)
     o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], return_final_state=False)
     assert f is None
@@ -143,7 +157,7 @@ def test_no_states(dr, dtype):
     assert d0 is None
     for x, n in ((dq, "dq"), (dk_, "dk"), (dv_, "dv")):
         check(x, g[n], dtype, n)
-    check(dla, g["dla"], "f32", "d_log_alpha")
+    check(dla, g["dla"], "f32", "d_log_alpha", slack)
 
 
 PACKED = [  # cu_seqlens, rows
@@ -161,6 +175,7 @@ def test_packed_sequences(dr, cu, T, d_, dtype):
     N, H = len(cu) - 1, 2
     d = inputs(1, T, H, d_, d_, dtype, N=N, seed=T)
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu, d["do"], d["ds"])
+    slack = dla_slack(d, g)
     for n in ("q", "k", "v", "la", "do"):
         d[n][:, :cu[0]] = float("nan")
         d[n][:, cu[-1]:] = float("inf")
@@ -175,7 +190,7 @@ def test_packed_sequences(dr, cu, T, d_, dtype):
                                           grads=gr)
     for x, n in ((dq, "dq"), (dk_, "dk"), (dv_, "dv")):
         check(x, g[n], dtype, n)
-    check(dla, g["dla"], "f32", "d_log_alpha")
+    check(dla, g["dla"], "f32", "d_log_alpha", slack)
     check(d0, g["d0"], "f32", "d_init_state")
     for x in (o, dq, dk_, dv_, dla):
         x = x.float().cpu()
@@ -223,13 +238,14 @@ def test_weak_and_strong_decay(dr, strength, dtype):
     its bound is that of its own size."""
     d = inputs(1, 400, 2, 128, 128, dtype, strength=strength, seed=11)
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    slack = dla_slack(d, g)
     c = cuda(d)
     o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
     check(o, out, dtype, "out")
     check(f, fin, "f32", "final_state")
     grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
     for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
-        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n)
+        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n, slack if n == "dla" else 0.0)
 
 
 @pytest.mark.gpu
@@ -240,13 +256,14 @@ def test_full_resets(dr, dtype):
     for t in (0, 5, 63, 64, 65, 66, 200, 299):
         d["la"][:, t] = -math.inf
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], do=d["do"], ds=d["ds"])
+    slack = dla_slack(d, g)
     c = cuda(d)
     o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
     check(o, out, dtype, "out")
     check(f, fin, "f32", "final_state")
     grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
     for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
-        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n)
+        check(x, g[n], "f32" if n in ("dla", "d0") else dtype, n, slack if n == "dla" else 0.0)
 
 
 @pytest.mark.gpu
@@ -264,13 +281,14 @@ def test_long_sequences_in_few_chains(dr, T, H, dk, dv, cu, strength):
     n = ctypes.c_size_t(0)
     assert dr.lib().dr_linrec_fwd_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)) == 0 and n.value > 0
     out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu, d["do"], d["ds"])
+    slack = dla_slack(d, g)
     c = cuda(d)
     o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc)
     check(o, out, "bf16", "out")
     check(f, fin, "f32", "final_state")
     grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)
     for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
-        check(x, g[n], "f32" if n in ("dla", "d0") else "bf16", n)
+        check(x, g[n], "f32" if n in ("dla", "d0") else "bf16", n, slack if n == "dla" else 0.0)
     assert dr.device_status() == 0
 
 
