@@ -33,7 +33,9 @@
 //
 // Work split: one CTA per (sequence, head, segment) walks its chunks.  Warps 0..7 hold the state,
 // warps 8..15 build P and Kt and write the outputs, warp 16 issues the TMA loads and scans the
-// gates, one thread of warp 17 issues the MMAs.  Few long chains are cut into segments: a
+// gates, one thread each of warps 17 to 19 issues the MMAs of X, of D, of R and O (each waits for
+// its own operands only; one thread for all three either waits for one while another is
+// ready or spends more time polling).  Few long chains are cut into segments: a
 // first launch sums each segment's state from zero (keys and values only), a small kernel
 // chains them (the transition is the scalar 2^(sum c)), a second launch runs all segments
 // from their true start states.
@@ -60,7 +62,8 @@ using tc::pack_bf16;
 using tc::wait_cycles;
 
 constexpr int kChunk = 64;
-constexpr int kStateWarps = 8, kEdgeWarps = 8, kLoadWarp = 16, kMmaWarp = 17, kThreads = 18 * 32;
+constexpr int kStateWarps = 8, kEdgeWarps = 8, kLoadWarp = 16, kScoreWarp = 17, kUpdateWarp = 18, kReadWarp = 19,
+              kThreads = 20 * 32;
 
 struct TcArgs {
     LinrecPass p;
@@ -127,29 +130,38 @@ constexpr float kFactorSpan = 60.f;
 template <int DK, int DV, bool DOT>
 struct Layout {
     static constexpr int PK = DK / 64, PV = DV / 64;
-    static constexpr int STAGES = DOT ? 2 : 3, NP = DOT ? 2 : 1;   // loaded chunks; buffers of P
+    static constexpr int STAGES = DOT ? 2 : 3, GATES = 4;    // chunks whose rows, whose gates are there
     static constexpr uint32_t V_STEP = DOT ? 16384 : 8192, Y0 = 0, V0 = DOT ? 8192 : 0;
     static constexpr uint32_t Q0 = PV * V_STEP, K0 = Q0 + 8192, QK_STEP = 16384;
     static constexpr uint32_t STAGE = Q0 + PK * QK_STEP;
-    static constexpr uint32_t KT = STAGES * STAGE;           // Kt: three terms of PK panels
-    static constexpr uint32_t P = KT + 3 * PK * 8192;
-    static constexpr uint32_t OUT = P + NP * 8192;           // output staging, PV panels
+    static constexpr uint32_t KT = STAGES * STAGE;           // Kt's second and third term (the first replaces K)
+    static constexpr uint32_t P = KT + 2 * PK * 8192;        // two chunks' P
+    static constexpr uint32_t OUT = P + 2 * 8192;            // output staging, PV panels
     static constexpr uint32_t SMALL = OUT + PV * 8192;
-    // per stage: c [66] as (multiple of 2^-10, remainder), the last pair's first word for whether
+    // per chunk: c [66] as (multiple of 2^-10, remainder), the last pair's first word for whether
     // P's factors are products; 2^.. factors of R, Kt, P's rows and P's columns [64] each
     static constexpr uint32_t GATE = 66 * 8 + 64 * 4 * 4;
-    static constexpr uint32_t DOTS = SMALL + STAGES * GATE;  // (kDot) [3][2][64] of X X2, [4][64] of R, [8] of the state
+    static constexpr uint32_t DOTS = SMALL + GATES * GATE;   // (kDot) [3][2][64] of X X2, [4][64] of R, [8] of the state
     static constexpr uint32_t DOT_R = 3 * 2 * 64, DOT_S = DOT_R + 4 * 64;
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
     static constexpr uint32_t TOTAL = BARS + 32 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
-    // tensor memory: U (X, then O^T) of two chunks, X2 (kDot) or a second R, R, D, the state operand
-    static constexpr uint32_t TM_U = 0, TM_X2 = 128, TM_R = 192, TM_D = 256;
+    // tensor memory: U (X, then O^T) of NU chunks, X2 (kDot), R of NR chunks, D, the state operand
+    static constexpr int NU = DOT ? 2 : 3, NR = DOT ? 1 : 2;
+    static constexpr uint32_t TM_X2 = 128, TM_R = 192, TM_D = 256, TM_R1 = 448;
     static constexpr int ND = DOT && DK == 128 ? 2 : 1;      // D comes in this many parts, one at a time
     static constexpr int DW = DK / ND;
     static constexpr uint32_t TM_S = DOT ? 320 : 384;        // terms of DK / 2 columns
-    static_assert(TM_D + DW <= TM_S && TM_S + (DOT ? 3 : 1) * DK / 2 <= 512, "tensor memory");
+    static_assert(TM_D + DW <= TM_S && TM_S + (DOT ? 3 : 1) * DK / 2 <= (DOT ? 512 : TM_R1), "tensor memory");
 };
+
+// The rest of a wait that was not over at once (out of line: the kernel's code is fetched by
+// eighteen warps at different places).
+static __device__ __noinline__ void wait_longer(uint64_t *bar, uint32_t parity, volatile int *aborted, int *status) {
+    if (*aborted || wait_cycles(bar, parity)) return;
+    *aborted = 1;
+    atomicExch(status, kErrTimeout);
+}
 
 template <int DK, int DV, bool DOT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -157,7 +169,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap ty,
                     const __grid_constant__ CUtensorMap to, const TcArgs a) {
     using L = Layout<DK, DV, DOT>;
-    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 3 : 1, NR = DOT ? 1 : 2, ND = L::ND;
+    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 3 : 1, NU = L::NU, NR = L::NR, ND = L::ND;
     constexpr int kStages = L::STAGES;
     const LinrecPass &p = a.p;
     const int H = p.H, h = (int)(blockIdx.x % H);
@@ -176,40 +188,47 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     extern __shared__ unsigned char dsm_raw[];
     unsigned char *sm = align1024(dsm_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
-    uint64_t *b_load = bars, *b_gate = bars + 3, *b_free = bars + 6;   // [kStages]
-    uint64_t *b_x = bars + 9;          // X (and X2) of a chunk is there
-    uint64_t *b_built = bars + 10;     // P, Kt are built, X and X2 read
-    uint64_t *b_d = bars + 11;         // [ND] D is there
-    uint64_t *b_dread = bars + 13;     // [ND] D is read
-    uint64_t *b_s = bars + 15;         // the state operand is there
-    uint64_t *b_r = bars + 16;         // R is there: the state operand may be replaced
-    uint64_t *b_o = bars + 17;         // R and O are there
-    uint64_t *b_oread = bars + 18;     // R and O are read
-    uint64_t *b_end = bars + 19;       // every MMA is done
+    uint64_t *b_load = bars, *b_free = bars + 3;   // [kStages] rows are there, are done with
+    uint64_t *b_gate = bars + 6, *b_gfree = bars + 10;   // [GATES] the same of the gates
+    uint64_t *b_x = bars + 14;         // [NU] X (and X2) of a chunk is there
+    uint64_t *b_built = bars + 17;     // [2] P, Kt are built, X and X2 read
+    uint64_t *b_d = bars + 19;         // [ND] D is there
+    uint64_t *b_dread = bars + 21;     // [ND] D is read
+    uint64_t *b_s = bars + 23;         // the state operand is there
+    uint64_t *b_r = bars + 24;         // R is there: the state operand may be replaced
+    uint64_t *b_o = bars + 25;         // [2] R and O are there
+    uint64_t *b_oread = bars + 27;     // [4] R and O are read
+    uint64_t *b_end = bars + 31;       // every MMA is done
+    // A parity wait tells a phase from its neighbours only: no barrier completes a second
+    // time before everyone who waits for it has seen the first.  Where a warp may run ahead of
+    // another (X of later chunks, outputs), consecutive chunks take different barriers.
     __shared__ uint32_t tmem_s;
     __shared__ int abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(b_load + i, 1);
-            mbar_init(b_gate + i, 1);
-            mbar_init(b_free + i, 1 + kEdgeWarps + kStateWarps);
+            mbar_init(b_free + i, (outputs ? 2 : 1) + (DOT ? kEdgeWarps : 0));   // MMAs; with Y, the outputs too
         }
-        mbar_init(b_x, 1);
-        mbar_init(b_built, kEdgeWarps);
+        for (int i = 0; i < L::GATES; ++i) {
+            mbar_init(b_gate + i, 1);
+            mbar_init(b_gfree + i, kEdgeWarps + kStateWarps);
+        }
+        for (int i = 0; i < NU; ++i) mbar_init(b_x + i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(b_built + i, kEdgeWarps);
         for (int i = 0; i < ND; ++i) {
             mbar_init(b_d + i, 1);
             mbar_init(b_dread + i, kStateWarps / ND);
         }
         mbar_init(b_s, kStateWarps);
         mbar_init(b_r, 1);
-        mbar_init(b_o, 1);
-        mbar_init(b_oread, kEdgeWarps);
-        mbar_init(b_end, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(b_o + i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(b_oread + i, kEdgeWarps);
+        mbar_init(b_end, outputs ? 3 : 1);
         abort_s = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kUpdateWarp) {
         tmem_alloc(&tmem_s, 512);
         tmem_relinquish();
     }
@@ -220,14 +239,11 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     volatile int *aborted = &abort_s;
     // `k`-th completion of a barrier (k = 0, 1, ..); after an expiry nobody waits any more
     auto wait = [&](uint64_t *bar, int k) {
-        if (!mbar_try_wait(bar, k & 1) && !*aborted && !wait_cycles(bar, k & 1)) {
-            *aborted = 1;
-            atomicExch(a.status, kErrTimeout);
-        }
+        if (!mbar_try_wait(bar, k & 1)) wait_longer(bar, k & 1, aborted, a.status);
         tc_fence_after();
     };
     auto stage = [&](int it) { return sm + (it % kStages) * L::STAGE; };
-    auto gate_c = [&](int it) { return reinterpret_cast<float2 *>(sm + L::SMALL + (it % kStages) * L::GATE); };
+    auto gate_c = [&](int it) { return reinterpret_cast<float2 *>(sm + L::SMALL + (it % L::GATES) * L::GATE); };
     auto gate_f = [&](int it) { return reinterpret_cast<float *>(gate_c(it) + 66); };   // [4][64] factors
     auto chunk_of = [&](int it) { return rev ? chunks - 1 - it : it; };
     auto row_of = [&](int it) { return s_lo + (int64_t)chunk_of(it) * kChunk; };
@@ -248,6 +264,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int it = 0; it < chunks; ++it) {
             const int s = it % kStages;
             if (it >= kStages) wait(b_free + s, it / kStages - 1);
+            if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
             __syncwarp();
             if (lane == 0 && !*aborted) {
                 unsigned char *st = stage(it);
@@ -310,87 +327,101 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
             if (lane == 0) g[65].x = -ce < (double)kFactorSpan ? 1.f : 0.f;
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_gate + s);
+            if (lane == 0) mbar_arrive(b_gate + it % L::GATES);
         }
         if (a.sums && lane == 0) a.seg_decay[slot * H + h] = (float)total;
         // the loads have landed before the block ends, also after an expiry
         if (lane == 0)
             for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kScoreWarp) {
         // ---------------------------------------------------------------- MMA issue
-        if (lane == 0 && chunks > 0) {
+        if (lane == 0 && chunks > 0 && (outputs || warp == kUpdateWarp)) {
             constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
                                ID_MM = idesc_bf16(128, L::DW, true, true);
             const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
             const uint64_t dV = smem_desc_sw128(smem_u32(sm), PV == 2 ? L::V_STEP : 8192, 1024);   // MN-major, V panels
-            const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // MN-major, Kt panels
-            auto off = [&](const unsigned char *x) { return (uint32_t)(x - sm); };
+            const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
+            const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
+            auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
+            auto u_of = [&](int it) { return tm + 64 * ((uint32_t)it % NU); };
             auto scores = [&](int it) {
-                const uint32_t st = off(stage(it));
+                const uint32_t st = at_stage(it);
+#pragma unroll
                 for (int ks = 0; ks < 4 * PK; ++ks) {
                     const uint32_t o = st + (ks >> 2) * L::QK_STEP + (ks & 3) * 32;
-                    mma_bf16(tm + L::TM_U + 64 * (it & 1), desc_add(dK, o + L::Q0), desc_add(dK, o + L::K0), ID_KK, ks > 0);
+                    mma_bf16(u_of(it), desc_add(dK, o + L::Q0), desc_add(dK, o + L::K0), ID_KK, ks > 0);
                 }
-                if (DOT)
+                if (DOT) {
+#pragma unroll
                     for (int ks = 0; ks < 4 * PV; ++ks) {
                         const uint32_t o = st + (ks >> 2) * L::V_STEP + (ks & 3) * 32;
                         mma_bf16(tm + L::TM_X2, desc_add(dK, o + L::Y0), desc_add(dK, o + L::V0), ID_KK, ks > 0);
                     }
-                mma_commit(b_x);
-            };
-            if (outputs) {
-                wait(b_load, 0);
-                scores(0);
-            }
-            for (int it = 0; it < chunks; ++it) {
-                const uint32_t st = off(stage(it));
-                wait(b_built, it);   // (X2 is read then, too)
-                if (!outputs) wait(b_load + it % kStages, it / kStages);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    if (ND == 2) {
-                        if (d == 1 || it > 0) wait(b_dread + (d ^ 1), d == 1 ? it : it - 1);   // one half at a time
-                    } else if (it > 0) {
-                        wait(b_dread, it - 1);
-                    }
-                    for (int t = 0; t < 3; ++t)
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16(tm + L::TM_D, desc_add(dV, st + L::V0 + ks * 2048),
-                                     desc_add(dT, L::KT + (t * PK + d) * 8192 + ks * 2048),
-                                     ID_MM, t + ks > 0);
-                    mma_commit(b_d + d);
                 }
-                if (outputs) {
-                    // the next chunk's X, first if its rows are there already
-                    bool next = it + 1 < chunks;
-                    auto next_scores = [&]() {
-                        wait(b_load + (it + 1) % kStages, (it + 1) / kStages);
-                        if (it >= 1) wait(b_oread, it - 1);      // O of the chunk before is read
-                        scores(it + 1);
-                        next = false;
-                    };
-                    if (next && mbar_test(b_load + (it + 1) % kStages, ((it + 1) / kStages) & 1)) next_scores();
-                    wait(b_s, it);
-                    if (NR == 1 && it >= 1) wait(b_oread, it - 1);
-                    const uint32_t r = tm + (NR == 2 && (it & 1) ? L::TM_X2 : L::TM_R);
-                    for (int t = 0; t < NS; ++t)
-                        for (int ks = 0; ks < 4 * PK; ++ks)
-                            mma_bf16_ts(r, tm + L::TM_S + t * (DK / 2) + 8 * ks,
-                                        desc_add(dK, st + L::Q0 + (ks >> 2) * L::QK_STEP + (ks & 3) * 32), ID_KK, t + ks > 0);
-                    mma_commit(b_r);
+                mma_commit(b_x + it % NU);
+            };
+            auto update = [&](int it, int d) {
+                const uint32_t st = at_stage(it);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm + L::TM_U + 64 * (it & 1), desc_add(dV, st + L::V0 + ks * 2048),
-                                 desc_add(dK, L::P + (it % L::NP) * 8192 + ks * 32), ID_MK, ks > 0);
-                    mma_commit(b_o);
-                    mma_commit(b_free + it % kStages);
-                    if (next) next_scores();
-                } else {
-                    mma_commit(b_free + it % kStages);
+                        mma_bf16(tm + L::TM_D, desc_add(dV, st + L::V0 + ks * 2048),
+                                 t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP + ks * 2048)
+                                        : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192 + ks * 2048),
+                                 ID_MM, t + ks > 0);
+                mma_commit(b_d + d);
+                if (d == ND - 1) mma_commit(b_free + it % kStages);
+            };
+            auto read_out = [&](int it) {
+                const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+#pragma unroll
+                    for (int ks = 0; ks < 4 * PK; ++ks)
+                        mma_bf16_ts(r, tm + L::TM_S + t * (DK / 2) + 8 * ks,
+                                    desc_add(dK, st + L::Q0 + (ks >> 2) * L::QK_STEP + (ks & 3) * 32), ID_KK, t + ks > 0);
+                mma_commit(b_r);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(u_of(it), desc_add(dV, st + L::V0 + ks * 2048),
+                             desc_add(dK, L::P + (it & 1) * 8192 + ks * 32), ID_MK, ks > 0);
+                mma_commit(b_o + (it & 1));
+                mma_commit(b_free + it % kStages);
+            };
+            auto read = [&](int it) {   // R and O of the chunk are read
+                if (it >= 0) wait(b_oread + (it & 3), it >> 2);
+            };
+            if (warp == kScoreWarp) {
+                for (int it = 0; it < chunks; ++it) {
+                    read(it - NU);
+                    if (DOT && it > 0) wait(b_built + ((it - 1) & 1), (it - 1) >> 1);   // X2 is read
+                    wait(b_load + it % kStages, it / kStages);
+                    scores(it);
+                }
+            } else if (warp == kUpdateWarp) {
+                for (int it = 0; it < chunks; ++it) {
+                    wait(b_load + it % kStages, it / kStages);
+                    wait(b_built + (it & 1), it >> 1);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {   // (D's halves, one at a time)
+                        const int before = d == 0 ? it - 1 : it;
+                        if (before >= 0) wait(b_dread + (ND == 2 ? d ^ 1 : 0), before);
+                        update(it, d);
+                    }
+                }
+            } else {
+                for (int it = 0; it < chunks; ++it) {
+                    wait(b_load + it % kStages, it / kStages);
+                    read(it - NR);
+                    wait(b_s, it);
+                    wait(b_built + (it & 1), it >> 1);
+                    read_out(it);
                 }
             }
             mma_commit(b_end);
-            wait_cycles(b_end, 0);
+            wait_cycles(b_end, 0);   // (after an expiry, too)
         }
         __syncwarp();
     } else if (warp < kStateWarps) {
@@ -415,6 +446,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float2 x = S[4 * b + i];
+                        // (opaque, so that no term is computed ahead and kept: 550 bytes of spills)
+                        if (NS > 1) asm volatile("" : "+f"(x.x), "+f"(x.y));
                         if (NS == 1) {
                             w[0][i] = pack_bf16(x.x, x.y);   // to the nearest
                         } else {
@@ -443,7 +476,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         };
         if (outputs && chunks > 0) put_operand();
         for (int it = 0; it < chunks; ++it) {
-            wait(b_gate + it % kStages, it / kStages);
+            wait(b_gate + it % L::GATES, it / L::GATES);
             const float2 ce = gate_c(it)[64], cl = gate_c(it)[63];
             const float decay = ex2(ce.x + ce.y);
             if (rev && at_anchor(it)) {
@@ -486,7 +519,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(b_dread + d);
-                mbar_arrive(b_free + it % kStages);
+                mbar_arrive(b_gfree + it % L::GATES);
             }
             if (!rev && at_anchor(it) && mine) {
                 float *dst = anchor_ptr(it);
@@ -514,38 +547,49 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint32_t smb = smem_u32(sm);
         float *dots = reinterpret_cast<float *>(sm + L::DOTS);
 
-        // Kt and P of chunk `it`.  The four warps whose lanes hold X's rows build P and a quarter
-        // of Kt, the other four the rest.
-        const int first_piece = (outputs ? (quarter < 2 ? half * 2 + quarter : 4 + 3 * (half * 2 + quarter - 2)) : 2 * ew) * PK;
-        const int pieces = (outputs ? (quarter < 2 ? 1 : 3) : 2) * PK;
+        // Kt and P of chunk `it`.  Kt is made in pieces of 32 x 16 bytes; P's 32 x 32 blocks belong
+        // to the four warps whose lanes hold X's rows, two of them on the diagonal (masked), one
+        // off it and one empty.  By instructions a diagonal block costs three pieces, a full one
+        // two: warps of no block take five pieces (of 32; three of 16 for dk = 64), and so on.
+        const int kind = !outputs ? 4 : quarter >= 2 ? 3 : quarter == half ? 0 : (quarter == 1) != rev ? 1 : 2;   // diagonal, full, empty, none
+        const int pieces = !outputs ? 2 * PK : PK == 2 ? (kind == 0 ? 2 : kind == 1 ? 3 : 5) : (kind == 0 ? 0 : kind == 1 ? 1 : 3);
+        int first_piece = 2 * PK * ew;
+        if (outputs) {
+            const int none = PK == 2 ? 5 : 3, diag = PK == 2 ? 2 : 0, full = PK == 2 ? 3 : 1;
+            first_piece = kind == 3 ? (half * 2 + quarter - 2) * none : 4 * none + (kind == 0 ? half * diag : 2 * diag + (kind == 1 ? 0 : full));
+        }
         auto build = [&](int it) {
             const int s = it % kStages, cnt = count_of(it);
-            wait(b_gate + s, it / kStages);
+            wait(b_gate + it % L::GATES, it / L::GATES);
             wait(b_load + s, it / kStages);
-            // the last chunk's D has read Kt (and b_built is in this chunk's phase for every warp)
+            if (outputs) wait(b_x + it % NU, it / NU);  // K's place may be written
+            // the last chunk's D has read Kt's other terms (and b_built is in this chunk's phase)
             if (it > 0) wait(b_d + ND - 1, it - 1);
             {
-                const unsigned char *k = stage(it) + L::K0;
-                const float *f = gate_f(it) + 64;
-#pragma unroll
-                for (int i = 0; i < 3 * PK; ++i) {
-                    if (i >= pieces) break;
-                    const uint32_t o = 512 * (first_piece + i) + 16 * lane, b = o >> 13;   // 16 bytes, at the place they have in K's panels
-                    const int r = (o >> 7) & 63;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(k + b * (L::QK_STEP - 8192) + o);
+                unsigned char *k = stage(it) + L::K0 + 16 * lane;
+                const uint32_t k_at = smem_u32(k), kt_at = smb + L::KT + 16 * lane;
+                const float *f = gate_f(it) + 64 + (lane >> 3);
+                auto piece = [&](int i) { return (uint32_t)((i & 15) * 512 + (i >> 4) * L::QK_STEP); };   // its place in K's panels
+                uint4 next = *reinterpret_cast<const uint4 *>(k + piece(first_piece));
+#pragma unroll 1
+                for (int i = first_piece; i < first_piece + pieces; ++i) {
+                    const uint32_t o = piece(i);
+                    uint4 u = next;
+                    if (i + 1 < first_piece + pieces) next = *reinterpret_cast<const uint4 *>(k + piece(i + 1));
+                    const float x = f[4 * (i & 15)];
+                    if (4 * (i & 15) + (lane >> 3) >= cnt) u = make_uint4(0u, 0u, 0u, 0u);   // no token's row
                     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
                     uint32_t w[3][4];
-                    const float x = f[r];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float2 y = mul2(make_float2(lo_bf16(in[e]), hi_bf16(in[e])), make_float2(x, x));
-                        if (r >= cnt) y = make_float2(0.f, 0.f);
                         w[0][e] = take_bf16(y);
                         w[1][e] = take_bf16(y);
                         w[2][e] = last_bf16(y);
                     }
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) sts128(smb + L::KT + c * PK * 8192 + o, w[c][0], w[c][1], w[c][2], w[c][3]);
+                    sts128(k_at + o, w[0][0], w[0][1], w[0][2], w[0][3]);
+                    sts128(kt_at + 512 * i, w[1][0], w[1][1], w[1][2], w[1][3]);
+                    sts128(kt_at + 512 * i + PK * 8192, w[2][0], w[2][1], w[2][2], w[2][3]);
                 }
                 if (cnt < kChunk) {   // rows of no token are zero values
                     const int per = 8 * (kChunk - cnt);
@@ -555,31 +599,34 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
             if (outputs && quarter < 2) {
                 // P: row `row`, columns 32 half ..
-                const uint32_t dst = smb + L::P + (it % L::NP) * 8192 + row * 128;
-                wait(b_x, it);
-                if (L::NP == 1 && it > 0) wait(b_o, it - 1);   // the last chunk's O has read P
+                // (P of two chunks before is read: its output was waited for)
+                const uint32_t dst = smb + L::P + (it & 1) * 8192 + row * 128;
+                const uint32_t xs = tl + 64 * ((uint32_t)it % NU);
                 float m = 0.f;
-                if (rev ? quarter <= half : quarter >= half) {
-                    const bool diagonal = quarter == half || cnt < kChunk;
+                if (kind < 2) {
+                    const bool masked = kind == 0 || cnt < kChunk;
                     const float2 *c = gate_c(it);
                     const bool product = c[65].x != 0.f;
                     const float2 cr = c[row];
                     const float *fs = gate_f(it) + 192 + 32 * half;
                     const float fr = gate_f(it)[128 + row];
-#pragma unroll
+#pragma unroll 1
                     for (int b = 0; b < 2; ++b) {
                         float x[16], x2[16];
-                        tmem_ld16(tl + L::TM_U + 64 * (it & 1) + 32 * half + 16 * b, x);
+                        tmem_ld16(xs + 32 * half + 16 * b, x);
                         if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
                         tmem_wait_ld();
                         if (product) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4) {
                                 const float4 f4 = *reinterpret_cast<const float4 *>(fs + 16 * b + i);
-                                x[i] *= f4.x * fr;
-                                x[i + 1] *= f4.y * fr;
-                                x[i + 2] *= f4.z * fr;
-                                x[i + 3] *= f4.w * fr;
+                                const float2 f2 = make_float2(fr, fr);
+                                const float2 u = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(f4.x, f4.y), f2));
+                                const float2 v = mul2(make_float2(x[i + 2], x[i + 3]), mul2(make_float2(f4.z, f4.w), f2));
+                                x[i] = u.x;
+                                x[i + 1] = u.y;
+                                x[i + 2] = v.x;
+                                x[i + 3] = v.y;
                             }
                         } else {
 #pragma unroll
@@ -589,7 +636,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                                 x[i] *= ex2(rev ? -d : d);
                             }
                         }
-                        if (diagonal) {
+                        if (masked) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const int col = 32 * half + 16 * b + i;
@@ -617,7 +664,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_built);
+            if (lane == 0) mbar_arrive(b_built + (it & 1));
         };
 
         if (chunks > 0) build(0);
@@ -625,13 +672,13 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (it + 1 < chunks) build(it + 1);
             if (!outputs) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_free + it % kStages);
+                if (lane == 0) mbar_arrive(b_gfree + it % L::GATES);
                 continue;
             }
             const int cnt = count_of(it);
             if (et == 0) bulk_wait_read_all();   // the staging has left
             named_sync(1, 32 * kEdgeWarps);
-            wait(b_o, it);
+            wait(b_o + (it & 1), it >> 1);
             if (32 * quarter < DV) {
                 // 32 channels x 32 tokens, transposed on the way: accumulator fragments, stored and
                 // (Y) loaded as transposed 8 x 8 matrices
@@ -643,14 +690,14 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 }
                 // this thread's matrix row: token 8 (matrix / 2) + lane % 8 of 16, channels + 8 (matrix % 2)
                 const int tok = 32 * half + 8 * (lane >> 4) + (lane & 7);
-#pragma unroll
+#pragma unroll 1
                 for (int g = 0; g < 2; ++g) {   // 16 channels
                     const uint32_t lanes = (uint32_t)(16 * g) << 16;
                     const int ch = 32 * quarter + 16 * g + 8 * ((lane >> 3) & 1);
                     const uint32_t mat = (ch >> 6) * 8192 + tok * 128 + ((((ch >> 3) ^ tok) & 7) << 4);
                     float r[16], o[16];
-                    tmem_ld_frag32(tl + lanes + (NR == 2 && (it & 1) ? L::TM_X2 : L::TM_R) + 32 * half, r);
-                    tmem_ld_frag32(tl + lanes + L::TM_U + 64 * (it & 1) + 32 * half, o);
+                    tmem_ld_frag32(tl + lanes + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R) + 32 * half, r);
+                    tmem_ld_frag32(tl + lanes + 64 * ((uint32_t)it % NU) + 32 * half, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {   // 16 tokens: matrices (b, channels), b = 2 e, 2 e + 1
@@ -660,9 +707,9 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {   // block b, channels + 8 (i % 2)
                             const int b = 2 * e + (i >> 1), v = 4 * b + 2 * (i & 1);
-                            const float2 x = mul2(f[b], make_float2(r[v], r[v + 1]));
-                            if (DOT) z[b] = fma2(x, make_float2(lo_bf16(y[i]), hi_bf16(y[i])), z[b]);
-                            w[i] = pack_bf16(x.x + o[v], x.y + o[v + 1]);
+                            const float2 r2 = make_float2(r[v], r[v + 1]), x = fma2(f[b], r2, make_float2(o[v], o[v + 1]));
+                            if (DOT) z[b] = fma2(mul2(f[b], r2), make_float2(lo_bf16(y[i]), hi_bf16(y[i])), z[b]);
+                            w[i] = pack_bf16(x.x, x.y);
                         }
                         stsm_x4_trans(smb + L::OUT + mat + e * 2048, w[0], w[1], w[2], w[3]);
                     }
@@ -684,8 +731,9 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(b_oread);
-                mbar_arrive(b_free + it % kStages);
+                mbar_arrive(b_oread + (it & 3));
+                mbar_arrive(b_gfree + it % L::GATES);
+                if (DOT) mbar_arrive(b_free + it % kStages);
             }
             named_sync(1, 32 * kEdgeWarps);
             const int64_t base = row_of(it);
@@ -713,7 +761,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+    if (warp == kUpdateWarp) tmem_dealloc(tm, 512);
 }
 
 template <int DK, int DV, bool DOT>
