@@ -27,9 +27,15 @@
 // kDot): R takes the state in three bf16 terms, and the intra-chunk part of out.y is
 // summed from the fp32 products X and X2 = Y V^T directly,
 //     out_r.y_r (without the row's own term) = 2^c_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s).
-// log2 decays are summed in fp64 and split into a multiple of 2^-10 and a remainder, so
-// that differences of prefix sums are exact whatever lies between (log alpha is taken as at least
-// -120: exp(-120) is 0 in fp32, which makes -inf a full reset).
+// log2 decays are held as a multiple of 2^-10, whose sums over a chunk are exact in fp32, and
+// a remainder, so that a difference of prefix sums is as exact as a single decay whatever
+// lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
+// reset).
+//
+// The loop's code is kept small (rolled loops, the rest of long waits out of line): twenty warps
+// run through different parts of it, and what does not fit the SM's instruction cache
+// comes from the cache that all SMs of a GPC share, which was the bound before (76 % of its
+// rate, 84 % hits in the SM's cache).
 //
 // Work split: one CTA per (sequence, head, segment) walks its chunks.  Warps 0..7 hold the state,
 // warps 8..15 build P and Kt and write the outputs, warp 16 issues the TMA loads and scans the
@@ -182,7 +188,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     const bool last_run = rev ? j == 0 : j == segs - 1, first_run = rev ? j == segs - 1 : j == 0;
     if (a.sums && last_run) return;            // nobody needs its sum
     const int64_t s_lo = lo + j * a.seg, s_hi = min(hi, s_lo + a.seg);
-    const int chunks = (int)((s_hi - s_lo + kChunk - 1) / kChunk);
+    const int rows = (int)(s_hi - s_lo), chunks = (rows + kChunk - 1) / kChunk;
     if (chunks == 0 && (!p.fin || !outputs)) return;
 
     extern __shared__ unsigned char dsm_raw[];
@@ -246,13 +252,13 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     auto gate_c = [&](int it) { return reinterpret_cast<float2 *>(sm + L::SMALL + (it % L::GATES) * L::GATE); };
     auto gate_f = [&](int it) { return reinterpret_cast<float *>(gate_c(it) + 66); };   // [4][64] factors
     auto chunk_of = [&](int it) { return rev ? chunks - 1 - it : it; };
-    auto row_of = [&](int it) { return s_lo + (int64_t)chunk_of(it) * kChunk; };
-    auto count_of = [&](int it) { return (int)min((int64_t)kChunk, s_hi - row_of(it)); };
+    auto row_of = [&](int it) { return s_lo + chunk_of(it) * kChunk; };
+    auto count_of = [&](int it) { return min(kChunk, rows - chunk_of(it) * kChunk); };
 
     if (warp == kLoadWarp) {
         // ---------------------------------------------------------------- loads and gates
         const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV + (DOT ? PV : 0) : PK + PV);
-        double total = 0.0;
+        float total = 0.f;
         float x[2];
         int issued = 0;   // (lane 0) chunks whose loads were issued; none after an expiry
         auto load_gates = [&](int it) {   // two tokens a lane; backwards the tokens one further on
@@ -261,6 +267,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             for (int e = 0; e < 2; ++e) x[e] = p.la && t + e < end ? p.la[(t + e) * H + h] : 0.f;
         };
         if (chunks > 0) load_gates(0);
+#pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int s = it % kStages;
             if (it >= kStages) wait(b_free + s, it / kStages - 1);
@@ -271,65 +278,68 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 issued = it + 1;
                 const int row = (int)row_of(it);
                 mbar_arrive_expect_tx(b_load + s, bytes);
+#pragma unroll 1
                 for (int b = 0; b < PK; ++b) {
                     if (outputs) tma_load_3d(st + L::Q0 + b * L::QK_STEP, &tq, b_load + s, 64 * b, h, row);
                     tma_load_3d(st + L::K0 + b * L::QK_STEP, &tk, b_load + s, 64 * b, h, row);
                 }
+#pragma unroll 1
                 for (int b = 0; b < PV; ++b) {
-                    if (DOT && outputs) tma_load_3d(st + L::Y0 + b * L::V_STEP, &ty, b_load + s, 64 * b, h, row);
+                    if (DOT) tma_load_3d(st + L::Y0 + b * L::V_STEP, &ty, b_load + s, 64 * b, h, row);
                     tma_load_3d(st + L::V0 + b * L::V_STEP, &tv, b_load + s, 64 * b, h, row);
                 }
             }
-            constexpr double kLog2e = 1.4426950408889634074;
-            const double y0 = kLog2e * fmaxf(x[0], -120.f), y1 = kLog2e * fmaxf(x[1], -120.f);
+            // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
+            float2 y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float v = fmaxf(x[e], -120.f), kLog2e = 1.44269504f, kRest = 1.92596299e-8f;
+                const float m = v * kLog2e, r = fmaf(v, kLog2e, -m) + v * kRest, q = rintf(m * 1024.f) * (1.f / 1024.f);
+                y[e] = make_float2(q, (m - q) + r);
+            }
             if (it + 1 < chunks) load_gates(it + 1);
-            double c = y0 + y1;
+            auto add = [](float2 u, float2 v) { return make_float2(u.x + v.x, u.y + v.y); };
+            auto sub = [](float2 u, float2 v) { return make_float2(u.x - v.x, u.y - v.y); };
+            auto from = [](float2 u, int l) {
+                return make_float2(__shfl_sync(0xffffffffu, u.x, l), __shfl_sync(0xffffffffu, u.y, l));
+            };
+            float2 c = add(y[0], y[1]);   // inclusive sum over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double z = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += z;
+                const float2 z = make_float2(__shfl_up_sync(0xffffffffu, c.x, o), __shfl_up_sync(0xffffffffu, c.y, o));
+                if (lane >= o) c = add(c, z);
             }
-            const double ce = __shfl_sync(0xffffffffu, c, 31), c0 = c - y1;   // c0, c: up to its first, its second token
-            total += ce;
+            const float2 ce = from(c, 31);
+            total += ce.x + ce.y;
+            // c of this lane's two tokens: forwards with, backwards without what was loaded for it
+            float2 u[2] = {sub(c, y[1]), c};
+            if (rev) {
+                u[1] = u[0];
+                u[0] = sub(u[0], y[0]);
+            }
+            const float2 mid = from(u[1], 15);
             float2 *g = gate_c(it);
             float *gr = gate_f(it);
-            auto split = [](double v) {
-                const float big = (float)(rint(v * 1024.0) * (1.0 / 1024.0));
-                return make_float2(big, (float)(v - (double)big));
-            };
-            if (rev) {
-                g[2 * lane + 1] = split(c0);
-                g[2 * lane + 2] = split(c);
-                if (lane == 0) g[0] = make_float2(0.f, 0.f);
-                const double cb = c0 - y0;   // c of token 2 lane
-                gr[2 * lane] = ex2((float)(ce - cb));
-                gr[2 * lane + 1] = ex2((float)(ce - c0));
-                gr[64 + 2 * lane] = ex2((float)cb);
-                gr[64 + 2 * lane + 1] = ex2((float)c0);
-                const double mid = __shfl_sync(0xffffffffu, c0, 15);   // c of token 31
-                gr[128 + 2 * lane] = ex2((float)(mid - cb));
-                gr[128 + 2 * lane + 1] = ex2((float)(mid - c0));
-                gr[192 + 2 * lane] = ex2((float)(cb - mid));
-                gr[192 + 2 * lane + 1] = ex2((float)(c0 - mid));
-            } else {
-                g[2 * lane] = split(c0);
-                g[2 * lane + 1] = split(c);
-                if (lane == 31) g[64] = split(c);
-                gr[2 * lane] = ex2((float)c0);
-                gr[2 * lane + 1] = ex2((float)c);
-                gr[64 + 2 * lane] = ex2((float)(ce - c0));
-                gr[64 + 2 * lane + 1] = ex2((float)(ce - c));
-                const double mid = __shfl_sync(0xffffffffu, c, 15);
-                gr[128 + 2 * lane] = ex2((float)(c0 - mid));
-                gr[128 + 2 * lane + 1] = ex2((float)(c - mid));
-                gr[192 + 2 * lane] = ex2((float)(mid - c0));
-                gr[192 + 2 * lane + 1] = ex2((float)(mid - c));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const float2 w = sub(ce, u[e]), m = sub(u[e], mid);
+                const float head = ex2(u[e].x + u[e].y), tail = ex2(w.x + w.y), d = m.x + m.y;
+                const float up = ex2(d), down = ex2(-d);
+                g[t] = u[e];
+                gr[t] = rev ? tail : head;
+                gr[64 + t] = rev ? head : tail;
+                gr[128 + t] = rev ? down : up;
+                gr[192 + t] = rev ? up : down;
             }
-            if (lane == 0) g[65].x = -ce < (double)kFactorSpan ? 1.f : 0.f;
+            if (lane == 0) {
+                g[64] = ce;
+                g[65].x = -ce.x < kFactorSpan ? 1.f : 0.f;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gate + it % L::GATES);
         }
-        if (a.sums && lane == 0) a.seg_decay[slot * H + h] = (float)total;
+        if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
         // the loads have landed before the block ends, also after an expiry
         if (lane == 0)
             for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
@@ -345,48 +355,49 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
             auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
             auto u_of = [&](int it) { return tm + 64 * ((uint32_t)it % NU); };
+            // four K = 16 steps through one panel (K-major: 32 bytes a step; MN-major: 2048)
+            auto four = [&](uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id, bool more) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(d, desc_add(da, ks * astep), desc_add(db, ks * bstep), id, more || ks > 0);
+            };
             auto scores = [&](int it) {
                 const uint32_t st = at_stage(it);
-#pragma unroll
-                for (int ks = 0; ks < 4 * PK; ++ks) {
-                    const uint32_t o = st + (ks >> 2) * L::QK_STEP + (ks & 3) * 32;
-                    mma_bf16(u_of(it), desc_add(dK, o + L::Q0), desc_add(dK, o + L::K0), ID_KK, ks > 0);
+#pragma unroll 1
+                for (int b = 0; b < PK; ++b) {
+                    const uint32_t o = st + b * L::QK_STEP;
+                    four(u_of(it), desc_add(dK, o + L::Q0), 32, desc_add(dK, o + L::K0), 32, ID_KK, b > 0);
                 }
                 if (DOT) {
-#pragma unroll
-                    for (int ks = 0; ks < 4 * PV; ++ks) {
-                        const uint32_t o = st + (ks >> 2) * L::V_STEP + (ks & 3) * 32;
-                        mma_bf16(tm + L::TM_X2, desc_add(dK, o + L::Y0), desc_add(dK, o + L::V0), ID_KK, ks > 0);
+#pragma unroll 1
+                    for (int b = 0; b < PV; ++b) {
+                        const uint32_t o = st + b * L::V_STEP;
+                        four(tm + L::TM_X2, desc_add(dK, o + L::Y0), 32, desc_add(dK, o + L::V0), 32, ID_KK, b > 0);
                     }
                 }
                 mma_commit(b_x + it % NU);
             };
             auto update = [&](int it, int d) {
                 const uint32_t st = at_stage(it);
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 3; ++t)
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tm + L::TM_D, desc_add(dV, st + L::V0 + ks * 2048),
-                                 t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP + ks * 2048)
-                                        : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192 + ks * 2048),
-                                 ID_MM, t + ks > 0);
+                    four(tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
+                         t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
+                         2048, ID_MM, t > 0);
                 mma_commit(b_d + d);
                 if (d == ND - 1) mma_commit(b_free + it % kStages);
             };
             auto read_out = [&](int it) {
                 const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
+#pragma unroll 1
+                for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
+                    const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
 #pragma unroll
-                for (int t = 0; t < NS; ++t)
-#pragma unroll
-                    for (int ks = 0; ks < 4 * PK; ++ks)
-                        mma_bf16_ts(r, tm + L::TM_S + t * (DK / 2) + 8 * ks,
-                                    desc_add(dK, st + L::Q0 + (ks >> 2) * L::QK_STEP + (ks & 3) * 32), ID_KK, t + ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_ts(r, tm + L::TM_S + 32 * b + 8 * ks, desc_add(dq, ks * 32), ID_KK, b + ks > 0);
+                }
                 mma_commit(b_r);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(u_of(it), desc_add(dV, st + L::V0 + ks * 2048),
-                             desc_add(dK, L::P + (it & 1) * 8192 + ks * 32), ID_MK, ks > 0);
+                four(u_of(it), desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, false);
                 mma_commit(b_o + (it & 1));
                 mma_commit(b_free + it % kStages);
             };
@@ -412,6 +423,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     }
                 }
             } else {
+#pragma unroll 1
                 for (int it = 0; it < chunks; ++it) {
                     wait(b_load + it % kStages, it / kStages);
                     read(it - NR);
@@ -474,8 +486,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const int64_t end = row_of(it) + count_of(it);
             return DOT && p.dot && outputs && (end == hi || (end - lo) % kAnchor == 0);
         };
-        if (outputs && chunks > 0) put_operand();
+#pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
+            if (outputs) {
+                if (it > 0) wait(b_r, it - 1);
+                put_operand();
+            }
             wait(b_gate + it % L::GATES, it / L::GATES);
             const float2 ce = gate_c(it)[64], cl = gate_c(it)[63];
             const float decay = ex2(ce.x + ce.y);
@@ -525,10 +541,6 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 float *dst = anchor_ptr(it);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) __stcs(dst + (size_t)i * 2 * DV, i & 1 ? S[i / 2].y : S[i / 2].x);
-            }
-            if (outputs && it + 1 < chunks) {
-                wait(b_r, it);
-                put_operand();
             }
         }
         float *fin = a.sums ? a.seg_state + (size_t)(slot * H + h) * (DK * DV)
@@ -667,9 +679,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (lane == 0) mbar_arrive(b_built + (it & 1));
         };
 
-        if (chunks > 0) build(0);
-        for (int it = 0; it < chunks; ++it) {
+#pragma unroll 1
+        for (int it = -1; it < chunks; ++it) {   // build one chunk ahead of the outputs (one copy of the code)
             if (it + 1 < chunks) build(it + 1);
+            if (it < 0) continue;
             if (!outputs) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_gfree + it % L::GATES);
