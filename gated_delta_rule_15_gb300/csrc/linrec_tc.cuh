@@ -32,7 +32,7 @@
 // lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
 // reset).
 //
-// The loop's code is kept small (rolled loops, the rest of long waits out of line): twenty warps
+// The loop's code is kept small (rolled loops): twenty warps
 // run through different parts of it, and what does not fit the SM's instruction cache
 // comes from the cache that all SMs of a GPC share, which was the bound before (76 % of its
 // rate, 84 % hits in the SM's cache).
@@ -68,8 +68,13 @@ using tc::pack_bf16;
 using tc::wait_cycles;
 
 constexpr int kChunk = 64;
-constexpr int kStateWarps = 8, kEdgeWarps = 8, kLoadWarp = 16, kScoreWarp = 17, kUpdateWarp = 18, kReadWarp = 19,
-              kThreads = 20 * 32;
+constexpr int kStateWarps = 8, kBuildWarps = 8, kOutWarps = 8, kBuild0 = kStateWarps, kOut0 = kBuild0 + kBuildWarps,
+              kLoadWarp = kOut0 + kOutWarps, kScoreWarp = kLoadWarp + 1, kUpdateWarp = kLoadWarp + 2,
+              kThreads = (kLoadWarp + 4) * 32;
+// Registers a thread: launched with kRegs; the state warps take what the others give back.
+constexpr int kRegs = 72, kStateRegs = 104, kEdgeRegs = 64, kIssueRegs = 40;
+static_assert(kStateWarps * kStateRegs + (kBuildWarps + kOutWarps) * kEdgeRegs + 4 * kIssueRegs <= kThreads / 32 * kRegs,
+              "register split");
 
 struct TcArgs {
     LinrecPass p;
@@ -150,7 +155,7 @@ struct Layout {
     static constexpr uint32_t DOTS = SMALL + GATES * GATE;   // (kDot) [3][2][64] of X X2, [4][64] of R, [8] of the state
     static constexpr uint32_t DOT_R = 3 * 2 * 64, DOT_S = DOT_R + 4 * 64;
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
-    static constexpr uint32_t TOTAL = BARS + 32 * 8;
+    static constexpr uint32_t TOTAL = BARS + 40 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
     // tensor memory: U (X, then O^T) of NU chunks, X2 (kDot), R of NR chunks, D, the state operand
     static constexpr int NU = DOT ? 2 : 3, NR = DOT ? 1 : 2;
@@ -161,12 +166,28 @@ struct Layout {
     static_assert(TM_D + DW <= TM_S && TM_S + (DOT ? 3 : 1) * DK / 2 <= (DOT ? 512 : TM_R1), "tensor memory");
 };
 
-// The rest of a wait that was not over at once (out of line: the kernel's code is fetched by
-// eighteen warps at different places).
-static __device__ __noinline__ void wait_longer(uint64_t *bar, uint32_t parity, volatile int *aborted, int *status) {
-    if (*aborted || wait_cycles(bar, parity)) return;
-    *aborted = 1;
-    atomicExch(status, kErrTimeout);
+// The rest of a wait that was not over at once; its budget and the other warps' expiries are
+// looked at every 256 polls (few instructions at each of the many places that wait; no call: the
+// register split below rules calls out).
+__device__ __forceinline__ void wait_longer(uint64_t *bar, uint32_t parity, volatile int *aborted, int *status) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) == 0 && (*aborted || clock64() - t0 > tc::kWaitCycles)) {
+            *aborted = 1;
+            atomicExch(status, kErrTimeout);
+            return;
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void more_regs() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int DK, int DV, bool DOT>
@@ -197,14 +218,14 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint64_t *b_load = bars, *b_free = bars + 3;   // [kStages] rows are there, are done with
     uint64_t *b_gate = bars + 6, *b_gfree = bars + 10;   // [GATES] the same of the gates
     uint64_t *b_x = bars + 14;         // [NU] X (and X2) of a chunk is there
-    uint64_t *b_built = bars + 17;     // [2] P, Kt are built, X and X2 read
-    uint64_t *b_d = bars + 19;         // [ND] D is there
-    uint64_t *b_dread = bars + 21;     // [ND] D is read
-    uint64_t *b_s = bars + 23;         // the state operand is there
-    uint64_t *b_r = bars + 24;         // R is there: the state operand may be replaced
-    uint64_t *b_o = bars + 25;         // [2] R and O are there
-    uint64_t *b_oread = bars + 27;     // [4] R and O are read
-    uint64_t *b_end = bars + 31;       // every MMA is done
+    uint64_t *b_built = bars + 17;     // [4] P, Kt are built, X and X2 read
+    uint64_t *b_d = bars + 21;         // [ND] D is there
+    uint64_t *b_dread = bars + 23;     // [ND] D is read
+    uint64_t *b_s = bars + 25;         // the state operand is there
+    uint64_t *b_r = bars + 26;         // R is there: the state operand may be replaced
+    uint64_t *b_o = bars + 27;         // [2] R and O are there
+    uint64_t *b_oread = bars + 29;     // [4] R and O are read
+    uint64_t *b_end = bars + 33;       // every MMA is done
     // A parity wait tells a phase from its neighbours only: no barrier completes a second
     // time before everyone who waits for it has seen the first.  Where a warp may run ahead of
     // another (X of later chunks, outputs), consecutive chunks take different barriers.
@@ -214,14 +235,14 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(b_load + i, 1);
-            mbar_init(b_free + i, (outputs ? 2 : 1) + (DOT ? kEdgeWarps : 0));   // MMAs; with Y, the outputs too
+            mbar_init(b_free + i, 1 + (DOT ? kOutWarps : 0));   // MMAs; with Y, the outputs too
         }
         for (int i = 0; i < L::GATES; ++i) {
             mbar_init(b_gate + i, 1);
-            mbar_init(b_gfree + i, kEdgeWarps + kStateWarps);
+            mbar_init(b_gfree + i, kStateWarps + (outputs ? kOutWarps : kBuildWarps));
         }
         for (int i = 0; i < NU; ++i) mbar_init(b_x + i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(b_built + i, kEdgeWarps);
+        for (int i = 0; i < 4; ++i) mbar_init(b_built + i, kBuildWarps);
         for (int i = 0; i < ND; ++i) {
             mbar_init(b_d + i, 1);
             mbar_init(b_dread + i, kStateWarps / ND);
@@ -229,8 +250,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         mbar_init(b_s, kStateWarps);
         mbar_init(b_r, 1);
         for (int i = 0; i < 2; ++i) mbar_init(b_o + i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(b_oread + i, kEdgeWarps);
-        mbar_init(b_end, outputs ? 3 : 1);
+        for (int i = 0; i < 4; ++i) mbar_init(b_oread + i, kOutWarps);
+        mbar_init(b_end, outputs ? 2 : 1);
         abort_s = 0;
         fence_mbar_init();
     }
@@ -255,188 +276,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     auto row_of = [&](int it) { return s_lo + chunk_of(it) * kChunk; };
     auto count_of = [&](int it) { return min(kChunk, rows - chunk_of(it) * kChunk); };
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- loads and gates
-        const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV + (DOT ? PV : 0) : PK + PV);
-        float total = 0.f;
-        float x[2];
-        int issued = 0;   // (lane 0) chunks whose loads were issued; none after an expiry
-        auto load_gates = [&](int it) {   // two tokens a lane; backwards the tokens one further on
-            const int64_t t = row_of(it) + 2 * lane + (rev ? 1 : 0), end = rev ? hi : row_of(it) + count_of(it);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[e] = p.la && t + e < end ? p.la[(t + e) * H + h] : 0.f;
-        };
-        if (chunks > 0) load_gates(0);
-#pragma unroll 1
-        for (int it = 0; it < chunks; ++it) {
-            const int s = it % kStages;
-            if (it >= kStages) wait(b_free + s, it / kStages - 1);
-            if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
-            __syncwarp();
-            if (lane == 0 && !*aborted) {
-                unsigned char *st = stage(it);
-                issued = it + 1;
-                const int row = (int)row_of(it);
-                mbar_arrive_expect_tx(b_load + s, bytes);
-#pragma unroll 1
-                for (int b = 0; b < PK; ++b) {
-                    if (outputs) tma_load_3d(st + L::Q0 + b * L::QK_STEP, &tq, b_load + s, 64 * b, h, row);
-                    tma_load_3d(st + L::K0 + b * L::QK_STEP, &tk, b_load + s, 64 * b, h, row);
-                }
-#pragma unroll 1
-                for (int b = 0; b < PV; ++b) {
-                    if (DOT) tma_load_3d(st + L::Y0 + b * L::V_STEP, &ty, b_load + s, 64 * b, h, row);
-                    tma_load_3d(st + L::V0 + b * L::V_STEP, &tv, b_load + s, 64 * b, h, row);
-                }
-            }
-            // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
-            float2 y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float v = fmaxf(x[e], -120.f), kLog2e = 1.44269504f, kRest = 1.92596299e-8f;
-                const float m = v * kLog2e, r = fmaf(v, kLog2e, -m) + v * kRest, q = rintf(m * 1024.f) * (1.f / 1024.f);
-                y[e] = make_float2(q, (m - q) + r);
-            }
-            if (it + 1 < chunks) load_gates(it + 1);
-            auto add = [](float2 u, float2 v) { return make_float2(u.x + v.x, u.y + v.y); };
-            auto sub = [](float2 u, float2 v) { return make_float2(u.x - v.x, u.y - v.y); };
-            auto from = [](float2 u, int l) {
-                return make_float2(__shfl_sync(0xffffffffu, u.x, l), __shfl_sync(0xffffffffu, u.y, l));
-            };
-            float2 c = add(y[0], y[1]);   // inclusive sum over the lanes
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float2 z = make_float2(__shfl_up_sync(0xffffffffu, c.x, o), __shfl_up_sync(0xffffffffu, c.y, o));
-                if (lane >= o) c = add(c, z);
-            }
-            const float2 ce = from(c, 31);
-            total += ce.x + ce.y;
-            // c of this lane's two tokens: forwards with, backwards without what was loaded for it
-            float2 u[2] = {sub(c, y[1]), c};
-            if (rev) {
-                u[1] = u[0];
-                u[0] = sub(u[0], y[0]);
-            }
-            const float2 mid = from(u[1], 15);
-            float2 *g = gate_c(it);
-            float *gr = gate_f(it);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float2 w = sub(ce, u[e]), m = sub(u[e], mid);
-                const float head = ex2(u[e].x + u[e].y), tail = ex2(w.x + w.y), d = m.x + m.y;
-                const float up = ex2(d), down = ex2(-d);
-                g[t] = u[e];
-                gr[t] = rev ? tail : head;
-                gr[64 + t] = rev ? head : tail;
-                gr[128 + t] = rev ? down : up;
-                gr[192 + t] = rev ? up : down;
-            }
-            if (lane == 0) {
-                g[64] = ce;
-                g[65].x = -ce.x < kFactorSpan ? 1.f : 0.f;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_gate + it % L::GATES);
-        }
-        if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
-        // the loads have landed before the block ends, also after an expiry
-        if (lane == 0)
-            for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
-        __syncwarp();
-    } else if (warp >= kScoreWarp) {
-        // ---------------------------------------------------------------- MMA issue
-        if (lane == 0 && chunks > 0 && (outputs || warp == kUpdateWarp)) {
-            constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
-                               ID_MM = idesc_bf16(128, L::DW, true, true);
-            const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
-            const uint64_t dV = smem_desc_sw128(smem_u32(sm), PV == 2 ? L::V_STEP : 8192, 1024);   // MN-major, V panels
-            const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
-            const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
-            auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
-            auto u_of = [&](int it) { return tm + 64 * ((uint32_t)it % NU); };
-            // four K = 16 steps through one panel (K-major: 32 bytes a step; MN-major: 2048)
-            auto four = [&](uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id, bool more) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(d, desc_add(da, ks * astep), desc_add(db, ks * bstep), id, more || ks > 0);
-            };
-            auto scores = [&](int it) {
-                const uint32_t st = at_stage(it);
-#pragma unroll 1
-                for (int b = 0; b < PK; ++b) {
-                    const uint32_t o = st + b * L::QK_STEP;
-                    four(u_of(it), desc_add(dK, o + L::Q0), 32, desc_add(dK, o + L::K0), 32, ID_KK, b > 0);
-                }
-                if (DOT) {
-#pragma unroll 1
-                    for (int b = 0; b < PV; ++b) {
-                        const uint32_t o = st + b * L::V_STEP;
-                        four(tm + L::TM_X2, desc_add(dK, o + L::Y0), 32, desc_add(dK, o + L::V0), 32, ID_KK, b > 0);
-                    }
-                }
-                mma_commit(b_x + it % NU);
-            };
-            auto update = [&](int it, int d) {
-                const uint32_t st = at_stage(it);
-#pragma unroll 1
-                for (int t = 0; t < 3; ++t)
-                    four(tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
-                         t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
-                         2048, ID_MM, t > 0);
-                mma_commit(b_d + d);
-                if (d == ND - 1) mma_commit(b_free + it % kStages);
-            };
-            auto read_out = [&](int it) {
-                const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
-#pragma unroll 1
-                for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
-                    const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ts(r, tm + L::TM_S + 32 * b + 8 * ks, desc_add(dq, ks * 32), ID_KK, b + ks > 0);
-                }
-                mma_commit(b_r);
-                four(u_of(it), desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, false);
-                mma_commit(b_o + (it & 1));
-                mma_commit(b_free + it % kStages);
-            };
-            auto read = [&](int it) {   // R and O of the chunk are read
-                if (it >= 0) wait(b_oread + (it & 3), it >> 2);
-            };
-            if (warp == kScoreWarp) {
-                for (int it = 0; it < chunks; ++it) {
-                    read(it - NU);
-                    if (DOT && it > 0) wait(b_built + ((it - 1) & 1), (it - 1) >> 1);   // X2 is read
-                    wait(b_load + it % kStages, it / kStages);
-                    scores(it);
-                }
-            } else if (warp == kUpdateWarp) {
-                for (int it = 0; it < chunks; ++it) {
-                    wait(b_load + it % kStages, it / kStages);
-                    wait(b_built + (it & 1), it >> 1);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) {   // (D's halves, one at a time)
-                        const int before = d == 0 ? it - 1 : it;
-                        if (before >= 0) wait(b_dread + (ND == 2 ? d ^ 1 : 0), before);
-                        update(it, d);
-                    }
-                }
-            } else {
-#pragma unroll 1
-                for (int it = 0; it < chunks; ++it) {
-                    wait(b_load + it % kStages, it / kStages);
-                    read(it - NR);
-                    wait(b_s, it);
-                    wait(b_built + (it & 1), it >> 1);
-                    read_out(it);
-                }
-            }
-            mma_commit(b_end);
-            wait_cycles(b_end, 0);   // (after an expiry, too)
-        }
-        __syncwarp();
-    } else if (warp < kStateWarps) {
+    if (warp < kStateWarps) {
+        more_regs<kStateRegs>();
         // ---------------------------------------------------------------- state
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane, i0 = half * (DK / 2);
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
@@ -551,32 +392,31 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
             for (int i = 0; i < NV; ++i) fin[at(i)] = f * (i & 1 ? S[i / 2].y : S[i / 2].x);
         }
-    } else {
-        // ---------------------------------------------------------------- operands and outputs
-        const int ew = warp - kStateWarps, quarter = ew & 3, half = ew >> 2, row = 32 * quarter + lane;
-        const int et = tid - 32 * kStateWarps;
-        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
-        const uint32_t smb = smem_u32(sm);
+    } else if (warp < kOut0) {
+        fewer_regs<kEdgeRegs>();
+        // ---------------------------------------------------------------- Kt and P
+        const int bw = warp - kBuild0, quarter = bw & 3, half = bw >> 2, row = 32 * quarter + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
         float *dots = reinterpret_cast<float *>(sm + L::DOTS);
-
-        // Kt and P of chunk `it`.  Kt is made in pieces of 32 x 16 bytes; P's 32 x 32 blocks belong
+        // Kt is made in pieces of 32 x 16 bytes; P's 32 x 32 blocks belong
         // to the four warps whose lanes hold X's rows, two of them on the diagonal (masked), one
         // off it and one empty.  By instructions a diagonal block costs three pieces, a full one
         // two: warps of no block take five pieces (of 32; three of 16 for dk = 64), and so on.
         const int kind = !outputs ? 4 : quarter >= 2 ? 3 : quarter == half ? 0 : (quarter == 1) != rev ? 1 : 2;   // diagonal, full, empty, none
         const int pieces = !outputs ? 2 * PK : PK == 2 ? (kind == 0 ? 2 : kind == 1 ? 3 : 5) : (kind == 0 ? 0 : kind == 1 ? 1 : 3);
-        int first_piece = 2 * PK * ew;
+        int first_piece = 2 * PK * bw;
         if (outputs) {
             const int none = PK == 2 ? 5 : 3, diag = PK == 2 ? 2 : 0, full = PK == 2 ? 3 : 1;
             first_piece = kind == 3 ? (half * 2 + quarter - 2) * none : 4 * none + (kind == 0 ? half * diag : 2 * diag + (kind == 1 ? 0 : full));
         }
-        auto build = [&](int it) {
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
             const int s = it % kStages, cnt = count_of(it);
             wait(b_gate + it % L::GATES, it / L::GATES);
             wait(b_load + s, it / kStages);
             if (outputs) wait(b_x + it % NU, it / NU);  // K's place may be written
-            // the last chunk's D has read Kt's other terms (and b_built is in this chunk's phase)
-            if (it > 0) wait(b_d + ND - 1, it - 1);
+            if (it > 0) wait(b_d + ND - 1, it - 1);     // Kt's other terms are read
+            if (outputs && it > 1) wait(b_o + (it & 1), (it - 2) >> 1);   // P of two chunks before is read
             {
                 unsigned char *k = stage(it) + L::K0 + 16 * lane;
                 const uint32_t k_at = smem_u32(k), kt_at = smb + L::KT + 16 * lane;
@@ -605,13 +445,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 }
                 if (cnt < kChunk) {   // rows of no token are zero values
                     const int per = 8 * (kChunk - cnt);
-                    for (int i = et; i < PV * per; i += 32 * kEdgeWarps)
+                    for (int i = 32 * bw + lane; i < PV * per; i += 32 * kBuildWarps)
                         sts128(smem_u32(stage(it)) + L::V0 + (i / per) * L::V_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
                 }
             }
             if (outputs && quarter < 2) {
                 // P: row `row`, columns 32 half ..
-                // (P of two chunks before is read: its output was waited for)
                 const uint32_t dst = smb + L::P + (it & 1) * 8192 + row * 128;
                 const uint32_t xs = tl + 64 * ((uint32_t)it % NU);
                 float m = 0.f;
@@ -676,21 +515,27 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_built + (it & 1));
-        };
-
-#pragma unroll 1
-        for (int it = -1; it < chunks; ++it) {   // build one chunk ahead of the outputs (one copy of the code)
-            if (it + 1 < chunks) build(it + 1);
-            if (it < 0) continue;
-            if (!outputs) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_gfree + it % L::GATES);
-                continue;
+            if (lane == 0) {
+                mbar_arrive(b_built + (it & 3));
+                if (!outputs) mbar_arrive(b_gfree + it % L::GATES);
             }
+        }
+    } else if (warp < kLoadWarp) {
+        fewer_regs<kEdgeRegs>();
+        // ---------------------------------------------------------------- outputs
+        const int ow = warp - kOut0, quarter = ow & 3, half = ow >> 2, et = tid - 32 * kOut0;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
+        float *dots = reinterpret_cast<float *>(sm + L::DOTS);
+#pragma unroll 1
+        for (int it = 0; it < (outputs ? chunks : 0); ++it) {
             const int cnt = count_of(it);
             if (et == 0) bulk_wait_read_all();   // the staging has left
-            named_sync(1, 32 * kEdgeWarps);
+            named_sync(1, 32 * kOutWarps);
+            wait(b_gate + it % L::GATES, it / L::GATES);
+            if (DOT) {
+                wait(b_load + it % kStages, it / kStages);
+                wait(b_built + (it & 3), it >> 2);
+            }
             wait(b_o + (it & 1), it >> 1);
             if (32 * quarter < DV) {
                 // 32 channels x 32 tokens, transposed on the way: accumulator fragments, stored and
@@ -748,7 +593,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 mbar_arrive(b_gfree + it % L::GATES);
                 if (DOT) mbar_arrive(b_free + it % kStages);
             }
-            named_sync(1, 32 * kEdgeWarps);
+            named_sync(1, 32 * kOutWarps);
             const int64_t base = row_of(it);
             if (cnt == kChunk) {
                 if (et == 0) {
@@ -756,7 +601,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     bulk_commit();
                 }
             } else {
-                for (int i = et; i < cnt * PV * 8; i += 32 * kEdgeWarps) {
+                for (int i = et; i < cnt * PV * 8; i += 32 * kOutWarps) {
                     const int r = i / (PV * 8), b = (i / 8) % PV, c = i % 8;
                     const uint4 u = *reinterpret_cast<const uint4 *>(sm + L::OUT + b * 8192 + r * 128 + (((c ^ r) & 7) << 4));
                     reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + ((size_t)(base + r) * H + h) * DV)[b * 8 + c] = u;
@@ -770,6 +615,187 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
         }
         if (et == 0) bulk_wait_all();
+    } else {
+        fewer_regs<kIssueRegs>();
+        if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- loads and gates
+            const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV + (DOT ? PV : 0) : PK + PV);
+            float total = 0.f;
+            float x[2];
+            int issued = 0;   // (lane 0) chunks whose loads were issued; none after an expiry
+            auto load_gates = [&](int it) {   // two tokens a lane; backwards the tokens one further on
+                const int64_t t = row_of(it) + 2 * lane + (rev ? 1 : 0), end = rev ? hi : row_of(it) + count_of(it);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x[e] = p.la && t + e < end ? p.la[(t + e) * H + h] : 0.f;
+            };
+            if (chunks > 0) load_gates(0);
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                const int s = it % kStages;
+                if (it >= kStages) wait(b_free + s, it / kStages - 1);
+                if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
+                __syncwarp();
+                if (lane == 0 && !*aborted) {
+                    unsigned char *st = stage(it);
+                    issued = it + 1;
+                    const int row = (int)row_of(it);
+                    mbar_arrive_expect_tx(b_load + s, bytes);
+#pragma unroll 1
+                    for (int b = 0; b < PK; ++b) {
+                        if (outputs) tma_load_3d(st + L::Q0 + b * L::QK_STEP, &tq, b_load + s, 64 * b, h, row);
+                        tma_load_3d(st + L::K0 + b * L::QK_STEP, &tk, b_load + s, 64 * b, h, row);
+                    }
+#pragma unroll 1
+                    for (int b = 0; b < PV; ++b) {
+                        if (DOT) tma_load_3d(st + L::Y0 + b * L::V_STEP, &ty, b_load + s, 64 * b, h, row);
+                        tma_load_3d(st + L::V0 + b * L::V_STEP, &tv, b_load + s, 64 * b, h, row);
+                    }
+                }
+                // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
+                float2 y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float v = fmaxf(x[e], -120.f), kLog2e = 1.44269504f, kRest = 1.92596299e-8f;
+                    const float m = v * kLog2e, r = fmaf(v, kLog2e, -m) + v * kRest, q = rintf(m * 1024.f) * (1.f / 1024.f);
+                    y[e] = make_float2(q, (m - q) + r);
+                }
+                if (it + 1 < chunks) load_gates(it + 1);
+                auto add = [](float2 u, float2 v) { return make_float2(u.x + v.x, u.y + v.y); };
+                auto sub = [](float2 u, float2 v) { return make_float2(u.x - v.x, u.y - v.y); };
+                auto from = [](float2 u, int l) {
+                    return make_float2(__shfl_sync(0xffffffffu, u.x, l), __shfl_sync(0xffffffffu, u.y, l));
+                };
+                float2 c = add(y[0], y[1]);   // inclusive sum over the lanes
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float2 z = make_float2(__shfl_up_sync(0xffffffffu, c.x, o), __shfl_up_sync(0xffffffffu, c.y, o));
+                    if (lane >= o) c = add(c, z);
+                }
+                const float2 ce = from(c, 31);
+                total += ce.x + ce.y;
+                // c of this lane's two tokens: forwards with, backwards without what was loaded for it
+                float2 u[2] = {sub(c, y[1]), c};
+                if (rev) {
+                    u[1] = u[0];
+                    u[0] = sub(u[0], y[0]);
+                }
+                const float2 mid = from(u[1], 15);
+                float2 *g = gate_c(it);
+                float *gr = gate_f(it);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 2 * lane + e;
+                    const float2 w = sub(ce, u[e]), m = sub(u[e], mid);
+                    const float head = ex2(u[e].x + u[e].y), tail = ex2(w.x + w.y), d = m.x + m.y;
+                    const float up = ex2(d), down = ex2(-d);
+                    g[t] = u[e];
+                    gr[t] = rev ? tail : head;
+                    gr[64 + t] = rev ? head : tail;
+                    gr[128 + t] = rev ? down : up;
+                    gr[192 + t] = rev ? up : down;
+                }
+                if (lane == 0) {
+                    g[64] = ce;
+                    g[65].x = -ce.x < kFactorSpan ? 1.f : 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_gate + it % L::GATES);
+            }
+            if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
+            // the loads have landed before the block ends, also after an expiry
+            if (lane == 0)
+                for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
+            __syncwarp();
+        } else if (warp >= kScoreWarp) {
+            // ---------------------------------------------------------------- MMA issue
+            if (lane == 0 && chunks > 0 && ((outputs && warp == kScoreWarp) || warp == kUpdateWarp)) {
+                constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
+                                   ID_MM = idesc_bf16(128, L::DW, true, true);
+                const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
+                const uint64_t dV = smem_desc_sw128(smem_u32(sm), PV == 2 ? L::V_STEP : 8192, 1024);   // MN-major, V panels
+                const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
+                const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
+                auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
+                auto u_of = [&](int it) { return tm + 64 * ((uint32_t)it % NU); };
+                // four K = 16 steps through one panel (K-major: 32 bytes a step; MN-major: 2048)
+                auto four = [&](uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id, bool more) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(d, desc_add(da, ks * astep), desc_add(db, ks * bstep), id, more || ks > 0);
+                };
+                auto scores = [&](int it) {
+                    const uint32_t st = at_stage(it);
+#pragma unroll 1
+                    for (int b = 0; b < PK; ++b) {
+                        const uint32_t o = st + b * L::QK_STEP;
+                        four(u_of(it), desc_add(dK, o + L::Q0), 32, desc_add(dK, o + L::K0), 32, ID_KK, b > 0);
+                    }
+                    if (DOT) {
+#pragma unroll 1
+                        for (int b = 0; b < PV; ++b) {
+                            const uint32_t o = st + b * L::V_STEP;
+                            four(tm + L::TM_X2, desc_add(dK, o + L::Y0), 32, desc_add(dK, o + L::V0), 32, ID_KK, b > 0);
+                        }
+                    }
+                    mma_commit(b_x + it % NU);
+                };
+                auto update = [&](int it, int d) {
+                    const uint32_t st = at_stage(it);
+#pragma unroll 1
+                    for (int t = 0; t < 3; ++t)
+                        four(tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
+                             t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
+                             2048, ID_MM, t > 0);
+                    mma_commit(b_d + d);
+                };
+                auto read_out = [&](int it) {
+                    const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
+#pragma unroll 1
+                    for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
+                        const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_bf16_ts(r, tm + L::TM_S + 32 * b + 8 * ks, desc_add(dq, ks * 32), ID_KK, b + ks > 0);
+                    }
+                    mma_commit(b_r);
+                    four(u_of(it), desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, false);
+                    mma_commit(b_o + (it & 1));
+                };
+                auto read = [&](int it) {   // R and O of the chunk are read
+                    if (it >= 0) wait(b_oread + (it & 3), it >> 2);
+                };
+                if (warp == kScoreWarp) {
+                    for (int it = 0; it < chunks; ++it) {
+                        read(it - NU);
+                        if (DOT && it > 0) wait(b_built + ((it - 1) & 3), (it - 1) >> 2);   // X2 is read
+                        wait(b_load + it % kStages, it / kStages);
+                        scores(it);
+                    }
+                } else {
+                    // D first: the next chunk's Kt waits for it
+#pragma unroll 1
+                    for (int it = 0; it < chunks; ++it) {
+                        wait(b_load + it % kStages, it / kStages);
+                        wait(b_built + (it & 3), it >> 2);
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) {   // (D's halves, one at a time)
+                            const int before = d == 0 ? it - 1 : it;
+                            if (before >= 0) wait(b_dread + (ND == 2 ? d ^ 1 : 0), before);
+                            update(it, d);
+                            if (outputs && d == 0) {
+                                read(it - NR);
+                                wait(b_s, it);
+                                read_out(it);
+                            }
+                        }
+                        mma_commit(b_free + it % kStages);
+                    }
+                }
+                mma_commit(b_end);
+                wait_cycles(b_end, 0);   // (after an expiry, too)
+            }
+            __syncwarp();
+        }
     }
     tc_fence_before();
     __syncthreads();
