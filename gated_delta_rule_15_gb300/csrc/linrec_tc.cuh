@@ -162,6 +162,7 @@ struct Layout {
     static constexpr uint32_t TM_X2 = 128, TM_R = 192, TM_D = 256, TM_R1 = 448;
     static constexpr int ND = DOT && DK == 128 ? 2 : 1;      // D comes in this many parts, one at a time
     static constexpr int DW = DK / ND;
+    static constexpr int HALVES = DOT ? 1 : 2;               // Kt is handed over in this many parts
     static constexpr uint32_t TM_S = DOT ? 320 : 384;        // terms of DK / 2 columns
     static_assert(TM_D + DW <= TM_S && TM_S + (DOT ? 3 : 1) * DK / 2 <= (DOT ? 512 : TM_R1), "tensor memory");
 };
@@ -218,14 +219,16 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint64_t *b_load = bars, *b_free = bars + 3;   // [kStages] rows are there, are done with
     uint64_t *b_gate = bars + 6, *b_gfree = bars + 10;   // [GATES] the same of the gates
     uint64_t *b_x = bars + 14;         // [NU] X (and X2) of a chunk is there
-    uint64_t *b_built = bars + 17;     // [4] P, Kt are built, X and X2 read
+    uint64_t *b_kt = bars + 17;        // [HALVES] Kt (rows 0..31, 32..63) is built
+    uint64_t *b_p = bars + 19;         // [2] P is built, X and X2 are read
     uint64_t *b_d = bars + 21;         // [ND] D is there
-    uint64_t *b_dread = bars + 23;     // [ND] D is read
-    uint64_t *b_s = bars + 25;         // the state operand is there
-    uint64_t *b_r = bars + 26;         // R is there: the state operand may be replaced
-    uint64_t *b_o = bars + 27;         // [2] R and O are there
-    uint64_t *b_oread = bars + 29;     // [4] R and O are read
-    uint64_t *b_end = bars + 33;       // every MMA is done
+    uint64_t *b_d1 = bars + 23;        // D has taken Kt's first half
+    uint64_t *b_dread = bars + 24;     // [ND] D is read
+    uint64_t *b_s = bars + 26;         // the state operand is there
+    uint64_t *b_r = bars + 27;         // R is there: the state operand may be replaced
+    uint64_t *b_o = bars + 28;         // [2] R and O are there
+    uint64_t *b_oread = bars + 30;     // [4] R and O are read
+    uint64_t *b_end = bars + 34;       // every MMA is done
     // A parity wait tells a phase from its neighbours only: no barrier completes a second
     // time before everyone who waits for it has seen the first.  Where a warp may run ahead of
     // another (X of later chunks, outputs), consecutive chunks take different barriers.
@@ -239,10 +242,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         }
         for (int i = 0; i < L::GATES; ++i) {
             mbar_init(b_gate + i, 1);
-            mbar_init(b_gfree + i, kStateWarps + (outputs ? kOutWarps : kBuildWarps));
+            mbar_init(b_gfree + i, kStateWarps + kBuildWarps + (outputs ? kOutWarps : 0));
         }
         for (int i = 0; i < NU; ++i) mbar_init(b_x + i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(b_built + i, kBuildWarps);
+        for (int i = 0; i < L::HALVES; ++i) mbar_init(b_kt + i, kBuildWarps);
+        mbar_init(b_d1, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(b_p + i, 4);
         for (int i = 0; i < ND; ++i) {
             mbar_init(b_d + i, 1);
             mbar_init(b_dread + i, kStateWarps / ND);
@@ -275,6 +280,80 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     auto chunk_of = [&](int it) { return rev ? chunks - 1 - it : it; };
     auto row_of = [&](int it) { return s_lo + chunk_of(it) * kChunk; };
     auto count_of = [&](int it) { return min(kChunk, rows - chunk_of(it) * kChunk); };
+
+    // P of chunk `nx`, by the warps whose lanes hold X's rows (quarters 0 and 1), 32 columns each: on
+    // the diagonal (masked), full or empty.
+    auto kind_of = [&](int quarter, int half) { return quarter == half ? 0 : (quarter == 1) != rev ? 1 : 2; };
+    auto build_p = [&](int nx, int quarter, int half) {
+        const int cnt = count_of(nx), kind = kind_of(quarter, half), row = 32 * quarter + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
+        wait(b_gate + nx % L::GATES, nx / L::GATES);
+        wait(b_x + nx % NU, nx / NU);
+        const uint32_t dst = smb + L::P + (nx & 1) * 8192 + row * 128;
+        const uint32_t xs = tl + 64 * ((uint32_t)nx % NU);
+        float m = 0.f;
+        if (kind < 2) {
+            const bool masked = kind == 0 || cnt < kChunk;
+            const float2 *c = gate_c(nx);
+            const bool product = c[65].x != 0.f;
+            const float2 cr = c[row];
+            const float *fs = gate_f(nx) + 192 + 32 * half;
+            const float fr = gate_f(nx)[128 + row];
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                float x[16], x2[16];
+                tmem_ld16(xs + 32 * half + 16 * b, x);
+                if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
+                tmem_wait_ld();
+                if (product) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f4 = *reinterpret_cast<const float4 *>(fs + 16 * b + i);
+                        const float2 f2 = make_float2(fr, fr);
+                        const float2 u = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(f4.x, f4.y), f2));
+                        const float2 v = mul2(make_float2(x[i + 2], x[i + 3]), mul2(make_float2(f4.z, f4.w), f2));
+                        x[i] = u.x;
+                        x[i + 1] = u.y;
+                        x[i + 2] = v.x;
+                        x[i + 3] = v.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 cs = c[32 * half + 16 * b + i];
+                        const float d = (cr.x - cs.x) + (cr.y - cs.y);
+                        x[i] *= ex2(rev ? -d : d);
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int col = 32 * half + 16 * b + i;
+                        const bool in = rev ? col >= row && col < cnt : col <= row;
+                        x[i] = in ? x[i] : 0.f;
+                        if (DOT) x2[i] = in && col != row ? x2[i] : 0.f;
+                    }
+                }
+                if (DOT) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) m = fmaf(x[i], x2[i], m);
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    sts128(dst + ((((4 * half + 2 * b + g) ^ row) & 7) << 4), pack_bf16(x[8 * g], x[8 * g + 1]),
+                           pack_bf16(x[8 * g + 2], x[8 * g + 3]), pack_bf16(x[8 * g + 4], x[8 * g + 5]),
+                           pack_bf16(x[8 * g + 6], x[8 * g + 7]));
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sts128(dst + ((((4 * half + g) ^ row) & 7) << 4), 0, 0, 0, 0);
+        }
+        if (DOT) reinterpret_cast<float *>(sm + L::DOTS)[((nx % 3) * 2 + half) * 64 + row] = m;
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + (nx & 1));
+    };
 
     if (warp < kStateWarps) {
         more_regs<kStateRegs>();
@@ -394,40 +473,52 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         }
     } else if (warp < kOut0) {
         fewer_regs<kEdgeRegs>();
-        // ---------------------------------------------------------------- Kt and P
-        const int bw = warp - kBuild0, quarter = bw & 3, half = bw >> 2, row = 32 * quarter + lane;
-        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
-        float *dots = reinterpret_cast<float *>(sm + L::DOTS);
-        // Kt is made in pieces of 32 x 16 bytes; P's 32 x 32 blocks belong
-        // to the four warps whose lanes hold X's rows, two of them on the diagonal (masked), one
-        // off it and one empty.  By instructions a diagonal block costs three pieces, a full one
-        // two: warps of no block take five pieces (of 32; three of 16 for dk = 64), and so on.
-        const int kind = !outputs ? 4 : quarter >= 2 ? 3 : quarter == half ? 0 : (quarter == 1) != rev ? 1 : 2;   // diagonal, full, empty, none
-        const int pieces = !outputs ? 2 * PK : PK == 2 ? (kind == 0 ? 2 : kind == 1 ? 3 : 5) : (kind == 0 ? 0 : kind == 1 ? 1 : 3);
-        int first_piece = 2 * PK * bw;
-        if (outputs) {
+        // ---------------------------------------------------------------- Kt
+        const int bw = warp - kBuild0;
+        const uint32_t smb = smem_u32(sm);
+        // Kt is made in pieces of 32 x 16 bytes (four rows of a panel).  Without Y (P belongs to the
+        // output warps) an eighth by each warp, in two halves of the rows, so that the second
+        // is made while D takes the first.  With Y, P is built here: by instructions its diagonal
+        // blocks cost three pieces, its full one two, so their warps take fewer (of 32; of 16).
+        const int quarter = bw & 3, half = bw >> 2, kind = quarter < 2 ? kind_of(quarter, half) : 3;
+        int pieces = 2 * PK, first_piece = pieces * bw;
+        if (DOT) {
             const int none = PK == 2 ? 5 : 3, diag = PK == 2 ? 2 : 0, full = PK == 2 ? 3 : 1;
+            pieces = kind == 0 ? diag : kind == 1 ? full : none;
             first_piece = kind == 3 ? (half * 2 + quarter - 2) * none : 4 * none + (kind == 0 ? half * diag : 2 * diag + (kind == 1 ? 0 : full));
         }
+        // the i-th piece of this warp: panel, group of four rows
+        auto place = [&](int i) { return DOT ? first_piece + i : (i % PK) * 16 + 8 * (i / PK) + bw; };
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int s = it % kStages, cnt = count_of(it);
             wait(b_gate + it % L::GATES, it / L::GATES);
             wait(b_load + s, it / kStages);
             if (outputs) wait(b_x + it % NU, it / NU);  // K's place may be written
-            if (it > 0) wait(b_d + ND - 1, it - 1);     // Kt's other terms are read
-            if (outputs && it > 1) wait(b_o + (it & 1), (it - 2) >> 1);   // P of two chunks before is read
+            if (it > 0) wait(L::HALVES == 2 ? b_d1 : b_d + ND - 1, it - 1);   // Kt's other terms are read
+            if (cnt < kChunk) {   // rows of no token are zero values
+                const int per = 8 * (kChunk - cnt);
+                for (int i = 32 * bw + lane; i < PV * per; i += 32 * kBuildWarps)
+                    sts128(smem_u32(stage(it)) + L::V0 + (i / per) * L::V_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
+            }
             {
                 unsigned char *k = stage(it) + L::K0 + 16 * lane;
                 const uint32_t k_at = smem_u32(k), kt_at = smb + L::KT + 16 * lane;
                 const float *f = gate_f(it) + 64 + (lane >> 3);
                 auto piece = [&](int i) { return (uint32_t)((i & 15) * 512 + (i >> 4) * L::QK_STEP); };   // its place in K's panels
-                uint4 next = *reinterpret_cast<const uint4 *>(k + piece(first_piece));
+                uint4 next = *reinterpret_cast<const uint4 *>(k + piece(place(0)));
 #pragma unroll 1
-                for (int i = first_piece; i < first_piece + pieces; ++i) {
+                for (int m = 0; m < pieces; ++m) {
+                    const int i = place(m);
+                    if (L::HALVES == 2 && m == PK) {   // the first half is done
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_kt);
+                        if (it > 0) wait(b_d, it - 1);
+                    }
                     const uint32_t o = piece(i);
                     uint4 u = next;
-                    if (i + 1 < first_piece + pieces) next = *reinterpret_cast<const uint4 *>(k + piece(i + 1));
+                    if (m + 1 < pieces) next = *reinterpret_cast<const uint4 *>(k + piece(place(m + 1)));
                     const float x = f[4 * (i & 15)];
                     if (4 * (i & 15) + (lane >> 3) >= cnt) u = make_uint4(0u, 0u, 0u, 0u);   // no token's row
                     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
@@ -443,82 +534,16 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     sts128(kt_at + 512 * i, w[1][0], w[1][1], w[1][2], w[1][3]);
                     sts128(kt_at + 512 * i + PK * 8192, w[2][0], w[2][1], w[2][2], w[2][3]);
                 }
-                if (cnt < kChunk) {   // rows of no token are zero values
-                    const int per = 8 * (kChunk - cnt);
-                    for (int i = 32 * bw + lane; i < PV * per; i += 32 * kBuildWarps)
-                        sts128(smem_u32(stage(it)) + L::V0 + (i / per) * L::V_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
-                }
-            }
-            if (outputs && quarter < 2) {
-                // P: row `row`, columns 32 half ..
-                const uint32_t dst = smb + L::P + (it & 1) * 8192 + row * 128;
-                const uint32_t xs = tl + 64 * ((uint32_t)it % NU);
-                float m = 0.f;
-                if (kind < 2) {
-                    const bool masked = kind == 0 || cnt < kChunk;
-                    const float2 *c = gate_c(it);
-                    const bool product = c[65].x != 0.f;
-                    const float2 cr = c[row];
-                    const float *fs = gate_f(it) + 192 + 32 * half;
-                    const float fr = gate_f(it)[128 + row];
-#pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        float x[16], x2[16];
-                        tmem_ld16(xs + 32 * half + 16 * b, x);
-                        if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
-                        tmem_wait_ld();
-                        if (product) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 f4 = *reinterpret_cast<const float4 *>(fs + 16 * b + i);
-                                const float2 f2 = make_float2(fr, fr);
-                                const float2 u = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(f4.x, f4.y), f2));
-                                const float2 v = mul2(make_float2(x[i + 2], x[i + 3]), mul2(make_float2(f4.z, f4.w), f2));
-                                x[i] = u.x;
-                                x[i + 1] = u.y;
-                                x[i + 2] = v.x;
-                                x[i + 3] = v.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 cs = c[32 * half + 16 * b + i];
-                                const float d = (cr.x - cs.x) + (cr.y - cs.y);
-                                x[i] *= ex2(rev ? -d : d);
-                            }
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int col = 32 * half + 16 * b + i;
-                                const bool in = rev ? col >= row && col < cnt : col <= row;
-                                x[i] = in ? x[i] : 0.f;
-                                if (DOT) x2[i] = in && col != row ? x2[i] : 0.f;
-                            }
-                        }
-                        if (DOT) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) m = fmaf(x[i], x2[i], m);
-                        }
-#pragma unroll
-                        for (int g = 0; g < 2; ++g)
-                            sts128(dst + ((((4 * half + 2 * b + g) ^ row) & 7) << 4), pack_bf16(x[8 * g], x[8 * g + 1]),
-                                   pack_bf16(x[8 * g + 2], x[8 * g + 3]), pack_bf16(x[8 * g + 4], x[8 * g + 5]),
-                                   pack_bf16(x[8 * g + 6], x[8 * g + 7]));
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) sts128(dst + ((((4 * half + g) ^ row) & 7) << 4), 0, 0, 0, 0);
-                }
-                if (DOT) dots[((it % 3) * 2 + half) * 64 + row] = m;
             }
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(b_built + (it & 3));
-                if (!outputs) mbar_arrive(b_gfree + it % L::GATES);
+            if (lane == 0) mbar_arrive(b_kt + L::HALVES - 1);
+            if (DOT && quarter < 2) {
+                if (it > 1) wait(b_o + (it & 1), (it - 2) >> 1);   // P of two chunks before is read
+                build_p(it, quarter, half);
             }
+            if (lane == 0) mbar_arrive(b_gfree + it % L::GATES);
         }
     } else if (warp < kLoadWarp) {
         fewer_regs<kEdgeRegs>();
@@ -527,14 +552,16 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
         float *dots = reinterpret_cast<float *>(sm + L::DOTS);
 #pragma unroll 1
-        for (int it = 0; it < (outputs ? chunks : 0); ++it) {
+        for (int it = DOT ? 0 : -1; outputs && it < chunks; ++it) {
+            if (!DOT && quarter < 2 && it + 1 < chunks) build_p(it + 1, quarter, half);
+            if (it < 0) continue;   // (P of two chunks before is read: its output was waited for)
             const int cnt = count_of(it);
             if (et == 0) bulk_wait_read_all();   // the staging has left
             named_sync(1, 32 * kOutWarps);
             wait(b_gate + it % L::GATES, it / L::GATES);
-            if (DOT) {
+            if (DOT) {   // Y and P's sums
                 wait(b_load + it % kStages, it / kStages);
-                wait(b_built + (it & 3), it >> 2);
+                wait(b_p + (it & 1), it >> 1);
             }
             wait(b_o + (it & 1), it >> 1);
             if (32 * quarter < DV) {
@@ -717,11 +744,15 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
                 auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
                 auto u_of = [&](int it) { return tm + 64 * ((uint32_t)it % NU); };
-                // four K = 16 steps through one panel (K-major: 32 bytes a step; MN-major: 2048)
-                auto four = [&](uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id, bool more) {
+                // K = 16 steps k0 .. k0 + kn - 1 through one panel (K-major: 32 bytes a step; MN-major: 2048)
+                auto steps = [&](int k0, int kn, uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id,
+                                 bool more) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(d, desc_add(da, ks * astep), desc_add(db, ks * bstep), id, more || ks > 0);
+                    for (int ks = 0; ks < kn; ++ks)
+                        mma_bf16(d, desc_add(da, (k0 + ks) * astep), desc_add(db, (k0 + ks) * bstep), id, more || ks > 0);
+                };
+                auto four = [&](uint32_t d, uint64_t da, uint32_t astep, uint64_t db, uint32_t bstep, uint32_t id, bool more) {
+                    steps(0, 4, d, da, astep, db, bstep, id, more);
                 };
                 auto scores = [&](int it) {
                     const uint32_t st = at_stage(it);
@@ -739,14 +770,15 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     }
                     mma_commit(b_x + it % NU);
                 };
-                auto update = [&](int it, int d) {
+                auto update = [&](int it, int d, int part) {   // part: of Kt's rows
                     const uint32_t st = at_stage(it);
+                    constexpr int KN = 4 / L::HALVES;
 #pragma unroll 1
                     for (int t = 0; t < 3; ++t)
-                        four(tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
-                             t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
-                             2048, ID_MM, t > 0);
-                    mma_commit(b_d + d);
+                        steps(part * KN, KN, tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
+                              t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
+                              2048, ID_MM, part + t > 0);
+                    mma_commit(part + 1 < L::HALVES ? b_d1 : b_d + d);
                 };
                 auto read_out = [&](int it) {
                     const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
@@ -767,7 +799,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (warp == kScoreWarp) {
                     for (int it = 0; it < chunks; ++it) {
                         read(it - NU);
-                        if (DOT && it > 0) wait(b_built + ((it - 1) & 3), (it - 1) >> 2);   // X2 is read
+                        if (DOT && it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X2 is read
                         wait(b_load + it % kStages, it / kStages);
                         scores(it);
                     }
@@ -776,14 +808,19 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll 1
                     for (int it = 0; it < chunks; ++it) {
                         wait(b_load + it % kStages, it / kStages);
-                        wait(b_built + (it & 3), it >> 2);
+                        wait(b_kt, it);
 #pragma unroll
                         for (int d = 0; d < ND; ++d) {   // (D's halves, one at a time)
                             const int before = d == 0 ? it - 1 : it;
                             if (before >= 0) wait(b_dread + (ND == 2 ? d ^ 1 : 0), before);
-                            update(it, d);
-                            if (outputs && d == 0) {
+                            update(it, d, 0);
+                            if (L::HALVES == 2) {
+                                wait(b_kt + 1, it);
+                                update(it, d, 1);
+                            }
+                            if (outputs && d == ND - 1) {
                                 read(it - NR);
+                                wait(b_p + (it & 1), it >> 1);
                                 wait(b_s, it);
                                 read_out(it);
                             }
