@@ -145,8 +145,8 @@ struct Layout {
     static constexpr uint32_t V_STEP = DOT ? 16384 : 8192, Y0 = 0, V0 = DOT ? 8192 : 0;
     static constexpr uint32_t Q0 = PV * V_STEP, K0 = Q0 + 8192, QK_STEP = 16384;
     static constexpr uint32_t STAGE = Q0 + PK * QK_STEP;
-    static constexpr uint32_t KT = STAGES * STAGE;           // Kt's second and third term (the first replaces K)
-    static constexpr uint32_t P = KT + 2 * PK * 8192;        // two chunks' P
+    static constexpr uint32_t KT = STAGES * STAGE;           // (kDot) Kt's second and third term (the first replaces K)
+    static constexpr uint32_t P = KT + (DOT ? 2 * PK * 8192 : 0);   // two chunks' P
     static constexpr uint32_t OUT = P + 2 * 8192;            // output staging, PV panels
     static constexpr uint32_t SMALL = OUT + PV * 8192;
     // per chunk: c [66] as (multiple of 2^-10, remainder), the last pair's first word for whether
@@ -157,14 +157,15 @@ struct Layout {
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
     static constexpr uint32_t TOTAL = BARS + 40 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
-    // tensor memory: U (X, then O^T) of NU chunks, X2 (kDot), R of NR chunks, D, the state operand
-    static constexpr int NU = DOT ? 2 : 3, NR = DOT ? 1 : 2;
-    static constexpr uint32_t TM_X2 = 128, TM_R = 192, TM_D = 256, TM_R1 = 448;
+    // tensor memory.  kDot: U (X, then O^T) of two chunks, X2, R, D, three terms of the state operand.
+    // Otherwise: X, R + O of two chunks, D, the state operand, three terms of Vt.
+    static constexpr int NU = DOT ? 2 : 1, NR = DOT ? 1 : 2;
+    static constexpr uint32_t TM_X2 = 128, TM_R = DOT ? 192 : 64, TM_D = DOT ? 256 : 192;
     static constexpr int ND = DOT && DK == 128 ? 2 : 1;      // D comes in this many parts, one at a time
     static constexpr int DW = DK / ND;
-    static constexpr int HALVES = DOT ? 1 : 2;               // Kt is handed over in this many parts
-    static constexpr uint32_t TM_S = DOT ? 320 : 384;        // terms of DK / 2 columns
-    static_assert(TM_D + DW <= TM_S && TM_S + (DOT ? 3 : 1) * DK / 2 <= (DOT ? 512 : TM_R1), "tensor memory");
+    static constexpr int HALVES = DOT ? 1 : 2;               // Kt (Vt) is handed over in this many parts
+    static constexpr uint32_t TM_S = 320, TM_V = 384;        // terms of DK / 2, of 32 columns
+    static_assert(TM_D + DW <= TM_S && (DOT ? TM_S + 3 * DK / 2 <= 512 : TM_S + DK / 2 <= TM_V), "tensor memory");
 };
 
 // The rest of a wait that was not over at once; its budget and the other warps' expiries are
@@ -291,13 +292,14 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         wait(b_x + nx % NU, nx / NU);
         const uint32_t dst = smb + L::P + (nx & 1) * 8192 + row * 128;
         const uint32_t xs = tl + 64 * ((uint32_t)nx % NU);
+        const float2 ce = gate_c(nx)[64];
         float m = 0.f;
         if (kind < 2) {
             const bool masked = kind == 0 || cnt < kChunk;
             const float2 *c = gate_c(nx);
             const bool product = c[65].x != 0.f;
             const float2 cr = c[row];
-            const float *fs = gate_f(nx) + 192 + 32 * half;
+            const float *fs = gate_f(nx) + (DOT ? 192 : 128) + 32 * half;
             const float fr = gate_f(nx)[128 + row];
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
@@ -306,23 +308,28 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (DOT) tmem_ld16(tl + L::TM_X2 + 32 * half + 16 * b, x2);
                 tmem_wait_ld();
                 if (product) {
+                    const float2 f2 = make_float2(fr, fr);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 f4 = *reinterpret_cast<const float4 *>(fs + 16 * b + i);
-                        const float2 f2 = make_float2(fr, fr);
-                        const float2 u = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(f4.x, f4.y), f2));
-                        const float2 v = mul2(make_float2(x[i + 2], x[i + 3]), mul2(make_float2(f4.z, f4.w), f2));
+                        float2 fu = make_float2(f4.x, f4.y), fv = make_float2(f4.z, f4.w);
+                        if (DOT) {
+                            fu = mul2(fu, f2);
+                            fv = mul2(fv, f2);
+                        }
+                        const float2 u = mul2(make_float2(x[i], x[i + 1]), fu), v = mul2(make_float2(x[i + 2], x[i + 3]), fv);
                         x[i] = u.x;
                         x[i + 1] = u.y;
                         x[i + 2] = v.x;
                         x[i + 3] = v.y;
                     }
                 } else {
+                    const float lr = DOT ? 0.f : fmaxf(rev ? (ce.x - cr.x) + (ce.y - cr.y) : cr.x + cr.y, -kFactorSpan);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 cs = c[32 * half + 16 * b + i];
                         const float d = (cr.x - cs.x) + (cr.y - cs.y);
-                        x[i] *= ex2(rev ? -d : d);
+                        x[i] *= ex2((rev ? -d : d) - lr);
                     }
                 }
                 if (masked) {
@@ -476,49 +483,75 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         // ---------------------------------------------------------------- Kt
         const int bw = warp - kBuild0;
         const uint32_t smb = smem_u32(sm);
-        // Kt is made in pieces of 32 x 16 bytes (four rows of a panel).  Without Y (P belongs to the
-        // output warps) an eighth by each warp, in two halves of the rows, so that the second
-        // is made while D takes the first.  With Y, P is built here: by instructions its diagonal
-        // blocks cost three pieces, its full one two, so their warps take fewer (of 32; of 16).
+        // Without Y (P belongs to the output warps) Vt, in two halves of the rows, so that the
+        // second is made while D takes the first.  With Y, Kt in pieces of 32 x 16 bytes (four
+        // rows of a panel), and P: by instructions its diagonal blocks cost three pieces, its full
+        // one two, so their warps take fewer pieces (of 32; of 16).
         const int quarter = bw & 3, half = bw >> 2, kind = quarter < 2 ? kind_of(quarter, half) : 3;
-        int pieces = 2 * PK, first_piece = pieces * bw;
-        if (DOT) {
-            const int none = PK == 2 ? 5 : 3, diag = PK == 2 ? 2 : 0, full = PK == 2 ? 3 : 1;
-            pieces = kind == 0 ? diag : kind == 1 ? full : none;
-            first_piece = kind == 3 ? (half * 2 + quarter - 2) * none : 4 * none + (kind == 0 ? half * diag : 2 * diag + (kind == 1 ? 0 : full));
-        }
-        // the i-th piece of this warp: panel, group of four rows
-        auto place = [&](int i) { return DOT ? first_piece + i : (i % PK) * 16 + 8 * (i / PK) + bw; };
+        const int none = PK == 2 ? 5 : 3, diag = PK == 2 ? 2 : 0, full = PK == 2 ? 3 : 1;
+        const int pieces = kind == 0 ? diag : kind == 1 ? full : none;
+        const int first_piece = kind == 3 ? (half * 2 + quarter - 2) * none : 4 * none + (kind == 0 ? half * diag : 2 * diag + (kind == 1 ? 0 : full));
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int s = it % kStages, cnt = count_of(it);
             wait(b_gate + it % L::GATES, it / L::GATES);
             wait(b_load + s, it / kStages);
-            if (outputs) wait(b_x + it % NU, it / NU);  // K's place may be written
-            if (it > 0) wait(L::HALVES == 2 ? b_d1 : b_d + ND - 1, it - 1);   // Kt's other terms are read
-            if (cnt < kChunk) {   // rows of no token are zero values
+            if (DOT) wait(b_x + it % NU, it / NU);      // K's place may be written
+            if (it > 0) wait(L::HALVES == 2 ? b_d1 : b_d + ND - 1, it - 1);   // Kt's other terms, Vt's first half are read
+            if (cnt < kChunk) {   // rows of no token are zero values (and keys, where they are not scaled)
                 const int per = 8 * (kChunk - cnt);
                 for (int i = 32 * bw + lane; i < PV * per; i += 32 * kBuildWarps)
                     sts128(smem_u32(stage(it)) + L::V0 + (i / per) * L::V_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
+                if (!DOT) {
+                    for (int i = 32 * bw + lane; i < PK * per; i += 32 * kBuildWarps)
+                        sts128(smem_u32(stage(it)) + L::K0 + (i / per) * L::QK_STEP + cnt * 128 + (i % per) * 16, 0, 0, 0, 0);
+                    named_sync(3, 32 * kBuildWarps);   // the warps read one another's rows
+                }
             }
-            {
-                unsigned char *k = stage(it) + L::K0 + 16 * lane;
-                const uint32_t k_at = smem_u32(k), kt_at = smb + L::KT + 16 * lane;
-                const float *f = gate_f(it) + 64 + (lane >> 3);
-                auto piece = [&](int i) { return (uint32_t)((i & 15) * 512 + (i >> 4) * L::QK_STEP); };   // its place in K's panels
-                uint4 next = *reinterpret_cast<const uint4 *>(k + piece(place(0)));
+            if constexpr (!DOT) {
+                // Vt: 16 channels by each warp, 16 tokens at a time: transposed fragments of V, scaled by
+                // the tokens' factors, as three bf16 terms in tensor memory
+                const int ch = 32 * quarter + 16 * half + 8 * ((lane >> 3) & 1), tok = 8 * (lane >> 4) + (lane & 7);
+                const uint32_t src = smem_u32(stage(it)) + L::V0 + (ch >> 6) * L::V_STEP + tok * 128 + ((((ch >> 3) ^ tok) & 7) << 4);
+                const uint32_t dst = tm + ((uint32_t)(32 * quarter + 16 * half) << 16) + L::TM_V;
+                const float *f = gate_f(it) + 64 + 2 * (lane & 3);
 #pragma unroll 1
-                for (int m = 0; m < pieces; ++m) {
-                    const int i = place(m);
-                    if (L::HALVES == 2 && m == PK) {   // the first half is done
+                for (int b = 0; b < 4; ++b) {
+                    if (b == 2) {   // the first half is done
+                        tmem_wait_st();
                         fence_proxy_async();
+                        tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(b_kt);
                         if (it > 0) wait(b_d, it - 1);
                     }
+                    if (32 * quarter < DV) {
+                        uint32_t u[4], w[3][4];
+                        ldsm_x4_trans(src + b * 2048, u);
+                        const float2 f0 = *reinterpret_cast<const float2 *>(f + 16 * b), f1 = *reinterpret_cast<const float2 *>(f + 16 * b + 8);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {   // tokens + 8 (e / 2), channels + 8 (e % 2)
+                            float2 y = mul2(make_float2(lo_bf16(u[e]), hi_bf16(u[e])), e < 2 ? f0 : f1);
+                            w[0][e] = take_bf16(y);
+                            w[1][e] = take_bf16(y);
+                            w[2][e] = last_bf16(y);
+                        }
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) tmem_st_frag8(dst + t * 32 + 8 * b, w[t]);
+                    }
+                }
+                tmem_wait_st();
+            } else {
+                unsigned char *k = stage(it) + L::K0 + 16 * lane;
+                const uint32_t k_at = smem_u32(k), kt_at = smb + L::KT + 16 * lane;
+                const float *f = gate_f(it) + 64 + (lane >> 3);
+                auto piece = [&](int i) { return (uint32_t)((i & 15) * 512 + (i >> 4) * L::QK_STEP); };   // its place in K's panels
+                uint4 next = *reinterpret_cast<const uint4 *>(k + piece(first_piece));
+#pragma unroll 1
+                for (int i = first_piece; i < first_piece + pieces; ++i) {
                     const uint32_t o = piece(i);
                     uint4 u = next;
-                    if (m + 1 < pieces) next = *reinterpret_cast<const uint4 *>(k + piece(place(m + 1)));
+                    if (i + 1 < first_piece + pieces) next = *reinterpret_cast<const uint4 *>(k + piece(i + 1));
                     const float x = f[4 * (i & 15)];
                     if (4 * (i & 15) + (lane >> 3) >= cnt) u = make_uint4(0u, 0u, 0u, 0u);   // no token's row
                     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
@@ -581,8 +614,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const int ch = 32 * quarter + 16 * g + 8 * ((lane >> 3) & 1);
                     const uint32_t mat = (ch >> 6) * 8192 + tok * 128 + ((((ch >> 3) ^ tok) & 7) << 4);
                     float r[16], o[16];
-                    tmem_ld_frag32(tl + lanes + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R) + 32 * half, r);
-                    tmem_ld_frag32(tl + lanes + 64 * ((uint32_t)it % NU) + 32 * half, o);
+                    tmem_ld_frag32(tl + lanes + L::TM_R + 64 * ((uint32_t)it % NR) + 32 * half, r);
+                    if (DOT) tmem_ld_frag32(tl + lanes + 64 * ((uint32_t)it % NU) + 32 * half, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {   // 16 tokens: matrices (b, channels), b = 2 e, 2 e + 1
@@ -592,7 +625,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {   // block b, channels + 8 (i % 2)
                             const int b = 2 * e + (i >> 1), v = 4 * b + 2 * (i & 1);
-                            const float2 r2 = make_float2(r[v], r[v + 1]), x = fma2(f[b], r2, make_float2(o[v], o[v + 1]));
+                            const float2 r2 = make_float2(r[v], r[v + 1]);
+                            const float2 x = DOT ? fma2(f[b], r2, make_float2(o[v], o[v + 1])) : mul2(f[b], r2);
                             if (DOT) z[b] = fma2(mul2(f[b], r2), make_float2(lo_bf16(y[i]), hi_bf16(y[i])), z[b]);
                             w[i] = pack_bf16(x.x, x.y);
                         }
@@ -712,14 +746,21 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
-                    const float2 w = sub(ce, u[e]), m = sub(u[e], mid);
-                    const float head = ex2(u[e].x + u[e].y), tail = ex2(w.x + w.y), d = m.x + m.y;
-                    const float up = ex2(d), down = ex2(-d);
+                    const float2 w = sub(ce, u[e]);
+                    const float lh = u[e].x + u[e].y, lt = w.x + w.y;
                     g[t] = u[e];
-                    gr[t] = rev ? tail : head;
-                    gr[64 + t] = rev ? head : tail;
-                    gr[128 + t] = rev ? down : up;
-                    gr[192 + t] = rev ? up : down;
+                    gr[64 + t] = ex2(rev ? lh : lt);
+                    if (DOT) {
+                        const float2 m = sub(u[e], mid);
+                        const float d = rev ? -m.x - m.y : m.x + m.y;
+                        gr[t] = ex2(rev ? lt : lh);
+                        gr[128 + t] = ex2(d);
+                        gr[192 + t] = ex2(-d);
+                    } else {
+                        const float lr = fmaxf(rev ? lt : lh, -kFactorSpan);
+                        gr[t] = ex2(lr);
+                        gr[128 + t] = ex2(-lr);
+                    }
                 }
                 if (lane == 0) {
                     g[64] = ce;
@@ -737,7 +778,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // ---------------------------------------------------------------- MMA issue
             if (lane == 0 && chunks > 0 && ((outputs && warp == kScoreWarp) || warp == kUpdateWarp)) {
                 constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
-                                   ID_MM = idesc_bf16(128, L::DW, true, true);
+                                   ID_MM = idesc_bf16(128, L::DW, DOT, true);
                 const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
                 const uint64_t dV = smem_desc_sw128(smem_u32(sm), PV == 2 ? L::V_STEP : 8192, 1024);   // MN-major, V panels
                 const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
@@ -774,14 +815,23 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const uint32_t st = at_stage(it);
                     constexpr int KN = 4 / L::HALVES;
 #pragma unroll 1
-                    for (int t = 0; t < 3; ++t)
+                    for (int t = 0; t < 3; ++t) {
+                        if (!DOT) {   // Vt from tensor memory, K as loaded
+                            const uint64_t dk = desc_add(dT0, st + L::K0 + part * KN * 2048);
+#pragma unroll
+                            for (int ks = 0; ks < KN; ++ks)
+                                mma_bf16_ts(tm + L::TM_D, tm + L::TM_V + 32 * t + 8 * (part * KN + ks), desc_add(dk, ks * 2048), ID_MM,
+                                            part + t + ks > 0);
+                            continue;
+                        }
                         steps(part * KN, KN, tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
                               t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
                               2048, ID_MM, part + t > 0);
+                    }
                     mma_commit(part + 1 < L::HALVES ? b_d1 : b_d + d);
                 };
                 auto read_out = [&](int it) {
-                    const uint32_t st = at_stage(it), r = tm + (NR == 2 && (it & 1) ? L::TM_R1 : L::TM_R);
+                    const uint32_t st = at_stage(it), r = tm + L::TM_R + 64 * ((uint32_t)it % NR);
 #pragma unroll 1
                     for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
                         const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
@@ -790,7 +840,9 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             mma_bf16_ts(r, tm + L::TM_S + 32 * b + 8 * ks, desc_add(dq, ks * 32), ID_KK, b + ks > 0);
                     }
                     mma_commit(b_r);
-                    four(u_of(it), desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, false);
+                    if (!DOT) wait(b_p + (it & 1), it >> 1);
+                    // without Y, onto R
+                    steps(0, 4, DOT ? u_of(it) : r, desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, !DOT);
                     mma_commit(b_o + (it & 1));
                 };
                 auto read = [&](int it) {   // R and O of the chunk are read
@@ -798,8 +850,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 };
                 if (warp == kScoreWarp) {
                     for (int it = 0; it < chunks; ++it) {
-                        read(it - NU);
-                        if (DOT && it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X2 is read
+                        if (DOT) read(it - NU);
+                        if (it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X, X2 are read
                         wait(b_load + it % kStages, it / kStages);
                         scores(it);
                     }
@@ -820,7 +872,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             }
                             if (outputs && d == ND - 1) {
                                 read(it - NR);
-                                wait(b_p + (it & 1), it >> 1);
+                                if (DOT) wait(b_p + (it & 1), it >> 1);
                                 wait(b_s, it);
                                 read_out(it);
                             }

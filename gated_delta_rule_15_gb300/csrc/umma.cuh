@@ -302,6 +302,12 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+// 16 lanes x 8 consecutive 32-bit columns from the layout of ldsm_x4_trans (an mma A fragment of
+// 16-bit pairs): v[0], v[1] = column t % 4 of lanes t / 4, t / 4 + 8; v[2], v[3] = column 4 + t % 4.
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 // 32 lanes x 4 consecutive 32-bit columns, raw bits.
 __device__ __forceinline__ void tmem_st4u(uint32_t taddr, const uint32_t (&v)[4]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
