@@ -135,17 +135,18 @@ __device__ __forceinline__ uint32_t last_bf16(float2 x) {
 // two powers around the chunk's middle, 2^(c_r - c_31) 2^(c_31 - c_s).
 constexpr float kFactorSpan = 60.f;
 
-// Shared memory.  A stage holds [Y? V | ...panels] and [Q K | ...panels], panels of 64 channels
-// x 64 tokens (8 KB, 128-byte swizzle): every panel used as the first half of a 128-row
-// operand has a loaded panel behind it, and so has V's when dv = 64.
+// Shared memory.  A stage holds the panels [V ..] and [Q K | ..], 64 channels x 64 tokens each (8 KB,
+// 128-byte swizzle): every panel used as the first half of a 128-row operand has another
+// one behind it, and so has V's when dv = 64.  Y, which the outputs read last, has stages of its own.
 template <int DK, int DV, bool DOT>
 struct Layout {
     static constexpr int PK = DK / 64, PV = DV / 64;
     static constexpr int STAGES = DOT ? 2 : 3, GATES = 4;    // chunks whose rows, whose gates are there
-    static constexpr uint32_t V_STEP = DOT ? 16384 : 8192, Y0 = 0, V0 = DOT ? 8192 : 0;
-    static constexpr uint32_t Q0 = PV * V_STEP, K0 = Q0 + 8192, QK_STEP = 16384;
+    static constexpr uint32_t V0 = 0, V_STEP = 8192, Q0 = PV * V_STEP, K0 = Q0 + 8192, QK_STEP = 16384;
     static constexpr uint32_t STAGE = Q0 + PK * QK_STEP;
-    static constexpr uint32_t KT = STAGES * STAGE;           // (kDot) Kt's second and third term (the first replaces K)
+    static constexpr int YS = DOT ? 3 : 0;
+    static constexpr uint32_t Y = STAGES * STAGE, Y_STAGE = PV * 8192;
+    static constexpr uint32_t KT = Y + YS * Y_STAGE;           // (kDot) Kt's second and third term (the first replaces K)
     static constexpr uint32_t P = KT + (DOT ? 2 * PK * 8192 : 0);   // two chunks' P
     static constexpr uint32_t OUT = P + 2 * 8192;            // output staging, PV panels
     static constexpr uint32_t SMALL = OUT + PV * 8192;
@@ -155,7 +156,7 @@ struct Layout {
     static constexpr uint32_t DOTS = SMALL + GATES * GATE;   // (kDot) [3][2][64] of X X2, [4][64] of R, [8] of the state
     static constexpr uint32_t DOT_R = 3 * 2 * 64, DOT_S = DOT_R + 4 * 64;
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
-    static constexpr uint32_t TOTAL = BARS + 40 * 8;
+    static constexpr uint32_t TOTAL = BARS + 42 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
     // tensor memory.  kDot: U (X, then O^T) of two chunks, X2, R, D, three terms of the state operand.
     // Otherwise: X, R + O of two chunks, D, the state operand, three terms of Vt.
@@ -230,6 +231,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint64_t *b_o = bars + 28;         // [2] R and O are there
     uint64_t *b_oread = bars + 30;     // [4] R and O are read
     uint64_t *b_end = bars + 34;       // every MMA is done
+    uint64_t *b_y = bars + 35, *b_yfree = bars + 38;   // [YS] Y is there, is done with
     // A parity wait tells a phase from its neighbours only: no barrier completes a second
     // time before everyone who waits for it has seen the first.  Where a warp may run ahead of
     // another (X of later chunks, outputs), consecutive chunks take different barriers.
@@ -239,7 +241,11 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(b_load + i, 1);
-            mbar_init(b_free + i, 1 + (DOT ? kOutWarps : 0));   // MMAs; with Y, the outputs too
+            mbar_init(b_free + i, 1);
+        }
+        for (int i = 0; i < L::YS; ++i) {
+            mbar_init(b_y + i, 1);
+            mbar_init(b_yfree + i, 1 + kOutWarps);   // X2, the outputs
         }
         for (int i = 0; i < L::GATES; ++i) {
             mbar_init(b_gate + i, 1);
@@ -422,6 +428,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             wait(b_gate + it % L::GATES, it / L::GATES);
             const float2 ce = gate_c(it)[64], cl = gate_c(it)[63];
             const float decay = ex2(ce.x + ce.y);
+            if (DOT && rev && it + 1 < chunks && at_anchor(it + 1) && mine) {   // the next one's stored state into L2
+                const float *d = anchor_ptr(it + 1) - lane;
+#pragma unroll
+                for (int i = 0; i < NV; i += 32)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(d + (size_t)(i + lane) * 2 * DV));
+            }
             if (rev && at_anchor(it)) {
                 float x = 0.f;
                 if (mine) {
@@ -429,7 +441,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         x = fmaf(__ldcs(d + (size_t)i * 2 * DV), i & 1 ? S[i / 2].y : S[i / 2].x, x);
-                        if (i % 8 == 7) asm volatile("" ::: "memory");   // eight loads at a time: registers
+                        if (i % 16 == 15) asm volatile("" ::: "memory");   // sixteen loads at a time: registers
                     }
                 }
 #pragma unroll
@@ -593,7 +605,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             named_sync(1, 32 * kOutWarps);
             wait(b_gate + it % L::GATES, it / L::GATES);
             if (DOT) {   // Y and P's sums
-                wait(b_load + it % kStages, it / kStages);
+                wait(b_y + it % 3, it / 3);
                 wait(b_p + (it & 1), it >> 1);
             }
             wait(b_o + (it & 1), it >> 1);
@@ -621,7 +633,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     for (int e = 0; e < 2; ++e) {   // 16 tokens: matrices (b, channels), b = 2 e, 2 e + 1
                         uint32_t w[4], y[4];
                         if (DOT)
-                            ldsm_x4_trans(smem_u32(stage(it)) + L::Y0 + mat + (ch >> 6) * (L::V_STEP - 8192) + e * 2048, y);
+                            ldsm_x4_trans(smb + L::Y + (uint32_t)(it % 3) * L::Y_STAGE + mat + e * 2048, y);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {   // block b, channels + 8 (i % 2)
                             const int b = 2 * e + (i >> 1), v = 4 * b + 2 * (i & 1);
@@ -652,7 +664,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (lane == 0) {
                 mbar_arrive(b_oread + (it & 3));
                 mbar_arrive(b_gfree + it % L::GATES);
-                if (DOT) mbar_arrive(b_free + it % kStages);
+                if (DOT) mbar_arrive(b_yfree + it % 3);
             }
             named_sync(1, 32 * kOutWarps);
             const int64_t base = row_of(it);
@@ -680,7 +692,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         fewer_regs<kIssueRegs>();
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- loads and gates
-            const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV + (DOT ? PV : 0) : PK + PV);
+            const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV : PK + PV);
             float total = 0.f;
             float x[2];
             int issued = 0;   // (lane 0) chunks whose loads were issued; none after an expiry
@@ -707,9 +719,14 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                         tma_load_3d(st + L::K0 + b * L::QK_STEP, &tk, b_load + s, 64 * b, h, row);
                     }
 #pragma unroll 1
-                    for (int b = 0; b < PV; ++b) {
-                        if (DOT) tma_load_3d(st + L::Y0 + b * L::V_STEP, &ty, b_load + s, 64 * b, h, row);
-                        tma_load_3d(st + L::V0 + b * L::V_STEP, &tv, b_load + s, 64 * b, h, row);
+                    for (int b = 0; b < PV; ++b) tma_load_3d(st + L::V0 + b * L::V_STEP, &tv, b_load + s, 64 * b, h, row);
+                    if (DOT) {
+                        const int y = it % 3;
+                        if (it >= 3) wait(b_yfree + y, it / 3 - 1);
+                        mbar_arrive_expect_tx(b_y + y, L::Y_STAGE);
+#pragma unroll 1
+                        for (int b = 0; b < PV; ++b)
+                            tma_load_3d(sm + L::Y + y * L::Y_STAGE + b * 8192, &ty, b_y + y, 64 * b, h, row);
                     }
                 }
                 // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
@@ -771,8 +788,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
             if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
             // the loads have landed before the block ends, also after an expiry
-            if (lane == 0)
+            if (lane == 0) {
                 for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
+                for (int it = max(0, issued - 3); DOT && it < issued; ++it) wait_cycles(b_y + it % 3, (it / 3) & 1);
+            }
             __syncwarp();
         } else if (warp >= kScoreWarp) {
             // ---------------------------------------------------------------- MMA issue
@@ -780,7 +799,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
                                    ID_MM = idesc_bf16(128, L::DW, DOT, true);
                 const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
-                const uint64_t dV = smem_desc_sw128(smem_u32(sm), PV == 2 ? L::V_STEP : 8192, 1024);   // MN-major, V panels
+                const uint64_t dV = smem_desc_sw128(smem_u32(sm), L::V_STEP, 1024);   // MN-major, V panels
                 const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
                 const uint64_t dT = smem_desc_sw128(smem_u32(sm), 8192, 1024);            // and its others
                 auto at_stage = [&](int it) { return (uint32_t)(it % kStages) * L::STAGE; };
@@ -805,11 +824,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     if (DOT) {
 #pragma unroll 1
                         for (int b = 0; b < PV; ++b) {
-                            const uint32_t o = st + b * L::V_STEP;
-                            four(tm + L::TM_X2, desc_add(dK, o + L::Y0), 32, desc_add(dK, o + L::V0), 32, ID_KK, b > 0);
+                            four(tm + L::TM_X2, desc_add(dK, L::Y + (uint32_t)(it % 3) * L::Y_STAGE + b * 8192), 32,
+                                 desc_add(dK, st + L::V0 + b * L::V_STEP), 32, ID_KK, b > 0);
                         }
                     }
                     mma_commit(b_x + it % NU);
+                    if (DOT) mma_commit(b_yfree + it % 3);
                 };
                 auto update = [&](int it, int d, int part) {   // part: of Kt's rows
                     const uint32_t st = at_stage(it);
@@ -853,6 +873,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                         if (DOT) read(it - NU);
                         if (it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X, X2 are read
                         wait(b_load + it % kStages, it / kStages);
+                        if (DOT) wait(b_y + it % 3, it / 3);
                         scores(it);
                     }
                 } else {

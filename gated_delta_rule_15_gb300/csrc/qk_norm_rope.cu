@@ -34,8 +34,9 @@ struct RopeArgs {
     const int64_t *pos;
     int64_t n_tok, seq_len, pos0;
     int heads[2], rot, groups;   // groups: runs of heads a token's rows are split into
+    int blocks[2];           // (gradient) blocks of q, of k
     float eps, scale;
-    float *partial;          // (gradient) [blocks][2][d] partial weight gradients, or NULL
+    float *partial;          // (gradient) [d][blocks of q], [d][blocks of k] partial weight gradients, or NULL
 };
 
 template <typename T> struct Vec8;   // 8 storage elements
@@ -87,46 +88,54 @@ __device__ __forceinline__ void st8(__nv_bfloat16 *p, const float (&f)[8]) {
     *reinterpret_cast<uint4 *>(p) = u;
 }
 
-// Cosine and sine (times c) of this lane's pairs: 8 (half layout, one per value) or 4.
+// Of this lane's 8 values: the cosine (times c) of each one's pair and the signed sine (times c) its
+// pair's other value enters with, for a rotation forwards or back; 1 and 0 behind the rotated part.
 template <bool HALF>
-__device__ __forceinline__ void angles(const RopeArgs &a, int64_t pos, int l, float (&co)[HALF ? 8 : 4],
-                                       float (&si)[HALF ? 8 : 4]) {
+__device__ __forceinline__ void angles(const RopeArgs &a, int64_t pos, int l, bool back, float (&co)[8], float (&si)[8]) {
     constexpr int NP = HALF ? 8 : 4;
     const int hr = a.rot / 2, i0 = HALF ? (8 * l < hr ? 8 * l : 8 * l - hr) : 4 * l;
+    if (8 * l >= a.rot) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            co[e] = 1.f;
+            si[e] = 0.f;
+        }
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
-        co[e] = 1.f;
-        si[e] = 0.f;
-    }
-    if (8 * l < a.rot) {
-#pragma unroll
-        for (int e = 0; e < NP; ++e) {
-            const uint64_t turn = (uint64_t)pos * __ldg(a.table + i0 + e);
-            // signed upper half: [-1/2, 1/2) turns, i.e. that many times 2 pi
-            const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;   // 2^-31
-            float s, c;
-            sincospif(half_turns, &s, &c);
-            co[e] = c * a.scale;
-            si[e] = s * a.scale;
+        const uint64_t turn = (uint64_t)pos * __ldg(a.table + i0 + e);
+        // signed upper half: [-1/2, 1/2) turns, i.e. that many times 2 pi
+        const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;   // 2^-31
+        float s, c;
+        sincospif(half_turns, &s, &c);
+        c *= a.scale;
+        s *= back ? -a.scale : a.scale;
+        if (HALF) {
+            co[e] = c;
+            si[e] = 8 * l < hr ? -s : s;
+        } else {
+            co[2 * e] = co[2 * e + 1] = c;
+            si[2 * e] = -s;
+            si[2 * e + 1] = s;
         }
     }
 }
 
-// (x_a cos - x_b sin, x_b cos + x_a sin) of this lane's 8 values; `other` holds the pairs'
-// other halves in the half layout.  The angle's sign is in si.
+// The lane that holds the other values of this lane's pairs (half layout).
 template <bool HALF>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&other)[8], bool first, const float (&co)[HALF ? 8 : 4],
-                                       const float (&si)[HALF ? 8 : 4]) {
+__device__ __forceinline__ int partner(const RopeArgs &a, int lane, int l) {
+    return HALF && 8 * l < a.rot ? (16 * l < a.rot ? lane + a.rot / 16 : lane - a.rot / 16) : lane;
+}
+// Each value's pair's other one.
+template <bool HALF, typename T>
+__device__ __forceinline__ void others(const Vec8<T> &raw, const float (&x)[8], int src, float (&o)[8]) {
     if (HALF) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf(first ? -other[e] : other[e], si[e], x[e] * co[e]);
+        const Vec8<T> v = shfl8(raw, src);
+        unpack(v, o);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float p = x[2 * e], q = x[2 * e + 1];
-            x[2 * e] = fmaf(-q, si[e], p * co[e]);
-            x[2 * e + 1] = fmaf(p, si[e], q * co[e]);
-        }
+        for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
     }
 }
 
@@ -137,163 +146,167 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// `it`-th unit of work: a token and a run of its q and k heads (numbered behind one another).
+// A group of lanes' unit of work: a token and a run of its q and k heads (numbered behind one
+// another).  Of each kind s (q, k) every row is
+//     y_e = r (A_e x_e + B_e x_e'),    A = w cos, B = +- w' sin
+// (x' the pair's other value), so weights, sines and signs are folded once a token.  Shuffles are
+// by whole warps: its groups make as many turns as the longest, the rest of them on no row.
 template <int D, bool HALF, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
 qk_rope_kernel(const RopeArgs a, int norm) {
-    constexpr int LPR = D / 8, U = 2;
-    const int lane = threadIdx.x & 31, l = lane % LPR;
+    constexpr int LPR = D / 8, U = 4;
+    const int lane = threadIdx.x & 31, l = lane % LPR, src = partner<HALF>(a, lane, l), lp = l + src - lane;
     const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
     const int64_t tok = unit / a.groups;
     const int g = (int)(unit % a.groups), all = a.heads[0] + a.heads[1];
-    const int h0 = (int)((int64_t)all * g / a.groups), h1 = (int)((int64_t)all * (g + 1) / a.groups);
-    const bool live = tok < a.n_tok;   // shuffles are by whole warps: idle groups stay, on no heads
+    const bool live = tok < a.n_tok;
     const int64_t pos = !live ? 0 : a.pos ? a.pos[tok] : a.pos0 + tok % a.seq_len;
-    float co[HALF ? 8 : 4], si[HALF ? 8 : 4];
-    angles<HALF>(a, pos, l, co, si);
-    const bool rotated = 8 * l < a.rot, first = 16 * l < a.rot;
-    const int src = HALF && rotated ? (lane + (first ? a.rot / 16 : -(a.rot / 16))) : lane;
-    // every group of a warp runs as often as the longest one
-    const int most = (all + a.groups - 1) / a.groups;
-    for (int i = 0; i < most; i += U) {
-        Vec8<T> raw[U];
+    float co[8], si[8];
+    angles<HALF>(a, pos, l, false, co, si);
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+        const int first = s ? a.heads[0] : 0, last = s ? all : a.heads[0];
+        const int h0 = max((int)((int64_t)all * g / a.groups), first), h1 = min((int)((int64_t)all * (g + 1) / a.groups), last);
+        const int rows = live && h1 > h0 ? h1 - h0 : 0, most = __reduce_max_sync(0xffffffffu, rows);
+        if (most == 0) continue;
+        const float *w = a.w[s];
+        float A[8], B[8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + i + u, s = h >= a.heads[0];
-            if (live && h < h1)
-                raw[u] = ld8((const T *)a.x[s] + tok * a.stride[s] + (int64_t)(h - s * a.heads[0]) * D + 8 * l);
-            else raw[u] = Vec8<T>{};
+        for (int e = 0; e < 8; ++e) {
+            A[e] = co[e] * (w ? __ldg(w + 8 * l + e) : 1.f);
+            B[e] = si[e] * (w ? __ldg(w + (HALF ? 8 * lp + e : 8 * l + (e ^ 1))) : 1.f);
         }
+        const T *x0 = (const T *)a.x[s] + tok * a.stride[s] + (int64_t)(h0 - first) * D + 8 * l;
+        T *y0 = (T *)a.y[s] + tok * a.out_stride[s] + (int64_t)(h0 - first) * D + 8 * l;
+#pragma unroll 1
+        for (int i = 0; i < most; i += U) {
+            Vec8<T> raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + i + u, s = h >= a.heads[0];
-            float x[8], o[8];
-            unpack(raw[u], x);
-            if (HALF) {
-                const Vec8<T> other = shfl8(raw[u], src);
-                unpack(other, o);
-            }
-            float r = 1.f;
-            if (norm != DR_NORM_NONE) {
-                float ss = 0.f;
+            for (int u = 0; u < U; ++u) raw[u] = i + u < rows ? ld8(x0 + (int64_t)(i + u) * D) : Vec8<T>{};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = row_sum<LPR>(ss);
-                r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
-            }
-            const float *w = a.w[s];
+            for (int u = 0; u < U; ++u) {
+                float x[8], o[8];
+                unpack(raw[u], x);
+                others<HALF>(raw[u], x, src, o);
+                float r = 1.f;
+                if (norm != DR_NORM_NONE) {
+                    float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] *= w ? r * __ldg(w + 8 * l + e) : r;
-                if (HALF) o[e] *= w ? r * __ldg(w + 8 * (l + src - lane) + e) : r;
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                    ss = row_sum<LPR>(ss);
+                    r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = r * fmaf(B[e], o[e], A[e] * x[e]);
+                if (i + u < rows) st8(y0 + (int64_t)(i + u) * D, x);
             }
-            if (rotated) rotate<HALF>(x, o, first, co, si);
-            if (live && h < h1)
-                st8((T *)a.y[s] + tok * a.out_stride[s] + (int64_t)(h - s * a.heads[0]) * D + 8 * l, x);
         }
     }
 }
 
-// Gradient: persistent groups of lanes over the tokens, the weight gradients of a lane's 8
-// values in registers, summed over the block at the end (a fixed order: no atomics).
+// Gradient: a block takes rows of one kind (q or k), its groups of lanes run over the tokens, the
+// weight gradients of a lane's 8 values in registers, summed over the block at the end (a
+// fixed order: no atomics).  The next row is loaded while one is worked on.
 template <int D, bool HALF, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 qk_rope_bwd_kernel(const RopeArgs a, int norm) {
     constexpr int LPR = D / 8, RPB = 256 / LPR;
-    const int lane = threadIdx.x & 31, l = lane % LPR, all = a.heads[0] + a.heads[1];
-    const bool rotated = 8 * l < a.rot, first = 16 * l < a.rot;
-    const int src = HALF && rotated ? (lane + (first ? a.rot / 16 : -(a.rot / 16))) : lane;
-    const int64_t units = a.n_tok * a.groups;
-    const int most = (all + a.groups - 1) / a.groups;
-    float dw[2][8];
+    const int lane = threadIdx.x & 31, l = lane % LPR, src = partner<HALF>(a, lane, l);
+    const int s = (int)blockIdx.x >= a.blocks[0], blocks = a.blocks[s], block = (int)blockIdx.x - s * a.blocks[0], heads = a.heads[s];
+    const int groups = a.groups < heads ? a.groups : heads;   // runs of heads a token's rows are split into
+    const int64_t units = a.n_tok * groups;
+    float dw[8], w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-    for (int64_t u0 = (int64_t)blockIdx.x * RPB; u0 < units; u0 += (int64_t)gridDim.x * RPB) {
-        const int64_t unit = u0 + threadIdx.x / LPR, tok = unit / a.groups;
+    for (int e = 0; e < 8; ++e) {
+        dw[e] = 0.f;
+        w[e] = a.w[s] ? a.w[s][8 * l + e] : 1.f;
+    }
+#pragma unroll 1
+    for (int64_t u0 = (int64_t)block * RPB; u0 < units; u0 += (int64_t)blocks * RPB) {
+        const int64_t unit = u0 + threadIdx.x / LPR, tok = unit / groups;
         const bool live = unit < units;
-        const int g = (int)(unit % a.groups);
-        const int h0 = (int)((int64_t)all * g / a.groups), h1 = (int)((int64_t)all * (g + 1) / a.groups);
+        const int g = (int)(unit % groups);
         const int64_t pos = !live ? 0 : a.pos ? a.pos[tok] : a.pos0 + tok % a.seq_len;
-        float co[HALF ? 8 : 4], si[HALF ? 8 : 4];
-        angles<HALF>(a, pos, l, co, si);
-#pragma unroll
-        for (int e = 0; e < (HALF ? 8 : 4); ++e) si[e] = -si[e];   // back
+        const int h0 = (int)((int64_t)heads * g / groups), h1 = (int)((int64_t)heads * (g + 1) / groups);
+        const int rows = live ? h1 - h0 : 0, most = __reduce_max_sync(0xffffffffu, rows);
+        const int64_t row = (int64_t)h0 * D + 8 * l;
+        const T *x0 = (const T *)a.x[s] + tok * a.stride[s] + row, *d0 = (const T *)a.dy[s] + tok * (int64_t)heads * D + row;
+        T *y0 = (T *)a.y[s] + tok * a.out_stride[s] + row;
+        Vec8<T> nx{}, nd{};
+        if (rows > 0) {
+            nx = ld8(x0);
+            nd = ld8(d0);
+        }
+        float co[8], si[8];
+        angles<HALF>(a, pos, l, true, co, si);
+#pragma unroll 1
         for (int i = 0; i < most; ++i) {
-            const int h = h0 + i, s = h >= a.heads[0];
-            const bool on = live && h < h1;
-            const int64_t row = (int64_t)(h - s * a.heads[0]) * D + 8 * l;
-            Vec8<T> vx{}, vd{};
-            if (on) {
-                vx = ld8((const T *)a.x[s] + tok * a.stride[s] + row);
-                vd = ld8((const T *)a.dy[s] + tok * (int64_t)a.heads[s] * D + row);
+            const Vec8<T> vx = nx, vd = nd;
+            if (i + 1 < rows) {
+                nx = ld8(x0 + (int64_t)(i + 1) * D);
+                nd = ld8(d0 + (int64_t)(i + 1) * D);
+            } else {
+                nx = nd = Vec8<T>{};
             }
             float x[8], u[8], o[8];
             unpack(vx, x);
             unpack(vd, u);
-            if (HALF) {
-                const Vec8<T> other = shfl8(vd, src);
-                unpack(other, o);
-            }
-            if (rotated) rotate<HALF>(u, o, first, co, si);
-            const float *w = a.w[s];
+            others<HALF>(vd, u, src, o);
             float r = 1.f, gx = 0.f, ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            if (norm != DR_NORM_NONE) {
-                ss = row_sum<LPR>(ss);
-                r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
-            }
-            if (a.partial) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float t = u[e] * x[e] * r;
-                    if (s) dw[1][e] += t; else dw[0][e] += t;
-                }
-            }
-#pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (w) u[e] *= __ldg(w + 8 * l + e);
-                gx = fmaf(u[e], x[e], gx);
+                ss = fmaf(x[e], x[e], ss);
+                u[e] = fmaf(si[e], o[e], co[e] * u[e]);   // rotated back
+                o[e] = u[e] * x[e];
+                u[e] *= w[e];
+                gx = fmaf(o[e], w[e], gx);
             }
             if (norm != DR_NORM_NONE) {
-                gx = row_sum<LPR>(gx);
-                const float f = -r * r * r * gx * (norm == DR_NORM_RMS ? 1.f / D : 1.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = fmaf(x[e], f, u[e] * r);
+                for (int k = 1; k < LPR; k <<= 1) {   // both sums of the row side by side
+                    ss += __shfl_xor_sync(0xffffffffu, ss, k);
+                    gx += __shfl_xor_sync(0xffffffffu, gx, k);
+                }
+                r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
+                const float f = -r * r * gx * (norm == DR_NORM_RMS ? 1.f / D : 1.f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = r * fmaf(x[e], f, u[e]);
             }
-            if (on) st8((T *)a.y[s] + tok * a.out_stride[s] + row, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dw[e] = fmaf(o[e], r, dw[e]);
+            if (i < rows) st8(y0 + (int64_t)i * D, u);
         }
     }
     if (!a.partial) return;
     __shared__ float sum[RPB][D];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[threadIdx.x / LPR][8 * l + e] = dw[s][e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < D; c += 256) {
-            float t = 0.f;
-            for (int r = 0; r < RPB; ++r) t += sum[r][c];
-            a.partial[((size_t)blockIdx.x * 2 + s) * D + c] = t;
-        }
+    for (int e = 0; e < 8; ++e) sum[threadIdx.x / LPR][8 * l + e] = dw[e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += 256) {
+        float t = 0.f;
+        for (int k = 0; k < RPB; ++k) t += sum[k][c];
+        a.partial[((size_t)s * a.blocks[0] * D) + (size_t)c * blocks + block] = t;
     }
 }
 
 // dw[s][c] = sum of the blocks' partial sums, in a fixed order: one warp per value.
 __global__ void __launch_bounds__(256)
-rope_weight_sum_kernel(const float *__restrict__ partial, int blocks, int d, float *__restrict__ dwq, float *__restrict__ dwk) {
+rope_weight_sum_kernel(const float *__restrict__ partial, int blocks_q, int blocks_k, int d, float *__restrict__ dwq,
+                       float *__restrict__ dwk) {
     const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // of 2 d
     if (c >= 2 * d) return;
+    const bool k = c >= d;
+    const int blocks = k ? blocks_k : blocks_q;
+    const float *p = partial + (k ? (size_t)blocks_q * d + (size_t)(c - d) * blocks : (size_t)c * blocks);
     float t = 0.f;
-    for (int b = lane; b < blocks; b += 32) t += partial[(size_t)b * 2 * d + c];
+    for (int b = lane; b < blocks; b += 32) t += p[b];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    float *dst = c < d ? dwq : dwk;
-    if (lane == 0 && dst) dst[c < d ? c : c - d] = t;
+    float *dst = k ? dwk : dwq;
+    if (lane == 0 && dst) dst[k ? c - d : c] = t;
 }
 
-constexpr int kGradBlocks = 608;   // four per SM
+constexpr int kGradBlocks = 456;   // three per SM, of q and k together
 
 template <int D, typename T>
 int launch_fwd(const RopeArgs &a, int norm, bool half, cudaStream_t s) {
@@ -304,12 +317,13 @@ int launch_fwd(const RopeArgs &a, int norm, bool half, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 template <int D, typename T>
-int launch_bwd(const RopeArgs &a, int norm, bool half, int blocks, float *dwq, float *dwk, cudaStream_t s) {
+int launch_bwd(const RopeArgs &a, int norm, bool half, float *dwq, float *dwk, cudaStream_t s) {
+    const int blocks = a.blocks[0] + a.blocks[1];
     if (half) qk_rope_bwd_kernel<D, true, T><<<blocks, 256, 0, s>>>(a, norm);
     else qk_rope_bwd_kernel<D, false, T><<<blocks, 256, 0, s>>>(a, norm);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     if (!a.partial) return kOk;
-    rope_weight_sum_kernel<<<(2 * D + 7) / 8, 256, 0, s>>>(a.partial, blocks, D, dwq, dwk);
+    rope_weight_sum_kernel<<<(2 * D + 7) / 8, 256, 0, s>>>(a.partial, a.blocks[0], a.blocks[1], D, dwq, dwk);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
@@ -359,9 +373,20 @@ RopeArgs common_args(const dr_qk_norm_rope_desc &d, const void *q, const void *k
     return a;
 }
 
-int grad_blocks(const dr_qk_norm_rope_desc &d) {
-    const int64_t rpb = 256 / (d.d / 8), need = (d.n_tok * head_groups(d) + rpb - 1) / rpb;
-    return (int)(need < kGradBlocks ? (need < 1 ? 1 : need) : kGradBlocks);
+// Blocks of q and of k: shares of kGradBlocks by their heads, no more than there are units of work.
+void grad_blocks(const dr_qk_norm_rope_desc &d, int (&blocks)[2]) {
+    const int64_t rpb = 256 / (d.d / 8), heads[2] = {d.Hq, d.Hk}, split = head_groups(d);
+    for (int s = 0; s < 2; ++s) {
+        const int64_t groups = split < heads[s] ? split : heads[s], need = (d.n_tok * groups + rpb - 1) / rpb;
+        int64_t share = kGradBlocks * heads[s] / (d.Hq + d.Hk);
+        if (share < 1) share = 1;
+        blocks[s] = heads[s] == 0 ? 0 : (int)(need < 1 ? 1 : need < share ? need : share);
+    }
+}
+size_t partial_bytes(const dr_qk_norm_rope_desc &d) {
+    int b[2];
+    grad_blocks(d, b);
+    return sizeof(float) * (size_t)d.d * (b[0] + b[1]);
 }
 
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -448,7 +473,7 @@ extern "C" int dr_qk_norm_rope_bwd_workspace_bytes(const dr_qk_norm_rope_desc *d
     if (!bytes) return kErrInvalid;
     const int rc = check_desc(desc);
     if (rc != kOk) return rc;
-    *bytes = desc->norm == DR_NORM_NONE ? 0 : sizeof(float) * 2 * (size_t)desc->d * grad_blocks(*desc);
+    *bytes = desc->norm == DR_NORM_NONE ? 0 : partial_bytes(*desc);
     return kOk;
 }
 
@@ -482,18 +507,18 @@ extern "C" int dr_qk_norm_rope_bwd(const dr_qk_norm_rope_desc *desc, const void 
             if (meet(y, {a.dy[i], wide[i], wide[i]}, d.n_tok, e)) return kErrInvalid;
         }
     const bool weights = dwq || dwk;
-    const int blocks = grad_blocks(d);
-    if (weights && (!workspace || workspace_bytes < sizeof(float) * 2 * (size_t)d.d * blocks)) return kErrWorkspace;
+    grad_blocks(d, a.blocks);
+    if (weights && (!workspace || workspace_bytes < partial_bytes(d))) return kErrWorkspace;
     if (d.n_tok == 0 && !weights) return kOk;
     a.partial = weights ? (float *)workspace : nullptr;
     const bool half = d.layout == DR_ROPE_HALF;
     cudaStream_t s = (cudaStream_t)stream;
     using bf = __nv_bfloat16;
     if (d.dtype == DR_BF16)
-        return d.d == 64    ? launch_bwd<64, bf>(a, d.norm, half, blocks, dwq, dwk, s)
-               : d.d == 128 ? launch_bwd<128, bf>(a, d.norm, half, blocks, dwq, dwk, s)
-                            : launch_bwd<256, bf>(a, d.norm, half, blocks, dwq, dwk, s);
-    return d.d == 64    ? launch_bwd<64, float>(a, d.norm, half, blocks, dwq, dwk, s)
-           : d.d == 128 ? launch_bwd<128, float>(a, d.norm, half, blocks, dwq, dwk, s)
-                        : launch_bwd<256, float>(a, d.norm, half, blocks, dwq, dwk, s);
+        return d.d == 64    ? launch_bwd<64, bf>(a, d.norm, half, dwq, dwk, s)
+               : d.d == 128 ? launch_bwd<128, bf>(a, d.norm, half, dwq, dwk, s)
+                            : launch_bwd<256, bf>(a, d.norm, half, dwq, dwk, s);
+    return d.d == 64    ? launch_bwd<64, float>(a, d.norm, half, dwq, dwk, s)
+           : d.d == 128 ? launch_bwd<128, float>(a, d.norm, half, dwq, dwk, s)
+                        : launch_bwd<256, float>(a, d.norm, half, dwq, dwk, s);
 }
