@@ -19,15 +19,16 @@ using umma::mul2;
 // fma.rn.f32x2, and a column's read-out is a register sum and two shuffles.  Per token and
 // element: one multiply (decay), two fused multiply-adds.  Bound by the packed FP32 rate,
 // 3 dk dv / 2 instructions a head-token.
-constexpr int kTile = 16;   // tokens staged in shared memory at a time; divides kAnchor
+// Rows come by asynchronous copies, a tile ahead.
+constexpr int kTile = 8, kGroup = 4;   // tokens staged in shared memory, summed at a time; kTile divides kAnchor
 
 template <int DK, int DV, bool REV, bool DOT, typename Tin, typename Tout>
 __global__ void __launch_bounds__(128)
 linrec_token_kernel(const LinrecPass p) {
     constexpr int M = DK / 16, PARTS = DV / kSimtCols;
-    __shared__ __align__(16) float sQ[kTile][DK], sK[kTile][DK], sV[kTile][kSimtCols], sO[kTile][kSimtCols];
-    __shared__ __align__(16) float sY[DOT ? kTile : 1][kSimtCols];
-    __shared__ float sA[kTile], sDot[4][kTile], sRed[4];
+    __shared__ __align__(16) Tin sQ_[2][kTile][DK], sK_[2][kTile][DK], sV_[2][kTile][kSimtCols], sY_[2][DOT ? kTile : 1][kSimtCols];
+    __shared__ __align__(16) float sO[kTile][kSimtCols];
+    __shared__ float sA_[2][kTile], sDot[4][kTile], sRed[4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rg = lane >> 3;
     const int part = blockIdx.x % PARTS, c0 = part * kSimtCols;
     const int64_t chain = blockIdx.x / PARTS, n = chain / p.H;
@@ -84,71 +85,112 @@ linrec_token_kernel(const LinrecPass p) {
         __syncthreads();
     };
 
-    for (int64_t it = 0; it < tiles; ++it) {
-        const int64_t tile = REV ? tiles - 1 - it : it, base = lo + tile * kTile;
-        const int cnt = (int)min((int64_t)kTile, hi - base);
-        __syncthreads();
-        for (int i = tid; i < cnt * (DK / 4); i += 128) {
-            const int r = i / (DK / 4), c = 4 * (i % (DK / 4));
-            const size_t g = ((size_t)(base + r) * H + h) * DK + c;
-            *reinterpret_cast<float4 *>(&sQ[r][c]) = load4(q + g);
-            *reinterpret_cast<float4 *>(&sK[r][c]) = load4(k + g);
-        }
-        for (int i = tid; i < cnt * (kSimtCols / 4); i += 128) {
-            const int r = i / (kSimtCols / 4), c = 4 * (i % (kSimtCols / 4));
-            const size_t g = ((size_t)(base + r) * H + h) * DV + c0 + c;
-            *reinterpret_cast<float4 *>(&sV[r][c]) = load4(v + g);
-            if (DOT) *reinterpret_cast<float4 *>(&sY[r][c]) = load4(y + g);
-        }
-        if (tid < cnt) {   // the decay in front of each token; backwards that of the next token
+    float la = 0.f;   // this thread's token's log decay of the tile that was issued last
+    auto tile_of = [&](int64_t it) { return REV ? tiles - 1 - it : it; };
+    auto issue = [&](int64_t it) {
+        if (it < tiles) {
+            constexpr int E = 16 / sizeof(Tin);   // elements of a 16-byte copy
+            const int64_t base = lo + tile_of(it) * kTile;
+            const int cnt = (int)min((int64_t)kTile, hi - base), b = (int)(it & 1);
+            for (int i = tid; i < cnt * (DK / E); i += 128) {
+                const int r = i / (DK / E), c = E * (i % (DK / E));
+                const size_t g = ((size_t)(base + r) * H + h) * DK + c;
+                umma::cp_async16(&sQ_[b][r][c], q + g);
+                umma::cp_async16(&sK_[b][r][c], k + g);
+            }
+            for (int i = tid; i < cnt * (kSimtCols / E); i += 128) {
+                const int r = i / (kSimtCols / E), c = E * (i % (kSimtCols / E));
+                const size_t g = ((size_t)(base + r) * H + h) * DV + c0 + c;
+                umma::cp_async16(&sV_[b][r][c], v + g);
+                if (DOT) umma::cp_async16(&sY_[b][r][c], y + g);
+            }
+            // the decay in front of each token; backwards that of the next token
             const int64_t t = base + tid + (REV ? 1 : 0);
-            sA[tid] = p.la && t < hi ? expf(p.la[t * H + h]) : 1.f;
+            la = p.la && tid < cnt && t < hi ? p.la[t * H + h] : 0.f;
         }
+        umma::cp_async_commit();   // (empty behind the last tile)
+    };
+    issue(0);
+    for (int64_t it = 0; it < tiles; ++it) {
+        const int64_t tile = tile_of(it), base = lo + tile * kTile;
+        const int cnt = (int)min((int64_t)kTile, hi - base);
+        const auto &sQ = sQ_[it & 1];
+        const auto &sK = sK_[it & 1];
+        const auto &sV = sV_[it & 1];
+        const auto &sY = sY_[it & 1];
+        float *sA = sA_[it & 1];
+        if (tid < cnt) sA[tid] = p.la ? expf(la) : 1.f;
+        issue(it + 1);   // the other buffer's readers have passed the barrier behind their tile
+        umma::cp_async_wait_group1();
         __syncthreads();
         if (DOT && REV && (tile + 1) * kTile % kAnchor == 0 || DOT && REV && it == 0)
             inner_product(((tile + 1) * kTile - 1) / kAnchor, sA[cnt - 1]);
-        for (int x = 0; x < cnt; ++x) {
-            const int t = REV ? cnt - 1 - x : x;
-            const float2 a2 = make_float2(sA[t], sA[t]);
-            const float2 vv = *reinterpret_cast<const float2 *>(&sV[t][wc]);
-            const float2 v2[2] = {make_float2(vv.x, vv.x), make_float2(vv.y, vv.y)};
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, qk = make_float2(0.f, 0.f);
+        // kGroup tokens' read-outs are summed over the lanes together: the shuffles' latency is paid
+        // once (rows behind the tile's end take no part; the condition is the block's)
+        for (int x0 = 0; x0 < cnt; x0 += kGroup) {
+            float o[kGroup][2], w[kGroup];
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sK[t][16 * m + 4 * rg]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&sQ[t][16 * m + 4 * rg]);
-                const float2 kk[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
-                const float2 qq[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
+            for (int g = 0; g < kGroup; ++g) {
+                o[g][0] = o[g][1] = w[g] = 0.f;
+                if (x0 + g >= cnt) continue;
+                const int t = REV ? cnt - 1 - (x0 + g) : x0 + g;
+                const float2 a2 = make_float2(sA[t], sA[t]);
+                const float v0 = to_f32(sV[t][wc]), v1 = to_f32(sV[t][wc + 1]);
+                const float2 v2[2] = {make_float2(v0, v0), make_float2(v1, v1)};
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, qk = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int m = 0; m < M; ++m) {
+                    const float4 k4 = load4(&sK[t][16 * m + 4 * rg]), q4 = load4(&sQ[t][16 * m + 4 * rg]);
+                    const float2 kk[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+                    const float2 qq[2] = {make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)};
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float2 &s = S[c][2 * m + e];
-                        s = mul2(a2, s);
-                        if (DOT) acc[c] = fma2(qq[e], s, acc[c]);
-                        s = fma2(kk[e], v2[c], s);
-                        if (!DOT) acc[c] = fma2(qq[e], s, acc[c]);
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float2 &s = S[c][2 * m + e];
+                            s = mul2(a2, s);
+                            if (DOT) acc[c] = fma2(qq[e], s, acc[c]);
+                            s = fma2(kk[e], v2[c], s);
+                            if (!DOT) acc[c] = fma2(qq[e], s, acc[c]);
+                        }
+                        if (DOT) qk = fma2(qq[e], kk[e], qk);
                     }
-                    if (DOT) qk = fma2(qq[e], kk[e], qk);
+                }
+                o[g][0] = acc[0].x + acc[0].y;
+                o[g][1] = acc[1].x + acc[1].y;
+                w[g] = qk.x + qk.y;
+            }
+#pragma unroll
+            for (int off = 8; off < 32; off <<= 1) {
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    o[g][0] += __shfl_xor_sync(0xffffffffu, o[g][0], off);
+                    o[g][1] += __shfl_xor_sync(0xffffffffu, o[g][1], off);
+                    if (DOT) w[g] += __shfl_xor_sync(0xffffffffu, w[g], off);
                 }
             }
-            float o0 = acc[0].x + acc[0].y, o1 = acc[1].x + acc[1].y, w = qk.x + qk.y;
-#pragma unroll
-            for (int o = 8; o < 32; o <<= 1) {
-                o0 += __shfl_xor_sync(0xffffffffu, o0, o);
-                o1 += __shfl_xor_sync(0xffffffffu, o1, o);
-                if (DOT) w += __shfl_xor_sync(0xffffffffu, w, o);
-            }
             if (DOT) {   // the other tokens' part of out . y, then the token's own term of out
-                const float2 yy = *reinterpret_cast<const float2 *>(&sY[t][wc]);
-                float x2 = fmaf(o0, yy.x, o1 * yy.y);
+                float d[kGroup];
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) x2 += __shfl_xor_sync(0xffffffffu, x2, o);
-                if (lane == 0) sDot[warp][t] = x2;
-                o0 = fmaf(w, vv.x, o0);
-                o1 = fmaf(w, vv.y, o1);
+                for (int g = 0; g < kGroup; ++g) {
+                    const int t = x0 + g < cnt ? (REV ? cnt - 1 - (x0 + g) : x0 + g) : 0;
+                    d[g] = fmaf(o[g][0], to_f32(sY[t][wc]), o[g][1] * to_f32(sY[t][wc + 1]));
+                    o[g][0] = fmaf(w[g], to_f32(sV[t][wc]), o[g][0]);
+                    o[g][1] = fmaf(w[g], to_f32(sV[t][wc + 1]), o[g][1]);
+                }
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) {
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g) d[g] += __shfl_xor_sync(0xffffffffu, d[g], off);
+                }
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g)
+                    if (lane == 0 && x0 + g < cnt) sDot[warp][REV ? cnt - 1 - (x0 + g) : x0 + g] = d[g];
             }
-            if (rg == 0) *reinterpret_cast<float2 *>(&sO[t][wc]) = make_float2(o0, o1);
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g)
+                if (rg == 0 && x0 + g < cnt)
+                    *reinterpret_cast<float2 *>(&sO[REV ? cnt - 1 - (x0 + g) : x0 + g][wc]) = make_float2(o[g][0], o[g][1]);
         }
         __syncthreads();
         for (int i = tid; i < cnt * (kSimtCols / 4); i += 128) {

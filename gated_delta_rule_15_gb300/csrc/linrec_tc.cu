@@ -95,7 +95,12 @@ int64_t segment_slots(const LinrecSeqs &s, int64_t seg) { return s.total / seg +
 }  // namespace
 
 bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_bf16) {
-    return in_bf16 && out_bf16 && s.total > 0 && s.total < ((int64_t)1 << 31) - 64 &&
+    // Up to 16 tokens the token recurrence is faster (forward / backward, us: one chain of 64 x 64, T 16,
+    // 5.2 / 19.9 against 6.7 / 24.2; 1024 chains of 128 x 128, 53.6 / 179 against 63.0 / 230), from 32
+    // on the chunks are, but for many short chains of 64 x 64 (one chain, T 32, 8.5 / 32.3 against 6.7 /
+    // 24.2; 1024 chains of 128 x 128, 95.6 / 325 against 62.9 / 232).  Packed sequences go by all
+    // their rows, which may be one sequence's.
+    return in_bf16 && out_bf16 && (s.cu ? s.total : s.T) > 16 && s.total < ((int64_t)1 << 31) - 64 &&
            segment_slots(s, segment_tokens(s, H)) * H < ((int64_t)1 << 31);
 }
 

@@ -458,17 +458,37 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, init_state=None, *, chunk: int = 64
 
 
 # ------------------------------------------------------------ additive gated recurrence
+# These calls also serve single tokens, where the host's time counts: addresses go to ctypes as
+# integers, shapes are compared as they are.
 def _on_one_device(*ts):
     """Contiguous tensors of the current device, or ValueError."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None and (not t.is_cuda or t.get_device() != dev or not t.is_contiguous()):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on the current CUDA device")
+
+
+_NO_SCOPE = contextlib.nullcontext()
 
 
 def _stream_scope(stream):
     """Buffers allocated for a call belong to the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NO_SCOPE if stream is None else torch.cuda.stream(stream)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _current_raw_stream(torch.cuda.current_device())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bytes(t):
@@ -476,7 +496,7 @@ def _bytes(t):
 
 
 def _like(t, shape, dtype, what):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
         raise ValueError(f"{what} must be {dtype} {list(shape)}")
 
 
@@ -538,9 +558,9 @@ def linrec_fwd(q, k, v, log_alpha=None, init_state=None, *, cu_seqlens=None, out
             final_state = torch.empty(states, dtype=torch.float32, device=q.device)
         workspace = _workspace(_lib.dr_linrec_fwd_workspace_bytes, desc, workspace, q.device,
                                "dr_linrec_fwd_workspace_bytes")
-        rc = _lib.dr_linrec_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
-                                _ptr(cu_seqlens), _ptr(init_state), _ptr(out), _ptr(final_state),
-                                _ptr(workspace), _bytes(workspace), _stream_handle(stream))
+        rc = _lib.dr_linrec_fwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(log_alpha),
+                                _at(cu_seqlens), _at(init_state), _at(out), _at(final_state),
+                                _at(workspace), _bytes(workspace), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_linrec_fwd")
     return out, final_state
@@ -574,11 +594,11 @@ def linrec_bwd(q, k, v, log_alpha, init_state, d_out, d_final_state=None, *, cu_
         dinit = torch.empty(states, dtype=torch.float32, device=q.device) if return_d_init else None
         workspace = _workspace(_lib.dr_linrec_bwd_workspace_bytes, desc, workspace, q.device,
                                "dr_linrec_bwd_workspace_bytes")
-        rc = _lib.dr_linrec_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
-                                _ptr(cu_seqlens), _ptr(init_state), _ptr(d_out),
-                                _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dla),
-                                _ptr(dinit), _ptr(workspace), _bytes(workspace),
-                                _stream_handle(stream))
+        rc = _lib.dr_linrec_bwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(log_alpha),
+                                _at(cu_seqlens), _at(init_state), _at(d_out),
+                                _at(d_final_state), _at(dq), _at(dk), _at(dv), _at(dla),
+                                _at(dinit), _at(workspace), _bytes(workspace),
+                                _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_linrec_bwd")
     return dq, dk, dv, dla, dinit
@@ -606,8 +626,8 @@ def linrec_step(q, k, v, log_alpha, state, *, out=None, out_dtype=None, stream=N
     if out is None:
         with _stream_scope(stream):
             out = torch.empty((B, H, dv), dtype=odt, device=q.device)
-    rc = _lib.dr_linrec_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
-                             _ptr(state), _ptr(out), _stream_handle(stream))
+    rc = _lib.dr_linrec_step(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(log_alpha),
+                             _at(state), _at(out), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_linrec_step")
     return out
@@ -631,8 +651,7 @@ def rope_table(rot: int, *, base: float = 10000.0, scaling=None, device="cuda"):
         raise ValueError(f"scaling {scaling!r}: kind linear (factor) or by_parts (factor, original, low, high)")
     t = torch.empty(max(rot, 0) // 2, dtype=torch.int64)
     rc = _lib.dr_rope_table(rot, base, kinds[kind][0], *(float(sc.get(n, 0.0)) for n in
-                            ("factor", "original", "low", "high")), _ptr(t) if t.numel() else
-                            ctypes.c_void_p(8))
+                            ("factor", "original", "low", "high")), t.data_ptr() if t.numel() else 8)
     if rc != DR_OK:
         raise DrError(rc, "dr_rope_table")
     return t.to(device)
@@ -660,7 +679,7 @@ def _rows_into(given, x, what):
         return None, 0
     if given is None:
         return torch.empty(x.shape, dtype=x.dtype, device=x.device), 0
-    if not given.is_cuda or given.get_device() != x.get_device() or given.dtype != x.dtype \
+    if given.get_device() != x.get_device() or given.dtype != x.dtype \
             or given.shape != x.shape:
         raise ValueError(f"{what} must have its input's shape, dtype and device")
     return given, _rows_of(given, what)[3]
@@ -669,7 +688,7 @@ def _rows_into(given, x, what):
 def _qk_desc(q, k, table, positions, offset, norm, wq, wk, eps, layout, rot_scale):
     dev = torch.cuda.current_device()
     for t in (q, k):
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError("q and k must be on the current CUDA device")
     _on_one_device(table, positions, wq, wk)
     if q.dtype not in _DT or (k is not None and k.dtype != q.dtype):
@@ -707,8 +726,8 @@ def qk_norm_rope(q, k, table, *, positions=None, offset: int = 0, norm="rms", wq
     with _stream_scope(stream):
         q_out, desc.q_out_stride = _rows_into(q_out, q, "q_out")
         k_out, desc.k_out_stride = _rows_into(k_out, k, "k_out")
-    rc = _lib.dr_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(table),
-                              _ptr(positions), _ptr(q_out), _ptr(k_out), _stream_handle(stream))
+    rc = _lib.dr_qk_norm_rope(ctypes.byref(desc), _at(q), _at(k), _at(wq), _at(wk), _at(table),
+                              _at(positions), _at(q_out), _at(k_out), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_qk_norm_rope")
     return q_out, k_out
@@ -735,10 +754,10 @@ def qk_norm_rope_bwd(q, k, table, dq_out, dk_out, *, positions=None, offset: int
         if dwq is not None or dwk is not None:
             workspace = _workspace(_lib.dr_qk_norm_rope_bwd_workspace_bytes, desc, workspace, q.device,
                                    "dr_qk_norm_rope_bwd_workspace_bytes")
-        rc = _lib.dr_qk_norm_rope_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk),
-                                      _ptr(table), _ptr(positions), _ptr(dq_out), _ptr(dk_out),
-                                      _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace),
-                                      _bytes(workspace), _stream_handle(stream))
+        rc = _lib.dr_qk_norm_rope_bwd(ctypes.byref(desc), _at(q), _at(k), _at(wq), _at(wk),
+                                      _at(table), _at(positions), _at(dq_out), _at(dk_out),
+                                      _at(dq), _at(dk), _at(dwq), _at(dwk), _at(workspace),
+                                      _bytes(workspace), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
