@@ -28,9 +28,10 @@ bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t H, int64_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The segments' start states from their sums: per chain, in the order of the pass,
-// start(next) = 2^decay start + sum.  The first segment starts from `init`, which its block
-// reads itself.  One thread per four state entries; in place.
+// The segments' start states from their sums: per chain, in the order of the pass, start(0) = init,
+// start(next) = 2^decay start + sum, over the sums (init may be the final state's buffer, which
+// another block than the first segment's writes).  One thread per four state entries, the
+// sums kAhead segments ahead of their use; a sequence of one segment is left alone.
 __global__ void __launch_bounds__(256)
 linrec_chain_kernel(const LinrecSeqs seqs, int H, int quads, bool rev, int64_t seg, const float *__restrict__ init,
                     float *__restrict__ state, const float *__restrict__ decay) {
@@ -43,16 +44,24 @@ linrec_chain_kernel(const LinrecSeqs seqs, int H, int quads, bool rev, int64_t s
     float4 s = init ? reinterpret_cast<const float4 *>(init)[chain * quads + e] : make_float4(0.f, 0.f, 0.f, 0.f);
     auto at = [&](int64_t i) { return (base + (rev ? segs - 1 - i : i)) * H + h; };
     float4 *st = reinterpret_cast<float4 *>(state);
-    float4 x = st[at(0) * quads + e];
-    float g = decay[at(0)];
-    for (int64_t i = 1; i < segs; ++i) {
-        const float4 x1 = i + 1 < segs ? st[at(i) * quads + e] : x;   // the next sum, ahead of the store over it
-        const float g1 = i + 1 < segs ? decay[at(i)] : 0.f, f = linrec::ex2(g);
-        s.x = fmaf(f, s.x, x.x); s.y = fmaf(f, s.y, x.y);
-        s.z = fmaf(f, s.z, x.z); s.w = fmaf(f, s.w, x.w);
-        st[at(i) * quads + e] = s;
-        x = x1;
-        g = g1;
+    constexpr int kAhead = 8;
+    for (int64_t i0 = 0; i0 < segs; i0 += kAhead) {
+        float4 x[kAhead];
+        float g[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {   // (the last segment has no sum)
+            const bool has = i0 + k + 1 < segs;
+            x[k] = has ? st[at(i0 + k) * quads + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            g[k] = has ? decay[at(i0 + k)] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i0 + k >= segs) break;
+            st[at(i0 + k) * quads + e] = s;
+            const float f = linrec::ex2(g[k]);
+            s.x = fmaf(f, s.x, x[k].x); s.y = fmaf(f, s.y, x[k].y);
+            s.z = fmaf(f, s.z, x[k].z); s.w = fmaf(f, s.w, x[k].w);
+        }
     }
 }
 

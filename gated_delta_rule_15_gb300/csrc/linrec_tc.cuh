@@ -209,7 +209,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     seq_range(p.seqs, n, lo, hi);
     const bool rev = p.rev, outputs = !a.sums;
     const int64_t segs = hi > lo ? (hi - lo + a.seg - 1) / a.seg : 1;
-    const bool last_run = rev ? j == 0 : j == segs - 1, first_run = rev ? j == segs - 1 : j == 0;
+    const bool last_run = rev ? j == 0 : j == segs - 1;
     if (a.sums && last_run) return;            // nobody needs its sum
     const int64_t s_lo = lo + j * a.seg, s_hi = min(hi, s_lo + a.seg);
     const int rows = (int)(s_hi - s_lo), chunks = (rows + kChunk - 1) / kChunk;
@@ -378,7 +378,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         auto at = [&](int i) { return p.state_t ? (size_t)row * DK + i0 + i : (size_t)(i0 + i) * DV + row; };
         float2 S[NV / 2];
         const float *init = a.sums ? nullptr
-                            : first_run ? (p.init ? p.init + (size_t)(n * H + h) * (DK * DV) : nullptr)
+                            : segs == 1 ? (p.init ? p.init + (size_t)(n * H + h) * (DK * DV) : nullptr)
                                         : a.seg_state + (size_t)(slot * H + h) * (DK * DV);
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i)

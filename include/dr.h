@@ -315,6 +315,7 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *     0 .. T (values outside are clamped; the sequences must not share rows); a sequence may
  *     be empty: its state passes through.  Rows of no sequence are neither read for
  *     another row's sake nor written.  States are [N, H, dk, dv] (N = B if not packed).
+ *   - The first call on a device looks up device addresses: make it before a stream capture.
  *   - log_alpha and d_log_alpha need 4-byte, cu_seqlens 8-byte alignment.
  *   - log_alpha = -inf is a full reset (alpha = 0).  Inputs of the sequences' rows are
  *     otherwise finite; values in rows of no sequence do not matter.

@@ -345,6 +345,36 @@ def test_state_carried_in_place_and_mixed_output(dr):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,T,H,cu", [("bf16", 9000, 2, None), ("bf16", 9000, 2, [0, 100, 6000, 9000]), ("f32", 300, 2, None)])
+def test_states_updated_in_place(dr, dtype, T, H, cu):
+    """final_state over init_state, d_init_state over d_final_state (long sequences run in segments
+    whose first and last blocks touch the same state)."""
+    import ctypes
+    N = len(cu) - 1 if cu else 1
+    c = cuda(inputs(1, T, H, 128, 128, dtype, N=N if cu else 0, strength=1e-3, seed=7))
+    cuc = None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda()
+    args = [c[n] for n in ("q", "k", "v", "la")]
+    want_o, want_f = dr.linrec_fwd(*args, c["s0"], cu_seqlens=cuc)
+    want_g = dr.linrec_bwd(*args, c["s0"], c["do"], c["ds"], cu_seqlens=cuc)
+    for _ in range(3):
+        s = c["s0"].clone()
+        o, f = dr.linrec_fwd(*args, s, cu_seqlens=cuc, final_state=s)
+        assert torch.equal(o, want_o) and torch.equal(s, want_f)
+        d = c["ds"].clone()
+        dt = dr._DT[c["q"].dtype]
+        desc = dr.LinrecDesc(1, T, H, 128, 128, N if cu else 0, dt, dt, 1, 0)
+        n = ctypes.c_size_t(0)
+        assert dr.lib().dr_linrec_bwd_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)) == 0
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        g = [torch.empty_like(x) for x in args]
+        p = lambda t: None if t is None else t.data_ptr()
+        rc = dr.lib().dr_linrec_bwd(ctypes.byref(desc), *map(p, args), p(cuc), p(c["s0"]), p(c["do"]), p(d), *map(p, g),
+                                    p(d), p(ws), n.value, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert all(torch.equal(a, b) for a, b in zip((*g, d), want_g))
+
+
+@pytest.mark.gpu
 def test_no_tokens(dr):
     """T = 0: the state and its gradient pass through."""
     s = torch.randn(2, 3, 64, 64).cuda()
@@ -354,6 +384,10 @@ def test_no_tokens(dr):
     assert o.shape == (2, 0, 3, 64) and torch.equal(f, s)
     g = dr.linrec_bwd(e, e, e, la, s, e, s)
     assert torch.equal(g[4], s)
+    e, la, cu = e[:1], la[:1], torch.zeros(3, dtype=torch.int64).cuda()     # two empty packed sequences
+    for dtype in (torch.float32, torch.bfloat16):
+        o, f = dr.linrec_fwd(e.to(dtype), e.to(dtype), e.to(dtype), la, s, cu_seqlens=cu)
+        assert torch.equal(f, s)
 
 
 @pytest.mark.gpu
