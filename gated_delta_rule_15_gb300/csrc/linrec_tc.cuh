@@ -162,11 +162,9 @@ struct Layout {
     // Otherwise: X, R + O of two chunks, D, the state operand, three terms of Vt.
     static constexpr int NU = DOT ? 2 : 1, NR = DOT ? 1 : 2;
     static constexpr uint32_t TM_X2 = 128, TM_R = DOT ? 192 : 64, TM_D = DOT ? 256 : 192;
-    static constexpr int ND = DOT && DK == 128 ? 2 : 1;      // D comes in this many parts, one at a time
-    static constexpr int DW = DK / ND;
     static constexpr int HALVES = DOT ? 1 : 2;               // Kt (Vt) is handed over in this many parts
-    static constexpr uint32_t TM_S = 320, TM_V = 384;        // terms of DK / 2, of 32 columns
-    static_assert(TM_D + DW <= TM_S && (DOT ? TM_S + 3 * DK / 2 <= 512 : TM_S + DK / 2 <= TM_V), "tensor memory");
+    static constexpr uint32_t TM_S = DOT ? 384 : 320, TM_V = 384;   // terms of DK / 2, of 32 columns
+    static_assert(TM_D + DK <= TM_S && (DOT ? TM_S + DK <= 512 : TM_S + DK / 2 <= TM_V), "tensor memory");
 };
 
 // The rest of a wait that was not over at once; its budget and the other warps' expiries are
@@ -199,7 +197,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap ty,
                     const __grid_constant__ CUtensorMap to, const TcArgs a) {
     using L = Layout<DK, DV, DOT>;
-    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 3 : 1, NU = L::NU, NR = L::NR, ND = L::ND;
+    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 2 : 1, NU = L::NU, NR = L::NR;
     constexpr int kStages = L::STAGES;
     const LinrecPass &p = a.p;
     const int H = p.H, h = (int)(blockIdx.x % H);
@@ -223,9 +221,9 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint64_t *b_x = bars + 14;         // [NU] X (and X2) of a chunk is there
     uint64_t *b_kt = bars + 17;        // [HALVES] Kt (rows 0..31, 32..63) is built
     uint64_t *b_p = bars + 19;         // [2] P is built, X and X2 are read
-    uint64_t *b_d = bars + 21;         // [ND] D is there
+    uint64_t *b_d = bars + 21;         // D is there
     uint64_t *b_d1 = bars + 23;        // D has taken Kt's first half
-    uint64_t *b_dread = bars + 24;     // [ND] D is read
+    uint64_t *b_dread = bars + 24;     // D is read
     uint64_t *b_s = bars + 26;         // the state operand is there
     uint64_t *b_r = bars + 27;         // R is there: the state operand may be replaced
     uint64_t *b_o = bars + 28;         // [2] R and O are there
@@ -255,10 +253,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int i = 0; i < L::HALVES; ++i) mbar_init(b_kt + i, kBuildWarps);
         mbar_init(b_d1, 1);
         for (int i = 0; i < 2; ++i) mbar_init(b_p + i, 4);
-        for (int i = 0; i < ND; ++i) {
-            mbar_init(b_d + i, 1);
-            mbar_init(b_dread + i, kStateWarps / ND);
-        }
+        mbar_init(b_d, 1);
+        mbar_init(b_dread, kStateWarps);
         mbar_init(b_s, kStateWarps);
         mbar_init(b_r, 1);
         for (int i = 0; i < 2; ++i) mbar_init(b_o + i, 1);
@@ -393,12 +389,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                         float2 x = S[4 * b + i];
                         // (opaque, so that no term is computed ahead and kept: 550 bytes of spills)
                         if (NS > 1) asm volatile("" : "+f"(x.x), "+f"(x.y));
-                        if (NS == 1) {
-                            w[0][i] = pack_bf16(x.x, x.y);   // to the nearest
-                        } else {
-                            w[0][i] = take_bf16(x);
-                            w[NS > 1 ? 1 : 0][i] = take_bf16(x);
-                            w[NS - 1][i] = last_bf16(x);
+                        w[0][i] = pack_bf16(x.x, x.y);   // to the nearest
+                        if (NS > 1) {
+                            x = fma2(make_float2(lo_bf16(w[0][i]), hi_bf16(w[0][i])), make_float2(-1.f, -1.f), x);
+                            w[NS - 1][i] = pack_bf16(x.x, x.y);
                         }
                     }
 #pragma unroll
@@ -457,13 +451,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 }
                 named_sync(2, 32 * kStateWarps);
             }
-            const int d = ND == 2 ? half : 0;
-            wait(b_d + d, it);
+            wait(b_d, it);
             if (mine) {
 #pragma unroll
                 for (int b = 0; b < NV / 16; ++b) {
                     float v[16];
-                    tmem_ld16(tl + L::TM_D + (ND == 2 ? 0 : i0) + 16 * b, v);
+                    tmem_ld16(tl + L::TM_D + i0 + 16 * b, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -473,7 +466,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(b_dread + d);
+                mbar_arrive(b_dread);
                 mbar_arrive(b_gfree + it % L::GATES);
             }
             if (!rev && at_anchor(it) && mine) {
@@ -509,7 +502,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             wait(b_gate + it % L::GATES, it / L::GATES);
             wait(b_load + s, it / kStages);
             if (DOT) wait(b_x + it % NU, it / NU);      // K's place may be written
-            if (it > 0) wait(L::HALVES == 2 ? b_d1 : b_d + ND - 1, it - 1);   // Kt's other terms, Vt's first half are read
+            if (it > 0) wait(L::HALVES == 2 ? b_d1 : b_d, it - 1);   // Kt's other terms, Vt's first half are read
             if (cnt < kChunk) {   // rows of no token are zero values (and keys, where they are not scaled)
                 const int per = 8 * (kChunk - cnt);
                 for (int i = 32 * bw + lane; i < PV * per; i += 32 * kBuildWarps)
@@ -797,7 +790,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // ---------------------------------------------------------------- MMA issue
             if (lane == 0 && chunks > 0 && ((outputs && warp == kScoreWarp) || warp == kUpdateWarp)) {
                 constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
-                                   ID_MM = idesc_bf16(128, L::DW, DOT, true);
+                                   ID_MM = idesc_bf16(128, DK, DOT, true);
                 const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
                 const uint64_t dV = smem_desc_sw128(smem_u32(sm), L::V_STEP, 1024);   // MN-major, V panels
                 const uint64_t dT0 = smem_desc_sw128(smem_u32(sm), L::QK_STEP, 1024);      // MN-major, Kt's first term
@@ -831,7 +824,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     mma_commit(b_x + it % NU);
                     if (DOT) mma_commit(b_yfree + it % 3);
                 };
-                auto update = [&](int it, int d, int part) {   // part: of Kt's rows
+                auto update = [&](int it, int part) {   // part: of Kt's rows
                     const uint32_t st = at_stage(it);
                     constexpr int KN = 4 / L::HALVES;
 #pragma unroll 1
@@ -845,10 +838,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             continue;
                         }
                         steps(part * KN, KN, tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
-                              t == 0 ? desc_add(dT0, st + L::K0 + d * L::QK_STEP) : desc_add(dT, L::KT + ((t - 1) * PK + d) * 8192),
+                              t == 0 ? desc_add(dT0, st + L::K0) : desc_add(dT, L::KT + (t - 1) * PK * 8192),
                               2048, ID_MM, part + t > 0);
                     }
-                    mma_commit(part + 1 < L::HALVES ? b_d1 : b_d + d);
+                    mma_commit(part + 1 < L::HALVES ? b_d1 : b_d);
                 };
                 auto read_out = [&](int it) {
                     const uint32_t st = at_stage(it), r = tm + L::TM_R + 64 * ((uint32_t)it % NR);
@@ -882,21 +875,17 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     for (int it = 0; it < chunks; ++it) {
                         wait(b_load + it % kStages, it / kStages);
                         wait(b_kt, it);
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) {   // (D's halves, one at a time)
-                            const int before = d == 0 ? it - 1 : it;
-                            if (before >= 0) wait(b_dread + (ND == 2 ? d ^ 1 : 0), before);
-                            update(it, d, 0);
-                            if (L::HALVES == 2) {
-                                wait(b_kt + 1, it);
-                                update(it, d, 1);
-                            }
-                            if (outputs && d == ND - 1) {
-                                read(it - NR);
-                                if (DOT) wait(b_p + (it & 1), it >> 1);
-                                wait(b_s, it);
-                                read_out(it);
-                            }
+                        if (it > 0) wait(b_dread, it - 1);
+                        update(it, 0);
+                        if (L::HALVES == 2) {
+                            wait(b_kt + 1, it);
+                            update(it, 1);
+                        }
+                        if (outputs) {
+                            read(it - NR);
+                            if (DOT) wait(b_p + (it & 1), it >> 1);
+                            wait(b_s, it);
+                            read_out(it);
                         }
                         mma_commit(b_free + it % kStages);
                     }
