@@ -167,17 +167,17 @@ struct Layout {
     static_assert(TM_D + DK <= TM_S && (DOT ? TM_S + DK <= 512 : TM_S + DK / 2 <= TM_V), "tensor memory");
 };
 
-// The rest of a wait that was not over at once; its budget and the other warps' expiries are
-// looked at every 256 polls (few instructions at each of the many places that wait; no call: the
-// register split below rules calls out).
-__device__ __forceinline__ void wait_longer(uint64_t *bar, uint32_t parity, volatile int *aborted, int *status) {
-    const long long t0 = clock64();
+// The rest of a wait that was not over at once: at most *polls more polls (each of 60 cycles at
+// least: a thirtieth of a second in all); then *polls becomes 0 and nobody waits any more.  Few
+// instructions, for the many places that wait, and no call: the register split rules calls out.
+constexpr int kPolls = 1 << 20;
+__device__ __forceinline__ void wait_longer(uint64_t *bar, uint32_t parity, volatile int *polls) {
+    int i = 0;
 #pragma unroll 1
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 255u) == 0 && (*aborted || clock64() - t0 > tc::kWaitCycles)) {
-            *aborted = 1;
-            atomicExch(status, kErrTimeout);
-            return;
+    while (!mbar_try_wait(bar, parity)) {
+        if (++i > *polls) {
+            *polls = 0;
+            break;
         }
     }
 }
@@ -234,7 +234,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     // time before everyone who waits for it has seen the first.  Where a warp may run ahead of
     // another (X of later chunks, outputs), consecutive chunks take different barriers.
     __shared__ uint32_t tmem_s;
-    __shared__ int abort_s;
+    __shared__ int polls_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -260,7 +260,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int i = 0; i < 2; ++i) mbar_init(b_o + i, 1);
         for (int i = 0; i < 4; ++i) mbar_init(b_oread + i, kOutWarps);
         mbar_init(b_end, outputs ? 2 : 1);
-        abort_s = 0;
+        polls_s = kPolls;
         fence_mbar_init();
     }
     if (warp == kUpdateWarp) {
@@ -271,10 +271,10 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_s;
-    volatile int *aborted = &abort_s;
+    volatile int *polls = &polls_s;
     // `k`-th completion of a barrier (k = 0, 1, ..); after an expiry nobody waits any more
     auto wait = [&](uint64_t *bar, int k) {
-        if (!mbar_try_wait(bar, k & 1)) wait_longer(bar, k & 1, aborted, a.status);
+        if (!mbar_try_wait(bar, k & 1)) wait_longer(bar, k & 1, polls);
         tc_fence_after();
     };
     auto stage = [&](int it) { return sm + (it % kStages) * L::STAGE; };
@@ -701,7 +701,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (it >= kStages) wait(b_free + s, it / kStages - 1);
                 if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
                 __syncwarp();
-                if (lane == 0 && !*aborted) {
+                if (lane == 0 && *polls != 0) {
                     unsigned char *st = stage(it);
                     issued = it + 1;
                     const int row = (int)row_of(it);
@@ -899,6 +899,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && polls_s == 0) atomicExch(a.status, kErrTimeout);
     if (warp == kUpdateWarp) tmem_dealloc(tm, 512);
 }
 
