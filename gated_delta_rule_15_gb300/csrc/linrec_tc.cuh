@@ -12,42 +12,56 @@
 //     S   <- 2^c_e S + (diag(2^c) K)^T V.
 //
 // Everything is kept transposed, so that the value channels are the tensor core's 128 rows:
-//     X    = Q K^T           [64 x 64]     (rows 64..127 of the instruction's M are not used)
-//     R^T  = S^T Q^T         [dv x 64]     S^T from tensor memory
-//     O^T  = V^T P^T         [dv x 64]     V as loaded, an MN-major operand
-//     D^T  = V^T Kt          [dv x dk]
+//     X   = Q K^T           [64 x 64]     (rows 64..127 of the instruction's M are not used)
+//     R^T = S^T Q^T         [dv x 64]     S^T from tensor memory
+//     O^T = V^T P^T         [dv x 64]     V as loaded, an MN-major operand
+//     D^T = Vt^T K = V^T Kt [dv x dk]     Vt = diag(w) V, Kt = diag(w) K, w the factors above
 // The state itself stays in the registers of eight warps in fp32 (S = 2^c_e S + D by fused
 // multiply-add, so no truncation of the tensor core's accumulator builds up over a long
 // sequence); each chunk it is written to tensor memory as R's bf16 operand.
 //
-// Precision.  Products of loaded rows are exact in fp32.  Kt = diag(..) K is split into three
-// bf16 terms (24 bits, D is three products), so the state is an fp32 result.  P and the
-// state operand of R enter as one bf16 each: for the bf16 output they are rounded once
-// more than it is, each by at most half a step.  The log-decay gradient needs more (mode
-// kDot): R takes the state in three bf16 terms, and the intra-chunk part of out.y is
-// summed from the fp32 products X and X2 = Y V^T directly,
-//     out_r.y_r (without the row's own term) = 2^c_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s).
+// Two forms.  Without Y (the forward, the dv pass) the factors w go to the values: Vt^T is made
+// from transposed 8 x 8 fragments of V (ldmatrix) straight into tensor memory, K is used as
+// loaded, and with P divided by its row's factor f_r of R, O is accumulated onto R and
+//     out_r = f_r (R_r + O_r)                  (f_r = 2^max(., -60): below, R_r does not matter)
+// With Y (the dq and dk passes of a gated backward) R is needed apart from O, tensor memory is full,
+// and Kt is made in shared memory, its first term in K's place.
+//
+// Precision.  Products of loaded rows are exact in fp32.  Vt, Kt enter as three bf16 terms (all
+// 24 bits, D is three products), so the state is an fp32 result.  P and the state operand of R
+// enter as one bf16 each: for the bf16 output they are rounded once more than it is, each by at
+// most half a step (measured 2.3e-3 of the 2-norm, 1.7e-3 from the output's rounding alone).  The
+// log-decay gradient needs more: with Y, R takes the state in two bf16 terms (2^-18), and the
+// intra-chunk part of out.y is summed from the fp32 products X and X2 = Y V^T directly,
+//     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s);
+// measured 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the backward of
+// B8 T2048 H16 d128).
 // log2 decays are held as a multiple of 2^-10, whose sums over a chunk are exact in fp32, and
 // a remainder, so that a difference of prefix sums is as exact as a single decay whatever
 // lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
 // reset).
 //
-// The loop's code is kept small (rolled loops): twenty warps
-// run through different parts of it, and what does not fit the SM's instruction cache
-// comes from the cache that all SMs of a GPC share, which was the bound before (76 % of its
-// rate, 84 % hits in the SM's cache).
+// Work split: one CTA per (sequence, head, segment) walks its chunks.  Warps 0..7 hold the state;
+// warps 8..15 make Vt, or Kt and P; warps 16..23 write the outputs and, without Y, build P; warp
+// 24 issues the TMA loads and scans the gates; one thread each of warps 25 and 26 issues the MMAs
+// of X, and of D, R and O (D first: the next chunk's Vt waits for it).  Few long chains are cut
+// into segments: a first launch sums each segment's state from zero (keys and values only), a
+// small kernel chains them (the transition is the scalar 2^(sum c)), a second launch runs all
+// segments from their true start states.
 //
-// Work split: one CTA per (sequence, head, segment) walks its chunks.  Warps 0..7 hold the state,
-// warps 8..15 build P and Kt and write the outputs, warp 16 issues the TMA loads and scans the
-// gates, one thread each of warps 17 to 19 issues the MMAs of X, of D, of R and O (each waits for
-// its own operands only; one thread for all three either waits for one while another is
-// ready or spends more time polling).  Few long chains are cut into segments: a
-// first launch sums each segment's state from zero (keys and values only), a small kernel
-// chains them (the transition is the scalar 2^(sum c)), a second launch runs all segments
-// from their true start states.
+// What bounds it (B8 T4096 H16 d128, 128 CTAs of 64 chunks, 112 us, 72 % of the copy bandwidth's
+// floor): the per-chunk work of 28 warps on an SM, about 7,300 warp instructions in 3,400 cycles,
+// 67 % issue on the SMs in use.  What it took to get there, each step as measured: 182 us with
+// eight warps for everything behind the state; 160 with MMAs issued by three threads instead of
+// one that waits for them in turn; 141 with less code in the loop (the SM's instruction cache
+// missed 16 % and the GPC's, which all its SMs share, ran at 76 % of its rate: rolled loops, fp32
+// gate scan); 131 with building and output on warps of their own; 117 with Vt in tensor memory
+// (with Kt in shared memory the chunk moves 336 KB through it, 2,690 cycles at 128 bytes); 112
+// with shorter waits.  The form with Y runs 6,300 cycles a chunk: its loop is larger (16 % misses),
+// the state operand and Kt cost more instructions.
 //
-// A sequence's last chunk may hold rows of the next sequence or none: value rows behind the
-// end are zeroed in shared memory, Kt and P are built as zero there, and the outputs leave by
+// A sequence's last chunk may hold rows of the next sequence or none: rows behind the end are
+// zeroed in shared memory, Vt, Kt and P are built as zero there, and the outputs leave by
 // plain stores of the valid rows.  Every wait is bounded: on expiry the kernel records
 // DR_ERR_TIMEOUT, runs its remaining steps without waiting, drains its copies and MMAs,
 // frees its tensor memory and returns.

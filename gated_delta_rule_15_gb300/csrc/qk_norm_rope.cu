@@ -16,6 +16,11 @@
 // one token and runs over its heads, so that sines and cosines are computed once for all of
 // them.  A pair's other half sits in the same lane (interleaved) or rot / 16 lanes away
 // (half): its raw values come by shuffle.
+// Measured, bf16, 16 + 16 heads of 128, half layout, RMS: forward of 32768 rows 95 us (537 MB, 83 % of
+// the copy bandwidth; 197 us while every row read its weights again and formed sine, sign and
+// weight apart), gradient of 16384 rows 88 us (403 MB, 67 %; 54 % while a thread kept the weight
+// gradients of both kinds).  The gradient is bound by issue (67 %): two shuffle trees and the
+// rotation, norm and weight sums on 8 values a lane.
 #include <math.h>
 
 #include "../../include/dr.h"
