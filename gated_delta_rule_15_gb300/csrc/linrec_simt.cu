@@ -18,16 +18,19 @@ using umma::mul2;
 // four addresses per warp lie side by side, two adjacent rows form the operand of one packed
 // fma.rn.f32x2, and a column's read-out is a register sum and two shuffles.  Per token and
 // element: one multiply (decay), two fused multiply-adds.  Many chains: bound by the packed FP32
-// rate, 3 dk dv / 2 instructions a head-token.  Few chains: by one token's latency, 0.2 us (64 x 64) and
-// 0.29 us (128 x 128): 49 us for one chain of 256 tokens (asynchronous copies and joint read-outs
-// took 2 and 2 us off).
+// rate, 3 dk dv / 2 instructions a head-token.  Few chains: by one token's latency, 0.14 us (64 x 64) and
+// 0.2 us (128 x 128).
 // Rows come by asynchronous copies, a tile ahead.
-constexpr int kTile = 8, kGroup = 4;   // tokens staged in shared memory, summed at a time; kTile divides kAnchor
+// kGroup tokens' read-outs are summed over the lanes at a time; kTile tokens (kAnchor is a multiple) are staged
+// in shared memory, of which 48 KB hold two tiles.  One chain of 256 tokens of 64 x 64 / 128 x 128, us: 47 / 65
+// with 8 and 4, 37 / 58 with 16 and 4, 47 / 57 with 8 and 8, 37 / 51 with 16 and 8.
+constexpr int kGroup = 8;
+template <typename Tin, int DK, bool DOT> constexpr int kTileOf = DK == 128 && sizeof(Tin) == 4 && DOT ? 8 : 16;
 
 template <int DK, int DV, bool REV, bool DOT, typename Tin, typename Tout>
 __global__ void __launch_bounds__(128)
 linrec_token_kernel(const LinrecPass p) {
-    constexpr int M = DK / 16, PARTS = DV / kSimtCols;
+    constexpr int M = DK / 16, PARTS = DV / kSimtCols, kTile = kTileOf<Tin, DK, DOT>;
     __shared__ __align__(16) Tin sQ_[2][kTile][DK], sK_[2][kTile][DK], sV_[2][kTile][kSimtCols], sY_[2][DOT ? kTile : 1][kSimtCols];
     __shared__ __align__(16) float sO[kTile][kSimtCols];
     __shared__ float sA_[2][kTile], sDot[4][kTile], sRed[4];

@@ -90,7 +90,8 @@ int64_t segment_tokens(const LinrecSeqs &s, int64_t H) {
     const int64_t chains = s.N * H, nc = (s.T + linrec::kChunk - 1) / linrec::kChunk;
     double best = (double)((chains + kSms - 1) / kSms) * nc;
     int64_t seg = whole;
-    for (int64_t cut = 2; cut <= kSms && cut * per <= nc; ++cut) {
+    const int64_t most = 2 + 4 * kSms / chains;   // further cuts add launches' work and no blocks side by side
+    for (int64_t cut = 2; cut <= most && cut * per <= nc; ++cut) {
         const int64_t len = ((nc + cut - 1) / cut + per - 1) / per * per, segs = (nc + len - 1) / len;
         const double cost = (double)((chains * segs + kSms - 1) / kSms) * len +
                             0.5 * (double)((chains * (segs - 1) + kSms - 1) / kSms) * len + 8;

@@ -459,10 +459,14 @@ def chunk_fwd_host(q, k, v, log_alpha, beta, init_state=None, *, chunk: int = 64
 
 # ------------------------------------------------------------ additive gated recurrence
 # These calls also serve single tokens, where the host's time counts: addresses go to ctypes as
-# integers, shapes are compared as they are.
+# integers, shapes are compared as they are, the device and the stream are asked for without
+# torch.cuda's own checks where this torch has the plain getters.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_one_device(*ts):
     """Contiguous tensors of the current device, or ValueError."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     for t in ts:
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on the current CUDA device")
@@ -484,7 +488,7 @@ def _raw_stream(stream):
         return stream.cuda_stream
     if _current_raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _current_raw_stream(torch.cuda.current_device())
+    return _current_raw_stream(_current_device())
 
 
 def _at(t):
@@ -686,7 +690,7 @@ def _rows_into(given, x, what):
 
 
 def _qk_desc(q, k, table, positions, offset, norm, wq, wk, eps, layout, rot_scale):
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     for t in (q, k):
         if t is not None and t.get_device() != dev:
             raise ValueError("q and k must be on the current CUDA device")
