@@ -43,8 +43,8 @@
 //
 // Work split: one CTA per (sequence, head, segment) walks its chunks.  Warps 0..7 hold the state;
 // warps 8..15 make Vt, or Kt and P; warps 16..23 write the outputs and, without Y, build P; warp
-// 24 issues the TMA loads and scans the gates; one thread each of warps 25 and 26 issues the MMAs
-// of X, and of D, R and O (D first: the next chunk's Vt waits for it).  Few long chains are cut
+// 24 issues the TMA loads, warp 27 scans the gates; one thread each of warps 25 and 26 issues the
+// MMAs of X, and of D, R and O (D first: the next chunk's Vt waits for it).  Few long chains are cut
 // into segments: a first launch sums each segment's state from zero (keys and values only), a
 // small kernel chains them (the transition is the scalar 2^(sum c)), a second launch runs all
 // segments from their true start states.
@@ -83,7 +83,7 @@ using tc::wait_cycles;
 
 constexpr int kChunk = 64;
 constexpr int kStateWarps = 8, kBuildWarps = 8, kOutWarps = 8, kBuild0 = kStateWarps, kOut0 = kBuild0 + kBuildWarps,
-              kLoadWarp = kOut0 + kOutWarps, kScoreWarp = kLoadWarp + 1, kUpdateWarp = kLoadWarp + 2,
+              kLoadWarp = kOut0 + kOutWarps, kScoreWarp = kLoadWarp + 1, kUpdateWarp = kLoadWarp + 2, kGateWarp = kLoadWarp + 3,
               kThreads = (kLoadWarp + 4) * 32;
 // Registers a thread: launched with kRegs; the state warps take what the others give back.
 constexpr int kRegs = 72, kStateRegs = 104, kEdgeRegs = 64, kIssueRegs = 40;
@@ -698,24 +698,15 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     } else {
         fewer_regs<kIssueRegs>();
         if (warp == kLoadWarp) {
-            // ---------------------------------------------------------------- loads and gates
-            const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV : PK + PV);
-            float total = 0.f;
-            float x[2];
-            int issued = 0;   // (lane 0) chunks whose loads were issued; none after an expiry
-            auto load_gates = [&](int it) {   // two tokens a lane; backwards the tokens one further on
-                const int64_t t = row_of(it) + 2 * lane + (rev ? 1 : 0), end = rev ? hi : row_of(it) + count_of(it);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) x[e] = p.la && t + e < end ? p.la[(t + e) * H + h] : 0.f;
-            };
-            if (chunks > 0) load_gates(0);
+            // ---------------------------------------------------------------- loads
+            if (lane == 0) {
+                const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV : PK + PV);
+                int issued = 0;   // chunks whose loads were issued; none after an expiry
 #pragma unroll 1
-            for (int it = 0; it < chunks; ++it) {
-                const int s = it % kStages;
-                if (it >= kStages) wait(b_free + s, it / kStages - 1);
-                if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
-                __syncwarp();
-                if (lane == 0 && *polls != 0) {
+                for (int it = 0; it < chunks; ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages) wait(b_free + s, it / kStages - 1);
+                    if (*polls == 0) break;
                     unsigned char *st = stage(it);
                     issued = it + 1;
                     const int row = (int)row_of(it);
@@ -736,6 +727,24 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             tma_load_3d(sm + L::Y + y * L::Y_STAGE + b * 8192, &ty, b_y + y, 64 * b, h, row);
                     }
                 }
+                // the loads have landed before the block ends, also after an expiry
+                for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
+                for (int it = max(0, issued - 3); DOT && it < issued; ++it) wait_cycles(b_y + it % 3, (it / 3) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kGateWarp) {
+            // ---------------------------------------------------------------- gates
+            float total = 0.f;
+            float x[2];
+            auto load_gates = [&](int it) {   // two tokens a lane; backwards the tokens one further on
+                const int64_t t = row_of(it) + 2 * lane + (rev ? 1 : 0), end = rev ? hi : row_of(it) + count_of(it);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x[e] = p.la && t + e < end ? p.la[(t + e) * H + h] : 0.f;
+            };
+            if (chunks > 0) load_gates(0);
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
                 // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
                 float2 y[2];
 #pragma unroll
@@ -794,13 +803,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (lane == 0) mbar_arrive(b_gate + it % L::GATES);
             }
             if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
-            // the loads have landed before the block ends, also after an expiry
-            if (lane == 0) {
-                for (int it = max(0, issued - kStages); it < issued; ++it) wait_cycles(b_load + it % kStages, (it / kStages) & 1);
-                for (int it = max(0, issued - 3); DOT && it < issued; ++it) wait_cycles(b_y + it % 3, (it / 3) & 1);
-            }
-            __syncwarp();
-        } else if (warp >= kScoreWarp) {
+        } else {
             // ---------------------------------------------------------------- MMA issue
             if (lane == 0 && chunks > 0 && ((outputs && warp == kScoreWarp) || warp == kUpdateWarp)) {
                 constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
