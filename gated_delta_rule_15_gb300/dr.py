@@ -672,6 +672,8 @@ def _rows_of(x, what):
     step = x.stride(-3) if x.shape[-3] > 1 else (x.stride(0) if x.dim() == 4 and x.shape[0] > 1 else H * d)
     if x.dim() == 4 and x.shape[0] > 1 and x.shape[1] > 1 and x.stride(0) != x.shape[1] * step:
         raise ValueError(f"{what}: rows must be equally far apart")
+    if n > 1 and step < H * d:   # a broadcast row's 0 would mean contiguous rows
+        raise ValueError(f"{what}: rows must not share memory")
     return n, H, d, step
 
 

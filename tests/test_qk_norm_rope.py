@@ -280,3 +280,16 @@ def test_host_side_errors(dr):
     assert bwd(f, dk=far["dq"] + 2 * 500) == -1 and bwd(f, dk=far["dq"] + 2 * 896) == -1
     assert bwd(f, dk=far["dq"] + 2 * 1024 * 3 + 2 * 256) == -1
     assert bwd(_desc(dr, q_out_stride=1024, k_out_stride=2048), dk=far["dq"] + 2 * 512) == -1
+
+
+@pytest.mark.parametrize("make", [
+    lambda x: x[:1].expand(6, 4, 64), lambda x: x[:1].unsqueeze(0).expand(2, 3, 4, 64),
+    lambda x: x[:1].unsqueeze(0).expand(6, 1, 4, 64), lambda x: x.as_strided((6, 4, 64), (128, 64, 1)),
+    lambda x: x[:3].unsqueeze(0).expand(2, 3, 4, 64)])
+def test_rows_that_share_memory_are_refused(dr, make):
+    """A broadcast row has stride 0, which the C ABI reads as contiguous rows: behind the tensor's end."""
+    x = torch.zeros(6, 4, 64)
+    assert dr._rows_of(x, "q") == (6, 4, 64, 256)
+    assert dr._rows_of(x[:1].expand(1, 4, 64), "q")[:3] == (1, 4, 64)
+    with pytest.raises(ValueError):
+        dr._rows_of(make(x), "q")
