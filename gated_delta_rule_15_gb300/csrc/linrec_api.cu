@@ -113,9 +113,11 @@ extern "C" int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const vo
     const size_t sb = sizeof(float) * (size_t)seqs.N * d.H * d.dk * d.dv, rows = (size_t)seqs.total * d.H;
     const size_t ie = d.in_dtype == DR_BF16 ? 2 : 4, ob = rows * d.dv * (d.out_dtype == DR_BF16 ? 2 : 4);
     if (final_state != init_state && overlaps(final_state, sb, init_state, sb)) return kErrInvalid;
-    if (overlaps(out, ob, q, rows * d.dk * ie) || overlaps(out, ob, k, rows * d.dk * ie) ||
-        overlaps(out, ob, v, rows * d.dv * ie) || overlaps(out, ob, init_state, sb) || overlaps(out, ob, final_state, sb))
-        return kErrInvalid;
+    const struct { const void *p; size_t n; } read[] = {
+        {q, rows * d.dk * ie}, {k, rows * d.dk * ie}, {v, rows * d.dv * ie}, {log_alpha, rows * sizeof(float)}};
+    for (const auto &r : read)
+        if (overlaps(out, ob, r.p, r.n) || overlaps(final_state, sb, r.p, r.n)) return kErrInvalid;
+    if (overlaps(out, ob, init_state, sb) || overlaps(out, ob, final_state, sb)) return kErrInvalid;
     size_t need = 0;
     dr_linrec_fwd_workspace_bytes(desc, &need);
     if (need > 0 && (!workspace || workspace_bytes < need)) return kErrWorkspace;
@@ -220,9 +222,11 @@ extern "C" int dr_linrec_step(const dr_step_desc *d, const void *q, const void *
     if ((uintptr_t)log_alpha & 3u) return kErrInvalid;
     const size_t n = (size_t)(d->B * d->H), sb = sizeof(float) * n * d->dk * d->dv;
     const size_t ie = d->in_dtype == DR_BF16 ? 2 : 4, ob = n * d->dv * (d->out_dtype == DR_BF16 ? 2 : 4);
-    if (overlaps(state, sb, out, ob) || overlaps(out, ob, q, n * d->dk * ie) || overlaps(out, ob, k, n * d->dk * ie) ||
-        overlaps(out, ob, v, n * d->dv * ie))
-        return kErrInvalid;
+    const struct { const void *p; size_t n; } read[] = {
+        {q, n * d->dk * ie}, {k, n * d->dk * ie}, {v, n * d->dv * ie}, {log_alpha, n * sizeof(float)}};
+    for (const auto &r : read)
+        if (overlaps(out, ob, r.p, r.n) || overlaps(state, sb, r.p, r.n)) return kErrInvalid;
+    if (overlaps(state, sb, out, ob)) return kErrInvalid;
     return launch_linrec_step((int64_t)n, (int)d->dk, (int)d->dv, d->in_dtype == DR_BF16, d->out_dtype == DR_BF16, q, k,
                               v, d->gate == DR_GATE_NONE ? nullptr : log_alpha, state, out, (cudaStream_t)stream);
 }

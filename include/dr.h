@@ -331,10 +331,11 @@ typedef struct {
 
 /*
  * Forward.  q, k, v, log_alpha, init_state, out, final_state as for dr_chunk_fwd (final_state
- * may equal init_state); cu_seqlens NULL unless N >= 1.  out overlaps no input or state.
- * Sums are fp32.  fp32 inputs: fp32 arithmetic throughout.  bf16 inputs: the state keeps at
- * least 16 bits of every product's factors and fp32 sums.  Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED,
- * DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace rules as for dr_chunk_fwd; its size depends
+ * may equal init_state); cu_seqlens NULL unless N >= 1.  out overlaps no input or state,
+ * final_state no input other than init_state.
+ * Sums are fp32.  fp32 inputs: fp32 arithmetic throughout.  bf16 inputs: the state's products
+ * are exact, its sums fp32; out reads the state and the scores in one bf16 term each.
+ * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED, DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace rules as for dr_chunk_fwd; its size depends
  * only on the descriptor.
  */
 int dr_linrec_fwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);

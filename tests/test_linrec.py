@@ -505,3 +505,25 @@ def test_host_tensors_are_refused(dr):
         dr.linrec_fwd(c, c, c, cu_seqlens=torch.tensor([0, 4], dtype=torch.int32).cuda())
     with pytest.raises(dr.DrError):
         dr.linrec_fwd(torch.zeros(1, 4, 1, 96).cuda(), torch.zeros(1, 4, 1, 96).cuda(), torch.zeros(1, 4, 1, 96).cuda())
+
+
+@no_gpu_only
+def test_written_buffers_over_inputs_are_refused(dr):
+    import ctypes
+    vp = ctypes.c_void_p
+    d, big = _desc(dr), 1 << 40
+
+    def fwd(**o):
+        names = ("q", "k", "v", "la", "cu", "s0", "out", "fin", "ws")
+        return dr.lib().dr_linrec_fwd(ctypes.byref(d), *[vp(o.get(n, (i + 1) << 36)) for i, n in enumerate(names)], big, None)
+
+    st = dr.StepDesc(4, 2, 128, 128, dr.DR_BF16, dr.DR_BF16, dr.DR_GATE_SCALAR, 0)
+
+    def step(**o):
+        names = ("q", "k", "v", "la", "s0", "out")
+        return dr.lib().dr_linrec_step(ctypes.byref(st), *[vp(o.get(n, (i + 1) << 36)) for i, n in enumerate(names)], None)
+
+    for i in range(4):   # q, k, v, log_alpha
+        x = (i + 1) << 36
+        assert fwd(out=x) == -1 and fwd(fin=x) == -1 and fwd(fin=x + 16) == -1
+        assert step(out=x) == -1 and step(s0=x) == -1 and step(s0=x + 16) == -1
