@@ -317,8 +317,11 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *     another row's sake nor written.  States are [N, H, dk, dv] (N = B if not packed).
  *   - The first call on a device looks up device addresses: make it before a stream capture.
  *   - log_alpha and d_log_alpha need 4-byte, cu_seqlens 8-byte alignment.
- *   - log_alpha = -inf is a full reset (alpha = 0).  Inputs of the sequences' rows are
- *     otherwise finite; values in rows of no sequence do not matter.
+ *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  bf16
+ *     problems run in chunks of 64 tokens: there the state in front of a chunk enters the
+ *     chunk's outputs with no less than 2^-60 (states and gradients of log_alpha: exactly).
+ *     Inputs of the sequences' rows are otherwise finite; a NaN or infinity may reach every
+ *     output of its chunk.  Values in rows of no sequence do not matter.
  */
 typedef struct {
     int64_t B, T, H, dk, dv;  /* B, H >= 1; T >= 0; dk, dv in {64, 128}                */
