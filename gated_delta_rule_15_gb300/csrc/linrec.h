@@ -62,6 +62,7 @@ struct LinrecPass {
     const float *init;           // state before the first (backwards: after the last) token, or NULL
     float *fin;                  // state at the other end, or NULL
     bool state_t;                // init and fin hold the transposed state
+    bool chained;                // the workspace still holds the segments' start states: the pass before had this state
     void *out;                   // [rows, H, dv]
     // log-decay gradient, in the dq and dk passes: dot[part][h][row] = sum over the part's
     // value columns of out without the row's own term, times y [rows, H, dv]

@@ -195,9 +195,11 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
         }
         if ((rc = pass(p)) != kOk) return rc;
     }
-    // dv backwards over dS, and the initial state's gradient
+    // dv backwards over dS, and the initial state's gradient; its segments start from the dk
+    // pass's states, which lie in the workspace in the caller's orientation
     p.dk = (int)d.dk; p.dv = (int)d.dv; p.rev = true; p.state_t = false;
     p.q = k; p.k = q; p.v = d_out; p.init = d_final_state; p.fin = d_init_state; p.out = dv;
+    p.chained = d.T > 0;
     p.y = nullptr; p.dot = p.anchor = p.inner = nullptr;
     if ((rc = pass(p)) != kOk) return rc;
     if (!gate) return kOk;

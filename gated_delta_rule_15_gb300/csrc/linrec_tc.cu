@@ -139,14 +139,16 @@ int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStre
     if (a.seg < s.total) {
         a.seg_state = (float *)workspace;
         a.seg_decay = a.seg_state + (size_t)slots * p.H * p.dk * p.dv;
-        a.sums = true;
-        int rc = dispatch(m, a, false, grid, stream);
-        if (rc != kOk) return rc;
-        const int quads = p.dk * p.dv / 4;
-        linrec_chain_kernel<<<dim3((unsigned)(s.N * p.H), (unsigned)(quads / 256)), 256, 0, stream>>>(
-            s, p.H, quads, p.rev, a.seg, p.init, a.seg_state, a.seg_decay);
-        if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-        a.sums = false;
+        if (!p.chained) {
+            a.sums = true;
+            int rc = dispatch(m, a, false, grid, stream);
+            if (rc != kOk) return rc;
+            const int quads = p.dk * p.dv / 4;
+            linrec_chain_kernel<<<dim3((unsigned)(s.N * p.H), (unsigned)(quads / 256)), 256, 0, stream>>>(
+                s, p.H, quads, p.rev, a.seg, p.init, a.seg_state, a.seg_decay);
+            if (cudaGetLastError() != cudaSuccess) return kErrCuda;
+            a.sums = false;
+        }
     }
     return dispatch(m, a, p.dot != nullptr, grid, stream);
 }
