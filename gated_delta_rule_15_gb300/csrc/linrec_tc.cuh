@@ -35,7 +35,7 @@
 // intra-chunk part of out.y is summed from the fp32 products X and X2 = Y V^T directly,
 //     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s);
 // measured 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the backward of
-// B8 T2048 H16 d128).
+// B8 T2048 H16 d128 as it was then).
 // log2 decays are held as a multiple of 2^-10, whose sums over a chunk are exact in fp32, and
 // a remainder, so that a difference of prefix sums is as exact as a single decay whatever
 // lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
@@ -57,8 +57,10 @@
 // missed 16 % and the GPC's, which all its SMs share, ran at 76 % of its rate: rolled loops, fp32
 // gate scan); 131 with building and output on warps of their own; 117 with Vt in tensor memory
 // (with Kt in shared memory the chunk moves 336 KB through it, 2,690 cycles at 128 bytes); 112
-// with shorter waits.  The form with Y runs 6,300 cycles a chunk: its loop is larger (16 % misses),
-// the state operand and Kt cost more instructions.
+// with shorter waits.  The form with Y runs 5,800 cycles a chunk (6,300 before the gates had a
+// warp of their own): a stage's tiles take 4,400 cycles from their request to their arrival, X,
+// Kt and P, O another 7,200, and shared memory holds two stages; its loop is larger, too, and Kt
+// and the state operand cost more instructions.
 //
 // A sequence's last chunk may hold rows of the next sequence or none: rows behind the end are
 // zeroed in shared memory, Vt, Kt and P are built as zero there, and the outputs leave by
