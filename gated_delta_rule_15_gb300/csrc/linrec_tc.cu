@@ -80,7 +80,8 @@ int dispatch(const CUtensorMap *m, const TcArgs &a, bool dot, unsigned grid, cud
 // all rows, 512 tokens at least, keep one long sequence from holding up the rest; shorter
 // sequences stay whole.  Forward / backward of 20011 rows x 8 heads of 64 in 23 sequences (longest 4077)
 // and of 16384 x 4 of 128 in 3 (11512), us, by the least segment: 256 tokens 87 / 282 and 64 / 248,
-// 512 87 / 283 and 49 / 183, 1024 90 / 298 and 65 / 246, 2048 108 / 351 and 104 / 386.
+// 512 87 / 283 and 49 / 183, 1024 90 / 298 and 65 / 246, 2048 108 / 351 and 104 / 386 (512 with the
+// present search for a block's sequence: 78 / 259 and 49 / 182).
 int64_t segment_tokens(const LinrecSeqs &s, int64_t H) {
     const int64_t whole = (s.total / kAnchor + 1) * kAnchor, per = kAnchor / linrec::kChunk;
     if (s.cu) {
