@@ -277,9 +277,11 @@ qk_rope_bwd_kernel(const RopeArgs a, int norm) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[e] = r * fmaf(x[e], f, u[e]);
             }
+            if (i < rows) {   // a turn on no row has sums of 0, and r is infinite there without eps
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dw[e] = fmaf(o[e], r, dw[e]);
-            if (i < rows) st8(y0 + (int64_t)i * D, u);
+                for (int e = 0; e < 8; ++e) dw[e] = fmaf(o[e], r, dw[e]);
+                st8(y0 + (int64_t)i * D, u);
+            }
         }
     }
     if (!a.partial) return;

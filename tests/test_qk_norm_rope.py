@@ -206,6 +206,33 @@ def test_streams_and_graph(dr):
     assert all(torch.equal(a, b) for a, b in zip(run(), res))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,Hq,Hk,d", [(37, 3, 2, 128), (37, 3, 2, 64), (1, 5, 3, 128), (1003, 5, 3, 64), (5000, 7, 1, 128), (3, 1, 1, 256)])
+def test_weight_gradients_without_eps(dr, n, Hq, Hk, d, dtype, norm):
+    """eps = 0 with rows that are not zero: lanes without a row of their own (odd numbers of rows,
+    uneven runs of heads) add nothing to the weights' gradients."""
+    gen = torch.Generator().manual_seed(n + d)
+    x = [torch.randn((n, h, d), generator=gen).to(DT[dtype]) for h in (Hq, Hk)]
+    g = [torch.randn((n, h, d), generator=gen).to(DT[dtype]) for h in (Hq, Hk)]
+    w = [1 + 0.2 * torch.randn(d, generator=gen) for _ in range(2)]
+    leaves, ws = ([t.double().requires_grad_() for t in ts] for ts in (x, w))
+    freq = frequencies(d // 2, 10000.0, None)
+    ref = [define(a, b, torch.arange(n), freq, norm, "half", 0.0, 1.0) for a, b in zip(leaves, ws)]
+    sum((r * t.double()).sum() for r, t in zip(ref, g)).backward()
+    table = dr.rope_table(d // 2)
+    cu = [[t.cuda() for t in ts] for ts in (x, g, w)]
+    kw = dict(norm=norm, wq=cu[2][0], wk=cu[2][1], eps=0.0)
+    y = dr.qk_norm_rope(*cu[0], table, **kw)
+    got = dr.qk_norm_rope_bwd(*cu[0], table, *cu[1], **kw)
+    bf = dtype == "bf16"
+    for i, s in enumerate("qk"):
+        check(y[i], ref[i].detach(), 2.0 ** -16, s, bf)
+        check(got[i], leaves[i].grad, 2.0 ** -15, "d" + s, bf)
+        check(got[2 + i], ws[i].grad, 2.0 ** -11, "dw" + s, False)
+
+
 # ---------------------------------------------------------------- without a GPU
 @pytest.mark.parametrize("rot", [0, 16, 64, 128, 256])
 @pytest.mark.parametrize("scaling", SCALINGS)
