@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
 qk_rope_kernel(const RopeArgs a, int norm) {
     constexpr int LPR = D / 8, U = 4;
     const int lane = threadIdx.x & 31, l = lane % LPR, src = partner<HALF>(a, lane, l), lp = l + src - lane;
+    const bool rotated = 8 * l < a.rot;
     const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
     const int64_t tok = unit / a.groups;
     const int g = (int)(unit % a.groups), all = a.heads[0] + a.heads[1];
@@ -202,7 +203,11 @@ qk_rope_kernel(const RopeArgs a, int norm) {
                     r = rsqrtf(norm == DR_NORM_RMS ? fmaf(ss, 1.f / D, a.eps) : ss + a.eps);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = r * fmaf(B[e], o[e], A[e] * x[e]);
+                for (int e = 0; e < 8; ++e) {   // (0 times an infinity would be NaN where there is no pair)
+                    float y = A[e] * x[e];
+                    if (rotated) y = fmaf(B[e], o[e], y);
+                    x[e] = r * y;
+                }
                 if (i + u < rows) st8(y0 + (int64_t)(i + u) * D, x);
             }
         }
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 qk_rope_bwd_kernel(const RopeArgs a, int norm) {
     constexpr int LPR = D / 8, RPB = 256 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, src = partner<HALF>(a, lane, l);
+    const bool rotated = 8 * l < a.rot;
     const int s = (int)blockIdx.x >= a.blocks[0], blocks = a.blocks[s], block = (int)blockIdx.x - s * a.blocks[0], heads = a.heads[s];
     const int groups = a.groups < heads ? a.groups : heads;   // runs of heads a token's rows are split into
     const int64_t units = a.n_tok * groups;
@@ -261,7 +267,8 @@ qk_rope_bwd_kernel(const RopeArgs a, int norm) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 ss = fmaf(x[e], x[e], ss);
-                u[e] = fmaf(si[e], o[e], co[e] * u[e]);   // rotated back
+                u[e] *= co[e];   // rotated back
+                if (rotated) u[e] = fmaf(si[e], o[e], u[e]);
                 o[e] = u[e] * x[e];
                 u[e] *= w[e];
                 gx = fmaf(o[e], w[e], gx);

@@ -233,6 +233,29 @@ def test_weight_gradients_without_eps(dr, n, Hq, Hk, d, dtype, norm):
         check(got[2 + i], ws[i].grad, 2.0 ** -11, "dw" + s, False)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(64, 0), (64, 16), (128, 48), (256, 128)])
+def test_values_behind_the_rotated_part_pass_through(dr, d, rot, layout, dtype):
+    """Without a norm they are handed on as they are, infinities and NaN among them, and touch no
+    other value; forwards and back."""
+    gen = torch.Generator().manual_seed(d + rot)
+    x = torch.randn((9, 3, d), generator=gen).to(DT[dtype])
+    clean = x.clone().cuda()
+    inf = float("inf")
+    for i, v in enumerate((inf, -inf, float("nan"), 0.0, inf)):
+        x[i, i % 3, rot + (7 * i + 1) % (d - rot)] = v
+    x, table = x.cuda(), dr.rope_table(rot) if rot else None
+    kw = dict(norm="none", layout=layout, offset=5)
+    for run in (lambda t: dr.qk_norm_rope(t, None, table, **kw)[0],
+                lambda t: dr.qk_norm_rope_bwd(clean, None, table, t, None, **kw)[0]):
+        y, want = run(x), run(clean)
+        assert torch.equal(torch.isnan(y), torch.isnan(x))
+        assert torch.equal(y[..., rot:].nan_to_num(nan=3.0), x[..., rot:].nan_to_num(nan=3.0))
+        assert torch.equal(y[..., :rot], want[..., :rot])
+
+
 # ---------------------------------------------------------------- without a GPU
 @pytest.mark.parametrize("rot", [0, 16, 64, 128, 256])
 @pytest.mark.parametrize("scaling", SCALINGS)
