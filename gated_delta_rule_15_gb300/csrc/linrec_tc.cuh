@@ -754,11 +754,12 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll 1
             for (int it = 0; it < chunks; ++it) {
                 if (it >= L::GATES) wait(b_gfree + it % L::GATES, it / L::GATES - 1);
-                // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision
+                // log2 decays as (multiple of 2^-10, remainder): x log2(e) to twice fp32's precision (a
+                // NaN stays one, and with it all that the token's decay reaches)
                 float2 y[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float v = fmaxf(x[e], -120.f), kLog2e = 1.44269504f, kRest = 1.92596299e-8f;
+                    const float v = x[e] < -120.f ? -120.f : x[e], kLog2e = 1.44269504f, kRest = 1.92596299e-8f;
                     const float m = v * kLog2e, r = fmaf(v, kLog2e, -m) + v * kRest, q = rintf(m * 1024.f) * (1.f / 1024.f);
                     y[e] = make_float2(q, (m - q) + r);
                 }

@@ -293,6 +293,36 @@ def test_long_sequences_in_few_chains(dr, T, H, dk, dv, cu, strength):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,t", [((70, 130, 64), 0), ((70, 130, 64), 77), ((20, 3000, 40), 1500), ((10, 5, 1), 3)])
+def test_nan_gate_shows_in_its_sequence(dr, lens, t, dtype):
+    """A NaN log decay reaches everything that depends on it, on every path, and no neighbour."""
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T, a, b = cu[-1], cu[1], cu[2]
+    c = cuda(inputs(1, T, 2, 64, 128, dtype, N=3, seed=T))
+    cuc = torch.tensor(cu, dtype=torch.int64).cuda()
+    run = lambda: (*dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc),
+                   *dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc))
+    want = run()
+    c["la"][0, a + t, 1] = float("nan")
+    got = run()
+    o, f, dq, dk_, dv_, dla, d0 = got
+    for x in (o, dq):                                   # rows that read a state behind the gate
+        assert torch.isnan(x[0, a + t:b, 1]).all()
+    for x in (dk_, dv_):                                # rows whose write passes through it
+        assert torch.isnan(x[0, a:a + t, 1]).all()
+    assert torch.isnan(f[1, 1]).all() and torch.isnan(d0[1, 1]).all() and torch.isnan(dla[0, a + t, 1])
+    for x, y in zip(got, want):
+        if x is f or x is d0:
+            assert torch.equal(x[[0, 2]], y[[0, 2]]) and torch.equal(x[:, 0], y[:, 0])
+        else:
+            assert torch.equal(x[:, :a], y[:, :a]) and torch.equal(x[:, b:], y[:, b:]) and torch.equal(x[:, :, 0], y[:, :, 0])
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
