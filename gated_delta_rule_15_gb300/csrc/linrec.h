@@ -19,7 +19,8 @@
 // same term (do_r.v_r)(q_r.k_r) of the token itself; it is left out of both, so that a
 // strong decay's small gradient is no difference of large numbers.  The sums run over at
 // most kAnchor tokens: the dq pass stores S at every such boundary and the dk pass, which
-// holds the same entries of dS there, adds the inner product.
+// holds the same entries of dS there, adds the inner product.  Where a_t is 0 the gradient is set
+// to 0: the sums are 0 there in exact arithmetic only.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -82,8 +83,8 @@ size_t linrec_tc_workspace_bytes(const LinrecSeqs &s, int64_t H, int dk, int dv)
 int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStream_t stream);
 
 // dlog a from the two passes' dot products and the inner products; `parts` of each.
-int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int parts, const float *dot_q, const float *dot_k,
-                            const float *inner, float *dla, cudaStream_t stream);
+int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int parts, const float *la, const float *dot_q,
+                            const float *dot_k, const float *inner, float *dla, cudaStream_t stream);
 
 int launch_linrec_step(int64_t chains, int dk, int dv, bool in_bf16, bool out_bf16, const void *q, const void *k,
                        const void *v, const float *la, float *state, void *out, cudaStream_t stream);

@@ -203,8 +203,9 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
     p.y = nullptr; p.dot = p.anchor = p.inner = nullptr;
     if ((rc = pass(p)) != kOk) return rc;
     if (!gate) return kOk;
-    return launch_linrec_gate_grad(seqs, (int)d.H, w.parts, (const float *)(ws + w.dot_q), (const float *)(ws + w.dot_k),
-                                   (const float *)(ws + w.inner), d_log_alpha, (cudaStream_t)stream);
+    return launch_linrec_gate_grad(seqs, (int)d.H, w.parts, log_alpha, (const float *)(ws + w.dot_q),
+                                   (const float *)(ws + w.dot_k), (const float *)(ws + w.inner), d_log_alpha,
+                                   (cudaStream_t)stream);
 }
 
 extern "C" int dr_linrec_step(const dr_step_desc *d, const void *q, const void *k, const void *v, const float *log_alpha,

@@ -242,9 +242,10 @@ int launch_token_types(const LinrecPass &p, cudaStream_t s) {
 
 // ---------------------------------------------------------------- log-decay gradient
 // One warp per run of kAnchor tokens of a chain: 8 consecutive tokens a lane, a suffix sum
-// over the lanes, the run's inner product added.  Reads 8 and writes 4 bytes a head-token.
+// over the lanes, the run's inner product added.  Where alpha is 0 (a reset) so is the gradient,
+// alpha <S, dS>: the sums would leave their rounding there.  Reads 12 and writes 4 bytes a head-token.
 __global__ void __launch_bounds__(256)
-linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__restrict__ dot_q,
+linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__restrict__ la, const float *__restrict__ dot_q,
                         const float *__restrict__ dot_k, const float *__restrict__ inner, float *__restrict__ dla) {
     const int64_t chain = blockIdx.x, n = chain / H;
     const int h = (int)(chain % H), lane = threadIdx.x & 31;
@@ -253,9 +254,12 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
     const int64_t runs = (hi - lo + kAnchor - 1) / kAnchor, slots = linrec_slots(seqs);
     for (int64_t j = blockIdx.y * 8 + (threadIdx.x >> 5); j < runs; j += (int64_t)gridDim.y * 8) {
         const int64_t t0 = lo + j * kAnchor + 8 * lane;
-        float x[8];
+        float x[8], a[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+            x[e] = 0.f;
+            a[e] = t0 + e < hi ? la[(t0 + e) * H + h] : 0.f;
+        }
         float d = 0.f;
         for (int part = 0; part < parts; ++part) {
             const size_t row = ((size_t)part * H + h) * seqs.total;
@@ -276,7 +280,7 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
         if (lane == 31) later = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (t0 + e < hi) dla[(t0 + e) * H + h] = x[e] + later + d;
+            if (t0 + e < hi) dla[(t0 + e) * H + h] = expf(a[e]) == 0.f ? 0.f : x[e] + later + d;
     }
 }
 
@@ -357,12 +361,12 @@ int launch_linrec_simt(const LinrecPass &p, cudaStream_t s) {
     return kErrUnsupported;
 }
 
-int launch_linrec_gate_grad(const LinrecSeqs &seqs, int H, int parts, const float *dot_q, const float *dot_k,
-                            const float *inner, float *dla, cudaStream_t s) {
+int launch_linrec_gate_grad(const LinrecSeqs &seqs, int H, int parts, const float *la, const float *dot_q,
+                            const float *dot_k, const float *inner, float *dla, cudaStream_t s) {
     const int64_t runs = ((seqs.cu ? seqs.total : seqs.T) + kAnchor - 1) / kAnchor;
     const int64_t y = runs < 8 ? 1 : (runs + 7) / 8 < 1024 ? (runs + 7) / 8 : 1024;
-    linrec_gate_grad_kernel<<<dim3((unsigned)(seqs.N * H), (unsigned)y), 256, 0, s>>>(seqs, H, parts, dot_q, dot_k,
-                                                                                     inner, dla);
+    linrec_gate_grad_kernel<<<dim3((unsigned)(seqs.N * H), (unsigned)y), 256, 0, s>>>(seqs, H, parts, la, dot_q,
+                                                                                     dot_k, inner, dla);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 

@@ -323,6 +323,21 @@ def test_nan_gate_shows_in_its_sequence(dr, lens, t, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,cu", [(300, None), (16, None), (3000, None), (300, [0, 5, 66, 300])])
+def test_gradient_of_a_reset_is_zero(dr, T, cu, dtype):
+    """d_log_alpha = alpha <S, dS> is 0 where alpha is, not the rounding of the sums it comes from."""
+    N = len(cu) - 1 if cu else 0
+    c = cuda(inputs(1, T, 2, 128, 64, dtype, N=N, seed=T))
+    at = [t for t in (0, 5, 15, 63, 64, 65, 200, 255, 256, 299, 2999) if t < T]
+    for i, t in enumerate(at):
+        c["la"][:, t, 0] = -math.inf if i % 2 else -200.0
+    cuc = None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda()
+    dla = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)[3]
+    assert (dla[:, at, 0] == 0).all() and (dla[:, at, 1] != 0).all()
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
