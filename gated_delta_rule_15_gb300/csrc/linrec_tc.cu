@@ -33,13 +33,14 @@ bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t H, int64_t
 // another block than the first segment's writes).  One thread per four state entries, the
 // sums kAhead segments ahead of their use; a sequence of one segment is left alone.
 __global__ void __launch_bounds__(256)
-linrec_chain_kernel(const LinrecSeqs seqs, int H, int quads, bool rev, int64_t seg, const float *__restrict__ init,
-                    float *__restrict__ state, const float *__restrict__ decay) {
+linrec_chain_kernel(const LinrecSeqs seqs, int H, int quads, bool rev, int64_t seg, bool by_rows,
+                    const float *__restrict__ init, float *__restrict__ state, const float *__restrict__ decay) {
     const int64_t chain = blockIdx.x, n = chain / H;
     const int h = (int)(chain % H), e = blockIdx.y * 256 + threadIdx.x;
     int64_t lo, hi;
     seq_range(seqs, n, lo, hi);
-    const int64_t segs = hi > lo ? (hi - lo + seg - 1) / seg : 1, base = lo / seg + n;
+    const int64_t segs = hi > lo ? (hi - lo + seg - 1) / seg : 1;
+    const int base = linrec::state_slot(by_rows, (int)(lo / seg + n), lo, seg, n);
     if (segs < 2 || e >= quads) return;
     float4 s = init ? reinterpret_cast<const float4 *>(init)[chain * quads + e] : make_float4(0.f, 0.f, 0.f, 0.f);
     auto at = [&](int64_t i) { return (base + (rev ? segs - 1 - i : i)) * H + h; };
@@ -104,7 +105,12 @@ int64_t segment_tokens(const LinrecSeqs &s, int64_t H) {
     return seg;
 }
 
-int64_t segment_slots(const LinrecSeqs &s, int64_t seg) { return s.total / seg + s.N; }
+int64_t segment_slots(const LinrecSeqs &s, int64_t seg) { return s.total / seg + s.N; }   // blocks a head
+// Of the segments' states: whole sequences have none, so many of them take no room.
+bool slots_by_rows(const LinrecSeqs &s, int64_t seg) { return s.total / seg + 1 < s.N; }
+int64_t state_slots(const LinrecSeqs &s, int64_t seg) {
+    return slots_by_rows(s, seg) ? 2 * (s.total / seg) + 1 : segment_slots(s, seg);
+}
 
 }  // namespace
 
@@ -121,7 +127,7 @@ bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_
 size_t linrec_tc_workspace_bytes(const LinrecSeqs &s, int64_t H, int dk, int dv) {
     const int64_t seg = segment_tokens(s, H);
     if (seg >= s.total) return 0;
-    return sizeof(float) * (size_t)(segment_slots(s, seg) * H) * ((size_t)dk * dv + 4);
+    return sizeof(float) * (size_t)(state_slots(s, seg) * H) * ((size_t)dk * dv + 4);
 }
 
 int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStream_t stream) {
@@ -135,18 +141,18 @@ int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStre
     a.p = p;
     a.status = status;
     a.seg = segment_tokens(s, p.H);
-    const int64_t slots = segment_slots(s, a.seg);
-    const unsigned grid = (unsigned)(slots * p.H);
+    const unsigned grid = (unsigned)(segment_slots(s, a.seg) * p.H);
     if (a.seg < s.total) {
+        a.by_rows = slots_by_rows(s, a.seg);
         a.seg_state = (float *)workspace;
-        a.seg_decay = a.seg_state + (size_t)slots * p.H * p.dk * p.dv;
+        a.seg_decay = a.seg_state + (size_t)state_slots(s, a.seg) * p.H * p.dk * p.dv;
         if (!p.chained) {
             a.sums = true;
             int rc = dispatch(m, a, false, grid, stream);
             if (rc != kOk) return rc;
             const int quads = p.dk * p.dv / 4;
             linrec_chain_kernel<<<dim3((unsigned)(s.N * p.H), (unsigned)(quads / 256)), 256, 0, stream>>>(
-                s, p.H, quads, p.rev, a.seg, p.init, a.seg_state, a.seg_decay);
+                s, p.H, quads, p.rev, a.seg, a.by_rows, p.init, a.seg_state, a.seg_decay);
             if (cudaGetLastError() != cudaSuccess) return kErrCuda;
             a.sums = false;
         }

@@ -97,9 +97,20 @@ struct TcArgs {
     int *status;
     int64_t seg;          // tokens of a segment, a multiple of kAnchor
     bool sums;            // first launch over segments: states from zero, no outputs
-    float *seg_state;     // [slot][h][dk dv] in the caller's orientation: the segments' sums, then start states
-    float *seg_decay;     // [slot][h] log2 decay over a segment
+    bool by_rows;         // how the states are numbered (state_slot)
+    float *seg_state;     // [state slot][h][dk dv] in the caller's orientation: the segments' sums, then start states
+    float *seg_decay;     // [state slot][h] log2 decay over a segment
 };
+
+// Slot of the state of segment j of a cut sequence, one of more than seg rows from row lo on.  Two
+// numberings, the host takes the one with fewer slots: that of the blocks (find_segment), total / seg + N
+// of them, or, by rows, 2 (lo / seg) + j: of two cut sequences in a row the second's
+// lo / seg is greater by the whole segments d >= 1 of the first, which has at most d + 1 <= 2 d segments.
+// lo / seg + j <= total / seg, so 2 (total / seg) + 1 slots do for any number of sequences.  From the
+// block's slot of the segment; rows, and slots times heads, fit in 31 bits.
+__device__ __forceinline__ int state_slot(bool by_rows, int slot, int64_t lo, int64_t seg, int64_t n) {
+    return by_rows ? slot + (int)((uint32_t)lo / (uint32_t)seg) - (int)n : slot;
+}
 
 // Sequence n's segment j is slot lo / seg + n + j (every sequence has at least one); finds
 // (n, j) of a slot, or false.  By whole warps: 32 sequences are asked at a time, since each
@@ -224,10 +235,11 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     constexpr int kStages = L::STAGES;
     const LinrecPass &p = a.p;
     const int H = p.H, h = (int)(blockIdx.x % H);
-    const int64_t slot = blockIdx.x / H;
+    int slot = blockIdx.x / H;   // (64 bits: backward of B8 T2048 H16 d128 2 % slower)
     int64_t n, j, lo, hi;
     if (!find_segment(p.seqs, a.seg, slot, n, j)) return;
     seq_range(p.seqs, n, lo, hi);
+    slot = state_slot(a.by_rows, slot, lo, a.seg, n);
     const bool rev = p.rev, outputs = !a.sums;
     const int64_t segs = hi > lo ? ((uint32_t)(hi - lo) + (uint32_t)a.seg - 1) / (uint32_t)a.seg : 1;
     const bool last_run = rev ? j == 0 : j == segs - 1;

@@ -20,6 +20,7 @@ about 2 u of its size, random signs) and up to 2 * 256 of them are added: sqrt(5
 the largest.  Where the decay is so strong that the gradient is small against q.dq and k.dk, that
 absolute error is the bound.
 """
+import ctypes
 import math
 
 import pytest
@@ -338,6 +339,27 @@ def test_gradient_of_a_reset_is_zero(dr, T, cu, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate", [True, False])
+def test_one_long_sequence_among_many_short(dr, gate):
+    """More sequences than segments: only the cut ones' states lie in the workspace."""
+    lens = [3, 0, 70] * 20 + [2100] + [1, 64, 5] * 15 + [600, 513, 512] + [17] * 9
+    cu = torch.tensor([0] + lens).cumsum(0)
+    T, N = int(cu[-1]) + 11, len(lens)
+    d = inputs(1, T, 2, 64, 128, "bf16", gate=gate, N=N, strength=0.01, seed=T)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu.tolist(), d["do"], d["ds"])
+    slack = dla_slack(d, g) if gate else 0.0
+    c, cuc = cuda(d), cu.cuda()
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc)
+    check(o, out, "bf16", "out")
+    check(f, fin, "f32", "final_state")
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)
+    for x, n in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
+        if n != "dla" or gate:
+            check(x, g[n], "f32" if n in ("dla", "d0") else "bf16", n, slack if n == "dla" else 0.0)
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
@@ -485,6 +507,22 @@ def test_bad_descriptors(dr, bad, status):
     n = ctypes.c_size_t(0)
     for f in (dr.lib().dr_linrec_fwd_workspace_bytes, dr.lib().dr_linrec_bwd_workspace_bytes):
         assert f(ctypes.byref(_desc(dr, **bad)), ctypes.byref(n)) == status
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_workspace_does_not_grow_with_whole_sequences(dr, which):
+    """Packed sequences that are not cut keep no state: at most two a segment's length of rows (512
+    tokens at least) and one more, however many sequences there are."""
+    f = getattr(dr.lib(), f"dr_linrec_{which}_workspace_bytes")
+
+    def size(N):
+        n = ctypes.c_size_t(0)
+        assert f(ctypes.byref(_desc(dr, B=1, T=102400, H=16, N=N, gate=dr.DR_GATE_NONE)), ctypes.byref(n)) == 0
+        return n.value
+
+    per = 16 * (128 * 128 + 4) * 4
+    assert 0 < size(1024) <= (2 * 102400 // 512 + 1) * per + 256
+    assert size(1024) == size(1 << 20) and size(3) <= size(1024)
 
 
 no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake-pointer checks run only without a GPU")
