@@ -114,13 +114,18 @@ extern "C" int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const vo
     const size_t ie = d.in_dtype == DR_BF16 ? 2 : 4, ob = rows * d.dv * (d.out_dtype == DR_BF16 ? 2 : 4);
     if (final_state != init_state && overlaps(final_state, sb, init_state, sb)) return kErrInvalid;
     const struct { const void *p; size_t n; } read[] = {
-        {q, rows * d.dk * ie}, {k, rows * d.dk * ie}, {v, rows * d.dv * ie}, {log_alpha, rows * sizeof(float)}};
+        {q, rows * d.dk * ie}, {k, rows * d.dk * ie}, {v, rows * d.dv * ie}, {log_alpha, rows * sizeof(float)},
+        {seqs.cu, sizeof(int64_t) * (size_t)(d.N + 1)}};
     for (const auto &r : read)
         if (overlaps(out, ob, r.p, r.n) || overlaps(final_state, sb, r.p, r.n)) return kErrInvalid;
     if (overlaps(out, ob, init_state, sb) || overlaps(out, ob, final_state, sb)) return kErrInvalid;
     size_t need = 0;
     dr_linrec_fwd_workspace_bytes(desc, &need);
     if (need > 0 && (!workspace || workspace_bytes < need)) return kErrWorkspace;
+    for (const auto &r : read)
+        if (overlaps(workspace, need, r.p, r.n)) return kErrInvalid;
+    if (overlaps(workspace, need, init_state, sb) || overlaps(workspace, need, out, ob) || overlaps(workspace, need, final_state, sb))
+        return kErrInvalid;
     if (d.T == 0 && !final_state) return kOk;
     LinrecPass p{};
     p.seqs = seqs;
@@ -156,16 +161,23 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
     const size_t e = d.in_dtype == DR_BF16 ? 2 : 4, kb = rows * d.dk * e, vb = rows * d.dv * e, gb = rows * sizeof(float);
     // no written buffer overlaps another one or an input; only d_init_state may be d_final_state
     const struct { const void *p; size_t n; } written[] = {{dq, kb}, {dk, kb}, {dv, vb}, {d_log_alpha, gb}, {d_init_state, sb}},
-        read[] = {{q, kb}, {k, kb}, {v, vb}, {log_alpha, gb}, {init_state, sb}, {d_out, vb}, {d_final_state, sb}};
+        read[] = {{q, kb}, {k, kb}, {v, vb}, {log_alpha, gb}, {init_state, sb}, {d_out, vb}, {d_final_state, sb},
+                  {seqs.cu, sizeof(int64_t) * (size_t)(d.N + 1)}};
     for (int i = 0; i < 5; ++i) {
         for (int j = i + 1; j < 5; ++j)
             if (overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return kErrInvalid;
-        for (int j = 0; j < 7; ++j)
+        for (int j = 0; j < 8; ++j)
             if (overlaps(written[i].p, written[i].n, read[j].p, read[j].n) && !(i == 4 && j == 6 && d_init_state == d_final_state))
                 return kErrInvalid;
     }
     const BwdSpace w = bwd_space(desc);
     if (w.bytes > 0 && d.T > 0 && (!workspace || workspace_bytes < w.bytes)) return kErrWorkspace;
+    if (d.T > 0) {
+        for (const auto &x : written)
+            if (overlaps(workspace, w.bytes, x.p, x.n)) return kErrInvalid;
+        for (const auto &x : read)
+            if (overlaps(workspace, w.bytes, x.p, x.n)) return kErrInvalid;
+    }
     if (d.T == 0 && !d_init_state) return kOk;
     char *ws = (char *)workspace;
     const bool tc = on_tensor_cores(desc, seqs);

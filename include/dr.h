@@ -335,7 +335,7 @@ typedef struct {
 /*
  * Forward.  q, k, v, log_alpha, init_state, out, final_state as for dr_chunk_fwd (final_state
  * may equal init_state); cu_seqlens NULL unless N >= 1.  out overlaps no input or state,
- * final_state no input other than init_state.
+ * final_state no input other than init_state, workspace nothing (DR_ERR_INVALID).
  * Sums are fp32.  fp32 inputs: fp32 arithmetic throughout.  bf16 inputs: the state's products
  * are exact, its sums fp32; out reads the state and the scores in one bf16 term each.
  * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED, DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace rules as for dr_chunk_fwd; its size depends
@@ -357,7 +357,8 @@ int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const void *k, cons
  * d_log_alpha_t = alpha_t <S_{t-1}, dL/dS_t> comes as a sum of q.dq - k.dk over the up to 256
  * tokens behind t and one inner product of states.  It is 0 where alpha is; where a strong decay
  * makes it small against those terms, it carries their rounding (some 1e-6 of the largest).
- * Written buffers overlap neither each other nor an input otherwise.  Results do not depend
+ * Written buffers, workspace among them, overlap neither each other nor an input otherwise
+ * (DR_ERR_INVALID).  Results do not depend
  * on the order in which the GPU runs its blocks.  Statuses as for dr_linrec_fwd.
  */
 int dr_linrec_bwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);

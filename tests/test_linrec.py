@@ -610,3 +610,25 @@ def test_written_buffers_over_inputs_are_refused(dr):
         x = (i + 1) << 36
         assert fwd(out=x) == -1 and fwd(fin=x) == -1 and fwd(fin=x + 16) == -1
         assert step(out=x) == -1 and step(s0=x) == -1 and step(s0=x + 16) == -1
+
+
+@no_gpu_only
+def test_offsets_and_workspace_under_written_buffers_are_refused(dr):
+    """The blocks of a call read the offsets while others write."""
+    vp = ctypes.c_void_p
+    d = _desc(dr, B=1, T=4096, N=300)
+    names = {"fwd": ("q", "k", "v", "la", "cu", "s0", "out", "fin", "ws"),
+             "bwd": ("q", "k", "v", "la", "cu", "s0", "do", "ds", "dq", "dk", "dv", "dla", "d0", "ws")}
+    written = {"fwd": ("out", "fin"), "bwd": ("dq", "dk", "dv", "dla", "d0")}
+    for f, ns in names.items():
+        far = {n: (i + 1) << 36 for i, n in enumerate(ns)}
+
+        def call(**o):
+            return getattr(dr.lib(), f"dr_linrec_{f}")(ctypes.byref(d), *[vp(o.get(n, far[n])) for n in ns], 1 << 40, None)
+
+        for w in written[f]:
+            assert call(cu=far[w]) == -1 and call(cu=far[w] + 8) == -1 and call(cu=far[w] - 8 * 300) == -1
+        n = ctypes.c_size_t(0)
+        assert getattr(dr.lib(), f"dr_linrec_{f}_workspace_bytes")(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value > 0
+        for x in ns[:-1]:
+            assert call(ws=far[x]) == -1 and call(ws=far[x] - n.value // 16 * 16 + 16) == -1, x
