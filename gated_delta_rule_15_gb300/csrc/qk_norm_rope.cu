@@ -23,6 +23,8 @@
 // rotation, norm and weight sums on 8 values a lane.
 #include <math.h>
 
+#include <array>
+
 #include "../../include/dr.h"
 #include "common.cuh"
 
@@ -420,6 +422,31 @@ bool meet(const Rows &a, const Rows &b, int64_t n_tok, int64_t e) {
     return off < a.width * e || off + b.width * e > row;
 }
 bool same(const Rows &a, const Rows &b) { return a.p == b.p && a.width == b.width && a.stride == b.stride; }
+// `bytes` bytes in one piece
+struct Block {
+    const void *p;
+    size_t bytes;
+};
+bool meet(const Block &a, const Block &b) {
+    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
+    return a.p && b.p && a0 < b0 + b.bytes && b0 < a0 + a.bytes;
+}
+// Whether a row shares a byte with the block, which may lie between two rows.
+bool meet(const Rows &a, const Block &b, int64_t n_tok, int64_t e) {
+    if (!a.p || !b.p || n_tok < 1 || a.width < 1 || b.bytes < 1) return false;
+    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
+    if (a0 + ((n_tok - 1) * a.stride + a.width) * e <= b0 || b0 + b.bytes <= a0) return false;
+    const int64_t row = a.stride * e, off = ((b0 - a0) % row + row) % row;
+    return off < a.width * e || off + (int64_t)b.bytes > row;
+}
+
+// What every block may read beside its rows.
+using Operands = std::array<Block, 4>;
+Operands operands(const dr_qk_norm_rope_desc &d, const RopeArgs &a) {
+    const size_t w = sizeof(float) * (size_t)d.d;
+    return {Block{a.w[0], w}, Block{a.w[1], w}, Block{a.table, sizeof(uint64_t) * (size_t)(d.rot / 2)},
+            Block{a.pos, sizeof(int64_t) * (size_t)d.n_tok}};
+}
 
 }  // namespace
 }  // namespace dr
@@ -466,12 +493,15 @@ extern "C" int dr_qk_norm_rope(const dr_qk_norm_rope_desc *desc, const void *q, 
     // an output is its own input (every row is read before it is written) or meets neither
     // input nor the other output
     const int64_t e = d.dtype == DR_BF16 ? 2 : 4, wide[2] = {d.Hq * d.d, d.Hk * d.d};
-    if (meet({q_out, wide[0], a.out_stride[0]}, {k_out, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
+    if (meet(Rows{q_out, wide[0], a.out_stride[0]}, Rows{k_out, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
     for (int o = 0; o < 2; ++o)
         for (int i = 0; i < 2; ++i) {
             const Rows y{a.y[o], wide[o], a.out_stride[o]}, x{a.x[i], wide[i], a.stride[i]};
             if (meet(y, x, d.n_tok, e) && !(o == i && same(y, x))) return kErrInvalid;
         }
+    for (const Block &x : operands(d, a))
+        for (int o = 0; o < 2; ++o)
+            if (meet({a.y[o], wide[o], a.out_stride[o]}, x, d.n_tok, e)) return kErrInvalid;
     const bool half = d.layout == DR_ROPE_HALF;
     cudaStream_t s = (cudaStream_t)stream;
     using bf = __nv_bfloat16;
@@ -513,16 +543,34 @@ extern "C" int dr_qk_norm_rope_bwd(const dr_qk_norm_rope_desc *desc, const void 
     a.y[0] = dq; a.y[1] = dk;
     // dq may be q and dk may be k; otherwise no written row meets another or an input's
     const int64_t e = d.dtype == DR_BF16 ? 2 : 4, wide[2] = {d.Hq * d.d, d.Hk * d.d};
-    if (meet({dq, wide[0], a.out_stride[0]}, {dk, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
+    if (meet(Rows{dq, wide[0], a.out_stride[0]}, Rows{dk, wide[1], a.out_stride[1]}, d.n_tok, e)) return kErrInvalid;
     for (int o = 0; o < 2; ++o)
         for (int i = 0; i < 2; ++i) {
             const Rows y{a.y[o], wide[o], a.out_stride[o]}, x{a.x[i], wide[i], a.stride[i]};
             if (meet(y, x, d.n_tok, e) && !(o == i && same(y, x))) return kErrInvalid;
-            if (meet(y, {a.dy[i], wide[i], wide[i]}, d.n_tok, e)) return kErrInvalid;
+            if (meet(y, Rows{a.dy[i], wide[i], wide[i]}, d.n_tok, e)) return kErrInvalid;
         }
+    const Operands ins = operands(d, a);
+    const Block dw[2] = {{dwq, sizeof(float) * (size_t)d.d}, {dwk, sizeof(float) * (size_t)d.d}};
+    for (int o = 0; o < 2; ++o) {
+        const Rows y{a.y[o], wide[o], a.out_stride[o]};
+        for (const Block &x : ins)
+            if (meet(y, x, d.n_tok, e)) return kErrInvalid;
+        if (meet(y, dw[0], d.n_tok, e) || meet(y, dw[1], d.n_tok, e)) return kErrInvalid;
+    }
+    if (meet(dw[0], dw[1])) return kErrInvalid;
     const bool weights = dwq || dwk;
     grad_blocks(d, a.blocks);
     if (weights && (!workspace || workspace_bytes < partial_bytes(d))) return kErrWorkspace;
+    if (weights) {   // the partial sums meet nothing that is read or written beside them
+        const Block ws{workspace, partial_bytes(d)};
+        for (int o = 0; o < 2; ++o)
+            if (meet({a.y[o], wide[o], a.out_stride[o]}, ws, d.n_tok, e) || meet({a.x[o], wide[o], a.stride[o]}, ws, d.n_tok, e) ||
+                meet({a.dy[o], wide[o], wide[o]}, ws, d.n_tok, e) || meet(dw[o], ws))
+                return kErrInvalid;
+        for (const Block &x : ins)
+            if (meet(ws, x)) return kErrInvalid;
+    }
     if (d.n_tok == 0 && !weights) return kOk;
     a.partial = weights ? (float *)workspace : nullptr;
     const bool half = d.layout == DR_ROPE_HALF;

@@ -427,7 +427,7 @@ int dr_rope_table(int64_t rot, double base, int32_t scaling, double factor, doub
  *   positions      NULL or int64 [n_tok] (device), any values
  *   q_out, k_out   [n_tok, Hq | Hk, d], rows q_out_stride, k_out_stride apart (written);
  *                  may be q, k themselves, with their strides; no written row shares a
- *                  byte with another or an input's otherwise
+ *                  byte with another or an input otherwise (DR_ERR_INVALID)
  * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
  */
 int dr_qk_norm_rope(const dr_qk_norm_rope_desc *desc, const void *q, const void *k,
@@ -438,7 +438,8 @@ int dr_qk_norm_rope(const dr_qk_norm_rope_desc *desc, const void *q, const void 
  * Its gradients, from the inputs of the forward and the outputs' gradients dq_out, dk_out
  * (contiguous, dtype).  dq, dk are rows q_out_stride, k_out_stride apart (parts of one fused
  * gradient's rows, for instance) and may be q, k themselves; dwq, dwk fp32 [d] or NULL
- * (not returned; only with wq, wk).  Workspace as for dr_chunk_fwd, needed for dwq or dwk only.
+ * (not returned; only with wq, wk), which overlap no other written buffer.  Workspace as for
+ * dr_chunk_fwd, needed for dwq or dwk only; it overlaps nothing (DR_ERR_INVALID).
  * The sums' order is fixed: equal inputs give equal results.
  */
 int dr_qk_norm_rope_bwd_workspace_bytes(const dr_qk_norm_rope_desc *desc, size_t *bytes);

@@ -343,3 +343,34 @@ def test_rows_that_share_memory_are_refused(dr, make):
     assert dr._rows_of(x[:1].expand(1, 4, 64), "q")[:3] == (1, 4, 64)
     with pytest.raises(ValueError):
         dr._rows_of(make(x), "q")
+
+
+@no_gpu_only
+def test_operands_under_written_rows_are_refused(dr):
+    """Weights, table and positions are read by every block; weight gradients and their partial sums
+    are written beside the rows."""
+    vp = ctypes.c_void_p
+    names = ("q", "k", "wq", "wk", "table", "pos", "yq", "yk", "gq", "gk", "dq", "dk", "dwq", "dwk", "ws")
+    far = {n: (i + 1) << 36 for i, n in enumerate(names)}
+
+    def fwd(desc, **o):
+        return dr.lib().dr_qk_norm_rope(ctypes.byref(desc), *[vp(o.get(n, far[n])) for n in names[:8]], None)
+
+    def bwd(desc, **o):
+        return dr.lib().dr_qk_norm_rope_bwd(ctypes.byref(desc), *[vp(o.get(n, far[n])) for n in names[:6] + names[8:]], 1 << 30, None)
+
+    d, f = _desc(dr), _desc(dr, q_out_stride=1024, k_out_stride=1024)     # rows of 8 heads of 128, 4 + 2 of them written
+    size = dict(wq=512, wk=512, table=256, pos=80, dwq=512, dwk=512)
+    for n in ("wq", "wk", "table", "pos"):
+        for y in ("yq", "yk"):
+            assert fwd(d, **{n: far[y]}) == -1 and fwd(d, **{n: far[y] + 2 * 256}) == -1 and fwd(d, **{n: far[y] - size[n] + 8}) == -1
+            assert fwd(f, **{n: far[y] + 2 * 1024 * 9}) == -1 and fwd(f, **{n: far[y] + 2 * 1024 * 9 - 16}) == -1
+    for n in ("wq", "wk", "table", "pos", "dwq", "dwk"):
+        for y in ("dq", "dk"):
+            assert bwd(d, **{n: far[y]}) == -1 and bwd(d, **{n: far[y] - size[n] + 8}) == -1
+            assert bwd(f, **{n: far[y] + 2 * 1024 * 9}) == -1
+    assert bwd(d, dwq=far["dwk"]) == -1 and bwd(d, dwq=far["dwk"] + 256) == -1
+    n = ctypes.c_size_t(0)
+    assert dr.lib().dr_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value > 512
+    for x in ("q", "k", "wq", "wk", "table", "pos", "gq", "gk", "dq", "dk", "dwq", "dwk"):
+        assert bwd(d, ws=far[x]) == -1 and bwd(d, ws=far[x] - n.value // 16 * 16 + 16) == -1, x
