@@ -86,6 +86,15 @@ int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStre
 int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int parts, const float *la, const float *dot_q,
                             const float *dot_k, const float *inner, float *dla, cudaStream_t stream);
 
+// Zeroes the rows of no sequence of `rows` (row_bytes a multiple of 16) and `gates` (words a row), where given.
+struct LinrecRest {
+    void *rows[3];
+    int64_t row_bytes[3];
+    float *gates;
+    int64_t gate_words;
+};
+int launch_linrec_zero_rest(const LinrecSeqs &s, const LinrecRest &r, cudaStream_t stream);
+
 int launch_linrec_step(int64_t chains, int dk, int dv, bool in_bf16, bool out_bf16, const void *q, const void *k,
                        const void *v, const float *la, float *state, void *out, cudaStream_t stream);
 

@@ -220,6 +220,28 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
                                    (cudaStream_t)stream);
 }
 
+extern "C" int dr_linrec_zero_rest(const dr_linrec_desc *desc, const int64_t *cu_seqlens, void *dq, void *dk, void *out,
+                                   float *d_log_alpha, dr_stream_t stream) {
+    const int rc = check_desc(desc);
+    if (rc != kOk) return rc;
+    const dr_linrec_desc &d = *desc;
+    if (d.N < 1 || !cu_seqlens || ((uintptr_t)cu_seqlens & 7u) || ((uintptr_t)d_log_alpha & 3u)) return kErrInvalid;
+    const LinrecSeqs seqs = seqs_of(desc, cu_seqlens);
+    LinrecRest r{};
+    const int64_t ie = d.in_dtype == DR_BF16 ? 2 : 4, oe = d.out_dtype == DR_BF16 ? 2 : 4;
+    r.rows[0] = dq; r.rows[1] = dk; r.rows[2] = out;
+    r.row_bytes[0] = r.row_bytes[1] = d.H * d.dk * ie;
+    r.row_bytes[2] = d.H * d.dv * oe;
+    r.gates = d_log_alpha;
+    r.gate_words = d.H;
+    const size_t cu = sizeof(int64_t) * (size_t)(d.N + 1);
+    for (int i = 0; i < 3; ++i)
+        if (!aligned16(r.rows[i]) || overlaps(r.rows[i], (size_t)(r.row_bytes[i] * d.T), cu_seqlens, cu)) return kErrInvalid;
+    if (overlaps(d_log_alpha, sizeof(float) * (size_t)(d.T * d.H), cu_seqlens, cu)) return kErrInvalid;
+    if (d.T == 0) return kOk;
+    return launch_linrec_zero_rest(seqs, r, (cudaStream_t)stream);
+}
+
 extern "C" int dr_linrec_step(const dr_step_desc *d, const void *q, const void *k, const void *v, const float *log_alpha,
                               float *state, void *out, dr_stream_t stream) {
     if (!d) return kErrInvalid;

@@ -284,6 +284,27 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
     }
 }
 
+// ---------------------------------------------------------------- rows of no sequence
+// Packed sequences lie behind one another, so the rest is in front of the first and behind the last.
+__global__ void __launch_bounds__(256)
+linrec_zero_rest_kernel(const LinrecSeqs seqs, const LinrecRest rest) {
+    int64_t lo, last, hi;
+    seq_range(seqs, 0, lo, hi);
+    seq_range(seqs, seqs.N - 1, last, hi);
+    const int64_t t0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+        if (!rest.rows[b]) continue;
+        uint4 *p = static_cast<uint4 *>(rest.rows[b]);
+        const int64_t w = rest.row_bytes[b] / 16;
+        for (int64_t i = t0; i < lo * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+        for (int64_t i = hi * w + t0; i < seqs.total * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (!rest.gates) return;
+    for (int64_t i = t0; i < lo * rest.gate_words; i += step) rest.gates[i] = 0.f;
+    for (int64_t i = hi * rest.gate_words + t0; i < seqs.total * rest.gate_words; i += step) rest.gates[i] = 0.f;
+}
+
 // ---------------------------------------------------------------- single token
 // S <- a S + k v^T in place, o = S^T q: a stream of the state through the SM, bound by HBM
 // bandwidth.  A CTA holds COLS value columns of one chain; lane (rr, cq) = (lane / 4, lane % 4)
@@ -367,6 +388,11 @@ int launch_linrec_gate_grad(const LinrecSeqs &seqs, int H, int parts, const floa
     const int64_t y = runs < 8 ? 1 : (runs + 7) / 8 < 1024 ? (runs + 7) / 8 : 1024;
     linrec_gate_grad_kernel<<<dim3((unsigned)(seqs.N * H), (unsigned)y), 256, 0, s>>>(seqs, H, parts, la, dot_q,
                                                                                      dot_k, inner, dla);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+int launch_linrec_zero_rest(const LinrecSeqs &seqs, const LinrecRest &r, cudaStream_t s) {
+    linrec_zero_rest_kernel<<<304, 256, 0, s>>>(seqs, r);   // two blocks an SM
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 

@@ -47,7 +47,7 @@ EXPORTED = ("dr_version", "dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd_min_work
             "dr_chunk_bwd_workspace_bytes", "dr_chunk_bwd", "dr_selftest_bounded_wait",
             "dr_chunk_fwd_host_dev_bytes", "dr_chunk_fwd_host",
             "dr_linrec_fwd_workspace_bytes", "dr_linrec_fwd", "dr_linrec_bwd_workspace_bytes",
-            "dr_linrec_bwd", "dr_linrec_step", "dr_rope_table", "dr_qk_norm_rope",
+            "dr_linrec_bwd", "dr_linrec_zero_rest", "dr_linrec_step", "dr_rope_table", "dr_qk_norm_rope",
             "dr_qk_norm_rope_bwd_workspace_bytes", "dr_qk_norm_rope_bwd")
 
 
@@ -131,6 +131,7 @@ for _name in ("dr_linrec_fwd_workspace_bytes", "dr_linrec_bwd_workspace_bytes"):
     getattr(_lib, _name).argtypes = [ctypes.POINTER(LinrecDesc), ctypes.POINTER(ctypes.c_size_t)]
 _lib.dr_linrec_fwd.argtypes = [ctypes.POINTER(LinrecDesc)] + [_vp] * 9 + [ctypes.c_size_t, _vp]
 _lib.dr_linrec_bwd.argtypes = [ctypes.POINTER(LinrecDesc)] + [_vp] * 14 + [ctypes.c_size_t, _vp]
+_lib.dr_linrec_zero_rest.argtypes = [ctypes.POINTER(LinrecDesc)] + [_vp] * 6
 _lib.dr_linrec_step.argtypes = [ctypes.POINTER(StepDesc)] + [_vp] * 7
 _lib.dr_rope_table.argtypes = [ctypes.c_int64, ctypes.c_double, ctypes.c_int32] + \
     [ctypes.c_double] * 4 + [_vp]
@@ -537,6 +538,17 @@ def _workspace(query, desc, workspace, device, what):
     return workspace
 
 
+def _zero_rest(desc, cu_seqlens, dq, dk, out, d_log_alpha, stream):
+    """New buffers of packed problems: zeros in the rows of no sequence, so that sums over all rows are
+    right."""
+    if cu_seqlens is None:
+        return
+    rc = _lib.dr_linrec_zero_rest(ctypes.byref(desc), _at(cu_seqlens), _at(dq), _at(dk), _at(out),
+                                  _at(d_log_alpha), _raw_stream(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_linrec_zero_rest")
+
+
 def linrec_fwd(q, k, v, log_alpha=None, init_state=None, *, cu_seqlens=None, out_dtype=None,
                return_final_state: bool = True, out=None, final_state=None, workspace=None,
                stream=None):
@@ -547,17 +559,19 @@ def linrec_fwd(q, k, v, log_alpha=None, init_state=None, *, cu_seqlens=None, out
     [N,H,dk,dv].  With ``cu_seqlens`` (int64 [N + 1] on the device) the T rows of the one
     batch row hold N sequences behind one another; without, N = B.  Returns (out
     [B,T,H,dv], final_state fp32 [N,H,dk,dv] or None); ``final_state`` may be the
-    ``init_state`` tensor.  Rows of ``out`` that belong to no sequence are left as they
-    are."""
+    ``init_state`` tensor.  Rows of no sequence are zero in a new ``out`` and left as they are
+    in a given one."""
     _on_one_device(q, k, v, log_alpha, cu_seqlens, init_state, out, final_state, workspace)
     desc = _linrec_desc(q, k, v, log_alpha, cu_seqlens, out_dtype or (q.dtype if out is None else out.dtype))
     states = (desc.N or desc.B, desc.H, desc.dk, desc.dv)
     _like(init_state, states, torch.float32, "init_state")
     _like(final_state, states, torch.float32, "final_state")
     _like(out, v.shape, _TORCH_DT[desc.out_dtype], "out")
+    rest = None
     with _stream_scope(stream):
         if out is None:
             out = torch.empty(v.shape, dtype=_TORCH_DT[desc.out_dtype], device=q.device)
+            rest = out
         if final_state is None and return_final_state:
             final_state = torch.empty(states, dtype=torch.float32, device=q.device)
         workspace = _workspace(_lib.dr_linrec_fwd_workspace_bytes, desc, workspace, q.device,
@@ -567,6 +581,8 @@ def linrec_fwd(q, k, v, log_alpha=None, init_state=None, *, cu_seqlens=None, out
                                 _at(workspace), _bytes(workspace), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_linrec_fwd")
+    if rest is not None:
+        _zero_rest(desc, cu_seqlens, None, None, rest, None, stream)
     return out, final_state
 
 
@@ -576,15 +592,16 @@ def linrec_bwd(q, k, v, log_alpha, init_state, d_out, d_final_state=None, *, cu_
     (dr_linrec_bwd).  Returns (dq, dk, dv, d_log_alpha, d_init_state): the first three in
     q's dtype, d_log_alpha fp32 (None without a gate), d_init_state fp32 (None unless
     return_d_init).  ``grads``: buffers (dq, dk, dv, d_log_alpha) to write into; their rows
-    of no sequence are left as they are."""
+    of no sequence are left as they are (new ones hold zeros there)."""
     _on_one_device(q, k, v, log_alpha, cu_seqlens, init_state, d_out, d_final_state, workspace)
     desc = _linrec_desc(q, k, v, log_alpha, cu_seqlens, d_out.dtype)
     states = (desc.N or desc.B, desc.H, desc.dk, desc.dv)
     _like(init_state, states, torch.float32, "init_state")
     _like(d_final_state, states, torch.float32, "d_final_state")
     _like(d_out, v.shape, d_out.dtype, "d_out")
+    new = grads is None
     with _stream_scope(stream):
-        if grads is None:
+        if new:
             grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
                      None if log_alpha is None else torch.empty_like(log_alpha))
         else:
@@ -605,6 +622,8 @@ def linrec_bwd(q, k, v, log_alpha, init_state, d_out, d_final_state=None, *, cu_
                                 _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_linrec_bwd")
+    if new:
+        _zero_rest(desc, cu_seqlens, dq, dk, dv, dla, stream)
     return dq, dk, dv, dla, dinit
 
 

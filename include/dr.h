@@ -369,6 +369,16 @@ int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const void *k, cons
                   size_t workspace_bytes, dr_stream_t stream);
 
 /*
+ * Zeroes what dr_linrec_fwd and dr_linrec_bwd leave alone, the rows of no sequence of a packed
+ * problem (N >= 1; those in front of cu_seqlens[0] and from cu_seqlens[N] on), in any of dq, dk
+ * [T, H, dk] in_dtype, out [T, H, dv] out_dtype (or dv) and d_log_alpha [T, H] (NULL: not given),
+ * for callers whose buffers are new and may be summed over all rows.  Returns DR_OK,
+ * DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
+ */
+int dr_linrec_zero_rest(const dr_linrec_desc *desc, const int64_t *cu_seqlens, void *dq, void *dk, void *out,
+                        float *d_log_alpha, dr_stream_t stream);
+
+/*
  * One token for B x H chains, the state updated in place: layouts and checks of
  * dr_recurrent_step, without beta (gate NONE or SCALAR).  log_alpha needs 4-byte alignment.
  */

@@ -360,6 +360,27 @@ def test_one_long_sequence_among_many_short(dr, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_new_buffers_hold_zeros_in_rows_of_no_sequence(dr, dtype):
+    """Results that the call allocates can be summed over all rows."""
+    cu = [3, 40, 40, 170]
+    c = cuda(inputs(1, 200, 2, 64, 128, dtype, N=3, seed=2))
+    cuc = torch.tensor(cu, dtype=torch.int64).cuda()
+    for _ in range(3):
+        junk = [torch.full_like(c[n], float("nan")) for n in ("v", "q", "k", "v", "la", "v")]
+        del junk                                        # freed blocks that hold NaN
+        o, _ = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc)
+        g = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)[:4]
+        for x in (o, *g):
+            assert (x[:, :cu[0]] == 0).all() and (x[:, cu[-1]:] == 0).all() and torch.isfinite(x).all()
+    other = torch.float32 if dtype == "bf16" else torch.bfloat16
+    with pytest.raises(dr.DrError):                     # refused before anything is written
+        dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"].to(other), c["ds"], cu_seqlens=cuc)
+    o, _ = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc, out_dtype=other)
+    assert o.dtype == other and (o[:, :cu[0]] == 0).all() and (o[:, cu[-1]:] == 0).all() and torch.isfinite(o).all()
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
@@ -632,3 +653,21 @@ def test_offsets_and_workspace_under_written_buffers_are_refused(dr):
         assert getattr(dr.lib(), f"dr_linrec_{f}_workspace_bytes")(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value > 0
         for x in ns[:-1]:
             assert call(ws=far[x]) == -1 and call(ws=far[x] - n.value // 16 * 16 + 16) == -1, x
+
+
+@no_gpu_only
+def test_zeroing_of_the_rest_refuses_bad_calls(dr):
+    vp = ctypes.c_void_p
+    names = ("cu", "dq", "dk", "out", "dla")
+    far = {n: (i + 1) << 36 for i, n in enumerate(names)}
+
+    def call(desc, **o):
+        p = [vp(o.get(n, far[n])) if o.get(n, 1) is not None else None for n in names]
+        return dr.lib().dr_linrec_zero_rest(ctypes.byref(desc), *p, None)
+
+    d = _desc(dr, B=1, N=3)
+    assert call(_desc(dr)) == -1 and call(_desc(dr, B=1, N=3, dk=96)) == -2          # not packed; not built
+    assert call(d, cu=None) == -1 and call(d, cu=far["cu"] + 4) == -1
+    for n in names[1:]:
+        assert call(d, **{n: far[n] + (2 if n == "dla" else 8)}) == -1 and call(d, cu=far[n]) == -1
+    assert call(_desc(dr, B=1, N=3, T=0)) == 0
