@@ -8,8 +8,9 @@
 //     dx = r g - x r^3 (g . x) / n,    dw = sum over rows of u x r.
 //
 // Angles: f_i enters as turns per position in units of 2^-64 turns (dr_rope_table), so the
-// 64-bit product with the position wraps to the exact fraction of a turn, however far the
-// position; its upper 32 bits go to sincospi in fp32.
+// 64-bit product with the position wraps to the exact fraction of a turn of the table's frequency,
+// however far the position; its upper 32 bits go to sincospi in fp32, which keeps 2^-26 of a turn (1e-7
+// rad).  The table's own 53 bits add at most |position| f_i 2^-52.6 turns.
 //
 // Both directions stream q and k once and are bound by HBM bandwidth.  A row is held by
 // d / 8 lanes with 8 values each, so a warp's accesses are whole rows; a group of lanes takes

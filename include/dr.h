@@ -395,8 +395,11 @@ int dr_linrec_step(const dr_step_desc *desc, const void *q, const void *k, const
  *
  * for the pairs i < rot / 2 of the first rot values: (a, b) = (i, i + rot / 2) in the half
  * layout, (2 i, 2 i + 1) in the interleaved one; p is the row's position, s rot_scale.  The
- * other d - rot values are not rotated.  Statistics are fp32; angles are exact to 2^-31 of a
- * turn at any position (dr_rope_table).
+ * other d - rot values are not rotated.  Statistics are fp32.  Angles: position times table
+ * entry (dr_rope_table) is exact modulo a turn at any position, then rounded to fp32: off by at
+ * most 2^-26 of a turn (1e-7 rad).  A table entry is within 2^-50 of its frequency, which against
+ * f_i itself adds at most |p| f_i 2^-52.6 turns: as much again at |p| = 2^26, below 2^-21 of a turn up
+ * to 2^31, where positions are meant to stay.
  */
 enum { DR_NORM_NONE = 0, DR_NORM_L2 = 1, DR_NORM_RMS = 2 };
 enum { DR_ROPE_HALF = 0, DR_ROPE_INTERLEAVED = 1 };
@@ -434,7 +437,7 @@ int dr_rope_table(int64_t rot, double base, int32_t scaling, double factor, doub
  *   q, k           [n_tok, Hq | Hk, d] dtype, rows q_stride, k_stride apart
  *   wq, wk         NULL (ones) or fp32 [d]; NULL without a norm
  *   table          device copy of dr_rope_table's array (NULL when rot is 0)
- *   positions      NULL or int64 [n_tok] (device), any values
+ *   positions      NULL or int64 [n_tok] (device), any values (angles: above)
  *   q_out, k_out   [n_tok, Hq | Hk, d], rows q_out_stride, k_out_stride apart (written);
  *                  may be q, k themselves, with their strides; no written row shares a
  *                  byte with another or an input otherwise (DR_ERR_INVALID)

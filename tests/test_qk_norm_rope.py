@@ -256,6 +256,24 @@ def test_values_behind_the_rotated_part_pass_through(dr, d, rot, layout, dtype):
         assert torch.equal(y[..., :rot], want[..., :rot])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("top", [1 << 20, 1 << 31, 1 << 44, (1 << 63) - 1])
+def test_angles_are_the_table_times_the_position(dr, top):
+    """The angle is the 64-bit product of position and table entry, whatever the position.  It is
+    cut to 2^-32 of a turn and rounded to fp32 (half a turn at most: 2^-26 of a turn), 2 pi
+    (2^-26 + 2^-32) < 1e-7; sine and cosine add an ulp or two and the products a rounding
+    each, 3 * 2^-23: 2^-21 in all."""
+    gen = torch.Generator().manual_seed(top % 1009)
+    pos = torch.cat([torch.randint(-top, top, (61,), generator=gen), torch.tensor([-top, -1, 0, 1, top])])
+    table = dr.rope_table(64, base=500000.0, device="cpu")
+    x = torch.zeros(len(pos), 1, 64)
+    x[..., :32] = 1
+    y, _ = dr.qk_norm_rope(x.cuda(), None, table.cuda(), positions=pos.cuda(), norm="none")
+    turns = torch.tensor([[(p * t) % (1 << 64) / 2.0 ** 64 for t in table.tolist()] for p in pos.tolist()], dtype=torch.float64)
+    want = torch.cat([(2 * math.pi * turns).cos(), (2 * math.pi * turns).sin()], -1)[:, None]
+    assert (y.double().cpu() - want).abs().max() <= 2.0 ** -21
+
+
 # ---------------------------------------------------------------- without a GPU
 @pytest.mark.parametrize("rot", [0, 16, 64, 128, 256])
 @pytest.mark.parametrize("scaling", SCALINGS)
@@ -267,6 +285,27 @@ def test_table(dr, rot, scaling):
     assert t.shape == (rot // 2,)
     for a, b in zip(t.tolist(), want.tolist()):
         assert abs((a % (1 << 64)) - b) <= 0.5 + 8 * 2.0 ** -53 * b
+
+
+@pytest.mark.parametrize("rot,base", [(64, 10000.0), (128, 500000.0), (256, 1.0000001), (16, 1e12)])
+@pytest.mark.parametrize("scaling", SCALINGS)
+def test_table_against_fifty_digits(dr, rot, base, scaling):
+    """Every frequency within 2^-50 of itself and half a unit of 2^-64 turns."""
+    from decimal import Decimal as D, localcontext
+    with localcontext() as ctx:
+        ctx.prec = 50
+        pi = D("3.14159265358979323846264338327950288419716939937511")
+        got = dr.rope_table(rot, base=base, scaling=scaling, device="cpu").tolist()
+        for i, t in enumerate(got):
+            f = (D(base).ln() * D(-2 * i) / D(rot)).exp()
+            if scaling and scaling["kind"] == "linear":
+                f /= D(scaling["factor"])
+            elif scaling:
+                w = (D(scaling["original"]) * f / (2 * pi) - D(scaling["low"])) / (D(scaling["high"]) - D(scaling["low"]))
+                w = min(D(1), max(D(0), w))
+                f *= w + (1 - w) / D(scaling["factor"])
+            want = f / (2 * pi) * D(2) ** 64
+            assert abs(D(t % (1 << 64)) - want) <= D("0.5") + want / D(2) ** 50
 
 
 @pytest.mark.parametrize("args,status", [
