@@ -381,6 +381,67 @@ def test_new_buffers_hold_zeros_in_rows_of_no_sequence(dr, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("B,T,H,dk,dv", [(3, 4100, 1, 128, 128), (5, 1900, 2, 64, 128), (2, 2049, 3, 128, 64), (7, 1500, 1, 64, 64)])
+def test_batches_whose_sequences_are_cut(dr, B, T, H, dk, dv, gate):
+    """Sequences that start off any segment's boundary, so that some slots stay empty."""
+    n = ctypes.c_size_t(0)
+    desc = _desc(dr, B=B, T=T, H=H, dk=dk, dv=dv, gate=int(gate))
+    assert dr.lib().dr_linrec_fwd_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)) == 0 and n.value > 0
+    d = inputs(B, T, H, dk, dv, "bf16", gate=gate, strength=0.01, seed=T)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], None, d["do"], d["ds"])
+    slack = dla_slack(d, g) if gate else 0.0
+    c = cuda(d)
+    o, f = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"])
+    check(o, out, "bf16", "out")
+    check(f, fin, "f32", "final_state")
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])
+    for x, m in zip(grads, ("dq", "dk", "dv", "dla", "d0")):
+        if m != "dla" or gate:
+            check(x, g[m], "f32" if m in ("dla", "d0") else "bf16", m, slack if m == "dla" else 0.0)
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", [None, [0, 100, 2600, 2600, 4000]])
+def test_cut_sequences_on_streams_and_in_graphs(dr, cu):
+    """Two streams at once, and two captured graphs with a workspace each, replayed on new inputs
+    side by side, at a length whose segments' states pass through the workspace."""
+    N, T = len(cu) - 1 if cu else 1, 4100
+    desc, n = _desc(dr, B=1, T=T, H=2, N=N if cu else 0), ctypes.c_size_t(0)
+    assert dr.lib().dr_linrec_fwd_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)) == 0 and n.value > 0
+    make = lambda seed: cuda(inputs(1, T, 2, 128, 128, "bf16", N=N if cu else 0, strength=0.01, seed=seed))
+    cuc = None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda()
+    run = lambda c, **o: (*dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc, **o),
+                          *dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc, **o))
+    first, second = make(1), make(2)
+    want = run(first), run(second)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [run(c, stream=s) for c, s in zip((first, second), streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    held, graphs, res = [make(3), make(4)], [], []
+    for c in held:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            res.append(run(c))
+    for c, new in zip(held, (first, second)):
+        for m in c:
+            c[m].copy_(new[m])
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(res, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
