@@ -31,7 +31,7 @@
 // 24 bits, D is three products), so the state is an fp32 result.  P and the state operand of R
 // enter as one bf16 each: for the bf16 output they are rounded once more than it is, each by at
 // most half a step (measured 2.3e-3 of the 2-norm, 1.7e-3 from the output's rounding alone).  The
-// log-decay gradient needs more: with Y, R takes the state in two bf16 terms (2^-18), and the
+// log-decay gradient needs more: with Y, R takes the state in two bf16 terms (2^-17), and the
 // intra-chunk part of out.y is summed from the fp32 products X and X2 = Y V^T directly,
 //     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s);
 // measured 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the backward of

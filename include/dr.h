@@ -312,14 +312,27 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *   - B sequences of T tokens, laid out as for dr_chunk_fwd; or (N >= 1, B = 1) N sequences
  *     packed behind one another in the T rows: sequence n has the rows cu_seqlens[n] ..
  *     cu_seqlens[n + 1] - 1.  cu_seqlens is a device array of N + 1 non-decreasing values in
- *     0 .. T (values outside are clamped; the sequences must not share rows); a sequence may
- *     be empty: its state passes through.  Rows of no sequence are neither read for
+ *     0 .. T (values outside are clamped; the sequences must not share rows: where decreasing
+ *     offsets make them, those rows' results are undefined, and no other memory is touched); a
+ *     sequence may be empty: its state passes through.  Rows of no sequence are neither read for
  *     another row's sake nor written.  States are [N, H, dk, dv] (N = B if not packed).
  *   - The first call on a device looks up device addresses: make it before a stream capture.
  *   - log_alpha and d_log_alpha need 4-byte, cu_seqlens 8-byte alignment.
- *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  bf16
- *     problems run in chunks of 64 tokens: there the state in front of a chunk enters the
- *     chunk's outputs with no less than 2^-60 (states and gradients of log_alpha: exactly).
+ *   - Two ways of computing, chosen by types and lengths alone.  bf16 inputs with bf16 results of
+ *     more than 16 tokens (packed: rows in all) run on the tensor cores in chunks of 64 tokens.
+ *     Everything else (fp32 inputs, fp32 results of bf16 inputs, up to 16 tokens) runs token
+ *     by token in fp32 arithmetic, in 15 (many chains) to 100 (few long ones) times the other's time.
+ *   - Precision.  Sums are fp32 everywhere.  On the tensor cores the state's products are exact;
+ *     out, dv, and without a gate dq and dk read the state rounded to one bf16 (dq and dk of a
+ *     gated problem and d_log_alpha: to two, 2^-17), and all but d_log_alpha the scores rounded to
+ *     one: bf16 results are off by 2.4e-3 of their 2-norm, 1.7e-3 of it their own rounding,
+ *     d_log_alpha by 5e-6, states by 5e-7.  Who wants fp32 arithmetic asks for fp32 results
+ *     (forward) or hands in fp32 rows (backward).
+ *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  On the tensor
+ *     cores the state in front of a chunk enters the chunk's results with no less than 2^-60
+ *     (dq, dk of a gated problem, states and d_log_alpha: exactly), and, without a gate's dq
+ *     and dk, sums are held divided by their row's decay within the chunk, 2^-60 at least: results
+ *     beyond 3.4e38 times that, 2.9e20 behind strong decays, overflow.
  *     Inputs of the sequences' rows are otherwise finite; a NaN or infinity may reach every
  *     output of its chunk.  Values in rows of no sequence do not matter.
  */
@@ -336,10 +349,8 @@ typedef struct {
  * Forward.  q, k, v, log_alpha, init_state, out, final_state as for dr_chunk_fwd (final_state
  * may equal init_state); cu_seqlens NULL unless N >= 1.  out overlaps no input or state,
  * final_state no input other than init_state, workspace nothing (DR_ERR_INVALID).
- * Sums are fp32.  fp32 inputs: fp32 arithmetic throughout.  bf16 inputs: the state's products
- * are exact, its sums fp32; out reads the state and the scores in one bf16 term each.
- * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED, DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace rules as for dr_chunk_fwd; its size depends
- * only on the descriptor.
+ * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED, DR_ERR_WORKSPACE or DR_ERR_CUDA.  Workspace
+ * rules as for dr_chunk_fwd; its size depends only on the descriptor.
  */
 int dr_linrec_fwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);
 int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const void *k, const void *v,
@@ -358,8 +369,8 @@ int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const void *k, cons
  * tokens behind t and one inner product of states.  It is 0 where alpha is; where a strong decay
  * makes it small against those terms, it carries their rounding (some 1e-6 of the largest).
  * Written buffers, workspace among them, overlap neither each other nor an input otherwise
- * (DR_ERR_INVALID).  Results do not depend
- * on the order in which the GPU runs its blocks.  Statuses as for dr_linrec_fwd.
+ * (DR_ERR_INVALID).  Results do not depend on the order in which the GPU runs its blocks.
+ * Statuses as for dr_linrec_fwd.
  */
 int dr_linrec_bwd_workspace_bytes(const dr_linrec_desc *desc, size_t *bytes);
 int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const void *k, const void *v,
