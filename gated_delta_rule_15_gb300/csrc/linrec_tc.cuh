@@ -29,13 +29,14 @@
 //
 // Precision.  Products of loaded rows are exact in fp32.  Vt, Kt enter as three bf16 terms (all
 // 24 bits, D is three products), so the state is an fp32 result.  P and the state operand of R
-// enter as one bf16 each: for the bf16 output they are rounded once more than it is, each by at
-// most half a step (measured 2.3e-3 of the 2-norm, 1.7e-3 from the output's rounding alone).  The
-// log-decay gradient needs more: with Y, R takes the state in two bf16 terms (2^-17), and the
-// intra-chunk part of out.y is summed from the fp32 products X and X2 = Y V^T directly,
-//     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s);
-// measured 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the backward of
-// B8 T2048 H16 d128 as it was then).
+// enter as two bf16 terms each (2^-17 of a value at most is lost), so that the bf16 results are off by
+// their own rounding: 1.66e-3 of the 2-norm, as rounding the exact result is.  (One term each: 2.35e-3,
+// and 105 instead of 122 us for the forward of B8 T4096 H16 d128, 273 instead of 289 for the backward at
+// T2048.)  The log-decay gradient, an fp32 result, is the less exact one: the intra-chunk part of out.y is
+// summed from the fp32 products X and X2 = Y V^T directly,
+//     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s),
+// and R's two terms leave 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the
+// backward of B8 T2048 H16 d128 as it was then; tensor memory is full with two).
 // log2 decays are held as a multiple of 2^-10, whose sums over a chunk are exact in fp32, and
 // a remainder, so that a difference of prefix sums is as exact as a single decay whatever
 // lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
@@ -165,6 +166,12 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
 __device__ __forceinline__ uint32_t last_bf16(float2 x) {
     return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
+// Two fp32 values as two bf16 pairs, each rounded to the nearest: 2^-17 of a value at most is lost.
+__device__ __forceinline__ void two_bf16(float2 x, uint32_t &w0, uint32_t &w1) {
+    w0 = pack_bf16(x.x, x.y);
+    x = fma2(make_float2(lo_bf16(w0), hi_bf16(w0)), make_float2(-1.f, -1.f), x);
+    w1 = pack_bf16(x.x, x.y);
+}
 // Largest log2 decay over a chunk for which P's factor 2^(c_r - c_s) is formed as a product of
 // two powers around the chunk's middle, 2^(c_r - c_31) 2^(c_31 - c_s).
 constexpr float kFactorSpan = 60.f;
@@ -181,8 +188,9 @@ struct Layout {
     static constexpr int YS = DOT ? 3 : 0;
     static constexpr uint32_t Y = STAGES * STAGE, Y_STAGE = PV * 8192;
     static constexpr uint32_t KT = Y + YS * Y_STAGE;           // (kDot) Kt's second and third term (the first replaces K)
-    static constexpr uint32_t P = KT + (DOT ? 2 * PK * 8192 : 0);   // two chunks' P
-    static constexpr uint32_t OUT = P + 2 * 8192;            // output staging, PV panels
+    static constexpr uint32_t P = KT + (DOT ? 2 * PK * 8192 : 0);   // two chunks' P, its first term
+    static constexpr int PLS = DOT ? 1 : 2;                  // stages of P's second term
+    static constexpr uint32_t PL = P + 2 * 8192, OUT = PL + PLS * 8192;   // output staging, PV panels
     static constexpr uint32_t SMALL = OUT + PV * 8192;
     // per chunk: c [66] as (multiple of 2^-10, remainder), the last pair's first word for whether
     // P's factors are products; 2^.. factors of R, Kt, P's rows and P's columns [64] each
@@ -193,14 +201,22 @@ struct Layout {
     static constexpr uint32_t TOTAL = BARS + 42 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
     // tensor memory.  kDot: U (X, then O^T) of two chunks, X2, R, D, three terms of the state operand.
-    // Otherwise: X, R + O of two chunks, D, the state operand, three terms of Vt.
-    static constexpr int NU = DOT ? 2 : 1, NR = DOT ? 1 : 2;
-    static constexpr uint32_t TM_X2 = 128, TM_R = DOT ? 192 : 64, TM_D = DOT ? 256 : 192;
+    // Otherwise: X, R + O, D, two terms of the state operand, three of Vt.
+    static constexpr int NU = DOT ? 2 : 1;
+    static constexpr uint32_t TM_X2 = 128, TM_R = DOT ? 192 : 64, TM_D = DOT ? 256 : 128;
     static constexpr int HALVES = DOT ? 1 : 2;               // Kt (Vt) is handed over in this many parts
-    static constexpr uint32_t TM_S = DOT ? 384 : 320, TM_V = 384;   // terms of DK / 2, of 32 columns
-    static_assert(TM_D + DK <= TM_S && (DOT ? TM_S + DK <= 512 : TM_S + DK / 2 <= TM_V), "tensor memory");
+    static constexpr uint32_t TM_S = DOT ? 384 : 256, TM_V = 384;   // terms of DK / 2, of 32 columns
+    static_assert(TM_D + DK <= TM_S && TM_S + DK <= (DOT ? 512 : TM_V), "tensor memory");
 };
 
+// One lane of a whole warp.  The compiler knows that this is one, and takes the operands of the MMAs
+// and copies behind it as they are; behind `lane == 0` it wraps each in a search for equal lanes
+// (forward of B8 T4096 H16 d128 144 us instead of 122).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
+}
 // The rest of a wait that was not over at once: at most *polls more polls (each of 60 cycles at
 // least: a thirtieth of a second in all); then *polls becomes 0 and nobody waits any more.  Few
 // instructions, for the many places that wait, and no call: the register split rules calls out.
@@ -231,7 +247,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap ty,
                     const __grid_constant__ CUtensorMap to, const TcArgs a) {
     using L = Layout<DK, DV, DOT>;
-    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 2 : 1, NU = L::NU, NR = L::NR;
+    constexpr int PK = L::PK, PV = L::PV, NS = 2, NU = L::NU;
     constexpr int kStages = L::STAGES;
     const LinrecPass &p = a.p;
     const int H = p.H, h = (int)(blockIdx.x % H);
@@ -327,7 +343,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
         wait(b_gate + nx % L::GATES, nx / L::GATES);
         wait(b_x + nx % NU, nx / NU);
-        const uint32_t dst = smb + L::P + (nx & 1) * 8192 + row * 128;
+        const uint32_t dst = smb + L::P + (nx & 1) * 8192 + row * 128, low = smb + L::PL + (nx % L::PLS) * 8192 + row * 128;
         const uint32_t xs = tl + 64 * ((uint32_t)nx % NU);
         const float2 ce = gate_c(nx)[64];
         float m = 0.f;
@@ -383,14 +399,22 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     for (int i = 0; i < 16; ++i) m = fmaf(x[i], x2[i], m);
                 }
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    sts128(dst + ((((4 * half + 2 * b + g) ^ row) & 7) << 4), pack_bf16(x[8 * g], x[8 * g + 1]),
-                           pack_bf16(x[8 * g + 2], x[8 * g + 3]), pack_bf16(x[8 * g + 4], x[8 * g + 5]),
-                           pack_bf16(x[8 * g + 6], x[8 * g + 7]));
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t w[2][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) two_bf16(make_float2(x[8 * g + 2 * i], x[8 * g + 2 * i + 1]), w[0][i], w[1][i]);
+                    const uint32_t at = (((4 * half + 2 * b + g) ^ row) & 7) << 4;
+                    sts128(dst + at, w[0][0], w[0][1], w[0][2], w[0][3]);
+                    sts128(low + at, w[1][0], w[1][1], w[1][2], w[1][3]);
+                }
             }
         } else {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) sts128(dst + ((((4 * half + g) ^ row) & 7) << 4), 0, 0, 0, 0);
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t at = (((4 * half + g) ^ row) & 7) << 4;
+                sts128(dst + at, 0, 0, 0, 0);
+                sts128(low + at, 0, 0, 0, 0);
+            }
         }
         if (DOT) reinterpret_cast<float *>(sm + L::DOTS)[((nx % 3) * 2 + half) * 64 + row] = m;
         fence_proxy_async();
@@ -423,12 +447,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     for (int i = 0; i < 4; ++i) {
                         float2 x = S[4 * b + i];
                         // (opaque, so that no term is computed ahead and kept: 550 bytes of spills)
-                        if (NS > 1) asm volatile("" : "+f"(x.x), "+f"(x.y));
-                        w[0][i] = pack_bf16(x.x, x.y);   // to the nearest
-                        if (NS > 1) {
-                            x = fma2(make_float2(lo_bf16(w[0][i]), hi_bf16(w[0][i])), make_float2(-1.f, -1.f), x);
-                            w[NS - 1][i] = pack_bf16(x.x, x.y);
-                        }
+                        asm volatile("" : "+f"(x.x), "+f"(x.y));
+                        two_bf16(x, w[0][i], w[1][i]);
                     }
 #pragma unroll
                     for (int t = 0; t < NS; ++t) tmem_st4u(tl + L::TM_S + t * (DK / 2) + (i0 + 8 * b) / 2, w[t]);
@@ -613,7 +633,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(b_kt + L::HALVES - 1);
             if (DOT && quarter < 2) {
-                if (it > 1) wait(b_o + (it & 1), (it - 2) >> 1);   // P of two chunks before is read
+                if (it > 0) wait(b_o + ((it - 1) & 1), (it - 1) >> 1);   // P of the chunk before is read
                 build_p(it, quarter, half);
             }
             if (lane == 0) mbar_arrive(b_gfree + it % L::GATES);
@@ -627,7 +647,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll 1
         for (int it = DOT ? 0 : -1; outputs && it < chunks; ++it) {
             if (!DOT && quarter < 2 && it + 1 < chunks) build_p(it + 1, quarter, half);
-            if (it < 0) continue;   // (P of two chunks before is read: its output was waited for)
+            if (it < 0) continue;   // (both terms of P of two chunks before are read: its output was waited for)
             const int cnt = count_of(it);
             if (et == 0) bulk_wait_read_all();   // the staging has left
             named_sync(1, 32 * kOutWarps);
@@ -654,7 +674,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const int ch = 32 * quarter + 16 * g + 8 * ((lane >> 3) & 1);
                     const uint32_t mat = (ch >> 6) * 8192 + tok * 128 + ((((ch >> 3) ^ tok) & 7) << 4);
                     float r[16], o[16];
-                    tmem_ld_frag32(tl + lanes + L::TM_R + 64 * ((uint32_t)it % NR) + 32 * half, r);
+                    tmem_ld_frag32(tl + lanes + L::TM_R + 32 * half, r);
                     if (DOT) tmem_ld_frag32(tl + lanes + 64 * ((uint32_t)it % NU) + 32 * half, o);
                     tmem_wait_ld();
 #pragma unroll
@@ -720,7 +740,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         fewer_regs<kIssueRegs>();
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- loads
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint32_t bytes = 8192u * (outputs ? 2 * PK + PV : PK + PV);
                 int issued = 0;   // chunks whose loads were issued; none after an expiry
 #pragma unroll 1
@@ -827,7 +847,8 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (a.sums && lane == 0) a.seg_decay[slot * H + h] = total;
         } else {
             // ---------------------------------------------------------------- MMA issue
-            if (lane == 0 && chunks > 0 && ((outputs && warp == kScoreWarp) || warp == kUpdateWarp)) {
+            const int role = __shfl_sync(0xffffffffu, warp, 0);
+            if (chunks > 0 && ((outputs && role == kScoreWarp) || role == kUpdateWarp) && elect_one()) {
                 constexpr uint32_t ID_KK = idesc_bf16(128, 64, false, false), ID_MK = idesc_bf16(128, 64, true, false),
                                    ID_MM = idesc_bf16(128, DK, DOT, true);
                 const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);              // K-major
@@ -883,7 +904,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     mma_commit(part + 1 < L::HALVES ? b_d1 : b_d);
                 };
                 auto read_out = [&](int it) {
-                    const uint32_t st = at_stage(it), r = tm + L::TM_R + 64 * ((uint32_t)it % NR);
+                    const uint32_t st = at_stage(it), r = tm + L::TM_R;
 #pragma unroll 1
                     for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
                         const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
@@ -894,13 +915,16 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     mma_commit(b_r);
                     if (!DOT) wait(b_p + (it & 1), it >> 1);
                     // without Y, onto R
-                    steps(0, 4, DOT ? u_of(it) : r, desc_add(dV, st + L::V0), 2048, desc_add(dK, L::P + (it & 1) * 8192), 32, ID_MK, !DOT);
+#pragma unroll 1
+                    for (int t = 0; t < 2; ++t)
+                        four(DOT ? u_of(it) : r, desc_add(dV, st + L::V0), 2048,
+                             desc_add(dK, t == 0 ? L::P + (it & 1) * 8192 : L::PL + (it % L::PLS) * 8192), 32, ID_MK, !DOT || t > 0);
                     mma_commit(b_o + (it & 1));
                 };
                 auto read = [&](int it) {   // R and O of the chunk are read
                     if (it >= 0) wait(b_oread + (it & 3), it >> 2);
                 };
-                if (warp == kScoreWarp) {
+                if (role == kScoreWarp) {
                     for (int it = 0; it < chunks; ++it) {
                         if (DOT) read(it - NU);
                         if (it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X, X2 are read
@@ -921,7 +945,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             update(it, 1);
                         }
                         if (outputs) {
-                            read(it - NR);
+                            read(it - 1);
                             if (DOT) wait(b_p + (it & 1), it >> 1);
                             wait(b_s, it);
                             read_out(it);

@@ -322,17 +322,15 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *     more than 16 tokens (packed: rows in all) run on the tensor cores in chunks of 64 tokens.
  *     Everything else (fp32 inputs, fp32 results of bf16 inputs, up to 16 tokens) runs token
  *     by token in fp32 arithmetic, in 15 (many chains) to 100 (few long ones) times the other's time.
- *   - Precision.  Sums are fp32 everywhere.  On the tensor cores the state's products are exact;
- *     out, dv, and without a gate dq and dk read the state rounded to one bf16 (dq and dk of a
- *     gated problem and d_log_alpha: to two, 2^-17), and all but d_log_alpha the scores rounded to
- *     one: bf16 results are off by 2.4e-3 of their 2-norm, 1.7e-3 of it their own rounding,
- *     d_log_alpha by 5e-6, states by 5e-7.  Who wants fp32 arithmetic asks for fp32 results
- *     (forward) or hands in fp32 rows (backward).
+ *   - Precision.  Sums are fp32 everywhere.  On the tensor cores the state's products are exact,
+ *     and scores and states are read out as two bf16 terms (2^-17 of a value at most is lost): bf16
+ *     results are off by their own rounding, d_log_alpha by 5e-6 of its 2-norm, states by 5e-7.
+ *     Who wants fp32 arithmetic asks for fp32 results (forward) or hands in fp32 rows (backward).
  *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  On the tensor
  *     cores the state in front of a chunk enters the chunk's results with no less than 2^-60
  *     (dq, dk of a gated problem, states and d_log_alpha: exactly), and, without a gate's dq
  *     and dk, sums are held divided by their row's decay within the chunk, 2^-60 at least: results
- *     beyond 3.4e38 times that, 2.9e20 behind strong decays, overflow.
+ *     beyond 3.4e38 times that, 2.9e20 behind strong decays, overflow (infinity or NaN).
  *     Inputs of the sequences' rows are otherwise finite; a NaN or infinity may reach every
  *     output of its chunk.  Values in rows of no sequence do not matter.
  */

@@ -442,6 +442,27 @@ def test_cut_sequences_on_streams_and_in_graphs(dr, cu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("strength", [0.1, 5.0, None])
+@pytest.mark.parametrize("T,dk,dv,cu", [(700, 128, 128, None), (2100, 64, 128, None), (900, 128, 64, [0, 130, 131, 890])])
+def test_bf16_results_are_rounded_once(dr, T, dk, dv, cu, strength):
+    """Off by their own rounding, 2^-8 of the value, and what an fp32 result is off by: scores and
+    states that enter as two bf16 terms lose 2^-17 each, 6 sqrt(2) 2^-17 / sqrt(3) = 3.8e-5 of the row's RMS
+    at the worst element's six standard deviations, beside the 2.5e-4 of fp32 sums."""
+    N = len(cu) - 1 if cu else 0
+    d = inputs(1, T, 2, dk, dv, "bf16", gate=strength is not None, N=N, strength=strength or 0.0, seed=T)
+    out, fin, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], cu, d["do"], d["ds"])
+    c, cuc = cuda(d), None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda()
+    o, _ = dr.linrec_fwd(c["q"], c["k"], c["v"], c["la"], c["s0"], cu_seqlens=cuc)
+    grads = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"], cu_seqlens=cuc)
+    for x, ref, n in ((o, out, "out"), *((y, g[m], m) for y, m in zip(grads, ("dq", "dk", "dv")))):
+        there = ~torch.isnan(ref)
+        rms = ref.square().mean(-1, keepdim=True).sqrt().expand(ref.shape)
+        bound = 2.0 ** -8 * ref.abs() + (F32_TOL + 3.8e-5) * torch.maximum(rms, ref.abs())
+        assert (((x.double().cpu() - ref).abs() / bound)[there] <= 1).all(), n
+    assert dr.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
