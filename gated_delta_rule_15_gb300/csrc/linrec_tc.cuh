@@ -28,15 +28,17 @@
 // and Kt is made in shared memory, its first term in K's place.
 //
 // Precision.  Products of loaded rows are exact in fp32.  Vt, Kt enter as three bf16 terms (all
-// 24 bits, D is three products), so the state is an fp32 result.  P and the state operand of R
-// enter as two bf16 terms each (2^-17 of a value at most is lost), so that the bf16 results are off by
+// 24 bits, D is three products), so the state is an fp32 result.  P and, without Y, the state operand
+// of R enter as two bf16 terms each (2^-17 of a value at most is lost), so that the bf16 results are off by
 // their own rounding: 1.66e-3 of the 2-norm, as rounding the exact result is.  (One term each: 2.35e-3,
-// and 105 instead of 122 us for the forward of B8 T4096 H16 d128, 273 instead of 289 for the backward at
-// T2048.)  The log-decay gradient, an fp32 result, is the less exact one: the intra-chunk part of out.y is
-// summed from the fp32 products X and X2 = Y V^T directly,
-//     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s),
-// and R's two terms leave 5e-6 of its 2-norm (three terms: 1.2e-6, and 350 instead of 303 us for the
-// backward of B8 T2048 H16 d128 as it was then; tensor memory is full with two).
+// and 105 instead of 121 us for the forward of B8 T4096 H16 d128, 273 instead of 289 for the backward at
+// T2048.)  The log-decay gradient is an fp32 result: with Y, R takes the state in three terms, the third
+// over the place of X2 once that is read, and the intra-chunk part of out.y is summed from the fp32
+// products X and X2 = Y V^T directly,
+//     out_r.y_r (without the row's own term) = f_r R_r.y_r + sum_{s != r} P_rs (y_r.v_s);
+// it is 0.5e-6 to 0.9e-6 off in the 2-norm (two terms: 5e-6 to 6e-6, backward 289 instead of 304 us).  Terms are
+// accumulated from the small one to the large one, since what the tensor core cuts off a sum goes by
+// the sum's size (the other way round 0.8e-6 to 1.4e-6, and states 5e-7 instead of 3e-7).
 // log2 decays are held as a multiple of 2^-10, whose sums over a chunk are exact in fp32, and
 // a remainder, so that a difference of prefix sums is as exact as a single decay whatever
 // lies between (log alpha is taken as at least -120: exp(-120) is 0 in fp32, which makes -inf a full
@@ -200,7 +202,8 @@ struct Layout {
     static constexpr uint32_t BARS = DOTS + (DOT ? (DOT_S + 8) * 4 : 0);
     static constexpr uint32_t TOTAL = BARS + 42 * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024 && KT % 1024 == 0 && SMALL % 16 == 0 && BARS % 8 == 0, "layout");
-    // tensor memory.  kDot: U (X, then O^T) of two chunks, X2, R, D, three terms of the state operand.
+    // tensor memory.  kDot: U (X, then O^T) of two chunks, X2 (then the state operand's third term), R, D,
+    // the other two terms of the state operand.
     // Otherwise: X, R + O, D, two terms of the state operand, three of Vt.
     static constexpr int NU = DOT ? 2 : 1;
     static constexpr uint32_t TM_X2 = 128, TM_R = DOT ? 192 : 64, TM_D = DOT ? 256 : 128;
@@ -247,7 +250,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap ty,
                     const __grid_constant__ CUtensorMap to, const TcArgs a) {
     using L = Layout<DK, DV, DOT>;
-    constexpr int PK = L::PK, PV = L::PV, NS = 2, NU = L::NU;
+    constexpr int PK = L::PK, PV = L::PV, NS = DOT ? 3 : 2, NU = L::NU;
     constexpr int kStages = L::STAGES;
     const LinrecPass &p = a.p;
     const int H = p.H, h = (int)(blockIdx.x % H);
@@ -269,14 +272,15 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     uint64_t *b_load = bars, *b_free = bars + 3;   // [kStages] rows are there, are done with
     uint64_t *b_gate = bars + 6, *b_gfree = bars + 10;   // [GATES] the same of the gates
-    uint64_t *b_x = bars + 14;         // [NU] X (and X2) of a chunk is there
+    uint64_t *b_x = bars + 14;         // [NU] X of a chunk is there
+    uint64_t *b_x2 = bars + 16;        // X2 is there
     uint64_t *b_kt = bars + 17;        // [HALVES] Kt (rows 0..31, 32..63) is built
     uint64_t *b_p = bars + 19;         // [2] P is built, X and X2 are read
     uint64_t *b_d = bars + 21;         // D is there
     uint64_t *b_d1 = bars + 23;        // D has taken Kt's first half
     uint64_t *b_dread = bars + 24;     // D is read
     uint64_t *b_s = bars + 26;         // the state operand is there
-    uint64_t *b_r = bars + 27;         // R is there: the state operand may be replaced
+    uint64_t *b_r = bars + 27;         // R is there: the state operand (and its third term by X2) may be replaced
     uint64_t *b_o = bars + 28;         // [2] R and O are there
     uint64_t *b_oread = bars + 30;     // [4] R and O are read
     uint64_t *b_end = bars + 34;       // every MMA is done
@@ -301,6 +305,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             mbar_init(b_gfree + i, kStateWarps + kBuildWarps + (outputs ? kOutWarps : 0));
         }
         for (int i = 0; i < NU; ++i) mbar_init(b_x + i, 1);
+        mbar_init(b_x2, 1);
         for (int i = 0; i < L::HALVES; ++i) mbar_init(b_kt + i, kBuildWarps);
         mbar_init(b_d1, 1);
         for (int i = 0; i < 2; ++i) mbar_init(b_p + i, 4);
@@ -343,6 +348,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), smb = smem_u32(sm);
         wait(b_gate + nx % L::GATES, nx / L::GATES);
         wait(b_x + nx % NU, nx / NU);
+        if (DOT) wait(b_x2, nx);
         const uint32_t dst = smb + L::P + (nx & 1) * 8192 + row * 128, low = smb + L::PL + (nx % L::PLS) * 8192 + row * 128;
         const uint32_t xs = tl + 64 * ((uint32_t)nx % NU);
         const float2 ce = gate_c(nx)[64];
@@ -438,23 +444,46 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i)
             S[i] = init && mine ? make_float2(init[at(2 * i)], init[at(2 * i + 1)]) : make_float2(0.f, 0.f);
-        auto put_operand = [&]() {   // S^T as NS bf16 terms
+        auto put_operand = [&](int it) {   // S^T as two bf16 terms, with Y as three
             if (mine) {
 #pragma unroll
                 for (int b = 0; b < NV / 8; ++b) {
-                    uint32_t w[NS][4];
+                    uint32_t w[2][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float2 x = S[4 * b + i];
                         // (opaque, so that no term is computed ahead and kept: 550 bytes of spills)
                         asm volatile("" : "+f"(x.x), "+f"(x.y));
-                        two_bf16(x, w[0][i], w[1][i]);
+                        if (DOT) {   // truncated: with the third all 24 bits
+                            w[0][i] = take_bf16(x);
+                            w[1][i] = last_bf16(x);
+                        } else {
+                            two_bf16(x, w[0][i], w[1][i]);
+                        }
                     }
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) tmem_st4u(tl + L::TM_S + t * (DK / 2) + (i0 + 8 * b) / 2, w[t]);
+                    for (int t = 0; t < 2; ++t) tmem_st4u(tl + L::TM_S + t * (DK / 2) + (i0 + 8 * b) / 2, w[t]);
                 }
-                tmem_wait_st();
             }
+            if (DOT) {   // the third term goes over X2, which P's warps have read
+                wait(b_p + (it & 1), it >> 1);
+                if (mine) {
+#pragma unroll
+                    for (int b = 0; b < NV / 8; ++b) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float2 x = S[4 * b + i];
+                            asm volatile("" : "+f"(x.x), "+f"(x.y));
+                            take_bf16(x);
+                            take_bf16(x);
+                            w[i] = last_bf16(x);
+                        }
+                        tmem_st4u(tl + L::TM_X2 + (i0 + 8 * b) / 2, w);
+                    }
+                }
+            }
+            if (mine) tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_s);
@@ -472,7 +501,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int it = 0; it < chunks; ++it) {
             if (outputs) {
                 if (it > 0) wait(b_r, it - 1);
-                put_operand();
+                put_operand(it);
             }
             wait(b_gate + it % L::GATES, it / L::GATES);
             const float2 ce = gate_c(it)[64], cl = gate_c(it)[63];
@@ -874,52 +903,55 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                         const uint32_t o = st + b * L::QK_STEP;
                         four(u_of(it), desc_add(dK, o + L::Q0), 32, desc_add(dK, o + L::K0), 32, ID_KK, b > 0);
                     }
-                    if (DOT) {
-#pragma unroll 1
-                        for (int b = 0; b < PV; ++b) {
-                            four(tm + L::TM_X2, desc_add(dK, L::Y + (uint32_t)(it % 3) * L::Y_STAGE + b * 8192), 32,
-                                 desc_add(dK, st + L::V0 + b * L::V_STEP), 32, ID_KK, b > 0);
-                        }
-                    }
                     mma_commit(b_x + it % NU);
-                    if (DOT) mma_commit(b_yfree + it % 3);
+                };
+                auto scores2 = [&](int it) {
+                    const uint32_t st = at_stage(it);
+#pragma unroll 1
+                    for (int b = 0; b < PV; ++b) {
+                        four(tm + L::TM_X2, desc_add(dK, L::Y + (uint32_t)(it % 3) * L::Y_STAGE + b * 8192), 32,
+                             desc_add(dK, st + L::V0 + b * L::V_STEP), 32, ID_KK, b > 0);
+                    }
+                    mma_commit(b_x2);
+                    mma_commit(b_yfree + it % 3);
                 };
                 auto update = [&](int it, int part) {   // part: of Kt's rows
                     const uint32_t st = at_stage(it);
                     constexpr int KN = 4 / L::HALVES;
 #pragma unroll 1
-                    for (int t = 0; t < 3; ++t) {
+                    for (int t = 2; t >= 0; --t) {
                         if (!DOT) {   // Vt from tensor memory, K as loaded
                             const uint64_t dk = desc_add(dT0, st + L::K0 + part * KN * 2048);
 #pragma unroll
                             for (int ks = 0; ks < KN; ++ks)
                                 mma_bf16_ts(tm + L::TM_D, tm + L::TM_V + 32 * t + 8 * (part * KN + ks), desc_add(dk, ks * 2048), ID_MM,
-                                            part + t + ks > 0);
+                                            part > 0 || t < 2 || ks > 0);
                             continue;
                         }
                         steps(part * KN, KN, tm + L::TM_D, desc_add(dV, st + L::V0), 2048,
                               t == 0 ? desc_add(dT0, st + L::K0) : desc_add(dT, L::KT + (t - 1) * PK * 8192),
-                              2048, ID_MM, part + t > 0);
+                              2048, ID_MM, part > 0 || t < 2);
                     }
                     mma_commit(part + 1 < L::HALVES ? b_d1 : b_d);
                 };
-                auto read_out = [&](int it) {
-                    const uint32_t st = at_stage(it), r = tm + L::TM_R;
+                auto read_state = [&](int it) {
+                    const uint32_t st = at_stage(it);
+                    // small terms first: what the tensor core cuts off a sum goes by the sum's size
 #pragma unroll 1
-                    for (int b = 0; b < NS * PK; ++b) {   // terms of the state operand behind one another
+                    for (int b = NS * PK - 1; b >= 0; --b) {
                         const uint64_t dq = desc_add(dK, st + L::Q0 + (PK == 2 ? (b & 1) * L::QK_STEP : 0));
+                        const uint32_t s = tm + 32 * b + (DOT && b >= 2 * PK ? L::TM_X2 - 64 * PK : L::TM_S);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16_ts(r, tm + L::TM_S + 32 * b + 8 * ks, desc_add(dq, ks * 32), ID_KK, b + ks > 0);
+                            mma_bf16_ts(tm + L::TM_R, s + 8 * ks, desc_add(dq, ks * 32), ID_KK, b < NS * PK - 1 || ks > 0);
                     }
                     mma_commit(b_r);
-                    if (!DOT) wait(b_p + (it & 1), it >> 1);
-                    // without Y, onto R
+                };
+                auto read_scores = [&](int it) {   // without Y, onto R
 #pragma unroll 1
-                    for (int t = 0; t < 2; ++t)
-                        four(DOT ? u_of(it) : r, desc_add(dV, st + L::V0), 2048,
-                             desc_add(dK, t == 0 ? L::P + (it & 1) * 8192 : L::PL + (it % L::PLS) * 8192), 32, ID_MK, !DOT || t > 0);
-                    mma_commit(b_o + (it & 1));
+                    for (int t = 1; t >= 0; --t)
+                        four(DOT ? u_of(it) : tm + L::TM_R, desc_add(dV, at_stage(it) + L::V0), 2048,
+                             desc_add(dK, t == 0 ? L::P + (it & 1) * 8192 : L::PL + (it % L::PLS) * 8192), 32, ID_MK, !DOT || t == 0);
                 };
                 auto read = [&](int it) {   // R and O of the chunk are read
                     if (it >= 0) wait(b_oread + (it & 3), it >> 2);
@@ -927,10 +959,16 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 if (role == kScoreWarp) {
                     for (int it = 0; it < chunks; ++it) {
                         if (DOT) read(it - NU);
-                        if (it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X, X2 are read
+                        if (!DOT && it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);   // X is read
                         wait(b_load + it % kStages, it / kStages);
-                        if (DOT) wait(b_y + it % 3, it / 3);
                         scores(it);
+                        if (DOT) {
+                            // X2, and what R took over its place, are read
+                            if (it > 0) wait(b_p + ((it - 1) & 1), (it - 1) >> 1);
+                            if (it > 0) wait(b_r, it - 1);
+                            wait(b_y + it % 3, it / 3);
+                            scores2(it);
+                        }
                     }
                 } else {
                     // D first: the next chunk's Kt waits for it
@@ -946,9 +984,11 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                         }
                         if (outputs) {
                             read(it - 1);
-                            if (DOT) wait(b_p + (it & 1), it >> 1);
-                            wait(b_s, it);
-                            read_out(it);
+                            wait(b_s, it);   // (with Y behind P)
+                            read_state(it);
+                            wait(b_p + (it & 1), it >> 1);
+                            read_scores(it);
+                            mma_commit(b_o + (it & 1));
                         }
                         mma_commit(b_free + it % kStages);
                     }

@@ -324,7 +324,7 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *     by token in fp32 arithmetic, in 15 (many chains) to 100 (few long ones) times the other's time.
  *   - Precision.  Sums are fp32 everywhere.  On the tensor cores the state's products are exact,
  *     and scores and states are read out as two bf16 terms (2^-17 of a value at most is lost): bf16
- *     results are off by their own rounding, d_log_alpha by 5e-6 of its 2-norm, states by 5e-7.
+ *     results are off by their own rounding, d_log_alpha (three terms) by 1e-6 of its 2-norm, states by 3e-7.
  *     Who wants fp32 arithmetic asks for fp32 results (forward) or hands in fp32 rows (backward).
  *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  On the tensor
  *     cores the state in front of a chunk enters the chunk's results with no less than 2^-60

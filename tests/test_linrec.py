@@ -463,6 +463,21 @@ def test_bf16_results_are_rounded_once(dr, T, dk, dv, cu, strength):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,T,dk,dv", [(2, 1024, 128, 128), (3, 700, 64, 128), (2, 900, 128, 64), (4, 515, 64, 64)])
+def test_log_decay_gradient_of_bf16_rows_is_an_fp32_result(dr, B, T, dk, dv):
+    """In the 2-norm.  A token's two terms are sums in dk / 16 (dv / 16) <= 8 tensor-core steps on the large
+    operand term, each of which cuts off less than 2^-23 of the sum so far: below 2^-20 = 9.6e-7, of one
+    sign, and the states in them carry 3e-7; sums of such terms keep the relative size.  The random
+    part, 2 u of each of up to 512 terms, stands against a gradient of the size of the decay's memory,
+    some 20 terms: sqrt(512 / 20) 2 u = 6e-7.  1.9e-6 in all."""
+    d = inputs(B, T, 2, dk, dv, "bf16", seed=T)
+    _, _, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], None, d["do"], d["ds"])
+    c = cuda(d)
+    dla = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])[3].double().cpu()
+    assert (dla - g["dla"]).norm() <= 1.9e-6 * g["dla"].norm()
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
