@@ -13,7 +13,7 @@ namespace {
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     const char *a0 = (const char *)a, *b0 = (const char *)b;
-    return a && b && a0 < b0 + nb && b0 < a0 + na;
+    return a && b && na && nb && a0 < b0 + nb && b0 < a0 + na;
 }
 
 int check_desc(const dr_linrec_desc *d) {

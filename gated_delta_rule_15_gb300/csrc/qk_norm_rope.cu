@@ -430,7 +430,7 @@ struct Block {
 };
 bool meet(const Block &a, const Block &b) {
     const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
-    return a.p && b.p && a0 < b0 + b.bytes && b0 < a0 + a.bytes;
+    return a.p && b.p && a.bytes && b.bytes && a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 // Whether a row shares a byte with the block, which may lie between two rows.
 bool meet(const Rows &a, const Block &b, int64_t n_tok, int64_t e) {

@@ -768,3 +768,20 @@ def test_zeroing_of_the_rest_refuses_bad_calls(dr):
     for n in names[1:]:
         assert call(d, **{n: far[n] + (2 if n == "dla" else 8)}) == -1 and call(d, cu=far[n]) == -1
     assert call(_desc(dr, B=1, N=3, T=0)) == 0
+
+
+@no_gpu_only
+def test_unused_workspaces_and_empty_inputs_overlap_nothing(dr):
+    """What a call neither reads nor writes may lie anywhere: a workspace of which it needs no byte, rows
+    of no token.  (Without a GPU a call that passes its checks ends in DR_ERR_CUDA.)"""
+    vp = ctypes.c_void_p
+    names = ("q", "k", "v", "la", "cu", "s0", "out", "fin", "ws")
+    far = {n: (i + 1) << 36 for i, n in enumerate(names)}
+
+    def fwd(desc, **o):
+        return dr.lib().dr_linrec_fwd(ctypes.byref(desc), *[vp(o.get(n, far[n])) for n in names], 1 << 40, None)
+
+    d = _desc(dr, in_dtype=dr.DR_F32, out_dtype=dr.DR_F32)
+    for n in names[:-1]:
+        assert fwd(d, ws=far[n] + 256) == dr.DR_ERR_CUDA, n
+    assert fwd(_desc(dr, T=0), q=far["fin"] + 256, v=far["s0"] + 256) == dr.DR_ERR_CUDA
