@@ -22,8 +22,8 @@ using umma::mul2;
 // 0.2 us (128 x 128).
 // Rows come by asynchronous copies, a tile ahead.
 // kGroup tokens' read-outs are summed over the lanes at a time; kTile tokens (kAnchor is a multiple) are staged
-// in shared memory, of which 48 KB hold two tiles.  One chain of 256 tokens of 64 x 64 / 128 x 128, us: 47 / 65
-// with 8 and 4, 37 / 58 with 16 and 4, 47 / 57 with 8 and 8, 37 / 51 with 16 and 8.
+// in shared memory, of which 48 KB hold two tiles.  One fp32 chain of 256 tokens of 64 x 64 / 128 x 128, us on
+// the GPU, by kTile and kGroup: 8 and 4 48 / 65, 16 and 4 37 / 57, 8 and 8 46 / 57, 16 and 8 37 / 50.
 constexpr int kGroup = 8;
 template <typename Tin, int DK, bool DOT> constexpr int kTileOf = DK == 128 && sizeof(Tin) == 4 && DOT ? 8 : 16;
 

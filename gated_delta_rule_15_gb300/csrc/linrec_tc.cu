@@ -79,10 +79,9 @@ int dispatch(const CUtensorMap *m, const TcArgs &a, bool dot, unsigned grid, cud
 // chain's last segment, and the cut costs about eight chunks' time in launches.
 // Packed sequences: their lengths are on the device.  Segments of half an SM's share of
 // all rows, 512 tokens at least, keep one long sequence from holding up the rest; shorter
-// sequences stay whole.  Forward / backward of 20011 rows x 8 heads of 64 in 23 sequences (longest 4077)
-// and of 16384 x 4 of 128 in 3 (11512), us, by the least segment: 256 tokens 87 / 282 and 64 / 248,
-// 512 87 / 283 and 49 / 183, 1024 90 / 298 and 65 / 246, 2048 108 / 351 and 104 / 386 (512 with the
-// present search for a block's sequence: 78 / 259 and 49 / 182).
+// sequences stay whole.  Forward / backward of 20011 rows x 8 heads of 64 in 23 sequences (longest 4608)
+// and of 16384 x 4 of 128 in 3 (11512), us on the GPU, by the least segment: 256 tokens 69 / 244 and
+// 56 / 254, 512 69 / 244 and 40 / 179, 1024 76 / 263 and 57 / 247, 2048 107 / 363 and 96 / 401.
 int64_t segment_tokens(const LinrecSeqs &s, int64_t H) {
     const int64_t whole = (s.total / kAnchor + 1) * kAnchor, per = kAnchor / linrec::kChunk;
     if (s.cu) {
@@ -115,11 +114,11 @@ int64_t state_slots(const LinrecSeqs &s, int64_t seg) {
 }  // namespace
 
 bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_bf16) {
-    // Up to 16 tokens the token recurrence is faster (forward / backward, us: one chain of 64 x 64, T 16,
-    // 5.2 / 19.9 against 6.7 / 24.2; 1024 chains of 128 x 128, 53.6 / 179 against 63.0 / 230), from 32
-    // on the chunks are, but for many short chains of 64 x 64 (one chain, T 32, 8.5 / 32.3 against 6.7 /
-    // 24.2; 1024 chains of 128 x 128, 95.6 / 325 against 62.9 / 232).  Packed sequences go by all
-    // their rows, which may be one sequence's.
+    // Up to 16 tokens the token recurrence is faster (forward / backward, us on the GPU: T 16, one chain of
+    // 64 x 64 4.8 / 16.9 against 6.5 / 22.8; 1024 chains of 128 x 128 51.8 / 164 against 54.4 / 186), from 32
+    // on the chunks are, but for many short chains of 64 x 64 (T 32, one chain 8.0 / 27.0 against 6.7 /
+    // 23.5; 1024 chains of 128 x 128 92.9 / 305 against 55.1 / 190, of 64 x 64 27.3 / 96.0 against 47.1 / 161).
+    // Packed sequences go by all their rows, which may be one sequence's.
     return in_bf16 && out_bf16 && (s.cu ? s.total : s.T) > 16 && s.total < ((int64_t)1 << 31) - 64 &&
            segment_slots(s, segment_tokens(s, H)) * H < ((int64_t)1 << 31);
 }

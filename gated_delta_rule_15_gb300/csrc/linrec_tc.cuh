@@ -52,18 +52,18 @@
 // small kernel chains them (the transition is the scalar 2^(sum c)), a second launch runs all
 // segments from their true start states.
 //
-// What bounds it (B8 T4096 H16 d128, 128 CTAs of 64 chunks, 112 us, 72 % of the copy bandwidth's
-// floor): the per-chunk work of 28 warps on an SM, about 7,300 warp instructions in 3,400 cycles,
-// 67 % issue on the SMs in use.  What it took to get there, each step as measured: 182 us with
-// eight warps for everything behind the state; 160 with MMAs issued by three threads instead of
-// one that waits for them in turn; 141 with less code in the loop (the SM's instruction cache
-// missed 16 % and the GPC's, which all its SMs share, ran at 76 % of its rate: rolled loops, fp32
-// gate scan); 131 with building and output on warps of their own; 117 with Vt in tensor memory
+// What bounds it (B8 T4096 H16 d128, 128 CTAs of 64 chunks, 121 us, 67 % of the copy bandwidth's
+// floor): the per-chunk work of 28 warps on an SM, about 8,500 warp instructions in 3,700 cycles,
+// 74 % issue on the SMs in use.  What it took to get there, each step as measured (with one term of P
+// and of the state): 182 us with eight warps for everything behind the state; 160 with MMAs issued by
+// three threads instead of one that waits for them in turn; 141 with less code in the loop (the SM's
+// instruction cache missed 16 % and the GPC's, which all its SMs share, ran at 76 % of its rate: rolled
+// loops, fp32 gate scan); 131 with building and output on warps of their own; 117 with Vt in tensor memory
 // (with Kt in shared memory the chunk moves 336 KB through it, 2,690 cycles at 128 bytes); 112
-// with shorter waits.  The form with Y runs 5,800 cycles a chunk (6,300 before the gates had a
-// warp of their own): a stage's tiles take 4,400 cycles from their request to their arrival, X,
-// Kt and P, O another 7,200, and shared memory holds two stages; its loop is larger, too, and Kt
-// and the state operand cost more instructions.
+// with shorter waits; 105 with MMAs issued by an elected lane.  The form with Y runs 14,200 instructions
+// in 6,600 cycles a chunk, 67 % issue: a stage's tiles take 4,400 cycles from their request to their
+// arrival, shared memory holds two stages, and its loop is larger (the SM's instruction cache misses
+// 15 %, the GPC's runs at 84 % of its rate).
 //
 // A sequence's last chunk may hold rows of the next sequence or none: rows behind the end are
 // zeroed in shared memory, Vt, Kt and P are built as zero there, and the outputs leave by
@@ -214,7 +214,7 @@ struct Layout {
 
 // One lane of a whole warp.  The compiler knows that this is one, and takes the operands of the MMAs
 // and copies behind it as they are; behind `lane == 0` it wraps each in a search for equal lanes
-// (forward of B8 T4096 H16 d128 144 us instead of 122).
+// (forward of B8 T4096 H16 d128 144 us instead of 121).
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
