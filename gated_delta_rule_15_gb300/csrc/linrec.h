@@ -18,7 +18,7 @@
 // for any e > t (dL/dS_{e-1} without the output of token e-1).  Both dot products hold the
 // same term (do_r.v_r)(q_r.k_r) of the token itself; it is left out of both, so that a
 // strong decay's small gradient is no difference of large numbers.  The sums run over at
-// most kAnchor tokens: the dq pass stores S at every such boundary and the dk pass, which
+// most `run` tokens: the dq pass stores S at every such boundary and the dk pass, which
 // holds the same entries of dS there, adds the inner product.  Where a_t is 0 the gradient is set
 // to 0: the sums are 0 there in exact arithmetic only.
 #pragma once
@@ -29,7 +29,11 @@
 
 namespace dr {
 
-constexpr int kAnchor = 256;   // tokens between two stored states of the log-decay gradient
+// Tokens between two stored states of the log-decay gradient, on the tensor cores and in the token
+// recurrence.  The sums' rounding grows with the root of it: of fp32 rows the gradient is 0.3e-6 to 0.8e-6 off
+// in the 2-norm (256 tokens: up to 1.1e-6); the chunks, for which the states' traffic counts, are 0.5e-6 to
+// 0.9e-6 off with 256.
+constexpr int kAnchor = 256, kTokenAnchor = 128;
 
 // The sequences of a problem: N of them, packed by `cu` (N + 1 device offsets into `total`
 // rows) or T rows each.  Offsets from the device are clamped into the rows that exist.
@@ -49,10 +53,10 @@ __device__ __forceinline__ void seq_range(const LinrecSeqs &s, int64_t n, int64_
     }
 }
 #endif
-// Slot of the stored state at the end of sequence n's `j`-th run of kAnchor tokens; two
+// Slot of the stored state at the end of sequence n's `j`-th run of `run` tokens; two
 // sequences never share one, and there are linrec_slots() of them.
-__host__ __device__ inline int64_t linrec_slot(int64_t lo, int64_t n, int64_t j) { return lo / kAnchor + n + j; }
-__host__ __device__ inline int64_t linrec_slots(const LinrecSeqs &s) { return s.total / kAnchor + s.N + 1; }
+__host__ __device__ inline int64_t linrec_slot(int run, int64_t lo, int64_t n, int64_t j) { return lo / run + n + j; }
+__host__ __device__ inline int64_t linrec_slots(int run, const LinrecSeqs &s) { return s.total / run + s.N + 1; }
 
 struct LinrecPass {
     LinrecSeqs seqs;
@@ -82,8 +86,8 @@ bool linrec_tc_supported(const LinrecSeqs &s, int64_t H, bool in_bf16, bool out_
 size_t linrec_tc_workspace_bytes(const LinrecSeqs &s, int64_t H, int dk, int dv);
 int launch_linrec_tc(const LinrecPass &p, void *workspace, int *status, cudaStream_t stream);
 
-// dlog a from the two passes' dot products and the inner products; `parts` of each.
-int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int parts, const float *la, const float *dot_q,
+// dlog a from the two passes' dot products and the inner products of runs of `run` tokens; `parts` of each.
+int launch_linrec_gate_grad(const LinrecSeqs &s, int H, int run, int parts, const float *la, const float *dot_q,
                             const float *dot_k, const float *inner, float *dla, cudaStream_t stream);
 
 // Zeroes the rows of no sequence of `rows` (row_bytes a multiple of 16) and `gates` (words a row), where given.

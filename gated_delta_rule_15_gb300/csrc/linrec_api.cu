@@ -55,7 +55,7 @@ LinrecSeqs shape_of(const dr_linrec_desc *d) {
 // stored states and their inner products.
 struct BwdSpace {
     size_t dot_q, dot_k, inner, anchor, bytes;
-    int parts;
+    int parts, run;
 };
 BwdSpace bwd_space(const dr_linrec_desc *d) {
     BwdSpace w{};
@@ -65,12 +65,14 @@ BwdSpace bwd_space(const dr_linrec_desc *d) {
     w.bytes = segs;
     if (d->gate == DR_GATE_NONE) return w;
     w.parts = tc ? 1 : (int)d->dk / kSimtCols;   // the dq and dk passes' value width is dk
+    w.run = tc ? kAnchor : kTokenAnchor;
+    const size_t slots = (size_t)linrec_slots(w.run, s);
     const size_t dot = round256(sizeof(float) * (size_t)w.parts * d->H * s.total);
     w.dot_q = segs;
     w.dot_k = segs + dot;
     w.inner = segs + 2 * dot;
-    w.anchor = w.inner + round256(sizeof(float) * (size_t)w.parts * linrec_slots(s) * d->H);
-    w.bytes = w.anchor + round256(sizeof(float) * (size_t)linrec_slots(s) * d->H * d->dk * d->dv);
+    w.anchor = w.inner + round256(sizeof(float) * (size_t)w.parts * slots * d->H);
+    w.bytes = w.anchor + round256(sizeof(float) * slots * d->H * d->dk * d->dv);
     return w;
 }
 
@@ -215,7 +217,7 @@ extern "C" int dr_linrec_bwd(const dr_linrec_desc *desc, const void *q, const vo
     p.y = nullptr; p.dot = p.anchor = p.inner = nullptr;
     if ((rc = pass(p)) != kOk) return rc;
     if (!gate) return kOk;
-    return launch_linrec_gate_grad(seqs, (int)d.H, w.parts, log_alpha, (const float *)(ws + w.dot_q),
+    return launch_linrec_gate_grad(seqs, (int)d.H, w.run, w.parts, log_alpha, (const float *)(ws + w.dot_q),
                                    (const float *)(ws + w.dot_k), (const float *)(ws + w.inner), d_log_alpha,
                                    (cudaStream_t)stream);
 }

@@ -21,7 +21,7 @@ using umma::mul2;
 // rate, 3 dk dv / 2 instructions a head-token.  Few chains: by one token's latency, 0.14 us (64 x 64) and
 // 0.2 us (128 x 128).
 // Rows come by asynchronous copies, a tile ahead.
-// kGroup tokens' read-outs are summed over the lanes at a time; kTile tokens (kAnchor is a multiple) are staged
+// kGroup tokens' read-outs are summed over the lanes at a time; kTile tokens (kTokenAnchor is a multiple) are staged
 // in shared memory, of which 48 KB hold two tiles.  One fp32 chain of 256 tokens of 64 x 64 / 128 x 128, us on
 // the GPU, by kTile and kGroup: 8 and 4 48 / 65, 16 and 4 37 / 57, 8 and 8 46 / 57, 16 and 8 37 / 50.
 constexpr int kGroup = 8;
@@ -59,7 +59,7 @@ linrec_token_kernel(const LinrecPass p) {
     Tout *out = (Tout *)p.out;
     // the stored states of this (head, part): one float2 per thread and register
     auto slot_ptr = [&](int64_t j) {
-        const int64_t s = linrec_slot(lo, n, j);
+        const int64_t s = linrec_slot(kTokenAnchor, lo, n, j);
         return reinterpret_cast<float2 *>(p.anchor) + ((size_t)(s * H + h) * PARTS + part) * (DK * kSimtCols / 2) + tid;
     };
     auto store_anchor = [&](int64_t j) {
@@ -85,7 +85,7 @@ linrec_token_kernel(const LinrecPass p) {
         if (lane == 0) sRed[warp] = x;
         __syncthreads();
         if (tid == 0)
-            p.inner[((size_t)part * linrec_slots(p.seqs) + linrec_slot(lo, n, j)) * H + h] =
+            p.inner[((size_t)part * linrec_slots(kTokenAnchor, p.seqs) + linrec_slot(kTokenAnchor, lo, n, j)) * H + h] =
                 decay * ((sRed[0] + sRed[1]) + (sRed[2] + sRed[3]));
         __syncthreads();
     };
@@ -128,8 +128,8 @@ linrec_token_kernel(const LinrecPass p) {
         issue(it + 1);   // the other buffer's readers have passed the barrier behind their tile
         umma::cp_async_wait_group1();
         __syncthreads();
-        if (DOT && REV && (tile + 1) * kTile % kAnchor == 0 || DOT && REV && it == 0)
-            inner_product(((tile + 1) * kTile - 1) / kAnchor, sA[cnt - 1]);
+        if (DOT && REV && (tile + 1) * kTile % kTokenAnchor == 0 || DOT && REV && it == 0)
+            inner_product(((tile + 1) * kTile - 1) / kTokenAnchor, sA[cnt - 1]);
         // kGroup tokens' read-outs are summed over the lanes together: the shuffles' latency is paid
         // once (rows behind the tile's end take no part; the condition is the block's)
         for (int x0 = 0; x0 < cnt; x0 += kGroup) {
@@ -205,8 +205,8 @@ linrec_token_kernel(const LinrecPass p) {
         if (DOT && tid < cnt)
             p.dot[((size_t)part * H + h) * p.seqs.total + base + tid] =
                 (sDot[0][tid] + sDot[1][tid]) + (sDot[2][tid] + sDot[3][tid]);
-        if (DOT && !REV && ((tile + 1) * kTile % kAnchor == 0 || it == tiles - 1))
-            store_anchor(((tile + 1) * kTile - 1) / kAnchor);
+        if (DOT && !REV && ((tile + 1) * kTile % kTokenAnchor == 0 || it == tiles - 1))
+            store_anchor(((tile + 1) * kTile - 1) / kTokenAnchor);
     }
     if (p.fin) {
         const float a = REV && len > 0 && p.la ? expf(p.la[lo * H + h]) : 1.f;
@@ -241,9 +241,10 @@ int launch_token_types(const LinrecPass &p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- log-decay gradient
-// One warp per run of kAnchor tokens of a chain: 8 consecutive tokens a lane, a suffix sum
+// One warp per run of 32 E tokens of a chain: E consecutive tokens a lane, a suffix sum
 // over the lanes, the run's inner product added.  Where alpha is 0 (a reset) so is the gradient,
 // alpha <S, dS>: the sums would leave their rounding there.  Reads 12 and writes 4 bytes a head-token.
+template <int E>
 __global__ void __launch_bounds__(256)
 linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__restrict__ la, const float *__restrict__ dot_q,
                         const float *__restrict__ dot_k, const float *__restrict__ inner, float *__restrict__ dla) {
@@ -251,12 +252,13 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
     const int h = (int)(chain % H), lane = threadIdx.x & 31;
     int64_t lo, hi;
     seq_range(seqs, n, lo, hi);
-    const int64_t runs = (hi - lo + kAnchor - 1) / kAnchor, slots = linrec_slots(seqs);
+    constexpr int RUN = 32 * E;
+    const int64_t runs = (hi - lo + RUN - 1) / RUN, slots = linrec_slots(RUN, seqs);
     for (int64_t j = blockIdx.y * 8 + (threadIdx.x >> 5); j < runs; j += (int64_t)gridDim.y * 8) {
-        const int64_t t0 = lo + j * kAnchor + 8 * lane;
-        float x[8], a[8];
+        const int64_t t0 = lo + j * RUN + E * lane;
+        float x[E], a[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
             x[e] = 0.f;
             a[e] = t0 + e < hi ? la[(t0 + e) * H + h] : 0.f;
         }
@@ -264,12 +266,12 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
         for (int part = 0; part < parts; ++part) {
             const size_t row = ((size_t)part * H + h) * seqs.total;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < E; ++e)
                 if (t0 + e < hi) x[e] += dot_q[row + t0 + e] - dot_k[row + t0 + e];
-            d += inner[((size_t)part * slots + linrec_slot(lo, n, j)) * H + h];
+            d += inner[((size_t)part * slots + linrec_slot(RUN, lo, n, j)) * H + h];
         }
 #pragma unroll
-        for (int e = 6; e >= 0; --e) x[e] += x[e + 1];
+        for (int e = E - 2; e >= 0; --e) x[e] += x[e + 1];
         float later = x[0];   // inclusive suffix sum over the lanes, then without the own part
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -279,7 +281,7 @@ linrec_gate_grad_kernel(const LinrecSeqs seqs, int H, int parts, const float *__
         later = __shfl_down_sync(0xffffffffu, later, 1);
         if (lane == 31) later = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < E; ++e)
             if (t0 + e < hi) dla[(t0 + e) * H + h] = expf(a[e]) == 0.f ? 0.f : x[e] + later + d;
     }
 }
@@ -382,12 +384,13 @@ int launch_linrec_simt(const LinrecPass &p, cudaStream_t s) {
     return kErrUnsupported;
 }
 
-int launch_linrec_gate_grad(const LinrecSeqs &seqs, int H, int parts, const float *la, const float *dot_q,
+int launch_linrec_gate_grad(const LinrecSeqs &seqs, int H, int run, int parts, const float *la, const float *dot_q,
                             const float *dot_k, const float *inner, float *dla, cudaStream_t s) {
-    const int64_t runs = ((seqs.cu ? seqs.total : seqs.T) + kAnchor - 1) / kAnchor;
+    const int64_t runs = ((seqs.cu ? seqs.total : seqs.T) + run - 1) / run;
     const int64_t y = runs < 8 ? 1 : (runs + 7) / 8 < 1024 ? (runs + 7) / 8 : 1024;
-    linrec_gate_grad_kernel<<<dim3((unsigned)(seqs.N * H), (unsigned)y), 256, 0, s>>>(seqs, H, parts, la, dot_q,
-                                                                                     dot_k, inner, dla);
+    const dim3 grid((unsigned)(seqs.N * H), (unsigned)y);
+    if (run == kAnchor) linrec_gate_grad_kernel<kAnchor / 32><<<grid, 256, 0, s>>>(seqs, H, parts, la, dot_q, dot_k, inner, dla);
+    else linrec_gate_grad_kernel<kTokenAnchor / 32><<<grid, 256, 0, s>>>(seqs, H, parts, la, dot_q, dot_k, inner, dla);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 

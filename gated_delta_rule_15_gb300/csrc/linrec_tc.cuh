@@ -491,7 +491,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         // this thread's entries of a stored state
         auto anchor_ptr = [&](int it) {
             const int64_t run = (row_of(it) - lo + kChunk - 1) / kAnchor;
-            return p.anchor + (size_t)(linrec_slot(lo, n, run) * H + h) * (DK * DV) + half * DV + row;
+            return p.anchor + (size_t)(linrec_slot(kAnchor, lo, n, run) * H + h) * (DK * DV) + half * DV + row;
         };
         auto at_anchor = [&](int it) {   // the chunk ends a run of kAnchor tokens or the sequence
             const int64_t end = row_of(it) + count_of(it);
@@ -529,7 +529,7 @@ linrec_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 named_sync(2, 32 * kStateWarps);
                 if (tid == 0) {
                     const int64_t run = (row_of(it) - lo + kChunk - 1) / kAnchor;
-                    p.inner[linrec_slot(lo, n, run) * H + h] =
+                    p.inner[linrec_slot(kAnchor, lo, n, run) * H + h] =
                         ex2((ce.x - cl.x) + (ce.y - cl.y)) *
                         (((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])));
                 }

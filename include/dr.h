@@ -363,9 +363,10 @@ int dr_linrec_fwd(const dr_linrec_desc *desc, const void *q, const void *k, cons
  *   dq, dk, dv     in_dtype (written);  d_log_alpha fp32 [B, T, H] (written), NULL exactly
  *                  when gate is NONE;  d_init_state NULL or fp32 [N, H, dk, dv] (written),
  *                  may equal d_final_state
- * d_log_alpha_t = alpha_t <S_{t-1}, dL/dS_t> comes as a sum of q.dq - k.dk over the up to 256
- * tokens behind t and one inner product of states.  It is 0 where alpha is; where a strong decay
- * makes it small against those terms, it carries their rounding (some 1e-6 of the largest).
+ * d_log_alpha_t = alpha_t <S_{t-1}, dL/dS_t> comes as a sum of q.dq - k.dk over the up to 256 tokens
+ * behind t (128 where the call runs token by token) and one inner product of states.  It is 0 where
+ * alpha is; where a strong decay makes it small against those terms, it carries their rounding
+ * (some 1e-6 of the largest).
  * Written buffers, workspace among them, overlap neither each other nor an input otherwise
  * (DR_ERR_INVALID).  Results do not depend on the order in which the GPU runs its blocks.
  * Statuses as for dr_linrec_fwd.

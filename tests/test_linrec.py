@@ -478,6 +478,20 @@ def test_log_decay_gradient_of_bf16_rows_is_an_fp32_result(dr, B, T, dk, dv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,T,H", [(4, 255, 2), (2, 1000, 2), (8, 255, 3)])
+def test_log_decay_gradient_of_fp32_rows(dr, B, T, H):
+    """In the 2-norm.  A token's terms are off by 3.2 u (16 products in a row, sqrt(16 / 6) u, the tree over
+    them and over the columns, u, and the state's own rounding over its memory of 20 tokens, sqrt(20 / 3) u); up
+    to 2 * 128 of them are added, against a gradient of the size of 20: sqrt(256 / 20) 3.2 u = 6.8e-7.  The
+    state's part is the same for neighbouring tokens and adds up faster, by 1.32 at most: 9e-7."""
+    d = inputs(B, T, H, 128, 128, "f32", seed=T)
+    _, _, g = reference(d["q"], d["k"], d["v"], d["la"], d["s0"], None, d["do"], d["ds"])
+    c = cuda(d)
+    dla = dr.linrec_bwd(c["q"], c["k"], c["v"], c["la"], c["s0"], c["do"], c["ds"])[3].double().cpu()
+    assert (dla - g["dla"]).norm() <= 9e-7 * g["dla"].norm()
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences(dr):
     """Directional derivatives of <do, out> + <ds, final> by central differences in fp32: the
     function is quadratic in q, k, v and the state, so the quotient is exact up to its
