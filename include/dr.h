@@ -327,10 +327,10 @@ int dr_chunk_fwd_noalloc(const dr_chunk_desc *desc,
  *     results are off by their own rounding, d_log_alpha (three terms) by 1e-6 of its 2-norm, states by 3e-7.
  *     Who wants fp32 arithmetic asks for fp32 results (forward) or hands in fp32 rows (backward).
  *   - log_alpha = -inf is a full reset (alpha = 0; from -120 on it is one in fp32).  On the tensor
- *     cores the state in front of a chunk enters the chunk's results with no less than 2^-60
- *     (dq, dk of a gated problem, states and d_log_alpha: exactly), and, without a gate's dq
- *     and dk, sums are held divided by their row's decay within the chunk, 2^-60 at least: results
- *     beyond 3.4e38 times that, 2.9e20 behind strong decays, overflow (infinity or NaN).
+ *     cores out and dv hold their sums divided by the row's decay within its chunk, 2^-60 at least: the
+ *     state in front of the chunk enters them with no less than 2^-60, and values beyond 3.4e38
+ *     times the divisor (2.9e20 behind strong decays) overflow to infinity or NaN.  dq, dk, states
+ *     and d_log_alpha know neither limit.
  *     Inputs of the sequences' rows are otherwise finite; a NaN or infinity may reach every
  *     output of its chunk.  Values in rows of no sequence do not matter.
  */
