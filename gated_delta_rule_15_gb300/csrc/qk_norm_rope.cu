@@ -28,6 +28,8 @@
 
 #include "../../include/dr.h"
 #include "common.cuh"
+#include "rope.cuh"
+#include "spans.h"
 
 namespace dr {
 namespace {
@@ -46,113 +48,6 @@ struct RopeArgs {
     float eps, scale;
     float *partial;          // (gradient) [d][blocks of q], [d][blocks of k] partial weight gradients, or NULL
 };
-
-template <typename T> struct Vec8;   // 8 storage elements
-template <> struct Vec8<float> { float4 a, b; };
-template <> struct Vec8<__nv_bfloat16> { uint4 a; };
-
-__device__ __forceinline__ Vec8<float> ld8(const float *p) {
-    return {*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + 4)};
-}
-__device__ __forceinline__ Vec8<__nv_bfloat16> ld8(const __nv_bfloat16 *p) { return {*reinterpret_cast<const uint4 *>(p)}; }
-__device__ __forceinline__ void unpack(const Vec8<float> &v, float (&f)[8]) {
-    f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
-    f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
-}
-__device__ __forceinline__ void unpack(const Vec8<__nv_bfloat16> &v, float (&f)[8]) {
-    const uint32_t u[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {   // bf16 is the upper half of fp32
-        f[2 * i] = __uint_as_float(u[i] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ Vec8<float> shfl8(const Vec8<float> &v, int src) {
-    Vec8<float> o;
-    o.a.x = __shfl_sync(0xffffffffu, v.a.x, src); o.a.y = __shfl_sync(0xffffffffu, v.a.y, src);
-    o.a.z = __shfl_sync(0xffffffffu, v.a.z, src); o.a.w = __shfl_sync(0xffffffffu, v.a.w, src);
-    o.b.x = __shfl_sync(0xffffffffu, v.b.x, src); o.b.y = __shfl_sync(0xffffffffu, v.b.y, src);
-    o.b.z = __shfl_sync(0xffffffffu, v.b.z, src); o.b.w = __shfl_sync(0xffffffffu, v.b.w, src);
-    return o;
-}
-__device__ __forceinline__ Vec8<__nv_bfloat16> shfl8(const Vec8<__nv_bfloat16> &v, int src) {
-    Vec8<__nv_bfloat16> o;
-    o.a.x = __shfl_sync(0xffffffffu, v.a.x, src); o.a.y = __shfl_sync(0xffffffffu, v.a.y, src);
-    o.a.z = __shfl_sync(0xffffffffu, v.a.z, src); o.a.w = __shfl_sync(0xffffffffu, v.a.w, src);
-    return o;
-}
-__device__ __forceinline__ void st8(float *p, const float (&f)[8]) {
-    store4(p, make_float4(f[0], f[1], f[2], f[3]));
-    store4(p + 4, make_float4(f[4], f[5], f[6], f[7]));
-}
-__device__ __forceinline__ void st8(__nv_bfloat16 *p, const float (&f)[8]) {
-    uint4 u;
-    uint32_t *w = &u.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = u;
-}
-
-// Of this lane's 8 values: the cosine (times c) of each one's pair and the signed sine (times c) its
-// pair's other value enters with, for a rotation forwards or back; 1 and 0 behind the rotated part.
-template <bool HALF>
-__device__ __forceinline__ void angles(const RopeArgs &a, int64_t pos, int l, bool back, float (&co)[8], float (&si)[8]) {
-    constexpr int NP = HALF ? 8 : 4;
-    const int hr = a.rot / 2, i0 = HALF ? (8 * l < hr ? 8 * l : 8 * l - hr) : 4 * l;
-    if (8 * l >= a.rot) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            co[e] = 1.f;
-            si[e] = 0.f;
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-        const uint64_t turn = (uint64_t)pos * __ldg(a.table + i0 + e);
-        // signed upper half: [-1/2, 1/2) turns, i.e. that many times 2 pi
-        const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;   // 2^-31
-        float s, c;
-        sincospif(half_turns, &s, &c);
-        c *= a.scale;
-        s *= back ? -a.scale : a.scale;
-        if (HALF) {
-            co[e] = c;
-            si[e] = 8 * l < hr ? -s : s;
-        } else {
-            co[2 * e] = co[2 * e + 1] = c;
-            si[2 * e] = -s;
-            si[2 * e + 1] = s;
-        }
-    }
-}
-
-// The lane that holds the other values of this lane's pairs (half layout).
-template <bool HALF>
-__device__ __forceinline__ int partner(const RopeArgs &a, int lane, int l) {
-    return HALF && 8 * l < a.rot ? (16 * l < a.rot ? lane + a.rot / 16 : lane - a.rot / 16) : lane;
-}
-// Each value's pair's other one.
-template <bool HALF, typename T>
-__device__ __forceinline__ void others(const Vec8<T> &raw, const float (&x)[8], int src, float (&o)[8]) {
-    if (HALF) {
-        const Vec8<T> v = shfl8(raw, src);
-        unpack(v, o);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-    }
-}
-
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
 
 // A group of lanes' unit of work: a token and a run of its q and k heads (numbered behind one
 // another).  Of each kind s (q, k) every row is
@@ -404,41 +299,6 @@ size_t partial_bytes(const dr_qk_norm_rope_desc &d) {
     int b[2];
     grad_blocks(d, b);
     return sizeof(float) * (size_t)d.d * (b[0] + b[1]);
-}
-
-bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-// n_tok rows of `width` elements, `stride` apart
-struct Rows {
-    const void *p;
-    int64_t width, stride;
-};
-// Whether rows of a and b share a byte.  Rows of one stride may lie between one another (the
-// parts of a fused projection's row); of different strides their whole spans count.
-bool meet(const Rows &a, const Rows &b, int64_t n_tok, int64_t e) {
-    if (!a.p || !b.p || n_tok < 1 || a.width < 1 || b.width < 1) return false;
-    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
-    if (a0 + ((n_tok - 1) * a.stride + a.width) * e <= b0 || b0 + ((n_tok - 1) * b.stride + b.width) * e <= a0) return false;
-    if (a.stride != b.stride) return true;
-    const int64_t row = a.stride * e, off = ((b0 - a0) % row + row) % row;
-    return off < a.width * e || off + b.width * e > row;
-}
-bool same(const Rows &a, const Rows &b) { return a.p == b.p && a.width == b.width && a.stride == b.stride; }
-// `bytes` bytes in one piece
-struct Block {
-    const void *p;
-    size_t bytes;
-};
-bool meet(const Block &a, const Block &b) {
-    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
-    return a.p && b.p && a.bytes && b.bytes && a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-// Whether a row shares a byte with the block, which may lie between two rows.
-bool meet(const Rows &a, const Block &b, int64_t n_tok, int64_t e) {
-    if (!a.p || !b.p || n_tok < 1 || a.width < 1 || b.bytes < 1) return false;
-    const char *a0 = (const char *)a.p, *b0 = (const char *)b.p;
-    if (a0 + ((n_tok - 1) * a.stride + a.width) * e <= b0 || b0 + b.bytes <= a0) return false;
-    const int64_t row = a.stride * e, off = ((b0 - a0) % row + row) % row;
-    return off < a.width * e || off + (int64_t)b.bytes > row;
 }
 
 // What every block may read beside its rows.

@@ -48,7 +48,9 @@ EXPORTED = ("dr_version", "dr_chunk_fwd_workspace_bytes", "dr_chunk_fwd_min_work
             "dr_chunk_fwd_host_dev_bytes", "dr_chunk_fwd_host",
             "dr_linrec_fwd_workspace_bytes", "dr_linrec_fwd", "dr_linrec_bwd_workspace_bytes",
             "dr_linrec_bwd", "dr_linrec_zero_rest", "dr_linrec_step", "dr_rope_table", "dr_qk_norm_rope",
-            "dr_qk_norm_rope_bwd_workspace_bytes", "dr_qk_norm_rope_bwd")
+            "dr_qk_norm_rope_bwd_workspace_bytes", "dr_qk_norm_rope_bwd",
+            "dr_window_attn_fwd", "dr_window_attn_bwd_workspace_bytes", "dr_window_attn_bwd",
+            "dr_kv_append", "dr_window_attn_step_workspace_bytes", "dr_window_attn_step")
 
 
 class ChunkDesc(ctypes.Structure):
@@ -81,6 +83,32 @@ class QkNormRopeDesc(ctypes.Structure):
                 ("norm", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("rot_scale", ctypes.c_float)]
+
+
+def _int64s(*names):
+    return [(n, ctypes.c_int64) for n in names]
+
+
+def _int32s(*names):
+    return [(n, ctypes.c_int32) for n in names]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = _int64s("B", "T", "Hq", "Hk", "d", "N", "window", "sinks", "q_stride", "k_stride", "v_stride",
+                       "dq_stride", "dk_stride", "dv_stride") + \
+        _int32s("dtype", "zero_rest", "reserved") + [("scale", ctypes.c_float)]
+
+
+class KvAppendDesc(ctypes.Structure):
+    _fields_ = _int64s("n_tok", "N", "Hq", "Hk", "d", "rot", "q_stride", "k_stride", "v_stride",
+                       "q_out_stride", "n_pages", "page", "max_pages") + \
+        _int32s("dtype", "norm", "layout", "zero_rest", "reserved") + \
+        [("eps", ctypes.c_float), ("rot_scale", ctypes.c_float)]
+
+
+class AttnStepDesc(ctypes.Structure):
+    _fields_ = _int64s("B", "Hq", "Hk", "d", "n_pages", "page", "max_pages", "window", "sinks") + \
+        _int32s("dtype", "reserved") + [("scale", ctypes.c_float)]
 
 
 _vp = ctypes.c_void_p
@@ -140,8 +168,15 @@ _lib.dr_qk_norm_rope_bwd_workspace_bytes.argtypes = [ctypes.POINTER(QkNormRopeDe
                                                      ctypes.POINTER(ctypes.c_size_t)]
 _lib.dr_qk_norm_rope_bwd.argtypes = [ctypes.POINTER(QkNormRopeDesc)] + [_vp] * 13 + \
     [ctypes.c_size_t, _vp]
+_lib.dr_window_attn_fwd.argtypes = [ctypes.POINTER(AttnDesc)] + [_vp] * 7
+_lib.dr_window_attn_bwd_workspace_bytes.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.dr_window_attn_bwd.argtypes = [ctypes.POINTER(AttnDesc)] + [_vp] * 11 + [ctypes.c_size_t, _vp]
+_lib.dr_kv_append.argtypes = [ctypes.POINTER(KvAppendDesc)] + [_vp] * 13
+_lib.dr_window_attn_step_workspace_bytes.argtypes = [ctypes.POINTER(AttnStepDesc),
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+_lib.dr_window_attn_step.argtypes = [ctypes.POINTER(AttnStepDesc)] + [_vp] * 8 + [ctypes.c_size_t, _vp]
 for _name in EXPORTED:
-    if "linrec" in _name or "rope" in _name:
+    if "linrec" in _name or "rope" in _name or "attn" in _name or "append" in _name:
         getattr(_lib, _name).restype = ctypes.c_int
 NOALLOC_SCRATCH_BYTES = 64 << 20   # DR_NOALLOC_SCRATCH_BYTES of include/dr.h
 
@@ -786,3 +821,194 @@ def qk_norm_rope_bwd(q, k, table, dq_out, dk_out, *, positions=None, offset: int
     if rc != DR_OK:
         raise DrError(rc, "dr_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+# ------------------------------------------------------------ window attention
+def _packed_count(cu_seqlens, B):
+    """N of packed sequences, 0 without offsets."""
+    if cu_seqlens is None:
+        return 0
+    _on_one_device(cu_seqlens)
+    if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be int64 [N + 1], N >= 1")
+    if B != 1:
+        raise ValueError("packed sequences come as one batch row (B = 1)")
+    return cu_seqlens.numel() - 1
+
+
+def _rows_here(x, what):
+    """Elements between the rows of a [..., H, d] tensor of the current device."""
+    if x.get_device() != _current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    return _rows_of(x, what)[3]
+
+
+def _attn_desc(q, k, v, cu_seqlens, window, sinks, scale):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k, v must be [B,T,H,d]")
+    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
+    B, T, Hq, d = q.shape
+    if k.shape[:2] != q.shape[:2] or k.shape[3] != d or v.shape != k.shape:
+        raise ValueError("inconsistent shapes")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    steps = [_rows_here(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"))]
+    return AttnDesc(B, T, Hq, k.shape[2], d, _packed_count(cu_seqlens, B), window, sinks, *steps, 0, 0, 0,
+                    _DT[q.dtype], 0, 0, d ** -0.5 if scale is None else scale)
+
+
+def window_attn_fwd(q, k, v, *, window: int = 0, sinks: int = 0, scale=None, cu_seqlens=None, out=None,
+                    lse=None, stream=None):
+    """Attention of every token over the last ``window`` tokens of its sequence (itself among them;
+    0: all before it) and the first ``sinks`` ones (dr_window_attn_fwd).
+
+    q [B,T,Hq,d], k, v [B,T,Hk,d], Hq a multiple of Hk; rows may be strided, as parts of a fused
+    projection's output.  ``scale`` of the scores: d ** -0.5 unless given.  ``cu_seqlens`` int64
+    [N + 1] (device): the one batch row holds N sequences behind one another.  Returns (out
+    [B,T,Hq,d], lse fp32 [B,T,Hq], the log of the softmax's sum).  Rows of no sequence are zero in
+    new buffers and left as they are in given ones."""
+    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale)
+    _on_one_device(out, lse)
+    _like(out, q.shape, q.dtype, "out")
+    _like(lse, q.shape[:3], torch.float32, "lse")
+    if (out is None) != (lse is None) and desc.N:
+        raise ValueError("packed sequences: give both of out and lse or neither")
+    desc.zero_rest = int(out is None and desc.N > 0)
+    with _stream_scope(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    rc = _lib.dr_window_attn_fwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(cu_seqlens), _at(out),
+                                 _at(lse), _raw_stream(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_window_attn_fwd")
+    return out, lse
+
+
+def window_attn_bwd(q, k, v, out, lse, d_out, *, window: int = 0, sinks: int = 0, scale=None,
+                    cu_seqlens=None, grads=None, workspace=None, stream=None):
+    """Gradients of <d_out, out> of window_attn_fwd from its inputs and results
+    (dr_window_attn_bwd): (dq, dk, dv) in q's dtype.  ``grads``: three buffers to write into (strided
+    rows, as parts of a fused gradient); their rows of no sequence are left as they are (new ones
+    hold zeros there)."""
+    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale)
+    _on_one_device(out, lse, d_out, workspace)
+    for t, n in ((out, "out"), (d_out, "d_out")):
+        _like(t, q.shape, q.dtype, n)
+    _like(lse, q.shape[:3], torch.float32, "lse")
+    with _stream_scope(stream):
+        if grads is None:
+            grads = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+            desc.zero_rest = int(desc.N > 0)
+        else:
+            if len(grads) != 3:
+                raise ValueError("grads must be (dq, dk, dv)")
+            for g, x, n in zip(grads, (q, k, v), ("dq", "dk", "dv")):
+                _like(g, x.shape, x.dtype, n)
+            desc.dq_stride, desc.dk_stride, desc.dv_stride = (
+                _rows_here(g, n) for g, n in zip(grads, ("dq", "dk", "dv")))
+        workspace = _workspace(_lib.dr_window_attn_bwd_workspace_bytes, desc, workspace, q.device,
+                               "dr_window_attn_bwd_workspace_bytes")
+        dq, dk, dv = grads
+        rc = _lib.dr_window_attn_bwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(cu_seqlens), _at(out),
+                                     _at(lse), _at(d_out), _at(dq), _at(dk), _at(dv), _at(workspace),
+                                     _bytes(workspace), _raw_stream(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_window_attn_bwd")
+    return dq, dk, dv
+
+
+def _cache_of(k_cache, v_cache, pages, rows, d, dtype):
+    """(n_pages, Hk, page, max_pages) of a paged cache for `rows` sequences."""
+    _on_one_device(k_cache, v_cache, pages)
+    if k_cache.dim() != 4 or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache, v_cache must be [n_pages,Hk,page,d]")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError("k_cache and v_cache must have the rows' dtype")
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != rows:
+        raise ValueError("pages must be int32 [N, max_pages]")
+    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], pages.shape[1]
+
+
+def kv_append(q, k, v, table, k_cache, v_cache, pages, start, *, cu_seqlens=None, norm="rms", wq=None,
+              wk=None, eps: float = 1e-6, layout="half", rot_scale: float = 1.0, q_out=None, stream=None):
+    """New tokens' keys, normalised and rotated by their positions as qk_norm_rope does it, and
+    their values into a paged cache (dr_kv_append); returns the same tokens' queries normalised and
+    rotated (None without q).
+
+    q [rows,Hq,d] or None, k, v [rows,Hk,d], rows possibly strided; k_cache, v_cache
+    [n_pages,Hk,page,d]; pages int32 [N,max_pages], entries outside the cache standing for pages
+    that are not there; start int64 [N]: tokens each sequence had before, negative for a slot without
+    a sequence.  One row for each sequence, or by ``cu_seqlens`` int64 [N + 1] the rows
+    cu_seqlens[n] .. cu_seqlens[n + 1] - 1.  Rows of no sequence are zero in a new ``q_out`` and left as
+    they are in a given one, which may be q."""
+    if k.dim() != 3 or v.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q, k, v must be [rows,H,d]")
+    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
+    n, Hk, d = k.shape
+    if v.shape != k.shape or (q is not None and (q.shape[0] != n or q.shape[2] != d)):
+        raise ValueError("inconsistent shapes")
+    if norm not in _NORMS or layout not in _LAYOUTS:
+        raise ValueError("norm must be none, l2 or rms; layout half or interleaved")
+    if q is None and (q_out is not None or wq is not None):
+        raise ValueError("q_out, wq without q")
+    _on_one_device(table, start, wq, wk)
+    if table is not None and (table.dtype != torch.int64 or table.dim() != 1):
+        raise ValueError("table must be rope_table's int64 [rot / 2]")
+    N = n if cu_seqlens is None else _packed_count(cu_seqlens, 1)
+    _like(start, (N,), torch.int64, "start")
+    _like(wq, (d,), torch.float32, "wq")
+    _like(wk, (d,), torch.float32, "wk")
+    n_pages, heads, page, max_pages = _cache_of(k_cache, v_cache, pages, N, d, k.dtype)
+    if heads != Hk:
+        raise ValueError("k_cache, v_cache must be [n_pages,Hk,page,d]")
+    steps = [0 if x is None else _rows_here(x, w) for x, w in ((q, "q"), (k, "k"), (v, "v"))]
+    if n == 0 and N == 0:
+        return None if q is None else q.clone() if q_out is None else q_out
+    desc = KvAppendDesc(n, N, 0 if q is None else q.shape[1], Hk, d, 0 if table is None else 2 * table.numel(),
+                        *steps, 0, n_pages, page, max_pages, _DT[k.dtype], _NORMS[norm], _LAYOUTS[layout],
+                        int(q_out is None and q is not None), 0, eps, rot_scale)
+    with _stream_scope(stream):
+        q_out, desc.q_out_stride = _rows_into(q_out, q, "q_out")
+    rc = _lib.dr_kv_append(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(wq), _at(wk), _at(table),
+                           _at(pages), _at(start), _at(cu_seqlens), _at(q_out), _at(k_cache), _at(v_cache),
+                           _raw_stream(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_kv_append")
+    return q_out
+
+
+def window_attn_step(q, k_cache, v_cache, pages, lens, *, window: int = 0, sinks: int = 0, scale=None,
+                     out=None, lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """window_attn_fwd of one new token for each sequence over the cache that kv_append fills
+    (dr_window_attn_step): q [B,Hq,d]; k_cache, v_cache, pages as there; lens int64 [B], the
+    sequences' tokens with the new one (<= 0: none).  Returns (out [B,Hq,d], lse fp32 [B,Hq] or
+    None)."""
+    _on_one_device(q, lens, out, lse, workspace)
+    if q.dim() != 3 or q.dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16 [B,Hq,d]")
+    B, Hq, d = q.shape
+    n_pages, Hk, page, max_pages = _cache_of(k_cache, v_cache, pages, B, d, q.dtype)
+    _like(lens, (B,), torch.int64, "lens")
+    _like(out, q.shape, q.dtype, "out")
+    _like(lse, (B, Hq), torch.float32, "lse")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    desc = AttnStepDesc(B, Hq, Hk, d, n_pages, page, max_pages, window, sinks, _DT[q.dtype], 0,
+                        d ** -0.5 if scale is None else scale)
+    with _stream_scope(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        workspace = _workspace(_lib.dr_window_attn_step_workspace_bytes, desc, workspace, q.device,
+                               "dr_window_attn_step_workspace_bytes")
+        rc = _lib.dr_window_attn_step(ctypes.byref(desc), _at(q), _at(k_cache), _at(v_cache), _at(pages),
+                                      _at(lens), _at(out), _at(lse), _at(workspace), _bytes(workspace),
+                                      _raw_stream(stream))
+    if rc != DR_OK:
+        raise DrError(rc, "dr_window_attn_step")
+    return out, lse

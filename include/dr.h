@@ -472,6 +472,126 @@ int dr_qk_norm_rope_bwd(const dr_qk_norm_rope_desc *desc, const void *q, const v
                         void *dq, void *dk, float *dwq, float *dwk, void *workspace,
                         size_t workspace_bytes, dr_stream_t stream);
 
+/*
+ * Attention over a window, for the layers of softmax attention that stand between recurrent ones: of
+ * a sequence, token i sees token j when
+ *
+ *     j <= i  and  (i - j < window  or  j < sinks),
+ *
+ * the last `window` tokens (itself among them; 0: all before it) and the first `sinks` ones, which stay
+ * visible.  Over the visible tokens, with s_ij = scale q_i.k_j,
+ *
+ *     lse_i = log sum_j exp(s_ij),    out_i = sum_j exp(s_ij - lse_i) v_j.
+ *
+ * Query head h reads key and value head h / (Hq / Hk).
+ *   - Sequences as for dr_linrec_fwd: B of T tokens, or (N >= 1, B = 1) N packed ones by cu_seqlens
+ *     (clamped; decreasing offsets make results undefined and touch no other memory).  Rows of no
+ *     sequence are left as they are, or zeroed (out, lse, gradients) with zero_rest.  They and
+ *     other sequences' rows do not enter a result whatever they hold; the sequence's own rows are finite (a NaN
+ *     or infinity may reach every row whose tile of 128 tokens meets it, visible or not).
+ *   - Sums, maxima and products' accumulators are fp32.  fp32 rows are computed in fp32 arithmetic.  Of bf16
+ *     rows the weights exp(s_ij - m) and, backwards, the score gradients enter their products rounded to bf16 (half
+ *     a step of 2^-8 each, at random), which leaves a result about as far off as its own rounding does.
+ *   - The first call on a device looks up device addresses: make it before a stream capture.
+ */
+typedef struct {
+    int64_t B, T, Hq, Hk, d;  /* B >= 1, T >= 0; Hq a multiple of Hk; d 64 or 128       */
+    int64_t N;                /* 0: B sequences of T tokens; >= 1: packed sequences     */
+    int64_t window, sinks;    /* >= 0                                                   */
+    int64_t q_stride, k_stride, v_stride; /* elements between the rows of q, k, v: 0 for
+                                 contiguous, else at least a row, multiples of 16 bytes */
+    int64_t dq_stride, dk_stride, dv_stride; /* (backward) the same of what is written  */
+    int32_t dtype;            /* DR_F32 or DR_BF16: every row                           */
+    int32_t zero_rest;        /* packed: 1 zeroes the rows of no sequence, 0 leaves them */
+    int32_t reserved;         /* must be 0                                              */
+    float scale;              /* of the scores, > 0                                     */
+} dr_attn_desc;
+
+/*
+ *   q          [B, T, Hq, d], rows q_stride apart;  k, v  [B, T, Hk, d], rows k_stride, v_stride apart
+ *   out        [B, T, Hq, d] contiguous (written);  lse  fp32 [B, T, Hq] (written), natural log
+ * out and lse meet neither each other nor an input (DR_ERR_INVALID).
+ * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
+ */
+int dr_window_attn_fwd(const dr_attn_desc *desc, const void *q, const void *k, const void *v,
+                       const int64_t *cu_seqlens, void *out, float *lse, dr_stream_t stream);
+
+/*
+ * Gradients of <d_out, out> from the forward's inputs, its results out and lse, and d_out [B, T, Hq, d]
+ * (contiguous).  dq, dk, dv: rows dq_stride, dk_stride, dv_stride apart (written); they meet
+ * neither each other nor an input.  Results do not depend on the order in which the GPU runs its blocks.
+ * A token that sees itself alone has dq = 0 up to the rounding of d_out.out.
+ * Workspace rules as for dr_chunk_fwd; its size depends only on the descriptor.
+ */
+int dr_window_attn_bwd_workspace_bytes(const dr_attn_desc *desc, size_t *bytes);
+int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const void *k, const void *v,
+                       const int64_t *cu_seqlens, const void *out, const float *lse, const void *d_out,
+                       void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
+                       dr_stream_t stream);
+
+/*
+ * Its paged cache.  k_cache, v_cache [n_pages, Hk, page, d]; sequence n keeps the token at position p
+ * in slot p % page of the page pages[n][p / page].  Entries outside 0 .. n_pages - 1 stand for
+ * pages that are not there (given back, since their tokens left the window, or not yet given).
+ *
+ * dr_kv_append writes new tokens: keys normalised and rotated by their position as dr_qk_norm_rope
+ * does, values as they are, and on the way (Hq > 0) the same tokens' queries normalised and rotated into
+ * q_out.  Row t of sequence n is its token at position start[n] + t, start[n] the tokens it had before.
+ *   q, k, v      [n_tok, Hq | Hk | Hk, d], rows q_stride, k_stride, v_stride apart
+ *   wq, wk, table  as for dr_qk_norm_rope
+ *   pages        int32 [N, max_pages];  start  int64 [N] (device)
+ *   cu_seqlens   NULL: one row for each sequence (n_tok = N); else int64 [N + 1], rows
+ *                cu_seqlens[n] .. cu_seqlens[n + 1] - 1 are sequence n's
+ *   q_out        [n_tok, Hq, d], rows q_out_stride apart (written); may be q itself
+ * start[n] < 0: a slot of the batch without a sequence; its rows and rows of no sequence are not
+ * written anywhere (q_out: zeroed with zero_rest).  Keys and values of tokens whose page is not there,
+ * or behind max_pages pages, are dropped.  Two rows of one call for the same slot: one of them
+ * stays.  Written buffers meet no other one (DR_ERR_INVALID).
+ * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
+ */
+typedef struct {
+    int64_t n_tok, N;         /* rows >= 0; sequences >= 1                              */
+    int64_t Hq, Hk;           /* query heads >= 0 (0: no q), key heads >= 1             */
+    int64_t d, rot;           /* head width 64 or 128; rotated part, a multiple of 16   */
+    int64_t q_stride, k_stride, v_stride, q_out_stride; /* as in dr_qk_norm_rope_desc   */
+    int64_t n_pages, page, max_pages; /* pages of the cache; tokens a page, a multiple of
+                                 16 up to 1024; pages a sequence                        */
+    int32_t dtype;            /* DR_F32 or DR_BF16: rows and cache                      */
+    int32_t norm, layout;     /* DR_NORM_*, DR_ROPE_HALF or DR_ROPE_INTERLEAVED         */
+    int32_t zero_rest;        /* 1 zeroes q_out's rows of no sequence, 0 leaves them    */
+    int32_t reserved;         /* must be 0                                              */
+    float eps, rot_scale;     /* eps >= 0                                               */
+} dr_kv_append_desc;
+int dr_kv_append(const dr_kv_append_desc *desc, const void *q, const void *k, const void *v,
+                 const float *wq, const float *wk, const uint64_t *table, const int32_t *pages,
+                 const int64_t *start, const int64_t *cu_seqlens, void *q_out, void *k_cache,
+                 void *v_cache, dr_stream_t stream);
+
+/*
+ * The attention of one new token for each of B sequences over that cache (the token itself has been
+ * appended).
+ *   q       [B, Hq, d] contiguous;  pages  int32 [B, max_pages];  lens  int64 [B]: tokens of each
+ *           sequence, the new one among them (<= 0: none; from 2^30 on: taken as 2^30)
+ *   out     [B, Hq, d] (written);  lse  NULL or fp32 [B, Hq] (written)
+ * Visible are the last `window` of lens tokens and the first `sinks`, as far as their pages are there;
+ * without any, out is 0 and lse -infinity.  What invisible slots of a page hold does not matter.
+ * bf16: scores in fp32, weights as two bf16 terms (2^-17 of one is lost): out is off by its own rounding.
+ * Workspace rules as for dr_chunk_fwd (some MB whatever the lengths); results do not depend
+ * on the order in which the GPU runs its blocks.
+ */
+typedef struct {
+    int64_t B, Hq, Hk, d;     /* as in dr_attn_desc                                     */
+    int64_t n_pages, page, max_pages; /* as in dr_kv_append_desc                        */
+    int64_t window, sinks;    /* as in dr_attn_desc                                     */
+    int32_t dtype;            /* DR_F32 or DR_BF16: q, cache, out                       */
+    int32_t reserved;         /* must be 0                                              */
+    float scale;              /* > 0                                                    */
+} dr_attn_step_desc;
+int dr_window_attn_step_workspace_bytes(const dr_attn_step_desc *desc, size_t *bytes);
+int dr_window_attn_step(const dr_attn_step_desc *desc, const void *q, const void *k_cache,
+                        const void *v_cache, const int32_t *pages, const int64_t *lens, void *out,
+                        float *lse, void *workspace, size_t workspace_bytes, dr_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the library's sticky device status word
    on the current device (DR_OK, or DR_ERR_TIMEOUT if a bounded device wait expired), or
    DR_ERR_CUDA if the synchronisation itself failed. */
