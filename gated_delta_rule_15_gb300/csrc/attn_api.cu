@@ -4,6 +4,7 @@
 
 #include "../../include/dr.h"
 #include "attn.h"
+#include "attn_tc.cuh"
 #include "common.cuh"
 #include "spans.h"
 
@@ -113,7 +114,10 @@ extern "C" int dr_window_attn_fwd(const dr_attn_desc *desc, const void *q, const
         const int rz = launch_attn_zero_rest(p.seqs, r, (cudaStream_t)stream);
         if (rz != kOk) return rz;
     }
-    return launch_attn_simt_fwd(p, (cudaStream_t)stream);
+    if (!p.bf16) return launch_attn_simt_fwd(p, (cudaStream_t)stream);
+    int *status = device_status_ptr();
+    if (!status) return kErrCuda;
+    return launch_attn_tc_fwd(p, status, (cudaStream_t)stream);
 }
 
 extern "C" int dr_window_attn_bwd_workspace_bytes(const dr_attn_desc *desc, size_t *bytes) {

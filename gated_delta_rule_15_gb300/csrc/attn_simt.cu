@@ -356,10 +356,6 @@ int bwd(const AttnProblem &p, cudaStream_t s) {
 
 int launch_attn_simt_fwd(const AttnProblem &p, cudaStream_t s) {
     const int64_t blocks = attn_tile_slots(p.seqs, kTile) * p.Hq;
-    using bf = __nv_bfloat16;
-    if (p.bf16)
-        return p.d == 64 ? launch(attn_simt_fwd_kernel<64, bf>, smem_bytes<64>(2), blocks, p, s)
-                         : launch(attn_simt_fwd_kernel<128, bf>, smem_bytes<128>(2), blocks, p, s);
     return p.d == 64 ? launch(attn_simt_fwd_kernel<64, float>, smem_bytes<64>(2), blocks, p, s)
                      : launch(attn_simt_fwd_kernel<128, float>, smem_bytes<128>(2), blocks, p, s);
 }

@@ -1,0 +1,87 @@
+// attn_tc.cuh -- what the tensor-core kernels of the window attention share: tensor maps, bounded waits,
+// masks and the key tiles of a run of queries.  The mathematics: attn.h.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attn.h"
+#include "common.cuh"
+#include "tc_common.cuh"
+#include "tc_issue.cuh"
+
+namespace dr {
+
+PFN_cuTensorMapEncodeTiled_v12000 tc_tensor_map_encoder();
+
+namespace attn {
+
+using namespace umma;
+using tc::elect_one;
+using tc::ex2;
+using tc::pack_bf16;
+
+constexpr int kSms = 152, kKeys = 128, kBox = 32;   // key tile; rows of a copy
+
+// [rows, heads, d] bf16, rows `stride` elements apart; boxes of 64 channels x `heads_box` x `rows_box`, 128-byte
+// swizzle.  Rows behind the last read as zeros.
+inline bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t heads, int64_t d, int64_t stride, int heads_box, int rows_box) {
+    auto enc = tc_tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows_box}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query heads (of those that share a key head) whose rows lie side by side in a tile of 128 rows, a
+// power of two: tiles then span fewer tokens, and less of what they compute is masked.
+inline int heads_in_tile(int group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// Which of the keys j0 .. j0 + 31 the query i sees, of those before `end`.
+__device__ __forceinline__ uint32_t seen_bits(int i, int j0, int end, int window, int sinks) {
+    return low_bits(min(i + 1, end) - j0) & (~low_bits(i - window + 1 - j0) | low_bits(sinks - j0));
+}
+
+// The key tiles of the queries q0 .. q0 + count - 1 of a sequence: sinks in front of the first one's window, then the
+// keys from there to the last one.
+struct KeyTiles {
+    int sinks, n_sink, near0, end, n;
+    __device__ __forceinline__ KeyTiles(int q0, int count, int len, int window, int all_sinks) {
+        near0 = max(0, q0 - window + 1);
+        sinks = min(all_sinks, near0);
+        end = min(len, q0 + count);
+        n_sink = (sinks + kKeys - 1) / kKeys;
+        n = n_sink + (end - near0 + kKeys - 1) / kKeys;
+    }
+    __device__ __forceinline__ int first(int t) const { return t < n_sink ? t * kKeys : near0 + (t - n_sink) * kKeys; }
+    __device__ __forceinline__ int stop(int t) const { return t < n_sink ? min(sinks, (t + 1) * kKeys) : min(end, first(t) + kKeys); }
+    // whether one of the queries a .. b - 1 sees a key of tile t
+    __device__ __forceinline__ bool meets(int t, int a, int b, int window, int all_sinks) const {
+        if (a >= b) return false;
+        const int k0 = first(t);
+        return t < n_sink || (k0 < b && (k0 + kKeys > a - window + 1 || k0 < all_sinks));
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
+}  // namespace attn
+
+// Tensor cores: bf16 rows.  `status`: the library's device status word.
+int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream);
+
+}  // namespace dr

@@ -1,0 +1,407 @@
+// attn_tc_fwd.cu -- forward of the window attention on the 5th-generation tensor cores (tcgen05,
+// TMEM, TMA) for bf16 rows.  The mathematics: attn.h.
+//
+// A block takes two tiles of 128 query rows (stages 0 and 1) that share their key tiles; it runs
+// through items of that kind (a run of tokens, a key head, up to four of its query heads side by side).
+//     S = Q K^T        [128 x 128]   both from shared memory, S in tensor memory
+//     O += P V         [128 x d]     P (bf16) from tensor memory, over S's place; V as loaded (MN-major)
+// The running softmax: a thread holds a row; with f = scale log2 e and m the row's reference, p = 2^(f s - f m), and
+// O and l hold the sums for that m.  m follows the row's maximum only when that is more than 2^8 above it
+// (p stays below 2^8, exact as a power-of-two-free rescale would be), so O in tensor memory is rescaled
+// a few times a row at most.  A row's decisions depend on the row alone.
+//
+// Warps 0..3 and 4..7 are the stages' softmax and write their outputs; warp 8 issues the copies, warp 9 the
+// MMAs: O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of the next tile, in turn, so that one stage's
+// softmax runs while the tensor cores work for the other.
+//
+// Rows of other sequences: their keys are masked; their values, which enter the product as 0 times
+// whatever they hold, are overwritten with zeros in shared memory in a sequence's last tile.
+// A parity wait tells a phase from its neighbours only: no barrier completes a second time before everyone who
+// waits for it has seen the first.
+// Every wait is bounded: on expiry the kernel records DR_ERR_TIMEOUT, runs its remaining steps
+// without waiting, drains its copies and MMAs, frees its tensor memory and returns.
+#include "attn_tc.cuh"
+
+namespace dr {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9;
+// Registers a thread: launched with 168; the softmax warps take what the others give back.
+constexpr int kSoftRegs = 208, kIssueRegs = 80;
+static_assert(8 * kSoftRegs + 4 * kIssueRegs <= 12 * 168, "register split");
+
+struct FwdArgs {
+    AttnProblem p;
+    int *status;
+    int gp, runs;          // query heads side by side; runs of them in a key head's group
+    int tokens;            // of an item: 2 * 128 / gp
+    int64_t items;
+};
+
+// What the load warp tells the others of an item.
+struct Item {
+    int lo, len, q0, h0;   // first row of the sequence, its length (-1: no more items), first token, first query head
+};
+
+template <int D>
+struct Layout {
+    static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;   // key and value buffers
+    static constexpr uint32_t Q = 0, KV = 2 * TILE, BARS = KV + NB * TILE;
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 12) * 8 + 2 * sizeof(Item);
+    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                const FwdArgs a) {
+    using L = Layout<D>;
+    constexpr int NB = L::NB;
+    extern __shared__ unsigned char dsm_raw[];
+    unsigned char *sm = align1024(dsm_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
+    uint64_t *b_full = bars, *b_free = bars + NB;        // [NB] a key or value tile is there, is done with
+    uint64_t *b_q = bars + 2 * NB, *b_qfree = b_q + 2;   // [2] the stage's queries (and the item)
+    uint64_t *b_s = b_q + 4, *b_p = b_q + 6, *b_o = b_q + 8;   // [2] S is there; P is; O is complete
+    uint64_t *b_end = b_q + 10;
+    Item *items = reinterpret_cast<Item *>(b_q + 12);    // [2]
+    __shared__ uint32_t tmem_s;
+    __shared__ int polls_s;
+    const AttnProblem &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_q + i, 1);
+            mbar_init(b_qfree + i, 1 + 4);   // the MMAs, and every softmax warp has seen the item
+            mbar_init(b_s + i, 1);
+            mbar_init(b_p + i, 4);
+            mbar_init(b_o + i, 1);
+        }
+        mbar_init(b_end, 1);
+        polls_s = tc::kPolls;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_s, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_s;
+    volatile int *polls = &polls_s;
+    // `k`-th completion of a barrier (k = 0, 1, ..); after an expiry nobody waits any more
+    auto wait = [&](uint64_t *bar, int k) {
+        if (!mbar_try_wait(bar, k & 1)) tc::wait_longer(bar, k & 1, polls);
+        tc_fence_after();
+    };
+    auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
+    const int tt = a.tokens / 2;       // tokens of a stage
+
+    if (warp < 8) {
+        tc::more_regs<kSoftRegs>();
+        // ---------------------------------------------------------------- softmax
+        const int st = warp >> 2, row = tid & 127, quarter = warp & 3;
+        const uint32_t tS = tm + ((uint32_t)(32 * quarter) << 16) + 128 * st, tO = tS + 256;
+        const float f = p.scale * kLog2e;
+        int n_tile = 0, n_out = 0, ring = 0;   // tiles and results of this stage so far; copies
+#pragma unroll 1
+        for (int it = 0;; ++it) {
+            wait(b_q + st, it);
+            const Item im = items[it & 1];
+            if (im.len < 0 || *polls == 0) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_qfree + st);
+            const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+            const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt), i = ta + row / a.gp;
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+#pragma unroll 1
+            for (int t = 0; t < kt.n; ++t) {
+                if (!kt.meets(t, ta, tb, p.window, p.sinks)) continue;
+                const int k0 = kt.first(t), stop = kt.stop(t), kc = stop - k0;
+                const bool whole = kc == kKeys && stop - 1 <= ta && (k0 > tb - 1 - p.window || stop <= p.sinks);
+                wait(b_s + st, n_tile);
+                ++n_tile;
+                float s[128];
+                float2 sum = make_float2(0.f, 0.f);
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (32 * c < kc) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+                tmem_wait_ld();
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (32 * c >= kc) continue;
+                        const uint32_t bits = seen_bits(i, k0 + 32 * c, stop, p.window, p.sinks);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) s[32 * c + x] = bits >> x & 1 ? s[32 * c + x] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (32 * c >= kc) continue;
+                    float u = -INFINITY, v = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        u = max3(u, s[32 * c + x], s[32 * c + x + 1]);
+                        v = max3(v, s[32 * c + x + 2], s[32 * c + x + 3]);
+                    }
+                    top = max3(top, u, v);
+                }
+                // the row's reference follows its maximum
+                const bool up = (top - m) * f > 8.f;       // (also from -infinity; not where both are)
+                if (__any_sync(0xffffffffu, up)) {
+                    const float turn = up ? ex2((m - top) * f) : 1.f;
+                    l *= turn;
+                    m = up ? top : m;
+                    if (!first) {       // S is there, so the products before it are done
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(tO + 32 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; x += 2) {
+                                const float2 y = mul2(make_float2(o[x], o[x + 1]), make_float2(turn, turn));
+                                o[x] = y.x;
+                                o[x + 1] = y.y;
+                            }
+                            tmem_st32(tO + 32 * c, o);
+                        }
+                    }
+                }
+                first = false;
+                const float base = m == -INFINITY ? 0.f : -m * f;
+                const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (32 * c >= kc) continue;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int at = 32 * c + 16 * e + 2 * x;
+                            float2 y = fma2(make_float2(s[at], s[at + 1]), f2, b2);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum = add2(sum, y);
+                            w[x] = pack_bf16(y.x, y.y);
+                        }
+                        tmem_st4u(tS + 16 * c + 8 * e, *reinterpret_cast<uint32_t(*)[4]>(w));
+                        tmem_st4u(tS + 16 * c + 8 * e + 4, *reinterpret_cast<uint32_t(*)[4]>(w + 4));
+                    }
+                }
+                l += sum.x + sum.y;
+                // values of rows behind the sequence's end that the product takes in are zeros
+                const int kc16 = (kc + 15) & ~15;
+                if (k0 + kc16 > im.len) {
+                    const int v = ring + 2 * t + 1;
+                    wait_ring(b_full, v);
+                    const uint32_t V = smem_u32(sm) + L::KV + (v % NB) * L::TILE;
+                    const int r0 = im.len - k0, n = (kc16 - r0) * 8;
+                    for (int x = row; x < L::PANELS * n; x += 128) {
+                        const int r = r0 + x % n / 8;
+                        sts128(V + (x / n) * 16384 + r * 128 + (x % 8) * 16, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p + st);
+            }
+            ring += 2 * kt.n;
+            if (ta < tb) {
+                wait(b_o + st, n_out++);
+                const bool mine = i < im.len;
+                const int h = im.h0 + row % a.gp;
+                const float inv = 1.f / l;
+                const int64_t at = (int64_t)(im.lo + i) * p.Hq + h;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) w[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+                    if (mine) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            reinterpret_cast<uint4 *>(dst + 32 * c)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    }
+                }
+                if (mine) p.lse[at] = (m * f + log2f(l)) * kLn2;
+            }
+            tc_fence_before();     // (the next item's first P follows)
+        }
+    } else {
+        tc::fewer_regs<kIssueRegs>();
+        if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- copies
+            int it = 0, ring = 0;
+            auto load = [&](int k, const CUtensorMap *map, int hk, int row0, int rows) {   // by one lane
+                const int b = k % NB;
+                if (k >= NB) wait(b_free + b, k / NB - 1);
+                const int boxes = (rows + kBox - 1) / kBox;
+                unsigned char *dst = sm + L::KV + b * L::TILE;
+                mbar_arrive_expect_tx(b_full + b, boxes * kBox * 128 * L::PANELS);
+                for (int e = 0; e < L::PANELS; ++e)
+                    for (int x = 0; x < boxes; ++x)
+                        tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, row0 + x * kBox);
+            };
+#pragma unroll 1
+            for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+                // long rows of keys first: the last tokens of all sequences, then the ones before them
+                const int nh = p.Hk * a.runs;
+                const int hr = (int)(k % nh);
+                int64_t n, lo;
+                int j, len;
+                if (p.seqs.cu) {
+                    if (!find_tile(p.seqs, a.tokens, (int)(k / nh), n, j, lo, len)) continue;
+                } else {
+                    const int per = (int)((p.seqs.T + a.tokens - 1) / a.tokens);
+                    j = per - 1 - (int)(k / nh / p.seqs.N);
+                    n = k / nh % p.seqs.N;
+                    lo = n * p.seqs.T;
+                    len = (int)p.seqs.T;
+                }
+                const int hk = hr / a.runs, q0 = j * a.tokens;
+                const Item im{(int)lo, len, q0, hk * (p.Hq / p.Hk) + (hr % a.runs) * a.gp};
+                const KeyTiles kt(q0, a.tokens, len, p.window, p.sinks);
+                if (elect_one()) {
+                    for (int st = 0; st < 2; ++st) {
+                        if (it > 0) wait(b_qfree + st, it - 1);
+                        if (st == 0) items[it & 1] = im;
+                        mbar_arrive_expect_tx(b_q + st, L::TILE);
+                        for (int e = 0; e < L::PANELS; ++e)
+                            tc::tma_load_3d(sm + L::Q + st * L::TILE + e * 16384, &tq, b_q + st, 64 * e, im.h0, im.lo + q0 + st * tt);
+                        if (st == 0) load(ring, &tk, hk, im.lo + kt.first(0), kt.stop(0) - kt.first(0));
+                    }
+                    for (int t = 0; t < kt.n; ++t) {
+                        if (t > 0) load(ring + 2 * t, &tk, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                        load(ring + 2 * t + 1, &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                    }
+                }
+                __syncwarp();
+                ring += 2 * kt.n;
+                ++it;
+            }
+            if (elect_one()) {
+                // the loads have landed before the block ends, also after an expiry
+                for (int k = max(0, ring - NB); k < ring; ++k) tc::wait_cycles(b_full + k % NB, (k / NB) & 1);
+                for (int st = 0; st < 2; ++st) {
+                    if (it > 0) {
+                        wait(b_qfree + st, it - 1);
+                        tc::wait_cycles(b_q + st, (it - 1) & 1);
+                    }
+                    if (st == 0) items[it & 1].len = -1;
+                    mbar_arrive(b_q + st);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- MMAs
+            if (elect_one()) {
+                const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
+                const uint64_t dV = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+                constexpr uint32_t ID_PV = idesc_bf16(128, D, false, true);
+                int ring = 0, n_p[2] = {0, 0};
+#pragma unroll 1
+                for (int it = 0;; ++it) {
+                    wait(b_q, it);
+                    const Item im = items[it & 1];
+                    if (im.len < 0 || *polls == 0) break;
+                    wait(b_q + 1, it);
+                    const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+                    int pend[2] = {-1, -1};
+                    bool more[2] = {false, false};
+                    auto flush = [&](int st) {     // O += P V of the tile whose S went before
+                        if (pend[st] < 0) return;
+                        const int t = pend[st], v = ring + 2 * t + 1, ks = (kt.stop(t) - kt.first(t) + 15) / 16;
+                        wait_ring(b_full, v);
+                        wait(b_p + st, n_p[st]++);
+                        const uint64_t dv = desc_add(dV, L::KV + (v % NB) * L::TILE);
+                        const uint32_t d = tm + 256 + 128 * st, src = tm + 128 * st;
+#pragma unroll 1
+                        for (int k = 0; k < ks; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
+                        more[st] = true;
+                        pend[st] = -1;
+                    };
+#pragma unroll 1
+                    for (int t = 0; t < kt.n; ++t) {
+                        const int k = ring + 2 * t, n16 = (kt.stop(t) - kt.first(t) + 15) & ~15;
+                        wait_ring(b_full, k);
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            const int ta = im.q0 + st * tt;
+                            flush(st);
+                            if (st == 1 && t > 0) mma_commit(b_free + (k - 1) % NB);
+                            if (!kt.meets(t, ta, min(im.len, ta + tt), p.window, p.sinks)) continue;
+                            const uint64_t dq = desc_add(dK, L::Q + st * L::TILE), dk = desc_add(dK, L::KV + (k % NB) * L::TILE);
+                            const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16 - 16) << 14);
+#pragma unroll
+                            for (int e = 0; e < D / 16; ++e)
+                                mma_bf16(tm + 128 * st, desc_add(dq, (e >> 2) * 16384 + (e & 3) * 32),
+                                         desc_add(dk, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
+                            mma_commit(b_s + st);
+                            pend[st] = t;
+                        }
+                        mma_commit(b_free + k % NB);
+                    }
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) mma_commit(b_qfree + st);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        flush(st);
+                        if (im.q0 + st * tt < im.len) mma_commit(b_o + st);
+                    }
+                    ring += 2 * kt.n;
+                    mma_commit(b_free + (ring - 1) % NB);
+                }
+                mma_commit(b_end);
+                tc::wait_cycles(b_end, 0);      // every MMA is done
+                if (*polls == 0) atomicExch(a.status, kErrTimeout);
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+int launch(const CUtensorMap *m, const FwdArgs &a, cudaStream_t s) {
+    constexpr int smem = Layout<D>::TOTAL + 1024;
+    if (cudaFuncSetAttribute(attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return kErrCuda;
+    attn_fwd_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kThreads, smem, s>>>(m[0], m[1], m[2], a);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+}  // namespace
+}  // namespace attn
+
+int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream) {
+    using namespace attn;
+    FwdArgs a{};
+    a.p = p;
+    a.status = status;
+    a.gp = heads_in_tile(p.Hq / p.Hk);
+    a.runs = p.Hq / p.Hk / a.gp;
+    a.tokens = 256 / a.gp;
+    a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
+    CUtensorMap m[3];
+    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, a.gp, 128 / a.gp) ||
+        !make_map(&m[1], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[2], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
+        return kErrCuda;
+    return p.d == 64 ? launch<64>(m, a, stream) : launch<128>(m, a, stream);
+}
+
+}  // namespace dr
