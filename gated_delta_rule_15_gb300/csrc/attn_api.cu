@@ -54,7 +54,11 @@ AttnProblem problem_of(const dr_attn_desc &d, const int64_t *cu) {
     return p;
 }
 
-size_t bwd_bytes(const dr_attn_desc &d) { return sizeof(float) * (size_t)(d.B * d.T * d.Hq); }
+size_t bwd_bytes(const dr_attn_desc &d) {
+    static const int64_t packed = 0;     // packed or not, not where the offsets lie
+    if (d.dtype == DR_BF16) return attn_tc_bwd_workspace_bytes(problem_of(d, &packed));
+    return sizeof(float) * (size_t)(d.B * d.T * d.Hq);
+}
 
 int check_step(const dr_attn_step_desc *d) {
     if (!d) return kErrInvalid;
@@ -169,7 +173,10 @@ extern "C" int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const
         const int rz = launch_attn_zero_rest(p.seqs, r, (cudaStream_t)stream);
         if (rz != kOk) return rz;
     }
-    return launch_attn_simt_bwd(p, (cudaStream_t)stream);
+    if (!p.bf16) return launch_attn_simt_bwd(p, (cudaStream_t)stream);
+    int *status = device_status_ptr();
+    if (!status) return kErrCuda;
+    return launch_attn_tc_bwd(p, workspace, status, (cudaStream_t)stream);
 }
 
 extern "C" int dr_window_attn_step_workspace_bytes(const dr_attn_step_desc *desc, size_t *bytes) {

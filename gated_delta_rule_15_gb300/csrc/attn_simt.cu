@@ -361,8 +361,6 @@ int launch_attn_simt_fwd(const AttnProblem &p, cudaStream_t s) {
 }
 
 int launch_attn_simt_bwd(const AttnProblem &p, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    if (p.bf16) return p.d == 64 ? bwd<64, bf>(p, s) : bwd<128, bf>(p, s);
     return p.d == 64 ? bwd<64, float>(p, s) : bwd<128, float>(p, s);
 }
 

@@ -83,5 +83,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // Tensor cores: bf16 rows.  `status`: the library's device status word.
 int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream);
+size_t attn_tc_bwd_workspace_bytes(const AttnProblem &p);   // (by seqs.cu being NULL or not, not what it holds)
+int launch_attn_tc_bwd(const AttnProblem &p, void *workspace, int *status, cudaStream_t stream);
 
 }  // namespace dr

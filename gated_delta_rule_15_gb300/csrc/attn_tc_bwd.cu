@@ -1,0 +1,769 @@
+// attn_tc_bwd.cu -- gradients of the window attention on the 5th-generation tensor cores (tcgen05,
+// TMEM, TMA) for bf16 rows.  The mathematics: attn.h.
+//
+// Two kernels, so that no sum depends on the order of blocks (one kernel would add dq up in memory from
+// many blocks); scores and do.v are formed in both, seven products a tile instead of five.
+//
+// dq: an item is 128 query rows (as in the forward); of each of its key tiles
+//     S = Q K^T,  dP = dO V^T     [128 x 128]
+//     dQ += dS K                  dS (bf16) from tensor memory, over S's place; K as loaded (MN-major)
+// with two places for S, so that the products of the next tile run while the softmax warps form dS; a
+// thread holds half a row.  Two more warps form delta = do.o an item ahead and leave it, with lse in
+// log2, in the order of tiles for the second kernel.
+//
+// dk, dv: a block takes 128 keys of a head and runs over the tiles of 128 query rows that see one of them, all
+// heads of the group one after another:
+//     S^T = K Q^T,  dP^T = V dO^T
+//     dV += P^T dO,  dK += dS^T Q       P^T, dS^T (bf16) from tensor memory over S's, dP's place; dO, Q as loaded
+// While the softmax warps form P^T of a tile the tensor cores work at the tile before (dK) and the
+// products of V, and the other way round.
+// Sinks are seen by every later query: the tiles of keys that hold some would take as long as the sequence is. What
+// lies behind their window is cut into chunks of queries, whose blocks leave fp32 sums for the sinks' rows that a last
+// kernel adds up in order.
+//
+// Rows of other sequences are masked; where they enter a product as 0 times whatever they hold they are
+// overwritten with zeros in shared memory.  Waits are bounded as in the forward.
+#include "attn_tc.cuh"
+
+namespace dr {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kStatWarp = 10;
+constexpr int kMaxSplitTiles = 8;      // key tiles with sinks that are cut
+
+struct BwdArgs {
+    AttnProblem p;
+    int *status;
+    int gp, runs, tokens;      // query heads side by side, runs of them, tokens of 128 rows
+    int64_t items;             // dq: items; dk, dv: blocks that are not chunks
+    float2 *stats;             // [key head and run][row][gp] (lse log2 e, delta)
+    // sinks: 0 tiles where they are not cut
+    int sink_tiles, sink_rows, chunk;
+    int64_t chunk_slots;
+    float *base, *parts;       // [n | chunk slot][Hk][sink tile][sink row][dk, dv][d]
+};
+
+struct Item {
+    int lo, len, q0, h0, hr;   // first row of the sequence, its length (-1: no more items), first token, first query head, run
+};
+
+// The k-th item of dq; long rows of keys first.  By whole warps; false for none.
+__device__ __forceinline__ bool item_of(const BwdArgs &a, int64_t k, Item &im) {
+    const AttnProblem &p = a.p;
+    const int nh = p.Hk * a.runs;
+    int64_t n, lo;
+    int j, len;
+    im.hr = (int)(k % nh);
+    if (p.seqs.cu) {
+        if (!find_tile(p.seqs, a.tokens, (int)(k / nh), n, j, lo, len)) return false;
+    } else {
+        const int per = (int)((p.seqs.T + a.tokens - 1) / a.tokens);
+        j = per - 1 - (int)(k / nh / p.seqs.N);
+        n = k / nh % p.seqs.N;
+        lo = n * p.seqs.T;
+        len = (int)p.seqs.T;
+    }
+    im.lo = (int)lo;
+    im.len = len;
+    im.q0 = j * a.tokens;
+    im.h0 = im.hr / a.runs * (p.Hq / p.Hk) + im.hr % a.runs * a.gp;
+    return true;
+}
+
+// Zeros into the rows r0 .. r1 - 1 of a tile of 128-byte rows in panels of 16 KB, by 256 threads.
+template <int PANELS>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int r1, int t) {
+    const int n = (r1 - r0) * 8;
+    for (int x = t; x < PANELS * n; x += 256) sts128(tile + (x / n) * 16384 + (r0 + x % n / 8) * 128 + (x % 8) * 16, 0, 0, 0, 0);
+    fence_proxy_async();
+}
+
+// bf16 rows of 32 accumulator columns times f
+__device__ __forceinline__ void put32(__nv_bfloat16 *dst, const float (&o)[32], float f) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        reinterpret_cast<uint4 *>(dst)[x] = make_uint4(pack_bf16(o[8 * x] * f, o[8 * x + 1] * f), pack_bf16(o[8 * x + 2] * f, o[8 * x + 3] * f),
+                                                       pack_bf16(o[8 * x + 4] * f, o[8 * x + 5] * f), pack_bf16(o[8 * x + 6] * f, o[8 * x + 7] * f));
+}
+
+// ------------------------------------------------------------------ dq
+template <int D>
+struct DqLayout {
+    static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;
+    static constexpr uint32_t Q = 0, O = TILE, KV = 2 * TILE, BARS = KV + NB * TILE;
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 12) * 8 + 2 * sizeof(Item);
+    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tk,
+               const __grid_constant__ CUtensorMap tv, const BwdArgs a) {
+    using L = DqLayout<D>;
+    constexpr int NB = L::NB;
+    extern __shared__ unsigned char dsm_raw[];
+    unsigned char *sm = align1024(dsm_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
+    uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a key or value tile is there, is done with
+    uint64_t *b_q = bars + 2 * NB, *b_qfree = b_q + 1; // the item and its rows are there, are done with
+    uint64_t *b_s = b_q + 2, *b_dp = b_q + 4, *b_ds = b_q + 5, *b_dq = b_q + 6;   // [2] S; dP; dS; dQ is complete
+    uint64_t *b_stat = b_q + 7, *b_sfree = b_q + 9;    // [2] the rows' statistics are there, are read
+    uint64_t *b_end = b_q + 11;
+    Item *items = reinterpret_cast<Item *>(b_q + 12);  // [2]
+    __shared__ uint32_t tmem_s;
+    __shared__ int polls_s;
+    const AttnProblem &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        mbar_init(b_q, 1);
+        mbar_init(b_qfree, 1 + 8);       // the MMAs, and every softmax warp has seen the item
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_s + i, 1);
+            mbar_init(b_stat + i, 2);
+            mbar_init(b_sfree + i, 8);
+        }
+        mbar_init(b_dp, 1);
+        mbar_init(b_ds, 8);
+        mbar_init(b_dq, 1);
+        mbar_init(b_end, 1);
+        polls_s = tc::kPolls;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_s, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_s;
+    constexpr uint32_t TM_DP = 256, TM_DQ = 384;
+    volatile int *polls = &polls_s;
+    auto wait = [&](uint64_t *bar, int k) {
+        if (!mbar_try_wait(bar, k & 1)) tc::wait_longer(bar, k & 1, polls);
+        tc_fence_after();
+    };
+    auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- dS
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), col0 = 64 * half;
+        const float f = p.scale * kLog2e;
+        int n_tile = 0;
+#pragma unroll 1
+        for (int it = 0;; ++it) {
+            wait(b_q, it);
+            const Item im = items[it & 1];
+            if (im.len < 0 || *polls == 0) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_qfree);
+            const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+            const int i = im.q0 + row / a.gp;
+            wait(b_stat + (it & 1), it >> 1);
+            const float2 stat = i < im.len ? a.stats[((int64_t)im.hr * p.seqs.total + im.lo + i) * a.gp + row % a.gp] : make_float2(0.f, 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_sfree + (it & 1));
+            const float2 f2 = make_float2(f, f), l2 = make_float2(-stat.x, -stat.x), d2 = make_float2(-stat.y, -stat.y);
+#pragma unroll 1
+            for (int t = 0; t < kt.n; ++t, ++n_tile) {
+                const int k0 = kt.first(t), stop = kt.stop(t), kc = stop - k0, kc16 = (kc + 15) & ~15;
+                const bool whole = kc == kKeys && stop - 1 <= im.q0 && (k0 > kt.end - 1 - p.window || stop <= p.sinks);
+                const uint32_t tS = tl + 128 * (n_tile & 1) + col0;
+                float s[64];
+                wait(b_s + (n_tile & 1), n_tile >> 1);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if ((int)col0 + 32 * c < kc) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 64; x += 2) {
+                    const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, l2);
+                    s[x] = ex2(y.x);
+                    s[x + 1] = ex2(y.y);
+                }
+                if (k0 + kc16 > im.len) zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (2 * n_tile % NB) * L::TILE, im.len - k0, kc16, tid);
+                wait(b_dp, n_tile);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if ((int)col0 + 32 * c >= kc) continue;
+                    float dp[32];
+                    tmem_ld32(tl + TM_DP + col0 + 32 * c, dp);
+                    tmem_wait_ld();
+                    const uint32_t bits = whole ? 0xffffffffu : seen_bits(i, k0 + (int)col0 + 32 * c, stop, p.window, p.sinks);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float2 y = mul2(make_float2(s[32 * c + x], s[32 * c + x + 1]), add2(make_float2(dp[x], dp[x + 1]), d2));
+                        if (!whole) {
+                            y.x = bits >> x & 1 ? y.x : 0.f;
+                            y.y = bits >> x & 2 ? y.y : 0.f;
+                        }
+                        w[x / 2] = pack_bf16(y.x, y.y);
+                    }
+                    tmem_st16u(tS + 16 * c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_ds);
+            }
+            wait(b_dq, it);
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.dq) + (int64_t)(im.lo + i) * p.dqs + (im.h0 + row % a.gp) * D + half * (D / 2);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                float o[32];
+                tmem_ld32(tl + TM_DQ + half * (D / 2) + 32 * c, o);
+                tmem_wait_ld();
+                if (i < im.len) put32(dst + 32 * c, o, p.scale);
+            }
+            tc_fence_before();
+        }
+    } else if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- copies
+        int it = 0, ring = 0;
+        auto load = [&](int k, const CUtensorMap *map, int hk, int row0, int rows) {   // by one lane
+            const int b = k % NB;
+            if (k >= NB) wait(b_free + b, k / NB - 1);
+            const int boxes = (rows + kBox - 1) / kBox;
+            unsigned char *dst = sm + L::KV + b * L::TILE;
+            mbar_arrive_expect_tx(b_full + b, boxes * kBox * 128 * L::PANELS);
+            for (int e = 0; e < L::PANELS; ++e)
+                for (int x = 0; x < boxes; ++x)
+                    tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, row0 + x * kBox);
+        };
+#pragma unroll 1
+        for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+            Item im;
+            if (!item_of(a, k, im)) continue;
+            const int hk = im.hr / a.runs;
+            const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+            if (elect_one()) {
+                if (it > 0) wait(b_qfree, it - 1);
+                items[it & 1] = im;
+                mbar_arrive_expect_tx(b_q, 2 * L::TILE);
+                for (int e = 0; e < L::PANELS; ++e) {
+                    tc::tma_load_3d(sm + L::Q + e * 16384, &tq, b_q, 64 * e, im.h0, im.lo + im.q0);
+                    tc::tma_load_3d(sm + L::O + e * 16384, &to, b_q, 64 * e, im.h0, im.lo + im.q0);
+                }
+                for (int t = 0; t < kt.n; ++t) {
+                    load(ring + 2 * t, &tk, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                    load(ring + 2 * t + 1, &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                }
+            }
+            __syncwarp();
+            ring += 2 * kt.n;
+            ++it;
+        }
+        if (elect_one()) {
+            // the loads have landed before the block ends, also after an expiry
+            for (int k = max(0, ring - NB); k < ring; ++k) tc::wait_cycles(b_full + k % NB, (k / NB) & 1);
+            if (it > 0) {
+                wait(b_qfree, it - 1);
+                tc::wait_cycles(b_q, (it - 1) & 1);
+            }
+            items[it & 1].len = -1;
+            mbar_arrive(b_q);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMAs
+        if (elect_one()) {
+            const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
+            const uint64_t dM = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+            constexpr uint32_t ID_DQ = idesc_bf16(128, D, false, true);
+            int ring = 0, n_tile = 0;
+#pragma unroll 1
+            for (int it = 0;; ++it) {
+                wait(b_q, it);
+                const Item im = items[it & 1];
+                if (im.len < 0 || *polls == 0) break;
+                const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+                auto n16 = [&](int t) { return (kt.stop(t) - kt.first(t) + 15) & ~15; };
+                auto rows_by_rows = [&](uint32_t d, uint32_t left, int k, int t) {
+                    const uint64_t da = desc_add(dK, left), db = desc_add(dK, L::KV + (k % NB) * L::TILE);
+                    const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16(t) - 16) << 14);
+                    wait_ring(b_full, k);
+#pragma unroll
+                    for (int e = 0; e < D / 16; ++e)
+                        mma_bf16(d, desc_add(da, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
+                };
+                auto scores = [&](int t) {
+                    rows_by_rows(tm + 128 * ((n_tile + t) & 1), L::Q, ring + 2 * t, t);
+                    mma_commit(b_s + ((n_tile + t) & 1));
+                };
+                auto dps = [&](int t) {
+                    rows_by_rows(tm + TM_DP, L::O, ring + 2 * t + 1, t);
+                    mma_commit(b_dp);
+                    mma_commit(b_free + (ring + 2 * t + 1) % NB);
+                };
+                scores(0);
+                dps(0);
+                if (kt.n > 1) scores(1);
+                else mma_commit(b_qfree);
+#pragma unroll 1
+                for (int t = 0; t < kt.n; ++t) {
+                    wait(b_ds, n_tile + t);
+                    if (t + 1 < kt.n) {
+                        dps(t + 1);
+                        if (t + 2 == kt.n) mma_commit(b_qfree);
+                    }
+                    const int k = ring + 2 * t, ks = n16(t) / 16;
+                    const uint64_t db = desc_add(dM, L::KV + (k % NB) * L::TILE);
+                    const uint32_t src = tm + 128 * ((n_tile + t) & 1);
+#pragma unroll 1
+                    for (int e = 0; e < ks; ++e)
+                        mma_bf16_ts(tm + TM_DQ, src + 8 * e + (e >= 4 ? 32 : 0), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                    mma_commit(b_free + k % NB);
+                    if (t + 2 < kt.n) scores(t + 2);
+                }
+                mma_commit(b_dq);
+                ring += 2 * kt.n;
+                n_tile += kt.n;
+            }
+            mma_commit(b_end);
+            tc::wait_cycles(b_end, 0);      // every MMA is done
+            if (*polls == 0) atomicExch(a.status, kErrTimeout);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- lse and delta of the rows
+        constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // lanes a row, rows a warp's access
+        const int l = lane % LPR;
+        int it = 0;
+#pragma unroll 1
+        for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+            Item im;
+            if (!item_of(a, k, im)) continue;
+            if (it > 1) wait(b_sfree + (it & 1), (it >> 1) - 1);
+#pragma unroll 1
+            for (int r0 = 64 * (warp - kStatWarp); r0 < 64 * (warp - kStatWarp) + 64; r0 += U * RPW) {
+                uint4 o[U], d[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + r / a.gp;
+                    o[u] = d[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < im.len) {
+                        const int64_t at = ((int64_t)(im.lo + i) * p.Hq + im.h0 + r % a.gp) * D + 8 * l;
+                        o[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.out) + at);
+                        d[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.d_out) + at);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + r / a.gp;
+                    const uint32_t x[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, y[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                        sum = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), sum);
+                    }
+#pragma unroll
+                    for (int w = 1; w < LPR; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                    if (l == 0 && i < im.len)
+                        a.stats[((int64_t)im.hr * p.seqs.total + im.lo + i) * a.gp + r % a.gp] =
+                            make_float2(p.lse[(int64_t)(im.lo + i) * p.Hq + im.h0 + r % a.gp] * kLog2e, sum);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_stat + (it & 1));
+            ++it;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+}
+
+// ------------------------------------------------------------------ dk, dv
+template <int D>
+struct DkvLayout {
+    static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 4 : 10, NS = 4;   // query-side tiles, statistics
+    static constexpr uint32_t K = 0, V = TILE, QO = 2 * TILE, STATS = QO + NB * TILE, BARS = STATS + NS * 128 * 8;
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 2 * NS + 6) * 8;
+    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const BwdArgs a) {
+    using L = DkvLayout<D>;
+    constexpr int NB = L::NB, NS = L::NS;
+    const AttnProblem &p = a.p;
+    // what this block does: key tile jt of sequence n, queries qa .. qb - 1
+    int64_t n, lo;
+    int jt, len, hk, chunk = -1;
+    int64_t slot = 0;
+    if ((int64_t)blockIdx.x < a.items) {
+        hk = (int)(blockIdx.x % p.Hk);
+        const int64_t k = blockIdx.x / p.Hk;
+        if (p.seqs.cu) {
+            if (!find_tile(p.seqs, kKeys, (int)k, n, jt, lo, len)) return;
+        } else {       // early keys, which most queries see, first
+            n = k % p.seqs.N;
+            jt = (int)(k / p.seqs.N);
+            lo = n * p.seqs.T;
+            len = (int)p.seqs.T;
+        }
+    } else {
+        int64_t k = blockIdx.x - a.items;
+        hk = (int)(k % p.Hk);
+        k /= p.Hk;
+        jt = (int)(k % a.sink_tiles);
+        slot = k / a.sink_tiles;
+        if (!find_tile(p.seqs, a.chunk, (int)slot, n, chunk, lo, len)) return;
+    }
+    const int k0 = jt * kKeys;
+    if (k0 >= len) return;
+    const int behind = min(len, min(k0 + kKeys - 1, kNoWindow - 1) + p.window);     // behind the last query whose window reaches the tile
+    const bool sink = k0 < p.sinks, cut = sink && jt < a.sink_tiles && behind < len;
+    int qa = k0, qb = sink && !cut ? len : behind;
+    if (chunk >= 0) {
+        qa = max(behind, chunk * a.chunk);
+        qb = min(len, (chunk + 1) * a.chunk);
+        if (!cut || qa >= qb) return;
+    }
+    const int nt = (qb - qa + a.tokens - 1) / a.tokens, tiles = nt * a.runs;
+
+    extern __shared__ unsigned char dsm_raw[];
+    unsigned char *sm = align1024(dsm_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
+    uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a query or d_out tile is there, is done with
+    uint64_t *b_stat = bars + 2 * NB, *b_sfree = b_stat + NS;   // [NS] the tile's statistics
+    uint64_t *b_kv = b_sfree + NS, *b_s = b_kv + 1, *b_p = b_kv + 2, *b_dp = b_kv + 3, *b_ds = b_kv + 4, *b_end = b_kv + 5;
+    float2 *stats = reinterpret_cast<float2 *>(sm + L::STATS);   // [NS][128]
+    __shared__ uint32_t tmem_s;
+    __shared__ int polls_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(b_stat + i, 1);
+            mbar_init(b_sfree + i, 8);
+        }
+        mbar_init(b_kv, 1);
+        mbar_init(b_s, 1);
+        mbar_init(b_p, 8);
+        mbar_init(b_dp, 1);
+        mbar_init(b_ds, 8);
+        mbar_init(b_end, 1);
+        polls_s = tc::kPolls;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_s, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_s;
+    constexpr uint32_t TM_DP = 128, TM_DV = 256, TM_DK = 384;
+    volatile int *polls = &polls_s;
+    auto wait = [&](uint64_t *bar, int k) {
+        if (!mbar_try_wait(bar, k & 1)) tc::wait_longer(bar, k & 1, polls);
+        tc_fence_after();
+    };
+    auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
+    auto first_of = [&](int t) { return qa + t % nt * a.tokens; };
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- P^T, dS^T
+        const int quarter = warp & 3, half = warp >> 2, j = k0 + 32 * quarter + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), col0 = 64 * half;
+        const float f = p.scale * kLog2e;
+        const float2 f2 = make_float2(f, f);
+        const int see = min(qb, j < p.sinks ? len : min(j, kNoWindow - 1) + p.window);    // behind the last query that sees this key
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const int q0 = first_of(t);
+            const bool whole = q0 >= k0 + kKeys - 1 && q0 + a.tokens <= qb && (q0 + a.tokens - 1 - k0 < p.window || k0 + kKeys <= p.sinks);
+            const float4 *st = reinterpret_cast<const float4 *>(stats + (t % NS) * 128 + col0);
+            float s[64];
+            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+            if (!whole) {
+                const int lo_c = max(j - q0, 0), hi_c = min(see - q0, 128);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int at = (int)col0 + 32 * c;
+                    bits[c] = low_bits(hi_c * a.gp - at) & ~low_bits(min(lo_c, 128) * a.gp - at);
+                }
+            }
+            wait(b_stat + t % NS, t / NS);
+            wait(b_s, t);
+            tmem_ld32(tl + col0, *reinterpret_cast<float(*)[32]>(s));
+            tmem_ld32(tl + col0 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float4 l = st[16 * c + x / 2];
+                    const float2 y = fma2(make_float2(s[32 * c + x], s[32 * c + x + 1]), f2, make_float2(-l.x, -l.z));
+                    float u = ex2(y.x), v = ex2(y.y);
+                    if (!whole) {
+                        u = bits[c] >> x & 1 ? u : 0.f;
+                        v = bits[c] >> x & 2 ? v : 0.f;
+                    }
+                    s[32 * c + x] = u;
+                    s[32 * c + x + 1] = v;
+                    w[x / 2] = pack_bf16(u, v);
+                }
+                tmem_st16u(tl + col0 + 16 * c, w);
+            }
+            if (q0 + a.tokens > len) {     // rows of no query of this sequence are zeros
+                wait_ring(b_full, 2 * t + 1);
+                for (int e = 0; e < 2; ++e)
+                    zero_rows<L::PANELS>(smem_u32(sm) + L::QO + ((2 * t + e) % NB) * L::TILE, (len - q0) * a.gp, 128, tid);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_p);
+            wait(b_dp, t);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float dp[32];
+                tmem_ld32(tl + TM_DP + col0 + 32 * c, dp);
+                tmem_wait_ld();
+                uint32_t w[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float4 l = st[16 * c + x / 2];
+                    float2 y = mul2(make_float2(s[32 * c + x], s[32 * c + x + 1]), add2(make_float2(dp[x], dp[x + 1]), make_float2(-l.y, -l.w)));
+                    if (!whole) {      // (the product of rows of others may be anything)
+                        y.x = bits[c] >> x & 1 ? y.x : 0.f;
+                        y.y = bits[c] >> x & 2 ? y.y : 0.f;
+                    }
+                    w[x / 2] = pack_bf16(y.x, y.y);
+                }
+                tmem_st16u(tl + TM_DP + col0 + 16 * c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(b_ds);
+                mbar_arrive(b_sfree + t % NS);
+            }
+        }
+        wait(b_end, 0);
+        // out: a sink's row is a part of a sum where its queries are cut
+        const bool part = cut && j < p.sinks;
+        float *sum = nullptr;
+        if (part) sum = (chunk >= 0 ? a.parts : a.base) + ((((chunk >= 0 ? slot : n) * p.Hk + hk) * a.sink_tiles + jt) * a.sink_rows + (j - k0)) * 2 * D;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {      // dk, dv
+            const float scale = e == 0 ? p.scale : 1.f;
+            __nv_bfloat16 *dst = e == 0 ? static_cast<__nv_bfloat16 *>(p.dk) + (lo + j) * p.dks : static_cast<__nv_bfloat16 *>(p.dv) + (lo + j) * p.dvs;
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                const int at = half * (D / 2) + 32 * c;
+                float o[32];
+                tmem_ld32(tl + (e == 0 ? TM_DK : TM_DV) + at, o);
+                tmem_wait_ld();
+                if (j >= len) continue;
+                if (part) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        store4(sum + e * D + at + x, make_float4(o[x] * scale, o[x + 1] * scale, o[x + 2] * scale, o[x + 3] * scale));
+                } else if (chunk < 0) {
+                    put32(dst + hk * D + at, o, scale);
+                }
+            }
+        }
+    } else if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- copies
+        if (elect_one()) {
+            mbar_arrive_expect_tx(b_kv, 2 * L::TILE);
+            for (int e = 0; e < L::PANELS; ++e)
+                for (int x = 0; x < kKeys / kBox; ++x) {
+                    tc::tma_load_3d(sm + L::K + e * 16384 + x * kBox * 128, &tk, b_kv, 64 * e, hk, (int)lo + k0 + x * kBox);
+                    tc::tma_load_3d(sm + L::V + e * 16384 + x * kBox * 128, &tv, b_kv, 64 * e, hk, (int)lo + k0 + x * kBox);
+                }
+            int issued = 0;
+#pragma unroll 1
+            for (; issued < 2 * tiles; ++issued) {
+                const int b = issued % NB, t = issued / 2;
+                if (issued >= NB) wait(b_free + b, issued / NB - 1);
+                if (*polls == 0) break;
+                mbar_arrive_expect_tx(b_full + b, L::TILE);
+                const int h0 = hk * (p.Hq / p.Hk) + t / nt * a.gp;
+                for (int e = 0; e < L::PANELS; ++e)
+                    tc::tma_load_3d(sm + L::QO + b * L::TILE + e * 16384, issued & 1 ? &to : &tq, b_full + b, 64 * e, h0, (int)lo + first_of(t));
+            }
+            // the loads have landed before the block ends, also after an expiry
+            tc::wait_cycles(b_kv, 0);
+            for (int k = max(0, issued - NB); k < issued; ++k) tc::wait_cycles(b_full + k % NB, (k / NB) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMAs
+        if (elect_one()) {
+            const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
+            const uint64_t dM = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+            constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_D = idesc_bf16(128, D, false, true);
+            auto rows_by_rows = [&](uint32_t d, uint32_t left, int k) {
+                const uint64_t da = desc_add(dK, left), db = desc_add(dK, L::QO + (k % NB) * L::TILE);
+                wait_ring(b_full, k);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e)
+                    mma_bf16(d, desc_add(da, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), ID_S, e > 0);
+            };
+            auto sums = [&](uint32_t d, uint32_t src, int k, bool more) {
+                const uint64_t db = desc_add(dM, L::QO + (k % NB) * L::TILE);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mma_bf16_ts(d, src + 8 * e + (e >= 4 ? 32 : 0), desc_add(db, e * 2048), ID_D, more || e > 0);
+                mma_commit(b_free + k % NB);
+            };
+            wait(b_kv, 0);
+            rows_by_rows(tm, L::K, 0);
+            mma_commit(b_s);
+            rows_by_rows(tm + TM_DP, L::V, 1);
+            mma_commit(b_dp);
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t) {
+                wait(b_p, t);
+                sums(tm + TM_DV, tm, 2 * t + 1, t > 0);
+                if (t + 1 < tiles) {
+                    rows_by_rows(tm, L::K, 2 * t + 2);
+                    mma_commit(b_s);
+                }
+                wait(b_ds, t);
+                sums(tm + TM_DK, tm + TM_DP, 2 * t, t > 0);
+                if (t + 1 < tiles) {
+                    rows_by_rows(tm + TM_DP, L::V, 2 * t + 3);
+                    mma_commit(b_dp);
+                }
+            }
+            mma_commit(b_end);
+            tc::wait_cycles(b_end, 0);      // every MMA is done
+            if (*polls == 0) atomicExch(a.status, kErrTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kStatWarp) {
+        // ---------------------------------------------------------------- statistics of the queries
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const int q0 = first_of(t);
+            const float2 *src = a.stats + ((int64_t)(hk * a.runs + t / nt) * p.seqs.total + lo + q0) * a.gp;
+            const int rows = min(len - q0, a.tokens) * a.gp;
+            float2 x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = lane + 32 * e < rows ? src[lane + 32 * e] : make_float2(0.f, 0.f);
+            if (t >= NS) wait(b_sfree + t % NS, t / NS - 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stats[(t % NS) * 128 + lane + 32 * e] = x[e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_stat + t % NS);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+}
+
+// The sinks' rows: what their window gave and the chunks, in order.  A block a key tile of a sequence and head.
+template <int D>
+__global__ void __launch_bounds__(256) attn_sink_sum_kernel(const BwdArgs a) {
+    const AttnProblem &p = a.p;
+    int64_t k = blockIdx.x, lo, hi;
+    const int jt = (int)(k % a.sink_tiles);
+    k /= a.sink_tiles;
+    const int hk = (int)(k % p.Hk);
+    const int64_t n = k / p.Hk;
+    seq_range(p.seqs, n, lo, hi);
+    const int len = (int)(hi - lo), k0 = jt * kKeys, rows = min(a.sink_rows, min(p.sinks, len) - k0);
+    const int behind = min(len, min(k0 + kKeys - 1, kNoWindow - 1) + p.window);
+    if (rows <= 0 || behind >= len) return;
+    const int64_t slot0 = p.seqs.cu ? lo / a.chunk + n : n * ((p.seqs.T + a.chunk - 1) / a.chunk);
+    const int c0 = behind / a.chunk, c1 = (len + a.chunk - 1) / a.chunk;
+    const int64_t tile = ((int64_t)hk * a.sink_tiles + jt) * a.sink_rows * 2 * D, step = (int64_t)p.Hk * a.sink_tiles * a.sink_rows * 2 * D;
+    for (int x = threadIdx.x; x < rows * 2 * D / 4; x += 256) {
+        float4 s = load4(a.base + n * step + tile + 4 * x);
+#pragma unroll 4
+        for (int c = c0; c < c1; ++c) {
+            const float4 y = load4(a.parts + (slot0 + c) * step + tile + 4 * x);
+            s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+        }
+        const int row = 4 * x / (2 * D), at = 4 * x % (2 * D);
+        const int64_t r = lo + k0 + row;
+        __nv_bfloat16 *dst = at < D ? static_cast<__nv_bfloat16 *>(p.dk) + r * p.dks + hk * D + at
+                                    : static_cast<__nv_bfloat16 *>(p.dv) + r * p.dvs + hk * D + at - D;
+        store4(dst, s);
+    }
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// How the sinks' queries are cut, and where the workspace's parts lie.
+size_t plan(const AttnProblem &p, BwdArgs &a, char *ws) {
+    a.p = p;
+    a.gp = heads_in_tile(p.Hq / p.Hk);
+    a.runs = p.Hq / p.Hk / a.gp;
+    a.tokens = 128 / a.gp;
+    size_t at = 0;
+    a.stats = (float2 *)(ws + at);
+    at += round256(sizeof(float2) * (size_t)(p.seqs.total * p.Hq));
+    const int64_t longest = p.seqs.cu ? p.seqs.total : p.seqs.T, sinks = p.sinks < longest ? p.sinks : longest;
+    const int64_t tiles = (sinks + kKeys - 1) / kKeys;
+    // (nobody is behind the window of the first tile of the longest sequence: nothing to cut)
+    if (p.window < kNoWindow && sinks > 0 && tiles <= kMaxSplitTiles && longest > p.window + kKeys - 1) {
+        a.sink_tiles = (int)tiles;
+        a.sink_rows = (int)(sinks < kKeys ? sinks : kKeys);
+        const int64_t own = p.window + kKeys;      // about as long as a block without sinks
+        a.chunk = (int)(((own < 1024 ? 1024 : own) + kKeys - 1) / kKeys * kKeys);
+        a.chunk_slots = p.seqs.cu ? p.seqs.total / a.chunk + p.seqs.N : p.seqs.N * ((p.seqs.T + a.chunk - 1) / a.chunk);
+        const size_t one = sizeof(float) * (size_t)p.Hk * a.sink_tiles * a.sink_rows * 2 * p.d;
+        a.base = (float *)(ws + at);
+        at += round256(one * p.seqs.N);
+        a.parts = (float *)(ws + at);
+        at += round256(one * a.chunk_slots);
+    }
+    return at;
+}
+
+template <int D>
+int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
+    CUtensorMap m[4];
+    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, a.gp, 128 / a.gp) ||
+        !make_map(&m[1], p.d_out, p.seqs.total, p.Hq, p.d, (int64_t)p.Hq * p.d, a.gp, 128 / a.gp) ||
+        !make_map(&m[2], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[3], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
+        return kErrCuda;
+    constexpr int smem_q = DqLayout<D>::TOTAL + 1024, smem_kv = DkvLayout<D>::TOTAL + 1024;
+    if (cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess)
+        return kErrCuda;
+    a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
+    attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
+    if (cudaGetLastError() != cudaSuccess) return kErrCuda;
+    a.items = attn_tile_slots(p.seqs, kKeys) * p.Hk;
+    const int64_t blocks = a.items + a.chunk_slots * p.Hk * a.sink_tiles;
+    attn_dkv_kernel<D><<<(unsigned)blocks, kThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
+    if (cudaGetLastError() != cudaSuccess) return kErrCuda;
+    if (a.sink_tiles == 0) return kOk;
+    attn_sink_sum_kernel<D><<<(unsigned)(p.seqs.N * p.Hk * a.sink_tiles), 256, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+
+}  // namespace
+}  // namespace attn
+
+size_t attn_tc_bwd_workspace_bytes(const AttnProblem &p) {
+    attn::BwdArgs a{};
+    return attn::plan(p, a, nullptr);
+}
+
+int launch_attn_tc_bwd(const AttnProblem &p, void *workspace, int *status, cudaStream_t stream) {
+    attn::BwdArgs a{};
+    attn::plan(p, a, (char *)workspace);
+    a.status = status;
+    return p.d == 64 ? attn::launch<64>(p, a, stream) : attn::launch<128>(p, a, stream);
+}
+
+}  // namespace dr

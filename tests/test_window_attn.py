@@ -129,7 +129,8 @@ SHAPES = [  # B, T, Hq, Hk, d, window, sinks
     (1, 127, 2, 2, 64, 0, 0), (2, 128, 2, 1, 128, 128, 0), (2, 129, 4, 2, 128, 64, 4), (1, 255, 1, 1, 64, 30, 40),
     (1, 257, 6, 2, 64, 100, 3), (1, 300, 8, 1, 128, 130, 200), (1, 400, 2, 2, 128, 1, 1), (1, 513, 2, 1, 64, 512, 0),
     (1, 640, 3, 3, 128, 128, 128), (3, 200, 2, 1, 64, 1000, 5), (1, 384, 2, 1, 128, 0, 7), (1, 520, 2, 1, 64, 7, 130),
-    (1, 641, 1, 1, 128, 129, 1), (1, 256, 16, 1, 64, 200, 16)]
+    (1, 641, 1, 1, 128, 129, 1), (1, 256, 16, 1, 64, 200, 16),
+    (1, 2500, 2, 1, 64, 40, 5), (2, 1400, 2, 1, 128, 200, 200), (1, 2300, 1, 1, 64, 50, 1100), (1, 1500, 3, 1, 64, 0, 0)]
 
 
 @pytest.mark.gpu
@@ -140,7 +141,7 @@ def test_forward_and_gradients(dr, B, T, Hq, Hk, d, window, sinks, dtype):
 
 
 PACKED = [([0, 100, 100, 101, 257, 700, 700], 720), ([0, 1], 1), ([0, 0, 64, 128, 129], 129), ([5, 130, 131, 400], 411),
-          ([0, 3, 5, 9, 10, 11, 12, 40, 41, 47], 50), ([0, 0, 0], 30), ([0, 640], 640)]
+          ([0, 3, 5, 9, 10, 11, 12, 40, 41, 47], 50), ([0, 0, 0], 30), ([0, 640], 640), ([0, 1300, 1310, 3500], 3600)]
 
 
 @pytest.mark.gpu
