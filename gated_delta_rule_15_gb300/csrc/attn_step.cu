@@ -3,15 +3,16 @@
 //
 // Every visible key and value is read once: HBM bandwidth bounds it.  The visible tokens of a unit (a
 // sequence, a key head and up to 16 of the query heads that share it) are cut into groups of 16 (fp32: 8), which never
-// cross a page: first the groups that hold sinks, then those of the window.  The units' groups, one
-// after another, are dealt out evenly: block c takes the groups c * per .. (c + 1) * per - 1, whatever
-// units they belong to, so that one long context fills the GPU as a batch does.  A unit that ends up
-// in several blocks leaves a partial result (maximum, sum, sum of values) in each, which a second kernel joins
-// in a fixed order.
+// cross a page: first the groups that hold sinks, then those of the window.  The units, one behind another,
+// are dealt out evenly to all warps of the GPU, a unit counting as its groups and one more for what it costs to
+// begin and end: a warp takes a run of groups, whatever units they belong to, so that one long context fills the
+// GPU as a batch of any lengths does.  A unit that ends up in several warps leaves a partial result (maximum, sum,
+// sum of values) for each, or for a block whose warps all work at it one, and a second kernel joins them in a fixed
+// order.  (Blocks as the takers, all their warps at one unit and their states added up at its end, took 2126 us
+// for 256 sequences of 16 to 16384 tokens: a block with the short ones spent 7 us on each.)
 //
-// Inside a block the warps take every eighth group, each with copies of its own: a tensor-map box of
-// a group's keys, one of its values, into a ring of kStages stages, so 192 KB are under way on an SM, and no
-// warp waits for another one but at a unit's end, where their states are added up.
+// A warp copies its groups by a tensor-map box of the group's keys and one of its values into a ring of
+// kStages stages of its own, so 192 KB are under way on an SM, and no warp waits for another one.
 //   bf16: S = Q K^T and O += P V as 16 x 8 x 16 tensor-core products of one warp (the query heads are the
 //   16 rows); P enters as two bf16 terms (2^-17 of a value is lost), which costs a memory-bound kernel
 //   nothing.
@@ -38,20 +39,21 @@ using namespace umma;
 
 constexpr int kWarps = 8, kStages = 3, kThreads = 32 * kWarps, kHeads = 16, kBlocks = 152;
 template <bool BF> constexpr int group_tokens() { return BF ? 16 : 8; }   // 8 KB of keys and values at d = 128
-constexpr int kLeast = kWarps;       // groups of a block, at least: one a warp
+constexpr int kLeast = 2;            // groups of a warp, at least
+constexpr int kUnitCost = 1;         // what a unit's begin and end count as, in groups
 
-// What a block leaves for the joining kernel: per row the maximum (log2) and the sum, then the values' sums.
-constexpr int kPartialFloats = kHeads * (128 + 2);
-struct Tail {                        // the unit that a block began and did not end
+struct Tail {                        // the unit that a warp (or a block, by its first warp) began and did not end
     int64_t b;                       // -1: none
-    int hu, last;                    // unit of the sequence, last block that has a part of it
+    int64_t first, end, per, total;  // its place in the row of all units; what a warp takes; the row's length
+    int hu;                          // unit of the sequence
 };
 
 struct StepArgs {
     AttnStep p;
     int hus, per_h;                  // units a sequence, units a key head
-    float *partial;                  // [block][head or tail part]
-    Tail *tail;                      // [block]
+    float *partial;                  // [warp][head or tail part] of part_floats: [rows][d] sums, [rows] (maximum, sum)
+    int part_floats;
+    Tail *tail;                      // [warp]
     int *status;
 };
 
@@ -77,20 +79,44 @@ struct Seen {
     }
 };
 
-// A place in the row of all units' groups.
+// Walks the units of a warp's run [begin, end) of the row of all units.
 template <int G>
-struct Cursor {
+struct Walk {
     int64_t b, first;                // sequence; where its current unit begins
-    int hu, n;                       // unit of the sequence; groups of the unit
-    __device__ __forceinline__ void seek(const StepArgs &a, int64_t at) {   // forwards, to the unit that holds group `at`
-        while (at >= first + n) {
-            first += n;
-            if (++hu == a.hus) {
-                hu = 0;
-                ++b;
-                n = b < a.p.B ? Seen<G>(a.p, a.p.lens[b]).n : 0x7fffffff;
-            }
+    int hu;                          // unit of the sequence
+    int lo, hi;                      // the unit's groups that are in the run
+    Seen<G> seen;
+    __device__ __forceinline__ Walk(const StepArgs &a, int64_t b0, int64_t first0, int64_t begin, int64_t end)
+        : b(b0), first(first0), hu(0), lo(0), hi(0), seen(a.p, b0 < a.p.B ? a.p.lens[b0] : 0) {
+        while (b < a.p.B && first + (seen.n > 0 ? a.hus * (seen.n + kUnitCost) : 0) <= begin) {   // whole sequences in front of it
+            if (seen.n > 0) first += a.hus * (seen.n + kUnitCost);
+            ++b;
+            seen = Seen<G>(a.p, b < a.p.B ? a.p.lens[b] : 0);
         }
+        if (seen.n > 0) {
+            hu = (int)((begin - first) / (seen.n + kUnitCost));
+            first += (int64_t)hu * (seen.n + kUnitCost);
+        }
+        cut(begin, end);
+    }
+    __device__ __forceinline__ void cut(int64_t begin, int64_t end) {
+        const int64_t l = begin - first - kUnitCost, h = end - first - kUnitCost;
+        lo = (int)max((int64_t)0, l);
+        hi = (int)min((int64_t)seen.n, h);
+    }
+    // On to the next unit; false behind the run.
+    __device__ __forceinline__ bool next(const StepArgs &a, int64_t begin, int64_t end) {
+        first += seen.n + kUnitCost;
+        if (first >= end) return false;
+        if (++hu == a.hus) {
+            hu = 0;
+            do {
+                ++b;
+                seen = Seen<G>(a.p, a.p.lens[b]);
+            } while (seen.n == 0);
+        }
+        cut(begin, end);
+        return true;
     }
 };
 
@@ -109,7 +135,7 @@ struct State<D, true> {
     static constexpr int KSTEPS = D / 16;
     uint32_t q[KSTEPS][4];
     float o[D / 8][4], m[2], l[2];
-    __device__ __forceinline__ void begin(const StepArgs &a, const Cursor<16> &u, int lane) {
+    __device__ __forceinline__ void begin(const StepArgs &a, const Walk<16> &u, int lane) {
         const int g = a.p.Hq / a.p.Hk, hk = u.hu / a.per_h, h0 = (u.hu % a.per_h) * kHeads;
         const __nv_bfloat16 *src = (const __nv_bfloat16 *)a.p.q + (u.b * a.p.Hq + hk * g + h0) * D + 2 * (lane & 3);
         const int r = lane >> 2;
@@ -130,7 +156,7 @@ struct State<D, true> {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
-    __device__ __forceinline__ void group(const StepArgs &a, const Seen<16> &seen, int j0, const unsigned char *stage, int lane, const float *) {
+    __device__ __forceinline__ void group(const StepArgs &a, const Seen<16> &seen, int j0, const unsigned char *stage, int lane, int64_t) {
         const uint32_t K = smem_u32(stage), V = K + D * 32;
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         const int mat = lane >> 3, row = lane & 7;
@@ -209,22 +235,37 @@ struct State<D, true> {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
     }
-    // [16][D] sums, then [16] maxima and sums
-    __device__ __forceinline__ void put(float *dst, int lane) const {
+    // [rows][D] sums, then [rows] maxima and sums
+    __device__ __forceinline__ void put(float *dst, int rows, int lane) const {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = (lane >> 2) + 8 * r;
+            if (row >= rows) continue;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
                 *reinterpret_cast<float2 *>(dst + row * D + 8 * i + 2 * (lane & 3)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-            if ((lane & 3) == 0) *reinterpret_cast<float2 *>(dst + kHeads * D + 2 * row) = make_float2(m[r], l[r]);
+            if ((lane & 3) == 0) *reinterpret_cast<float2 *>(dst + rows * D + 2 * row) = make_float2(m[r], l[r]);
         }
     }
-    __device__ __forceinline__ void add(const float *src, int lane) {
+    __device__ __forceinline__ void out(const AttnStep &p, int64_t head, int rows, int lane) const {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = (lane >> 2) + 8 * r;
-            const float2 ml = *reinterpret_cast<const float2 *>(src + kHeads * D + 2 * row);
+            if (row >= rows) continue;
+            const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + (head + row) * D + 2 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint32_t *>(dst + 8 * i) = tc::pack_bf16(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
+            if (p.lse && (lane & 3) == 0) p.lse[head + row] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ void add(const float *src, int rows, int lane) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = (lane >> 2) + 8 * r;
+            if (row >= rows) continue;
+            const float2 ml = *reinterpret_cast<const float2 *>(src + rows * D + 2 * row);
             const float top = fmaxf(m[r], ml.x), base = top == -INFINITY ? 0.f : top;
             const float f = tc::ex2(m[r] - base), e = tc::ex2(ml.x - base);
             m[r] = top;
@@ -245,10 +286,9 @@ template <int D>
 struct State<D, false> {
     static constexpr int C = D / 32;
     float o[kHeads][C], m[kHeads], l[kHeads];
-    int rows;
-    __device__ __forceinline__ void begin(const StepArgs &a, const Cursor<8> &u, int) {
-        const int g = a.p.Hq / a.p.Hk;
-        rows = min(kHeads, g - (u.hu % a.per_h) * kHeads);
+    int rows;                        // query heads of the unit
+    __device__ __forceinline__ void begin(const StepArgs &a, const Walk<8> &u, int) {
+        rows = min(kHeads, a.p.Hq / a.p.Hk - (u.hu % a.per_h) * kHeads);
         reset();
     }
     __device__ __forceinline__ void reset() {
@@ -260,8 +300,9 @@ struct State<D, false> {
             for (int c = 0; c < C; ++c) o[h][c] = 0.f;
         }
     }
-    __device__ __forceinline__ void group(const StepArgs &a, const Seen<8> &seen, int j0, const unsigned char *stage, int lane, const float *q_s) {
-        const uint32_t K = smem_u32(stage), V = K + D * 32, Q = smem_u32(q_s);
+    __device__ __forceinline__ void group(const StepArgs &a, const Seen<8> &seen, int j0, const unsigned char *stage, int lane, int64_t head) {
+        const uint32_t K = smem_u32(stage), V = K + D * 32;
+        const float4 *Q = reinterpret_cast<const float4 *>(a.p.q) + head * (D / 4);   // (stays in L1)
         const int t = lane & 7, part = lane >> 3;
         const bool in = seen.sees(j0 + t), whole = seen.whole(j0);
         float s[kHeads];
@@ -274,7 +315,7 @@ struct State<D, false> {
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 if (h >= rows) break;
-                const float4 q = lds128f(Q + (h * D + 4 * c) * 4);
+                const float4 q = __ldg(Q + h * (D / 4) + c);
                 s[h] = fmaf(k.x, q.x, s[h]);
                 s[h] = fmaf(k.y, q.y, s[h]);
                 s[h] = fmaf(k.z, q.z, s[h]);
@@ -331,18 +372,30 @@ struct State<D, false> {
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
     }
-    __device__ __forceinline__ void put(float *dst, int lane) const {
+    __device__ __forceinline__ void put(float *dst, int n, int lane) const {
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
+            if (h >= n) break;
 #pragma unroll
             for (int c = 0; c < C; ++c) dst[h * D + C * lane + c] = o[h][c];
-            if (lane == 0) *reinterpret_cast<float2 *>(dst + kHeads * D + 2 * h) = make_float2(m[h], l[h]);
+            if (lane == 0) *reinterpret_cast<float2 *>(dst + n * D + 2 * h) = make_float2(m[h], l[h]);
         }
     }
-    __device__ __forceinline__ void add(const float *src, int lane) {
+    __device__ __forceinline__ void out(const AttnStep &p, int64_t head, int n, int lane) const {
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
-            const float2 ml = *reinterpret_cast<const float2 *>(src + kHeads * D + 2 * h);
+            if (h >= n) break;
+            const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) ((float *)p.out)[(head + h) * D + C * lane + c] = o[h][c] * inv;
+            if (p.lse && lane == 0) p.lse[head + h] = l[h] > 0.f ? (m[h] + log2f(l[h])) * kLn2 : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ void add(const float *src, int n, int lane) {
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            if (h >= n) break;
+            const float2 ml = *reinterpret_cast<const float2 *>(src + n * D + 2 * h);
             const float top = fmaxf(m[h], ml.x), base = top == -INFINITY ? 0.f : top;
             const float f = exp2f(m[h] - base), e = exp2f(ml.x - base);
             m[h] = top;
@@ -359,38 +412,38 @@ struct Layout {
     static constexpr int STAGES = kStages * 128 / D;                   // a warp's
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int PART = kHeads * (D + 2) * 4;                                 // a warp's state
-    static constexpr int PARTS = RING, Q = PARTS, BARS = PARTS + kWarps / 2 * PART;   // (fp32 queries in the states' place)
+    static constexpr int PARTS = RING, BARS = PARTS + kWarps / 2 * PART;
     static constexpr int TOTAL = BARS + kWarps * STAGES * 8;
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
-
-template <typename T>
-__device__ __forceinline__ void put_out(T *dst, float x) { *dst = from_f32<T>(x); }
 
 template <int D, bool BF>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const StepArgs a) {
     using L = Layout<D, BF>;
     using T = typename std::conditional<BF, __nv_bfloat16, float>::type;
+    constexpr int G = group_tokens<BF>();
     extern __shared__ unsigned char dsm_raw[];
     __shared__ int polls_s;
     unsigned char *sm = align1024(dsm_raw);
-    constexpr int G = group_tokens<BF>();
-    const float *q_s = reinterpret_cast<const float *>(sm + L::Q);
-    int64_t *sums = reinterpret_cast<int64_t *>(sm + L::PARTS);   // (until the first unit's end)
-    static_assert(8 * kThreads <= L::PART, "shared memory");
     const AttnStep &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *parts = reinterpret_cast<float *>(sm + L::PARTS);
+    int64_t *sums = reinterpret_cast<int64_t *>(sm + L::PARTS);   // [kThreads], [kWarps] (until the runs are known)
+    static_assert(8 * (kThreads + kWarps) <= kWarps / 2 * L::PART, "shared memory");
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS) + warp * L::STAGES;
     if (lane == 0)
         for (int i = 0; i < L::STAGES; ++i) mbar_init(bars + i, 1);
     if (tid == 0) polls_s = tc::kPolls;
     fence_mbar_init();
 
-    // the units' groups up to each of 256 runs of sequences
+    // what the units in front of each of 256 runs of sequences cost
     const int64_t run = (p.B + kThreads - 1) / kThreads;
     int64_t mine = 0;
-    for (int64_t b = tid * run; b < min(p.B, (tid + 1) * run); ++b) mine += Seen<G>(p, p.lens[b]).n;
+    for (int64_t b = tid * run; b < min(p.B, (tid + 1) * run); ++b) {
+        const int n = Seen<G>(p, p.lens[b]).n;
+        mine += n > 0 ? n + kUnitCost : 0;
+    }
     mine *= a.hus;
     int64_t upto = mine;
 #pragma unroll
@@ -398,185 +451,210 @@ attn_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, w);
         if (lane >= w) upto += x;
     }
-    __shared__ int64_t warps_s[kWarps];
-    if (lane == 31) warps_s[warp] = upto;
+    if (lane == 31) sums[kThreads + warp] = upto;
     __syncthreads();
     int64_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warps_s[w];
-        total += warps_s[w];
+        if (w < warp) before += sums[kThreads + w];
+        total += sums[kThreads + w];
     }
     sums[tid] = before + upto - mine;
     __syncthreads();
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t per = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
     per = per < kLeast ? kLeast : per;
-    const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
+    const int wid = blockIdx.x * kWarps + warp;
+    const int64_t block0 = min(total, (int64_t)blockIdx.x * kWarps * per), block1 = min(total, block0 + kWarps * per);
+    const int64_t begin = min(total, wid * per), end = min(total, begin + per);
 
     // sequences without a visible token
-    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+    for (int64_t b = wid; b < p.B; b += gridDim.x * kWarps) {
         if (Seen<G>(p, p.lens[b]).n > 0) continue;
-        for (int i = tid; i < p.Hq * D; i += kThreads) put_out((T *)p.out + b * p.Hq * D + i, 0.f);
-        for (int i = tid; p.lse && i < p.Hq; i += kThreads) p.lse[b * p.Hq + i] = -INFINITY;
+        for (int i = lane; i < p.Hq * D; i += 32) ((T *)p.out)[b * p.Hq * D + i] = from_f32<T>(0.f);
+        for (int i = lane; p.lse && i < p.Hq; i += 32) p.lse[b * p.Hq + i] = -INFINITY;
     }
-    if (tid == 0) a.tail[blockIdx.x].b = -1;
-    if (begin >= end) return;
+    if (lane == 0) a.tail[wid].b = -1;
+    if (block0 >= block1) return;
 
-    Cursor<G> load, cur;
-    {   // the last run that begins at or before `begin` and is not empty there
+    // the last run of sequences that begins at or before `at`
+    auto run_of = [&](int64_t at) {
         int lo = 0, hi = kThreads - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (sums[mid] <= begin) lo = mid;
+            if (sums[mid] <= at) lo = mid;
             else hi = mid - 1;
         }
-        cur.b = lo * run;
-        cur.first = sums[lo];
-        cur.hu = 0;
-        cur.n = cur.b < p.B ? Seen<G>(p, p.lens[cur.b]).n : 0x7fffffff;
-    }
-    __syncthreads();
-    cur.seek(a, begin);
-    load = cur;
+        return lo;
+    };
+    // (a warp without a run of its own stands where the block begins)
+    const int r = run_of(begin < end ? begin : block0);
+    Walk<G> u(a, r * run, sums[r], begin < end ? begin : block0, end);
+    // whether all warps work at one unit
+    const bool joint = block1 - block0 > per && u.first <= block0 && block1 <= u.first + u.seen.n + kUnitCost;
+    const bool all_joint = __syncthreads_and(joint);
 
     unsigned char *ring = sm + warp * L::STAGES * L::STAGE;
     const int rows_all = (int)(p.n_pages * p.Hk * p.page);   // behind the cache's end: zeros
-    int64_t next = begin + warp;          // group to load
+    Walk<G> load = u;
+    bool loading = begin < end;
     int issued = 0;
+    uint32_t there = 0;                   // of the stages: the group's page is there
     auto issue = [&]() {
-        if (next >= end) return;
-        load.seek(a, next);
+        while (loading && load.lo >= load.hi) loading = load.next(a, begin, end);
+        if (!loading) return;
+        const int j0 = load.seen.group(load.lo++) * G, s = issued % L::STAGES;
+        const int page = p.pages[load.b * p.max_pages + j0 / p.page];
+        const bool is = page >= 0 && page < p.n_pages;
+        there = (there & ~(1u << s)) | (uint32_t)is << s;
         if (lane == 0) {
-            const Seen<G> seen(p, p.lens[load.b]);
-            const int j0 = seen.group((int)(next - load.first)) * G;
-            const int page = p.pages[load.b * p.max_pages + j0 / p.page];
-            const int hk = load.hu / a.per_h;
-            const int row = page >= 0 && page < p.n_pages ? (int)(((int64_t)page * p.Hk + hk) * p.page + j0 % p.page) : rows_all;
-            const int s = issued % L::STAGES;
+            const int row = is ? (int)(((int64_t)page * p.Hk + load.hu / a.per_h) * p.page + j0 % p.page) : rows_all;
             mbar_arrive_expect_tx(bars + s, L::STAGE);
             tc::tma_load_3d(ring + s * L::STAGE, &tk, bars + s, 0, row, 0);
             tc::tma_load_3d(ring + s * L::STAGE + L::TILE, &tv, bars + s, 0, row, 0);
         }
         ++issued;
-        next += kWarps;
     };
 #pragma unroll 1
     for (int i = 0; i < L::STAGES; ++i) issue();
 
     State<D, BF> st;
-    float *parts = reinterpret_cast<float *>(sm + L::PARTS);
-    int64_t at = begin + warp;
     int done = 0;
 #pragma unroll 1
-    for (int64_t unit0 = begin; unit0 < end;) {
-        cur.seek(a, unit0);
-        const int64_t unit1 = min(end, cur.first + cur.n);
-        const Seen<G> seen(p, p.lens[cur.b]);
-        const int g = p.Hq / p.Hk, hk = cur.hu / a.per_h, h0 = (cur.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0);
-        const int64_t head = cur.b * p.Hq + hk * g + h0;
-        if (!BF) {
-            float *Q = reinterpret_cast<float *>(sm + L::Q);
-            for (int i = tid; i < rows * D; i += kThreads) Q[i] = ((const float *)p.q)[head * D + i];
-            __syncthreads();
-        }
-        st.begin(a, cur, lane);
+    for (bool more = begin < end; more || all_joint;) {
+        const int h0 = (u.hu % a.per_h) * kHeads, g = p.Hq / p.Hk, rows = min(kHeads, g - h0);
+        const int64_t head = u.b * p.Hq + u.hu / a.per_h * g + h0;
+        st.begin(a, u, lane);
+        const int lo = u.lo;
+        if (more) {
 #pragma unroll 1
-        for (; at < unit1; at += kWarps) {
-            const int s = done % L::STAGES;
-            const int j0 = seen.group((int)(at - cur.first)) * G;
-            // (a page that is not there is not visible)
-            const int page = p.pages[cur.b * p.max_pages + j0 / p.page];
-            if (!mbar_try_wait(bars + s, (done / L::STAGES) & 1)) tc::wait_longer(bars + s, (done / L::STAGES) & 1, &polls_s);
-            if (page >= 0 && page < p.n_pages) st.group(a, seen, j0, ring + s * L::STAGE, lane, q_s);
-            __syncwarp();
-            ++done;
-            issue();
+            for (; u.lo < u.hi; ++u.lo) {
+                const int s = done % L::STAGES, j0 = u.seen.group(u.lo) * G;
+                if (!mbar_try_wait(bars + s, (done / L::STAGES) & 1)) tc::wait_longer(bars + s, (done / L::STAGES) & 1, &polls_s);
+                if (there >> s & 1) st.group(a, u.seen, j0, ring + s * L::STAGE, lane, head);
+                __syncwarp();
+                ++done;
+                issue();
+            }
         }
         st.end();
-        if (!BF) __syncthreads();   // the queries are read
-        // the warps' states, the upper half's into the lower half's
+        bool begins = lo == 0, ends = u.hi == u.seen.n;
+        if (all_joint) {      // the warps' states, the upper half's into the lower half's
+            begins = block0 <= u.first + kUnitCost;
+            ends = block1 == u.first + u.seen.n + kUnitCost;
 #pragma unroll 1
-        for (int w = kWarps / 2; w > 0; w >>= 1) {
-            if (warp >= w && warp < 2 * w) st.put(parts + (warp - w) * (L::PART / 4), lane);
-            __syncthreads();
-            if (warp < w) st.add(parts + warp * (L::PART / 4), lane);
-            __syncthreads();
-        }
-        const bool starts = unit0 == cur.first, ends = unit1 == cur.first + cur.n;
-        if (warp == 0) st.put(starts && ends ? parts : a.partial + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * kPartialFloats, lane);
-        if (starts && ends) {
-            __syncthreads();
-            for (int i = tid; i < rows * D; i += kThreads) {
-                const float sum = parts[kHeads * D + 2 * (i / D) + 1];
-                put_out((T *)p.out + head * D + i, sum > 0.f ? parts[i] / sum : 0.f);
+            for (int w = kWarps / 2; w > 0; w >>= 1) {
+                if (warp >= w && warp < 2 * w) st.put(parts + (warp - w) * (L::PART / 4), rows, lane);
+                __syncthreads();
+                if (warp < w) st.add(parts + warp * (L::PART / 4), rows, lane);
+                __syncthreads();
             }
-            if (p.lse && tid < rows) {
-                const float2 ml = *reinterpret_cast<const float2 *>(parts + kHeads * D + 2 * tid);
-                p.lse[head + tid] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
-            }
-            __syncthreads();
-        } else if (starts && tid == 0) {
-            a.tail[blockIdx.x] = Tail{cur.b, cur.hu, (int)((cur.first + cur.n - 1) / per)};
         }
-        unit0 = unit1;
+        if ((all_joint && warp == 0) || (!all_joint && lo < u.hi)) {
+            if (begins && ends) {
+                st.out(p, head, rows, lane);
+            } else {
+                st.put(a.partial + ((int64_t)wid * 2 + (begins ? 1 : 0)) * a.part_floats, rows, lane);
+                if (begins && lane == 0) a.tail[wid] = Tail{u.b, u.first, u.first + u.seen.n + kUnitCost, per, total, u.hu};
+            }
+        }
+        if (all_joint) break;
+        more = u.next(a, begin, end);
     }
     // (after an expiry) the copies have landed before the block ends
     for (int i = max(0, issued - L::STAGES); i < issued; ++i) tc::wait_cycles(bars + i % L::STAGES, (i / L::STAGES) & 1);
-    if (tid == 0 && polls_s == 0) atomicExch(a.status, kErrTimeout);
+    if (lane == 0 && polls_s == 0) atomicExch(a.status, kErrTimeout);
 }
 
-// Joins the parts of the unit that block blockIdx.x began and other blocks went on with.
+// Joins the parts of the units that the warps of block blockIdx.x began and others went on with, one after another.
 template <int D, bool BF>
 __global__ void __launch_bounds__(512) attn_join_kernel(const StepArgs a) {
     using T = typename std::conditional<BF, __nv_bfloat16, float>::type;
-    const Tail tail = a.tail[blockIdx.x];
-    if (tail.b < 0) return;
-    __shared__ float weight[kBlocks][kHeads];
+    constexpr int kMost = kBlocks + 2 * kWarps;      // parts: a block's one, but for the first and last block's warps
+    __shared__ int slot_s[kMost], n_s;
+    __shared__ float weight[kMost][kHeads];
     __shared__ float4 sum_s[512];
     const AttnStep &p = a.p;
-    const int g = p.Hq / p.Hk, hk = tail.hu / a.per_h, h0 = (tail.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0);
-    const int64_t head = tail.b * p.Hq + hk * g + h0;
-    const int first = blockIdx.x, n = tail.last - first + 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto part = [&](int c) { return a.partial + ((int64_t)(first + c) * 2 + (c == 0 ? 1 : 0)) * kPartialFloats; };
-    // a warp a row: the parts' weights
-    if (warp < rows) {
-        float top = -INFINITY;
-        for (int c = lane; c < n; c += 32) top = fmaxf(top, part(c)[kHeads * D + 2 * warp]);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#pragma unroll 1
+    for (int own = 0; own < kWarps; ++own) {
+        const Tail tail = a.tail[blockIdx.x * kWarps + own];
+        if (tail.b < 0) continue;
+        __syncthreads();
+        const int g = p.Hq / p.Hk, h0 = (tail.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0);
+        const int64_t head = tail.b * p.Hq + tail.hu / a.per_h * g + h0;
+        // the parts' slots, in order
+        const int64_t group0 = tail.first + kUnitCost, per = tail.per;
+        const int block_a = (int)(group0 / (per * kWarps)), block_b = (int)((tail.end - 1) / (per * kWarps));
+        if (warp == 0) {
+            int n = 0;
+#pragma unroll 1
+            for (int c0 = block_a; c0 <= block_b; c0 += 32) {
+                const int c = c0 + lane;
+                int first = 0, count = 0;      // warps of the block that have a part
+                if (c <= block_b) {
+                    const int64_t x0 = c * per * kWarps, x1 = min(tail.total, x0 + per * kWarps);
+                    const bool joint = x1 - x0 > per && tail.first <= x0 && x1 <= tail.end;   // its warps left one part
+                    first = (int)max((int64_t)0, (group0 - x0) / per);
+                    count = joint ? 1 : (int)min((int64_t)kWarps, (tail.end - x0 + per - 1) / per) - first;
+                    if (joint) first = 0;
+                }
+                int at = count;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int c = lane; c < n; c += 32) {
-            const float e = exp2f(part(c)[kHeads * D + 2 * warp] - base);
-            weight[c][warp] = e;
-            sum = fmaf(part(c)[kHeads * D + 2 * warp + 1], e, sum);
+                for (int w = 1; w < 32; w <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, at, w);
+                    if (lane >= w) at += x;
+                }
+                const int all = __shfl_sync(0xffffffffu, at, 31);
+                at += n - count;
+                for (int e = 0; e < count; ++e) slot_s[at + e] = c * kWarps + first + e;
+                n += all;
+            }
+            if (lane == 0) n_s = n;
         }
+        __syncthreads();
+        const int n = n_s;
+        auto part = [&](int c) { return a.partial + ((int64_t)slot_s[c] * 2 + (c == 0 ? 1 : 0)) * a.part_floats; };
+        // a warp a row: the parts' weights
+        if (warp < rows) {
+            float top = -INFINITY;
+            for (int c = lane; c < n; c += 32) top = fmaxf(top, part(c)[rows * D + 2 * warp]);
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        __syncwarp();
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        for (int c = lane; c < n; c += 32) weight[c][warp] *= inv;
-        if (p.lse && lane == 0) p.lse[head + warp] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-    }
-    __syncthreads();
-    // four channels of a row a thread, the parts dealt out to the threads that are left
-    const int quads = rows * (D / 4), ways = 512 / quads, way = tid / quads, i = tid % quads, row = i / (D / 4);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (way < ways)
+            for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            for (int c = lane; c < n; c += 32) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part(c) + rows * D + 2 * warp);
+                const float e = exp2f(ml.x - base);
+                weight[c][warp] = e;
+                sum = fmaf(ml.y, e, sum);
+            }
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            __syncwarp();
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            for (int c = lane; c < n; c += 32) weight[c][warp] *= inv;
+            if (p.lse && lane == 0) p.lse[head + warp] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
+        // four channels of a row a thread, the parts dealt out to the threads that are left
+        const int quads = rows * (D / 4), ways = 512 / quads, way = tid / quads, i = tid % quads, row = i / (D / 4);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (way < ways)
 #pragma unroll 4
-        for (int c = way; c < n; c += ways) {
-            const float4 y = reinterpret_cast<const float4 *>(part(c))[i];
-            const float w = weight[c][row];
-            x.x = fmaf(w, y.x, x.x); x.y = fmaf(w, y.y, x.y); x.z = fmaf(w, y.z, x.z); x.w = fmaf(w, y.w, x.w);
+            for (int c = way; c < n; c += ways) {
+                const float4 y = reinterpret_cast<const float4 *>(part(c))[i];
+                const float w = weight[c][row];
+                x.x = fmaf(w, y.x, x.x); x.y = fmaf(w, y.y, x.y); x.z = fmaf(w, y.z, x.z); x.w = fmaf(w, y.w, x.w);
+            }
+        sum_s[tid] = x;
+        __syncthreads();
+        if (tid < quads) {
+            for (int c = 1; c < ways; ++c) {
+                const float4 y = sum_s[c * quads + tid];
+                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+            }
+            store4((T *)p.out + head * D + 4 * i, x);
         }
-    sum_s[tid] = x;
-    __syncthreads();
-    if (tid < quads) {
-        for (int c = 1; c < ways; ++c) {
-            const float4 y = sum_s[c * quads + tid];
-            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-        }
-        store4((T *)p.out + head * D + 4 * i, x);
     }
 }
 
@@ -595,7 +673,7 @@ bool make_map(CUtensorMap *m, const void *base, const AttnStep &p) {
 
 // Blocks: as many as the most groups that the sequences can have give work to.
 int blocks_of(const AttnStep &p) {
-    const int64_t G = p.bf16 ? 16 : 8;
+    const int64_t G = p.bf16 ? 16 : 8, least = kWarps * kLeast;
     const int64_t units = p.B * p.Hk * ((p.Hq / p.Hk + kHeads - 1) / kHeads);
     const int64_t room = ((int64_t)p.max_pages * p.page + G - 1) / G;
     int64_t groups = room;
@@ -603,10 +681,12 @@ int blocks_of(const AttnStep &p) {
         const int64_t seen = (p.window + G - 1) / G + 1 + (p.sinks + G - 1) / G;
         groups = seen < room ? seen : room;
     }
-    if (groups > kBlocks * kLeast || units > kBlocks * kLeast) return kBlocks;
-    const int64_t n = (units * groups + kLeast - 1) / kLeast;
-    return (int)(n < 1 ? 1 : n < kBlocks ? n : kBlocks);
+    if (groups > kBlocks * least || units > kBlocks * least) return kBlocks;
+    const int64_t n = (units * (groups + kUnitCost) + least - 1) / least;
+    return (int)(n < kBlocks ? n : kBlocks);
 }
+int part_rows(const AttnStep &p) { return p.Hq / p.Hk < kHeads ? p.Hq / p.Hk : kHeads; }
+int part_floats(const AttnStep &p) { return (part_rows(p) * (p.d + 2) + 3) / 4 * 4; }
 
 template <int D, bool BF>
 int launch(const CUtensorMap *m, const StepArgs &a, int blocks, cudaStream_t s) {
@@ -614,16 +694,14 @@ int launch(const CUtensorMap *m, const StepArgs &a, int blocks, cudaStream_t s) 
     if (cudaFuncSetAttribute(attn_step_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return kErrCuda;
     attn_step_kernel<D, BF><<<blocks, kThreads, smem, s>>>(m[0], m[1], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    if (blocks == 1) return kOk;
-    attn_join_kernel<D, BF><<<blocks - 1, 512, 0, s>>>(a);
+    attn_join_kernel<D, BF><<<blocks, 512, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
 
 }  // namespace
 
 size_t attn_step_workspace_bytes(const AttnStep &p) {
-    const int64_t n = blocks_of(p);
-    return (size_t)n * (2 * sizeof(float) * kPartialFloats + sizeof(Tail));
+    return (size_t)blocks_of(p) * kWarps * (2 * sizeof(float) * part_floats(p) + sizeof(Tail));
 }
 
 int launch_attn_step(const AttnStep &p, void *workspace, int *status, cudaStream_t stream) {
@@ -635,7 +713,8 @@ int launch_attn_step(const AttnStep &p, void *workspace, int *status, cudaStream
     a.per_h = (p.Hq / p.Hk + kHeads - 1) / kHeads;
     a.hus = p.Hk * a.per_h;
     a.partial = (float *)workspace;
-    a.tail = (Tail *)((char *)workspace + (size_t)blocks * 2 * sizeof(float) * kPartialFloats);
+    a.part_floats = part_floats(p);
+    a.tail = (Tail *)((char *)workspace + (size_t)blocks * kWarps * 2 * sizeof(float) * a.part_floats);
     a.status = status;
     if (p.bf16) return p.d == 64 ? launch<64, true>(m, a, blocks, stream) : launch<128, true>(m, a, blocks, stream);
     return p.d == 64 ? launch<64, false>(m, a, blocks, stream) : launch<128, false>(m, a, blocks, stream);
