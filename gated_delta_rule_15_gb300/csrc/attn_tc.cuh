@@ -79,6 +79,46 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+
+// 8 N bf16 values of one row a lane (32 rows a warp) to global memory: the lanes exchange 16-byte pieces within
+// groups of N, so that a group writes 16 N bytes of one row at a time.  `at(r)`: where this lane's columns' first
+// one of the warp's row r lies, or NULL.
+template <int N, class At>
+__device__ __forceinline__ void put_rows(uint4 (&u)[N], int lane, At at) {
+#pragma unroll
+    for (int b = 1; b < N; b <<= 1)
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+            if (s & b) continue;
+            const bool up = lane & b;
+            uint4 x = up ? u[s] : u[s | b];
+            x.x = __shfl_xor_sync(0xffffffffu, x.x, b);
+            x.y = __shfl_xor_sync(0xffffffffu, x.y, b);
+            x.z = __shfl_xor_sync(0xffffffffu, x.z, b);
+            x.w = __shfl_xor_sync(0xffffffffu, x.w, b);
+            if (up) u[s] = x;
+            else u[s | b] = x;
+        }
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        __nv_bfloat16 *dst = at((lane & ~(N - 1)) + r);
+        if (dst) reinterpret_cast<uint4 *>(dst)[lane & (N - 1)] = u[r];
+    }
+}
+// C accumulator columns times f as bf16 pieces
+template <int C>
+__device__ __forceinline__ void to_pieces(const float (&o)[C], float f, uint4 (&u)[C / 8]) {
+#pragma unroll
+    for (int x = 0; x < C / 8; ++x)
+        u[x] = make_uint4(pack_bf16(o[8 * x] * f, o[8 * x + 1] * f), pack_bf16(o[8 * x + 2] * f, o[8 * x + 3] * f),
+                          pack_bf16(o[8 * x + 4] * f, o[8 * x + 5] * f), pack_bf16(o[8 * x + 6] * f, o[8 * x + 7] * f));
+}
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[C]) {
+    if constexpr (C == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+}
+
 }  // namespace attn
 
 // Tensor cores: bf16 rows.  `status`: the library's device status word.

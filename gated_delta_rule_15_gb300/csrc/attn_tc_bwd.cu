@@ -6,10 +6,10 @@
 //
 // dq: an item is 128 query rows (as in the forward); of each of its key tiles
 //     S = Q K^T,  dP = dO V^T     [128 x 128]
-//     dQ += dS K                  dS (bf16) from tensor memory, over S's place; K as loaded (MN-major)
-// with two places for S, so that the products of the next tile run while the softmax warps form dS; a
-// thread holds half a row.  Two more warps form delta = do.o an item ahead and leave it, with lse in
-// log2, in the order of tiles for the second kernel.
+//     dQ += dS K                  dS (bf16) from tensor memory, over dP's place; K as loaded (MN-major)
+// with two places for dP; the next tile's S follows as soon as the softmax warps have S in registers.  Sixteen
+// warps form dS, a thread of them 32 keys of a row.  Four more form delta = do.o an item ahead and leave it,
+// with lse in log2, in the order of tiles for the second kernel.
 //
 // dk, dv: a block takes 128 keys of a head and runs over the tiles of 128 query rows that see one of them, all
 // heads of the group one after another:
@@ -29,7 +29,11 @@ namespace dr {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kStatWarp = 10;
+constexpr int kSoftWarps = 16, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 2;
+constexpr int kStatWarps = 4, kDqThreads = 32 * (kSoftWarps + 8), kDkvThreads = 32 * (kSoftWarps + 4);
+// Registers a thread: launched with 80 and 96; the softmax warps take what the others give back.
+constexpr int kDqSoftRegs = 96, kDqOtherRegs = 48, kDkvSoftRegs = 104, kDkvOtherRegs = 56;
+static_assert(16 * kDqSoftRegs + 8 * kDqOtherRegs <= 24 * 80 && 16 * kDkvSoftRegs + 4 * kDkvOtherRegs <= 20 * 96, "register split");
 constexpr int kMaxSplitTiles = 8;      // key tiles with sinks that are cut
 
 struct BwdArgs {
@@ -71,20 +75,12 @@ __device__ __forceinline__ bool item_of(const BwdArgs &a, int64_t k, Item &im) {
     return true;
 }
 
-// Zeros into the rows r0 .. r1 - 1 of a tile of 128-byte rows in panels of 16 KB, by 256 threads.
+// Zeros into the rows r0 .. r1 - 1 of a tile of 128-byte rows in panels of 16 KB, by the softmax warps.
 template <int PANELS>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int r0, int r1, int t) {
     const int n = (r1 - r0) * 8;
-    for (int x = t; x < PANELS * n; x += 256) sts128(tile + (x / n) * 16384 + (r0 + x % n / 8) * 128 + (x % 8) * 16, 0, 0, 0, 0);
+    for (int x = t; x < PANELS * n; x += 32 * kSoftWarps) sts128(tile + (x / n) * 16384 + (r0 + x % n / 8) * 128 + (x % 8) * 16, 0, 0, 0, 0);
     fence_proxy_async();
-}
-
-// bf16 rows of 32 accumulator columns times f
-__device__ __forceinline__ void put32(__nv_bfloat16 *dst, const float (&o)[32], float f) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-        reinterpret_cast<uint4 *>(dst)[x] = make_uint4(pack_bf16(o[8 * x] * f, o[8 * x + 1] * f), pack_bf16(o[8 * x + 2] * f, o[8 * x + 3] * f),
-                                                       pack_bf16(o[8 * x + 4] * f, o[8 * x + 5] * f), pack_bf16(o[8 * x + 6] * f, o[8 * x + 7] * f));
 }
 
 // ------------------------------------------------------------------ dq
@@ -92,12 +88,12 @@ template <int D>
 struct DqLayout {
     static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;
     static constexpr uint32_t Q = 0, O = TILE, KV = 2 * TILE, BARS = KV + NB * TILE;
-    static constexpr uint32_t TOTAL = BARS + (2 * NB + 12) * 8 + 2 * sizeof(Item);
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 13) * 8 + 2 * sizeof(Item);
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
 attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tk,
                const __grid_constant__ CUtensorMap tv, const BwdArgs a) {
     using L = DqLayout<D>;
@@ -107,10 +103,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a key or value tile is there, is done with
     uint64_t *b_q = bars + 2 * NB, *b_qfree = b_q + 1; // the item and its rows are there, are done with
-    uint64_t *b_s = b_q + 2, *b_dp = b_q + 4, *b_ds = b_q + 5, *b_dq = b_q + 6;   // [2] S; dP; dS; dQ is complete
-    uint64_t *b_stat = b_q + 7, *b_sfree = b_q + 9;    // [2] the rows' statistics are there, are read
-    uint64_t *b_end = b_q + 11;
-    Item *items = reinterpret_cast<Item *>(b_q + 12);  // [2]
+    uint64_t *b_s = b_q + 2, *b_sread = b_q + 3, *b_dp = b_q + 4, *b_ds = b_q + 6, *b_dq = b_q + 7;   // S; S is read; [2] dP; dS; dQ is complete
+    uint64_t *b_stat = b_q + 8, *b_sfree = b_q + 10;   // [2] the rows' statistics are there, are read
+    uint64_t *b_end = b_q + 12;
+    Item *items = reinterpret_cast<Item *>(b_q + 13);  // [2]
     __shared__ uint32_t tmem_s;
     __shared__ int polls_s;
     const AttnProblem &p = a.p;
@@ -118,14 +114,15 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     if (tid == 0) {
         for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
         mbar_init(b_q, 1);
-        mbar_init(b_qfree, 1 + 8);       // the MMAs, and every softmax warp has seen the item
+        mbar_init(b_qfree, 1 + kSoftWarps);       // the MMAs, and every softmax warp has seen the item
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_s + i, 1);
-            mbar_init(b_stat + i, 2);
-            mbar_init(b_sfree + i, 8);
+            mbar_init(b_dp + i, 1);
+            mbar_init(b_stat + i, kStatWarps);
+            mbar_init(b_sfree + i, kSoftWarps);
         }
-        mbar_init(b_dp, 1);
-        mbar_init(b_ds, 8);
+        mbar_init(b_s, 1);
+        mbar_init(b_sread, kSoftWarps);
+        mbar_init(b_ds, kSoftWarps);
         mbar_init(b_dq, 1);
         mbar_init(b_end, 1);
         polls_s = tc::kPolls;
@@ -139,7 +136,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_s;
-    constexpr uint32_t TM_DP = 256, TM_DQ = 384;
+    constexpr uint32_t TM_DP = 128, TM_DQ = 384;      // S at 0
+    // places of an item's tiles in the ring: K0, V0, V1, K1, V2, K2, .., so that V is a tile ahead
+    auto k_at = [](int t) { return t == 0 ? 0 : 2 * t + 1; };
+    auto v_at = [](int t) { return t == 0 ? 1 : 2 * t; };
     volatile int *polls = &polls_s;
     auto wait = [&](uint64_t *bar, int k) {
         if (!mbar_try_wait(bar, k & 1)) tc::wait_longer(bar, k & 1, polls);
@@ -147,12 +147,13 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     };
     auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
 
-    if (warp < 8) {
+    if (warp < kSoftWarps) {
+        tc::more_regs<kDqSoftRegs>();
         // ---------------------------------------------------------------- dS
-        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), col0 = 64 * half;
+        const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane, col0 = 32 * group;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
         const float f = p.scale * kLog2e;
-        int n_tile = 0;
+        int n_tile = 0, ring = 0;
 #pragma unroll 1
         for (int it = 0;; ++it) {
             wait(b_q, it);
@@ -171,57 +172,69 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             for (int t = 0; t < kt.n; ++t, ++n_tile) {
                 const int k0 = kt.first(t), stop = kt.stop(t), kc = stop - k0, kc16 = (kc + 15) & ~15;
                 const bool whole = kc == kKeys && stop - 1 <= im.q0 && (k0 > kt.end - 1 - p.window || stop <= p.sinks);
-                const uint32_t tS = tl + 128 * (n_tile & 1) + col0;
-                float s[64];
-                wait(b_s + (n_tile & 1), n_tile >> 1);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if ((int)col0 + 32 * c < kc) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 64; x += 2) {
-                    const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, l2);
-                    s[x] = ex2(y.x);
-                    s[x + 1] = ex2(y.y);
-                }
-                if (k0 + kc16 > im.len) zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (2 * n_tile % NB) * L::TILE, im.len - k0, kc16, tid);
-                wait(b_dp, n_tile);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if ((int)col0 + 32 * c >= kc) continue;
-                    float dp[32];
-                    tmem_ld32(tl + TM_DP + col0 + 32 * c, dp);
+                const bool mine = col0 < kc;
+                const uint32_t tD = tl + TM_DP + 128 * (n_tile & 1) + col0;
+                float s[32];
+                wait(b_s, n_tile);
+                if (mine) {
+                    tmem_ld32(tl + col0, s);
                     tmem_wait_ld();
-                    const uint32_t bits = whole ? 0xffffffffu : seen_bits(i, k0 + (int)col0 + 32 * c, stop, p.window, p.sinks);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_sread);
+                if (mine) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, l2);
+                        s[x] = ex2(y.x);
+                        s[x + 1] = ex2(y.y);
+                    }
+                }
+                if (k0 + kc16 > im.len)
+                    zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (ring + k_at(t)) % NB * L::TILE, im.len - k0, kc16, tid);
+                wait(b_dp + (n_tile & 1), n_tile >> 1);
+                if (mine) {
+                    float dp[32];
+                    tmem_ld32(tD, dp);
+                    tmem_wait_ld();
                     uint32_t w[16];
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
-                        float2 y = mul2(make_float2(s[32 * c + x], s[32 * c + x + 1]), add2(make_float2(dp[x], dp[x + 1]), d2));
-                        if (!whole) {
-                            y.x = bits >> x & 1 ? y.x : 0.f;
-                            y.y = bits >> x & 2 ? y.y : 0.f;
-                        }
-                        w[x / 2] = pack_bf16(y.x, y.y);
+                        const float2 y = mul2(make_float2(s[x], s[x + 1]), add2(make_float2(dp[x], dp[x + 1]), d2));
+                        s[x] = y.x;
+                        s[x + 1] = y.y;
                     }
-                    tmem_st16u(tS + 16 * c, w);
+                    if (!whole) {      // (0 times the product of rows of others may be anything)
+                        const uint32_t bits = seen_bits(i, k0 + col0, stop, p.window, p.sinks);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) s[x] = bits >> x & 1 ? s[x] : 0.f;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16(s[x], s[x + 1]);
+                    tmem_st16u(tD, w);
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_ds);
             }
+            ring += 2 * kt.n;
             wait(b_dq, it);
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.dq) + (int64_t)(im.lo + i) * p.dqs + (im.h0 + row % a.gp) * D + half * (D / 2);
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                float o[32];
-                tmem_ld32(tl + TM_DQ + half * (D / 2) + 32 * c, o);
-                tmem_wait_ld();
-                if (i < im.len) put32(dst + 32 * c, o, p.scale);
-            }
+            constexpr int C = D / 4;
+            float o[C];
+            uint4 u[C / 8];
+            tmem_ld_cols(tl + TM_DQ + C * group, o);
+            tmem_wait_ld();
+            to_pieces(o, p.scale, u);
+            put_rows<C / 8>(u, lane, [&](int r) {
+                const int rr = 32 * quarter + r, ii = im.q0 + rr / a.gp;
+                return ii < im.len ? static_cast<__nv_bfloat16 *>(p.dq) + (int64_t)(im.lo + ii) * p.dqs + (im.h0 + rr % a.gp) * D + C * group : nullptr;
+            });
             tc_fence_before();
         }
     } else if (warp == kLoadWarp) {
+        tc::fewer_regs<kDqOtherRegs>();
         // ---------------------------------------------------------------- copies
         int it = 0, ring = 0;
         auto load = [&](int k, const CUtensorMap *map, int hk, int row0, int rows) {   // by one lane
@@ -248,9 +261,14 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     tc::tma_load_3d(sm + L::Q + e * 16384, &tq, b_q, 64 * e, im.h0, im.lo + im.q0);
                     tc::tma_load_3d(sm + L::O + e * 16384, &to, b_q, 64 * e, im.h0, im.lo + im.q0);
                 }
-                for (int t = 0; t < kt.n; ++t) {
-                    load(ring + 2 * t, &tk, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
-                    load(ring + 2 * t + 1, &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                auto tile = [&](bool key, int t) {
+                    load(ring + (key ? k_at(t) : v_at(t)), key ? &tk : &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                };
+                tile(true, 0);
+                tile(false, 0);
+                for (int t = 1; t < kt.n; ++t) {
+                    tile(false, t);
+                    tile(true, t);
                 }
             }
             __syncwarp();
@@ -269,6 +287,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
+        tc::fewer_regs<kDqOtherRegs>();
         // ---------------------------------------------------------------- MMAs
         if (elect_one()) {
             const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
@@ -291,33 +310,40 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         mma_bf16(d, desc_add(da, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
                 };
                 auto scores = [&](int t) {
-                    rows_by_rows(tm + 128 * ((n_tile + t) & 1), L::Q, ring + 2 * t, t);
-                    mma_commit(b_s + ((n_tile + t) & 1));
+                    rows_by_rows(tm, L::Q, ring + k_at(t), t);
+                    mma_commit(b_s);
                 };
                 auto dps = [&](int t) {
-                    rows_by_rows(tm + TM_DP, L::O, ring + 2 * t + 1, t);
-                    mma_commit(b_dp);
-                    mma_commit(b_free + (ring + 2 * t + 1) % NB);
+                    const int b = (n_tile + t) & 1, v = ring + v_at(t);
+                    rows_by_rows(tm + TM_DP + 128 * b, L::O, v, t);
+                    mma_commit(b_dp + b);
+                    mma_commit(b_free + v % NB);
                 };
-                scores(0);
+                scores(0);      // (S of the item before is read: its last dS was waited for)
                 dps(0);
-                if (kt.n > 1) scores(1);
+                if (kt.n > 1) dps(1);
                 else mma_commit(b_qfree);
 #pragma unroll 1
                 for (int t = 0; t < kt.n; ++t) {
-                    wait(b_ds, n_tile + t);
                     if (t + 1 < kt.n) {
-                        dps(t + 1);
+                        wait(b_sread, n_tile + t);
+                        scores(t + 1);
                         if (t + 2 == kt.n) mma_commit(b_qfree);
                     }
-                    const int k = ring + 2 * t, ks = n16(t) / 16;
+                    wait(b_ds, n_tile + t);
+                    const int k = ring + k_at(t), ks = n16(t) / 16;
                     const uint64_t db = desc_add(dM, L::KV + (k % NB) * L::TILE);
-                    const uint32_t src = tm + 128 * ((n_tile + t) & 1);
+                    const uint32_t src = tm + TM_DP + 128 * ((n_tile + t) & 1);
+                    if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                    } else {
 #pragma unroll 1
-                    for (int e = 0; e < ks; ++e)
-                        mma_bf16_ts(tm + TM_DQ, src + 8 * e + (e >= 4 ? 32 : 0), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                        for (int e = 0; e < ks; ++e)
+                            mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                    }
                     mma_commit(b_free + k % NB);
-                    if (t + 2 < kt.n) scores(t + 2);
+                    if (t + 2 < kt.n) dps(t + 2);
                 }
                 mma_commit(b_dq);
                 ring += 2 * kt.n;
@@ -328,9 +354,12 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (*polls == 0) atomicExch(a.status, kErrTimeout);
         }
         __syncwarp();
+    } else if (warp >= kStatWarp + kStatWarps) {
+        tc::fewer_regs<kDqOtherRegs>();
     } else {
+        tc::fewer_regs<kDqOtherRegs>();
         // ---------------------------------------------------------------- lse and delta of the rows
-        constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // lanes a row, rows a warp's access
+        constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4, ROWS = 128 / kStatWarps;      // lanes a row, rows a warp's access, rows a warp
         const int l = lane % LPR;
         int it = 0;
 #pragma unroll 1
@@ -339,7 +368,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (!item_of(a, k, im)) continue;
             if (it > 1) wait(b_sfree + (it & 1), (it >> 1) - 1);
 #pragma unroll 1
-            for (int r0 = 64 * (warp - kStatWarp); r0 < 64 * (warp - kStatWarp) + 64; r0 += U * RPW) {
+            for (int r0 = ROWS * (warp - kStatWarp); r0 < ROWS * (warp - kStatWarp + 1); r0 += U * RPW) {
                 uint4 o[U], d[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -388,7 +417,7 @@ struct DkvLayout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
 attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const BwdArgs a) {
     using L = DkvLayout<D>;
@@ -435,7 +464,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a query or d_out tile is there, is done with
     uint64_t *b_stat = bars + 2 * NB, *b_sfree = b_stat + NS;   // [NS] the tile's statistics
     uint64_t *b_kv = b_sfree + NS, *b_s = b_kv + 1, *b_p = b_kv + 2, *b_dp = b_kv + 3, *b_ds = b_kv + 4, *b_end = b_kv + 5;
-    float2 *stats = reinterpret_cast<float2 *>(sm + L::STATS);   // [NS][128]
+    float *stats = reinterpret_cast<float *>(sm + L::STATS);   // [NS][-lse log2 e, -delta][128]
     __shared__ uint32_t tmem_s;
     __shared__ int polls_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -443,13 +472,13 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(b_stat + i, 1);
-            mbar_init(b_sfree + i, 8);
+            mbar_init(b_sfree + i, kSoftWarps);
         }
         mbar_init(b_kv, 1);
         mbar_init(b_s, 1);
-        mbar_init(b_p, 8);
+        mbar_init(b_p, kSoftWarps);
         mbar_init(b_dp, 1);
-        mbar_init(b_ds, 8);
+        mbar_init(b_ds, kSoftWarps);
         mbar_init(b_end, 1);
         polls_s = tc::kPolls;
         fence_mbar_init();
@@ -469,53 +498,43 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         tc_fence_after();
     };
     auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
-    auto first_of = [&](int t) { return qa + t % nt * a.tokens; };
 
-    if (warp < 8) {
+    if (warp < kSoftWarps) {
+        tc::more_regs<kDkvSoftRegs>();
         // ---------------------------------------------------------------- P^T, dS^T
-        const int quarter = warp & 3, half = warp >> 2, j = k0 + 32 * quarter + lane;
-        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), col0 = 64 * half;
+        const int quarter = warp & 3, group = warp >> 2, j = k0 + 32 * quarter + lane, col0 = 32 * group;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
         const float f = p.scale * kLog2e;
         const float2 f2 = make_float2(f, f);
         const int see = min(qb, j < p.sinks ? len : min(j, kNoWindow - 1) + p.window);    // behind the last query that sees this key
+        int q0 = qa;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const int q0 = first_of(t);
             const bool whole = q0 >= k0 + kKeys - 1 && q0 + a.tokens <= qb && (q0 + a.tokens - 1 - k0 < p.window || k0 + kKeys <= p.sinks);
-            const float4 *st = reinterpret_cast<const float4 *>(stats + (t % NS) * 128 + col0);
-            float s[64];
-            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
-            if (!whole) {
-                const int lo_c = max(j - q0, 0), hi_c = min(see - q0, 128);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int at = (int)col0 + 32 * c;
-                    bits[c] = low_bits(hi_c * a.gp - at) & ~low_bits(min(lo_c, 128) * a.gp - at);
-                }
-            }
+            const float4 *st = reinterpret_cast<const float4 *>(stats + (t % NS) * 256 + col0);
+            float s[32];
+            uint32_t w[16], bits = 0xffffffffu;
+            if (!whole) bits = low_bits(min(see - q0, 128) * a.gp - col0) & ~low_bits(min(max(j - q0, 0), 128) * a.gp - col0);
             wait(b_stat + t % NS, t / NS);
             wait(b_s, t);
-            tmem_ld32(tl + col0, *reinterpret_cast<float(*)[32]>(s));
-            tmem_ld32(tl + col0 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+            tmem_ld32(tl + col0, s);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    const float4 l = st[16 * c + x / 2];
-                    const float2 y = fma2(make_float2(s[32 * c + x], s[32 * c + x + 1]), f2, make_float2(-l.x, -l.z));
-                    float u = ex2(y.x), v = ex2(y.y);
-                    if (!whole) {
-                        u = bits[c] >> x & 1 ? u : 0.f;
-                        v = bits[c] >> x & 2 ? v : 0.f;
-                    }
-                    s[32 * c + x] = u;
-                    s[32 * c + x + 1] = v;
-                    w[x / 2] = pack_bf16(u, v);
-                }
-                tmem_st16u(tl + col0 + 16 * c, w);
+            for (int x = 0; x < 32; x += 4) {
+                const float4 l = st[x / 4];
+                const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, make_float2(l.x, l.y)), z = fma2(make_float2(s[x + 2], s[x + 3]), f2, make_float2(l.z, l.w));
+                s[x] = ex2(y.x);
+                s[x + 1] = ex2(y.y);
+                s[x + 2] = ex2(z.x);
+                s[x + 3] = ex2(z.y);
             }
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = bits >> x & 1 ? s[x] : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16(s[x], s[x + 1]);
+            tmem_st16u(tl + col0, w);
             if (q0 + a.tokens > len) {     // rows of no query of this sequence are zeros
                 wait_ring(b_full, 2 * t + 1);
                 for (int e = 0; e < 2; ++e)
@@ -526,24 +545,24 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) mbar_arrive(b_p);
             wait(b_dp, t);
+            float dp[32];
+            tmem_ld32(tl + TM_DP + col0, dp);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float dp[32];
-                tmem_ld32(tl + TM_DP + col0 + 32 * c, dp);
-                tmem_wait_ld();
-                uint32_t w[16];
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    const float4 l = st[16 * c + x / 2];
-                    float2 y = mul2(make_float2(s[32 * c + x], s[32 * c + x + 1]), add2(make_float2(dp[x], dp[x + 1]), make_float2(-l.y, -l.w)));
-                    if (!whole) {      // (the product of rows of others may be anything)
-                        y.x = bits[c] >> x & 1 ? y.x : 0.f;
-                        y.y = bits[c] >> x & 2 ? y.y : 0.f;
-                    }
-                    w[x / 2] = pack_bf16(y.x, y.y);
+            for (int x = 0; x < 32; x += 4) {
+                const float4 d = st[32 + x / 4];
+                float2 y = mul2(make_float2(s[x], s[x + 1]), add2(make_float2(dp[x], dp[x + 1]), make_float2(d.x, d.y)));
+                float2 z = mul2(make_float2(s[x + 2], s[x + 3]), add2(make_float2(dp[x + 2], dp[x + 3]), make_float2(d.z, d.w)));
+                if (!whole) {      // (0 times the product of rows of others may be anything)
+                    y.x = bits >> x & 1 ? y.x : 0.f;
+                    y.y = bits >> x & 2 ? y.y : 0.f;
+                    z.x = bits >> x & 4 ? z.x : 0.f;
+                    z.y = bits >> x & 8 ? z.y : 0.f;
                 }
-                tmem_st16u(tl + TM_DP + col0 + 16 * c, w);
+                w[x / 2] = pack_bf16(y.x, y.y);
+                w[x / 2 + 1] = pack_bf16(z.x, z.y);
             }
+            tmem_st16u(tl + TM_DP + col0, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -551,33 +570,35 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 mbar_arrive(b_ds);
                 mbar_arrive(b_sfree + t % NS);
             }
+            q0 += a.tokens;
+            if (q0 >= qb) q0 = qa;         // the next heads
         }
         wait(b_end, 0);
         // out: a sink's row is a part of a sum where its queries are cut
-        const bool part = cut && j < p.sinks;
-        float *sum = nullptr;
-        if (part) sum = (chunk >= 0 ? a.parts : a.base) + ((((chunk >= 0 ? slot : n) * p.Hk + hk) * a.sink_tiles + jt) * a.sink_rows + (j - k0)) * 2 * D;
+        constexpr int C = D / 4;
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {      // dk, dv
             const float scale = e == 0 ? p.scale : 1.f;
-            __nv_bfloat16 *dst = e == 0 ? static_cast<__nv_bfloat16 *>(p.dk) + (lo + j) * p.dks : static_cast<__nv_bfloat16 *>(p.dv) + (lo + j) * p.dvs;
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                const int at = half * (D / 2) + 32 * c;
-                float o[32];
-                tmem_ld32(tl + (e == 0 ? TM_DK : TM_DV) + at, o);
-                tmem_wait_ld();
-                if (j >= len) continue;
-                if (part) {
+            float o[C];
+            tmem_ld_cols(tl + (e == 0 ? TM_DK : TM_DV) + C * group, o);
+            tmem_wait_ld();
+            if (cut && j < min(p.sinks, len)) {
+                float *sum = (chunk >= 0 ? a.parts : a.base) + ((((chunk >= 0 ? slot : n) * p.Hk + hk) * a.sink_tiles + jt) * a.sink_rows + (j - k0)) * 2 * D + e * D + C * group;
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        store4(sum + e * D + at + x, make_float4(o[x] * scale, o[x + 1] * scale, o[x + 2] * scale, o[x + 3] * scale));
-                } else if (chunk < 0) {
-                    put32(dst + hk * D + at, o, scale);
-                }
+                for (int x = 0; x < C; x += 4) store4(sum + x, make_float4(o[x] * scale, o[x + 1] * scale, o[x + 2] * scale, o[x + 3] * scale));
             }
+            if (chunk >= 0) continue;
+            uint4 u[C / 8];
+            to_pieces(o, scale, u);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e == 0 ? p.dk : p.dv) + hk * D + C * group;
+            const int64_t stride = e == 0 ? p.dks : p.dvs;
+            put_rows<C / 8>(u, lane, [&](int r) {
+                const int jj = k0 + 32 * quarter + r;
+                return jj < len && !(cut && jj < p.sinks) ? out + (lo + jj) * stride : nullptr;
+            });
         }
     } else if (warp == kLoadWarp) {
+        tc::fewer_regs<kDkvOtherRegs>();
         // ---------------------------------------------------------------- copies
         if (elect_one()) {
             mbar_arrive_expect_tx(b_kv, 2 * L::TILE);
@@ -586,16 +607,22 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tc::tma_load_3d(sm + L::K + e * 16384 + x * kBox * 128, &tk, b_kv, 64 * e, hk, (int)lo + k0 + x * kBox);
                     tc::tma_load_3d(sm + L::V + e * 16384 + x * kBox * 128, &tv, b_kv, 64 * e, hk, (int)lo + k0 + x * kBox);
                 }
-            int issued = 0;
+            int issued = 0, q0 = qa, h0 = hk * (p.Hq / p.Hk);
 #pragma unroll 1
             for (; issued < 2 * tiles; ++issued) {
-                const int b = issued % NB, t = issued / 2;
+                const int b = issued % NB;
                 if (issued >= NB) wait(b_free + b, issued / NB - 1);
                 if (*polls == 0) break;
                 mbar_arrive_expect_tx(b_full + b, L::TILE);
-                const int h0 = hk * (p.Hq / p.Hk) + t / nt * a.gp;
                 for (int e = 0; e < L::PANELS; ++e)
-                    tc::tma_load_3d(sm + L::QO + b * L::TILE + e * 16384, issued & 1 ? &to : &tq, b_full + b, 64 * e, h0, (int)lo + first_of(t));
+                    tc::tma_load_3d(sm + L::QO + b * L::TILE + e * 16384, issued & 1 ? &to : &tq, b_full + b, 64 * e, h0, (int)lo + q0);
+                if (issued & 1) {
+                    q0 += a.tokens;
+                    if (q0 >= qb) {
+                        q0 = qa;
+                        h0 += a.gp;
+                    }
+                }
             }
             // the loads have landed before the block ends, also after an expiry
             tc::wait_cycles(b_kv, 0);
@@ -603,6 +630,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
+        tc::fewer_regs<kDkvOtherRegs>();
         // ---------------------------------------------------------------- MMAs
         if (elect_one()) {
             const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
@@ -618,7 +646,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             auto sums = [&](uint32_t d, uint32_t src, int k, bool more) {
                 const uint64_t db = desc_add(dM, L::QO + (k % NB) * L::TILE);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mma_bf16_ts(d, src + 8 * e + (e >= 4 ? 32 : 0), desc_add(db, e * 2048), ID_D, more || e > 0);
+                for (int e = 0; e < 8; ++e) mma_bf16_ts(d, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_D, more || e > 0);
                 mma_commit(b_free + k % NB);
             };
             wait(b_kv, 0);
@@ -647,21 +675,33 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
         __syncwarp();
     } else if (warp == kStatWarp) {
+        tc::fewer_regs<kDkvOtherRegs>();
         // ---------------------------------------------------------------- statistics of the queries
+        int q0 = qa;
+        const float2 *src = a.stats + ((int64_t)hk * a.runs * p.seqs.total + lo) * a.gp;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const int q0 = first_of(t);
-            const float2 *src = a.stats + ((int64_t)(hk * a.runs + t / nt) * p.seqs.total + lo + q0) * a.gp;
             const int rows = min(len - q0, a.tokens) * a.gp;
             float2 x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = lane + 32 * e < rows ? src[lane + 32 * e] : make_float2(0.f, 0.f);
+            for (int e = 0; e < 4; ++e) x[e] = lane + 32 * e < rows ? src[(int64_t)q0 * a.gp + lane + 32 * e] : make_float2(0.f, 0.f);
             if (t >= NS) wait(b_sfree + t % NS, t / NS - 1);
+            float *dst = stats + (t % NS) * 256 + lane;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) stats[(t % NS) * 128 + lane + 32 * e] = x[e];
+            for (int e = 0; e < 4; ++e) {
+                dst[32 * e] = -x[e].x;
+                dst[128 + 32 * e] = -x[e].y;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(b_stat + t % NS);
+            q0 += a.tokens;
+            if (q0 >= qb) {
+                q0 = qa;
+                src += p.seqs.total * a.gp;
+            }
         }
+    } else {
+        tc::fewer_regs<kDkvOtherRegs>();
     }
     tc_fence_before();
     __syncthreads();
@@ -740,11 +780,11 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
         cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess)
         return kErrCuda;
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
-    attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
+    attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kDqThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     a.items = attn_tile_slots(p.seqs, kKeys) * p.Hk;
     const int64_t blocks = a.items + a.chunk_slots * p.Hk * a.sink_tiles;
-    attn_dkv_kernel<D><<<(unsigned)blocks, kThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
+    attn_dkv_kernel<D><<<(unsigned)blocks, kDkvThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     if (a.sink_tiles == 0) return kOk;
     attn_sink_sum_kernel<D><<<(unsigned)(p.seqs.N * p.Hk * a.sink_tiles), 256, 0, s>>>(a);

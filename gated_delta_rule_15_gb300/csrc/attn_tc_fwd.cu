@@ -222,20 +222,17 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const int h = im.h0 + row % a.gp;
                 const float inv = 1.f / l;
                 const int64_t at = (int64_t)(im.lo + i) * p.Hq + h;
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
+                    uint4 u[4];
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
-                    uint32_t w[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) w[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
-                    if (mine) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            reinterpret_cast<uint4 *>(dst + 32 * c)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-                    }
+                    to_pieces(o, inv, u);
+                    put_rows<4>(u, lane, [&](int r) {
+                        const int rr = 32 * quarter + r, ii = ta + rr / a.gp;
+                        return ii < im.len ? static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(im.lo + ii) * p.Hq + im.h0 + rr % a.gp) * D + 32 * c : nullptr;
+                    });
                 }
                 if (mine) p.lse[at] = (m * f + log2f(l)) * kLn2;
             }
@@ -329,8 +326,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         wait(b_p + st, n_p[st]++);
                         const uint64_t dv = desc_add(dV, L::KV + (v % NB) * L::TILE);
                         const uint32_t d = tm + 256 + 128 * st, src = tm + 128 * st;
+                        if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
+                        } else {
 #pragma unroll 1
-                        for (int k = 0; k < ks; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
+                            for (int k = 0; k < ks; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
+                        }
                         more[st] = true;
                         pend[st] = -1;
                     };
