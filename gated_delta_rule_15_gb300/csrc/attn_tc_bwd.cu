@@ -29,7 +29,7 @@ namespace dr {
 namespace attn {
 namespace {
 
-constexpr int kSoftWarps = 16, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 2;
+constexpr int kSoftWarps = 16, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1, kStatWarp = kLoadWarp + 3;   // (two MMA warps)
 constexpr int kStatWarps = 4, kDqThreads = 32 * (kSoftWarps + 8), kDkvThreads = 32 * (kSoftWarps + 4);
 // Registers a thread: launched with 80 and 96; the softmax warps take what the others give back.
 constexpr int kDqSoftRegs = 96, kDqOtherRegs = 48, kDkvSoftRegs = 104, kDkvOtherRegs = 56;
@@ -88,7 +88,7 @@ template <int D>
 struct DqLayout {
     static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;
     static constexpr uint32_t Q = 0, O = TILE, KV = 2 * TILE, BARS = KV + NB * TILE;
-    static constexpr uint32_t TOTAL = BARS + (2 * NB + 13) * 8 + 2 * sizeof(Item);
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 14) * 8 + 2 * sizeof(Item);
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -103,28 +103,31 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a key or value tile is there, is done with
     uint64_t *b_q = bars + 2 * NB, *b_qfree = b_q + 1; // the item and its rows are there, are done with
-    uint64_t *b_s = b_q + 2, *b_sread = b_q + 3, *b_dp = b_q + 4, *b_ds = b_q + 6, *b_dq = b_q + 7;   // S; S is read; [2] dP; dS; dQ is complete
-    uint64_t *b_stat = b_q + 8, *b_sfree = b_q + 10;   // [2] the rows' statistics are there, are read
-    uint64_t *b_end = b_q + 12;
-    Item *items = reinterpret_cast<Item *>(b_q + 13);  // [2]
+    uint64_t *b_s = b_q + 2, *b_sread = b_q + 3, *b_dp = b_q + 4, *b_ds = b_q + 6, *b_dq = b_q + 8;   // S; S is read; [2] dP; [2] dS; dQ is complete
+    uint64_t *b_stat = b_q + 9, *b_sfree = b_q + 11;   // [2] the rows' statistics are there, are read
+    uint64_t *b_end = b_q + 13;
+    Item *items = reinterpret_cast<Item *>(b_q + 14);  // [2]
     __shared__ uint32_t tmem_s;
     __shared__ int polls_s;
     const AttnProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(b_full + i, 1);
+            mbar_init(b_free + i, 2);        // both MMA warps
+        }
         mbar_init(b_q, 1);
-        mbar_init(b_qfree, 1 + kSoftWarps);       // the MMAs, and every softmax warp has seen the item
+        mbar_init(b_qfree, 2 + kSoftWarps);       // the MMAs, and every softmax warp has seen the item
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_dp + i, 1);
+            mbar_init(b_ds + i, kSoftWarps);     // (a warp may be a tile ahead of another one)
             mbar_init(b_stat + i, kStatWarps);
             mbar_init(b_sfree + i, kSoftWarps);
         }
         mbar_init(b_s, 1);
         mbar_init(b_sread, kSoftWarps);
-        mbar_init(b_ds, kSoftWarps);
         mbar_init(b_dq, 1);
-        mbar_init(b_end, 1);
+        mbar_init(b_end, 2);
         polls_s = tc::kPolls;
         fence_mbar_init();
     }
@@ -217,7 +220,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_ds);
+                if (lane == 0) mbar_arrive(b_ds + (n_tile & 1));
             }
             ring += 2 * kt.n;
             wait(b_dq, it);
@@ -286,12 +289,14 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             mbar_arrive(b_q);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kMmaWarp + 2) {
         tc::fewer_regs<kDqOtherRegs>();
-        // ---------------------------------------------------------------- MMAs
+        // ---------------------------------------------------------------- MMAs: S; dP and dQ
+        const bool first = warp == kMmaWarp;
         if (elect_one()) {
-            const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
-            const uint64_t dM = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+            const uint64_t dA = smem_desc_sw128(smem_u32(sm) + (first ? L::Q : L::O), 16, 1024);        // K-major
+            const uint64_t dK = smem_desc_sw128(smem_u32(sm) + L::KV, 16, 1024);
+            const uint64_t dM = smem_desc_sw128(smem_u32(sm) + L::KV, 16384, 1024);     // MN-major, panels of 64 channels
             constexpr uint32_t ID_DQ = idesc_bf16(128, D, false, true);
             int ring = 0, n_tile = 0;
 #pragma unroll 1
@@ -301,51 +306,56 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 if (im.len < 0 || *polls == 0) break;
                 const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
                 auto n16 = [&](int t) { return (kt.stop(t) - kt.first(t) + 15) & ~15; };
-                auto rows_by_rows = [&](uint32_t d, uint32_t left, int k, int t) {
-                    const uint64_t da = desc_add(dK, left), db = desc_add(dK, L::KV + (k % NB) * L::TILE);
+                auto rows_by_rows = [&](uint32_t d, int b, int t) {
+                    const uint64_t db = desc_add(dK, b * L::TILE);
                     const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16(t) - 16) << 14);
-                    wait_ring(b_full, k);
 #pragma unroll
                     for (int e = 0; e < D / 16; ++e)
-                        mma_bf16(d, desc_add(da, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
+                        mma_bf16(d, desc_add(dA, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
                 };
-                auto scores = [&](int t) {
-                    rows_by_rows(tm, L::Q, ring + k_at(t), t);
-                    mma_commit(b_s);
-                };
-                auto dps = [&](int t) {
-                    const int b = (n_tile + t) & 1, v = ring + v_at(t);
-                    rows_by_rows(tm + TM_DP + 128 * b, L::O, v, t);
-                    mma_commit(b_dp + b);
-                    mma_commit(b_free + v % NB);
-                };
-                scores(0);      // (S of the item before is read: its last dS was waited for)
-                dps(0);
-                if (kt.n > 1) dps(1);
-                else mma_commit(b_qfree);
+                if (first) {
 #pragma unroll 1
-                for (int t = 0; t < kt.n; ++t) {
-                    if (t + 1 < kt.n) {
-                        wait(b_sread, n_tile + t);
-                        scores(t + 1);
-                        if (t + 2 == kt.n) mma_commit(b_qfree);
+                    for (int t = 0; t < kt.n; ++t) {
+                        const int k = ring + k_at(t), b = k % NB;
+                        wait(b_full + b, k / NB);
+                        if (n_tile + t > 0) wait(b_sread, n_tile + t - 1);
+                        rows_by_rows(tm, b, t);
+                        mma_commit(b_s);
+                        mma_commit(b_free + b);
                     }
-                    wait(b_ds, n_tile + t);
-                    const int k = ring + k_at(t), ks = n16(t) / 16;
-                    const uint64_t db = desc_add(dM, L::KV + (k % NB) * L::TILE);
-                    const uint32_t src = tm + TM_DP + 128 * ((n_tile + t) & 1);
-                    if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
+                    mma_commit(b_qfree);
+                } else {
+                    auto dps = [&](int t) {
+                        const int g = n_tile + t, v = ring + v_at(t), b = v % NB;
+                        wait(b_full + b, v / NB);
+                        rows_by_rows(tm + TM_DP + 128 * (g & 1), b, t);
+                        mma_commit(b_dp + (g & 1));
+                        mma_commit(b_free + b);
+                        mma_commit(b_free + b);      // (the other warp does not read it)
+                        if (t + 1 == kt.n) mma_commit(b_qfree);
+                    };
+                    dps(0);
+                    if (kt.n > 1) dps(1);
+#pragma unroll 1
+                    for (int t = 0; t < kt.n; ++t) {
+                        const int k = ring + k_at(t), b = k % NB, ks = n16(t) / 16;
+                        const uint64_t db = desc_add(dM, b * L::TILE);
+                        const uint32_t src = tm + TM_DP + 128 * ((n_tile + t) & 1);
+                        wait(b_full + b, k / NB);
+                        wait(b_ds + ((n_tile + t) & 1), (n_tile + t) >> 1);
+                        if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
-                    } else {
+                            for (int e = 0; e < 8; ++e) mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                        } else {
 #pragma unroll 1
-                        for (int e = 0; e < ks; ++e)
-                            mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                            for (int e = 0; e < ks; ++e)
+                                mma_bf16_ts(tm + TM_DQ, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_DQ, t > 0 || e > 0);
+                        }
+                        mma_commit(b_free + b);
+                        if (t + 2 < kt.n) dps(t + 2);
                     }
-                    mma_commit(b_free + k % NB);
-                    if (t + 2 < kt.n) dps(t + 2);
+                    mma_commit(b_dq);
                 }
-                mma_commit(b_dq);
                 ring += 2 * kt.n;
                 n_tile += kt.n;
             }
@@ -410,10 +420,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 // ------------------------------------------------------------------ dk, dv
 template <int D>
 struct DkvLayout {
-    static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 4 : 10, NS = 4;   // query-side tiles, statistics
+    // query-side tiles (with four of them Q waits for the product before the last: 2874 instead of 2500 cycles a tile), statistics
+    static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10, NS = 2;
     static constexpr uint32_t K = 0, V = TILE, QO = 2 * TILE, STATS = QO + NB * TILE, BARS = STATS + NS * 128 * 8;
-    static constexpr uint32_t TOTAL = BARS + (2 * NB + 2 * NS + 6) * 8;
-    static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 2 * NS + 6) * 8 + 8;
+    static_assert(TOTAL <= 227 * 1024, "shared memory");       // (no room for aligning: the array is declared aligned)
 };
 
 template <int D>
@@ -458,18 +469,24 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     }
     const int nt = (qb - qa + a.tokens - 1) / a.tokens, tiles = nt * a.runs;
 
-    extern __shared__ unsigned char dsm_raw[];
-    unsigned char *sm = align1024(dsm_raw);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    if (smem_u32(sm) & 1023u) {      // (never seen: nothing static lies in front of it)
+        if (threadIdx.x == 0) atomicExch(a.status, kErrCuda);
+        return;
+    }
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     uint64_t *b_full = bars, *b_free = bars + NB;      // [NB] a query or d_out tile is there, is done with
     uint64_t *b_stat = bars + 2 * NB, *b_sfree = b_stat + NS;   // [NS] the tile's statistics
     uint64_t *b_kv = b_sfree + NS, *b_s = b_kv + 1, *b_p = b_kv + 2, *b_dp = b_kv + 3, *b_ds = b_kv + 4, *b_end = b_kv + 5;
     float *stats = reinterpret_cast<float *>(sm + L::STATS);   // [NS][-lse log2 e, -delta][128]
-    __shared__ uint32_t tmem_s;
-    __shared__ int polls_s;
+    uint32_t &tmem_s = *reinterpret_cast<uint32_t *>(b_end + 1);
+    int &polls_s = *reinterpret_cast<int *>(&tmem_s + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(b_full + i, 1);
+            mbar_init(b_free + i, 2);        // both MMA warps
+        }
         for (int i = 0; i < NS; ++i) {
             mbar_init(b_stat + i, 1);
             mbar_init(b_sfree + i, kSoftWarps);
@@ -479,7 +496,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         mbar_init(b_p, kSoftWarps);
         mbar_init(b_dp, 1);
         mbar_init(b_ds, kSoftWarps);
-        mbar_init(b_end, 1);
+        mbar_init(b_end, 2);
         polls_s = tc::kPolls;
         fence_mbar_init();
     }
@@ -629,45 +646,39 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             for (int k = max(0, issued - NB); k < issued; ++k) tc::wait_cycles(b_full + k % NB, (k / NB) & 1);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kMmaWarp + 2) {
         tc::fewer_regs<kDkvOtherRegs>();
-        // ---------------------------------------------------------------- MMAs
+        // ---------------------------------------------------------------- MMAs: S and dV; dP and dK
+        const int second = warp - kMmaWarp;      // S^T = K Q^T, dV += P^T dO; dP^T = V dO^T, dK += dS^T Q
         if (elect_one()) {
-            const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
-            const uint64_t dM = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+            const uint64_t dA = smem_desc_sw128(smem_u32(sm) + (second ? L::V : L::K), 16, 1024);        // K-major
+            const uint64_t dB = smem_desc_sw128(smem_u32(sm) + L::QO, 16, 1024);
+            const uint64_t dM = smem_desc_sw128(smem_u32(sm) + L::QO, 16384, 1024);     // MN-major, panels of 64 channels
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_D = idesc_bf16(128, D, false, true);
-            auto rows_by_rows = [&](uint32_t d, uint32_t left, int k) {
-                const uint64_t da = desc_add(dK, left), db = desc_add(dK, L::QO + (k % NB) * L::TILE);
-                wait_ring(b_full, k);
+            const uint32_t x = tm + (second ? TM_DP : 0), sum = tm + (second ? TM_DK : TM_DV);
+            uint64_t *b_made = second ? b_dp : b_s, *b_read = second ? b_ds : b_p;
+            auto product = [&](int k) {
+                const int b = k % NB;
+                const uint64_t db = desc_add(dB, b * L::TILE);
+                wait(b_full + b, k / NB);
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e)
-                    mma_bf16(d, desc_add(da, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), ID_S, e > 0);
-            };
-            auto sums = [&](uint32_t d, uint32_t src, int k, bool more) {
-                const uint64_t db = desc_add(dM, L::QO + (k % NB) * L::TILE);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mma_bf16_ts(d, src + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_D, more || e > 0);
-                mma_commit(b_free + k % NB);
+                    mma_bf16(x, desc_add(dA, (e >> 2) * 16384 + (e & 3) * 32), desc_add(db, (e >> 2) * 16384 + (e & 3) * 32), ID_S, e > 0);
+                mma_commit(b_made);
+                mma_commit(b_free + b);
             };
             wait(b_kv, 0);
-            rows_by_rows(tm, L::K, 0);
-            mma_commit(b_s);
-            rows_by_rows(tm + TM_DP, L::V, 1);
-            mma_commit(b_dp);
+            product(second);
 #pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-                wait(b_p, t);
-                sums(tm + TM_DV, tm, 2 * t + 1, t > 0);
-                if (t + 1 < tiles) {
-                    rows_by_rows(tm, L::K, 2 * t + 2);
-                    mma_commit(b_s);
-                }
-                wait(b_ds, t);
-                sums(tm + TM_DK, tm + TM_DP, 2 * t, t > 0);
-                if (t + 1 < tiles) {
-                    rows_by_rows(tm + TM_DP, L::V, 2 * t + 3);
-                    mma_commit(b_dp);
-                }
+                const int k = 2 * t + 1 - second, b = k % NB;
+                const uint64_t db = desc_add(dM, b * L::TILE);
+                wait(b_full + b, k / NB);
+                wait(b_read, t);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mma_bf16_ts(sum, x + 32 * (e >> 1) + 8 * (e & 1), desc_add(db, e * 2048), ID_D, t > 0 || e > 0);
+                mma_commit(b_free + b);
+                if (t + 1 < tiles) product(2 * t + 2 + second);
             }
             mma_commit(b_end);
             tc::wait_cycles(b_end, 0);      // every MMA is done
@@ -775,7 +786,7 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
         !make_map(&m[1], p.d_out, p.seqs.total, p.Hq, p.d, (int64_t)p.Hq * p.d, a.gp, 128 / a.gp) ||
         !make_map(&m[2], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[3], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
         return kErrCuda;
-    constexpr int smem_q = DqLayout<D>::TOTAL + 1024, smem_kv = DkvLayout<D>::TOTAL + 1024;
+    constexpr int smem_q = DqLayout<D>::TOTAL + 1024, smem_kv = DkvLayout<D>::TOTAL;
     if (cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q) != cudaSuccess ||
         cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess)
         return kErrCuda;

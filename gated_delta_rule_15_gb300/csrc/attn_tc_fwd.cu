@@ -10,9 +10,10 @@
 // (p stays below 2^8, exact as a power-of-two-free rescale would be), so O in tensor memory is rescaled
 // a few times a row at most.  A row's decisions depend on the row alone.
 //
-// Warps 0..3 and 4..7 are the stages' softmax and write their outputs; warp 8 issues the copies, warp 9 the
-// MMAs: O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of the next tile, in turn, so that one stage's
-// softmax runs while the tensor cores work for the other.
+// Warps 0..3 and 4..7 are the stages' softmax and write their outputs; warp 8 issues the copies, warps 9 and 10
+// the stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor
+// cores work for the other.  (One thread for both stages is late: a tile's sixteen products take it 900 cycles to
+// issue and their waits 400, which the tensor cores need 1024 for.)
 //
 // Rows of other sequences: their keys are masked; their values, which enter the product as 0 times
 // whatever they hold, are overwritten with zeros in shared memory in a sequence's last tile.
@@ -71,7 +72,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const AttnProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < 2 * NB; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(b_full + i, 1);
+            mbar_init(b_free + i, 2);        // both stages
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + i, 1);
             mbar_init(b_qfree + i, 1 + 4);   // the MMAs, and every softmax warp has seen the item
@@ -79,7 +83,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(b_p + i, 4);
             mbar_init(b_o + i, 1);
         }
-        mbar_init(b_end, 1);
+        mbar_init(b_end, 2);
         polls_s = tc::kPolls;
         fence_mbar_init();
     }
@@ -303,69 +307,64 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 }
             }
             __syncwarp();
-        } else if (warp == kMmaWarp) {
-            // ---------------------------------------------------------------- MMAs
+        } else if (warp < kMmaWarp + 2) {
+            // ---------------------------------------------------------------- MMAs of a stage
+            const int st = warp - kMmaWarp;
             if (elect_one()) {
-                const uint64_t dK = smem_desc_sw128(smem_u32(sm), 16, 1024);        // K-major
-                const uint64_t dV = smem_desc_sw128(smem_u32(sm), 16384, 1024);     // MN-major, panels of 64 channels
+                const uint64_t dQ = smem_desc_sw128(smem_u32(sm) + L::Q + st * L::TILE, 16, 1024);   // K-major
+                const uint64_t dK = smem_desc_sw128(smem_u32(sm) + L::KV, 16, 1024);
+                const uint64_t dV = smem_desc_sw128(smem_u32(sm) + L::KV, 16384, 1024);     // MN-major, panels of 64 channels
                 constexpr uint32_t ID_PV = idesc_bf16(128, D, false, true);
-                int ring = 0, n_p[2] = {0, 0};
+                const uint32_t tS = tm + 128 * st, tO = tS + 256;
+                int ring = 0, n_p = 0;
 #pragma unroll 1
                 for (int it = 0;; ++it) {
-                    wait(b_q, it);
+                    wait(b_q + st, it);
                     const Item im = items[it & 1];
                     if (im.len < 0 || *polls == 0) break;
-                    wait(b_q + 1, it);
                     const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-                    int pend[2] = {-1, -1};
-                    bool more[2] = {false, false};
-                    auto flush = [&](int st) {     // O += P V of the tile whose S went before
-                        if (pend[st] < 0) return;
-                        const int t = pend[st], v = ring + 2 * t + 1, ks = (kt.stop(t) - kt.first(t) + 15) / 16;
-                        wait_ring(b_full, v);
-                        wait(b_p + st, n_p[st]++);
-                        const uint64_t dv = desc_add(dV, L::KV + (v % NB) * L::TILE);
-                        const uint32_t d = tm + 256 + 128 * st, src = tm + 128 * st;
-                        if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
+                    const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt);
+                    int pend = -1;         // the tile whose S went last
+                    bool more = false;
+                    auto flush = [&](int t) {     // O += P V of tile t - 1, or nothing of it
+                        const int v = ring + 2 * t - 1, b = v % NB;
+                        wait(b_full + b, v / NB);
+                        if (pend >= 0) {
+                            const int ks = (kt.stop(pend) - kt.first(pend) + 15) / 16;
+                            const uint64_t dv = desc_add(dV, b * L::TILE);
+                            wait(b_p + st, n_p++);
+                            if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
-                        } else {
+                                for (int k = 0; k < 8; ++k) mma_bf16_ts(tO, tS + 8 * k, desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                            } else {
 #pragma unroll 1
-                            for (int k = 0; k < ks; ++k) mma_bf16_ts(d, src + 8 * k, desc_add(dv, k * 2048), ID_PV, more[st] || k > 0);
+                                for (int k = 0; k < ks; ++k) mma_bf16_ts(tO, tS + 8 * k, desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                            }
+                            more = true;
+                            pend = -1;
                         }
-                        more[st] = true;
-                        pend[st] = -1;
+                        mma_commit(b_free + b);
                     };
 #pragma unroll 1
                     for (int t = 0; t < kt.n; ++t) {
-                        const int k = ring + 2 * t, n16 = (kt.stop(t) - kt.first(t) + 15) & ~15;
-                        wait_ring(b_full, k);
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            const int ta = im.q0 + st * tt;
-                            flush(st);
-                            if (st == 1 && t > 0) mma_commit(b_free + (k - 1) % NB);
-                            if (!kt.meets(t, ta, min(im.len, ta + tt), p.window, p.sinks)) continue;
-                            const uint64_t dq = desc_add(dK, L::Q + st * L::TILE), dk = desc_add(dK, L::KV + (k % NB) * L::TILE);
+                        const int k = ring + 2 * t, b = k % NB, n16 = (kt.stop(t) - kt.first(t) + 15) & ~15;
+                        wait(b_full + b, k / NB);
+                        if (t > 0) flush(t);
+                        if (kt.meets(t, ta, tb, p.window, p.sinks)) {
+                            const uint64_t dk = desc_add(dK, b * L::TILE);
                             const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16 - 16) << 14);
 #pragma unroll
                             for (int e = 0; e < D / 16; ++e)
-                                mma_bf16(tm + 128 * st, desc_add(dq, (e >> 2) * 16384 + (e & 3) * 32),
-                                         desc_add(dk, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
+                                mma_bf16(tS, desc_add(dQ, (e >> 2) * 16384 + (e & 3) * 32), desc_add(dk, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
                             mma_commit(b_s + st);
-                            pend[st] = t;
+                            pend = t;
                         }
-                        mma_commit(b_free + k % NB);
+                        mma_commit(b_free + b);
                     }
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) mma_commit(b_qfree + st);
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        flush(st);
-                        if (im.q0 + st * tt < im.len) mma_commit(b_o + st);
-                    }
+                    mma_commit(b_qfree + st);
+                    flush(kt.n);
+                    if (ta < im.len) mma_commit(b_o + st);
                     ring += 2 * kt.n;
-                    mma_commit(b_free + (ring - 1) % NB);
                 }
                 mma_commit(b_end);
                 tc::wait_cycles(b_end, 0);      // every MMA is done

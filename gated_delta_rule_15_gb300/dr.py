@@ -824,38 +824,51 @@ def qk_norm_rope_bwd(q, k, table, dq_out, dk_out, *, positions=None, offset: int
 
 
 # ------------------------------------------------------------ window attention
-def _packed_count(cu_seqlens, B):
-    """N of packed sequences, 0 without offsets."""
-    if cu_seqlens is None:
-        return 0
-    _on_one_device(cu_seqlens)
-    if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+# (sizes and strides are asked for once a tensor: the host's time counts for short calls)
+def _rows_at(x, shape, dev, what):
+    """Elements between the rows of x [..., H, d] of `shape` on device `dev`."""
+    if x.get_device() != dev:
+        raise ValueError(f"{what} must be on the current CUDA device")
+    s, d = x.stride(), shape[-1]
+    step = s[-3]
+    if s[-1] == 1 and s[-2] == d and step >= shape[-2] * d and \
+            (len(shape) == 3 or shape[0] == 1 or s[0] == shape[1] * step):
+        return step
+    return _rows_of(x, what)[3]
+
+
+def _contiguous_at(t, shape, dtype, dev, what):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous and on the current CUDA device")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+
+
+def _packed_count(cu_seqlens, B, dev):
+    """N of packed sequences."""
+    if cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous():
+        raise ValueError("tensors must be contiguous and on the current CUDA device")
+    if cu_seqlens.dtype is not torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be int64 [N + 1], N >= 1")
     if B != 1:
         raise ValueError("packed sequences come as one batch row (B = 1)")
     return cu_seqlens.numel() - 1
 
 
-def _rows_here(x, what):
-    """Elements between the rows of a [..., H, d] tensor of the current device."""
-    if x.get_device() != _current_device():
-        raise ValueError(f"{what} must be on the current CUDA device")
-    return _rows_of(x, what)[3]
-
-
-def _attn_desc(q, k, v, cu_seqlens, window, sinks, scale):
-    if q.dim() != 4 or k.dim() != 4:
+def _attn_desc(q, k, v, cu_seqlens, window, sinks, scale, dev):
+    shape, kv, dt = q.shape, k.shape, q.dtype
+    if len(shape) != 4 or len(kv) != 4:
         raise ValueError("q, k, v must be [B,T,H,d]")
-    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
+    if dt not in _DT or k.dtype is not dt or v.dtype is not dt:
         raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
-    B, T, Hq, d = q.shape
-    if k.shape[:2] != q.shape[:2] or k.shape[3] != d or v.shape != k.shape:
+    B, T, Hq, d = shape
+    if kv[0] != B or kv[1] != T or kv[3] != d or v.shape != kv:
         raise ValueError("inconsistent shapes")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
-    steps = [_rows_here(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"))]
-    return AttnDesc(B, T, Hq, k.shape[2], d, _packed_count(cu_seqlens, B), window, sinks, *steps, 0, 0, 0,
-                    _DT[q.dtype], 0, 0, d ** -0.5 if scale is None else scale)
+    return AttnDesc(B, T, Hq, kv[2], d, 0 if cu_seqlens is None else _packed_count(cu_seqlens, B, dev), window, sinks,
+                    _rows_at(q, shape, dev, "q"), _rows_at(k, kv, dev, "k"), _rows_at(v, kv, dev, "v"), 0, 0, 0,
+                    _DT[dt], 0, 0, d ** -0.5 if scale is None else scale)
 
 
 def window_attn_fwd(q, k, v, *, window: int = 0, sinks: int = 0, scale=None, cu_seqlens=None, out=None,
@@ -868,20 +881,24 @@ def window_attn_fwd(q, k, v, *, window: int = 0, sinks: int = 0, scale=None, cu_
     [N + 1] (device): the one batch row holds N sequences behind one another.  Returns (out
     [B,T,Hq,d], lse fp32 [B,T,Hq], the log of the softmax's sum).  Rows of no sequence are zero in
     new buffers and left as they are in given ones."""
-    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale)
-    _on_one_device(out, lse)
-    _like(out, q.shape, q.dtype, "out")
-    _like(lse, q.shape[:3], torch.float32, "lse")
-    if (out is None) != (lse is None) and desc.N:
-        raise ValueError("packed sequences: give both of out and lse or neither")
-    desc.zero_rest = int(out is None and desc.N > 0)
-    with _stream_scope(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    rc = _lib.dr_window_attn_fwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(cu_seqlens), _at(out),
-                                 _at(lse), _raw_stream(stream))
+    dev = _current_device()
+    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale, dev)
+    if out is not None:
+        _contiguous_at(out, q.shape, q.dtype, dev, "out")
+    if lse is not None:
+        _contiguous_at(lse, q.shape[:3], torch.float32, dev, "lse")
+    if out is None or lse is None:
+        if desc.N:
+            if out is not None or lse is not None:
+                raise ValueError("packed sequences: give both of out and lse or neither")
+            desc.zero_rest = 1
+        with _stream_scope(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            if lse is None:
+                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    rc = _lib.dr_window_attn_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(cu_seqlens),
+                                 out.data_ptr(), lse.data_ptr(), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_window_attn_fwd")
     return out, lse
@@ -893,43 +910,52 @@ def window_attn_bwd(q, k, v, out, lse, d_out, *, window: int = 0, sinks: int = 0
     (dr_window_attn_bwd): (dq, dk, dv) in q's dtype.  ``grads``: three buffers to write into (strided
     rows, as parts of a fused gradient); their rows of no sequence are left as they are (new ones
     hold zeros there)."""
-    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale)
-    _on_one_device(out, lse, d_out, workspace)
-    for t, n in ((out, "out"), (d_out, "d_out")):
-        _like(t, q.shape, q.dtype, n)
-    _like(lse, q.shape[:3], torch.float32, "lse")
+    dev = _current_device()
+    desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale, dev)
+    shape, kv, dt = q.shape, k.shape, q.dtype
+    _contiguous_at(out, shape, dt, dev, "out")
+    _contiguous_at(d_out, shape, dt, dev, "d_out")
+    _contiguous_at(lse, shape[:3], torch.float32, dev, "lse")
+    if workspace is not None:
+        _on_one_device(workspace)
     with _stream_scope(stream):
         if grads is None:
-            grads = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+            dq = torch.empty(shape, dtype=dt, device=dev)
+            dk, dv = torch.empty(kv, dtype=dt, device=dev), torch.empty(kv, dtype=dt, device=dev)
             desc.zero_rest = int(desc.N > 0)
         else:
             if len(grads) != 3:
                 raise ValueError("grads must be (dq, dk, dv)")
-            for g, x, n in zip(grads, (q, k, v), ("dq", "dk", "dv")):
-                _like(g, x.shape, x.dtype, n)
-            desc.dq_stride, desc.dk_stride, desc.dv_stride = (
-                _rows_here(g, n) for g, n in zip(grads, ("dq", "dk", "dv")))
-        workspace = _workspace(_lib.dr_window_attn_bwd_workspace_bytes, desc, workspace, q.device,
-                               "dr_window_attn_bwd_workspace_bytes")
-        dq, dk, dv = grads
-        rc = _lib.dr_window_attn_bwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(cu_seqlens), _at(out),
-                                     _at(lse), _at(d_out), _at(dq), _at(dk), _at(dv), _at(workspace),
-                                     _bytes(workspace), _raw_stream(stream))
+            dq, dk, dv = grads
+            for g, x, n in ((dq, shape, "dq"), (dk, kv, "dk"), (dv, kv, "dv")):
+                if g.dtype is not dt or g.shape != x:
+                    raise ValueError(f"{n} must be {dt} {list(x)}")
+            desc.dq_stride = _rows_at(dq, shape, dev, "dq")
+            desc.dk_stride, desc.dv_stride = _rows_at(dk, kv, dev, "dk"), _rows_at(dv, kv, dev, "dv")
+        if workspace is None:
+            workspace = _workspace(_lib.dr_window_attn_bwd_workspace_bytes, desc, None, dev,
+                                   "dr_window_attn_bwd_workspace_bytes")
+    rc = _lib.dr_window_attn_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(cu_seqlens),
+                                 out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), _at(workspace), _bytes(workspace), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_window_attn_bwd")
     return dq, dk, dv
 
 
-def _cache_of(k_cache, v_cache, pages, rows, d, dtype):
-    """(n_pages, Hk, page, max_pages) of a paged cache for `rows` sequences."""
-    _on_one_device(k_cache, v_cache, pages)
-    if k_cache.dim() != 4 or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
+def _cache_of(k_cache, v_cache, pages, N, d, dtype, dev):
+    """(n_pages, Hk, page, max_pages) of a paged cache for N sequences."""
+    shape, table = k_cache.shape, pages.shape
+    for t in (k_cache, v_cache, pages):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous and on the current CUDA device")
+    if len(shape) != 4 or shape[3] != d or v_cache.shape != shape:
         raise ValueError("k_cache, v_cache must be [n_pages,Hk,page,d]")
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must have the rows' dtype")
-    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != rows:
+    if pages.dtype is not torch.int32 or len(table) != 2 or table[0] != N:
         raise ValueError("pages must be int32 [N, max_pages]")
-    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], pages.shape[1]
+    return shape[0], shape[1], shape[2], table[1]
 
 
 def kv_append(q, k, v, table, k_cache, v_cache, pages, start, *, cu_seqlens=None, norm="rms", wq=None,
@@ -944,38 +970,52 @@ def kv_append(q, k, v, table, k_cache, v_cache, pages, start, *, cu_seqlens=None
     a sequence.  One row for each sequence, or by ``cu_seqlens`` int64 [N + 1] the rows
     cu_seqlens[n] .. cu_seqlens[n + 1] - 1.  Rows of no sequence are zero in a new ``q_out`` and left as
     they are in a given one, which may be q."""
-    if k.dim() != 3 or v.dim() != 3 or (q is not None and q.dim() != 3):
+    dev = _current_device()
+    shape, dt = k.shape, k.dtype
+    if len(shape) != 3:
         raise ValueError("q, k, v must be [rows,H,d]")
-    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    if dt not in _DT or v.dtype is not dt:
         raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
-    n, Hk, d = k.shape
-    if v.shape != k.shape or (q is not None and (q.shape[0] != n or q.shape[2] != d)):
+    n, Hk, d = shape
+    if v.shape != shape:
         raise ValueError("inconsistent shapes")
     if norm not in _NORMS or layout not in _LAYOUTS:
         raise ValueError("norm must be none, l2 or rms; layout half or interleaved")
-    if q is None and (q_out is not None or wq is not None):
-        raise ValueError("q_out, wq without q")
-    _on_one_device(table, start, wq, wk)
-    if table is not None and (table.dtype != torch.int64 or table.dim() != 1):
-        raise ValueError("table must be rope_table's int64 [rot / 2]")
-    N = n if cu_seqlens is None else _packed_count(cu_seqlens, 1)
-    _like(start, (N,), torch.int64, "start")
-    _like(wq, (d,), torch.float32, "wq")
-    _like(wk, (d,), torch.float32, "wk")
-    n_pages, heads, page, max_pages = _cache_of(k_cache, v_cache, pages, N, d, k.dtype)
+    Hq, q_step, out_step, rot = 0, 0, 0, 0
+    if q is None:
+        if q_out is not None or wq is not None:
+            raise ValueError("q_out, wq without q")
+    else:
+        qs = q.shape
+        if q.dtype is not dt or len(qs) != 3 or qs[0] != n or qs[2] != d:
+            raise ValueError("q must have k's dtype, rows and d")
+        Hq, q_step = qs[1], _rows_at(q, qs, dev, "q")
+        if q_out is not None:
+            if q_out.dtype is not dt or q_out.shape != qs:
+                raise ValueError("q_out must have its input's shape, dtype and device")
+            out_step = _rows_at(q_out, qs, dev, "q_out")
+    if table is not None:
+        if table.get_device() != dev or table.dtype is not torch.int64 or table.dim() != 1 or not table.is_contiguous():
+            raise ValueError("table must be rope_table's int64 [rot / 2] on the current CUDA device")
+        rot = 2 * table.numel()
+    N = n if cu_seqlens is None else _packed_count(cu_seqlens, 1, dev)
+    _contiguous_at(start, (N,), torch.int64, dev, "start")
+    if wq is not None:
+        _contiguous_at(wq, (d,), torch.float32, dev, "wq")
+    if wk is not None:
+        _contiguous_at(wk, (d,), torch.float32, dev, "wk")
+    n_pages, heads, page, max_pages = _cache_of(k_cache, v_cache, pages, N, d, dt, dev)
     if heads != Hk:
         raise ValueError("k_cache, v_cache must be [n_pages,Hk,page,d]")
-    steps = [0 if x is None else _rows_here(x, w) for x, w in ((q, "q"), (k, "k"), (v, "v"))]
-    if n == 0 and N == 0:
-        return None if q is None else q.clone() if q_out is None else q_out
-    desc = KvAppendDesc(n, N, 0 if q is None else q.shape[1], Hk, d, 0 if table is None else 2 * table.numel(),
-                        *steps, 0, n_pages, page, max_pages, _DT[k.dtype], _NORMS[norm], _LAYOUTS[layout],
-                        int(q_out is None and q is not None), 0, eps, rot_scale)
-    with _stream_scope(stream):
-        q_out, desc.q_out_stride = _rows_into(q_out, q, "q_out")
-    rc = _lib.dr_kv_append(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(wq), _at(wk), _at(table),
-                           _at(pages), _at(start), _at(cu_seqlens), _at(q_out), _at(k_cache), _at(v_cache),
-                           _raw_stream(stream))
+    desc = KvAppendDesc(n, N, Hq, Hk, d, rot, q_step, _rows_at(k, shape, dev, "k"), _rows_at(v, shape, dev, "v"), out_step,
+                        n_pages, page, max_pages, _DT[dt], _NORMS[norm], _LAYOUTS[layout],
+                        int(q is not None and q_out is None), 0, eps, rot_scale)
+    if q is not None and q_out is None:
+        with _stream_scope(stream):
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    rc = _lib.dr_kv_append(ctypes.byref(desc), _at(q), k.data_ptr(), v.data_ptr(), _at(wq), _at(wk), _at(table),
+                           pages.data_ptr(), start.data_ptr(), _at(cu_seqlens), _at(q_out), k_cache.data_ptr(),
+                           v_cache.data_ptr(), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_kv_append")
     return q_out
@@ -987,28 +1027,35 @@ def window_attn_step(q, k_cache, v_cache, pages, lens, *, window: int = 0, sinks
     (dr_window_attn_step): q [B,Hq,d]; k_cache, v_cache, pages as there; lens int64 [B], the
     sequences' tokens with the new one (<= 0: none).  Returns (out [B,Hq,d], lse fp32 [B,Hq] or
     None)."""
-    _on_one_device(q, lens, out, lse, workspace)
-    if q.dim() != 3 or q.dtype not in _DT:
+    dev = _current_device()
+    shape, dt = q.shape, q.dtype
+    if len(shape) != 3 or dt not in _DT:
         raise ValueError("q must be float32 or bfloat16 [B,Hq,d]")
-    B, Hq, d = q.shape
-    n_pages, Hk, page, max_pages = _cache_of(k_cache, v_cache, pages, B, d, q.dtype)
-    _like(lens, (B,), torch.int64, "lens")
-    _like(out, q.shape, q.dtype, "out")
-    _like(lse, (B, Hq), torch.float32, "lse")
+    B, Hq, d = shape
+    _contiguous_at(q, shape, dt, dev, "q")
+    n_pages, Hk, page, max_pages = _cache_of(k_cache, v_cache, pages, B, d, dt, dev)
+    _contiguous_at(lens, (B,), torch.int64, dev, "lens")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
-    desc = AttnStepDesc(B, Hq, Hk, d, n_pages, page, max_pages, window, sinks, _DT[q.dtype], 0,
+    desc = AttnStepDesc(B, Hq, Hk, d, n_pages, page, max_pages, window, sinks, _DT[dt], 0,
                         d ** -0.5 if scale is None else scale)
     with _stream_scope(stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        workspace = _workspace(_lib.dr_window_attn_step_workspace_bytes, desc, workspace, q.device,
-                               "dr_window_attn_step_workspace_bytes")
-        rc = _lib.dr_window_attn_step(ctypes.byref(desc), _at(q), _at(k_cache), _at(v_cache), _at(pages),
-                                      _at(lens), _at(out), _at(lse), _at(workspace), _bytes(workspace),
-                                      _raw_stream(stream))
+            out = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _contiguous_at(out, shape, dt, dev, "out")
+        if lse is not None:
+            _contiguous_at(lse, (B, Hq), torch.float32, dev, "lse")
+        elif return_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _workspace(_lib.dr_window_attn_step_workspace_bytes, desc, None, dev,
+                                   "dr_window_attn_step_workspace_bytes")
+        else:
+            _on_one_device(workspace)
+    rc = _lib.dr_window_attn_step(ctypes.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                  pages.data_ptr(), lens.data_ptr(), out.data_ptr(), _at(lse), _at(workspace),
+                                  _bytes(workspace), _raw_stream(stream))
     if rc != DR_OK:
         raise DrError(rc, "dr_window_attn_step")
     return out, lse
