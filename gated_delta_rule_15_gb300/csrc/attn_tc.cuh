@@ -37,8 +37,8 @@ inline bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t hea
 }
 
 // Query heads (of those that share a key head) whose rows lie side by side in a tile of 128 rows, a
-// power of two: tiles then span fewer tokens, and less of what they compute is masked.
-inline int heads_in_tile(int group) { return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1; }
+// power of two (its log2): tiles then span fewer tokens, and less of what they compute is masked.
+inline int heads_in_tile(int group) { return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0; }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 // Which of the keys j0 .. j0 + 31 the query i sees, of those before `end`.
@@ -67,6 +67,13 @@ struct KeyTiles {
     }
 };
 
+// Whether x holds in any thread of the two warps that share the named barrier `id`.
+__device__ __forceinline__ bool any_of(uint32_t id, bool x) {
+    uint32_t y;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, 64, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(y) : "r"((uint32_t)x), "r"(id) : "memory");
+    return y != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

@@ -39,9 +39,9 @@ constexpr int kMaxSplitTiles = 8;      // key tiles with sinks that are cut
 struct BwdArgs {
     AttnProblem p;
     int *status;
-    int gp, runs, tokens;      // query heads side by side, runs of them, tokens of 128 rows
+    int gs, runs, tokens;      // log2 of the query heads side by side, runs of them, tokens of 128 rows
     int64_t items;             // dq: items; dk, dv: blocks that are not chunks
-    float2 *stats;             // [key head and run][row][gp] (lse log2 e, delta)
+    float2 *stats;             // [key head and run][row][head of the run] (lse log2 e, delta)
     // sinks: 0 tiles where they are not cut
     int sink_tiles, sink_rows, chunk;
     int64_t chunk_slots;
@@ -71,7 +71,7 @@ __device__ __forceinline__ bool item_of(const BwdArgs &a, int64_t k, Item &im) {
     im.lo = (int)lo;
     im.len = len;
     im.q0 = j * a.tokens;
-    im.h0 = im.hr / a.runs * (p.Hq / p.Hk) + im.hr % a.runs * a.gp;
+    im.h0 = im.hr / a.runs * (p.Hq / p.Hk) + (im.hr % a.runs << a.gs);
     return true;
 }
 
@@ -165,9 +165,9 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(b_qfree);
             const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-            const int i = im.q0 + row / a.gp;
+            const int i = im.q0 + (row >> a.gs);
             wait(b_stat + (it & 1), it >> 1);
-            const float2 stat = i < im.len ? a.stats[((int64_t)im.hr * p.seqs.total + im.lo + i) * a.gp + row % a.gp] : make_float2(0.f, 0.f);
+            const float2 stat = i < im.len ? a.stats[(((int64_t)im.hr * p.seqs.total + im.lo + i) << a.gs) + (row & ((1 << a.gs) - 1))] : make_float2(0.f, 0.f);
             __syncwarp();
             if (lane == 0) mbar_arrive(b_sfree + (it & 1));
             const float2 f2 = make_float2(f, f), l2 = make_float2(-stat.x, -stat.x), d2 = make_float2(-stat.y, -stat.y);
@@ -231,8 +231,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             tmem_wait_ld();
             to_pieces(o, p.scale, u);
             put_rows<C / 8>(u, lane, [&](int r) {
-                const int rr = 32 * quarter + r, ii = im.q0 + rr / a.gp;
-                return ii < im.len ? static_cast<__nv_bfloat16 *>(p.dq) + (int64_t)(im.lo + ii) * p.dqs + (im.h0 + rr % a.gp) * D + C * group : nullptr;
+                const int rr = 32 * quarter + r, ii = im.q0 + (rr >> a.gs);
+                return ii < im.len ? static_cast<__nv_bfloat16 *>(p.dq) + (int64_t)(im.lo + ii) * p.dqs + (im.h0 + (rr & ((1 << a.gs) - 1))) * D + C * group : nullptr;
             });
             tc_fence_before();
         }
@@ -382,17 +382,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 uint4 o[U], d[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + r / a.gp;
+                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + (r >> a.gs);
                     o[u] = d[u] = make_uint4(0u, 0u, 0u, 0u);
                     if (i < im.len) {
-                        const int64_t at = ((int64_t)(im.lo + i) * p.Hq + im.h0 + r % a.gp) * D + 8 * l;
+                        const int64_t at = ((int64_t)(im.lo + i) * p.Hq + im.h0 + (r & ((1 << a.gs) - 1))) * D + 8 * l;
                         o[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.out) + at);
                         d[u] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.d_out) + at);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + r / a.gp;
+                    const int r = r0 + u * RPW + lane / LPR, i = im.q0 + (r >> a.gs);
                     const uint32_t x[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, y[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
                     float sum = 0.f;
 #pragma unroll
@@ -403,8 +403,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                     for (int w = 1; w < LPR; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
                     if (l == 0 && i < im.len)
-                        a.stats[((int64_t)im.hr * p.seqs.total + im.lo + i) * a.gp + r % a.gp] =
-                            make_float2(p.lse[(int64_t)(im.lo + i) * p.Hq + im.h0 + r % a.gp] * kLog2e, sum);
+                        a.stats[(((int64_t)im.hr * p.seqs.total + im.lo + i) << a.gs) + (r & ((1 << a.gs) - 1))] =
+                            make_float2(p.lse[(int64_t)(im.lo + i) * p.Hq + im.h0 + (r & ((1 << a.gs) - 1))] * kLog2e, sum);
                 }
             }
             __syncwarp();
@@ -531,7 +531,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const float4 *st = reinterpret_cast<const float4 *>(stats + (t % NS) * 256 + col0);
             float s[32];
             uint32_t w[16], bits = 0xffffffffu;
-            if (!whole) bits = low_bits(min(see - q0, 128) * a.gp - col0) & ~low_bits(min(max(j - q0, 0), 128) * a.gp - col0);
+            if (!whole) bits = low_bits(min(see - q0, 128) * (1 << a.gs) - col0) & ~low_bits((min(max(j - q0, 0), 128) << a.gs) - col0);
             wait(b_stat + t % NS, t / NS);
             wait(b_s, t);
             tmem_ld32(tl + col0, s);
@@ -555,7 +555,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (q0 + a.tokens > len) {     // rows of no query of this sequence are zeros
                 wait_ring(b_full, 2 * t + 1);
                 for (int e = 0; e < 2; ++e)
-                    zero_rows<L::PANELS>(smem_u32(sm) + L::QO + ((2 * t + e) % NB) * L::TILE, (len - q0) * a.gp, 128, tid);
+                    zero_rows<L::PANELS>(smem_u32(sm) + L::QO + ((2 * t + e) % NB) * L::TILE, (len - q0) << a.gs, 128, tid);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -637,7 +637,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     q0 += a.tokens;
                     if (q0 >= qb) {
                         q0 = qa;
-                        h0 += a.gp;
+                        h0 += 1 << a.gs;
                     }
                 }
             }
@@ -689,13 +689,13 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         tc::fewer_regs<kDkvOtherRegs>();
         // ---------------------------------------------------------------- statistics of the queries
         int q0 = qa;
-        const float2 *src = a.stats + ((int64_t)hk * a.runs * p.seqs.total + lo) * a.gp;
+        const float2 *src = a.stats + (((int64_t)hk * a.runs * p.seqs.total + lo) << a.gs);
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const int rows = min(len - q0, a.tokens) * a.gp;
+            const int rows = min(len - q0, a.tokens) << a.gs;
             float2 x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = lane + 32 * e < rows ? src[(int64_t)q0 * a.gp + lane + 32 * e] : make_float2(0.f, 0.f);
+            for (int e = 0; e < 4; ++e) x[e] = lane + 32 * e < rows ? src[((int64_t)q0 << a.gs) + lane + 32 * e] : make_float2(0.f, 0.f);
             if (t >= NS) wait(b_sfree + t % NS, t / NS - 1);
             float *dst = stats + (t % NS) * 256 + lane;
 #pragma unroll
@@ -708,7 +708,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             q0 += a.tokens;
             if (q0 >= qb) {
                 q0 = qa;
-                src += p.seqs.total * a.gp;
+                src += p.seqs.total << a.gs;
             }
         }
     } else {
@@ -755,9 +755,9 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // How the sinks' queries are cut, and where the workspace's parts lie.
 size_t plan(const AttnProblem &p, BwdArgs &a, char *ws) {
     a.p = p;
-    a.gp = heads_in_tile(p.Hq / p.Hk);
-    a.runs = p.Hq / p.Hk / a.gp;
-    a.tokens = 128 / a.gp;
+    a.gs = heads_in_tile(p.Hq / p.Hk);
+    a.runs = p.Hq / p.Hk >> a.gs;
+    a.tokens = 128 >> a.gs;
     size_t at = 0;
     a.stats = (float2 *)(ws + at);
     at += round256(sizeof(float2) * (size_t)(p.seqs.total * p.Hq));
@@ -782,8 +782,8 @@ size_t plan(const AttnProblem &p, BwdArgs &a, char *ws) {
 template <int D>
 int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
     CUtensorMap m[4];
-    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, a.gp, 128 / a.gp) ||
-        !make_map(&m[1], p.d_out, p.seqs.total, p.Hq, p.d, (int64_t)p.Hq * p.d, a.gp, 128 / a.gp) ||
+    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, 1 << a.gs, 128 >> a.gs) ||
+        !make_map(&m[1], p.d_out, p.seqs.total, p.Hq, p.d, (int64_t)p.Hq * p.d, 1 << a.gs, 128 >> a.gs) ||
         !make_map(&m[2], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[3], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
         return kErrCuda;
     constexpr int smem_q = DqLayout<D>::TOTAL + 1024, smem_kv = DkvLayout<D>::TOTAL;

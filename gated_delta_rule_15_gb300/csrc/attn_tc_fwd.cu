@@ -5,13 +5,13 @@
 // through items of that kind (a run of tokens, a key head, up to four of its query heads side by side).
 //     S = Q K^T        [128 x 128]   both from shared memory, S in tensor memory
 //     O += P V         [128 x d]     P (bf16) from tensor memory, over S's place; V as loaded (MN-major)
-// The running softmax: a thread holds a row; with f = scale log2 e and m the row's reference, p = 2^(f s - f m), and
-// O and l hold the sums for that m.  m follows the row's maximum only when that is more than 2^8 above it
-// (p stays below 2^8, exact as a power-of-two-free rescale would be), so O in tensor memory is rescaled
+// The running softmax: with f = scale log2 e and m the row's reference, p = 2^(f s - f m), and
+// O and l hold the sums for that m.  m follows the row's maximum only when that is more than 2^kAbove above it
+// (P is a floating-point operand: its precision does not depend on m), so O in tensor memory is rescaled
 // a few times a row at most.  A row's decisions depend on the row alone.
 //
-// Warps 0..3 and 4..7 are the stages' softmax and write their outputs; warp 8 issues the copies, warps 9 and 10
-// the stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor
+// Warps 0..7 and 8..15 are the stages' softmax and write their outputs, two for each 32 rows with 64 keys a
+// thread, which ask one another only whether a maximum rose; warp 16 issues the copies, warps 17 and 18 the stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor
 // cores work for the other.  (One thread for both stages is late: a tile's sixteen products take it 900 cycles to
 // issue and their waits 400, which the tensor cores need 1024 for.)
 //
@@ -27,16 +27,17 @@ namespace dr {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9;
-// Registers a thread: launched with 168; the softmax warps take what the others give back.
-constexpr int kSoftRegs = 208, kIssueRegs = 80;
-static_assert(8 * kSoftRegs + 4 * kIssueRegs <= 12 * 168, "register split");
+constexpr int kStageWarps = 8, kLoadWarp = 2 * kStageWarps, kMmaWarp = kLoadWarp + 1, kThreads = 32 * (kLoadWarp + 4);   // (two MMA warps)
+// Registers a thread: launched with 96; the softmax warps take what the others give back.
+constexpr int kSoftRegs = 104, kIssueRegs = 56;
+static_assert(2 * kStageWarps * kSoftRegs + 4 * kIssueRegs <= kThreads / 32 * 96, "register split");
+constexpr float kAbove = 8.f;
 
 struct FwdArgs {
     AttnProblem p;
     int *status;
-    int gp, runs;          // query heads side by side; runs of them in a key head's group
-    int tokens;            // of an item: 2 * 128 / gp
+    int gs, runs;          // log2 of the query heads side by side; runs of them in a key head's group
+    int tokens;            // of an item: 256 >> gs
     int64_t items;
 };
 
@@ -48,7 +49,7 @@ struct Item {
 template <int D>
 struct Layout {
     static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;   // key and value buffers
-    static constexpr uint32_t Q = 0, KV = 2 * TILE, BARS = KV + NB * TILE;
+    static constexpr uint32_t Q = 0, KV = 2 * TILE, ROWS = KV + NB * TILE, BARS = ROWS + 2 * 128 * 4;
     static constexpr uint32_t TOTAL = BARS + (2 * NB + 12) * 8 + 2 * sizeof(Item);
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
@@ -78,9 +79,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + i, 1);
-            mbar_init(b_qfree + i, 1 + 4);   // the MMAs, and every softmax warp has seen the item
+            mbar_init(b_qfree + i, 1 + kStageWarps);   // the MMAs, and every softmax warp has seen the item
             mbar_init(b_s + i, 1);
-            mbar_init(b_p + i, 4);
+            mbar_init(b_p + i, kStageWarps);
             mbar_init(b_o + i, 1);
         }
         mbar_init(b_end, 2);
@@ -104,12 +105,23 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     auto wait_ring = [&](uint64_t *bar, int k) { wait(bar + k % NB, k / NB); };
     const int tt = a.tokens / 2;       // tokens of a stage
 
-    if (warp < 8) {
+    if (warp < kLoadWarp) {
         tc::more_regs<kSoftRegs>();
         // ---------------------------------------------------------------- softmax
-        const int st = warp >> 2, row = tid & 127, quarter = warp & 3;
-        const uint32_t tS = tm + ((uint32_t)(32 * quarter) << 16) + 128 * st, tO = tS + 256;
+        // this thread: a row, half of the keys; the warp with the other half is the pair's other one
+        const int st = warp / kStageWarps, quarter = warp & 3, half = warp >> 2 & 1, row = 32 * quarter + lane, col0 = 64 * half;
+        const uint32_t tS = tm + ((uint32_t)(32 * quarter) << 16) + 128 * st, tO = tS + 256 + half * (D / 2), pair = 1 + 4 * st + quarter;
+        float *rows = reinterpret_cast<float *>(sm + L::ROWS) + 128 * st + row;
+        // the other thread's x, for both
+        auto exchange = [&](float x, auto join) {
+            if (half) *rows = x;
+            named_sync(pair, 64);
+            if (!half) *rows = x = join(x, *rows);
+            named_sync(pair, 64);
+            return half ? *rows : x;
+        };
         const float f = p.scale * kLog2e;
+        const float2 f2 = make_float2(f, f);
         int n_tile = 0, n_out = 0, ring = 0;   // tiles and results of this stage so far; copies
 #pragma unroll 1
         for (int it = 0;; ++it) {
@@ -119,8 +131,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) mbar_arrive(b_qfree + st);
             const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-            const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt), i = ta + row / a.gp;
-            float m = -INFINITY, l = 0.f;
+            const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt), i = ta + (row >> a.gs);
+            float m = -INFINITY;
+            float2 l = make_float2(0.f, 0.f);      // of this thread's keys
             bool first = true;
 #pragma unroll 1
             for (int t = 0; t < kt.n; ++t) {
@@ -129,78 +142,62 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const bool whole = kc == kKeys && stop - 1 <= ta && (k0 > tb - 1 - p.window || stop <= p.sinks);
                 wait(b_s + st, n_tile);
                 ++n_tile;
-                float s[128];
-                float2 sum = make_float2(0.f, 0.f);
-                float top = -INFINITY;
+                float s[64];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (32 * c < kc) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+                for (int c = 0; c < 2; ++c)
+                    if (col0 + 32 * c < kc) tmem_ld32(tS + col0 + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
                 tmem_wait_ld();
                 if (!whole) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (32 * c >= kc) continue;
-                        const uint32_t bits = seen_bits(i, k0 + 32 * c, stop, p.window, p.sinks);
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t bits = seen_bits(i, k0 + col0 + 32 * c, stop, p.window, p.sinks);
 #pragma unroll
                         for (int x = 0; x < 32; ++x) s[32 * c + x] = bits >> x & 1 ? s[32 * c + x] : -INFINITY;
                     }
                 }
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c >= kc) continue;
-                    float u = -INFINITY, v = -INFINITY;
+                for (int x = 0; x < 64; x += 8)
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4) {
-                        u = max3(u, s[32 * c + x], s[32 * c + x + 1]);
-                        v = max3(v, s[32 * c + x + 2], s[32 * c + x + 3]);
-                    }
-                    top = max3(top, u, v);
-                }
+                    for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[x + 2 * e], s[x + 2 * e + 1]);
+                float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                 // the row's reference follows its maximum
-                const bool up = (top - m) * f > 8.f;       // (also from -infinity; not where both are)
-                if (__any_sync(0xffffffffu, up)) {
+                if (any_of(pair, (top - m) * f > kAbove)) {
+                    top = exchange(top, [](float x, float y) { return fmaxf(x, y); });
+                    const bool up = (top - m) * f > kAbove;       // (also from -infinity; not where both are)
                     const float turn = up ? ex2((m - top) * f) : 1.f;
-                    l *= turn;
+                    l = mul2(l, make_float2(turn, turn));
                     m = up ? top : m;
                     if (!first) {       // S is there, so the products before it are done
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            tmem_ld32(tO + 32 * c, o);
+                            float o[16];
+                            tmem_ld16(tO + 16 * c, o);
                             tmem_wait_ld();
+                            uint32_t w[16];
 #pragma unroll
-                            for (int x = 0; x < 32; x += 2) {
-                                const float2 y = mul2(make_float2(o[x], o[x + 1]), make_float2(turn, turn));
-                                o[x] = y.x;
-                                o[x + 1] = y.y;
-                            }
-                            tmem_st32(tO + 32 * c, o);
+                            for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * turn);
+                            tmem_st16u(tO + 16 * c, w);
                         }
                     }
                 }
                 first = false;
                 const float base = m == -INFINITY ? 0.f : -m * f;
-                const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
+                const float2 b2 = make_float2(base, base);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c >= kc) continue;
+                for (int c = 0; c < 2; ++c) {
+                    if (col0 + 32 * c >= kc) break;
+                    uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int at = 32 * c + 16 * e + 2 * x;
-                            float2 y = fma2(make_float2(s[at], s[at + 1]), f2, b2);
-                            y.x = ex2(y.x);
-                            y.y = ex2(y.y);
-                            sum = add2(sum, y);
-                            w[x] = pack_bf16(y.x, y.y);
-                        }
-                        tmem_st4u(tS + 16 * c + 8 * e, *reinterpret_cast<uint32_t(*)[4]>(w));
-                        tmem_st4u(tS + 16 * c + 8 * e + 4, *reinterpret_cast<uint32_t(*)[4]>(w + 4));
+                    for (int x = 0; x < 16; ++x) {
+                        float2 y = fma2(make_float2(s[32 * c + 2 * x], s[32 * c + 2 * x + 1]), f2, b2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        l = add2(l, y);
+                        w[x] = pack_bf16(y.x, y.y);
                     }
+                    tmem_st16u(tS + col0 + 16 * c, w);
                 }
-                l += sum.x + sum.y;
                 // values of rows behind the sequence's end that the product takes in are zeros
                 const int kc16 = (kc + 15) & ~15;
                 if (k0 + kc16 > im.len) {
@@ -208,7 +205,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     wait_ring(b_full, v);
                     const uint32_t V = smem_u32(sm) + L::KV + (v % NB) * L::TILE;
                     const int r0 = im.len - k0, n = (kc16 - r0) * 8;
-                    for (int x = row; x < L::PANELS * n; x += 128) {
+                    for (int x = tid & 255; x < L::PANELS * n; x += 256) {
                         const int r = r0 + x % n / 8;
                         sts128(V + (x / n) * 16384 + r * 128 + (x % 8) * 16, 0, 0, 0, 0);
                     }
@@ -221,24 +218,22 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             }
             ring += 2 * kt.n;
             if (ta < tb) {
+                const float sum = exchange(l.x + l.y, [](float x, float y) { return x + y; }), inv = 1.f / sum;
+                if (half == 0 && i < im.len) p.lse[(int64_t)(im.lo + i) * p.Hq + im.h0 + (row & ((1 << a.gs) - 1))] = (m * f + log2f(sum)) * kLn2;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(im.lo + ta) * p.Hq + im.h0) * D + half * (D / 2);
                 wait(b_o + st, n_out++);
-                const bool mine = i < im.len;
-                const int h = im.h0 + row % a.gp;
-                const float inv = 1.f / l;
-                const int64_t at = (int64_t)(im.lo + i) * p.Hq + h;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
                     float o[32];
                     uint4 u[4];
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
                     to_pieces(o, inv, u);
                     put_rows<4>(u, lane, [&](int r) {
-                        const int rr = 32 * quarter + r, ii = ta + rr / a.gp;
-                        return ii < im.len ? static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(im.lo + ii) * p.Hq + im.h0 + rr % a.gp) * D + 32 * c : nullptr;
+                        const int rr = 32 * quarter + r, x = rr >> a.gs;
+                        return ta + x < im.len ? out + ((int64_t)x * p.Hq + (rr & ((1 << a.gs) - 1))) * D + 32 * c : nullptr;
                     });
                 }
-                if (mine) p.lse[at] = (m * f + log2f(l)) * kLn2;
             }
             tc_fence_before();     // (the next item's first P follows)
         }
@@ -274,7 +269,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     len = (int)p.seqs.T;
                 }
                 const int hk = hr / a.runs, q0 = j * a.tokens;
-                const Item im{(int)lo, len, q0, hk * (p.Hq / p.Hk) + (hr % a.runs) * a.gp};
+                const Item im{(int)lo, len, q0, hk * (p.Hq / p.Hk) + (hr % a.runs << a.gs)};
                 const KeyTiles kt(q0, a.tokens, len, p.window, p.sinks);
                 if (elect_one()) {
                     for (int st = 0; st < 2; ++st) {
@@ -335,10 +330,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                             wait(b_p + st, n_p++);
                             if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) mma_bf16_ts(tO, tS + 8 * k, desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                                for (int k = 0; k < 8; ++k) mma_bf16_ts(tO, tS + 8 * k + (k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
                             } else {
 #pragma unroll 1
-                                for (int k = 0; k < ks; ++k) mma_bf16_ts(tO, tS + 8 * k, desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                                for (int k = 0; k < ks; ++k) mma_bf16_ts(tO, tS + 8 * k + (k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
                             }
                             more = true;
                             pend = -1;
@@ -394,12 +389,12 @@ int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream) {
     FwdArgs a{};
     a.p = p;
     a.status = status;
-    a.gp = heads_in_tile(p.Hq / p.Hk);
-    a.runs = p.Hq / p.Hk / a.gp;
-    a.tokens = 256 / a.gp;
+    a.gs = heads_in_tile(p.Hq / p.Hk);
+    a.runs = p.Hq / p.Hk >> a.gs;
+    a.tokens = 256 >> a.gs;
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
     CUtensorMap m[3];
-    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, a.gp, 128 / a.gp) ||
+    if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, 1 << a.gs, 128 >> a.gs) ||
         !make_map(&m[1], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[2], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
         return kErrCuda;
     return p.d == 64 ? launch<64>(m, a, stream) : launch<128>(m, a, stream);
