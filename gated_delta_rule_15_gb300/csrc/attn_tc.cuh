@@ -46,25 +46,37 @@ __device__ __forceinline__ uint32_t seen_bits(int i, int j0, int end, int window
     return low_bits(min(i + 1, end) - j0) & (~low_bits(i - window + 1 - j0) | low_bits(sinks - j0));
 }
 
-// The key tiles of the queries q0 .. q0 + count - 1 of a sequence: sinks in front of the first one's window, then the
-// keys from there to the last one.
+// The keys of the queries q0 .. q0 + count - 1 of a sequence, one behind another: the sinks in front of the first
+// one's window, filled up to a multiple of 32 (the rest is masked), then the keys from there to the last one; in tiles of 128.
+// (Tiles of sinks apart cost an item a tile's time for four keys.)
 struct KeyTiles {
-    int sinks, n_sink, near0, end, n;
+    int sinks, s32, near0, end, total, n;
     __device__ __forceinline__ KeyTiles(int q0, int count, int len, int window, int all_sinks) {
         near0 = max(0, q0 - window + 1);
         sinks = min(all_sinks, near0);
+        s32 = (sinks + 31) & ~31;          // (at most q0: those rows are the sequence's)
         end = min(len, q0 + count);
-        n_sink = (sinks + kKeys - 1) / kKeys;
-        n = n_sink + (end - near0 + kKeys - 1) / kKeys;
+        total = s32 + end - near0;
+        n = (total + kKeys - 1) / kKeys;
     }
-    __device__ __forceinline__ int first(int t) const { return t < n_sink ? t * kKeys : near0 + (t - n_sink) * kKeys; }
-    __device__ __forceinline__ int stop(int t) const { return t < n_sink ? min(sinks, (t + 1) * kKeys) : min(end, first(t) + kKeys); }
-    // whether one of the queries a .. b - 1 sees a key of tile t
+    __device__ __forceinline__ int count(int t) const { return min(kKeys, total - t * kKeys); }
+    __device__ __forceinline__ int key(int at) const { return at < s32 ? at : near0 + at - s32; }
+    // the keys of `at` .. + 31 (a multiple of 32) that query i sees
+    __device__ __forceinline__ uint32_t bits(int i, int at, int window, int all_sinks) const {
+        return seen_bits(i, key(at), at < s32 ? sinks : end, window, all_sinks);
+    }
+    // whether every one of the queries a .. b - 1 sees all of tile t; whether one sees any of it
+    __device__ __forceinline__ bool whole(int t, int a, int b, int window, int all_sinks) const {
+        const int at = t * kKeys, k0 = near0 + at - s32;
+        if (at < s32) return at + kKeys <= sinks;
+        return at + kKeys <= total && k0 + kKeys - 1 <= a && (k0 > b - 1 - window || k0 + kKeys <= all_sinks);
+    }
     __device__ __forceinline__ bool meets(int t, int a, int b, int window, int all_sinks) const {
-        if (a >= b) return false;
-        const int k0 = first(t);
-        return t < n_sink || (k0 < b && (k0 + kKeys > a - window + 1 || k0 < all_sinks));
+        const int at = t * kKeys, k0 = near0 + at - s32;
+        return a < b && (at < s32 || (k0 < b && (k0 + kKeys > a - window + 1 || k0 < all_sinks)));
     }
+    // tile t's first row that is behind the sequence
+    __device__ __forceinline__ int behind(int t, int len) const { return s32 + len - near0 - t * kKeys; }
 };
 
 // Whether x holds in any thread of the two warps that share the named barrier `id`.

@@ -173,8 +173,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const float2 f2 = make_float2(f, f), l2 = make_float2(-stat.x, -stat.x), d2 = make_float2(-stat.y, -stat.y);
 #pragma unroll 1
             for (int t = 0; t < kt.n; ++t, ++n_tile) {
-                const int k0 = kt.first(t), stop = kt.stop(t), kc = stop - k0, kc16 = (kc + 15) & ~15;
-                const bool whole = kc == kKeys && stop - 1 <= im.q0 && (k0 > kt.end - 1 - p.window || stop <= p.sinks);
+                const int kc = kt.count(t), kc16 = (kc + 15) & ~15, r0 = kt.behind(t, im.len);
+                const bool whole = kt.whole(t, im.q0, kt.end, p.window, p.sinks);
                 const bool mine = col0 < kc;
                 const uint32_t tD = tl + TM_DP + 128 * (n_tile & 1) + col0;
                 float s[32];
@@ -194,8 +194,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         s[x + 1] = ex2(y.y);
                     }
                 }
-                if (k0 + kc16 > im.len)
-                    zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (ring + k_at(t)) % NB * L::TILE, im.len - k0, kc16, tid);
+                if (kc16 > r0) zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (ring + k_at(t)) % NB * L::TILE, r0, kc16, tid);
                 wait(b_dp + (n_tile & 1), n_tile >> 1);
                 if (mine) {
                     float dp[32];
@@ -209,7 +208,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         s[x + 1] = y.y;
                     }
                     if (!whole) {      // (0 times the product of rows of others may be anything)
-                        const uint32_t bits = seen_bits(i, k0 + col0, stop, p.window, p.sinks);
+                        const uint32_t bits = kt.bits(i, kKeys * t + col0, p.window, p.sinks);
 #pragma unroll
                         for (int x = 0; x < 32; ++x) s[x] = bits >> x & 1 ? s[x] : 0.f;
                     }
@@ -240,15 +239,15 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         tc::fewer_regs<kDqOtherRegs>();
         // ---------------------------------------------------------------- copies
         int it = 0, ring = 0;
-        auto load = [&](int k, const CUtensorMap *map, int hk, int row0, int rows) {   // by one lane
+        auto load = [&](int k, const CUtensorMap *map, int hk, int lo, const KeyTiles &kt, int t) {   // by one lane
             const int b = k % NB;
             if (k >= NB) wait(b_free + b, k / NB - 1);
-            const int boxes = (rows + kBox - 1) / kBox;
+            const int boxes = (kt.count(t) + kBox - 1) / kBox;
             unsigned char *dst = sm + L::KV + b * L::TILE;
             mbar_arrive_expect_tx(b_full + b, boxes * kBox * 128 * L::PANELS);
             for (int e = 0; e < L::PANELS; ++e)
                 for (int x = 0; x < boxes; ++x)
-                    tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, row0 + x * kBox);
+                    tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, lo + kt.key(t * kKeys + x * kBox));
         };
 #pragma unroll 1
         for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
@@ -265,7 +264,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     tc::tma_load_3d(sm + L::O + e * 16384, &to, b_q, 64 * e, im.h0, im.lo + im.q0);
                 }
                 auto tile = [&](bool key, int t) {
-                    load(ring + (key ? k_at(t) : v_at(t)), key ? &tk : &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                    load(ring + (key ? k_at(t) : v_at(t)), key ? &tk : &tv, hk, im.lo, kt, t);
                 };
                 tile(true, 0);
                 tile(false, 0);
@@ -305,7 +304,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const Item im = items[it & 1];
                 if (im.len < 0 || *polls == 0) break;
                 const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-                auto n16 = [&](int t) { return (kt.stop(t) - kt.first(t) + 15) & ~15; };
+                auto n16 = [&](int t) { return (kt.count(t) + 15) & ~15; };
                 auto rows_by_rows = [&](uint32_t d, int b, int t) {
                     const uint64_t db = desc_add(dK, b * L::TILE);
                     const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16(t) - 16) << 14);

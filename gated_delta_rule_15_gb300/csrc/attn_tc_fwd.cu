@@ -138,8 +138,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 #pragma unroll 1
             for (int t = 0; t < kt.n; ++t) {
                 if (!kt.meets(t, ta, tb, p.window, p.sinks)) continue;
-                const int k0 = kt.first(t), stop = kt.stop(t), kc = stop - k0;
-                const bool whole = kc == kKeys && stop - 1 <= ta && (k0 > tb - 1 - p.window || stop <= p.sinks);
+                const int kc = kt.count(t);
+                const bool whole = kt.whole(t, ta, tb, p.window, p.sinks);
                 wait(b_s + st, n_tile);
                 ++n_tile;
                 float s[64];
@@ -150,7 +150,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint32_t bits = seen_bits(i, k0 + col0 + 32 * c, stop, p.window, p.sinks);
+                        const uint32_t bits = kt.bits(i, kKeys * t + col0 + 32 * c, p.window, p.sinks);
 #pragma unroll
                         for (int x = 0; x < 32; ++x) s[32 * c + x] = bits >> x & 1 ? s[32 * c + x] : -INFINITY;
                     }
@@ -199,12 +199,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     tmem_st16u(tS + col0 + 16 * c, w);
                 }
                 // values of rows behind the sequence's end that the product takes in are zeros
-                const int kc16 = (kc + 15) & ~15;
-                if (k0 + kc16 > im.len) {
+                const int kc16 = (kc + 15) & ~15, r0 = kt.behind(t, im.len);
+                if (kc16 > r0) {
                     const int v = ring + 2 * t + 1;
                     wait_ring(b_full, v);
                     const uint32_t V = smem_u32(sm) + L::KV + (v % NB) * L::TILE;
-                    const int r0 = im.len - k0, n = (kc16 - r0) * 8;
+                    const int n = (kc16 - r0) * 8;
                     for (int x = tid & 255; x < L::PANELS * n; x += 256) {
                         const int r = r0 + x % n / 8;
                         sts128(V + (x / n) * 16384 + r * 128 + (x % 8) * 16, 0, 0, 0, 0);
@@ -242,15 +242,15 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- copies
             int it = 0, ring = 0;
-            auto load = [&](int k, const CUtensorMap *map, int hk, int row0, int rows) {   // by one lane
+            auto load = [&](int k, const CUtensorMap *map, int hk, int lo, const KeyTiles &kt, int t) {   // by one lane
                 const int b = k % NB;
                 if (k >= NB) wait(b_free + b, k / NB - 1);
-                const int boxes = (rows + kBox - 1) / kBox;
+                const int boxes = (kt.count(t) + kBox - 1) / kBox;
                 unsigned char *dst = sm + L::KV + b * L::TILE;
                 mbar_arrive_expect_tx(b_full + b, boxes * kBox * 128 * L::PANELS);
                 for (int e = 0; e < L::PANELS; ++e)
                     for (int x = 0; x < boxes; ++x)
-                        tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, row0 + x * kBox);
+                        tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, lo + kt.key(t * kKeys + x * kBox));
             };
 #pragma unroll 1
             for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
@@ -278,11 +278,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         mbar_arrive_expect_tx(b_q + st, L::TILE);
                         for (int e = 0; e < L::PANELS; ++e)
                             tc::tma_load_3d(sm + L::Q + st * L::TILE + e * 16384, &tq, b_q + st, 64 * e, im.h0, im.lo + q0 + st * tt);
-                        if (st == 0) load(ring, &tk, hk, im.lo + kt.first(0), kt.stop(0) - kt.first(0));
+                        if (st == 0) load(ring, &tk, hk, im.lo, kt, 0);
                     }
                     for (int t = 0; t < kt.n; ++t) {
-                        if (t > 0) load(ring + 2 * t, &tk, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
-                        load(ring + 2 * t + 1, &tv, hk, im.lo + kt.first(t), kt.stop(t) - kt.first(t));
+                        if (t > 0) load(ring + 2 * t, &tk, hk, im.lo, kt, t);
+                        load(ring + 2 * t + 1, &tv, hk, im.lo, kt, t);
                     }
                 }
                 __syncwarp();
@@ -325,7 +325,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         const int v = ring + 2 * t - 1, b = v % NB;
                         wait(b_full + b, v / NB);
                         if (pend >= 0) {
-                            const int ks = (kt.stop(pend) - kt.first(pend) + 15) / 16;
+                            const int ks = (kt.count(pend) + 15) / 16;
                             const uint64_t dv = desc_add(dV, b * L::TILE);
                             wait(b_p + st, n_p++);
                             if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
@@ -342,7 +342,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     };
 #pragma unroll 1
                     for (int t = 0; t < kt.n; ++t) {
-                        const int k = ring + 2 * t, b = k % NB, n16 = (kt.stop(t) - kt.first(t) + 15) & ~15;
+                        const int k = ring + 2 * t, b = k % NB, n16 = (kt.count(t) + 15) & ~15;
                         wait(b_full + b, k / NB);
                         if (t > 0) flush(t);
                         if (kt.meets(t, ta, tb, p.window, p.sinks)) {
