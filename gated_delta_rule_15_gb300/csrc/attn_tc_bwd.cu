@@ -40,7 +40,7 @@ struct BwdArgs {
     AttnProblem p;
     int *status;
     int gs, runs, tokens;      // log2 of the query heads side by side, runs of them, tokens of 128 rows
-    int64_t items;             // dq: items; dk, dv: blocks that are not chunks
+    int64_t items;             // of dq
     float2 *stats;             // [key head and run][row][head of the run] (lse log2 e, delta)
     // sinks: 0 tiles where they are not cut
     int sink_tiles, sink_rows, chunk;
@@ -437,9 +437,11 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     int64_t n, lo;
     int jt, len, hk, chunk = -1;
     int64_t slot = 0;
-    if ((int64_t)blockIdx.x < a.items) {
-        hk = (int)(blockIdx.x % p.Hk);
-        const int64_t k = blockIdx.x / p.Hk;
+    const int64_t chunks = a.chunk_slots * p.Hk * a.sink_tiles;     // first: short blocks come last
+    if ((int64_t)blockIdx.x >= chunks) {
+        int64_t k = blockIdx.x - chunks;
+        hk = (int)(k % p.Hk);
+        k /= p.Hk;
         if (p.seqs.cu) {
             if (!find_tile(p.seqs, kKeys, (int)k, n, jt, lo, len)) return;
         } else {       // early keys, which most queries see, first
@@ -449,7 +451,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             len = (int)p.seqs.T;
         }
     } else {
-        int64_t k = blockIdx.x - a.items;
+        int64_t k = blockIdx.x;
         hk = (int)(k % p.Hk);
         k /= p.Hk;
         jt = (int)(k % a.sink_tiles);
@@ -792,8 +794,7 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
     attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kDqThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    a.items = attn_tile_slots(p.seqs, kKeys) * p.Hk;
-    const int64_t blocks = a.items + a.chunk_slots * p.Hk * a.sink_tiles;
+    const int64_t blocks = (attn_tile_slots(p.seqs, kKeys) + a.chunk_slots * a.sink_tiles) * p.Hk;
     attn_dkv_kernel<D><<<(unsigned)blocks, kDkvThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     if (a.sink_tiles == 0) return kOk;
