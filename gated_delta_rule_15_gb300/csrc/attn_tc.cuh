@@ -51,6 +51,7 @@ __device__ __forceinline__ uint32_t seen_bits(int i, int j0, int end, int window
 // (Tiles of sinks apart cost an item a tile's time for four keys.)
 struct KeyTiles {
     int sinks, s32, near0, end, total, n;
+    KeyTiles() = default;
     __device__ __forceinline__ KeyTiles(int q0, int count, int len, int window, int all_sinks) {
         near0 = max(0, q0 - window + 1);
         sinks = min(all_sinks, near0);
@@ -65,19 +66,34 @@ struct KeyTiles {
     __device__ __forceinline__ uint32_t bits(int i, int at, int window, int all_sinks) const {
         return seen_bits(i, key(at), at < s32 ? sinks : end, window, all_sinks);
     }
-    // whether every one of the queries a .. b - 1 sees all of tile t; whether one sees any of it
-    __device__ __forceinline__ bool whole(int t, int a, int b, int window, int all_sinks) const {
-        const int at = t * kKeys, k0 = near0 + at - s32;
-        if (at < s32) return at + kKeys <= sinks;
-        return at + kKeys <= total && k0 + kKeys - 1 <= a && (k0 > b - 1 - window || k0 + kKeys <= all_sinks);
-    }
-    __device__ __forceinline__ bool meets(int t, int a, int b, int window, int all_sinks) const {
-        const int at = t * kKeys, k0 = near0 + at - s32;
-        return a < b && (at < s32 || (k0 < b && (k0 + kKeys > a - window + 1 || k0 < all_sinks)));
-    }
     // tile t's first row that is behind the sequence
     __device__ __forceinline__ int behind(int t, int len) const { return s32 + len - near0 - t * kKeys; }
 };
+
+// Of the tiles, those of which one of the queries a .. b - 1 sees a key, and those of which every one sees all keys.
+struct TileRanges {
+    int s_any, n_any0, n_any1, s_all, n_all0, n_all1;      // t < s or n0 <= t < n1
+    TileRanges() = default;
+    __device__ __forceinline__ TileRanges(const KeyTiles &kt, int a, int b, int window, int all_sinks) {
+        // tile t of the window starts at key k0 + 128 t
+        const int k0 = kt.near0 - kt.s32, some = (kt.s32 + kKeys - 1) / kKeys;
+        s_any = a < b ? some : 0;
+        n_any0 = a < b ? max(some, k0 < all_sinks && kt.near0 < all_sinks ? 0 : (max(0, a - window + 1 - kKeys - k0) + kKeys - 1) / kKeys) : kt.n;
+        n_any1 = a < b ? min(kt.n, (max(0, b - k0) + kKeys - 1) / kKeys) : 0;
+        s_all = kt.sinks / kKeys;
+        n_all0 = max(some, (max(0, b - window - k0) + kKeys - 1) / kKeys);
+        n_all1 = min(kt.total / kKeys, a + 1 - k0 >= 0 ? (a + 1 - k0) / kKeys : 0);
+    }
+    __device__ __forceinline__ bool meets(int t) const { return t < s_any || (t >= n_any0 && t < n_any1); }
+    __device__ __forceinline__ bool whole(int t) const { return t < s_all || (t >= n_all0 && t < n_all1); }
+};
+
+// This block's item of a round.  Items of falling length (every query sees all before it) are dealt every other round
+// backwards, so that blocks get equal shares of long ones and short ones: forward of B2 T8192 H16 d128 469 -> 427 us; equal
+// ones are dealt straight on (dq of B8 T2048 H16/4 w1024 160 us, every other round backwards 180).
+__device__ __forceinline__ int64_t dealt(int64_t round, bool falling) {
+    return round * gridDim.x + (falling && round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
 
 // Whether x holds in any thread of the two warps that share the named barrier `id`.
 __device__ __forceinline__ bool any_of(uint32_t id, bool x) {

@@ -41,6 +41,7 @@ struct BwdArgs {
     int *status;
     int gs, runs, tokens;      // log2 of the query heads side by side, runs of them, tokens of 128 rows
     int64_t items;             // of dq
+    bool falling;              // later items are shorter
     float2 *stats;             // [key head and run][row][head of the run] (lse log2 e, delta)
     // sinks: 0 tiles where they are not cut
     int sink_tiles, sink_rows, chunk;
@@ -50,6 +51,9 @@ struct BwdArgs {
 
 struct Item {
     int lo, len, q0, h0, hr;   // first row of the sequence, its length (-1: no more items), first token, first query head, run
+    KeyTiles kt;
+    TileRanges tr;
+    int last16, r0;            // rows of the last key tile: in the product, of the sequence
 };
 
 // The k-th item of dq; long rows of keys first.  By whole warps; false for none.
@@ -160,11 +164,12 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll 1
         for (int it = 0;; ++it) {
             wait(b_q, it);
-            const Item im = items[it & 1];
+            const Item &im = items[it & 1];
             if (im.len < 0 || *polls == 0) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_qfree);
-            const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+            const KeyTiles &kt = im.kt;
+            const TileRanges &tr = im.tr;
             const int i = im.q0 + (row >> a.gs);
             wait(b_stat + (it & 1), it >> 1);
             const float2 stat = i < im.len ? a.stats[(((int64_t)im.hr * p.seqs.total + im.lo + i) << a.gs) + (row & ((1 << a.gs) - 1))] : make_float2(0.f, 0.f);
@@ -173,50 +178,42 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const float2 f2 = make_float2(f, f), l2 = make_float2(-stat.x, -stat.x), d2 = make_float2(-stat.y, -stat.y);
 #pragma unroll 1
             for (int t = 0; t < kt.n; ++t, ++n_tile) {
-                const int kc = kt.count(t), kc16 = (kc + 15) & ~15, r0 = kt.behind(t, im.len);
-                const bool whole = kt.whole(t, im.q0, kt.end, p.window, p.sinks);
-                const bool mine = col0 < kc;
+                const bool whole = tr.whole(t);
                 const uint32_t tD = tl + TM_DP + 128 * (n_tile & 1) + col0;
                 float s[32];
                 wait(b_s, n_tile);
-                if (mine) {
-                    tmem_ld32(tl + col0, s);
-                    tmem_wait_ld();
-                }
+                tmem_ld32(tl + col0, s);      // (columns behind the last key hold anything and are masked)
+                tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_sread);
-                if (mine) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, l2);
-                        s[x] = ex2(y.x);
-                        s[x + 1] = ex2(y.y);
-                    }
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 y = fma2(make_float2(s[x], s[x + 1]), f2, l2);
+                    s[x] = ex2(y.x);
+                    s[x + 1] = ex2(y.y);
                 }
-                if (kc16 > r0) zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (ring + k_at(t)) % NB * L::TILE, r0, kc16, tid);
+                if (t == kt.n - 1 && im.last16 > im.r0) zero_rows<L::PANELS>(smem_u32(sm) + L::KV + (ring + k_at(t)) % NB * L::TILE, im.r0, im.last16, tid);
                 wait(b_dp + (n_tile & 1), n_tile >> 1);
-                if (mine) {
-                    float dp[32];
-                    tmem_ld32(tD, dp);
-                    tmem_wait_ld();
-                    uint32_t w[16];
+                float dp[32];
+                tmem_ld32(tD, dp);
+                tmem_wait_ld();
+                uint32_t w[16];
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        const float2 y = mul2(make_float2(s[x], s[x + 1]), add2(make_float2(dp[x], dp[x + 1]), d2));
-                        s[x] = y.x;
-                        s[x + 1] = y.y;
-                    }
-                    if (!whole) {      // (0 times the product of rows of others may be anything)
-                        const uint32_t bits = kt.bits(i, kKeys * t + col0, p.window, p.sinks);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) s[x] = bits >> x & 1 ? s[x] : 0.f;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16(s[x], s[x + 1]);
-                    tmem_st16u(tD, w);
-                    tmem_wait_st();
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 y = mul2(make_float2(s[x], s[x + 1]), add2(make_float2(dp[x], dp[x + 1]), d2));
+                    s[x] = y.x;
+                    s[x + 1] = y.y;
                 }
+                if (!whole) {      // (0 times the product of rows of others may be anything)
+                    const uint32_t bits = kt.bits(i, kKeys * t + col0, p.window, p.sinks);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) s[x] = bits >> x & 1 ? s[x] : 0.f;
+                }
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16(s[x], s[x + 1]);
+                tmem_st16u(tD, w);
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_ds + (n_tile & 1));
@@ -250,11 +247,15 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, lo + kt.key(t * kKeys + x * kBox));
         };
 #pragma unroll 1
-        for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < a.items && *polls != 0; ++round) {
             Item im;
-            if (!item_of(a, k, im)) continue;
+            if (dealt(round, a.falling) >= a.items || !item_of(a, dealt(round, a.falling), im)) continue;
             const int hk = im.hr / a.runs;
             const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+            im.kt = kt;
+            im.tr = TileRanges(kt, im.q0, kt.end, p.window, p.sinks);
+            im.last16 = (kt.count(kt.n - 1) + 15) & ~15;
+            im.r0 = kt.behind(kt.n - 1, im.len);
             if (elect_one()) {
                 if (it > 0) wait(b_qfree, it - 1);
                 items[it & 1] = im;
@@ -301,9 +302,9 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll 1
             for (int it = 0;; ++it) {
                 wait(b_q, it);
-                const Item im = items[it & 1];
+                const Item &im = items[it & 1];
                 if (im.len < 0 || *polls == 0) break;
-                const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
+                const KeyTiles &kt = im.kt;
                 auto n16 = [&](int t) { return (kt.count(t) + 15) & ~15; };
                 auto rows_by_rows = [&](uint32_t d, int b, int t) {
                     const uint64_t db = desc_add(dK, b * L::TILE);
@@ -372,9 +373,9 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const int l = lane % LPR;
         int it = 0;
 #pragma unroll 1
-        for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+        for (int64_t round = 0; round * gridDim.x < a.items && *polls != 0; ++round) {
             Item im;
-            if (!item_of(a, k, im)) continue;
+            if (dealt(round, a.falling) >= a.items || !item_of(a, dealt(round, a.falling), im)) continue;
             if (it > 1) wait(b_sfree + (it & 1), (it >> 1) - 1);
 #pragma unroll 1
             for (int r0 = ROWS * (warp - kStatWarp); r0 < ROWS * (warp - kStatWarp + 1); r0 += U * RPW) {
@@ -792,6 +793,7 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
         cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv) != cudaSuccess)
         return kErrCuda;
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
+    a.falling = !p.seqs.cu && p.window > p.seqs.T / 2;
     attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kDqThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     const int64_t blocks = (attn_tile_slots(p.seqs, kKeys) + a.chunk_slots * a.sink_tiles) * p.Hk;

@@ -4,7 +4,8 @@
 // A block takes two tiles of 128 query rows (stages 0 and 1) that share their key tiles; it runs
 // through items of that kind (a run of tokens, a key head, up to four of its query heads side by side).
 //     S = Q K^T        [128 x 128]   both from shared memory, S in tensor memory
-//     O += P V         [128 x d]     P (bf16) from tensor memory, over S's place; V as loaded (MN-major)
+//     O += P V         [128 x d]     P (bf16) from tensor memory, over S's place (d = 64: apart, so that the next S
+//                                    does not wait for the product); V as loaded (MN-major)
 // The running softmax: with f = scale log2 e and m the row's reference, p = 2^(f s - f m), and
 // O and l hold the sums for that m.  m follows the row's maximum only when that is more than 2^kAbove above it
 // (P is a floating-point operand: its precision does not depend on m), so O in tensor memory is rescaled
@@ -39,18 +40,25 @@ struct FwdArgs {
     int gs, runs;          // log2 of the query heads side by side; runs of them in a key head's group
     int tokens;            // of an item: 256 >> gs
     int64_t items;
+    bool falling;          // later items are shorter
 };
 
-// What the load warp tells the others of an item.
+// What the load warp, which is ahead of them, tells the others of an item.
 struct Item {
     int lo, len, q0, h0;   // first row of the sequence, its length (-1: no more items), first token, first query head
+    KeyTiles kt;
+    TileRanges tr[2];      // of the stages
+    int last16, r0;        // rows of the last key tile: in the product, of the sequence
 };
 
 template <int D>
 struct Layout {
     static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10;   // key and value buffers
     static constexpr uint32_t Q = 0, KV = 2 * TILE, ROWS = KV + NB * TILE, BARS = ROWS + 2 * 128 * 4;
-    static constexpr uint32_t TOTAL = BARS + (2 * NB + 12) * 8 + 2 * sizeof(Item);
+    static constexpr uint32_t TOTAL = BARS + (2 * NB + 16) * 8 + 3 * sizeof(Item);
+    // tensor memory: S of both stages, O of both, P of both where there is room for it apart from S
+    static constexpr bool APART = D == 64;
+    static constexpr uint32_t TM_O = 256, TM_P = 384;
     static_assert(TOTAL + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -66,8 +74,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     uint64_t *b_full = bars, *b_free = bars + NB;        // [NB] a key or value tile is there, is done with
     uint64_t *b_q = bars + 2 * NB, *b_qfree = b_q + 2;   // [2] the stage's queries (and the item)
     uint64_t *b_s = b_q + 4, *b_p = b_q + 6, *b_o = b_q + 8;   // [2] S is there; P is; O is complete
-    uint64_t *b_end = b_q + 10;
-    Item *items = reinterpret_cast<Item *>(b_q + 12);    // [2]
+    uint64_t *b_sread = b_q + 10, *b_pv = b_q + 12;      // [2] (P apart) S is read; O += P V is done
+    uint64_t *b_end = b_q + 14;
+    Item *items = reinterpret_cast<Item *>(b_q + 16);    // [3]: a stage may be one behind the other
     __shared__ uint32_t tmem_s;
     __shared__ int polls_s;
     const AttnProblem &p = a.p;
@@ -83,6 +92,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(b_s + i, 1);
             mbar_init(b_p + i, kStageWarps);
             mbar_init(b_o + i, 1);
+            mbar_init(b_sread + i, kStageWarps);
+            mbar_init(b_pv + i, 1);
         }
         mbar_init(b_end, 2);
         polls_s = tc::kPolls;
@@ -110,7 +121,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         // ---------------------------------------------------------------- softmax
         // this thread: a row, half of the keys; the warp with the other half is the pair's other one
         const int st = warp / kStageWarps, quarter = warp & 3, half = warp >> 2 & 1, row = 32 * quarter + lane, col0 = 64 * half;
-        const uint32_t tS = tm + ((uint32_t)(32 * quarter) << 16) + 128 * st, tO = tS + 256 + half * (D / 2), pair = 1 + 4 * st + quarter;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16), tS = tl + 128 * st, tO = tl + L::TM_O + D * st + half * (D / 2);
+        const uint32_t tP = L::APART ? tl + L::TM_P + 64 * st + 32 * half : tS + col0, pair = 1 + 4 * st + quarter;
         float *rows = reinterpret_cast<float *>(sm + L::ROWS) + 128 * st + row;
         // the other thread's x, for both
         auto exchange = [&](float x, auto join) {
@@ -126,28 +138,33 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 #pragma unroll 1
         for (int it = 0;; ++it) {
             wait(b_q + st, it);
-            const Item im = items[it & 1];
+            const Item &im = items[it % 3];
             if (im.len < 0 || *polls == 0) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_qfree + st);
-            const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-            const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt), i = ta + (row >> a.gs);
+            const KeyTiles &kt = im.kt;
+            const TileRanges &tr = im.tr[st];
+            const int ta = im.q0 + st * tt, i = ta + (row >> a.gs);
             float m = -INFINITY;
             float2 l = make_float2(0.f, 0.f);      // of this thread's keys
             bool first = true;
 #pragma unroll 1
             for (int t = 0; t < kt.n; ++t) {
-                if (!kt.meets(t, ta, tb, p.window, p.sinks)) continue;
-                const int kc = kt.count(t);
-                const bool whole = kt.whole(t, ta, tb, p.window, p.sinks);
+                if (!tr.meets(t)) continue;
                 wait(b_s + st, n_tile);
                 ++n_tile;
                 float s[64];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (col0 + 32 * c < kc) tmem_ld32(tS + col0 + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+                // (columns behind the last key hold anything and are masked)
+                tmem_ld32(tS + col0, *reinterpret_cast<float(*)[32]>(s));
+                tmem_ld32(tS + col0 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
                 tmem_wait_ld();
-                if (!whole) {
+                bool stored = !L::APART || n_tile == 1;      // whether P's place (and O) is free
+                if (L::APART) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_sread + st);
+                }
+                if (!tr.whole(t)) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const uint32_t bits = kt.bits(i, kKeys * t + col0 + 32 * c, p.window, p.sinks);
@@ -168,7 +185,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     const float turn = up ? ex2((m - top) * f) : 1.f;
                     l = mul2(l, make_float2(turn, turn));
                     m = up ? top : m;
-                    if (!first) {       // S is there, so the products before it are done
+                    if (!first) {       // (P in S's place: S is there, so the products before it are done)
+                        if (!stored) wait(b_pv + st, n_tile - 2);
+                        stored = true;
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[16];
@@ -182,11 +201,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     }
                 }
                 first = false;
+                if (!stored) wait(b_pv + st, n_tile - 2);
                 const float base = m == -INFINITY ? 0.f : -m * f;
                 const float2 b2 = make_float2(base, base);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (col0 + 32 * c >= kc) break;
                     uint32_t w[16];
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
@@ -196,15 +215,15 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         l = add2(l, y);
                         w[x] = pack_bf16(y.x, y.y);
                     }
-                    tmem_st16u(tS + col0 + 16 * c, w);
+                    tmem_st16u(tP + 16 * c, w);
                 }
                 // values of rows behind the sequence's end that the product takes in are zeros
-                const int kc16 = (kc + 15) & ~15, r0 = kt.behind(t, im.len);
-                if (kc16 > r0) {
+                if (t == kt.n - 1 && im.last16 > im.r0) {
+                    const int r0 = im.r0, last16 = im.last16;
                     const int v = ring + 2 * t + 1;
                     wait_ring(b_full, v);
                     const uint32_t V = smem_u32(sm) + L::KV + (v % NB) * L::TILE;
-                    const int n = (kc16 - r0) * 8;
+                    const int n = (last16 - r0) * 8;
                     for (int x = tid & 255; x < L::PANELS * n; x += 256) {
                         const int r = r0 + x % n / 8;
                         sts128(V + (x / n) * 16384 + r * 128 + (x % 8) * 16, 0, 0, 0, 0);
@@ -217,7 +236,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(b_p + st);
             }
             ring += 2 * kt.n;
-            if (ta < tb) {
+            if (ta < im.len) {
                 const float sum = exchange(l.x + l.y, [](float x, float y) { return x + y; }), inv = 1.f / sum;
                 if (half == 0 && i < im.len) p.lse[(int64_t)(im.lo + i) * p.Hq + im.h0 + (row & ((1 << a.gs) - 1))] = (m * f + log2f(sum)) * kLn2;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(im.lo + ta) * p.Hq + im.h0) * D + half * (D / 2);
@@ -253,7 +272,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         tc::tma_load_3d(dst + e * 16384 + x * kBox * 128, map, b_full + b, 64 * e, hk, lo + kt.key(t * kKeys + x * kBox));
             };
 #pragma unroll 1
-            for (int64_t k = blockIdx.x; k < a.items && *polls != 0; k += gridDim.x) {
+            for (int64_t round = 0; round * gridDim.x < a.items && *polls != 0; ++round) {
+                const int64_t k = dealt(round, a.falling);
+                if (k >= a.items) continue;
                 // long rows of keys first: the last tokens of all sequences, then the ones before them
                 const int nh = p.Hk * a.runs;
                 const int hr = (int)(k % nh);
@@ -269,12 +290,20 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     len = (int)p.seqs.T;
                 }
                 const int hk = hr / a.runs, q0 = j * a.tokens;
-                const Item im{(int)lo, len, q0, hk * (p.Hq / p.Hk) + (hr % a.runs << a.gs)};
+                Item im;
+                im.lo = (int)lo;
+                im.len = len;
+                im.q0 = q0;
+                im.h0 = hk * (p.Hq / p.Hk) + (hr % a.runs << a.gs);
                 const KeyTiles kt(q0, a.tokens, len, p.window, p.sinks);
+                im.kt = kt;
+                for (int st = 0; st < 2; ++st) im.tr[st] = TileRanges(kt, q0 + st * tt, min(len, q0 + (st + 1) * tt), p.window, p.sinks);
+                im.last16 = (kt.count(kt.n - 1) + 15) & ~15;
+                im.r0 = kt.behind(kt.n - 1, len);
                 if (elect_one()) {
                     for (int st = 0; st < 2; ++st) {
                         if (it > 0) wait(b_qfree + st, it - 1);
-                        if (st == 0) items[it & 1] = im;
+                        if (st == 0) items[it % 3] = im;
                         mbar_arrive_expect_tx(b_q + st, L::TILE);
                         for (int e = 0; e < L::PANELS; ++e)
                             tc::tma_load_3d(sm + L::Q + st * L::TILE + e * 16384, &tq, b_q + st, 64 * e, im.h0, im.lo + q0 + st * tt);
@@ -297,7 +326,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         wait(b_qfree + st, it - 1);
                         tc::wait_cycles(b_q + st, (it - 1) & 1);
                     }
-                    if (st == 0) items[it & 1].len = -1;
+                    if (st == 0) items[it % 3].len = -1;
                     mbar_arrive(b_q + st);
                 }
             }
@@ -310,18 +339,19 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const uint64_t dK = smem_desc_sw128(smem_u32(sm) + L::KV, 16, 1024);
                 const uint64_t dV = smem_desc_sw128(smem_u32(sm) + L::KV, 16384, 1024);     // MN-major, panels of 64 channels
                 constexpr uint32_t ID_PV = idesc_bf16(128, D, false, true);
-                const uint32_t tS = tm + 128 * st, tO = tS + 256;
-                int ring = 0, n_p = 0;
+                const uint32_t tS = tm + 128 * st, tO = tm + L::TM_O + D * st, tP = L::APART ? tm + L::TM_P + 64 * st : tS;
+                int ring = 0, n_p = 0, n_s = 0;
 #pragma unroll 1
                 for (int it = 0;; ++it) {
                     wait(b_q + st, it);
-                    const Item im = items[it & 1];
+                    const Item &im = items[it % 3];
                     if (im.len < 0 || *polls == 0) break;
-                    const KeyTiles kt(im.q0, a.tokens, im.len, p.window, p.sinks);
-                    const int ta = im.q0 + st * tt, tb = min(im.len, ta + tt);
-                    int pend = -1;         // the tile whose S went last
+                    const KeyTiles &kt = im.kt;
+                    const TileRanges tr = im.tr[st];
+                    const int ta = im.q0 + st * tt;
+                    int pend = -1;         // the tile whose S went last, if it was the one before
                     bool more = false;
-                    auto flush = [&](int t) {     // O += P V of tile t - 1, or nothing of it
+                    auto flush = [&](int t) {     // O += P V of tile t - 1
                         const int v = ring + 2 * t - 1, b = v % NB;
                         wait(b_full + b, v / NB);
                         if (pend >= 0) {
@@ -330,13 +360,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                             wait(b_p + st, n_p++);
                             if (ks == 8) {      // (a rolled loop issues a product in 85 cycles, which the tensor core takes in 64)
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) mma_bf16_ts(tO, tS + 8 * k + (k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                                for (int k = 0; k < 8; ++k) mma_bf16_ts(tO, tP + 8 * k + (!L::APART && k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
                             } else {
 #pragma unroll 1
-                                for (int k = 0; k < ks; ++k) mma_bf16_ts(tO, tS + 8 * k + (k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
+                                for (int k = 0; k < ks; ++k) mma_bf16_ts(tO, tP + 8 * k + (!L::APART && k >= 4 ? 32 : 0), desc_add(dv, k * 2048), ID_PV, more || k > 0);
                             }
                             more = true;
-                            pend = -1;
+                            if (L::APART) mma_commit(b_pv + st);
                         }
                         mma_commit(b_free + b);
                     };
@@ -344,17 +374,21 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     for (int t = 0; t < kt.n; ++t) {
                         const int k = ring + 2 * t, b = k % NB, n16 = (kt.count(t) + 15) & ~15;
                         wait(b_full + b, k / NB);
-                        if (t > 0) flush(t);
-                        if (kt.meets(t, ta, tb, p.window, p.sinks)) {
+                        if (!L::APART && t > 0) flush(t);
+                        const bool met = tr.meets(t);
+                        if (met) {
+                            if (L::APART && n_s > 0) wait(b_sread + st, n_s - 1);
+                            ++n_s;
                             const uint64_t dk = desc_add(dK, b * L::TILE);
                             const uint32_t id = idesc_bf16(128, 16, false, false) + ((uint32_t)(n16 - 16) << 14);
 #pragma unroll
                             for (int e = 0; e < D / 16; ++e)
                                 mma_bf16(tS, desc_add(dQ, (e >> 2) * 16384 + (e & 3) * 32), desc_add(dk, (e >> 2) * 16384 + (e & 3) * 32), id, e > 0);
                             mma_commit(b_s + st);
-                            pend = t;
                         }
                         mma_commit(b_free + b);
+                        if (L::APART && t > 0) flush(t);
+                        pend = met ? t : -1;
                     }
                     mma_commit(b_qfree + st);
                     flush(kt.n);
@@ -393,6 +427,7 @@ int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream) {
     a.runs = p.Hq / p.Hk >> a.gs;
     a.tokens = 256 >> a.gs;
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
+    a.falling = !p.seqs.cu && p.window > p.seqs.T / 2;
     CUtensorMap m[3];
     if (!make_map(&m[0], p.q, p.seqs.total, p.Hq, p.d, p.qs, 1 << a.gs, 128 >> a.gs) ||
         !make_map(&m[1], p.k, p.seqs.total, p.Hk, p.d, p.ks, 1, kBox) || !make_map(&m[2], p.v, p.seqs.total, p.Hk, p.d, p.vs, 1, kBox))
