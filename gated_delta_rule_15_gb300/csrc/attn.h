@@ -33,7 +33,7 @@ struct AttnProblem {
     const void *d_out;                 // [rows, Hq, d]
     void *dq, *dk, *dv;                // rows dqs, dks, dvs elements apart
     int64_t dqs, dks, dvs;
-    float *delta;                      // (workspace) [Hq][rows]
+    float *delta;                      // (workspace, fp32 rows) [Hq][rows]
 };
 
 #ifdef __CUDACC__
@@ -75,7 +75,8 @@ __device__ __forceinline__ bool find_tile(const LinrecSeqs &s, int tile, int slo
 
 // CUDA cores: fp32 rows.
 int launch_attn_simt_fwd(const AttnProblem &p, cudaStream_t stream);
-int launch_attn_simt_bwd(const AttnProblem &p, cudaStream_t stream);
+size_t attn_simt_bwd_workspace_bytes(const AttnProblem &p);   // (by seqs.cu being NULL or not, not what it holds)
+int launch_attn_simt_bwd(const AttnProblem &p, void *workspace, cudaStream_t stream);
 
 // Zeroes the rows of no sequence of a packed problem: `n` buffers of `bytes[i]` bytes a row,
 // `stride[i]` bytes apart (both multiples of 4; a NULL buffer is passed over).

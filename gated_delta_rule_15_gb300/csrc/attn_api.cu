@@ -56,8 +56,8 @@ AttnProblem problem_of(const dr_attn_desc &d, const int64_t *cu) {
 
 size_t bwd_bytes(const dr_attn_desc &d) {
     static const int64_t packed = 0;     // packed or not, not where the offsets lie
-    if (d.dtype == DR_BF16) return attn_tc_bwd_workspace_bytes(problem_of(d, &packed));
-    return sizeof(float) * (size_t)(d.B * d.T * d.Hq);
+    const AttnProblem p = problem_of(d, &packed);
+    return p.bf16 ? attn_tc_bwd_workspace_bytes(p) : attn_simt_bwd_workspace_bytes(p);
 }
 
 int check_step(const dr_attn_step_desc *d) {
@@ -149,7 +149,7 @@ extern "C" int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const
     if (!workspace || workspace_bytes < need) return kErrWorkspace;
     AttnProblem p = problem_of(d, cu_seqlens);
     p.q = q; p.k = k; p.v = v; p.out = const_cast<void *>(out); p.lse = const_cast<float *>(lse); p.d_out = d_out;
-    p.dq = dq; p.dk = dk; p.dv = dv; p.delta = (float *)workspace;
+    p.dq = dq; p.dk = dk; p.dv = dv;
     const int64_t e = p.bf16 ? 2 : 4, n = p.seqs.total, wq = d.Hq * d.d, wk = d.Hk * d.d;
     // no written row meets another one, an input or the workspace
     const Rows written[3] = {{dq, wq, p.dqs}, {dk, wk, p.dks}, {dv, wk, p.dvs}};
@@ -173,7 +173,7 @@ extern "C" int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const
         const int rz = launch_attn_zero_rest(p.seqs, r, (cudaStream_t)stream);
         if (rz != kOk) return rz;
     }
-    if (!p.bf16) return launch_attn_simt_bwd(p, (cudaStream_t)stream);
+    if (!p.bf16) return launch_attn_simt_bwd(p, workspace, (cudaStream_t)stream);
     int *status = device_status_ptr();
     if (!status) return kErrCuda;
     return launch_attn_tc_bwd(p, workspace, status, (cudaStream_t)stream);

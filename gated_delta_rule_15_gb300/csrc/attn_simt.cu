@@ -1,72 +1,89 @@
 // attn_simt.cu -- window attention on the CUDA cores (fp32 rows): forward, gradients.  The
-// mathematics: attn.h.
+// mathematics: attn.h; the blocks of dk and dv: attn_sinks.cuh.
 //
-// Tiles of 64 queries by 64 keys, 256 threads as 16 x 16: a thread holds 4 x 4 scores (queries
-// 4 ty + r, keys tx + 16 c) and 4 rows x d / 16 columns of what is summed.  Products run over rows in
-// shared memory as float4 of both operands (64 FMAs per 8 loads of 16 bytes), whose row stride of
-// d + 4 floats keeps the 16 keys of a load on different banks.
-// A query's keys come in one pass, first the sinks in front of its tile's window, then the window,
-// with the running maximum and sum of the softmax in registers.
+// Tiles of 16 R rows (queries; of dk, dv keys) by 64 others, 256 threads as 16 x 16: a thread holds R x 4 scores (rows
+// R ty + r, others tx + 16 c) and R rows x d / 16 columns of what is summed.  Products run over rows in
+// shared memory as float4 of both operands and two FMAs an instruction (R = 4: 32 of them to 8 loads); the
+// row stride of d + 4 floats keeps the 16 rows of a load on different banks.  The scores' sums go over even and odd
+// channels apart, and what is summed over tiles is first summed within one, so that sums of a thousand
+// terms are off by less than one of them would be.
+// The 64 others come by asynchronous copies a tile ahead.  A query's keys: first the sinks in front of its tile's window, then the
+// window, with the running maximum and sum of the softmax in registers.
+// R = 4, or 1 where tiles of 64 rows would not give every SM one (T256 H2 d64 w64: 21.3 us with R = 4).
 #include "../../include/dr.h"
 #include "attn.h"
+#include "attn_sinks.cuh"
 #include "common.cuh"
+#include "umma.cuh"
 
 namespace dr {
 namespace {
+
+using umma::add2;
+using umma::fma2;
+using umma::mul2;
 
 constexpr int kTile = 64, kThreads = 256, kPs = kTile + 4;
 
 template <int D> constexpr int row_floats() { return D + 4; }
 
-// Rows row0 .. row0 + n - 1 of one head as fp32, zeros behind them.
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t stride, int n) {
+// Rows 0 .. ROWS - 1 of one head as at(r) says, zeros where that is NULL, on their way.  `any`: some address of the rows.
+template <int D, int ROWS, class At>
+__device__ __forceinline__ void fetch(float *dst, const void *any, At at) {
     constexpr int PER = D / 4;
 #pragma unroll
-    for (int i = threadIdx.x; i < kTile * PER; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * PER; i += kThreads) {
         const int r = i / PER, c = i % PER;
-        const float4 x = r < n ? load4(src + (int64_t)r * stride + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        store4(dst + r * row_floats<D>() + 4 * c, x);
+        const float *src = at(r);
+        umma::cp_async16(dst + r * row_floats<D>() + 4 * c, src ? src + 4 * c : any, src ? 16u : 0u);
     }
 }
 
-// acc[r][c] = sum over d of A[4 ty + r] B[tx + 16 c]
-template <int D>
-__device__ __forceinline__ void rows_by_rows(float (&acc)[4][4], const float *A, const float *B, int ty, int tx) {
+// acc[r][c] = sum over d of A[R ty + r] B[tx + 16 c]
+template <int D, int R>
+__device__ __forceinline__ void rows_by_rows(float (&acc)[R][4], const float *A, const float *B, int ty, int tx) {
     constexpr int S = row_floats<D>();
+    float2 x[R][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+        for (int c = 0; c < 4; ++c) x[r][c] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-        float4 a[4], b[4];
+        float4 a[R], b[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = load4(A + (4 * ty + r) * S + k);
+        for (int r = 0; r < R; ++r) a[r] = load4(A + (R * ty + r) * S + k);
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[c] = load4(B + (tx + 16 * c) * S + k);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                acc[r][c] = fmaf(a[r].x, b[c].x, acc[r][c]);
-                acc[r][c] = fmaf(a[r].y, b[c].y, acc[r][c]);
-                acc[r][c] = fmaf(a[r].z, b[c].z, acc[r][c]);
-                acc[r][c] = fmaf(a[r].w, b[c].w, acc[r][c]);
+                x[r][c] = fma2(make_float2(a[r].x, a[r].y), make_float2(b[c].x, b[c].y), x[r][c]);
+                x[r][c] = fma2(make_float2(a[r].z, a[r].w), make_float2(b[c].z, b[c].w), x[r][c]);
             }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = x[r][c].x + x[r][c].y;
 }
 
-// acc[r][4 u + e] += sum over 64 k of P[4 ty + r][k] X[k][64 u + 4 tx + e]
-template <int D>
-__device__ __forceinline__ void rows_by_cols(float (&acc)[4][D / 16], const float *P, const float *X, int ty, int tx) {
+// acc[r][2 u + h] += sum over `n` k (a multiple of 4) of P[R ty + r][k] X[k][64 u + 4 tx + 2 h, + 1]
+template <int D, int R>
+__device__ __forceinline__ void rows_by_cols(float2 (&acc)[R][D / 32], const float *P, const float *X, int n, int ty, int tx) {
     constexpr int S = row_floats<D>(), U = D / 64;
-#pragma unroll 2
-    for (int k = 0; k < kTile; k += 4) {
-        float p[4][4];
+    float2 sum[R][D / 32];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float4 x = load4(P + (4 * ty + r) * kPs + k);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) sum[r][u] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < n; k += 4) {
+        float p[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float4 x = load4(P + (R * ty + r) * kPs + k);
             p[r][0] = x.x; p[r][1] = x.y; p[r][2] = x.z; p[r][3] = x.w;
         }
 #pragma unroll
@@ -75,21 +92,27 @@ __device__ __forceinline__ void rows_by_cols(float (&acc)[4][D / 16], const floa
             for (int u = 0; u < U; ++u) {
                 const float4 x = load4(X + (k + e) * S + 64 * u + 4 * tx);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    acc[r][4 * u] = fmaf(p[r][e], x.x, acc[r][4 * u]);
-                    acc[r][4 * u + 1] = fmaf(p[r][e], x.y, acc[r][4 * u + 1]);
-                    acc[r][4 * u + 2] = fmaf(p[r][e], x.z, acc[r][4 * u + 2]);
-                    acc[r][4 * u + 3] = fmaf(p[r][e], x.w, acc[r][4 * u + 3]);
+                for (int r = 0; r < R; ++r) {
+                    sum[r][2 * u] = fma2(make_float2(p[r][e], p[r][e]), make_float2(x.x, x.y), sum[r][2 * u]);
+                    sum[r][2 * u + 1] = fma2(make_float2(p[r][e], p[r][e]), make_float2(x.z, x.w), sum[r][2 * u + 1]);
                 }
             }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) acc[r][u] = add2(acc[r][u], sum[r][u]);
 }
 
-__device__ __forceinline__ void put_scores(float *P, const float (&s)[4][4], int ty, int tx) {
+// A thread's scores where the 16 threads of its rows, which are in its warp, read them.
+template <int R>
+__device__ __forceinline__ void put_scores(float *P, const float (&s)[R][4], int ty, int tx) {
+    __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) P[(4 * ty + r) * kPs + tx + 16 * c] = s[r][c];
+        for (int c = 0; c < 4; ++c) P[(R * ty + r) * kPs + tx + 16 * c] = s[r][c];
+    __syncwarp();
 }
 
 __device__ __forceinline__ float max16(float x) {
@@ -107,59 +130,88 @@ __device__ __forceinline__ bool sees(const AttnProblem &p, int i, int j) {
     return j <= i && (i - j < p.window || j < p.sinks);
 }
 
-// The key tiles of a query tile: sinks in front of the window of its first query, then the keys
-// from there to its last query.
-struct KeyTiles {
-    int sinks, n_sink, near0, end, n;
-    __device__ KeyTiles(const AttnProblem &p, int q0, int len) {
+// The keys of the queries q0 .. q0 + rows - 1, one behind another: sinks in front of the first one's window, then the keys
+// from there to the last one.
+struct Keys {
+    int sinks, near0, total;
+    __device__ __forceinline__ Keys(const AttnProblem &p, int q0, int rows, int len) {
         near0 = max(0, q0 - p.window + 1);
         sinks = min(p.sinks, near0);
-        end = min(len, q0 + kTile);
-        n_sink = (sinks + kTile - 1) / kTile;
-        n = n_sink + (end - near0 + kTile - 1) / kTile;
+        total = sinks + min(len, q0 + rows) - near0;
     }
-    __device__ void get(int t, int &k0, int &count) const {
-        k0 = t < n_sink ? t * kTile : near0 + (t - n_sink) * kTile;
-        count = min(kTile, (t < n_sink ? sinks : end) - k0);
-    }
+    __device__ __forceinline__ int at(int v) const { return v < sinks ? v : near0 + v - sinks; }
 };
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProblem p) {
-    constexpr int S = row_floats<D>();
-    extern __shared__ float sm[];
-    float *Q = sm, *KV = Q + kTile * S, *P = KV + kTile * S;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
-    int64_t n, lo;
-    int j, len;
-    if (!find_tile(p.seqs, kTile, blockIdx.x / p.Hq, n, j, lo, len)) return;
-    const int q0 = j * kTile;
-    load_tile<D>(Q, (const T *)p.q + (lo + q0) * p.qs + h * D, p.qs, len - q0);
-    float m[4], l[4], o[4][D / 16];
+template <int D, int R>
+__device__ __forceinline__ void put_rows(float *dst, int64_t stride, int n, const float2 (&x)[R][D / 32], float f, int ty, int tx) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
+        if (R * ty + r >= n) continue;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u)
+            store4(dst + (int64_t)(R * ty + r) * stride + 64 * u + 4 * tx,
+                   make_float4(f * x[r][2 * u].x, f * x[r][2 * u].y, f * x[r][2 * u + 1].x, f * x[r][2 * u + 1].y));
+    }
+}
+
+// A query tile's block: (sequence tile, head).
+template <int ROWS>
+__device__ __forceinline__ bool query_tile(const AttnProblem &p, int &h, int &hk, int64_t &lo, int &len, int &q0) {
+    int64_t n;
+    int j;
+    h = blockIdx.x % p.Hq;
+    hk = h / (p.Hq / p.Hk);
+    if (!find_tile(p.seqs, ROWS, blockIdx.x / p.Hq, n, j, lo, len)) return false;
+    q0 = j * ROWS;
+    return true;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProblem p) {
+    constexpr int S = row_floats<D>(), ROWS = 16 * R;
+    extern __shared__ float sm[];
+    float *Q = sm, *KV = Q + ROWS * S, *P = KV + 4 * kTile * S;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    int64_t lo;
+    int h, hk, len, q0;
+    if (!query_tile<ROWS>(p, h, hk, lo, len, q0)) return;
+    const Keys keys(p, q0, ROWS, len);
+    const float *q = (const float *)p.q + (lo + q0) * p.qs + h * D, *k = (const float *)p.k + lo * p.ks + hk * D,
+                *v = (const float *)p.v + lo * p.vs + hk * D;
+    auto fetch_keys = [&](int t) {
+        float *dst = KV + (t & 1) * 2 * kTile * S;
+        fetch<D, kTile>(dst, k, [&](int r) { return kTile * t + r < keys.total ? k + (int64_t)keys.at(kTile * t + r) * p.ks : nullptr; });
+        fetch<D, kTile>(dst + kTile * S, v, [&](int r) { return kTile * t + r < keys.total ? v + (int64_t)keys.at(kTile * t + r) * p.vs : nullptr; });
+    };
+    fetch<D, ROWS>(Q, p.q, [&](int r) { return q0 + r < len ? q + (int64_t)r * p.qs : nullptr; });
+    fetch_keys(0);
+    umma::cp_async_commit();
+    float m[R], l[R];
+    float2 o[R][D / 32];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) o[r][c] = make_float2(0.f, 0.f);
     }
-    const KeyTiles tiles(p, q0, len);
-    for (int t = 0; t < tiles.n; ++t) {
-        int k0, count;
-        tiles.get(t, k0, count);
+    const int tiles = (keys.total + kTile - 1) / kTile;
+    for (int t = 0; t < tiles; ++t) {
+        umma::cp_async_wait_all();
         __syncthreads();
-        load_tile<D>(KV, (const T *)p.k + (lo + k0) * p.ks + hk * D, p.ks, count);
-        __syncthreads();
-        float s[4][4];
-        rows_by_rows<D>(s, Q, KV, ty, tx);
+        if (t + 1 < tiles) fetch_keys(t + 1);
+        umma::cp_async_commit();
+        const float *K = KV + (t & 1) * 2 * kTile * S;
+        float s[R][4];
+        rows_by_rows<D, R>(s, Q, K, ty, tx);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = q0 + 4 * ty + r;
+        for (int r = 0; r < R; ++r) {
+            const int i = q0 + R * ty + r;
             float top = m[r];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int kj = tx + 16 * c;
-                s[r][c] = kj < count && sees(p, i, k0 + kj) ? p.scale * s[r][c] : -INFINITY;
+                const int at = kTile * t + tx + 16 * c;
+                s[r][c] = at < keys.total && sees(p, i, keys.at(at)) ? p.scale * s[r][c] : -INFINITY;
                 top = fmaxf(top, s[r][c]);
             }
             top = max16(top);
@@ -173,63 +225,59 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
             }
             l[r] = fmaf(l[r], turn, sum);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) o[r][c] *= turn;
+            for (int c = 0; c < D / 32; ++c) o[r][c] = mul2(o[r][c], make_float2(turn, turn));
         }
-        put_scores(P, s, ty, tx);
-        __syncthreads();
-        load_tile<D>(KV, (const T *)p.v + (lo + k0) * p.vs + hk * D, p.vs, count);
-        __syncthreads();
-        rows_by_cols<D>(o, P, KV, ty, tx);
+        put_scores<R>(P, s, ty, tx);
+        rows_by_cols<D, R>(o, P, K + kTile * S, min(kTile, (keys.total - kTile * t + 3) & ~3), ty, tx);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
         const float sum = sum16(l[r]), inv = 1.f / sum;
-        const int i = q0 + 4 * ty + r;
-        if (i >= len) continue;
-        T *dst = (T *)p.out + ((lo + i) * p.Hq + h) * D;
+        const int i = q0 + R * ty + r;
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            store4(dst + 64 * u + 4 * tx, make_float4(o[r][4 * u] * inv, o[r][4 * u + 1] * inv, o[r][4 * u + 2] * inv, o[r][4 * u + 3] * inv));
-        if (tx == 0) p.lse[(lo + i) * p.Hq + h] = m[r] + logf(sum);
+        for (int c = 0; c < D / 32; ++c) o[r][c] = mul2(o[r][c], make_float2(inv, inv));
+        if (i < len && tx == 0) p.lse[(lo + i) * p.Hq + h] = m[r] + logf(sum);
     }
-}
-
-template <int D, typename T>
-__device__ __forceinline__ void put_rows(T *dst, int64_t stride, int n, const float (&x)[4][D / 16], float f, int ty, int tx) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        if (4 * ty + r >= n) continue;
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            store4(dst + (int64_t)(4 * ty + r) * stride + 64 * u + 4 * tx,
-                   make_float4(f * x[r][4 * u], f * x[r][4 * u + 1], f * x[r][4 * u + 2], f * x[r][4 * u + 3]));
-    }
+    put_rows<D, R>((float *)p.out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, len - q0, o, 1.f, ty, tx);
 }
 
 // dq of a query tile, and delta of its rows.
-template <int D, typename T>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProblem p) {
-    constexpr int S = row_floats<D>();
+    constexpr int S = row_floats<D>(), ROWS = 16 * R;
     extern __shared__ float sm[];
-    float *Q = sm, *O = Q + kTile * S, *K = O + kTile * S, *V = K + kTile * S, *P = V + kTile * S;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, h = blockIdx.x % p.Hq, hk = h / (p.Hq / p.Hk);
-    int64_t n, lo;
-    int j, len;
-    if (!find_tile(p.seqs, kTile, blockIdx.x / p.Hq, n, j, lo, len)) return;
-    const int q0 = j * kTile, rows = len - q0;
-    load_tile<D>(K, (const T *)p.out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, rows);   // (K's place is free)
-    load_tile<D>(O, (const T *)p.d_out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, rows);
-    load_tile<D>(Q, (const T *)p.q + (lo + q0) * p.qs + h * D, p.qs, rows);
-    __syncthreads();
-    float delta[4], lse[4], dq[4][D / 16];
+    float *Q = sm, *O = Q + ROWS * S, *KV = O + ROWS * S, *P = KV + 4 * kTile * S;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    int64_t lo;
+    int h, hk, len, q0;
+    if (!query_tile<ROWS>(p, h, hk, lo, len, q0)) return;
+    const int rows = len - q0;
+    const Keys keys(p, q0, ROWS, len);
+    const float *q = (const float *)p.q + (lo + q0) * p.qs + h * D, *k = (const float *)p.k + lo * p.ks + hk * D,
+                *v = (const float *)p.v + lo * p.vs + hk * D;
+    const int64_t at0 = ((lo + q0) * p.Hq + h) * D, step = (int64_t)p.Hq * D;
+    auto fetch_keys = [&](int t) {
+        float *dst = KV + (t & 1) * 2 * kTile * S;
+        fetch<D, kTile>(dst, k, [&](int r) { return kTile * t + r < keys.total ? k + (int64_t)keys.at(kTile * t + r) * p.ks : nullptr; });
+        fetch<D, kTile>(dst + kTile * S, v, [&](int r) { return kTile * t + r < keys.total ? v + (int64_t)keys.at(kTile * t + r) * p.vs : nullptr; });
+    };
+    fetch<D, ROWS>(O, p.d_out, [&](int r) { return r < rows ? (const float *)p.d_out + at0 + r * step : nullptr; });
+    fetch<D, ROWS>(Q, p.q, [&](int r) { return r < rows ? q + (int64_t)r * p.qs : nullptr; });
+    fetch_keys(0);
+    umma::cp_async_commit();
+    float delta[R], lse[R];
+    float2 dq[R][D / 32];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i = 4 * ty + r;
+    for (int r = 0; r < R; ++r) {
+        const int i = R * ty + r;
         float x = 0.f;
+        if (i < rows) {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) {
-            const float4 a = load4(K + i * S + 64 * u + 4 * tx), b = load4(O + i * S + 64 * u + 4 * tx);
-            x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+            for (int u = 0; u < D / 64; ++u) {
+                const float4 a = load4((const float *)p.out + at0 + i * step + 64 * u + 4 * tx),
+                             b = load4((const float *)p.d_out + at0 + i * step + 64 * u + 4 * tx);
+                x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+            }
         }
         delta[r] = sum16(x);
         lse[r] = 0.f;
@@ -238,88 +286,103 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
             if (tx == 0) p.delta[h * p.seqs.total + lo + q0 + i] = delta[r];
         }
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dq[r][c] = 0.f;
+        for (int c = 0; c < D / 32; ++c) dq[r][c] = make_float2(0.f, 0.f);
     }
-    const KeyTiles tiles(p, q0, len);
-    for (int t = 0; t < tiles.n; ++t) {
-        int k0, count;
-        tiles.get(t, k0, count);
+    const int tiles = (keys.total + kTile - 1) / kTile;
+    for (int t = 0; t < tiles; ++t) {
+        umma::cp_async_wait_all();
         __syncthreads();
-        load_tile<D>(K, (const T *)p.k + (lo + k0) * p.ks + hk * D, p.ks, count);
-        load_tile<D>(V, (const T *)p.v + (lo + k0) * p.vs + hk * D, p.vs, count);
-        __syncthreads();
-        float s[4][4], dp[4][4];
-        rows_by_rows<D>(s, Q, K, ty, tx);
-        rows_by_rows<D>(dp, O, V, ty, tx);
+        if (t + 1 < tiles) fetch_keys(t + 1);
+        umma::cp_async_commit();
+        const float *K = KV + (t & 1) * 2 * kTile * S;
+        float s[R][4], dp[R][4];
+        rows_by_rows<D, R>(s, Q, K, ty, tx);
+        rows_by_rows<D, R>(dp, O, K + kTile * S, ty, tx);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int kj = tx + 16 * c;
-                const bool in = kj < count && sees(p, q0 + 4 * ty + r, k0 + kj);
+                const int at = kTile * t + tx + 16 * c;
+                const bool in = at < keys.total && sees(p, q0 + R * ty + r, keys.at(at));
                 s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -lse[r])) * (dp[r][c] - delta[r]) : 0.f;
             }
-        put_scores(P, s, ty, tx);
-        __syncthreads();
-        rows_by_cols<D>(dq, P, K, ty, tx);
+        put_scores<R>(P, s, ty, tx);
+        rows_by_cols<D, R>(dq, P, K, min(kTile, (keys.total - kTile * t + 3) & ~3), ty, tx);
     }
-    put_rows<D>((T *)p.dq + (lo + q0) * p.dqs + h * D, p.dqs, rows, dq, p.scale, ty, tx);
+    put_rows<D, R>((float *)p.dq + (lo + q0) * p.dqs + h * D, p.dqs, rows, dq, p.scale, ty, tx);
 }
 
-// dk and dv of a key tile, over all queries that see a key of it and all heads that share it.
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProblem p) {
-    constexpr int S = row_floats<D>();
+// dk and dv of a key tile, over the block's queries and all heads that share the keys.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProblem p, const attn::SinkPlan plan) {
+    constexpr int S = row_floats<D>(), ROWS = 16 * R;
     extern __shared__ float sm[];
-    float *Q = sm, *O = Q + kTile * S, *K = O + kTile * S, *V = K + kTile * S, *P = V + kTile * S;
-    __shared__ float lse[kTile], delta[kTile];
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, hk = blockIdx.x % p.Hk, g = p.Hq / p.Hk;
-    int64_t n, lo;
-    int j, len;
-    if (!find_tile(p.seqs, kTile, blockIdx.x / p.Hk, n, j, lo, len)) return;
-    const int k0 = j * kTile, rows = len - k0;
-    load_tile<D>(K, (const T *)p.k + (lo + k0) * p.ks + hk * D, p.ks, rows);
-    load_tile<D>(V, (const T *)p.v + (lo + k0) * p.vs + hk * D, p.vs, rows);
-    float dk[4][D / 16], dv[4][D / 16];
+    float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + ROWS * kPs;   // [2][lse, delta][64]
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, g = p.Hq / p.Hk;
+    attn::KeyBlock kb;
+    if (!kb.find(p, plan, blockIdx.x)) return;
+    const int64_t lo = kb.lo;
+    const int len = kb.len, hk = kb.hk, k0 = kb.k0, rows = len - k0;
+    const int nt = (kb.qb - kb.qa + kTile - 1) / kTile, tiles = nt * g;
+    auto fetch_queries = [&](int t) {
+        const int h = hk * g + t / nt, q0 = kb.qa + t % nt * kTile, n = kb.qb - q0;
+        float *dst = QO + (t & 1) * 2 * kTile * S, *st = stat + (t & 1) * 2 * kTile;
+        const float *q = (const float *)p.q + (lo + q0) * p.qs + h * D, *d = (const float *)p.d_out + ((lo + q0) * p.Hq + h) * D;
+        fetch<D, kTile>(dst, p.q, [&](int r) { return r < n ? q + (int64_t)r * p.qs : nullptr; });
+        fetch<D, kTile>(dst + kTile * S, p.d_out, [&](int r) { return r < n ? d + (int64_t)r * p.Hq * D : nullptr; });
+        const int r = threadIdx.x & (kTile - 1);
+        if (threadIdx.x < kTile) umma::cp_async4(st + r, r < n ? p.lse + (lo + q0 + r) * p.Hq + h : p.lse, r < n ? 4u : 0u);
+        else if (threadIdx.x < 2 * kTile) umma::cp_async4(st + kTile + r, r < n ? p.delta + h * p.seqs.total + lo + q0 + r : p.delta, r < n ? 4u : 0u);
+    };
+    fetch<D, ROWS>(K, p.k, [&](int r) { return r < rows ? (const float *)p.k + (lo + k0 + r) * p.ks + hk * D : nullptr; });
+    fetch<D, ROWS>(V, p.v, [&](int r) { return r < rows ? (const float *)p.v + (lo + k0 + r) * p.vs + hk * D : nullptr; });
+    fetch_queries(0);
+    umma::cp_async_commit();
+    float2 dk[R][D / 32], dv[R][D / 32];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dk[r][c] = dv[r][c] = 0.f;
-    const int end = k0 < p.sinks ? len : min(len, k0 + kTile - 1 + p.window);
-    for (int h = hk * g; h < (hk + 1) * g; ++h)
-        for (int q0 = k0; q0 < end; q0 += kTile) {
-            const int count = len - q0;
-            __syncthreads();
-            load_tile<D>(Q, (const T *)p.q + (lo + q0) * p.qs + h * D, p.qs, count);
-            load_tile<D>(O, (const T *)p.d_out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, count);
-            if (threadIdx.x < kTile) {
-                const bool in = (int)threadIdx.x < count;
-                lse[threadIdx.x] = in ? p.lse[(lo + q0 + threadIdx.x) * p.Hq + h] : 0.f;
-                delta[threadIdx.x] = in ? p.delta[h * p.seqs.total + lo + q0 + threadIdx.x] : 0.f;
+        for (int c = 0; c < D / 32; ++c) dk[r][c] = dv[r][c] = make_float2(0.f, 0.f);
+    for (int t = 0; t < tiles; ++t) {
+        umma::cp_async_wait_all();
+        __syncthreads();
+        if (t + 1 < tiles) fetch_queries(t + 1);
+        umma::cp_async_commit();
+        const int q0 = kb.qa + t % nt * kTile, n = min(kTile, (kb.qb - q0 + 3) & ~3);
+        const float *Q = QO + (t & 1) * 2 * kTile * S, *O = Q + kTile * S, *st = stat + (t & 1) * 2 * kTile;
+        float s[R][4], dp[R][4];
+        rows_by_rows<D, R>(s, K, Q, ty, tx);
+        rows_by_rows<D, R>(dp, V, O, ty, tx);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int qi = tx + 16 * c, j = k0 + R * ty + r;
+                const bool in = q0 + qi < kb.qb && sees(p, q0 + qi, j) && (kb.chunk < 0 || j < p.sinks);
+                s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -st[qi])) : 0.f;
+                dp[r][c] = in ? s[r][c] * (dp[r][c] - st[kTile + qi]) : 0.f;
             }
-            __syncthreads();
-            float s[4][4], dp[4][4];
-            rows_by_rows<D>(s, K, Q, ty, tx);
-            rows_by_rows<D>(dp, V, O, ty, tx);
+        put_scores<R>(P, s, ty, tx);
+        rows_by_cols<D, R>(dv, P, O, n, ty, tx);
+        put_scores<R>(P, dp, ty, tx);
+        rows_by_cols<D, R>(dk, P, Q, n, ty, tx);
+    }
+    // a sink's row is a part of a sum where its queries are cut
+    const int sinks = kb.cut ? min(p.sinks - k0, rows) : 0;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r) {
+        const int row = R * ty + r;
+        const bool part = row < sinks;
+        if (row >= rows || (kb.chunk >= 0 && !part)) continue;
+        float *to_k = part ? kb.sum(p, plan, k0 + row) : (float *)p.dk + (lo + k0 + row) * p.dks + hk * D;
+        float *to_v = part ? to_k + D : (float *)p.dv + (lo + k0 + row) * p.dvs + hk * D;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int qi = tx + 16 * c;
-                    const bool in = qi < count && sees(p, q0 + qi, k0 + 4 * ty + r);
-                    s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -lse[qi])) : 0.f;
-                    dp[r][c] = s[r][c] * (dp[r][c] - delta[qi]);
-                }
-            put_scores(P, s, ty, tx);
-            __syncthreads();
-            rows_by_cols<D>(dv, P, O, ty, tx);
-            __syncthreads();
-            put_scores(P, dp, ty, tx);
-            __syncthreads();
-            rows_by_cols<D>(dk, P, Q, ty, tx);
+        for (int u = 0; u < D / 64; ++u) {
+            const float2 a = mul2(dk[r][2 * u], make_float2(p.scale, p.scale)), b = mul2(dk[r][2 * u + 1], make_float2(p.scale, p.scale));
+            store4(to_k + 64 * u + 4 * tx, make_float4(a.x, a.y, b.x, b.y));
+            store4(to_v + 64 * u + 4 * tx, make_float4(dv[r][2 * u].x, dv[r][2 * u].y, dv[r][2 * u + 1].x, dv[r][2 * u + 1].y));
         }
-    put_rows<D>((T *)p.dk + (lo + k0) * p.dks + hk * D, p.dks, rows, dk, p.scale, ty, tx);
-    put_rows<D>((T *)p.dv + (lo + k0) * p.dvs + hk * D, p.dvs, rows, dv, 1.f, ty, tx);
+    }
 }
 
 // Rows in front of the first sequence and behind the last.
@@ -337,31 +400,61 @@ __global__ void __launch_bounds__(256) attn_zero_rest_kernel(const LinrecSeqs s,
     }
 }
 
-template <class F>
-int launch(F *kernel, size_t smem, int64_t blocks, const AttnProblem &p, cudaStream_t s) {
+constexpr int kSms = 152;
+
+// Whether tiles of 64 rows would leave SMs without one.
+bool few(const AttnProblem &p, int heads) { return attn_tile_slots(p.seqs, kTile) * heads < kSms; }
+
+template <class F, class... A>
+int launch(F *kernel, size_t floats, int64_t blocks, cudaStream_t s, const A &...args) {
+    const size_t smem = sizeof(float) * floats;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return kErrCuda;
-    kernel<<<(unsigned)blocks, kThreads, smem, s>>>(p);
+    kernel<<<(unsigned)blocks, kThreads, smem, s>>>(args...);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
-template <int D> constexpr size_t smem_bytes(int tiles) { return sizeof(float) * (tiles * kTile * row_floats<D>() + kTile * kPs); }
+// a block's own tiles of ROWS rows, the four of 64, the scores
+template <int D> constexpr size_t floats(int own, int rows) { return (size_t)(own * rows + 4 * kTile) * row_floats<D>() + (size_t)rows * kPs; }
 
-template <int D, typename T>
-int bwd(const AttnProblem &p, cudaStream_t s) {
-    const int64_t slots = attn_tile_slots(p.seqs, kTile);
-    const int rc = launch(attn_simt_dq_kernel<D, T>, smem_bytes<D>(4), slots * p.Hq, p, s);
-    return rc != kOk ? rc : launch(attn_simt_dkv_kernel<D, T>, smem_bytes<D>(4), slots * p.Hk, p, s);
+template <int D, int R>
+int fwd(const AttnProblem &p, cudaStream_t s) {
+    return launch(attn_simt_fwd_kernel<D, R>, floats<D>(1, 16 * R), attn_tile_slots(p.seqs, 16 * R) * p.Hq, s, p);
+}
+template <int D, int R>
+int bwd_q(const AttnProblem &p, cudaStream_t s) {
+    return launch(attn_simt_dq_kernel<D, R>, floats<D>(2, 16 * R), attn_tile_slots(p.seqs, 16 * R) * p.Hq, s, p);
+}
+
+int key_rows(const AttnProblem &p) { return few(p, p.Hk) ? 16 : 64; }
+size_t delta_bytes(const AttnProblem &p) { return attn::round256(sizeof(float) * (size_t)(p.seqs.total * p.Hq)); }
+
+template <int D>
+int bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
+    int rc = few(p, p.Hq) ? bwd_q<D, 1>(p, s) : bwd_q<D, 4>(p, s);
+    if (rc != kOk) return rc;
+    attn::SinkPlan plan;
+    attn::plan_sinks(p, key_rows(p), 256, (char *)workspace + delta_bytes(p), plan);
+    const int64_t blocks = attn::key_blocks(p, plan);
+    rc = plan.tile == 16 ? launch(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 4 * kTile, blocks, s, p, plan)
+                         : launch(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 4 * kTile, blocks, s, p, plan);
+    return rc != kOk ? rc : attn::launch_sink_sum<D, float>(p, plan, s);
 }
 
 }  // namespace
 
 int launch_attn_simt_fwd(const AttnProblem &p, cudaStream_t s) {
-    const int64_t blocks = attn_tile_slots(p.seqs, kTile) * p.Hq;
-    return p.d == 64 ? launch(attn_simt_fwd_kernel<64, float>, smem_bytes<64>(2), blocks, p, s)
-                     : launch(attn_simt_fwd_kernel<128, float>, smem_bytes<128>(2), blocks, p, s);
+    if (few(p, p.Hq)) return p.d == 64 ? fwd<64, 1>(p, s) : fwd<128, 1>(p, s);
+    return p.d == 64 ? fwd<64, 4>(p, s) : fwd<128, 4>(p, s);
 }
 
-int launch_attn_simt_bwd(const AttnProblem &p, cudaStream_t s) {
-    return p.d == 64 ? bwd<64, float>(p, s) : bwd<128, float>(p, s);
+size_t attn_simt_bwd_workspace_bytes(const AttnProblem &p) {
+    attn::SinkPlan plan;
+    return delta_bytes(p) + attn::plan_sinks(p, key_rows(p), 256, nullptr, plan);
+}
+
+int launch_attn_simt_bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
+    AttnProblem x = p;
+    x.delta = (float *)workspace;
+    return p.d == 64 ? bwd<64>(x, workspace, s) : bwd<128>(x, workspace, s);
 }
 
 int launch_attn_zero_rest(const LinrecSeqs &s, const AttnRest &r, cudaStream_t stream) {

@@ -1,0 +1,139 @@
+// attn_sinks.cuh -- the blocks of the window attention's dk and dv: which keys and queries a block takes.
+//
+// A block takes a tile of keys of a head and the queries whose window reaches it.  Sinks are seen by every later
+// query: a tile that holds some would take as long as the sequence is.  Where few tiles do, the queries
+// behind the tile's window are cut into chunks with blocks of their own, which leave fp32 sums of the sinks' rows, and so does
+// the tile's own block; attn_sink_sum_kernel adds them up in order.
+#pragma once
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace dr {
+namespace attn {
+
+constexpr int kMaxSplitTiles = 8;      // key tiles with sinks that are cut
+
+struct SinkPlan {
+    int tile;                  // keys of a block
+    int tiles, rows, chunk;    // tiles that are cut (0: none), rows of their sums, tokens of a chunk
+    int64_t slots;             // chunks of all sequences
+    float *base, *parts;       // [n | chunk slot][Hk][tile][row][dk, dv][d]
+};
+
+inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// How the sinks' queries are cut, and the bytes of workspace (at ws) that this takes.
+inline size_t plan_sinks(const AttnProblem &p, int tile, int least, char *ws, SinkPlan &s) {
+    s = SinkPlan{};
+    s.tile = tile;
+    s.chunk = 1 << 30;
+    const int64_t longest = p.seqs.cu ? p.seqs.total : p.seqs.T, sinks = p.sinks < longest ? p.sinks : longest;
+    const int64_t tiles = (sinks + tile - 1) / tile;
+    // (nobody is behind the window of the first tile of the longest sequence: nothing to cut)
+    if (p.window >= kNoWindow || sinks == 0 || tiles > kMaxSplitTiles || longest <= p.window + tile - 1) return 0;
+    s.tiles = (int)tiles;
+    s.rows = (int)(sinks < tile ? sinks : tile);
+    const int64_t own = p.window + tile;       // about as long as a block without sinks
+    s.chunk = (int)(((own < least ? least : own) + 127) / 128 * 128);
+    s.slots = p.seqs.cu ? p.seqs.total / s.chunk + p.seqs.N : p.seqs.N * ((p.seqs.T + s.chunk - 1) / s.chunk);
+    const size_t one = sizeof(float) * (size_t)p.Hk * s.tiles * s.rows * 2 * p.d, base = round256(one * p.seqs.N);
+    s.base = (float *)ws;
+    s.parts = (float *)(ws + base);
+    return base + round256(one * s.slots);
+}
+
+#ifdef __CUDACC__
+// Chunks come first, short blocks last (dk, dv of B8 T2048 H16/4 w1024 170 us; chunks last 194).
+inline int64_t key_blocks(const AttnProblem &p, const SinkPlan &s) {
+    return (attn_tile_slots(p.seqs, s.tile) + s.slots * s.tiles) * p.Hk;
+}
+
+struct KeyBlock {
+    int64_t n, lo, slot;       // sequence, its first row; the chunk's slot
+    int len, hk, jt, k0;       // its length; head, tile, first key
+    int chunk;                 // -1: the tile's own block
+    int qa, qb;                // queries
+    bool cut;                  // the sinks' rows are parts of sums
+    // What the block does, false for nothing.  By whole warps.
+    __device__ __forceinline__ bool find(const AttnProblem &p, const SinkPlan &s, int64_t block) {
+        const int64_t chunks = s.slots * p.Hk * s.tiles;
+        chunk = -1;
+        slot = 0;
+        if (block >= chunks) {
+            int64_t k = block - chunks;
+            hk = (int)(k % p.Hk);
+            k /= p.Hk;
+            if (p.seqs.cu) {
+                if (!find_tile(p.seqs, s.tile, (int)k, n, jt, lo, len)) return false;
+            } else {       // early keys, which most queries see, first
+                n = k % p.seqs.N;
+                jt = (int)(k / p.seqs.N);
+                lo = n * p.seqs.T;
+                len = (int)p.seqs.T;
+            }
+        } else {
+            int64_t k = block;
+            hk = (int)(k % p.Hk);
+            k /= p.Hk;
+            jt = (int)(k % s.tiles);
+            slot = k / s.tiles;
+            if (!find_tile(p.seqs, s.chunk, (int)slot, n, chunk, lo, len)) return false;
+        }
+        k0 = jt * s.tile;
+        if (k0 >= len) return false;
+        const int behind = min(len, min(k0 + s.tile - 1, kNoWindow - 1) + p.window);     // behind the last query whose window reaches the tile
+        const bool sink = k0 < p.sinks;
+        cut = sink && jt < s.tiles && behind < len;
+        qa = k0;
+        qb = sink && !cut ? len : behind;
+        if (chunk >= 0) {
+            qa = max(behind, chunk * s.chunk);
+            qb = min(len, (chunk + 1) * s.chunk);
+            return cut && qa < qb;
+        }
+        return true;
+    }
+    // The sum of key j's row, a sink (dk, then dv).
+    __device__ __forceinline__ float *sum(const AttnProblem &p, const SinkPlan &s, int j) const {
+        return (chunk >= 0 ? s.parts : s.base) + ((((chunk >= 0 ? slot : n) * p.Hk + hk) * s.tiles + jt) * s.rows + (j - k0)) * 2 * p.d;
+    }
+};
+
+// The sinks' rows: what their window gave and the chunks, in order.  A block a key tile of a sequence and head.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) attn_sink_sum_kernel(const AttnProblem p, const SinkPlan s) {
+    int64_t k = blockIdx.x, lo, hi;
+    const int jt = (int)(k % s.tiles);
+    k /= s.tiles;
+    const int hk = (int)(k % p.Hk);
+    const int64_t n = k / p.Hk;
+    seq_range(p.seqs, n, lo, hi);
+    const int len = (int)(hi - lo), k0 = jt * s.tile, rows = min(s.rows, min(p.sinks, len) - k0);
+    const int behind = min(len, min(k0 + s.tile - 1, kNoWindow - 1) + p.window);
+    if (rows <= 0 || behind >= len) return;
+    const int64_t slot0 = p.seqs.cu ? lo / s.chunk + n : n * ((p.seqs.T + s.chunk - 1) / s.chunk);
+    const int c0 = behind / s.chunk, c1 = (len + s.chunk - 1) / s.chunk;
+    const int64_t tile = ((int64_t)hk * s.tiles + jt) * s.rows * 2 * D, step = (int64_t)p.Hk * s.tiles * s.rows * 2 * D;
+    for (int x = threadIdx.x; x < rows * 2 * D / 4; x += 256) {
+        float4 sum = load4(s.base + n * step + tile + 4 * x);
+#pragma unroll 4
+        for (int c = c0; c < c1; ++c) {
+            const float4 y = load4(s.parts + (slot0 + c) * step + tile + 4 * x);
+            sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+        }
+        const int row = 4 * x / (2 * D), at = 4 * x % (2 * D);
+        const int64_t r = lo + k0 + row;
+        store4(at < D ? static_cast<T *>(p.dk) + r * p.dks + hk * D + at : static_cast<T *>(p.dv) + r * p.dvs + hk * D + at - D, sum);
+    }
+}
+template <int D, typename T>
+int launch_sink_sum(const AttnProblem &p, const SinkPlan &s, cudaStream_t stream) {
+    if (s.tiles == 0) return kOk;
+    attn_sink_sum_kernel<D, T><<<(unsigned)(p.seqs.N * p.Hk * s.tiles), 256, 0, stream>>>(p, s);
+    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+}
+#endif
+
+}  // namespace attn
+}  // namespace dr

@@ -17,12 +17,11 @@
 //     dV += P^T dO,  dK += dS^T Q       P^T, dS^T (bf16) from tensor memory over S's, dP's place; dO, Q as loaded
 // While the softmax warps form P^T of a tile the tensor cores work at the tile before (dK) and the
 // products of V, and the other way round.
-// Sinks are seen by every later query: the tiles of keys that hold some would take as long as the sequence is. What
-// lies behind their window is cut into chunks of queries, whose blocks leave fp32 sums for the sinks' rows that a last
-// kernel adds up in order.
+// Which keys and queries a block takes, and how tiles that hold sinks are cut: attn_sinks.cuh.
 //
 // Rows of other sequences are masked; where they enter a product as 0 times whatever they hold they are
 // overwritten with zeros in shared memory.  Waits are bounded as in the forward.
+#include "attn_sinks.cuh"
 #include "attn_tc.cuh"
 
 namespace dr {
@@ -34,7 +33,6 @@ constexpr int kStatWarps = 4, kDqThreads = 32 * (kSoftWarps + 8), kDkvThreads = 
 // Registers a thread: launched with 80 and 96; the softmax warps take what the others give back.
 constexpr int kDqSoftRegs = 96, kDqOtherRegs = 48, kDkvSoftRegs = 104, kDkvOtherRegs = 56;
 static_assert(16 * kDqSoftRegs + 8 * kDqOtherRegs <= 24 * 80 && 16 * kDkvSoftRegs + 4 * kDkvOtherRegs <= 20 * 96, "register split");
-constexpr int kMaxSplitTiles = 8;      // key tiles with sinks that are cut
 
 struct BwdArgs {
     AttnProblem p;
@@ -43,10 +41,7 @@ struct BwdArgs {
     int64_t items;             // of dq
     bool falling;              // later items are shorter
     float2 *stats;             // [key head and run][row][head of the run] (lse log2 e, delta)
-    // sinks: 0 tiles where they are not cut
-    int sink_tiles, sink_rows, chunk;
-    int64_t chunk_slots;
-    float *base, *parts;       // [n | chunk slot][Hk][sink tile][sink row][dk, dv][d]
+    SinkPlan sinks;
 };
 
 struct Item {
@@ -434,41 +429,10 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     using L = DkvLayout<D>;
     constexpr int NB = L::NB, NS = L::NS;
     const AttnProblem &p = a.p;
-    // what this block does: key tile jt of sequence n, queries qa .. qb - 1
-    int64_t n, lo;
-    int jt, len, hk, chunk = -1;
-    int64_t slot = 0;
-    const int64_t chunks = a.chunk_slots * p.Hk * a.sink_tiles;     // first: short blocks come last
-    if ((int64_t)blockIdx.x >= chunks) {
-        int64_t k = blockIdx.x - chunks;
-        hk = (int)(k % p.Hk);
-        k /= p.Hk;
-        if (p.seqs.cu) {
-            if (!find_tile(p.seqs, kKeys, (int)k, n, jt, lo, len)) return;
-        } else {       // early keys, which most queries see, first
-            n = k % p.seqs.N;
-            jt = (int)(k / p.seqs.N);
-            lo = n * p.seqs.T;
-            len = (int)p.seqs.T;
-        }
-    } else {
-        int64_t k = blockIdx.x;
-        hk = (int)(k % p.Hk);
-        k /= p.Hk;
-        jt = (int)(k % a.sink_tiles);
-        slot = k / a.sink_tiles;
-        if (!find_tile(p.seqs, a.chunk, (int)slot, n, chunk, lo, len)) return;
-    }
-    const int k0 = jt * kKeys;
-    if (k0 >= len) return;
-    const int behind = min(len, min(k0 + kKeys - 1, kNoWindow - 1) + p.window);     // behind the last query whose window reaches the tile
-    const bool sink = k0 < p.sinks, cut = sink && jt < a.sink_tiles && behind < len;
-    int qa = k0, qb = sink && !cut ? len : behind;
-    if (chunk >= 0) {
-        qa = max(behind, chunk * a.chunk);
-        qb = min(len, (chunk + 1) * a.chunk);
-        if (!cut || qa >= qb) return;
-    }
+    KeyBlock kb;
+    if (!kb.find(p, a.sinks, blockIdx.x)) return;
+    const int64_t lo = kb.lo;
+    const int len = kb.len, hk = kb.hk, k0 = kb.k0, qa = kb.qa, qb = kb.qb;
     const int nt = (qb - qa + a.tokens - 1) / a.tokens, tiles = nt * a.runs;
 
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -601,19 +565,19 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             float o[C];
             tmem_ld_cols(tl + (e == 0 ? TM_DK : TM_DV) + C * group, o);
             tmem_wait_ld();
-            if (cut && j < min(p.sinks, len)) {
-                float *sum = (chunk >= 0 ? a.parts : a.base) + ((((chunk >= 0 ? slot : n) * p.Hk + hk) * a.sink_tiles + jt) * a.sink_rows + (j - k0)) * 2 * D + e * D + C * group;
+            if (kb.cut && j < min(p.sinks, len)) {
+                float *sum = kb.sum(p, a.sinks, j) + e * D + C * group;
 #pragma unroll
                 for (int x = 0; x < C; x += 4) store4(sum + x, make_float4(o[x] * scale, o[x + 1] * scale, o[x + 2] * scale, o[x + 3] * scale));
             }
-            if (chunk >= 0) continue;
+            if (kb.chunk >= 0) continue;
             uint4 u[C / 8];
             to_pieces(o, scale, u);
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e == 0 ? p.dk : p.dv) + hk * D + C * group;
             const int64_t stride = e == 0 ? p.dks : p.dvs;
             put_rows<C / 8>(u, lane, [&](int r) {
                 const int jj = k0 + 32 * quarter + r;
-                return jj < len && !(cut && jj < p.sinks) ? out + (lo + jj) * stride : nullptr;
+                return jj < len && !(kb.cut && jj < p.sinks) ? out + (lo + jj) * stride : nullptr;
             });
         }
     } else if (warp == kLoadWarp) {
@@ -721,64 +685,15 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     if (warp == kMmaWarp) tmem_dealloc(tm, 512);
 }
 
-// The sinks' rows: what their window gave and the chunks, in order.  A block a key tile of a sequence and head.
-template <int D>
-__global__ void __launch_bounds__(256) attn_sink_sum_kernel(const BwdArgs a) {
-    const AttnProblem &p = a.p;
-    int64_t k = blockIdx.x, lo, hi;
-    const int jt = (int)(k % a.sink_tiles);
-    k /= a.sink_tiles;
-    const int hk = (int)(k % p.Hk);
-    const int64_t n = k / p.Hk;
-    seq_range(p.seqs, n, lo, hi);
-    const int len = (int)(hi - lo), k0 = jt * kKeys, rows = min(a.sink_rows, min(p.sinks, len) - k0);
-    const int behind = min(len, min(k0 + kKeys - 1, kNoWindow - 1) + p.window);
-    if (rows <= 0 || behind >= len) return;
-    const int64_t slot0 = p.seqs.cu ? lo / a.chunk + n : n * ((p.seqs.T + a.chunk - 1) / a.chunk);
-    const int c0 = behind / a.chunk, c1 = (len + a.chunk - 1) / a.chunk;
-    const int64_t tile = ((int64_t)hk * a.sink_tiles + jt) * a.sink_rows * 2 * D, step = (int64_t)p.Hk * a.sink_tiles * a.sink_rows * 2 * D;
-    for (int x = threadIdx.x; x < rows * 2 * D / 4; x += 256) {
-        float4 s = load4(a.base + n * step + tile + 4 * x);
-#pragma unroll 4
-        for (int c = c0; c < c1; ++c) {
-            const float4 y = load4(a.parts + (slot0 + c) * step + tile + 4 * x);
-            s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
-        }
-        const int row = 4 * x / (2 * D), at = 4 * x % (2 * D);
-        const int64_t r = lo + k0 + row;
-        __nv_bfloat16 *dst = at < D ? static_cast<__nv_bfloat16 *>(p.dk) + r * p.dks + hk * D + at
-                                    : static_cast<__nv_bfloat16 *>(p.dv) + r * p.dvs + hk * D + at - D;
-        store4(dst, s);
-    }
-}
-
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-// How the sinks' queries are cut, and where the workspace's parts lie.
+// Where the workspace's parts lie.
 size_t plan(const AttnProblem &p, BwdArgs &a, char *ws) {
     a.p = p;
     a.gs = heads_in_tile(p.Hq / p.Hk);
     a.runs = p.Hq / p.Hk >> a.gs;
     a.tokens = 128 >> a.gs;
-    size_t at = 0;
-    a.stats = (float2 *)(ws + at);
-    at += round256(sizeof(float2) * (size_t)(p.seqs.total * p.Hq));
-    const int64_t longest = p.seqs.cu ? p.seqs.total : p.seqs.T, sinks = p.sinks < longest ? p.sinks : longest;
-    const int64_t tiles = (sinks + kKeys - 1) / kKeys;
-    // (nobody is behind the window of the first tile of the longest sequence: nothing to cut)
-    if (p.window < kNoWindow && sinks > 0 && tiles <= kMaxSplitTiles && longest > p.window + kKeys - 1) {
-        a.sink_tiles = (int)tiles;
-        a.sink_rows = (int)(sinks < kKeys ? sinks : kKeys);
-        const int64_t own = p.window + kKeys;      // about as long as a block without sinks
-        a.chunk = (int)(((own < 1024 ? 1024 : own) + kKeys - 1) / kKeys * kKeys);
-        a.chunk_slots = p.seqs.cu ? p.seqs.total / a.chunk + p.seqs.N : p.seqs.N * ((p.seqs.T + a.chunk - 1) / a.chunk);
-        const size_t one = sizeof(float) * (size_t)p.Hk * a.sink_tiles * a.sink_rows * 2 * p.d;
-        a.base = (float *)(ws + at);
-        at += round256(one * p.seqs.N);
-        a.parts = (float *)(ws + at);
-        at += round256(one * a.chunk_slots);
-    }
-    return at;
+    a.stats = (float2 *)ws;
+    const size_t stats = round256(sizeof(float2) * (size_t)(p.seqs.total * p.Hq));
+    return stats + plan_sinks(p, kKeys, 1024, ws + stats, a.sinks);
 }
 
 template <int D>
@@ -796,12 +711,10 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
     a.falling = !p.seqs.cu && p.window > p.seqs.T / 2;
     attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kDqThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    const int64_t blocks = (attn_tile_slots(p.seqs, kKeys) + a.chunk_slots * a.sink_tiles) * p.Hk;
+    const int64_t blocks = key_blocks(p, a.sinks);
     attn_dkv_kernel<D><<<(unsigned)blocks, kDkvThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    if (a.sink_tiles == 0) return kOk;
-    attn_sink_sum_kernel<D><<<(unsigned)(p.seqs.N * p.Hk * a.sink_tiles), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+    return launch_sink_sum<D, __nv_bfloat16>(p, a.sinks, s);
 }
 
 }  // namespace
