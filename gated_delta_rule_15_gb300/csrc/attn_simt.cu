@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "attn_sinks.cuh"
 #include "common.cuh"
+#include "launch_chain.cuh"
 #include "umma.cuh"
 
 namespace dr {
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     int64_t lo;
     int h, hk, len, q0;
+    let_next_start();
     if (!query_tile<ROWS>(p, h, hk, lo, len, q0)) return;
     const int rows = len - q0;
     const Keys keys(p, q0, ROWS, len);
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
     float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + ROWS * kPs;   // [2][lse, delta][64]
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, g = p.Hq / p.Hk;
     attn::KeyBlock kb;
+    let_next_start();
     if (!kb.find(p, plan, blockIdx.x)) return;
     const int64_t lo = kb.lo;
     const int len = kb.len, hk = kb.hk, k0 = kb.k0, rows = len - k0;
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
     };
     fetch<D, ROWS>(K, p.k, [&](int r) { return r < rows ? (const float *)p.k + (lo + k0 + r) * p.ks + hk * D : nullptr; });
     fetch<D, ROWS>(V, p.v, [&](int r) { return r < rows ? (const float *)p.v + (lo + k0 + r) * p.vs + hk * D : nullptr; });
+    wait_for_last();       // delta
     fetch_queries(0);
     umma::cp_async_commit();
     float2 dk[R][D / 32], dv[R][D / 32];
@@ -412,6 +416,12 @@ int launch(F *kernel, size_t floats, int64_t blocks, cudaStream_t s, const A &..
     kernel<<<(unsigned)blocks, kThreads, smem, s>>>(args...);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
 }
+template <class F, class... A>
+int launch_next(F *kernel, size_t floats, int64_t blocks, cudaStream_t s, const A &...args) {
+    const size_t smem = sizeof(float) * floats;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return kErrCuda;
+    return launch_after(kernel, (unsigned)blocks, kThreads, smem, s, args...);
+}
 // a block's own tiles of ROWS rows, the four of 64, the scores
 template <int D> constexpr size_t floats(int own, int rows) { return (size_t)(own * rows + 4 * kTile) * row_floats<D>() + (size_t)rows * kPs; }
 
@@ -434,8 +444,8 @@ int bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
     attn::SinkPlan plan;
     attn::plan_sinks(p, key_rows(p), 256, (char *)workspace + delta_bytes(p), plan);
     const int64_t blocks = attn::key_blocks(p, plan);
-    rc = plan.tile == 16 ? launch(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 4 * kTile, blocks, s, p, plan)
-                         : launch(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 4 * kTile, blocks, s, p, plan);
+    rc = plan.tile == 16 ? launch_next(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 4 * kTile, blocks, s, p, plan)
+                         : launch_next(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 4 * kTile, blocks, s, p, plan);
     return rc != kOk ? rc : attn::launch_sink_sum<D, float>(p, plan, s);
 }
 

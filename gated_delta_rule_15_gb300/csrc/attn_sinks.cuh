@@ -8,6 +8,7 @@
 
 #include "attn.h"
 #include "common.cuh"
+#include "launch_chain.cuh"
 
 namespace dr {
 namespace attn {
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(256) attn_sink_sum_kernel(const AttnProblem p,
     const int len = (int)(hi - lo), k0 = jt * s.tile, rows = min(s.rows, min(p.sinks, len) - k0);
     const int behind = min(len, min(k0 + s.tile - 1, kNoWindow - 1) + p.window);
     if (rows <= 0 || behind >= len) return;
+    wait_for_last();
     const int64_t slot0 = p.seqs.cu ? lo / s.chunk + n : n * ((p.seqs.T + s.chunk - 1) / s.chunk);
     const int c0 = behind / s.chunk, c1 = (len + s.chunk - 1) / s.chunk;
     const int64_t tile = ((int64_t)hk * s.tiles + jt) * s.rows * 2 * D, step = (int64_t)p.Hk * s.tiles * s.rows * 2 * D;
@@ -130,8 +132,7 @@ __global__ void __launch_bounds__(256) attn_sink_sum_kernel(const AttnProblem p,
 template <int D, typename T>
 int launch_sink_sum(const AttnProblem &p, const SinkPlan &s, cudaStream_t stream) {
     if (s.tiles == 0) return kOk;
-    attn_sink_sum_kernel<D, T><<<(unsigned)(p.seqs.N * p.Hk * s.tiles), 256, 0, stream>>>(p, s);
-    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+    return launch_after(attn_sink_sum_kernel<D, T>, (unsigned)(p.seqs.N * p.Hk * s.tiles), 256, 0, stream, p, s);
 }
 #endif
 

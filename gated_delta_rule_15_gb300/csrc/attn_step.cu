@@ -26,6 +26,7 @@
 #include "../../include/dr.h"
 #include "attn.h"
 #include "common.cuh"
+#include "launch_chain.cuh"
 #include "tc_common.cuh"
 #include "tc_issue.cuh"
 
@@ -436,6 +437,7 @@ attn_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         for (int i = 0; i < L::STAGES; ++i) mbar_init(bars + i, 1);
     if (tid == 0) polls_s = tc::kPolls;
     fence_mbar_init();
+    let_next_start();
 
     // what the units in front of each of 256 runs of sequences cost
     const int64_t run = (p.B + kThreads - 1) / kThreads;
@@ -575,6 +577,7 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const StepArgs a) {
     __shared__ float4 sum_s[512];
     const AttnStep &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_for_last();
 #pragma unroll 1
     for (int own = 0; own < kWarps; ++own) {
         const Tail tail = a.tail[blockIdx.x * kWarps + own];
@@ -694,8 +697,7 @@ int launch(const CUtensorMap *m, const StepArgs &a, int blocks, cudaStream_t s) 
     if (cudaFuncSetAttribute(attn_step_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return kErrCuda;
     attn_step_kernel<D, BF><<<blocks, kThreads, smem, s>>>(m[0], m[1], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    attn_join_kernel<D, BF><<<blocks, 512, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
+    return launch_after(attn_join_kernel<D, BF>, (unsigned)blocks, 512, 0, s, a);
 }
 
 }  // namespace

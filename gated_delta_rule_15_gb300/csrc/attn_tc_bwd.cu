@@ -134,6 +134,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         tmem_alloc(&tmem_s, 512);
         tmem_relinquish();
     }
+    let_next_start();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -470,6 +471,8 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         tmem_alloc(&tmem_s, 512);
         tmem_relinquish();
     }
+    let_next_start();
+    wait_for_last();       // its statistics, and the workspace of a call before it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -712,9 +715,8 @@ int launch(const AttnProblem &p, BwdArgs a, cudaStream_t s) {
     attn_dq_kernel<D><<<(unsigned)(a.items < kSms ? a.items : kSms), kDqThreads, smem_q, s>>>(m[0], m[1], m[2], m[3], a);
     if (cudaGetLastError() != cudaSuccess) return kErrCuda;
     const int64_t blocks = key_blocks(p, a.sinks);
-    attn_dkv_kernel<D><<<(unsigned)blocks, kDkvThreads, smem_kv, s>>>(m[0], m[1], m[2], m[3], a);
-    if (cudaGetLastError() != cudaSuccess) return kErrCuda;
-    return launch_sink_sum<D, __nv_bfloat16>(p, a.sinks, s);
+    const int rc = launch_after(attn_dkv_kernel<D>, (unsigned)blocks, kDkvThreads, smem_kv, s, m[0], m[1], m[2], m[3], a);
+    return rc != kOk ? rc : launch_sink_sum<D, __nv_bfloat16>(p, a.sinks, s);
 }
 
 }  // namespace
