@@ -567,39 +567,84 @@ attn_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     if (lane == 0 && polls_s == 0) atomicExch(a.status, kErrTimeout);
 }
 
-// Joins the parts of the units that the warps of block blockIdx.x began and others went on with, one after another.
+// Whether the warps of block c work at one unit, and left one part of it.
+__device__ __forceinline__ bool joint_block(const Tail &t, int64_t c) {
+    const int64_t x0 = c * t.per * kWarps, x1 = min(t.total, x0 + t.per * kWarps);
+    return x1 - x0 > t.per && t.first <= x0 && x1 <= t.end;
+}
+
+// Joins the parts of the units that the warps of block blockIdx.x began and others went on with.  Units in few warps (those
+// of short contexts, several a block): a warp each, a part a lane.  Units in more: the whole block, one after another.
 template <int D, bool BF>
 __global__ void __launch_bounds__(512) attn_join_kernel(const StepArgs a) {
     using T = typename std::conditional<BF, __nv_bfloat16, float>::type;
     constexpr int kMost = kBlocks + 2 * kWarps;      // parts: a block's one, but for the first and last block's warps
+    __shared__ Tail tails[kWarps];
     __shared__ int slot_s[kMost], n_s;
     __shared__ float weight[kMost][kHeads];
     __shared__ float4 sum_s[512];
     const AttnStep &p = a.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = p.Hq / p.Hk;
     wait_for_last();
+    if (tid < kWarps) tails[tid] = a.tail[blockIdx.x * kWarps + tid];
+    __syncthreads();
+    auto first_warp = [&](const Tail &t) { return (t.first + kUnitCost) / t.per; };
+    auto warps_of = [&](const Tail &t) { return (t.end - 1) / t.per - first_warp(t) + 1; };
+    if (tails[warp % kWarps].b >= 0 && warps_of(tails[warp % kWarps]) <= 32) {      // (two warps, every other row)
+        const Tail &t = tails[warp % kWarps];
+        const int h0 = (t.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0), n = (int)warps_of(t);
+        const int64_t head = t.b * p.Hq + t.hu / a.per_h * g + h0, w = first_warp(t) + lane;
+        const bool is = lane < n && (!joint_block(t, w / kWarps) || w % kWarps == 0);
+        const float *mine = a.partial + (w * 2 + (lane == 0 ? 1 : 0)) * a.part_floats;
+        const uint32_t all = __ballot_sync(0xffffffffu, is);
+        constexpr int C = D / 32;
+#pragma unroll 2
+        for (int row = warp / kWarps; row < rows; row += 2) {
+            const float2 ml = is ? *reinterpret_cast<const float2 *>(mine + rows * D + 2 * row) : make_float2(-INFINITY, 0.f);
+            float top = ml.x;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float base = top == -INFINITY ? 0.f : top, e = exp2f(ml.x - base);
+            float sum = ml.y * e;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            const float f = sum > 0.f ? e / sum : 0.f;
+            float o[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] = 0.f;
+            for (uint32_t left = all; left; left &= left - 1) {
+                const int l = __ffs(left) - 1;
+                const float *src = a.partial + ((first_warp(t) + l) * 2 + (l == 0 ? 1 : 0)) * a.part_floats + row * D + C * lane;
+                const float x = __shfl_sync(0xffffffffu, f, l);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = fmaf(x, src[c], o[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) ((T *)p.out)[(head + row) * D + C * lane + c] = from_f32<T>(o[c]);
+            if (p.lse && lane == 0) p.lse[head + row] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        }
+    }
 #pragma unroll 1
     for (int own = 0; own < kWarps; ++own) {
-        const Tail tail = a.tail[blockIdx.x * kWarps + own];
-        if (tail.b < 0) continue;
+        const Tail &t = tails[own];
+        if (t.b < 0 || warps_of(t) <= 32) continue;
         __syncthreads();
-        const int g = p.Hq / p.Hk, h0 = (tail.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0);
-        const int64_t head = tail.b * p.Hq + tail.hu / a.per_h * g + h0;
+        const int h0 = (t.hu % a.per_h) * kHeads, rows = min(kHeads, g - h0);
+        const int64_t head = t.b * p.Hq + t.hu / a.per_h * g + h0;
         // the parts' slots, in order
-        const int64_t group0 = tail.first + kUnitCost, per = tail.per;
-        const int block_a = (int)(group0 / (per * kWarps)), block_b = (int)((tail.end - 1) / (per * kWarps));
         if (warp == 0) {
+            const int64_t group0 = t.first + kUnitCost, per = t.per;
+            const int block_a = (int)(group0 / (per * kWarps)), block_b = (int)((t.end - 1) / (per * kWarps));
             int n = 0;
 #pragma unroll 1
             for (int c0 = block_a; c0 <= block_b; c0 += 32) {
                 const int c = c0 + lane;
                 int first = 0, count = 0;      // warps of the block that have a part
                 if (c <= block_b) {
-                    const int64_t x0 = c * per * kWarps, x1 = min(tail.total, x0 + per * kWarps);
-                    const bool joint = x1 - x0 > per && tail.first <= x0 && x1 <= tail.end;   // its warps left one part
-                    first = (int)max((int64_t)0, (group0 - x0) / per);
-                    count = joint ? 1 : (int)min((int64_t)kWarps, (tail.end - x0 + per - 1) / per) - first;
-                    if (joint) first = 0;
+                    const int64_t x0 = c * per * kWarps;
+                    const bool joint = joint_block(t, c);
+                    first = joint ? 0 : (int)max((int64_t)0, (group0 - x0) / per);
+                    count = joint ? 1 : (int)min((int64_t)kWarps, (t.end - x0 + per - 1) / per) - first;
                 }
                 int at = count;
 #pragma unroll
@@ -619,23 +664,28 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const StepArgs a) {
         auto part = [&](int c) { return a.partial + ((int64_t)slot_s[c] * 2 + (c == 0 ? 1 : 0)) * a.part_floats; };
         // a warp a row: the parts' weights
         if (warp < rows) {
-            float top = -INFINITY;
-            for (int c = lane; c < n; c += 32) top = fmaxf(top, part(c)[rows * D + 2 * warp]);
+            constexpr int E = (kMost + 31) / 32;
+            float2 ml[E];
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                ml[e] = lane + 32 * e < n ? *reinterpret_cast<const float2 *>(part(lane + 32 * e) + rows * D + 2 * warp) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = fmaxf(top, ml[e].x);
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
             const float base = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-            for (int c = lane; c < n; c += 32) {
-                const float2 ml = *reinterpret_cast<const float2 *>(part(c) + rows * D + 2 * warp);
-                const float e = exp2f(ml.x - base);
-                weight[c][warp] = e;
-                sum = fmaf(ml.y, e, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                ml[e].x = exp2f(ml[e].x - base);
+                sum = fmaf(ml[e].y, ml[e].x, sum);
             }
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            __syncwarp();
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            for (int c = lane; c < n; c += 32) weight[c][warp] *= inv;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (lane + 32 * e < n) weight[lane + 32 * e][warp] = ml[e].x * inv;
             if (p.lse && lane == 0) p.lse[head + warp] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
         }
         __syncthreads();
@@ -643,7 +693,7 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const StepArgs a) {
         const int quads = rows * (D / 4), ways = 512 / quads, way = tid / quads, i = tid % quads, row = i / (D / 4);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (way < ways)
-#pragma unroll 4
+#pragma unroll 10
             for (int c = way; c < n; c += ways) {
                 const float4 y = reinterpret_cast<const float4 *>(part(c))[i];
                 const float w = weight[c][row];
