@@ -323,7 +323,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, g = p.Hq / p.Hk;
     attn::KeyBlock kb;
     let_next_start();
-    if (!kb.find(p, plan, blockIdx.x)) return;
+    if (!kb.find(p, plan, blockIdx.x)) {
+        wait_for_last();
+        return;
+    }
     const int64_t lo = kb.lo;
     const int len = kb.len, hk = kb.hk, k0 = kb.k0, rows = len - k0;
     const int nt = (kb.qb - kb.qa + kTile - 1) / kTile, tiles = nt * g;

@@ -104,6 +104,7 @@ struct KeyBlock {
 // The sinks' rows: what their window gave and the chunks, in order.  A block a key tile of a sequence and head.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) attn_sink_sum_kernel(const AttnProblem p, const SinkPlan s) {
+    wait_for_last();       // (blocks without a row too: what follows in the stream waits for this kernel alone)
     int64_t k = blockIdx.x, lo, hi;
     const int jt = (int)(k % s.tiles);
     k /= s.tiles;
@@ -113,7 +114,6 @@ __global__ void __launch_bounds__(256) attn_sink_sum_kernel(const AttnProblem p,
     const int len = (int)(hi - lo), k0 = jt * s.tile, rows = min(s.rows, min(p.sinks, len) - k0);
     const int behind = min(len, min(k0 + s.tile - 1, kNoWindow - 1) + p.window);
     if (rows <= 0 || behind >= len) return;
-    wait_for_last();
     const int64_t slot0 = p.seqs.cu ? lo / s.chunk + n : n * ((p.seqs.T + s.chunk - 1) / s.chunk);
     const int c0 = behind / s.chunk, c1 = (len + s.chunk - 1) / s.chunk;
     const int64_t tile = ((int64_t)hk * s.tiles + jt) * s.rows * 2 * D, step = (int64_t)p.Hk * s.tiles * s.rows * 2 * D;

@@ -431,7 +431,10 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     constexpr int NB = L::NB, NS = L::NS;
     const AttnProblem &p = a.p;
     KeyBlock kb;
-    if (!kb.find(p, a.sinks, blockIdx.x)) return;
+    if (!kb.find(p, a.sinks, blockIdx.x)) {
+        wait_for_last();
+        return;
+    }
     const int64_t lo = kb.lo;
     const int len = kb.len, hk = kb.hk, k0 = kb.k0, qa = kb.qa, qb = kb.qb;
     const int nt = (qb - qa + a.tokens - 1) / a.tokens, tiles = nt * a.runs;

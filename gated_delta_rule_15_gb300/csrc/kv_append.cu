@@ -46,8 +46,8 @@ __device__ __forceinline__ bool place(const AppendArgs &a, int64_t tok, int64_t 
         first = max(first, (int64_t)0);
     }
     const int64_t s = __ldg(a.start + n);
-    pos = s + (tok - first);
-    return s >= 0;
+    pos = (int64_t)((uint64_t)s + (uint64_t)(tok - first));
+    return s >= 0 && pos >= 0;       // (a start near 2^63 wraps)
 }
 
 template <int D, bool HALF, typename T>
@@ -60,14 +60,6 @@ kv_append_kernel(const AppendArgs a, int norm) {
     const int64_t tok = unit / a.groups;
     const int g = (int)(unit % a.groups), all = a.Hq + 2 * a.Hk;
     const bool there = tok < a.n_tok;
-    // the first rows are on their way while the token's place and angles are found
-    if (there && l % (128 / (8 * (int)sizeof(T))) == 0) {
-        const int h0 = (int)((int64_t)all * g / a.groups), h1 = min((int)((int64_t)all * (g + 1) / a.groups), h0 + U);
-        for (int h = h0; h < h1; ++h) {
-            const int s = h < a.Hq ? 0 : h < a.Hq + a.Hk ? 1 : 2;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.x[s] + tok * a.stride[s] + (int64_t)(h - (s == 0 ? 0 : a.Hq + (s - 1) * a.Hk)) * D + 8 * l));
-        }
-    }
     int64_t n = 0, pos = 0;
     const bool live = there && place(a, tok, n, pos);
     // the token's slot: element of its row in head 0 of the cache, or -1

@@ -9,7 +9,8 @@ namespace dr {
 
 // In the kernel before: its successor's blocks may take SMs that have no work left.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// In the successor, in front of the first access to what the kernel before reads or writes: waits until that has ended.
+// In the successor, by every block, in front of the first access to what the kernel before writes and of the first write of
+// its own: waits until that kernel has ended.
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... P, class... A>
