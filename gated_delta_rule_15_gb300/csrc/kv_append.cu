@@ -2,7 +2,8 @@
 // normalised and rotated on the way (declared in include/dr.h).  The row's mathematics: qk_norm_rope.cu.
 //
 // One pass, bound by HBM bandwidth: a group of d / 8 lanes takes a token and a run of its heads (queries,
-// keys, values, one behind another), 8 values a lane, so a warp's accesses are whole rows.  A token finds
+// keys, values, one behind another), 8 values a lane, so a warp's accesses are whole rows.  (Its tokens lie in the
+// grid's x, its run in y: with 64-bit divisions for those and for the page the kernel was bound by issue, 70 %.)  A token finds
 // its sequence in the offsets by bisection (they stay in L1), its position from the sequence's length before the call,
 // and its page in the table.
 #include <math.h>
@@ -24,8 +25,8 @@ struct AppendArgs {
     const uint64_t *table;
     const int *pages;
     const int64_t *cu, *start;
-    int64_t n_tok, N, n_pages, max_pages;
-    int page, Hq, Hk, rot, groups, zero_rest;
+    int64_t n_tok, N, n_pages, max_pages, room;   // room: tokens of a sequence's pages
+    int page, Hq, Hk, rot, run, zero_rest;        // run: heads (of queries, keys, values, one behind another) a block takes
     float eps, scale;
 };
 
@@ -56,24 +57,24 @@ kv_append_kernel(const AppendArgs a, int norm) {
     constexpr int LPR = D / 8, U = 4;
     const int lane = threadIdx.x & 31, l = lane % LPR, src = partner<HALF>(a, lane, l), lp = l + src - lane;
     const bool rotated = 8 * l < a.rot;
-    const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
-    const int64_t tok = unit / a.groups;
-    const int g = (int)(unit % a.groups), all = a.Hq + 2 * a.Hk;
+    const int64_t tok = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int run0 = blockIdx.y * a.run, run1 = run0 + a.run;      // this block's heads
     const bool there = tok < a.n_tok;
     int64_t n = 0, pos = 0;
     const bool live = there && place(a, tok, n, pos);
     // the token's slot: element of its row in head 0 of the cache, or -1
     int64_t slot = -1;
-    if (live && pos / a.page < a.max_pages) {
-        const int64_t pg = __ldg(a.pages + n * a.max_pages + pos / a.page);
-        if (pg >= 0 && pg < a.n_pages) slot = (pg * a.Hk * a.page + pos % a.page) * D;
+    if (live && pos < a.room) {
+        const int64_t at = pos >> 32 ? pos / a.page : (int64_t)((uint32_t)pos / (uint32_t)a.page);   // (64-bit divisions are long)
+        const int64_t pg = __ldg(a.pages + n * a.max_pages + at);
+        if (pg >= 0 && pg < a.n_pages) slot = (pg * a.Hk * a.page + (pos - at * a.page)) * D;
     }
     float co[8], si[8];
     angles<HALF>(a, pos, l, false, co, si);
 #pragma unroll 1
     for (int s = 0; s < 3; ++s) {
         const int first = s == 0 ? 0 : a.Hq + (s - 1) * a.Hk, last = s == 0 ? a.Hq : first + a.Hk;
-        const int h0 = max((int)((int64_t)all * g / a.groups), first), h1 = min((int)((int64_t)all * (g + 1) / a.groups), last);
+        const int h0 = max(run0, first), h1 = min(run1, last);
         const bool mine = s == 0 ? there && (live || a.zero_rest) : slot >= 0;
         const int rows = mine && h1 > h0 ? h1 - h0 : 0, most = __reduce_max_sync(0xffffffffu, rows);
         if (most == 0) continue;
@@ -128,8 +129,7 @@ kv_append_kernel(const AppendArgs a, int norm) {
 
 template <int D, typename T>
 int launch(const AppendArgs &a, int norm, bool half, cudaStream_t s) {
-    const int64_t threads = a.n_tok * a.groups * (D / 8);
-    const unsigned blocks = (unsigned)((threads + 255) / 256);
+    const dim3 blocks((unsigned)((a.n_tok * (D / 8) + 255) / 256), (unsigned)((a.Hq + 2 * a.Hk + a.run - 1) / a.run));
     if (half) kv_append_kernel<D, true, T><<<blocks, 256, 0, s>>>(a, norm);
     else kv_append_kernel<D, false, T><<<blocks, 256, 0, s>>>(a, norm);
     return cudaGetLastError() == cudaSuccess ? kOk : kErrCuda;
@@ -212,8 +212,9 @@ extern "C" int dr_kv_append(const dr_kv_append_desc *desc, const void *q, const 
     // runs of heads a token's rows are split into: one while the tokens alone give every SM its 2048 threads
     const int64_t threads = d.n_tok * (d.d / 8), all = d.Hq + 2 * d.Hk, want = (int64_t)152 * 2048;
     const int64_t groups = threads >= want ? 1 : (want + threads - 1) / threads;
-    a.groups = (int)(groups < all ? groups : all);
-    if (d.n_tok * a.groups * (d.d / 8) > (int64_t)256 * 0x7fffffff) return kErrUnsupported;
+    a.run = (int)(groups < all ? (all + groups - 1) / groups : 1);
+    if (a.run < (all + 65534) / 65535) a.run = (int)((all + 65534) / 65535);      // (the grid's second extent)
+    a.room = d.max_pages * d.page;
     const bool half = d.layout == DR_ROPE_HALF;
     cudaStream_t s = (cudaStream_t)stream;
     if (d.dtype == DR_BF16)
