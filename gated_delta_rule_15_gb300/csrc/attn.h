@@ -33,7 +33,7 @@ struct AttnProblem {
     const void *d_out;                 // [rows, Hq, d]
     void *dq, *dk, *dv;                // rows dqs, dks, dvs elements apart
     int64_t dqs, dks, dvs;
-    float *delta;                      // (workspace, fp32 rows) [Hq][rows]
+    float *delta, *inv_l;              // (workspace, fp32 rows) [Hq][rows]; inv_l: attn_simt.cu
 };
 
 #ifdef __CUDACC__

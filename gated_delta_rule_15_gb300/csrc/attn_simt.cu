@@ -4,9 +4,8 @@
 // Tiles of 16 R rows (queries; of dk, dv keys) by 64 others, 256 threads as 16 x 16: a thread holds R x 4 scores (rows
 // R ty + r, others tx + 16 c) and R rows x d / 16 columns of what is summed.  Products run over rows in
 // shared memory as float4 of both operands and two FMAs an instruction (R = 4: 32 of them to 8 loads); the
-// row stride of d + 4 floats keeps the 16 rows of a load on different banks.  The scores' sums go over even and odd
-// channels apart, and what is summed over tiles is first summed within one, so that sums of a thousand
-// terms are off by less than one of them would be.
+// row stride of d + 4 floats keeps the 16 rows of a load on different banks.  What is summed over tiles is first summed
+// within one, so that sums of a thousand terms are less off than one chain of them would be.
 // The 64 others come by asynchronous copies a tile ahead.  A query's keys: first the sinks in front of its tile's window, then the
 // window, with the running maximum and sum of the softmax in registers.
 // R = 4, or 1 where tiles of 64 rows would not give every SM one (T256 H2 d64 w64: 21.3 us with R = 4).
@@ -40,34 +39,44 @@ __device__ __forceinline__ void fetch(float *dst, const void *any, At at) {
     }
 }
 
-// acc[r][c] = sum over d of A[R ty + r] B[tx + 16 c]
+// acc[r][c] = sum over d of A[R ty + r] B[tx + 16 c], in sums of 8 of the even and 8 of the odd channels (a score's error is
+// its weight's)
 template <int D, int R>
 __device__ __forceinline__ void rows_by_rows(float (&acc)[R][4], const float *A, const float *B, int ty, int tx) {
     constexpr int S = row_floats<D>();
-    float2 x[R][4];
+    float2 sum[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[r][c] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < D; k += 4) {
-        float4 a[R], b[4];
+        for (int c = 0; c < 4; ++c) sum[r][c] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < D; k0 += 16) {
+        float2 x[R][4];
 #pragma unroll
-        for (int r = 0; r < R; ++r) a[r] = load4(A + (R * ty + r) * S + k);
+        for (int k = 0; k < 16; k += 4) {
+            float4 a[R], b[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) b[c] = load4(B + (tx + 16 * c) * S + k);
+            for (int r = 0; r < R; ++r) a[r] = load4(A + (R * ty + r) * S + k0 + k);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) b[c] = load4(B + (tx + 16 * c) * S + k0 + k);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 a0 = make_float2(a[r].x, a[r].y), b0 = make_float2(b[c].x, b[c].y);
+                    x[r][c] = k == 0 ? mul2(a0, b0) : fma2(a0, b0, x[r][c]);
+                    x[r][c] = fma2(make_float2(a[r].z, a[r].w), make_float2(b[c].z, b[c].w), x[r][c]);
+                }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[r][c] = fma2(make_float2(a[r].x, a[r].y), make_float2(b[c].x, b[c].y), x[r][c]);
-                x[r][c] = fma2(make_float2(a[r].z, a[r].w), make_float2(b[c].z, b[c].w), x[r][c]);
-            }
+            for (int c = 0; c < 4; ++c) sum[r][c] = add2(sum[r][c], x[r][c]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = x[r][c].x + x[r][c].y;
+        for (int c = 0; c < 4; ++c) acc[r][c] = sum[r][c].x + sum[r][c].y;
 }
 
 // acc[r][2 u + h] += sum over `n` k (a multiple of 4) of P[R ty + r][k] X[k][64 u + 4 tx + 2 h, + 1]
@@ -242,7 +251,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
     put_rows<D, R>((float *)p.out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, len - q0, o, 1.f, ty, tx);
 }
 
-// dq of a query tile, and delta of its rows.
+// dq of a query tile, and of its rows l and delta.  lse and out are rounded, and results of other sums than this kernel's:
+// with w_ij = exp(s_ij - lse_i), l = sum_j w_ij is not quite 1 and sum_j w_ij (do_i.v_j - do_i.o_i) not quite 0, which what
+// the keys have in common magnifies.  So
+//     x_ij = w_ij (do_i.v_j - do_i.o_i),   e = sum_j x_ij / l,   delta_i = do_i.o_i + e,
+//     dq_i = scale (sum_j x_ij k_j - e sum_j w_ij k_j) / l,
+// a fourth product to three (keys with a common direction of 3 times their spread, sequences of 10 tokens: dq off by 2.5e-6
+// without, where all in one arithmetic is off by 1.1e-6).
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProblem p) {
     constexpr int S = row_floats<D>(), ROWS = 16 * R;
@@ -267,8 +282,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
     fetch<D, ROWS>(Q, p.q, [&](int r) { return r < rows ? q + (int64_t)r * p.qs : nullptr; });
     fetch_keys(0);
     umma::cp_async_commit();
-    float delta[R], lse[R];
-    float2 dq[R][D / 32];
+    float delta[R], lse[R], l[R], e[R];
+    float2 dq[R][D / 32], wk[R][D / 32];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = R * ty + r;
@@ -282,13 +297,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
             }
         }
         delta[r] = sum16(x);
-        lse[r] = 0.f;
-        if (i < rows) {
-            lse[r] = p.lse[(lo + q0 + i) * p.Hq + h];
-            if (tx == 0) p.delta[h * p.seqs.total + lo + q0 + i] = delta[r];
-        }
+        lse[r] = i < rows ? p.lse[(lo + q0 + i) * p.Hq + h] : 0.f;
+        l[r] = e[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) dq[r][c] = make_float2(0.f, 0.f);
+        for (int c = 0; c < D / 32; ++c) dq[r][c] = wk[r][c] = make_float2(0.f, 0.f);
     }
     const int tiles = (keys.total + kTile - 1) / kTile;
     for (int t = 0; t < tiles; ++t) {
@@ -301,15 +313,37 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
         rows_by_rows<D, R>(s, Q, K, ty, tx);
         rows_by_rows<D, R>(dp, O, K + kTile * S, ty, tx);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            float sw = 0.f, sx = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int at = kTile * t + tx + 16 * c;
                 const bool in = at < keys.total && sees(p, q0 + R * ty + r, keys.at(at));
-                s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -lse[r])) * (dp[r][c] - delta[r]) : 0.f;
+                s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -lse[r])) : 0.f;
+                dp[r][c] = in ? s[r][c] * (dp[r][c] - delta[r]) : 0.f;
+                sw += s[r][c];
+                sx += dp[r][c];
             }
+            l[r] += sw;
+            e[r] += sx;
+        }
+        const int n = min(kTile, (keys.total - kTile * t + 3) & ~3);
         put_scores<R>(P, s, ty, tx);
-        rows_by_cols<D, R>(dq, P, K, min(kTile, (keys.total - kTile * t + 3) & ~3), ty, tx);
+        rows_by_cols<D, R>(wk, P, K, n, ty, tx);
+        put_scores<R>(P, dp, ty, tx);
+        rows_by_cols<D, R>(dq, P, K, n, ty, tx);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = R * ty + r;
+        const float inv = 1.f / sum16(l[r]), x = sum16(e[r]) * inv;
+        if (tx == 0 && i < rows) {
+            const int64_t at = h * p.seqs.total + lo + q0 + i;
+            p.delta[at] = delta[r] + x;
+            p.inv_l[at] = inv;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) dq[r][c] = mul2(fma2(make_float2(-x, -x), wk[r][c], dq[r][c]), make_float2(inv, inv));
     }
     put_rows<D, R>((float *)p.dq + (lo + q0) * p.dqs + h * D, p.dqs, rows, dq, p.scale, ty, tx);
 }
@@ -319,7 +353,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProblem p, const attn::SinkPlan plan) {
     constexpr int S = row_floats<D>(), ROWS = 16 * R;
     extern __shared__ float sm[];
-    float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + ROWS * kPs;   // [2][lse, delta][64]
+    float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + ROWS * kPs;   // [2][lse, delta, 1 / l][64]
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, g = p.Hq / p.Hk;
     attn::KeyBlock kb;
     let_next_start();
@@ -332,17 +366,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
     const int nt = (kb.qb - kb.qa + kTile - 1) / kTile, tiles = nt * g;
     auto fetch_queries = [&](int t) {
         const int h = hk * g + t / nt, q0 = kb.qa + t % nt * kTile, n = kb.qb - q0;
-        float *dst = QO + (t & 1) * 2 * kTile * S, *st = stat + (t & 1) * 2 * kTile;
+        float *dst = QO + (t & 1) * 2 * kTile * S, *st = stat + (t & 1) * 3 * kTile;
         const float *q = (const float *)p.q + (lo + q0) * p.qs + h * D, *d = (const float *)p.d_out + ((lo + q0) * p.Hq + h) * D;
         fetch<D, kTile>(dst, p.q, [&](int r) { return r < n ? q + (int64_t)r * p.qs : nullptr; });
         fetch<D, kTile>(dst + kTile * S, p.d_out, [&](int r) { return r < n ? d + (int64_t)r * p.Hq * D : nullptr; });
         const int r = threadIdx.x & (kTile - 1);
         if (threadIdx.x < kTile) umma::cp_async4(st + r, r < n ? p.lse + (lo + q0 + r) * p.Hq + h : p.lse, r < n ? 4u : 0u);
-        else if (threadIdx.x < 2 * kTile) umma::cp_async4(st + kTile + r, r < n ? p.delta + h * p.seqs.total + lo + q0 + r : p.delta, r < n ? 4u : 0u);
+        else if (threadIdx.x < 3 * kTile) {
+            const float *from = threadIdx.x < 2 * kTile ? p.delta : p.inv_l;
+            umma::cp_async4(st + threadIdx.x, r < n ? from + h * p.seqs.total + lo + q0 + r : from, r < n ? 4u : 0u);
+        }
     };
     fetch<D, ROWS>(K, p.k, [&](int r) { return r < rows ? (const float *)p.k + (lo + k0 + r) * p.ks + hk * D : nullptr; });
     fetch<D, ROWS>(V, p.v, [&](int r) { return r < rows ? (const float *)p.v + (lo + k0 + r) * p.vs + hk * D : nullptr; });
-    wait_for_last();       // delta
+    wait_for_last();       // delta, 1 / l
     fetch_queries(0);
     umma::cp_async_commit();
     float2 dk[R][D / 32], dv[R][D / 32];
@@ -356,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
         if (t + 1 < tiles) fetch_queries(t + 1);
         umma::cp_async_commit();
         const int q0 = kb.qa + t % nt * kTile, n = min(kTile, (kb.qb - q0 + 3) & ~3);
-        const float *Q = QO + (t & 1) * 2 * kTile * S, *O = Q + kTile * S, *st = stat + (t & 1) * 2 * kTile;
+        const float *Q = QO + (t & 1) * 2 * kTile * S, *O = Q + kTile * S, *st = stat + (t & 1) * 3 * kTile;
         float s[R][4], dp[R][4];
         rows_by_rows<D, R>(s, K, Q, ty, tx);
         rows_by_rows<D, R>(dp, V, O, ty, tx);
@@ -366,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
             for (int c = 0; c < 4; ++c) {
                 const int qi = tx + 16 * c, j = k0 + R * ty + r;
                 const bool in = q0 + qi < kb.qb && sees(p, q0 + qi, j) && (kb.chunk < 0 || j < p.sinks);
-                s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -st[qi])) : 0.f;
+                s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -st[qi])) * st[2 * kTile + qi] : 0.f;
                 dp[r][c] = in ? s[r][c] * (dp[r][c] - st[kTile + qi]) : 0.f;
             }
         put_scores<R>(P, s, ty, tx);
@@ -438,17 +475,18 @@ int bwd_q(const AttnProblem &p, cudaStream_t s) {
 }
 
 int key_rows(const AttnProblem &p) { return few(p, p.Hk) ? 16 : 64; }
-size_t delta_bytes(const AttnProblem &p) { return attn::round256(sizeof(float) * (size_t)(p.seqs.total * p.Hq)); }
+// delta, or 1 / l
+size_t stat_bytes(const AttnProblem &p) { return attn::round256(sizeof(float) * (size_t)(p.seqs.total * p.Hq)); }
 
 template <int D>
 int bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
     int rc = few(p, p.Hq) ? bwd_q<D, 1>(p, s) : bwd_q<D, 4>(p, s);
     if (rc != kOk) return rc;
     attn::SinkPlan plan;
-    attn::plan_sinks(p, key_rows(p), 256, (char *)workspace + delta_bytes(p), plan);
+    attn::plan_sinks(p, key_rows(p), 256, (char *)workspace + 2 * stat_bytes(p), plan);
     const int64_t blocks = attn::key_blocks(p, plan);
-    rc = plan.tile == 16 ? launch_next(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 4 * kTile, blocks, s, p, plan)
-                         : launch_next(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 4 * kTile, blocks, s, p, plan);
+    rc = plan.tile == 16 ? launch_next(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 6 * kTile, blocks, s, p, plan)
+                         : launch_next(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 6 * kTile, blocks, s, p, plan);
     return rc != kOk ? rc : attn::launch_sink_sum<D, float>(p, plan, s);
 }
 
@@ -461,12 +499,13 @@ int launch_attn_simt_fwd(const AttnProblem &p, cudaStream_t s) {
 
 size_t attn_simt_bwd_workspace_bytes(const AttnProblem &p) {
     attn::SinkPlan plan;
-    return delta_bytes(p) + attn::plan_sinks(p, key_rows(p), 256, nullptr, plan);
+    return 2 * stat_bytes(p) + attn::plan_sinks(p, key_rows(p), 256, nullptr, plan);
 }
 
 int launch_attn_simt_bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
     AttnProblem x = p;
     x.delta = (float *)workspace;
+    x.inv_l = (float *)((char *)workspace + stat_bytes(p));
     return p.d == 64 ? bwd<64>(x, workspace, s) : bwd<128>(x, workspace, s);
 }
 
