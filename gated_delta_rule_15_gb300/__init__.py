@@ -1,5 +1,5 @@
 """GB300-native gated delta rule: chunkwise forward, backward and single-token decode; the additive
-gated recurrence; queries and keys normalised and rotated.
+gated recurrence; queries and keys normalised and rotated; window attention and its paged cache.
 
 The compute lives in the C-ABI library ``libdr.so`` (CUDA, sm_103a), declared in
 ``include/dr.h``.  ``gated_delta_rule_15_gb300.dr`` is its thin ctypes binding; importing
