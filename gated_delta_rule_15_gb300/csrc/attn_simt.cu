@@ -8,7 +8,12 @@
 // within one, so that sums of a thousand terms are less off than one chain of them would be.
 // The 64 others come by asynchronous copies a tile ahead.  A query's keys: first the sinks in front of its tile's window, then the
 // window, with the running maximum and sum of the softmax in registers.
-// R = 4, or 1 where tiles of 64 rows would not give every SM one (T256 H2 d64 w64: 21.3 us with R = 4).
+// R = 4, or 1 where tiles of 64 rows would leave more than half of the SMs without one.  Measured with R = 1 and 4, by the
+// number of tiles of 64: forward 8 (T256 H2 d64 w64) 10.3 and 18.5 us, 32 (T512 H4 d128) 51 and 74, 80 (T300 H16 d64 w64) 14.3 and
+// 16.4, 102 (T1037 H6 d64 w200) 39 and 31, 128 (T2048 H4 d128) 414 and 275; dq 32 35 us less, 80 18 and 102 30 us more; dk, dv 51 25
+// us less, 64 (B2 T1024 H8/2) 8 us less, 128 (T4096 H2 d64 w256) 40 us more.
+// What bounds it: issue and shared memory (R = 4: 12 of its cycles to 16 of FMAs; R = 1: 9 to 4), and
+// for the few blocks of small problems the longest one's tiles, one behind another.
 #include "../../include/dr.h"
 #include "attn.h"
 #include "attn_sinks.cuh"
@@ -446,8 +451,8 @@ __global__ void __launch_bounds__(256) attn_zero_rest_kernel(const LinrecSeqs s,
 
 constexpr int kSms = 152;
 
-// Whether tiles of 64 rows would leave SMs without one.
-bool few(const AttnProblem &p, int heads) { return attn_tile_slots(p.seqs, kTile) * heads < kSms; }
+// Whether to take tiles of 16 rows (above).
+bool few(const AttnProblem &p, int heads) { return attn_tile_slots(p.seqs, kTile) * heads < kSms / 2; }
 
 template <class F, class... A>
 int launch(F *kernel, size_t floats, int64_t blocks, cudaStream_t s, const A &...args) {

@@ -19,6 +19,11 @@
 // products of V, and the other way round.
 // Which keys and queries a block takes, and how tiles that hold sinks are cut: attn_sinks.cuh.
 //
+// What bounds them (B8 T2048 H16/4 d128 w1024: dq 162 us, dk and dv 170): a tile of dq takes 2,100 cycles where the tensor cores
+// need 1,536 and shared memory 1,750 (operands of three products, the last one's A from tensor memory, and two copies); a tile of
+// dk, dv 2,600 where both need 2,048.  The rest is the chain from S and dP to dS, half covered by the
+// products of the neighbouring tiles, and the items' begin and end.
+//
 // Rows of other sequences are masked; where they enter a product as 0 times whatever they hold they are
 // overwritten with zeros in shared memory.  Waits are bounded as in the forward.
 #include "attn_sinks.cuh"
@@ -416,7 +421,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 // ------------------------------------------------------------------ dk, dv
 template <int D>
 struct DkvLayout {
-    // query-side tiles (with four of them Q waits for the product before the last: 2874 instead of 2500 cycles a tile), statistics
+    // query-side tiles (two in use, two on their way, one to spare), statistics
     static constexpr int PANELS = D / 64, TILE = 128 * D * 2, NB = D == 128 ? 5 : 10, NS = 2;
     static constexpr uint32_t K = 0, V = TILE, QO = 2 * TILE, STATS = QO + NB * TILE, BARS = STATS + NS * 128 * 8;
     static constexpr uint32_t TOTAL = BARS + (2 * NB + 2 * NS + 6) * 8 + 8;

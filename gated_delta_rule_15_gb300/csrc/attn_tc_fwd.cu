@@ -12,9 +12,17 @@
 // a few times a row at most.  A row's decisions depend on the row alone.
 //
 // Warps 0..7 and 8..15 are the stages' softmax and write their outputs, two for each 32 rows with 64 keys a
-// thread, which ask one another only whether a maximum rose; warp 16 issues the copies, warps 17 and 18 the stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor
-// cores work for the other.  (One thread for both stages is late: a tile's sixteen products take it 900 cycles to
+// thread, which ask one another only whether a maximum rose; warp 16 issues the copies, warps 17 and 18 the
+// stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor cores work for the other.  (One thread for both stages is late: a tile's sixteen products take it 900 cycles to
 // issue and their waits 400, which the tensor cores need 1024 for.)
+//
+// What bounds it (bf16, d = 128): the tensor cores need 2,048 cycles for a key tile of both stages (64 for 16 of a product's depth), it
+// takes 2,400 where every query sees all before it (B2 T8192 H16: 400 us, 1.37 PFLOP/s) and 2,900 with a window (B8 T4096
+// H16/4 w1024: 225 us, 1.09 PFLOP/s), where items are ten tiles long and each begins and ends with the tensor cores idle.  Between
+// them stands the chain S, softmax, P, O += P V of a stage, which the other stage covers but for its ends: the
+// softmax warps issue in about 60 % of the cycles.  Rows of 128 with a thread for half of one, so that a maximum or a sum is one
+// exchange of two threads; with 16 lanes a row (fragments as mma.sync has them) fewer exponentials
+// wait for tensor memory, but the reductions' shuffles cost more (1,825 against 1,730 us of B1 T65536 w4096 then).
 //
 // Rows of other sequences: their keys are masked; their values, which enter the product as 0 times
 // whatever they hold, are overwritten with zeros in shared memory in a sequence's last tile.

@@ -519,7 +519,8 @@ int dr_window_attn_fwd(const dr_attn_desc *desc, const void *q, const void *k, c
 /*
  * Gradients of <d_out, out> from the forward's inputs, its results out and lse, and d_out [B, T, Hq, d]
  * (contiguous).  dq, dk, dv: rows dq_stride, dk_stride, dv_stride apart (written); they meet
- * neither each other nor an input.  Results do not depend on the order in which the GPU runs its blocks.
+ * neither each other nor an input.  fp32 rows: weights and delta_i are summed anew, so out and lse may come from
+ * a forward with other roundings.  Results do not depend on the order in which the GPU runs its blocks.
  * A token that sees itself alone has dq = 0 up to the rounding of d_out.out.
  * Workspace rules as for dr_chunk_fwd; its size depends only on the descriptor.
  */
@@ -545,8 +546,8 @@ int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const void *k, c
  *   q_out        [n_tok, Hq, d], rows q_out_stride apart (written); may be q itself
  * start[n] < 0: a slot of the batch without a sequence; its rows and rows of no sequence are not
  * written anywhere (q_out: zeroed with zero_rest).  Keys and values of tokens whose page is not there,
- * or behind max_pages pages, are dropped.  Two rows of one call for the same slot: one of them
- * stays.  Written buffers meet no other one (DR_ERR_INVALID).
+ * or behind max_pages pages, are dropped.  Rows of one call for the same slot (a page in two
+ * sequences' tables): every value there is one of theirs.  Written buffers meet no other one (DR_ERR_INVALID).
  * Returns DR_OK, DR_ERR_INVALID, DR_ERR_UNSUPPORTED or DR_ERR_CUDA.
  */
 typedef struct {

@@ -329,6 +329,55 @@ def test_streams_and_graphs(dr, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_first_tokens_with_most_of_the_weight(dr, d):
+    """A row whose weight is nearly all one key's has score gradients that are differences of nearly equal numbers; that they
+    add up to zero over the row has to hold for those that the kernel forms, whatever the roundings of out and lse (here 8 u at
+    random, as of a forward with other sums), or dq is off by the key's size.  fp32, u = 2^-24, roundings at random: a product do.v is off by 4 u
+    sqrt(d) (sums of 16 channels of size 4, 8 of them), a weight by 8 u of it; moving score gradient j by e with the sum
+    kept zero moves dq by scale e (k_j - sum p k).  The sum over the keys and the result: 4 u of the terms' norm and of dq.  The
+    bound is the 2-norm of these over all elements, times 2 for what 73 rows may deviate from the mean."""
+    u, scale, cu, sinks = 2.0 ** -24, d ** -0.5, [0, 1, 9, 20, 31, 60, 73], 8
+    q, k, v, do = make(1, 73, 6, 3, d, "f32", seed=13)
+    lean = torch.randn((3, d), generator=torch.Generator().manual_seed(14))
+    lean = lean / lean.norm(dim=1, keepdim=True) * d ** 0.25
+    q = q + lean.repeat_interleave(2, 0)
+    for lo in cu[:-1]:
+        for t in range(lo, min(lo + 4, 73)):
+            k[:, t] += 3.0 * lean
+    R, _ = reference(q, k, v, 0, sinks, scale, False, cu, do)
+    g = torch.Generator().manual_seed(15)
+    out, lse = (R[n] * (1 + 8 * u * torch.randn(R[n].shape, generator=g, dtype=torch.float64)) for n in ("out", "lse"))
+    c = [x.cuda() for x in (q, k, v, out.float(), lse.float(), do)]
+    dq, _, _ = dr.window_attn_bwd(*c, sinks=sinks, cu_seqlens=torch.tensor(cu).cuda())
+    bound = 0.0
+    for lo, hi in zip(cu[:-1], cu[1:]):
+        for h in range(6):
+            Q, K, V, D = (x[0, lo:hi, i].double() for x, i in ((q, h), (k, h // 2), (v, h // 2), (do, h)))
+            s = (scale * Q @ K.T).masked_fill(~visible(hi - lo, 0, sinks), -math.inf)
+            p = torch.softmax(s, 1)
+            dp = D @ V.T
+            ds = p * (dp - (p * dp).sum(1, keepdim=True))
+            e = 8 * u * ds.abs() + 4 * u * d ** 0.5 * p
+            apart = K[None] - (p @ K)[:, None]                      # [i, j, channel]
+            terms = (e[:, :, None] * apart) ** 2 + (4 * u * ds[:, :, None] * K[None]) ** 2
+            bound += scale ** 2 * terms.sum().item()
+    bound = 2 * (bound + (4 * u * R["dq"].norm().item()) ** 2) ** 0.5
+    off = (dq.double().cpu() - R["dq"]).norm().item()
+    assert off <= bound, f"{off / bound:.2f} of the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sequences_without_tokens(dr, dtype):
+    q, k, v, do = make(1, 40, 2, 1, 64, dtype, seed=3)
+    for cu in ([0, 0, 0], [40, 40], [17] * 300):
+        got = run(dr, q, k, v, do, 9, 2, cu=cu)
+        assert all((x == 0).all() for x in got.values())
+    both(dr, 1, 40, 2, 1, 64, 9, 2, dtype, seed=3)      # and the next call is as ever
+
+
+@pytest.mark.gpu
 def test_no_tokens(dr):
     x = torch.empty((2, 0, 2, 64), device="cuda")
     out, lse = dr.window_attn_fwd(x, x, x)
@@ -623,6 +672,26 @@ def test_append_rows_of_no_sequence_may_hold_anything(dr, dtype):
     pages = torch.tensor([[0], [1], [2], [1]], dtype=torch.int32).cuda()
     out = dr.kv_append(q, k, v, dr.rope_table(64), kc, vc, pages, torch.tensor([-1, -2, -1, -9]).cuda(), eps=0.0)
     assert (out == 0).all() and (kc == 1).all() and (vc == 1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_where_positions_end(dr, dtype):
+    dt = DT[dtype]
+    q, k, v = (torch.randn((7, h, 64), device="cuda").to(dt) for h in (2, 1, 1))
+    kc, vc = (torch.ones((2, 1, 16, 64), dtype=dt, device="cuda") for _ in range(2))
+    pages = torch.tensor([[0], [1]], dtype=torch.int32).cuda()
+    out = torch.full_like(q, 7.0)
+    dr.kv_append(q, k, v, dr.rope_table(64), kc, vc, pages, torch.tensor([2 ** 63 - 2, -2 ** 63]).cuda(),
+                 cu_seqlens=torch.tensor([0, 4, 7]).cuda(), q_out=out)
+    assert (kc == 1).all() and (vc == 1).all()
+    assert torch.isfinite(out[:2]).all() and not (out[:2] == 7).any() and (out[2:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_many_heads_of_many_sequences(dr, dtype):
+    append_case(dr, [1] * 300, [5 * n - 3 for n in range(300)], 70, 10, 64, 32, 16, dtype, seed=6, fused=True)
 
 
 @pytest.mark.gpu
