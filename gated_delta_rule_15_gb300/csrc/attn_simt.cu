@@ -1,19 +1,20 @@
 // attn_simt.cu -- window attention on the CUDA cores (fp32 rows): forward, gradients.  The
 // mathematics: attn.h; the blocks of dk and dv: attn_sinks.cuh.
 //
-// Tiles of 16 R rows (queries; of dk, dv keys) by 64 others, 256 threads as 16 x 16: a thread holds R x 4 scores (rows
-// R ty + r, others tx + 16 c) and R rows x d / 16 columns of what is summed.  Products run over rows in
-// shared memory as float4 of both operands and two FMAs an instruction (R = 4: 32 of them to 8 loads); the
-// row stride of d + 4 floats keeps the 16 rows of a load on different banks.  What is summed over tiles is first summed
-// within one, so that sums of a thousand terms are less off than one chain of them would be.
-// The 64 others come by asynchronous copies a tile ahead.  A query's keys: first the sinks in front of its tile's window, then the
-// window, with the running maximum and sum of the softmax in registers.
-// R = 4, or 1 where tiles of 64 rows would leave more than half of the SMs without one.  Measured with R = 1 and 4, by the
-// number of tiles of 64: forward 8 (T256 H2 d64 w64) 10.3 and 18.5 us, 32 (T512 H4 d128) 51 and 74, 80 (T300 H16 d64 w64) 14.3 and
-// 16.4, 102 (T1037 H6 d64 w200) 39 and 31, 128 (T2048 H4 d128) 414 and 275; dq 32 35 us less, 80 18 and 102 30 us more; dk, dv 51 25
-// us less, 64 (B2 T1024 H8/2) 8 us less, 128 (T4096 H2 d64 w256) 40 us more.
-// What bounds it: issue and shared memory (R = 4: 12 of its cycles to 16 of FMAs; R = 1: 9 to 4), and
-// for the few blocks of small problems the longest one's tiles, one behind another.
+// A block takes a tile of 64 or 16 rows (queries; of dk, dv keys) and 64 others at a time, with 256 threads: Across and Patches below say who
+// has which scores and sums.  Products run over rows in shared memory as float4 of both operands and two FMAs an
+// instruction; the row stride of d + 4 floats keeps the rows of a load on different banks.  What is summed
+// over tiles is first summed within one, so that sums of a thousand terms are less off than one chain of them would be.
+// The 64 others come by asynchronous copies a tile ahead.  A query's keys: first the sinks in front of its tile's window, then
+// the window, with the running maximum and sum of the softmax in registers.
+//
+// Tiles of 16 rows where those of 64 would leave more than half of the SMs without one.  Measured with 16 and 64, by the
+// number of tiles of 64: forward 8 (T256 H2 d64 w64) 10.3 and 18.5 us, 32 (T512 H4 d128) 51 and 74, 80 (T300 H16 d64 w64) 14.3
+// and 16.4, 102 (T1037 H6 d64 w200) 39 and 31, 128 (T2048 H4 d128) 414 and 275; all of the backward, dq's tiles: 32 (T512 H4 d128) 119 and
+// 182, 80 (T300 H16/4) 55 and 57, 102 (T1037 H6/3) 105 and 99; dk's and dv's: 20 (T300 H16/4) 57 and 94, 51 (T1037 H6/3) 99 and 150, 64 (B2
+// T1024 H8/2) 158 and 211, 128 (B4 T512 H4 d128 w256) 172 and 156.
+// What bounds it: T1037 H6/3 d64 w200, 0.73 GFLOP, 99 us where the FMA rate would allow 10: 102 and 210 blocks of four to
+// six tiles one behind another, 8 warps an SM whose FMAs, loads from shared memory and barriers wait for one another.
 #include "../../include/dr.h"
 #include "attn.h"
 #include "attn_sinks.cuh"
@@ -44,30 +45,62 @@ __device__ __forceinline__ void fetch(float *dst, const void *any, At at) {
     }
 }
 
-// acc[r][c] = sum over d of A[R ty + r] B[tx + 16 c], in sums of 8 of the even and 8 of the odd channels (a score's error is
-// its weight's)
+// Which scores and sums a thread has, of a block's rows by 64 others.  Across: 16 x 16 threads, a row's 64 scores in one warp.
 template <int D, int R>
-__device__ __forceinline__ void rows_by_rows(float (&acc)[R][4], const float *A, const float *B, int ty, int tx) {
-    constexpr int S = row_floats<D>();
-    float2 sum[R][4];
+struct Across {
+    static constexpr int ROWS = 16 * R, NR = R, NC = 4, NU = D / 64;      // rows, scores a row, float4 columns a row
+    static constexpr int LANES = 16;                                      // neighbours with the same rows
+    static constexpr bool ALONE = true;                                   // no other warp needs a row's scores
+    static constexpr int PARTS = 1;                                       // threads that each sum over a part of the 64
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    __device__ __forceinline__ int lane() const { return tx; }
+    __device__ __forceinline__ int row(int r) const { return R * ty + r; }
+    __device__ __forceinline__ int other(int c) const { return tx + 16 * c; }
+    __device__ __forceinline__ int col(int u) const { return 64 * u + 4 * tx; }
+    __device__ __forceinline__ int part() const { return 0; }
+    __device__ __forceinline__ int group() const { return 0; }
+};
+// Patches: 16 rows; a warp takes 8 rows by 16 others, and by 32 columns of what is summed (d = 64: over half of the
+// others), so that a load's 8 rows, or columns, are all different: shared memory is busy for 32 cycles where Across<D, 1>
+// takes 72 (the backward of T1037 H6/3 d64 100 us, 125 with that for dk and dv).
+template <int D>
+struct Patches {
+    static constexpr int ROWS = 16, NR = 2, NC = 2, NU = 1, LANES = 8;
+    static constexpr bool ALONE = false;
+    static constexpr int PARTS = 128 / D;
+    const int w = threadIdx.x / 32, lr = threadIdx.x / 8 % 4, lc = threadIdx.x % 8;
+    __device__ __forceinline__ int lane() const { return lc; }
+    __device__ __forceinline__ int row(int r) const { return 8 * (w & 1) + lr + 4 * r; }
+    __device__ __forceinline__ int other(int c) const { return 16 * (w >> 1) + lc + 8 * c; }
+    __device__ __forceinline__ int col(int) const { return 32 * ((w >> 1) % (D / 32)) + 4 * lc; }
+    __device__ __forceinline__ int part() const { return (w >> 1) / (D / 32); }
+    __device__ __forceinline__ int group() const { return w >> 1; }       // of the four with the same rows
+};
+
+// acc[r][c] = sum over d of A[row r] B[other c], in sums of 8 of the even and 8 of the odd channels (a score's error is
+// its weight's)
+template <int D, class M>
+__device__ __forceinline__ void rows_by_rows(float (&acc)[M::NR][M::NC], const float *A, const float *B, const M &m) {
+    constexpr int S = row_floats<D>(), R = M::NR, C = M::NC;
+    float2 sum[R][C];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum[r][c] = make_float2(0.f, 0.f);
+        for (int c = 0; c < C; ++c) sum[r][c] = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int k0 = 0; k0 < D; k0 += 16) {
-        float2 x[R][4];
+        float2 x[R][C];
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
-            float4 a[R], b[4];
+            float4 a[R], b[C];
 #pragma unroll
-            for (int r = 0; r < R; ++r) a[r] = load4(A + (R * ty + r) * S + k0 + k);
+            for (int r = 0; r < R; ++r) a[r] = load4(A + m.row(r) * S + k0 + k);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = load4(B + (tx + 16 * c) * S + k0 + k);
+            for (int c = 0; c < C; ++c) b[c] = load4(B + m.other(c) * S + k0 + k);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < C; ++c) {
                     const float2 a0 = make_float2(a[r].x, a[r].y), b0 = make_float2(b[c].x, b[c].y);
                     x[r][c] = k == 0 ? mul2(a0, b0) : fma2(a0, b0, x[r][c]);
                     x[r][c] = fma2(make_float2(a[r].z, a[r].w), make_float2(b[c].z, b[c].w), x[r][c]);
@@ -76,36 +109,44 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[R][4], const float *A,
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[r][c] = add2(sum[r][c], x[r][c]);
+            for (int c = 0; c < C; ++c) sum[r][c] = add2(sum[r][c], x[r][c]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = sum[r][c].x + sum[r][c].y;
+        for (int c = 0; c < C; ++c) acc[r][c] = sum[r][c].x + sum[r][c].y;
 }
 
-// acc[r][2 u + h] += sum over `n` k (a multiple of 4) of P[R ty + r][k] X[k][64 u + 4 tx + 2 h, + 1]
-template <int D, int R>
-__device__ __forceinline__ void rows_by_cols(float2 (&acc)[R][D / 32], const float *P, const float *X, int n, int ty, int tx) {
-    constexpr int S = row_floats<D>(), U = D / 64;
-    float2 sum[R][D / 32];
+template <class M> using Sums = float2[M::NR][2 * M::NU];     // of a thread: its rows' columns col(u) .. col(u) + 3
+
+template <class M>
+__device__ __forceinline__ void clear(Sums<M> &x) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < M::NR; ++r)
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) sum[r][u] = make_float2(0.f, 0.f);
+        for (int u = 0; u < 2 * M::NU; ++u) x[r][u] = make_float2(0.f, 0.f);
+}
+
+// acc[r][columns] += sum over `n` k (a multiple of 4) of P[row r][k] X[k][columns]
+template <int D, class M>
+__device__ __forceinline__ void rows_by_cols(Sums<M> &acc, const float *P, const float *X, int n, const M &m) {
+    constexpr int S = row_floats<D>(), R = M::NR, U = M::NU, PART = kTile / M::PARTS;
+    Sums<M> sum;
+    clear<M>(sum);
+    const int k0 = PART * m.part(), k1 = min(n, k0 + PART);
 #pragma unroll 2
-    for (int k = 0; k < n; k += 4) {
+    for (int k = k0; k < k1; k += 4) {
         float p[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float4 x = load4(P + (R * ty + r) * kPs + k);
+            const float4 x = load4(P + m.row(r) * kPs + k);
             p[r][0] = x.x; p[r][1] = x.y; p[r][2] = x.z; p[r][3] = x.w;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float4 x = load4(X + (k + e) * S + 64 * u + 4 * tx);
+                const float4 x = load4(X + (k + e) * S + m.col(u));
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     sum[r][2 * u] = fma2(make_float2(p[r][e], p[r][e]), make_float2(x.x, x.y), sum[r][2 * u]);
@@ -116,28 +157,68 @@ __device__ __forceinline__ void rows_by_cols(float2 (&acc)[R][D / 32], const flo
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) acc[r][u] = add2(acc[r][u], sum[r][u]);
+        for (int u = 0; u < 2 * U; ++u) acc[r][u] = add2(acc[r][u], sum[r][u]);
 }
 
-// A thread's scores where the 16 threads of its rows, which are in its warp, read them.
-template <int R>
-__device__ __forceinline__ void put_scores(float *P, const float (&s)[R][4], int ty, int tx) {
-    __syncwarp();
+// The parts' sums added up in those of part 0, by way of shared memory (a block's rows, no longer read).
+template <int D, class M>
+__device__ __forceinline__ void join_parts(Sums<M> &x, float *sm, const M &m) {
+    if constexpr (M::PARTS == 2) {
+        __syncthreads();
+        if (m.part())
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+            for (int r = 0; r < M::NR; ++r) store4(sm + m.row(r) * row_floats<D>() + m.col(0), make_float4(x[r][0].x, x[r][0].y, x[r][1].x, x[r][1].y));
+        __syncthreads();
+        if (!m.part())
 #pragma unroll
-        for (int c = 0; c < 4; ++c) P[(R * ty + r) * kPs + tx + 16 * c] = s[r][c];
-    __syncwarp();
+            for (int r = 0; r < M::NR; ++r) {
+                const float4 y = load4(sm + m.row(r) * row_floats<D>() + m.col(0));
+                x[r][0] = add2(x[r][0], make_float2(y.x, y.y));
+                x[r][1] = add2(x[r][1], make_float2(y.z, y.w));
+            }
+    }
 }
 
+// A thread's scores where the others of its rows read them.
+template <class M>
+__device__ __forceinline__ void put_scores(float *P, const float (&s)[M::NR][M::NC], const M &m) {
+#pragma unroll
+    for (int r = 0; r < M::NR; ++r)
+#pragma unroll
+        for (int c = 0; c < M::NC; ++c) P[m.row(r) * kPs + m.other(c)] = s[r][c];
+}
+// x += P X, y += P2 Y with scores s and s2.
+template <int D, class M>
+__device__ __forceinline__ void two_sums(Sums<M> &x, const float (&s)[M::NR][M::NC], const float *X, Sums<M> &y,
+                                         const float (&s2)[M::NR][M::NC], const float *Y, float *P, int n, const M &m) {
+    if constexpr (M::ALONE) {
+        __syncwarp();
+        put_scores(P, s, m);
+        __syncwarp();
+        rows_by_cols<D>(x, P, X, n, m);
+        __syncwarp();
+        put_scores(P, s2, m);
+        __syncwarp();
+        rows_by_cols<D>(y, P, Y, n, m);
+    } else {                                  // (the tile's barrier is behind the last ones' reads)
+        put_scores(P, s, m);
+        put_scores(P + M::ROWS * kPs, s2, m);
+        __syncthreads();
+        rows_by_cols<D>(x, P, X, n, m);
+        rows_by_cols<D>(y, P + M::ROWS * kPs, Y, n, m);
+    }
+}
+
+// Over the neighbours with the same rows.
+template <class M>
+__device__ __forceinline__ float sum_lanes(float x) {
+#pragma unroll
+    for (int o = M::LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
 __device__ __forceinline__ float max16(float x) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
@@ -157,15 +238,14 @@ struct Keys {
     __device__ __forceinline__ int at(int v) const { return v < sinks ? v : near0 + v - sinks; }
 };
 
-template <int D, int R>
-__device__ __forceinline__ void put_rows(float *dst, int64_t stride, int n, const float2 (&x)[R][D / 32], float f, int ty, int tx) {
+template <class M>
+__device__ __forceinline__ void put_rows(float *dst, int64_t stride, int n, const Sums<M> &x, float f, const M &m) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (R * ty + r >= n) continue;
+    for (int r = 0; r < M::NR; ++r) {
+        if (m.row(r) >= n || m.part()) continue;
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            store4(dst + (int64_t)(R * ty + r) * stride + 64 * u + 4 * tx,
-                   make_float4(f * x[r][2 * u].x, f * x[r][2 * u].y, f * x[r][2 * u + 1].x, f * x[r][2 * u + 1].y));
+        for (int u = 0; u < M::NU; ++u)
+            store4(dst + m.row(r) * stride + m.col(u), make_float4(f * x[r][2 * u].x, f * x[r][2 * u].y, f * x[r][2 * u + 1].x, f * x[r][2 * u + 1].y));
     }
 }
 
@@ -183,10 +263,12 @@ __device__ __forceinline__ bool query_tile(const AttnProblem &p, int &h, int &hk
 
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProblem p) {
-    constexpr int S = row_floats<D>(), ROWS = 16 * R;
+    constexpr int S = row_floats<D>(), ROWS = Across<D, R>::ROWS;
     extern __shared__ float sm[];
     float *Q = sm, *KV = Q + ROWS * S, *P = KV + 4 * kTile * S;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    using M = Across<D, R>;
+    static_assert(M::ALONE, "the maxima are a warp's own");
+    const M mine;
     int64_t lo;
     int h, hk, len, q0;
     if (!query_tile<ROWS>(p, h, hk, lo, len, q0)) return;
@@ -202,13 +284,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
     fetch_keys(0);
     umma::cp_async_commit();
     float m[R], l[R];
-    float2 o[R][D / 32];
+    Sums<M> o;
+    clear<M>(o);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) o[r][c] = make_float2(0.f, 0.f);
     }
     const int tiles = (keys.total + kTile - 1) / kTile;
     for (int t = 0; t < tiles; ++t) {
@@ -218,14 +299,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
         umma::cp_async_commit();
         const float *K = KV + (t & 1) * 2 * kTile * S;
         float s[R][4];
-        rows_by_rows<D, R>(s, Q, K, ty, tx);
+        rows_by_rows<D>(s, Q, K, mine);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int i = q0 + R * ty + r;
+            const int i = q0 + mine.row(r);
             float top = m[r];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int at = kTile * t + tx + 16 * c;
+                const int at = kTile * t + mine.other(c);
                 s[r][c] = at < keys.total && sees(p, i, keys.at(at)) ? p.scale * s[r][c] : -INFINITY;
                 top = fmaxf(top, s[r][c]);
             }
@@ -242,18 +323,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) o[r][c] = mul2(o[r][c], make_float2(turn, turn));
         }
-        put_scores<R>(P, s, ty, tx);
-        rows_by_cols<D, R>(o, P, K + kTile * S, min(kTile, (keys.total - kTile * t + 3) & ~3), ty, tx);
+        __syncwarp();
+        put_scores(P, s, mine);
+        __syncwarp();
+        rows_by_cols<D>(o, P, K + kTile * S, min(kTile, (keys.total - kTile * t + 3) & ~3), mine);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float sum = sum16(l[r]), inv = 1.f / sum;
-        const int i = q0 + R * ty + r;
+        const float sum = sum_lanes<M>(l[r]), inv = 1.f / sum;
+        const int i = q0 + mine.row(r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) o[r][c] = mul2(o[r][c], make_float2(inv, inv));
-        if (i < len && tx == 0) p.lse[(lo + i) * p.Hq + h] = m[r] + logf(sum);
+        if (i < len && mine.lane() == 0) p.lse[(lo + i) * p.Hq + h] = m[r] + logf(sum);
     }
-    put_rows<D, R>((float *)p.out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, len - q0, o, 1.f, ty, tx);
+    put_rows((float *)p.out + ((lo + q0) * p.Hq + h) * D, (int64_t)p.Hq * D, len - q0, o, 1.f, mine);
 }
 
 // dq of a query tile, and of its rows l and delta.  lse and out are rounded, and results of other sums than this kernel's:
@@ -263,12 +346,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const AttnProbl
 //     dq_i = scale (sum_j x_ij k_j - e sum_j w_ij k_j) / l,
 // a fourth product to three (keys with a common direction of 3 times their spread, sequences of 10 tokens: dq off by 2.5e-6
 // without, where all in one arithmetic is off by 1.1e-6).
-template <int D, int R>
+template <int D, class M>
 __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProblem p) {
-    constexpr int S = row_floats<D>(), ROWS = 16 * R;
+    constexpr int S = row_floats<D>(), ROWS = M::ROWS, R = M::NR, C = M::NC;
     extern __shared__ float sm[];
     float *Q = sm, *O = Q + ROWS * S, *KV = O + ROWS * S, *P = KV + 4 * kTile * S;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const M mine;
     int64_t lo;
     int h, hk, len, q0;
     let_next_start();
@@ -288,24 +371,23 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
     fetch_keys(0);
     umma::cp_async_commit();
     float delta[R], lse[R], l[R], e[R];
-    float2 dq[R][D / 32], wk[R][D / 32];
+    Sums<M> dq, wk;
+    clear<M>(dq);
+    clear<M>(wk);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int i = R * ty + r;
+        const int i = mine.row(r);
         float x = 0.f;
         if (i < rows) {
 #pragma unroll
-            for (int u = 0; u < D / 64; ++u) {
-                const float4 a = load4((const float *)p.out + at0 + i * step + 64 * u + 4 * tx),
-                             b = load4((const float *)p.d_out + at0 + i * step + 64 * u + 4 * tx);
+            for (int c = 4 * mine.lane(); c < D; c += 4 * M::LANES) {
+                const float4 a = load4((const float *)p.out + at0 + i * step + c), b = load4((const float *)p.d_out + at0 + i * step + c);
                 x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
             }
         }
-        delta[r] = sum16(x);
+        delta[r] = sum_lanes<M>(x);
         lse[r] = i < rows ? p.lse[(lo + q0 + i) * p.Hq + h] : 0.f;
         l[r] = e[r] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) dq[r][c] = wk[r][c] = make_float2(0.f, 0.f);
     }
     const int tiles = (keys.total + kTile - 1) / kTile;
     for (int t = 0; t < tiles; ++t) {
@@ -314,16 +396,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
         if (t + 1 < tiles) fetch_keys(t + 1);
         umma::cp_async_commit();
         const float *K = KV + (t & 1) * 2 * kTile * S;
-        float s[R][4], dp[R][4];
-        rows_by_rows<D, R>(s, Q, K, ty, tx);
-        rows_by_rows<D, R>(dp, O, K + kTile * S, ty, tx);
+        float s[R][C], dp[R][C];
+        rows_by_rows<D>(s, Q, K, mine);
+        rows_by_rows<D>(dp, O, K + kTile * S, mine);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float sw = 0.f, sx = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int at = kTile * t + tx + 16 * c;
-                const bool in = at < keys.total && sees(p, q0 + R * ty + r, keys.at(at));
+            for (int c = 0; c < C; ++c) {
+                const int at = kTile * t + mine.other(c);
+                const bool in = at < keys.total && sees(p, q0 + mine.row(r), keys.at(at));
                 s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -lse[r])) : 0.f;
                 dp[r][c] = in ? s[r][c] * (dp[r][c] - delta[r]) : 0.f;
                 sw += s[r][c];
@@ -332,34 +414,52 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const AttnProble
             l[r] += sw;
             e[r] += sx;
         }
-        const int n = min(kTile, (keys.total - kTile * t + 3) & ~3);
-        put_scores<R>(P, s, ty, tx);
-        rows_by_cols<D, R>(wk, P, K, n, ty, tx);
-        put_scores<R>(P, dp, ty, tx);
-        rows_by_cols<D, R>(dq, P, K, n, ty, tx);
+        two_sums<D>(wk, s, K, dq, dp, K, P, min(kTile, (keys.total - kTile * t + 3) & ~3), mine);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int i = R * ty + r;
-        const float inv = 1.f / sum16(l[r]), x = sum16(e[r]) * inv;
-        if (tx == 0 && i < rows) {
+        l[r] = sum_lanes<M>(l[r]);
+        e[r] = sum_lanes<M>(e[r]);
+    }
+    if constexpr (!M::ALONE) {                // over the warps with the same rows
+        __syncthreads();
+        float2 *all = reinterpret_cast<float2 *>(P);
+        if (mine.lane() == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r) all[4 * mine.row(r) + mine.group()] = make_float2(l[r], e[r]);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float2 *a = all + 4 * mine.row(r);
+            l[r] = (a[0].x + a[1].x) + (a[2].x + a[3].x);
+            e[r] = (a[0].y + a[1].y) + (a[2].y + a[3].y);
+        }
+    }
+    join_parts<D>(dq, KV, mine);
+    join_parts<D>(wk, KV, mine);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = mine.row(r);
+        const float inv = 1.f / l[r], x = e[r] * inv;
+        if (mine.lane() == 0 && mine.group() == 0 && i < rows) {
             const int64_t at = h * p.seqs.total + lo + q0 + i;
             p.delta[at] = delta[r] + x;
             p.inv_l[at] = inv;
         }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) dq[r][c] = mul2(fma2(make_float2(-x, -x), wk[r][c], dq[r][c]), make_float2(inv, inv));
+        for (int c = 0; c < 2 * M::NU; ++c) dq[r][c] = mul2(fma2(make_float2(-x, -x), wk[r][c], dq[r][c]), make_float2(inv, inv));
     }
-    put_rows<D, R>((float *)p.dq + (lo + q0) * p.dqs + h * D, p.dqs, rows, dq, p.scale, ty, tx);
+    put_rows((float *)p.dq + (lo + q0) * p.dqs + h * D, p.dqs, rows, dq, p.scale, mine);
 }
 
 // dk and dv of a key tile, over the block's queries and all heads that share the keys.
-template <int D, int R>
+template <int D, class M>
 __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProblem p, const attn::SinkPlan plan) {
-    constexpr int S = row_floats<D>(), ROWS = 16 * R;
+    constexpr int S = row_floats<D>(), ROWS = M::ROWS, R = M::NR, C = M::NC;
     extern __shared__ float sm[];
-    float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + ROWS * kPs;   // [2][lse, delta, 1 / l][64]
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, g = p.Hq / p.Hk;
+    float *K = sm, *V = K + ROWS * S, *QO = V + ROWS * S, *P = QO + 4 * kTile * S, *stat = P + (M::ALONE ? 1 : 2) * ROWS * kPs;   // [2][lse, delta, 1 / l][64]
+    const M mine;
+    const int g = p.Hq / p.Hk;
     attn::KeyBlock kb;
     let_next_start();
     if (!kb.find(p, plan, blockIdx.x)) {
@@ -387,11 +487,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
     wait_for_last();       // delta, 1 / l
     fetch_queries(0);
     umma::cp_async_commit();
-    float2 dk[R][D / 32], dv[R][D / 32];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) dk[r][c] = dv[r][c] = make_float2(0.f, 0.f);
+    Sums<M> dk, dv;
+    clear<M>(dk);
+    clear<M>(dv);
     for (int t = 0; t < tiles; ++t) {
         umma::cp_async_wait_all();
         __syncthreads();
@@ -399,37 +497,36 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const AttnProbl
         umma::cp_async_commit();
         const int q0 = kb.qa + t % nt * kTile, n = min(kTile, (kb.qb - q0 + 3) & ~3);
         const float *Q = QO + (t & 1) * 2 * kTile * S, *O = Q + kTile * S, *st = stat + (t & 1) * 3 * kTile;
-        float s[R][4], dp[R][4];
-        rows_by_rows<D, R>(s, K, Q, ty, tx);
-        rows_by_rows<D, R>(dp, V, O, ty, tx);
+        float s[R][C], dp[R][C];
+        rows_by_rows<D>(s, K, Q, mine);
+        rows_by_rows<D>(dp, V, O, mine);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int qi = tx + 16 * c, j = k0 + R * ty + r;
+            for (int c = 0; c < C; ++c) {
+                const int qi = mine.other(c), j = k0 + mine.row(r);
                 const bool in = q0 + qi < kb.qb && sees(p, q0 + qi, j) && (kb.chunk < 0 || j < p.sinks);
                 s[r][c] = in ? expf(fmaf(s[r][c], p.scale, -st[qi])) * st[2 * kTile + qi] : 0.f;
                 dp[r][c] = in ? s[r][c] * (dp[r][c] - st[kTile + qi]) : 0.f;
             }
-        put_scores<R>(P, s, ty, tx);
-        rows_by_cols<D, R>(dv, P, O, n, ty, tx);
-        put_scores<R>(P, dp, ty, tx);
-        rows_by_cols<D, R>(dk, P, Q, n, ty, tx);
+        two_sums<D>(dv, s, O, dk, dp, Q, P, n, mine);
     }
+    join_parts<D>(dk, QO, mine);
+    join_parts<D>(dv, QO, mine);
     // a sink's row is a part of a sum where its queries are cut
     const int sinks = kb.cut ? min(p.sinks - k0, rows) : 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int row = R * ty + r;
+        const int row = mine.row(r);
         const bool part = row < sinks;
-        if (row >= rows || (kb.chunk >= 0 && !part)) continue;
+        if (row >= rows || (kb.chunk >= 0 && !part) || mine.part()) continue;
         float *to_k = part ? kb.sum(p, plan, k0 + row) : (float *)p.dk + (lo + k0 + row) * p.dks + hk * D;
         float *to_v = part ? to_k + D : (float *)p.dv + (lo + k0 + row) * p.dvs + hk * D;
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) {
+        for (int u = 0; u < M::NU; ++u) {
             const float2 a = mul2(dk[r][2 * u], make_float2(p.scale, p.scale)), b = mul2(dk[r][2 * u + 1], make_float2(p.scale, p.scale));
-            store4(to_k + 64 * u + 4 * tx, make_float4(a.x, a.y, b.x, b.y));
-            store4(to_v + 64 * u + 4 * tx, make_float4(dv[r][2 * u].x, dv[r][2 * u].y, dv[r][2 * u + 1].x, dv[r][2 * u + 1].y));
+            store4(to_k + mine.col(u), make_float4(a.x, a.y, b.x, b.y));
+            store4(to_v + mine.col(u), make_float4(dv[r][2 * u].x, dv[r][2 * u].y, dv[r][2 * u + 1].x, dv[r][2 * u + 1].y));
         }
     }
 }
@@ -474,9 +571,9 @@ template <int D, int R>
 int fwd(const AttnProblem &p, cudaStream_t s) {
     return launch(attn_simt_fwd_kernel<D, R>, floats<D>(1, 16 * R), attn_tile_slots(p.seqs, 16 * R) * p.Hq, s, p);
 }
-template <int D, int R>
+template <int D, class M>
 int bwd_q(const AttnProblem &p, cudaStream_t s) {
-    return launch(attn_simt_dq_kernel<D, R>, floats<D>(2, 16 * R), attn_tile_slots(p.seqs, 16 * R) * p.Hq, s, p);
+    return launch(attn_simt_dq_kernel<D, M>, floats<D>(2, M::ROWS) + (M::ALONE ? 0 : M::ROWS * kPs), attn_tile_slots(p.seqs, M::ROWS) * p.Hq, s, p);
 }
 
 int key_rows(const AttnProblem &p) { return few(p, p.Hk) ? 16 : 64; }
@@ -485,13 +582,13 @@ size_t stat_bytes(const AttnProblem &p) { return attn::round256(sizeof(float) * 
 
 template <int D>
 int bwd(const AttnProblem &p, void *workspace, cudaStream_t s) {
-    int rc = few(p, p.Hq) ? bwd_q<D, 1>(p, s) : bwd_q<D, 4>(p, s);
+    int rc = few(p, p.Hq) ? bwd_q<D, Patches<D>>(p, s) : bwd_q<D, Across<D, 4>>(p, s);
     if (rc != kOk) return rc;
     attn::SinkPlan plan;
     attn::plan_sinks(p, key_rows(p), 256, (char *)workspace + 2 * stat_bytes(p), plan);
     const int64_t blocks = attn::key_blocks(p, plan);
-    rc = plan.tile == 16 ? launch_next(attn_simt_dkv_kernel<D, 1>, floats<D>(2, 16) + 6 * kTile, blocks, s, p, plan)
-                         : launch_next(attn_simt_dkv_kernel<D, 4>, floats<D>(2, 64) + 6 * kTile, blocks, s, p, plan);
+    rc = plan.tile == 16 ? launch_next(attn_simt_dkv_kernel<D, Patches<D>>, floats<D>(2, 16) + 16 * kPs + 6 * kTile, blocks, s, p, plan)
+                         : launch_next(attn_simt_dkv_kernel<D, Across<D, 4>>, floats<D>(2, 64) + 6 * kTile, blocks, s, p, plan);
     return rc != kOk ? rc : attn::launch_sink_sum<D, float>(p, plan, s);
 }
 
