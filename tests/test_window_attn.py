@@ -715,6 +715,47 @@ def test_append_in_a_graph(dr, dtype):
     assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_behind_four_gigabytes(dr, dtype):
+    """The same pages' contents at either end of a cache of more than 2^31 values: the same bits."""
+    dt, Hk, d, page, n_pages = DT[dtype], 8, 128, 16, 132000
+    q, k, v, _ = make(1, 40, 16, Hk, d, dtype, seed=21)
+    q, k, v = (x[0].cuda() for x in (q, k, v))
+    kc, vc = (torch.empty((n_pages, Hk, page, d), dtype=dt, device="cuda") for _ in range(2))
+    table, start, cu = dr.rope_table(d), torch.tensor([0]).cuda(), torch.tensor([0, 40]).cuda()
+    got = []
+    for first in (0, n_pages - 3):
+        kc[first:first + 3] = 0
+        vc[first:first + 3] = 0
+        pages = torch.arange(first, first + 3, dtype=torch.int32).view(1, 3).cuda()
+        q1 = dr.kv_append(q, k, v, table, kc, vc, pages, start, cu_seqlens=cu)
+        out, lse = dr.window_attn_step(q1[39:], kc, vc, pages, start + 40, window=30, sinks=2, return_lse=True)
+        got.append((q1, out, lse, kc[first:first + 3].clone(), vc[first:first + 3].clone()))
+    for x, y in zip(*got):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_far_apart(dr, dtype):
+    """Rows whose last one is more than 2^32 values behind the first: the same bits as next to one another."""
+    T, apart = 1100, 1 << 22
+    q, k, v, do = (x.cuda() for x in make(1, T, 2, 1, 64, dtype, seed=22))
+    kw = dict(window=100, sinks=3)
+    out, lse = dr.window_attn_fwd(q, k, v, **kw)
+    grads = dr.window_attn_bwd(q, k, v, out, lse, do, **kw)
+    room = torch.empty(T * apart, dtype=DT[dtype], device="cuda")
+    at = lambda h, first: room.as_strided((1, T, h, 64), (T * apart, apart, 64, 1), first)
+    far = [at(h, 1024 * i) for i, h in enumerate((2, 1, 1, 2, 1, 1))]
+    for x, y in zip(far, (q, k, v)):
+        x.copy_(y)
+    out2, lse2 = dr.window_attn_fwd(*far[:3], **kw)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    for x, y in zip(grads, dr.window_attn_bwd(*far[:3], out, lse, do, grads=far[3:], **kw)):
+        assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
