@@ -13,8 +13,9 @@
 // and 16.4, 102 (T1037 H6 d64 w200) 39 and 31, 128 (T2048 H4 d128) 414 and 275; all of the backward, dq's tiles: 32 (T512 H4 d128) 119 and
 // 182, 80 (T300 H16/4) 55 and 57, 102 (T1037 H6/3) 105 and 99; dk's and dv's: 20 (T300 H16/4) 57 and 94, 51 (T1037 H6/3) 99 and 150, 64 (B2
 // T1024 H8/2) 158 and 211, 128 (B4 T512 H4 d128 w256) 172 and 156.
-// What bounds it: T1037 H6/3 d64 w200, 0.73 GFLOP, 99 us where the FMA rate would allow 10: 102 and 210 blocks of four to
-// six tiles one behind another, 8 warps an SM whose FMAs, loads from shared memory and barriers wait for one another.
+// What bounds it: loads from shared memory, 16 bytes a lane take as long as two paired FMAs of every scheduler, and Across<D, 4> has 8 for 32
+// (backward of B4 T2048 H8/2 d128 w512: 1,974 us, 30 TFLOP/s of some 77).  Small problems: the longest block's
+// tiles, one behind another (T1037 H6/3 d64 w200, 0.73 GFLOP: 99 us, 102 and 210 blocks of four to six tiles).
 #include "../../include/dr.h"
 #include "attn.h"
 #include "attn_sinks.cuh"
@@ -61,8 +62,9 @@ struct Across {
     __device__ __forceinline__ int group() const { return 0; }
 };
 // Patches: 16 rows; a warp takes 8 rows by 16 others, and by 32 columns of what is summed (d = 64: over half of the
-// others), so that a load's 8 rows, or columns, are all different: shared memory is busy for 32 cycles where Across<D, 1>
-// takes 72 (the backward of T1037 H6/3 d64 100 us, 125 with that for dk and dv).
+// others).  A thread loads 4 times for 8 paired FMAs of a product over rows and 6 times for 16 of one over columns, where Across<D, 1> loads
+// 5 times for 8, and a load's 8 rows, or columns, are all different (the backward of T1037 H6/3 d64 100 us, 125 with that for
+// dk and dv).
 template <int D>
 struct Patches {
     static constexpr int ROWS = 16, NR = 2, NC = 2, NU = 1, LANES = 8;
