@@ -844,6 +844,16 @@ def _contiguous_at(t, shape, dtype, dev, what):
         raise ValueError(f"{what} must be {dtype} {list(shape)}")
 
 
+def _in_one_piece(t, shape, dtype, dev, what):
+    """t, or, where it is a view of something else (the front of padded results, a gradient that was
+    expanded or transposed), its values in one piece."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
 def _packed_count(cu_seqlens, B, dev):
     """N of packed sequences."""
     if cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous():
@@ -907,18 +917,18 @@ def window_attn_fwd(q, k, v, *, window: int = 0, sinks: int = 0, scale=None, cu_
 def window_attn_bwd(q, k, v, out, lse, d_out, *, window: int = 0, sinks: int = 0, scale=None,
                     cu_seqlens=None, grads=None, workspace=None, stream=None):
     """Gradients of <d_out, out> of window_attn_fwd from its inputs and results
-    (dr_window_attn_bwd): (dq, dk, dv) in q's dtype.  ``grads``: three buffers to write into (strided
+    (dr_window_attn_bwd): (dq, dk, dv) in q's dtype.  out, lse and d_out may be views of any strides; those
+    that are not contiguous are copied first.  ``grads``: three buffers to write into (strided
     rows, as parts of a fused gradient); their rows of no sequence are left as they are (new ones
     hold zeros there)."""
     dev = _current_device()
     desc = _attn_desc(q, k, v, cu_seqlens, window, sinks, scale, dev)
     shape, kv, dt = q.shape, k.shape, q.dtype
-    _contiguous_at(out, shape, dt, dev, "out")
-    _contiguous_at(d_out, shape, dt, dev, "d_out")
-    _contiguous_at(lse, shape[:3], torch.float32, dev, "lse")
     if workspace is not None:
         _on_one_device(workspace)
     with _stream_scope(stream):
+        out, d_out = _in_one_piece(out, shape, dt, dev, "out"), _in_one_piece(d_out, shape, dt, dev, "d_out")
+        lse = _in_one_piece(lse, shape[:3], torch.float32, dev, "lse")
         if grads is None:
             dq = torch.empty(shape, dtype=dt, device=dev)
             dk, dv = torch.empty(kv, dtype=dt, device=dev), torch.empty(kv, dtype=dt, device=dev)

@@ -228,6 +228,39 @@ def test_rows_of_a_fused_projection(dr, B, T, cu, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,cu", [(2, 130, None), (3, 1, None), (1, 300, [0, 100, 290])])
+def test_backward_takes_views(dr, B, T, cu, dtype):
+    """Results that are the front of padded ones, gradients that are transposed or expanded: the bits of
+    the contiguous call, on this stream, on another one and in a graph."""
+    q, k, v, do = (x.cuda() for x in make(B, T, 4, 2, 64, dtype, seed=12))
+    kw = dict(window=40, sinks=2, cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda())
+    out, lse = dr.window_attn_fwd(q, k, v, **kw)
+    pad = lambda x: torch.cat((x, torch.full_like(x[:, :1], float("nan")).expand(-1, 5, *x.shape[2:])), 1)[:, :T]
+    views = [(pad(out), pad(lse), do.transpose(1, 2).contiguous().transpose(1, 2), do),
+             (out, lse.transpose(1, 2).contiguous().transpose(1, 2), do[:1, :1, :, :1].expand(B, T, 4, 64),
+              do[:1, :1, :, :1].expand(B, T, 4, 64).contiguous())]
+    side = torch.cuda.Stream()
+    for o, l, d, d_whole in views:
+        want = dr.window_attn_bwd(q, k, v, out, lse, d_whole, **kw)
+        torch.cuda.synchronize()
+        got = [dr.window_attn_bwd(q, k, v, o, l, d, **kw), dr.window_attn_bwd(q, k, v, o, l, d, stream=side, **kw)]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(dr.window_attn_bwd(q, k, v, o, l, d, **kw))
+        graph.replay()
+        torch.cuda.synchronize()
+        for g in got:
+            for x, y in zip(want, g):
+                assert torch.equal(x, y)
+    with pytest.raises(ValueError):
+        dr.window_attn_bwd(q, k, v, out, lse.transpose(1, 2), do, **kw)
+    with pytest.raises(ValueError):
+        dr.window_attn_bwd(q, k, v, out, lse, do.cpu(), **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("size,scale", [(20.0, None), (1.0, 2.0), (1e-3, None), (0.0, None), (1.0, 1e-4)])
 def test_sharp_and_flat_weights(dr, size, scale, dtype):
     both(dr, 1, 300, 2, 1, 128, 90, 2, dtype, seed=11, size=size, scale=scale)
