@@ -438,9 +438,8 @@ def run(state):
         into = {} if st["into"] is None else dict(out=st["into"][0], lse=st["into"][1])
         out, lse = dr.window_attn_fwd(st["q"], st["k"], st["v"], cu_seqlens=st["cu"], **seen, **into)
         return dict(out=out, lse=lse)
-    # (the plain forward's results may be the front of padded ones; the call takes contiguous ones)
-    dq, dk, dv = dr.window_attn_bwd(st["q"], st["k"], st["v"], st["out"].contiguous(), st["lse"].contiguous(), st["do"],
-                                    cu_seqlens=st["cu"], grads=st["into"], **seen)
+    dq, dk, dv = dr.window_attn_bwd(st["q"], st["k"], st["v"], st["out"], st["lse"], st["do"], cu_seqlens=st["cu"],
+                                    grads=st["into"], **seen)
     return dict(dq=dq, dk=dk, dv=dv)
 
 
