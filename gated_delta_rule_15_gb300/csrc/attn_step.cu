@@ -90,8 +90,8 @@ struct Walk {
     Seen<G> seen;
     __device__ __forceinline__ Walk(const StepArgs &a, int64_t b0, int64_t first0, int64_t begin, int64_t end)
         : b(b0), first(first0), hu(0), lo(0), hi(0), seen(a.p, b0 < a.p.B ? a.p.lens[b0] : 0) {
-        while (b < a.p.B && first + (seen.n > 0 ? a.hus * (seen.n + kUnitCost) : 0) <= begin) {   // whole sequences in front of it
-            if (seen.n > 0) first += a.hus * (seen.n + kUnitCost);
+        while (b < a.p.B && first + length(a) <= begin) {   // whole sequences in front of it
+            first += length(a);
             ++b;
             seen = Seen<G>(a.p, b < a.p.B ? a.p.lens[b] : 0);
         }
@@ -101,6 +101,8 @@ struct Walk {
         }
         cut(begin, end);
     }
+    // of the sequence in the row of all units (units of 2^30 tokens and some tens of heads pass 31 bits)
+    __device__ __forceinline__ int64_t length(const StepArgs &a) const { return seen.n > 0 ? (int64_t)a.hus * (seen.n + kUnitCost) : 0; }
     __device__ __forceinline__ void cut(int64_t begin, int64_t end) {
         const int64_t l = begin - first - kUnitCost, h = end - first - kUnitCost;
         lo = (int)max((int64_t)0, l);

@@ -544,6 +544,31 @@ def test_step_lengths_behind_the_table(dr, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,Hk", [("f32", 16), ("bf16", 32)])
+def test_step_units_that_pass_31_bits(dr, Hk, dtype):
+    """A context of 2^30 tokens, nearly all of its pages not there: its groups of tokens times its heads are more than 2^31.  A
+    short one behind it."""
+    page, d, most = 1024, 64, 1 << 20
+    there = [0, 5, most // 2 + 1, most - 1]
+    n = len(there) * page
+    q, k, v, _ = make(2, n, Hk, Hk, d, dtype, seed=31)
+    q = q[:, 0].contiguous()
+    kc, vc = (torch.cat((x[0].view(4, page, Hk, d), x[1, :page][None])).transpose(1, 2).contiguous() for x in (k, v))
+    pages = torch.full((2, most), -1, dtype=torch.int32)
+    pages[0, there] = torch.arange(4, dtype=torch.int32)
+    pages[1, 0] = 4
+    assert Hk * (2 ** 30 // (16 if dtype == "bf16" else 8) + 1) >= 2 ** 31
+    got = dr.window_attn_step(q.cuda(), kc.cuda(), vc.cuda(), pages.cuda(), torch.tensor([1 << 30, 40]).cuda(), return_lse=True)
+    torch.cuda.synchronize()
+    assert dr.lib().dr_get_device_status(None) == 0
+    # (tokens that are not there take no part, so those that are may stand side by side)
+    R, E = step_reference(q, k, v, [n, 40], 0, 0, d ** -0.5, dtype == "bf16")
+    for name, x in zip(("out", "lse"), got):
+        worst = ((x.double().cpu() - R[name]).abs() / (E[name] + 1e-30)).max().item()
+        assert worst <= 1, f"{name}: {worst:.3f} of the bound"
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_step_in_graphs_with_one_workspace(dr, dtype):
     """Two captured steps that share a workspace, their lengths updated on the device between replays."""
