@@ -42,6 +42,7 @@ static_assert(16 * kDqSoftRegs + 8 * kDqOtherRegs <= 24 * 80 && 16 * kDkvSoftReg
 struct BwdArgs {
     AttnProblem p;
     int *status;
+    int polls;                 // of a wait, at most
     int gs, runs, tokens;      // log2 of the query heads side by side, runs of them, tokens of 128 rows
     int64_t items;             // of dq
     bool falling;              // later items are shorter
@@ -132,7 +133,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         mbar_init(b_sread, kSoftWarps);
         mbar_init(b_dq, 1);
         mbar_init(b_end, 2);
-        polls_s = tc::kPolls;
+        polls_s = a.polls;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -472,7 +473,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         mbar_init(b_dp, 1);
         mbar_init(b_ds, kSoftWarps);
         mbar_init(b_end, 2);
-        polls_s = tc::kPolls;
+        polls_s = a.polls;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -702,6 +703,7 @@ size_t plan(const AttnProblem &p, BwdArgs &a, char *ws) {
     a.gs = heads_in_tile(p.Hq / p.Hk);
     a.runs = p.Hq / p.Hk >> a.gs;
     a.tokens = 128 >> a.gs;
+    a.polls = item_polls(p, a.tokens);
     a.stats = (float2 *)ws;
     const size_t stats = round256(sizeof(float2) * (size_t)(p.seqs.total * p.Hq));
     return stats + plan_sinks(p, kKeys, 1024, ws + stats, a.sinks);

@@ -45,6 +45,7 @@ constexpr float kAbove = 8.f;
 struct FwdArgs {
     AttnProblem p;
     int *status;
+    int polls;             // of a wait, at most
     int gs, runs;          // log2 of the query heads side by side; runs of them in a key head's group
     int tokens;            // of an item: 256 >> gs
     int64_t items;
@@ -104,7 +105,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(b_pv + i, 1);
         }
         mbar_init(b_end, 2);
-        polls_s = tc::kPolls;
+        polls_s = a.polls;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -434,6 +435,7 @@ int launch_attn_tc_fwd(const AttnProblem &p, int *status, cudaStream_t stream) {
     a.gs = heads_in_tile(p.Hq / p.Hk);
     a.runs = p.Hq / p.Hk >> a.gs;
     a.tokens = 256 >> a.gs;
+    a.polls = item_polls(p, a.tokens);
     a.items = attn_tile_slots(p.seqs, a.tokens) * p.Hk * a.runs;
     a.falling = !p.seqs.cu && p.window > p.seqs.T / 2;
     CUtensorMap m[3];

@@ -795,6 +795,57 @@ def test_pages_behind_four_gigabytes(dr, dtype):
 
 
 @pytest.mark.gpu
+def test_millions_of_tokens_in_sight(dr):
+    """Items of 36,000 key tiles (the last one's second stage without rows): waits that last an item do not run out.  Of a sample of rows, by
+    the docstring's bounds and what long sums add at worst: a tensor-core accumulator is off by one step, 2^-23, with each of
+    its T / 16 additions, a softmax's sum by half a step, 2^-24, with each of its four chains' T / 4.  The gradients' reference
+    takes out and lse as they are given."""
+    T, d = 256 * 18359 + 96, 64
+    g = torch.Generator(device="cuda").manual_seed(41)
+    q, k, v, do = (torch.randn((1, T, 1, d), generator=g, device="cuda") for _ in range(4))
+    q, k, v, do = (x.to(torch.bfloat16) for x in (q, k, v.mul_(0.5).add_(1.0), do))
+    out, lse = dr.window_attn_fwd(q, k, v)
+    grads = dr.window_attn_bwd(q, k, v, out, lse, do)
+    torch.cuda.synchronize()
+    assert dr.lib().dr_get_device_status(None) == 0
+    for x in (out, lse) + grads:
+        assert torch.isfinite(x).all()
+    scale, steps, chain = d ** -0.5, T / 16 * 2.0 ** -23, T / 4 * 2.0 ** -24
+    last = 64
+    K, V = k[0, :, 0].double(), v[0, :, 0].double()
+    dk, dv, e_dk, e_dv = (torch.zeros((last, d), dtype=torch.float64, device="cuda") for _ in range(4))
+
+    def near(what, got, want, bound):
+        worst = ((got.double() - want).abs() / bound).max().item()
+        assert worst <= 1, f"{what}: {worst:.3f} of the bound"
+
+    rows = torch.cat((torch.tensor([0, 1, 127, 128, 255, 256, 5000, T // 3, T // 2 + 77, T - 300, T - 97, T - 96, T - 70, T - 66, T - 65]),
+                      torch.arange(T - last, T))).cuda()
+    for at in rows.split(8):
+        Q, D, o, l = q[0, at, 0].double(), do[0, at, 0].double(), out[0, at, 0].double(), lse[0, at, 0].double()
+        n = int(at.max()) + 1
+        s = (scale * Q @ K[:n].T).masked_fill(torch.arange(n, device="cuda")[None] > at[:, None], -math.inf)
+        u = U17 * max(1.0, scale * float((Q.abs() @ K[:n].abs().T).max()) / 16)
+        want_l = torch.logsumexp(s, 1)
+        p = (s - want_l[:, None]).exp()
+        want_o, size = p @ V[:n], p @ V[:n].abs()
+        near("lse", l, want_l, u * (1 + want_l.abs()) + chain)
+        near("out", o, want_o, (u + HALF + steps + chain) * size + HALF * want_o.abs())
+        p = (s - l[:, None]).exp()
+        ds = p * (D @ V[:n].T - (D * o).sum(1, keepdim=True))
+        off = u * p * (D.abs() @ V[:n].abs().T + (D * o).abs().sum(1, keepdim=True)) + HALF * ds.abs()
+        want = scale * ds @ K[:n]
+        near("dq", grads[0][0, at, 0], want, scale * (off + steps * ds.abs()) @ K[:n].abs() + HALF * want.abs())
+        if n > T - last:       # (rows in front of these keys do not see them: p is 0)
+            dk += torch.nn.functional.pad(scale * ds[:, T - last:].T @ Q, (0, 0, 0, T - n))
+            dv += torch.nn.functional.pad(p[:, T - last:].T @ D, (0, 0, 0, T - n))
+            e_dk += torch.nn.functional.pad(scale * off[:, T - last:].T @ Q.abs(), (0, 0, 0, T - n))
+            e_dv += torch.nn.functional.pad((u + HALF) * p[:, T - last:].T @ D.abs(), (0, 0, 0, T - n))
+    near("dk", grads[1][0, T - last:, 0], dk, e_dk + HALF * dk.abs())
+    near("dv", grads[2][0, T - last:, 0], dv, e_dv + HALF * dv.abs())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_far_apart(dr, dtype):
     """Rows whose last one is more than 2^32 values behind the first: the same bits as next to one another."""
