@@ -42,8 +42,28 @@ struct AttnProblem {
 __host__ __device__ inline int64_t attn_tile_slots(const LinrecSeqs &s, int tile) {
     return s.cu ? s.total / tile + s.N : s.N * ((s.T + tile - 1) / tile);
 }
+// The last of the packed sequences whose key(n, first row) is at most `slot`, and its rows; keys do not fall.  By
+// whole warps: 32 sequences are asked at a time.
+template <class Key>
+__device__ __forceinline__ int64_t last_sequence(const LinrecSeqs &s, int slot, Key key, int64_t &lo, int &len) {
+    int64_t a = 0, b = s.N - 1, hi;
+    while (a < b) {
+        const int64_t step = (b - a + 31) >> 5, m = a + 1 + (threadIdx.x & 31) * step;
+        bool in = false;
+        if (m <= b) {
+            seq_range(s, m, lo, hi);
+            in = key(m, lo) <= slot;
+        }
+        const int k = __popc(__ballot_sync(0xffffffffu, in));
+        b = min(b, a + k * step);
+        if (k > 0) a += 1 + (k - 1) * step;
+    }
+    seq_range(s, a, lo, hi);
+    len = (int)(hi - lo);
+    return a;
+}
 // Finds (n, j) of a slot and the sequence's rows, or false where the slot has no tile.  By whole
-// warps: 32 sequences are asked at a time.  Rows and slots fit in 31 bits.
+// warps.  Rows and slots fit in 31 bits.
 __device__ __forceinline__ bool find_tile(const LinrecSeqs &s, int tile, int slot, int64_t &n, int &j, int64_t &lo, int &len) {
     if (!s.cu) {
         const int per = (int)((s.T + tile - 1) / tile);
@@ -53,22 +73,9 @@ __device__ __forceinline__ bool find_tile(const LinrecSeqs &s, int tile, int slo
         len = (int)s.T;
         return true;
     }
-    int64_t a = 0, b = s.N - 1, hi;   // the last n whose first slot is at most `slot`
-    while (a < b) {
-        const int64_t step = (b - a + 31) >> 5, m = a + 1 + (threadIdx.x & 31) * step;
-        bool in = false;
-        if (m <= b) {
-            seq_range(s, m, lo, hi);
-            in = (uint32_t)lo / (uint32_t)tile + m <= slot;
-        }
-        const int k = __popc(__ballot_sync(0xffffffffu, in));
-        b = min(b, a + k * step);
-        if (k > 0) a += 1 + (k - 1) * step;
-    }
-    seq_range(s, a, lo, hi);
-    n = a;
-    len = (int)(hi - lo);
-    j = slot - (int)((uint32_t)lo / (uint32_t)tile + a);
+    // the first slot of a sequence is lo / tile + n
+    n = last_sequence(s, slot, [&](int64_t m, int64_t at) { return (uint32_t)at / (uint32_t)tile + m; }, lo, len);
+    j = slot - (int)((uint32_t)lo / (uint32_t)tile + n);
     return j >= 0 && (int64_t)j * tile < len;
 }
 #endif

@@ -522,7 +522,8 @@ int dr_window_attn_fwd(const dr_attn_desc *desc, const void *q, const void *k, c
  * neither each other nor an input.  fp32 rows: weights and delta_i are summed anew, so out and lse may come from
  * a forward with other roundings.  Results do not depend on the order in which the GPU runs its blocks.
  * A token that sees itself alone has dq = 0 up to the rounding of d_out.out.
- * Workspace rules as for dr_chunk_fwd; its size depends only on the descriptor.
+ * Workspace rules as for dr_chunk_fwd; its size depends only on the descriptor: 8 bytes a row and query head and, with
+ * a window and sinks, sums of the sinks' rows that follow the rows / window, not N: at most 16 bytes a value of dq, dk, dv.
  */
 int dr_window_attn_bwd_workspace_bytes(const dr_attn_desc *desc, size_t *bytes);
 int dr_window_attn_bwd(const dr_attn_desc *desc, const void *q, const void *k, const void *v,

@@ -164,6 +164,38 @@ def test_many_short_sequences(dr):
     both(dr, 1, cu[-1] + 3, 2, 1, 64, 3, 1, "bf16", seed=3, cu=cu)
 
 
+def lengths_between_short_ones(long, short, n):
+    """n sequences: the long ones with 0 to `short` tokens' ones between them."""
+    ls = [(5 * i) % (short + 1) for i in range(n)]
+    for i, x in enumerate(long):
+        ls[(i * n) // len(long)] = x
+    return [int(x) for x in torch.tensor([0] + ls).cumsum(0)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (2, 1)])
+@pytest.mark.parametrize("long,short,n,window,sinks", [
+    ([600, 17, 16], 2, 50, 1, 20), ([600, 260, 280], 3, 50, 2, 130), ([2500, 131, 130, 1300], 6, 160, 3, 20), ([2500, 400, 1400, 300], 8, 160, 100, 150),
+    ([1250, 200, 329, 328], 5, 220, 200, 1), ([2600, 1200], 4, 200, 1, 1000)])
+def test_sinks_of_some_of_many_sequences(dr, long, short, n, window, sinks, Hq, Hk, dtype):
+    """More sequences than can be longer than the window: sums of sinks' rows lie by rows, not by sequence.  The workspace is
+    full of NaN beforehand."""
+    cu = lengths_between_short_ones(long, short, n)
+    T = cu[-1] + 2
+    q, k, v, do = make(1, T, Hq, Hk, 64, dtype, seed=n + window)
+    c, cu_d = [x.cuda() for x in (q, k, v, do)], torch.tensor(cu).cuda()
+    kw = dict(window=window, sinks=sinks, cu_seqlens=cu_d)
+    out, lse = dr.window_attn_fwd(*c[:3], **kw)
+    size = bwd_bytes(dr, B=1, T=T, Hq=Hq, Hk=Hk, d=64, N=n, window=window, sinks=sinks, dtype=dr.DR_BF16 if dtype == "bf16" else dr.DR_F32)
+    ws = torch.full((size // 4,), float("nan"), device="cuda")
+    dq, dk, dv = dr.window_attn_bwd(*c[:3], out, lse, c[3], workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert dr.lib().dr_get_device_status(None) == 0
+    R, E = reference(q, k, v, window, sinks, 0.125, dtype == "bf16", cu, do)
+    compare(dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv), R, E)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
@@ -946,6 +978,27 @@ def test_bad_attention_descriptors(dr, bad, status):
 def test_bad_step_descriptors(dr, bad, status):
     n = ctypes.c_size_t(0)
     assert dr.lib().dr_window_attn_step_workspace_bytes(ctypes.byref(step_desc(dr, **bad)), ctypes.byref(n)) == status
+
+
+def bwd_bytes(dr, **kw):
+    n = ctypes.c_size_t(0)
+    assert dr.lib().dr_window_attn_bwd_workspace_bytes(ctypes.byref(attn_desc(dr, **kw)), ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("dtype", ["DR_F32", "DR_BF16"])
+@pytest.mark.parametrize("window,sinks", [(1024, 4), (1024, 128), (1024, 1024), (64, 200), (1, 1024), (1, 1), (65000, 500)])
+def test_workspace_of_many_sequences(dr, window, sinks, dtype):
+    """Only sequences longer than the window can have sums of sinks' rows, at most T / window of them: the
+    workspace does not grow with the sequences behind that, and never past four times the gradients in fp32."""
+    T, H, d = 65536, 8, 128
+    kw = dict(B=1, T=T, Hq=H, Hk=H, d=d, window=window, sinks=sinks, dtype=getattr(dr, dtype))
+    stats = 8 * T * H + 256
+    few, many, most = (bwd_bytes(dr, N=n, **kw) for n in (1, 4096, 65536))
+    assert all(stats - 256 <= x <= stats + 4 * 4 * T * 3 * H * d + 512 for x in (few, many, most))
+    assert many == most
+    # sums of one sequence's own blocks and of two chunks of queries for every `window` rows
+    assert most <= stats + 512 + 4 * H * (-(-sinks // 128) * 128) * 2 * d * (3 * T // window + 1)
 
 
 no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="fake-pointer checks run only without a GPU")
