@@ -16,6 +16,7 @@ sum |do| e(out), which enters dq as scale sum p |k| times that.
 """
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -194,6 +195,82 @@ def test_sinks_of_some_of_many_sequences(dr, long, short, n, window, sinks, Hq, 
     assert dr.lib().dr_get_device_status(None) == 0
     R, E = reference(q, k, v, window, sinks, 0.125, dtype == "bf16", cu, do)
     compare(dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv), R, E)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hk", [(8, 16, 16), (4, 32, 16), (4, 32, 8), (9, 12, 4), (1, 32, 16), (1, 20, 20)])
+def test_blocks_of_many_items(dr, B, Hq, Hk, d, window, sinks):
+    """Each of 152 blocks gets four items and more, of up to a dozen key tiles (B 1: ragged sequences in one row): the bits of calls for a
+    key head of a batch row, where a block has one, and those against the reference."""
+    T, g, cu = 1451, Hq // Hk, None
+    if B == 1:
+        cu = [int(x) for x in torch.tensor([3, 700, 0, 129, 1, 1451, 128, 64, 900, 257, 0, 77, 1023, 300, 65, 1100]).cumsum(0)]
+        T = cu[-1] + 9
+    tokens = 256 // (4 if g % 4 == 0 else 2 if g % 2 == 0 else 1)
+    per = g if g % 2 else g // (4 if g % 4 == 0 else 2)
+    lens = [T] * B if cu is None else [b - a for a, b in zip(cu, cu[1:])]
+    assert sum(-(-n // tokens) for n in lens) * Hk * per >= 4 * 152
+    q, k, v, do = make(B, T, Hq, Hk, d, "bf16", seed=Hq + B)
+    got = run(dr, q, k, v, do, window, sinks, cu=cu)
+    c = [x.cuda() for x in (q, k, v, do)]
+    kw = dict(window=window, sinks=sinks, cu_seqlens=None if cu is None else torch.tensor(cu).cuda())
+    for b in range(B):
+        for h in range(Hk):
+            one = [x[b:b + 1, :, h * n:(h + 1) * n] for x, n in zip(c, (g, 1, 1, g))]
+            out, lse = dr.window_attn_fwd(*one[:3], **kw)
+            grads = dr.window_attn_bwd(*one[:3], out, lse, one[3], **kw)
+            for name, x, n in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads, (g, g, g, 1, 1)):
+                assert torch.equal(x[0], got[name][b, :, h * n:(h + 1) * n]), (name, b, h)
+    b, h = B - 1, Hk // 2
+    one = [x[b:b + 1, :, h * n:(h + 1) * n] for x, n in zip((q, k, v, do), (g, 1, 1, g))]
+    R, E = reference(*one[:3], window, sinks, d ** -0.5, True, cu, one[3])
+    compare({name: got[name][b:b + 1, :, h * n:(h + 1) * n] for name, n in zip(("out", "lse", "dq", "dk", "dv"), (g, g, g, 1, 1))}, R, E)
+
+
+def log_int(rng, lo, hi):
+    return round(math.exp(rng.uniform(math.log(lo), math.log(hi))))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("seed", range(40))
+def test_drawn_problems(dr, seed, dtype):
+    """Any heads, lengths, windows, sinks, sequences and strides together."""
+    rng = random.Random(seed)
+    d, Hk = rng.choice([64, 128]), rng.randint(1, 8)
+    Hq = Hk * rng.choice([1, 2, 3, 4, 8])
+    window = rng.choice([0, 1, 2, 2]) and log_int(rng, 1, 700)
+    sinks = rng.choice([0, rng.randint(1, 8), log_int(rng, 1, 400)])
+    n, cu = rng.choice([0, 0, rng.randint(1, 32)]), None
+    T = log_int(rng, 1 if n == 0 else 64, 700)
+    B = 1 if n else rng.randint(1, 3)
+    if n:
+        ends = sorted(rng.randint(0, T) for _ in range(n))
+        cu = [rng.choice([0, ends[0]])] + ends
+    q, k, v, do = make(B, T, Hq, Hk, d, dtype, seed)
+    fused = rng.random() < 0.5
+    row = torch.cat((q, k, v), 2).cuda()
+    c = row.split((Hq, Hk, Hk), 2) if fused else [x.cuda() for x in (q, k, v)]
+    kw = dict(window=window, sinks=sinks, cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int64).cuda())
+    out, lse = dr.window_attn_fwd(*c, **kw)
+    grads = dr.window_attn_bwd(*c, out, lse, do.cuda(), grads=torch.zeros_like(row).split((Hq, Hk, Hk), 2) if fused else None, **kw)
+    torch.cuda.synchronize()
+    assert dr.lib().dr_get_device_status(None) == 0
+    R, E = reference(q, k, v, window, sinks, d ** -0.5, dtype == "bf16", cu, do)
+    compare(dict(zip(R, (out, lse) + grads)), R, E)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_steps(dr, seed, dtype):
+    rng = random.Random(seed)
+    Hk = rng.randint(1, 8)
+    window, sinks = rng.choice([0, 1, 2]) and log_int(rng, 1, 700), rng.choice([0, rng.randint(1, 8), log_int(rng, 1, 200)])
+    lens = [rng.choice([-1, 0, log_int(rng, 1, 900), log_int(rng, 1, 900)]) for _ in range(log_int(rng, 1, 30))]
+    step_case(dr, lens, Hk * rng.choice([1, 2, 3, 4, 8]), Hk, rng.choice([64, 128]), window, sinks, 16 << rng.randint(0, 4), dtype, seed=seed)
 
 
 @pytest.mark.gpu
@@ -782,6 +859,24 @@ def test_append_where_positions_end(dr, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_append_many_heads_of_many_sequences(dr, dtype):
     append_case(dr, [1] * 300, [5 * n - 3 for n in range(300)], 70, 10, 64, 32, 16, dtype, seed=6, fused=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_appends(dr, seed, dtype):
+    rng = random.Random(seed)
+    d, Hk, N = rng.choice([64, 128]), rng.randint(1, 8), log_int(rng, 1, 40)
+    packed = rng.random() < 0.6
+    rows = [rng.choice([0, 1, log_int(rng, 1, 60)]) if packed else 1 for _ in range(N)]
+    cu = [0] + [int(x) for x in torch.tensor(rows).cumsum(0)] if packed else None
+    if packed and cu[-1] == 0:
+        rows, cu = [3] * N, [3 * n for n in range(N + 1)]
+    start = [rng.choice([-1, 0, rng.randint(0, 300), rng.randint(0, 300)]) for _ in range(N)]
+    fused, given = rng.random() < 0.5, rng.random() < 0.7
+    append_case(dr, rows, start, Hk * rng.choice([0, 1, 2, 3, 4, 8]), Hk, d, rng.choice([0, d, d // 2, d // 4]), 16 << rng.randint(0, 4), dtype,
+                rng.choice(["rms", "l2", "none"]), rng.choice(["half", "interleaved"]), cu, fused=fused, given=given,
+                in_place=fused and given and rng.random() < 0.5, seed=seed)
 
 
 @pytest.mark.gpu
