@@ -12,9 +12,10 @@
 // number of tiles of 64: forward 8 (T256 H2 d64 w64) 10.3 and 18.5 us, 32 (T512 H4 d128) 51 and 74, 80 (T300 H16 d64 w64) 14.3
 // and 16.4, 102 (T1037 H6 d64 w200) 39 and 31, 128 (T2048 H4 d128) 414 and 275; all of the backward, dq's tiles: 32 (T512 H4 d128) 119 and
 // 182, 80 (T300 H16/4) 55 and 57, 102 (T1037 H6/3) 105 and 99; dk's and dv's: 20 (T300 H16/4) 57 and 94, 51 (T1037 H6/3) 99 and 150, 64 (B2
-// T1024 H8/2) 158 and 211, 128 (B4 T512 H4 d128 w256) 172 and 156.
+// T1024 H8/2) 158 and 211, 128 (B4 T512 H4 d128 w256) 172 and 156.  So the sides cross between 80 tiles and 102; near there they are
+// two microseconds apart, and the border stays at 76, where the rule's reason ends.
 // What bounds it: loads from shared memory, 16 bytes a lane take as long as two paired FMAs of every scheduler, and Across<D, 4> has 8 for 32
-// (backward of B4 T2048 H8/2 d128 w512: 1,974 us, 30 TFLOP/s of some 77).  Small problems: the longest block's
+// (backward of B4 T2048 H8/2 d128 w512: 1,974 us, 30 TFLOP/s of some 77 with the eight products that it forms for five).  Small problems: the longest block's
 // tiles, one behind another (T1037 H6/3 d64 w200, 0.73 GFLOP: 99 us, 102 and 210 blocks of four to six tiles).
 #include "../../include/dr.h"
 #include "attn.h"

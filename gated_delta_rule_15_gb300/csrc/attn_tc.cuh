@@ -97,7 +97,7 @@ __device__ __forceinline__ int64_t dealt(int64_t round, bool falling) {
 
 // Polls of a wait (tc::wait_longer).  Most waits last a tile, but some an item: those of dq's statistics warps, which are
 // items ahead, and those of a forward's second stage whose rows lie behind the sequence's end while the first runs through
-// all key tiles.  So the bound follows the longest item: a tile takes some 50 polls of 60 cycles.
+// all key tiles.  So the bound follows the longest item: a tile takes some 60 polls of 60 cycles.
 inline int item_polls(const AttnProblem &p, int tokens) {
     const int64_t longest = p.seqs.cu ? p.seqs.total : p.seqs.T, reach = (int64_t)p.window + p.sinks + tokens + 32;
     const int64_t tiles = (longest < reach ? longest : reach) / kKeys + 2;

@@ -19,9 +19,9 @@
 // products of V, and the other way round.
 // Which keys and queries a block takes, and how tiles that hold sinks are cut: attn_sinks.cuh.
 //
-// What bounds them (B8 T2048 H16/4 d128 w1024: dq 162 us, dk and dv 170): a tile of dq takes 2,100 cycles where the tensor cores
-// need 1,536 and shared memory 1,750 (operands of three products, the last one's A from tensor memory, and two copies); a tile of
-// dk, dv 2,600 where both need 2,048.  The rest is the chain from S and dP to dS, half covered by the
+// What bounds them (B8 T2048 H16/4 d128 w1024: dq 162 us, dk and dv 171): by the cycles of a launch and its tiles, items' begin and end
+// among them, a tile of dq takes 3,420 cycles where the tensor cores need 1,536 and shared memory 1,790 (operands of three
+// products, the last one's A from tensor memory, and two copies); a tile of dk, dv 3,410 where both need 2,048.  The rest is the chain from S and dP to dS, half covered by the
 // products of the neighbouring tiles, and the items' begin and end.
 //
 // Rows of other sequences are masked; where they enter a product as 0 times whatever they hold they are

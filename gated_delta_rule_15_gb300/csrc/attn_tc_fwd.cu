@@ -16,9 +16,10 @@
 // stages' MMAs: O += P V, then S of the next tile, so that one stage's softmax runs while the tensor cores work for the other.  (One thread for both stages is late: a tile's sixteen products take it 900 cycles to
 // issue and their waits 400, which the tensor cores need 1024 for.)
 //
-// What bounds it (bf16, d = 128): the tensor cores need 2,048 cycles for a key tile of both stages (64 for 16 of a product's depth), it
-// takes 2,400 where every query sees all before it (B2 T8192 H16: 400 us, 1.37 PFLOP/s) and 2,900 with a window (B8 T4096
-// H16/4 w1024: 225 us, 1.09 PFLOP/s), where items are ten tiles long and each begins and ends with the tensor cores idle.  Between
+// What bounds it (bf16, d = 128): the tensor cores need 2,048 cycles for a key tile of both stages (64 for 16 of a product's depth).  By
+// the cycles of a launch and its tiles it takes 3,200 in long items (B1 T65536 H16/4 w4096: 1,540 us, 1.38 PFLOP/s), 3,590 where
+// every query sees all before it (B2 T8192 H16: 430 us, 1.28 PFLOP/s), where items are of any length, and 4,110 with a window
+// (B8 T4096 H16/4 w1024: 232 us, 1.04 PFLOP/s), where they are nine tiles long and each begins and ends with the tensor cores idle.  Between
 // them stands the chain S, softmax, P, O += P V of a stage, which the other stage covers but for its ends: the
 // softmax warps issue in about 60 % of the cycles.  Rows of 128 with a thread for half of one, so that a maximum or a sum is one
 // exchange of two threads; with 16 lanes a row (fragments as mma.sync has them) fewer exponentials
